@@ -69,7 +69,14 @@
  *                            or infinite (for sv_verify_sample_logits: a
  *                            logit that is NaN or infinite).  The regular
  *                            build does not look, and such inputs give
- *                            unspecified results.
+ *                            unspecified results.  sv_warp_sample always
+ *                            looks: a NaN or +infinite logit, or a
+ *                            temperature that is not positive and finite;
+ *       SV_STATUS_BAD_PAGE   a page id outside the cache (the append skips
+ *                            the token; the attention takes zeros in place
+ *                            of that page's keys and values);
+ *       SV_STATUS_BAD_LENGTH lengths that do not fit the tokens or the page
+ *                            table (see sv_paged_cache).
  */
 #ifndef SPECVERIFY_H
 #define SPECVERIFY_H
@@ -95,6 +102,8 @@ typedef struct CUstream_st *sv_stream_t;
 #define SV_STATUS_BAD_MODE 8u
 #define SV_STATUS_TIMEOUT 16u
 #define SV_STATUS_BAD_VALUE 32u
+#define SV_STATUS_BAD_PAGE 64u
+#define SV_STATUS_BAD_LENGTH 128u
 
 #define SV_MAX_K 64
 
@@ -250,6 +259,119 @@ int sv_verify_sample_logits(const float *zp, int64_t zp_row_stride,
 int sv_alpha(const float *p, int64_t p_row_stride, const float *q, int64_t q_row_stride,
              int32_t B, int32_t K, int64_t V, double *alpha, double *expected_length,
              void *workspace, size_t workspace_bytes, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The target pass of a round: a paged cache of keys and values, attention of
+ * the new tokens over it, and the warp of logits into probability rows.  The
+ * pages have no counterpart to these calls; they make the rows that the
+ * verification calls above take.  All arrays are device memory (else
+ * SV_EINVAL).  The calls share a workspace of their own kind:
+ * sv_cache_workspace_size() bytes, 256-byte aligned, zeroed once with
+ * sv_workspace_init, one call at a time in stream order, status read with
+ * sv_get_status.  A workspace of the verification calls does not serve here,
+ * nor one of these there. */
+
+/* Element types. */
+#define SV_F32 0
+#define SV_BF16 1
+#define SV_F16 2
+
+/* A paged cache and the batch that works on it.
+ *   k, v       [num_pages][page_size][kv_heads][head_dim] of `dtype` (SV_BF16
+ *              or SV_F16): element (p, s, h, d) is at p * stride[0] +
+ *              s * stride[1] + h * stride[2] + d, in any order of the axes.
+ *              Strides are multiples of 8 elements and the bases 16-byte
+ *              aligned.  head_dim is a multiple of 8, 8 to 128; page_size a
+ *              multiple of 8.
+ *   pages      [B][max_pages] int32, rows pages_stride apart: slot s of
+ *              sequence b is slot s % page_size of page
+ *              pages[b][s / page_size].  Entries past a sequence's length are
+ *              not read.
+ *   q_start    [B + 1] int32: the new tokens of sequence b are rows
+ *              q_start[b] .. q_start[b + 1] - 1 of the token arrays.
+ *   kv_len     [B] int32: the sequence's length with its new tokens: new
+ *              token j of n sits in slot kv_len[b] - n + j.
+ *   tokens     rows of the token arrays (an upper limit for q_start).
+ * q_start and kv_len are read on the device.  A sequence whose rows do not
+ * lie in [0, tokens], or whose kv_len is outside [0, max_pages * page_size],
+ * is left out with SV_STATUS_BAD_LENGTH (its outputs are not written). */
+typedef struct sv_paged_cache {
+    void *k, *v;
+    int64_t k_stride[3], v_stride[3];
+    int32_t num_pages, page_size, kv_heads, head_dim, dtype, B, tokens, max_pages;
+    const int32_t *pages;
+    int64_t pages_stride;
+    const int32_t *q_start;
+    const int32_t *kv_len;
+} sv_paged_cache;
+
+/* Bytes of the workspace the calls of this section need, whatever the sizes. */
+size_t sv_cache_workspace_size(void);
+
+/* Writes the new tokens' keys and values into their slots, the keys rotated
+ * by their positions, and rotates the queries alike.
+ *   k, v  [tokens][kv_heads][head_dim]; q, q_out [tokens][q_heads][head_dim]
+ *         of the cache's type; element (t, h, d) at t * stride[0] +
+ *         h * stride[1] + d; strides multiples of 8, bases 16-byte aligned.
+ *         q may be NULL (then q_heads = 0); q_out may be q itself.
+ *   inv_freq  [rot_dim / 2] f64, radians per position, or NULL with
+ *         rot_dim = 0 (no rotation).  Pair i of a head's first rot_dim values
+ *         turns by position * inv_freq[i]; pair i is (i, i + rot_dim / 2), or
+ *         (2i, 2i + 1) when interleaved.  rot_dim is a multiple of 4, at most
+ *         head_dim.
+ *   positions [tokens] int32, or NULL: a token's position is its slot.
+ * Angles are reduced to one turn in fp64, so far positions lose nothing; the
+ * rotation is fp32, rounded once.  A token whose slot is outside the page
+ * table (SV_STATUS_BAD_LENGTH) or whose page id is outside the cache
+ * (SV_STATUS_BAD_PAGE) is not written; its query is rotated all the same. */
+int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_stride,
+                 const void *v, const int64_t *v_stride, const void *q, const int64_t *q_stride,
+                 void *q_out, const int64_t *q_out_stride, int32_t q_heads,
+                 const double *inv_freq, int32_t rot_dim, int32_t interleaved,
+                 const int32_t *positions, void *workspace, size_t workspace_bytes,
+                 sv_stream_t stream);
+
+/* Attention of the new tokens over the paged cache (which holds them already):
+ *   out[t][h] = sum_s softmax_s(scale * q[t][h] . k[s][g]) v[s][g],
+ * g = h / (q_heads / kv_heads), over the slots s <= kv_len[b] - n + j of
+ * token j of n (causal), and s > kv_len[b] - n + j - window when window > 0.
+ * A row that sees no slot is written as zeros.  q and out are
+ * [tokens][q_heads][head_dim] of the cache's type, strides as for
+ * sv_append_kv; q_heads is a multiple of kv_heads.  scale must be finite.
+ * Products are accumulated and the softmax's statistics kept in fp32; the
+ * weights are rounded to the cache's type for the product with v.  What an
+ * unused slot of a page holds does not matter (NaN included); slots inside a
+ * sequence's length must be finite.  With a window, pages that lie wholly
+ * before every row's window are not read. */
+int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t *q_stride,
+                       void *out, const int64_t *out_stride, int32_t q_heads, float scale,
+                       int32_t window, void *workspace, size_t workspace_bytes,
+                       sv_stream_t stream);
+
+/* Warps rows of logits and draws from them.  z holds R rows of V logits of
+ * type z_dtype (SV_F32, SV_BF16 or SV_F16), z_row_stride (>= V) apart.  Row r:
+ *   1. w_v = exp((z_v - max) / temperature[r])   (1 when temperature is NULL);
+ *   2. top_k[r] in [1, V): only the top_k largest logits stay;
+ *   3. top_p[r] < 1: of those, in descending order, only the tokens before
+ *      which less than top_p[r] of their mass lies (the first always stays);
+ *   4. min_p[r] > 0: of those, only the ones with w_v >= min_p[r] (the first
+ *      always stays);
+ * equal logits are ordered by index, lowest first.  NULL leaves a filter off,
+ * as do top_k outside [1, V), top_p >= 1 or NaN, min_p <= 0 or NaN.
+ *   token[r]  (u and token not NULL): the smallest v whose running mass in
+ *             index order exceeds u[r] times the kept mass, u in [0, 1) f64;
+ *   probs     (not NULL): [R] rows of V f32, probs_row_stride (>= V) apart:
+ *             w_v over the kept mass, 0 for what was left out.
+ * The kept set and the token are those of a 64-bit evaluation: masses are
+ * summed to about 1e-11.  -inf logits have no mass.  A row without mass (all
+ * -inf: SV_STATUS_ZERO_MASS), with a NaN or +inf logit, or with a bad
+ * temperature (SV_STATUS_BAD_VALUE) gives token -1 and a row of zeros.  Rows
+ * warped alike serve as the p and q of sv_verify_sample. */
+int sv_warp_sample(const void *z, int64_t z_row_stride, int32_t z_dtype, int32_t R, int64_t V,
+                   const float *temperature, const int32_t *top_k, const float *top_p,
+                   const float *min_p, const double *u, int32_t *token, float *probs,
+                   int64_t probs_row_stride, void *workspace, size_t workspace_bytes,
+                   sv_stream_t stream);
 
 /* Number of CTAs the last call on this thread launched (its grid size). */
 int64_t sv_last_grid_size(void);

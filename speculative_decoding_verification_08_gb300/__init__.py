@@ -36,7 +36,9 @@ STATUS_ZERO_MASS = 2
 STATUS_OVERFLOW = 4
 STATUS_BAD_MODE = 8
 STATUS_TIMEOUT = 16
-STATUS_BAD_VALUE = 32   # debug builds only (built with SV_DEBUG=1)
+STATUS_BAD_VALUE = 32   # verification: debug builds only (built with SV_DEBUG=1); warp_sample: always
+STATUS_BAD_PAGE = 64
+STATUS_BAD_LENGTH = 128
 MAX_K = 64
 
 # every symbol include/specverify.h declares
@@ -45,7 +47,8 @@ EXPORTED = (
     "sv_verify_round", "sv_get_status", "sv_set_ctas_per_sm", "sv_last_grid_size",
     "sv_last_kernel_count", "sv_alpha", "sv_verify_sample_logits",
     "sv_status_string", "sv_version", "sv_verify_sample_noalloc", "sv_trace_reset",
-    "sv_trace_read",
+    "sv_trace_read", "sv_cache_workspace_size", "sv_append_kv", "sv_paged_attention",
+    "sv_warp_sample",
 )
 
 _lock = threading.Lock()
@@ -73,6 +76,22 @@ def load():
                 "speculative_decoding_verification_08_gb300.build() (no CPU fallback exists)")
         _lib = _declare(ctypes.CDLL(LIBRARY))
         return _lib
+
+
+class _PagedCache(ctypes.Structure):
+    """sv_paged_cache of include/specverify.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p)]
+
+
+_Stride2 = ctypes.c_int64 * 2
+_Stride3 = ctypes.c_int64 * 3
 
 
 def _declare(lib):
@@ -114,6 +133,15 @@ def _declare(lib):
     lib.sv_trace_reset.restype = ctypes.c_int
     lib.sv_trace_read.argtypes = [P, sz, ctypes.POINTER(sz), P]
     lib.sv_trace_read.restype = ctypes.c_int
+    C, S = ctypes.POINTER(_PagedCache), ctypes.POINTER(ctypes.c_int64)
+    lib.sv_cache_workspace_size.argtypes = []
+    lib.sv_cache_workspace_size.restype = sz
+    lib.sv_append_kv.argtypes = [C, P, S, P, S, P, S, P, S, i32, P, i32, i32, P, P, sz, P]
+    lib.sv_append_kv.restype = ctypes.c_int
+    lib.sv_paged_attention.argtypes = [C, P, S, P, S, i32, ctypes.c_float, i32, P, sz, P]
+    lib.sv_paged_attention.restype = ctypes.c_int
+    lib.sv_warp_sample.argtypes = [P, i64, i32, i32, i64, P, P, P, P, P, P, P, i64, P, sz, P]
+    lib.sv_warp_sample.restype = ctypes.c_int
     return lib
 
 
@@ -493,6 +521,246 @@ class HostVerifier:
         self.next_host.copy_(self.next, non_blocking=True)
         torch.cuda.current_stream().synchronize()
         return self.n_host, self.next_host
+
+
+# ---------------------------------------------------------------------------
+# the target pass of a round: paged cache, attention over it, warped rows
+
+class CacheWorkspace:
+    """Device scratch of append_kv, paged_attention and warp_sample: one size
+    for all sizes, one call at a time in stream order."""
+
+    def __init__(self, device=None, stream=None):
+        torch = _torch()
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        self.nbytes = int(load().sv_cache_workspace_size())
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+        self.ptr = self.buf.data_ptr()
+        _check(load().sv_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
+               "sv_workspace_init")
+
+    def status(self, stream=None) -> int:
+        """Waits for the stream and returns (and clears) the device status bits."""
+        out = ctypes.c_uint32(0)
+        _check(load().sv_get_status(self.ptr, _stream_handle(stream), ctypes.byref(out)),
+               "sv_get_status")
+        return int(out.value)
+
+
+def cache_workspace(device=None, stream=None) -> CacheWorkspace:
+    """The workspace that calls without one share on this device and stream
+    (calls on different streams never share an implicit one)."""
+    torch = _torch()
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return _cache_ws(None, dev, _raw_stream(dev, stream), stream)
+
+
+def _raw_stream(device, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch().cuda.current_stream(device).cuda_stream
+
+
+def _cache_ws(ws, device, raw, stream):
+    if ws is not None:
+        return ws
+    key = (device.index, raw)
+    w = _ws_cache.get(key)
+    if w is None:
+        w = _ws_cache[key] = CacheWorkspace(device, stream)
+    return w
+
+
+def _cache_dtype(dtype, name) -> int:
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return 1
+    if dtype == torch.float16:
+        return 2
+    raise SpecVerifyError(f"{name} must be torch.bfloat16 or torch.float16, got {dtype}")
+
+
+def _heads3(x, like, heads, D, N, name):
+    """A token array [N][heads][D] of the cache's type and device."""
+    if x.dtype != like.dtype or x.device != like.device:
+        raise SpecVerifyError(f"{name} must be {like.dtype} on {like.device}, got {x.dtype} on "
+                              f"{x.device}")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads) or \
+            (N is not None and shape[0] != N):
+        raise SpecVerifyError(f"{name}: expected [{'N' if N is None else N}]"
+                              f"[{'heads' if heads is None else heads}][{D}], got {tuple(shape)}")
+    st = x.stride()
+    if st[2] != 1 and D > 1:
+        raise SpecVerifyError(f"{name}: the head dimension must be contiguous")
+    return _Stride2(st[0], st[1])
+
+
+def _ints(x, shape, name, device):
+    torch = _torch()
+    if x.dtype != torch.int32 or x.device != device:
+        raise SpecVerifyError(f"{name} must be torch.int32 on {device}, got {x.dtype} on {x.device}")
+    if shape is not None and (tuple(x.shape) != shape or not x.is_contiguous()):
+        raise SpecVerifyError(f"{name}: expected {list(shape)} contiguous, got {tuple(x.shape)}")
+
+
+def _paged(k_cache, v_cache, pages, q_start, kv_len, N):
+    """The batch's sv_paged_cache, checked."""
+    if not k_cache.is_cuda or v_cache.device != k_cache.device:
+        raise SpecVerifyError("k_cache and v_cache must be CUDA tensors on one device")
+    dt = _cache_dtype(k_cache.dtype, "k_cache")
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or k_cache.dim() != 4:
+        raise SpecVerifyError("k_cache and v_cache must be [pages][page_size][kv_heads][head_dim] "
+                              "of one type")
+    P, ps, H, D = k_cache.shape
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise SpecVerifyError("the caches' head dimension must be contiguous")
+    dev = k_cache.device
+    _ints(kv_len, None, "kv_len", dev)
+    B = kv_len.numel()
+    _ints(kv_len, (B,), "kv_len", dev)
+    _ints(q_start, (B + 1,), "q_start", dev)
+    _ints(pages, None, "pages", dev)
+    if pages.dim() != 2 or pages.shape[0] != B or (pages.shape[1] > 1 and pages.stride(1) != 1):
+        raise SpecVerifyError(f"pages: expected [{B}][max_pages] rows, got {tuple(pages.shape)}")
+    wide = pages.shape[1]
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _Stride3(*ks[:3]), _Stride3(*vs[:3]),
+                       P, ps, H, D, dt, B, N, wide, pages.data_ptr(),
+                       pages.stride(0) if B > 1 else wide, q_start.data_ptr(), kv_len.data_ptr())
+
+
+def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, q=None,
+              q_out=None, positions=None, interleaved=False, ws=None, stream=None):
+    """Writes the new tokens' keys and values [N][kv_heads][D] into their slots
+    of the paged cache [pages][page_size][kv_heads][D] (any order of the axes),
+    the keys rotated by their positions, and returns q [N][q_heads][D] rotated
+    alike (None without q; q_out may be q itself).
+
+    pages [B][max_pages] int32, q_start [B + 1] int32 (rows of each sequence's
+    new tokens), kv_len [B] int32 (lengths with the new tokens).  inv_freq
+    [rot_dim / 2] f64 gives radians per position of each pair (None: no
+    rotation); pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) when
+    interleaved.  positions [N] int32 overrides the slots as positions."""
+    torch = _torch()
+    N = k.shape[0]
+    c = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
+    dev, D = k_cache.device, c.head_dim
+    kst = _heads3(k, k_cache, c.kv_heads, D, N, "k")
+    vst = _heads3(v, k_cache, c.kv_heads, D, N, "v")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1 or \
+                not inv_freq.is_contiguous():
+            raise SpecVerifyError(f"inv_freq must be a contiguous float64 vector on {dev}")
+        rot = 2 * inv_freq.shape[0]
+    if positions is not None:
+        _ints(positions, (N,), "positions", dev)
+    heads, qp, qst, op, ost = 0, 0, None, 0, None
+    if q is not None:
+        qst = _heads3(q, k_cache, None, D, N, "q")
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        ost = _heads3(q_out, k_cache, heads, D, N, "q_out")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise SpecVerifyError("q_out without q")
+    raw = _raw_stream(dev, stream)
+    w = _cache_ws(ws, dev, raw, stream)
+    rc = load().sv_append_kv(c, k.data_ptr(), kst, v.data_ptr(), vst, qp, qst, op, ost, heads,
+                             0 if inv_freq is None else inv_freq.data_ptr(), rot,
+                             1 if interleaved else 0,
+                             0 if positions is None else positions.data_ptr(), w.ptr, w.nbytes,
+                             raw)
+    if rc:
+        _check(rc, "sv_append_kv")
+    return q_out
+
+
+def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, window=0,
+                    out=None, ws=None, stream=None):
+    """Attention of the new tokens q [N][q_heads][D] over the paged cache that
+    holds them already (append_kv): causal, over the last `window` slots when
+    window > 0, scale 1 / sqrt(D) by default; q_heads a multiple of kv_heads.
+    Arrays as for append_kv.  Rows that see nothing are zeros.  Returns out
+    [N][q_heads][D]."""
+    torch = _torch()
+    N = q.shape[0]
+    c = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
+    D = c.head_dim
+    qst = _heads3(q, k_cache, None, D, N, "q")
+    heads = q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ost = _heads3(out, k_cache, heads, D, N, "out")
+    raw = _raw_stream(q.device, stream)
+    w = _cache_ws(ws, q.device, raw, stream)
+    rc = load().sv_paged_attention(c, q.data_ptr(), qst, out.data_ptr(), ost, heads,
+                                   D ** -0.5 if scale is None else scale, window, w.ptr, w.nbytes,
+                                   raw)
+    if rc:
+        _check(rc, "sv_paged_attention")
+    return out
+
+
+def _per_row(x, R, name, dtype, device):
+    if x is None:
+        return 0
+    if x.dtype != dtype or x.device != device or x.numel() != R or not x.is_contiguous():
+        raise SpecVerifyError(f"{name}: expected {R} contiguous {dtype} on {device}")
+    return x.data_ptr()
+
+
+def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=None, probs=False,
+                probs_out=None, token_out=None, ws=None, stream=None):
+    """Warps rows of logits z [..., V] (f32, bf16 or f16) by temperature, top-k,
+    top-p and min-p, in this order, each on what the one before left, and draws
+    a token per row with u [...] f64 in [0, 1).  The filters are tensors with
+    one value per row (f32; top_k int32) or None (off).  Returns (token int32
+    or None without u, probs [..., V] f32 or None unless probs or probs_out):
+    rows as verify_sample takes them.  A row without mass or with a NaN or +inf
+    logit gives token -1 and zeros."""
+    torch = _torch()
+    if not z.is_cuda:
+        raise SpecVerifyError("z must be a CUDA tensor")
+    dt = 0 if z.dtype == torch.float32 else _cache_dtype(z.dtype, "z (or torch.float32)")
+    lead, dev = z.shape[:-1], z.device
+    V = z.shape[-1]
+    z2 = z if z.dim() == 2 else z.reshape(1, V) if z.dim() == 1 else z.view(-1, V)
+    if z2.stride(1) != 1 and V > 1:
+        raise SpecVerifyError("z: the vocabulary dimension must be contiguous")
+    R = z2.shape[0]
+    up = _per_row(u, R, "u", torch.float64, dev)
+    tp = _per_row(temperature, R, "temperature", torch.float32, dev)
+    kp = _per_row(top_k, R, "top_k", torch.int32, dev)
+    pp = _per_row(top_p, R, "top_p", torch.float32, dev)
+    mp = _per_row(min_p, R, "min_p", torch.float32, dev)
+    if u is not None:
+        if token_out is None:
+            token_out = torch.empty(lead, dtype=torch.int32, device=dev)
+        else:
+            _per_row(token_out, R, "token_out", torch.int32, dev)
+    elif token_out is not None:
+        raise SpecVerifyError("token_out without u")
+    pst = V
+    if probs or probs_out is not None:
+        if probs_out is None:
+            probs_out = torch.empty(z.shape, dtype=torch.float32, device=dev)
+        elif probs_out.dtype != torch.float32 or probs_out.device != dev or \
+                probs_out.shape != z.shape or not probs_out.is_contiguous():
+            raise SpecVerifyError(f"probs_out: expected {tuple(z.shape)} contiguous f32 on {dev}")
+    if token_out is None and probs_out is None:
+        raise SpecVerifyError("nothing to compute: give u, or ask for probs")
+    raw = _raw_stream(dev, stream)
+    w = _cache_ws(ws, dev, raw, stream)
+    rc = load().sv_warp_sample(z2.data_ptr(), z2.stride(0) if R > 1 else V, dt, R, V, tp, kp, pp,
+                               mp, up, 0 if token_out is None else token_out.data_ptr(),
+                               0 if probs_out is None else probs_out.data_ptr(), pst, w.ptr,
+                               w.nbytes, raw)
+    if rc:
+        _check(rc, "sv_warp_sample")
+    return token_out, probs_out
 
 
 # ---------------------------------------------------------------------------

@@ -8,11 +8,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "specverify.cu")]
+SOURCES = [os.path.join(CSRC, "specverify.cu"), os.path.join(CSRC, "cache.cu"),
+           os.path.join(CSRC, "warp.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "sv_device.cuh"), os.path.join(CSRC, "sv_tma.cuh"),
                      os.path.join(CSRC, "sv_item.cuh"), os.path.join(CSRC, "sv_alpha.cuh"),
                      os.path.join(CSRC, "sv_logits.cuh"), os.path.join(CSRC, "sv_debug.cuh"),
-                     os.path.join(CSRC, "sv_trace.cuh"),
+                     os.path.join(CSRC, "sv_trace.cuh"), os.path.join(CSRC, "sv_host.cuh"),
+                     os.path.join(CSRC, "sv_cache.cuh"), os.path.join(CSRC, "sv_append.cuh"),
+                     os.path.join(CSRC, "sv_attend.cuh"), os.path.join(CSRC, "sv_warp.cuh"),
                      os.path.join(INCLUDE, "specverify.h")]
 LIBRARY = os.path.join(PKG, "libspecverify.so")
 
@@ -20,6 +23,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
+    "-t", "0",   # the sources compile side by side
 ]
 
 

@@ -1,0 +1,204 @@
+// cache.cu -- host side of the paged-cache calls (sv_append_kv,
+// sv_paged_attention): argument checks and launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "specverify.h"
+#include "sv_append.cuh"
+#include "sv_attend.cuh"
+#include "sv_host.cuh"
+
+namespace {
+
+using svhost::g_last_grid;
+using svhost::g_last_kernels;
+using svhost::kAlign;
+using svhost::kOnDevice;
+using svhost::place;
+
+bool on_device(const void *p) {
+    const void *x = p;
+    return p && place(x) == kOnDevice;
+}
+
+bool vec_ok(const void *p, const int64_t *st, int n) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return false;
+    for (int i = 0; i < n; ++i)
+        if (st[i] < 0 || st[i] % 8 != 0) return false;
+    return true;
+}
+
+// What can be told from the cache descriptor's values alone.
+int check_cache(const sv_paged_cache *c) {
+    if (!c) return SV_EINVAL;
+    if (c->B < 0 || c->tokens < 0 || c->kv_heads < 1 || c->head_dim < 8 ||
+        c->head_dim > sv::kMaxHeadDim || c->head_dim % 8 != 0 || c->page_size < 8 ||
+        c->page_size % 8 != 0 || c->num_pages < 1 || c->max_pages < 1 ||
+        (c->dtype != SV_BF16 && c->dtype != SV_F16))
+        return SV_EINVAL;
+    if ((int64_t)c->max_pages * c->page_size > (int64_t)INT32_MAX - 1024) return SV_EINVAL;
+    if (c->B == 0 || c->tokens == 0) return SV_OK;
+    if (!c->k || !c->v || !c->pages || !c->q_start || !c->kv_len || c->pages_stride < c->max_pages)
+        return SV_EINVAL;
+    return vec_ok(c->k, c->k_stride, 3) && vec_ok(c->v, c->v_stride, 3) ? SV_OK : SV_EINVAL;
+}
+
+// Checks where the workspace and the cache's arrays live, and fills in the
+// batch the device sees.
+int bind_cache(const sv_paged_cache *c, void *ws, size_t ws_bytes, sv::Batch &b) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0 ||
+        ws_bytes < sv_cache_workspace_size())
+        return SV_EWORKSPACE;
+    if (!on_device(ws)) return SV_EWORKSPACE;
+    if (!on_device(c->k) || !on_device(c->v) || !on_device(c->pages) || !on_device(c->q_start) ||
+        !on_device(c->kv_len))
+        return SV_EINVAL;
+    b.pages = c->pages;
+    b.pages_stride = c->pages_stride;
+    b.q_start = c->q_start;
+    b.kv_len = c->kv_len;
+    b.B = c->B;
+    b.tokens = c->tokens;
+    b.num_pages = c->num_pages;
+    b.page_size = c->page_size;
+    b.max_pages = c->max_pages;
+    b.status = static_cast<uint32_t *>(ws);
+    return SV_OK;
+}
+
+template <class T, int kVec>
+void launch_append(const sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
+                   cudaStream_t st) {
+    if (interleaved)
+        sv::append_kernel<T, kVec, true><<<grid, sv::kAppendThreads, 0, st>>>(A, per_block);
+    else
+        sv::append_kernel<T, kVec, false><<<grid, sv::kAppendThreads, 0, st>>>(A, per_block);
+}
+
+template <class T>
+void launch_append(const sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
+                   cudaStream_t st) {
+    // both halves of a rotated pair start on a pack: 16, 8 or 4 bytes
+    const int half = A.rot_dim / 2;
+    if (half % 8 == 0)
+        launch_append<T, 8>(A, interleaved, grid, per_block, st);
+    else if (half % 4 == 0)
+        launch_append<T, 4>(A, interleaved, grid, per_block, st);
+    else
+        launch_append<T, 2>(A, interleaved, grid, per_block, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sv_cache_workspace_size(void) { return kAlign; }
+
+int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_stride,
+                 const void *v, const int64_t *v_stride, const void *q, const int64_t *q_stride,
+                 void *q_out, const int64_t *q_out_stride, int32_t q_heads,
+                 const double *inv_freq, int32_t rot_dim, int32_t interleaved,
+                 const int32_t *positions, void *workspace, size_t workspace_bytes,
+                 sv_stream_t stream) {
+    sv::AppendParams A{};
+    int rc = check_cache(cache);
+    if (rc != SV_OK) return rc;
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 4 != 0 || (rot_dim > 0 && !inv_freq) ||
+        q_heads < 0 || (q == nullptr) != (q_heads == 0))
+        return SV_EINVAL;
+    if (cache->B == 0 || cache->tokens == 0) return SV_OK;
+    if (!k || !v || !k_stride || !v_stride || !vec_ok(k, k_stride, 2) || !vec_ok(v, v_stride, 2))
+        return SV_EINVAL;
+    if (q && (!q_out || !q_stride || !q_out_stride || !vec_ok(q, q_stride, 2) ||
+              !vec_ok(q_out, q_out_stride, 2)))
+        return SV_EINVAL;
+    if ((rc = bind_cache(cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!on_device(k) || !on_device(v) || (q && (!on_device(q) || !on_device(q_out))))
+        return SV_EINVAL;
+    if ((inv_freq && !on_device(inv_freq)) || (positions && !on_device(positions)))
+        return SV_EINVAL;
+    A.k = k;
+    A.v = v;
+    A.q = q;
+    A.q_out = q_out;
+    A.k_cache = cache->k;
+    A.v_cache = cache->v;
+    for (int i = 0; i < 2; ++i) {
+        A.k_st[i] = k_stride[i];
+        A.v_st[i] = v_stride[i];
+        if (q) {
+            A.q_st[i] = q_stride[i];
+            A.o_st[i] = q_out_stride[i];
+        }
+    }
+    for (int i = 0; i < 3; ++i) {
+        A.kc_st[i] = cache->k_stride[i];
+        A.vc_st[i] = cache->v_stride[i];
+    }
+    A.inv_freq = inv_freq;
+    A.positions = positions;
+    A.q_heads = q_heads;
+    A.kv_heads = cache->kv_heads;
+    A.head_dim = cache->head_dim;
+    A.rot_dim = rot_dim;
+    const int per_block = cache->tokens >= 16384 ? sv::kAppendTokens : 1;
+    const unsigned grid = (unsigned)((cache->tokens + per_block - 1) / per_block);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cache->dtype == SV_BF16)
+        launch_append<__nv_bfloat16>(A, interleaved != 0, grid, per_block, st);
+    else
+        launch_append<__half>(A, interleaved != 0, grid, per_block, st);
+    if (cudaGetLastError() != cudaSuccess) return SV_ECUDA;
+    g_last_grid = grid;
+    g_last_kernels = 1;
+    return SV_OK;
+}
+
+int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t *q_stride,
+                       void *out, const int64_t *out_stride, int32_t q_heads, float scale,
+                       int32_t window, void *workspace, size_t workspace_bytes,
+                       sv_stream_t stream) {
+    sv::AttendParams A{};
+    int rc = check_cache(cache);
+    if (rc != SV_OK) return rc;
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || !std::isfinite(scale) || window < 0)
+        return SV_EINVAL;
+    if (cache->B == 0 || cache->tokens == 0) return SV_OK;
+    if (!q || !out || !q_stride || !out_stride || !vec_ok(q, q_stride, 2) ||
+        !vec_ok(out, out_stride, 2))
+        return SV_EINVAL;
+    if ((rc = bind_cache(cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!on_device(q) || !on_device(out)) return SV_EINVAL;
+    A.q = q;
+    A.out = out;
+    A.k_cache = cache->k;
+    A.v_cache = cache->v;
+    for (int i = 0; i < 2; ++i) {
+        A.q_st[i] = q_stride[i];
+        A.o_st[i] = out_stride[i];
+    }
+    for (int i = 0; i < 3; ++i) {
+        A.kc_st[i] = cache->k_stride[i];
+        A.vc_st[i] = cache->v_stride[i];
+    }
+    A.q_heads = q_heads;
+    A.kv_heads = cache->kv_heads;
+    A.head_dim = cache->head_dim;
+    A.window = window;
+    A.scale = scale;
+    const int64_t warps = (int64_t)cache->tokens * q_heads;
+    const unsigned grid = (unsigned)((warps + 7) / 8);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cache->dtype == SV_BF16)
+        sv::attend_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(A);
+    else
+        sv::attend_kernel<__half><<<grid, 256, 0, st>>>(A);
+    if (cudaGetLastError() != cudaSuccess) return SV_ECUDA;
+    g_last_grid = grid;
+    g_last_kernels = 1;
+    return SV_OK;
+}
+
+}  // extern "C"

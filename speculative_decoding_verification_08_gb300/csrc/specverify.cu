@@ -15,6 +15,7 @@
 
 #include "sv_alpha.cuh"
 #include "sv_device.cuh"
+#include "sv_host.cuh"
 #include "sv_item.cuh"
 #include "sv_logits.cuh"
 #include "specverify.h"
@@ -72,11 +73,21 @@ static_assert(SV_TRACE_CTA_RECORDS == sv::kTraceCtaCap && SV_TRACE_RECORDS == sv
 #define SV_ITEM_SMALL_B_MIN_SEGS 8
 #endif
 
+thread_local int64_t svhost::g_last_grid = 0;
+thread_local int32_t svhost::g_last_kernels = 0;
+
 namespace {
 
-constexpr size_t kAlign = 256;
-
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+using svhost::g_last_grid;
+using svhost::g_last_kernels;
+using svhost::kAlign;
+using svhost::kOnDevice;
+using svhost::kOnHost;
+using svhost::kUnusable;
+using svhost::launch_dependent;
+using svhost::place;
+using svhost::Residence;
+using svhost::round_up;
 
 int64_t num_segments(int64_t V) { return (V + sv::kSeg - 1) / sv::kSeg; }
 
@@ -148,8 +159,6 @@ Layout layout(int32_t B, int32_t K, int64_t V) {
 }
 
 std::atomic<int32_t> g_ctas_per_sm{0};
-thread_local int64_t g_last_grid = 0;
-thread_local int32_t g_last_kernels = 0;
 
 struct DeviceInfo {
     int sms = 0;
@@ -250,25 +259,6 @@ bool logits_info(int *sms, int *task_occ, int *ring_occ) {
     *task_occ = cached_task[dev];
     *ring_occ = cached_ring[dev];
     return true;
-}
-
-// Launches kernel on stream st as a programmatic dependent of the previous
-// launch: it may be scheduled while that grid's CTAs retire and waits on the
-// device (griddepcontrol.wait) before it reads their results.
-template <class Kernel, class Args>
-int launch_dependent(Kernel kernel, unsigned grid, unsigned threads, size_t smem,
-                     const Args &P, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? SV_OK : SV_ECUDA;
 }
 
 bool aligned_rows(const float *base, int64_t stride) {
@@ -410,28 +400,6 @@ int prepare_state(const sv::Params &P, void *ws, cudaStream_t st) {
     k.K = P.K;
     k.V = P.V;
     return SV_OK;
-}
-
-// Where a pointer lives, as the runtime knows it: device (or managed) memory,
-// page-locked host memory the GPU reads over the host link, or neither
-// (pageable host memory, which the kernels must not be given).
-enum Residence { kOnDevice = 0, kOnHost = 1, kUnusable = 2 };
-
-template <class T>
-Residence place(T *&ptr) {
-    if (!ptr) return kOnDevice;
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
-        cudaGetLastError();
-        return kUnusable;
-    }
-    if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) return kOnDevice;
-    if (a.type != cudaMemoryTypeHost || !a.devicePointer) return kUnusable;
-    // the address the device uses for this page-locked block
-    const char *base = static_cast<const char *>(a.hostPointer);
-    const ptrdiff_t off = reinterpret_cast<const char *>(ptr) - base;
-    ptr = reinterpret_cast<T *>(static_cast<char *>(a.devicePointer) + off);
-    return kOnHost;
 }
 
 // Checks where every caller array lives and rewrites host addresses to their
@@ -764,6 +732,9 @@ const char *sv_status_string(int code) {
         case (int)SV_STATUS_TIMEOUT: return "a bounded wait inside a kernel gave up";
         case (int)SV_STATUS_BAD_VALUE:
             return "an input probability is negative, NaN or infinite (debug builds)";
+        case (int)SV_STATUS_BAD_PAGE: return "page id outside the cache";
+        case (int)SV_STATUS_BAD_LENGTH:
+            return "sequence lengths that do not fit the tokens or the page table";
         default: return "unknown code";
     }
 }
