@@ -16,6 +16,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, "sv_device.cuh"), os.path.join(CSRC, "sv
                      os.path.join(CSRC, "sv_trace.cuh"), os.path.join(CSRC, "sv_host.cuh"),
                      os.path.join(CSRC, "sv_cache.cuh"), os.path.join(CSRC, "sv_append.cuh"),
                      os.path.join(CSRC, "sv_attend.cuh"), os.path.join(CSRC, "sv_warp.cuh"),
+                     os.path.join(CSRC, "sv_tc.cuh"), os.path.join(CSRC, "sv_barrier.cuh"),
                      os.path.join(INCLUDE, "specverify.h")]
 LIBRARY = os.path.join(PKG, "libspecverify.so")
 

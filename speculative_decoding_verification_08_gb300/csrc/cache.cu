@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "specverify.h"
@@ -90,11 +92,101 @@ void launch_append(const sv::AppendParams &A, bool interleaved, unsigned grid, i
         launch_append<T, 2>(A, interleaved, grid, per_block, st);
 }
 
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (looked up once; the library does not link
+// libcuda).
+EncodeTiled encoder() {
+    static const EncodeTiled f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                             &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(fn);
+    }();
+    return f;
+}
+
+// A map of one cache for boxes of 64 values x one head x `piece` slots of a
+// page: [pages][slots][heads][values], whatever their order in memory.
+// Values past head_dim and pages outside the cache read as zeros.
+int box_map(CUtensorMap *map, const sv_paged_cache *c, void *base, const int64_t *stride,
+            int piece) {
+    const EncodeTiled encode = encoder();
+    if (!encode) return SV_ECUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->kv_heads,
+                                (cuuint64_t)c->page_size, (cuuint64_t)c->num_pages};
+    cuuint64_t bytes[3] = {(cuuint64_t)stride[2] * 2, (cuuint64_t)stride[1] * 2,
+                           (cuuint64_t)stride[0] * 2};
+    // the stride of an axis of length 1 means nothing: any valid one will do
+    for (int i = 0; i < 3; ++i)
+        if (dims[i + 1] == 1) bytes[i] = (cuuint64_t)c->head_dim * 2;
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)piece, 1}, step[4] = {1, 1, 1, 1};
+    const CUresult r = encode(
+        map, c->dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+        4, base, dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SV_OK : SV_EINVAL;
+}
+
+// SM count of the current device, queried once.
+int sm_count() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    static std::atomic<int> cached[64];
+    int n = cached[dev].load();
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cached[dev].store(n);
+    }
+    return n;
+}
+
+template <class T, int DP>
+int launch_attend(const sv::AttendParams &A, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                  cudaStream_t st) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ECUDA;
+    constexpr int bytes = sv::AttendSmem<DP>::kBytes;
+    static std::atomic<int> raised[64];
+    if (!raised[dev].load()) {
+        if (cudaFuncSetAttribute(sv::attend_kernel<T, DP>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return SV_ECUDA;
+        raised[dev].store(1);
+    }
+    const int sms = sm_count();
+    if (sms <= 0) return SV_ECUDA;
+    const unsigned grid = (unsigned)std::min(sms, sv::kAttendMaxCtas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(sv::kAttendThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, sv::attend_kernel<T, DP>, A, kmap, vmap) != cudaSuccess)
+        return SV_ECUDA;
+    g_last_grid = grid;
+    g_last_kernels = 1;
+    return SV_OK;
+}
+
 }  // namespace
 
 extern "C" {
 
-size_t sv_cache_workspace_size(void) { return kAlign; }
+size_t sv_cache_workspace_size(void) { return svhost::round_up(sv::kAttendWorkspace); }
 
 int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_stride,
                  const void *v, const int64_t *v_stride, const void *q, const int64_t *q_stride,
@@ -173,32 +265,30 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     if (!on_device(q) || !on_device(out)) return SV_EINVAL;
     A.q = q;
     A.out = out;
-    A.k_cache = cache->k;
-    A.v_cache = cache->v;
     for (int i = 0; i < 2; ++i) {
         A.q_st[i] = q_stride[i];
         A.o_st[i] = out_stride[i];
     }
-    for (int i = 0; i < 3; ++i) {
-        A.kc_st[i] = cache->k_stride[i];
-        A.vc_st[i] = cache->v_stride[i];
-    }
     A.q_heads = q_heads;
     A.kv_heads = cache->kv_heads;
+    A.group = q_heads / cache->kv_heads;
     A.head_dim = cache->head_dim;
     A.window = window;
-    A.scale = scale;
-    const int64_t warps = (int64_t)cache->tokens * q_heads;
-    const unsigned grid = (unsigned)((warps + 7) / 8);
+    A.piece = 8;
+    while (A.piece < sv::kKeys && cache->page_size % (2 * A.piece) == 0) A.piece *= 2;
+    A.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504f;
+    A.q_mode = scale == 0.f ? 2 : scale < 0.f ? 1 : 0;
+    A.workspace = static_cast<char *>(workspace);
+    CUtensorMap kmap, vmap;
+    if ((rc = box_map(&kmap, cache, cache->k, cache->k_stride, A.piece)) != SV_OK) return rc;
+    if ((rc = box_map(&vmap, cache, cache->v, cache->v_stride, A.piece)) != SV_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cache->dtype == SV_BF16)
-        sv::attend_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(A);
-    else
-        sv::attend_kernel<__half><<<grid, 256, 0, st>>>(A);
-    if (cudaGetLastError() != cudaSuccess) return SV_ECUDA;
-    g_last_grid = grid;
-    g_last_kernels = 1;
-    return SV_OK;
+    const bool bf16 = cache->dtype == SV_BF16;
+    if (cache->head_dim > 64)
+        return bf16 ? launch_attend<__nv_bfloat16, 128>(A, kmap, vmap, st)
+                    : launch_attend<__half, 128>(A, kmap, vmap, st);
+    return bf16 ? launch_attend<__nv_bfloat16, 64>(A, kmap, vmap, st)
+                : launch_attend<__half, 64>(A, kmap, vmap, st);
 }
 
 }  // extern "C"

@@ -1,69 +1,828 @@
-// sv_attend.cuh -- attention of new tokens over the paged cache.
+// sv_attend.cuh -- attention of new tokens over the paged cache, on the
+// fifth-generation tensor cores.
+//
+// Rows.  A kv head's queries are packed token by token, the G = q_heads /
+// kv_heads heads of a token side by side: packed row j * G + g.  Every key and
+// value is then read once for all G heads.  A tile is up to 256 packed rows of
+// one (sequence, kv head), worked by two softmax groups of 128 threads, one
+// thread per row:
+//   pair tiles (more than 128 rows): group g has rows 128 g .. 128 g + 127 and
+//     both walk all key blocks;
+//   split tiles (up to 128 rows, rounds and single tokens): both groups have
+//     the same rows and take the even and the odd key blocks; their softmax
+//     states are joined at the end.
+// A key block is 128 slots.  Per group and block: S = Q K^T (128 x 128 fp32 in
+// tensor memory), the group's threads turn their rows of S into weights P
+// (running maximum and sum in registers, fp32), written over S in 16 bits, and
+// O += P V accumulates in tensor memory.  While one group computes weights the
+// tensor cores work for the other.
+//
+// Running maximum.  Weights are taken relative to a reference that follows the
+// maximum only when it has grown by more than 2^8: up to that the weights stay
+// below 256, which no type here overflows, and the 128 x head_dim rescaling of
+// O is skipped for nearly all blocks.  P rounded to 16 bits is the one
+// rounding between fp32 scores and the result; the sum is of the unrounded
+// weights.
+//
+// Work split.  A tile costs its key blocks.  The batch's blocks in a fixed
+// order (sequence, tile, head, block) are cut into equal runs, one per CTA, so
+// every SM gets the same number of blocks whatever the lengths.  A tile cut
+// between CTAs leaves partial states (unnormalised O, reference, sum) in the
+// workspace, and the last CTA of a tile to arrive joins them in order: results
+// do not depend on timing.
+//
+// Warps 0-7 softmax (208 registers a thread), 8 copies (one TMA box per page piece and 64 values of a
+// head, 128-byte swizzle), 9 issues the products.  Every wait is bounded; when
+// one gives up the CTA runs through its remaining steps without waiting,
+// copying or multiplying, and reports SV_STATUS_TIMEOUT.
 #pragma once
 
 #include "sv_append.cuh"
 #include "sv_cache.cuh"
+#include "sv_tc.cuh"
 
 namespace sv {
 
+constexpr int kAttendThreads = 384;
+// Registers per thread after the roles part: 256 softmax threads and 128 others
+// share the 384 x 168 that the block is launched with.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kAttendThreads * 168, "register split");
+constexpr int kRows = 128;           // packed rows per softmax group
+constexpr int kKeys = 128;           // slots per key block
+constexpr int kAttendMaxCtas = 160;  // partial states the workspace holds room for
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleAbove = 8.f;  // log2
+
+// Workspace: header (status), tile counters [ctas][2], partial statistics
+// [ctas * 2 slots][2 groups][128 rows] (reference, sum), partial O
+// [ctas * 2][32 column quads][256 rows] float4.
+constexpr size_t kAttendCounters = 256;
+constexpr size_t kAttendStats = kAttendCounters + 2 * 4 * 256;
+constexpr size_t kAttendOut = kAttendStats + (size_t)kAttendMaxCtas * 2 * 2 * kRows * sizeof(float2);
+constexpr size_t kAttendWorkspace =
+    kAttendOut + (size_t)kAttendMaxCtas * 2 * (kMaxHeadDim / 4) * 2 * kRows * sizeof(float4);
+
 struct AttendParams {
     Batch batch;
-    const void *q, *k_cache, *v_cache;
+    const void *q;
     void *out;
-    int64_t q_st[2], o_st[2], kc_st[3], vc_st[3];
-    int32_t q_heads, kv_heads, head_dim, window;
-    float scale;
+    int64_t q_st[2], o_st[2];
+    int32_t q_heads, kv_heads, group, head_dim, window;
+    int32_t piece;      // slots per copied box: the largest power of two in page_size, <= 128
+    float scale_log2;   // |scale| * log2(e); the sign goes into q
+    int32_t q_mode;     // 0: q, 1: -q, 2: zeros (scale 0)
+    char *workspace;
 };
 
-// One warp per (token, query head): the running maximum and sum of the
-// softmax over one key at a time, lanes over the head's values.
-template <class T>
-__global__ void __launch_bounds__(256) attend_kernel(const __grid_constant__ AttendParams A) {
-    const int lane = threadIdx.x % 32;
-    const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (w >= (int64_t)A.batch.tokens * A.q_heads) return;
-    const int32_t t = (int32_t)(w / A.q_heads), h = (int32_t)(w - (int64_t)t * A.q_heads);
-    const int32_t b = find_sequence(A.batch.q_start, A.batch.B, t, lane);
-    if (b < 0) return;
-    const Sequence s = load_sequence(A.batch, b);
-    if (s.bad) {
-        if (lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_LENGTH);
-        return;
+template <int DP>
+struct AttendSmem {
+    static constexpr int kTile = kRows * DP * 2;  // a Q tile, a K or V block
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kMisc = 1024;
+    static constexpr int kBytes = kMisc + (2 + kStages) * kTile + 1024;
+};
+
+// ---------------------------------------------------------------------------
+// the split of the work
+
+struct SeqCost {
+    int32_t n, len, row0, tiles;
+    int32_t G, window;
+    __device__ __forceinline__ void load(const AttendParams &A, int32_t b) {
+        const Sequence s = load_sequence(A.batch, b);
+        n = s.n;
+        len = s.len;
+        row0 = s.row0;
+        G = A.group;
+        window = A.window;
+        tiles = (int32_t)(((int64_t)n * G + 2 * kRows - 1) / (2 * kRows));
     }
-    const int32_t j = t - s.row0;
-    if (j < 0 || j >= s.n) return;
-    const int32_t g = h / (A.q_heads / A.kv_heads);
-    const T *q = static_cast<const T *>(A.q) + t * A.q_st[0] + h * A.q_st[1];
-    float qv[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < 4; ++i)
-        qv[i] = lane + 32 * i < A.head_dim ? to_f32<T>(q[lane + 32 * i]) * A.scale : 0.f;
-    const int32_t last = s.len - s.n + j;
-    const int32_t first = A.window > 0 ? max(0, last - A.window + 1) : 0;
-    float m = -INFINITY, l = 0.f;
-    for (int32_t x = first; x <= last; ++x) {
-        const int32_t pg = x / A.batch.page_size, at = x - pg * A.batch.page_size;
-        const int32_t id = __ldg(A.batch.pages + b * A.batch.pages_stride + pg);
-        const bool ok = id >= 0 && id < A.batch.num_pages;
-        if (!ok && lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_PAGE);
-        const T *k = static_cast<const T *>(A.k_cache) + id * A.kc_st[0] + at * A.kc_st[1] +
-                     g * A.kc_st[2];
-        const T *v = static_cast<const T *>(A.v_cache) + id * A.vc_st[0] + at * A.vc_st[1] +
-                     g * A.vc_st[2];
-        float dot = 0.f;
-        for (int i = 0; i < 4; ++i)
-            if (ok && lane + 32 * i < A.head_dim) dot += qv[i] * to_f32<T>(k[lane + 32 * i]);
-        for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        const float mn = fmaxf(m, dot), keep = __expf(m - mn), p = __expf(dot - mn);
-        m = mn;
-        l = l * keep + p;
-        for (int i = 0; i < 4; ++i) {
-            o[i] *= keep;
-            if (ok && lane + 32 * i < A.head_dim) o[i] += p * to_f32<T>(v[lane + 32 * i]);
+    __device__ __forceinline__ int rows(int t) const {
+        return (int)min((int64_t)(2 * kRows), (int64_t)n * G - (int64_t)t * 2 * kRows);
+    }
+    // key blocks [lo, hi) that tile t's rows see, and one past its last slot
+    __device__ __forceinline__ void blocks(int t, int &lo, int &hi, int &end) const {
+        const int64_t r0 = (int64_t)t * 2 * kRows;
+        const int jlo = (int)(r0 / G), jhi = (int)((r0 + rows(t) - 1) / G);
+        end = max(0, len - n + jhi + 1);
+        hi = (end + kKeys - 1) / kKeys;
+        lo = window > 0 ? max(0, len - n + jlo - window + 1) / kKeys : 0;
+        if (lo > hi) lo = hi;
+    }
+    __device__ __forceinline__ int cost(int t) const {
+        int lo, hi, end;
+        blocks(t, lo, hi, end);
+        return max(1, hi - lo);
+    }
+};
+
+struct Piece {
+    int32_t b, h, tile, rows;  // rows of the whole tile
+    int32_t lo, hi;            // its key blocks, this CTA's part
+    int32_t end;               // one past the tile's last slot
+    int32_t first;             // CTA that holds the tile's start
+    int32_t parts;             // CTAs that share the tile
+    bool split;                // split tile
+    int32_t n0, n1;            // blocks of group 0 and 1
+    __device__ __forceinline__ int block(int g, int i) const {
+        return split ? lo + 2 * i + g : lo + i;
+    }
+};
+
+// Walks one CTA's run of the work, the same way in every warp.
+struct Walker {
+    SeqCost s;
+    int32_t b, t, h, off;
+    int64_t left, unit, total;
+    int32_t ctas;
+
+    __device__ __forceinline__ void start(const AttendParams &A, int32_t b0, int64_t skip,
+                                          int64_t unit0, int64_t count, int64_t total_,
+                                          int32_t ctas_) {
+        b = b0;
+        left = count;
+        unit = unit0;
+        total = total_;
+        ctas = ctas_;
+        t = h = off = 0;
+        if (left <= 0) return;
+        s.load(A, b);
+        for (; t < s.tiles; ++t) {
+            const int64_t c = (int64_t)s.cost(t) * A.kv_heads;
+            if (skip < c) break;
+            skip -= c;
+        }
+        const int c = s.cost(t);
+        h = (int32_t)(skip / c);
+        off = (int32_t)(skip - (int64_t)h * c);
+    }
+
+    __device__ __forceinline__ int32_t cta_of(int64_t u) const {
+        return (int32_t)(((u + 1) * ctas - 1) / total);
+    }
+
+    __device__ __forceinline__ bool next(const AttendParams &A, Piece &p) {
+        if (left <= 0) return false;
+        while (t >= s.tiles) {
+            if (++b >= A.batch.B) return false;
+            s.load(A, b);
+            t = h = off = 0;
+        }
+        int lo, hi, end;
+        s.blocks(t, lo, hi, end);
+        const int cost = max(1, hi - lo);
+        const int take = (int)min(left, (int64_t)(cost - off));
+        p.b = b;
+        p.h = h;
+        p.tile = t;
+        p.rows = s.rows(t);
+        p.end = end;
+        p.lo = lo + off;
+        p.hi = min(hi, lo + off + take);
+        p.split = p.rows <= kRows;
+        const int nb = p.hi - p.lo;
+        p.n0 = p.split ? (nb + 1) / 2 : nb;
+        p.n1 = p.split ? nb / 2 : nb;
+        p.first = cta_of(unit - off);
+        p.parts = cta_of(unit - off + cost - 1) - p.first + 1;
+        left -= take;
+        unit += take;
+        off += take;
+        if (off >= cost) {
+            off = 0;
+            if (++h >= A.kv_heads) {
+                h = 0;
+                ++t;
+            }
+        }
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------
+
+struct AttendShared {
+    unsigned long long full[8], empty[8];
+    unsigned long long s_full[2], p_full[2], o_full[2], q_full[2], drain;
+    uint32_t tmem;
+    int32_t dead, b0, last[2];
+    int64_t skip, total;
+    int64_t sums[kAttendThreads / 32];
+};
+static_assert(sizeof(AttendShared) <= 1024, "misc region");
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A wait that gives up for the whole CTA.
+__device__ __forceinline__ bool hold(AttendShared &sh, unsigned long long *bar, uint32_t parity,
+                                     uint32_t *status) {
+    if (*(volatile int32_t *)&sh.dead) return false;
+    if (mbar_wait(bar, parity)) return true;
+    *(volatile int32_t *)&sh.dead = 1;
+    atomicOr(status, SV_STATUS_TIMEOUT);
+    return false;
+}
+
+// Cost of sequence b's tiles over all heads, for each lane's own b (< 0: none).
+__device__ __forceinline__ int64_t sequence_cost(const AttendParams &A, int32_t b, int lane) {
+    SeqCost s;
+    s.n = s.tiles = 0;
+    if (b >= 0) s.load(A, b);
+    int64_t c = 0;
+    if (s.tiles <= 2)
+        for (int t = 0; t < s.tiles; ++t) c += s.cost(t);
+    // long prompts: the whole warp adds up one lane's tiles
+    unsigned long_ones = __ballot_sync(0xffffffffu, s.tiles > 2);
+    while (long_ones) {
+        const int who = __ffs(long_ones) - 1;
+        long_ones &= long_ones - 1;
+        SeqCost o;
+        o.n = __shfl_sync(0xffffffffu, s.n, who);
+        o.len = __shfl_sync(0xffffffffu, s.len, who);
+        o.tiles = __shfl_sync(0xffffffffu, s.tiles, who);
+        o.G = A.group;
+        o.window = A.window;
+        int64_t x = 0;
+        for (int t = lane; t < o.tiles; t += 32) x += o.cost(t);
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (lane == who) c = x;
+    }
+    return c * A.kv_heads;
+}
+
+template <class T, int DP>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+    attend_kernel(const __grid_constant__ AttendParams A, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+    typedef AttendSmem<DP> L;
+    constexpr bool kBf16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
+    constexpr int kHalves = DP / 64;
+    constexpr int kHalfBytes = kKeys * 128;
+    constexpr uint32_t kIdescS = tc::instr_desc(kBf16, false, kRows, kKeys);
+    constexpr uint32_t kIdescO = tc::instr_desc(kBf16, true, kRows, DP);
+    extern __shared__ char raw[];
+    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    AttendShared &sh = *reinterpret_cast<AttendShared *>(smem);
+    char *sq = smem + L::kMisc;
+    char *ring = sq + 2 * L::kTile;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    uint32_t *status = A.batch.status;
+
+    if (warp == 9) tc::tmem_alloc(&sh.tmem, kTmemCols);
+    if (tid == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&sh.s_full[g], 1);
+            mbar_init(&sh.p_full[g], 4);
+            mbar_init(&sh.o_full[g], 1);
+            mbar_init(&sh.q_full[g], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.dead = 0;
+        sh.b0 = -1;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    wait_for_primary_grid();
+
+    // the batch's blocks, and where this CTA's run of them begins
+    int64_t c = 0;
+    for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
+        const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
+        c += sequence_cost(A, b, lane);
+        if (blockIdx.x == 0 && b >= 0 && load_sequence(A.batch, b).bad)
+            atomicOr(status, SV_STATUS_BAD_LENGTH);
+    }
+    for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+    if (lane == 0) sh.sums[warp] = c;
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    int64_t total = 0;
+    for (int w = 0; w < kAttendThreads / 32; ++w) total += sh.sums[w];
+    const int32_t ctas = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, total));
+    const int64_t u0 = (int64_t)blockIdx.x * total / ctas, u1 = ((int64_t)blockIdx.x + 1) * total / ctas;
+    const bool idle = total == 0 || (int32_t)blockIdx.x >= ctas || u0 >= u1;
+    if (!idle) {
+        int64_t base = 0;
+        for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
+            const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
+            const int64_t own = sequence_cost(A, b, lane);
+            int64_t inc = own;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += o;
+            }
+            __syncthreads();
+            if (lane == 31) sh.sums[warp] = inc;
+            __syncthreads();
+            int64_t at = base;
+            for (int w = 0; w < kAttendThreads / 32; ++w) {
+                if (w < warp) at += sh.sums[w];
+                base += sh.sums[w];
+            }
+            if (own > 0 && at + inc - own <= u0 && u0 < at + inc) {
+                sh.b0 = b;
+                sh.skip = u0 - (at + inc - own);
+            }
+            if (base > u0) break;
+        }
+        __syncthreads();
+    }
+    const uint32_t tmem = sh.tmem;
+
+    Walker walk;
+    if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas);
+    else walk.left = 0;
+    Piece p;
+
+    if (warp >= 8)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+
+    if (warp == 8) {
+        // ---- copies -------------------------------------------------------
+        const int pieces = kKeys / A.piece;
+        const int mine = lane % pieces, half = lane / pieces;
+        const bool active = half < kHalves;
+        int it = 0;
+        while (walk.next(A, p)) {
+            const int64_t table = p.b * A.batch.pages_stride;
+            const int first = A.window > 0 ? max(0, walk.s.len - walk.s.n +
+                                                        (int)((int64_t)p.tile * 2 * kRows / A.group) -
+                                                        A.window + 1)
+                                           : 0;
+            auto load = [&](const CUtensorMap &map, int kb) {
+                const int st = it % L::kStages;
+                const int s0 = kb * kKeys + mine * A.piece;
+                int id = A.batch.num_pages, at = 0;  // outside the cache: zeros
+                if (active && s0 < p.end && s0 + A.piece > first) {
+                    const int pg = s0 / A.batch.page_size;
+                    at = s0 - pg * A.batch.page_size;
+                    id = __ldg(A.batch.pages + table + pg);
+                    if (id < 0 || id >= A.batch.num_pages) {
+                        atomicOr(status, SV_STATUS_BAD_PAGE);
+                        id = A.batch.num_pages;
+                    }
+                }
+                const bool ok = hold(sh, &sh.empty[st], ((it / L::kStages) & 1) ^ 1, status);
+                if (__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], L::kTile);
+                    __syncwarp();
+                    if (active)
+                        tc::load_box(ring + st * L::kTile + half * kHalfBytes + mine * A.piece * 128,
+                                     &map, half * 64, p.h, at, id, &sh.full[st]);
+                    ++it;
+                }
+            };
+            if (p.n0 == 0) continue;
+            if (p.split) {
+                load(kmap, p.block(0, 0));
+                if (p.n1 > 0) load(kmap, p.block(1, 0));
+                for (int i = 0; i < p.n0; ++i) {
+                    load(vmap, p.block(0, i));
+                    if (i + 1 < p.n0) load(kmap, p.block(0, i + 1));
+                    if (i < p.n1) {
+                        load(vmap, p.block(1, i));
+                        if (i + 1 < p.n1) load(kmap, p.block(1, i + 1));
+                    }
+                }
+            } else {
+                load(kmap, p.block(0, 0));
+                for (int i = 0; i < p.n0; ++i) {
+                    load(vmap, p.block(0, i));
+                    if (i + 1 < p.n0) load(kmap, p.block(0, i + 1));
+                }
+            }
+        }
+        // the last fills must have been taken before the CTA may end; after a
+        // wait gave up, they must at least have landed
+        if (*(volatile int32_t *)&sh.dead) {
+            for (int k = max(0, it - L::kStages); k < it; ++k)
+                mbar_wait(&sh.full[k % L::kStages], (k / L::kStages) & 1);
+        } else {
+            for (int k = max(0, it - L::kStages); k < it; ++k)
+                hold(sh, &sh.empty[k % L::kStages], (k / L::kStages) & 1, status);
+        }
+    } else if (warp == 9) {
+        // ---- products -----------------------------------------------------
+        int it = 0;
+        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
+        const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(sq);
+        auto acquire = [&]() -> int {  // the next stage, filled
+            const int st = it % L::kStages;
+            hold(sh, &sh.full[st], (it / L::kStages) & 1, status);
+            ++it;
+            return st;
+        };
+        auto alive = [&]() -> bool {
+            return __all_sync(0xffffffffu, *(volatile int32_t *)&sh.dead == 0);
+        };
+        auto release = [&](int st) {
+            if (alive() && lane == 0) tc::commit(&sh.empty[st]);
+        };
+        auto scores = [&](int g, int st) {  // S_g = Q_g K^T
+            if (alive() && lane == 0) {
+                tc::fence_after();
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t at = (k / 4) * kHalfBytes + (k % 4) * 32;
+                    tc::mma_ss(tmem + g * kKeys,
+                               tc::smem_desc(q_at + g * L::kTile + at, 16, 1024),
+                               tc::smem_desc(ring_at + st * L::kTile + at, 16, 1024), kIdescS,
+                               k > 0);
+                }
+                tc::commit(&sh.s_full[g]);
+            }
+            __syncwarp();
+        };
+        auto values = [&](int g, int st, bool add) {  // O_g (+)= P_g V
+            hold(sh, &sh.p_full[g], pn[g]++ & 1, status);
+            if (alive() && lane == 0) {
+                tc::fence_after();
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    tc::mma_ts(tmem + 2 * kKeys + g * 128, tmem + g * kKeys + k * 8,
+                               tc::smem_desc(ring_at + st * L::kTile + k * 2048, kHalfBytes, 1024),
+                               kIdescO, add || k > 0);
+            }
+            __syncwarp();
+        };
+        // slots past the tile's last one in a page that holds it: their weights
+        // are zero, and zero times whatever lies there must be zero
+        auto clear_tail = [&](int st, int kb) {
+            const int r0 = p.end - kb * kKeys;
+            if (r0 >= kKeys || r0 <= 0) return;
+            const int r1 = min(kKeys, (r0 + A.piece - 1) / A.piece * A.piece);
+            if (r0 == r1) return;
+            char *v = ring + st * L::kTile;
+            for (int i = lane; i < (r1 - r0) * 8 * kHalves; i += 32) {
+                const int half = i / ((r1 - r0) * 8), x = i - half * (r1 - r0) * 8;
+                *reinterpret_cast<uint4 *>(v + half * kHalfBytes + r0 * 128 + x * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+        };
+        while (walk.next(A, p)) {
+            if (p.n0 == 0) continue;
+            hold(sh, &sh.q_full[0], qn[0]++ & 1, status);
+            if (p.split) {
+                int st = acquire();
+                scores(0, st);
+                release(st);
+                if (p.n1 > 0) {
+                    hold(sh, &sh.q_full[1], qn[1]++ & 1, status);
+                    st = acquire();
+                    scores(1, st);
+                    release(st);
+                }
+                for (int i = 0; i < p.n0; ++i)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int ng = g ? p.n1 : p.n0;
+                        if (i >= ng) continue;
+                        st = acquire();
+                        clear_tail(st, p.block(g, i));
+                        values(g, st, i > 0);
+                        release(st);
+                        if (i + 1 < ng) {
+                            st = acquire();
+                            scores(g, st);
+                            release(st);
+                        } else if (alive() && lane == 0) {
+                            tc::commit(&sh.o_full[g]);
+                        }
+                    }
+            } else {
+                hold(sh, &sh.q_full[1], qn[1]++ & 1, status);
+                int ks = acquire();
+                scores(0, ks);
+                scores(1, ks);
+                release(ks);
+                for (int i = 0; i < p.n0; ++i) {
+                    const int vs = acquire();
+                    clear_tail(vs, p.block(0, i));
+                    const bool more = i + 1 < p.n0;
+                    values(0, vs, i > 0);
+                    if (more) {
+                        ks = acquire();
+                        scores(0, ks);
+                    } else if (alive() && lane == 0) {
+                        tc::commit(&sh.o_full[0]);
+                    }
+                    values(1, vs, i > 0);
+                    release(vs);
+                    if (more) {
+                        scores(1, ks);
+                        release(ks);
+                    } else if (alive() && lane == 0) {
+                        tc::commit(&sh.o_full[1]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) tc::commit(&sh.drain);
+        __syncwarp();
+        mbar_wait(&sh.drain, 0);
+    } else if (warp < 8) {
+        // ---- softmax ------------------------------------------------------
+        const int g = warp / 4, gt = tid - g * 128, gw = warp % 4;
+        const uint32_t lanes = (uint32_t)(gw * 32) << 16;
+        const uint32_t t_s = tmem + lanes + g * kKeys;
+        const uint32_t t_o[2] = {tmem + lanes + 2 * kKeys, tmem + lanes + 2 * kKeys + 128};
+        uint32_t sn = 0, on[2] = {0, 0};
+        char *q_s = sq + g * L::kTile;
+        float2 *stats[2] = {reinterpret_cast<float2 *>(sq), reinterpret_cast<float2 *>(sq + L::kTile)};
+        float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
+        float4 *part_out = reinterpret_cast<float4 *>(A.workspace + kAttendOut);
+        uint32_t *counters = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters);
+        const int D = A.head_dim;
+
+        while (walk.next(A, p)) {
+            const int n = walk.s.n, len = walk.s.len, row0 = walk.s.row0;
+            const int steps = g ? p.n1 : p.n0;
+            const int64_t r_base = (int64_t)p.tile * 2 * kRows + (p.split ? 0 : g * kRows);
+            const int rows = p.split ? p.rows : min(kRows, p.rows - g * kRows);
+            if (steps > 0) {
+                for (int i = gt; i < rows * (DP / 8); i += 128) {
+                    const int r = i / (DP / 8), ch = i - r * (DP / 8);
+                    const int64_t pr = r_base + r;
+                    const int64_t j = pr / A.group;
+                    const int64_t hq = (int64_t)p.h * A.group + (pr - j * A.group);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (ch * 8 < D && A.q_mode != 2)
+                        x = __ldg(reinterpret_cast<const uint4 *>(
+                            static_cast<const uint16_t *>(A.q) + (row0 + j) * A.q_st[0] +
+                            hq * A.q_st[1] + ch * 8));
+                    if (A.q_mode == 1) {
+                        x.x ^= 0x80008000u;
+                        x.y ^= 0x80008000u;
+                        x.z ^= 0x80008000u;
+                        x.w ^= 0x80008000u;
+                    }
+                    *reinterpret_cast<uint4 *>(q_s + (ch / 8) * kHalfBytes + r * 128 +
+                                               (((ch % 8) ^ (r & 7)) * 16)) = x;
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full[g]);
+            }
+            const bool mine = gw * 32 + lane < rows;       // this thread's row exists
+            const bool any = gw * 32 < rows;               // one of the warp's does
+            const int64_t pr = r_base + gw * 32 + lane;
+            const int limit = mine ? len - n + (int)(pr / A.group) : len;  // last slot it sees
+            const int lowest = A.window > 0 ? limit - A.window + 1 : 0;
+            float ref = -INFINITY, sum = 0.f;
+            for (int i = 0; i < steps; ++i) {
+                const bool ok = hold(sh, &sh.s_full[g], sn++ & 1, status);
+                if (any && __all_sync(0xffffffffu, ok)) {
+                    tc::fence_after();
+                    const int k0 = p.block(g, i) * kKeys;
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc::ld32(x[q], t_s + 32 * q);
+                    tc::wait_ld();
+                    if (__any_sync(0xffffffffu, mine && (k0 + kKeys - 1 > limit || k0 < lowest))) {
+                        const int hi = limit - k0, lo = lowest - k0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * q + e > hi || 32 * q + e < lo) x[q][e] = 0xff800000u;
+                    }
+                    float m = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            m = fmaxf(m, __uint_as_float(x[q][e]));
+                            m1 = fmaxf(m1, __uint_as_float(x[q][e + 1]));
+                        }
+                    m = fmaxf(m, m1) * A.scale_log2;
+                    const bool grow = mine && (m > ref + kRescaleAbove || (ref == -INFINITY && m > ref));
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float to = grow ? m : ref;
+                        const float a = ref == -INFINITY ? 0.f : ex2(ref - to);
+                        if (i > 0 && __any_sync(0xffffffffu, grow && ref != -INFINITY)) {
+                            const float f = grow ? a : 1.f;
+#pragma unroll
+                            for (int q = 0; q < DP / 32; ++q) {
+                                uint32_t o[32];
+                                tc::ld32(o, t_o[g] + 32 * q);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::st32(t_o[g] + 32 * q, o);
+                            }
+                        }
+                        if (grow) sum *= a;
+                        ref = to;
+                    }
+                    const float minus = ref == -INFINITY ? 0.f : -ref;
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float a = ex2(fmaf(__uint_as_float(x[q + e / 16][2 * (e % 16)]),
+                                                     A.scale_log2, minus));
+                            const float b = ex2(fmaf(__uint_as_float(x[q + e / 16][2 * (e % 16) + 1]),
+                                                     A.scale_log2, minus));
+                            s0 += a;
+                            s1 += b;
+                            w[e] = pack2<T>(a, b);
+                        }
+                        tc::st32(t_s + 16 * q, w);
+                    }
+                    sum += s0 + s1;
+                    tc::wait_st();
+                    tc::fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[g]);
+            }
+            const int n_of[2] = {p.n0, p.n1};
+            float a_of[2] = {1.f, 1.f};
+            if (p.split) {
+                // join the groups' states; group g then has half the columns
+                if (steps > 0) hold(sh, &sh.o_full[g], on[g]++ & 1, status);
+                if (n_of[1 - g] > 0) hold(sh, &sh.o_full[1 - g], on[1 - g]++ & 1, status);
+                stats[g][gt] = make_float2(ref, sum);
+                tc::named_barrier(1, 256);
+                const float2 o = stats[1 - g][gt];
+                const float to = fmaxf(ref, o.x);
+                a_of[g] = ref == -INFINITY ? 0.f : ex2(ref - to);
+                a_of[1 - g] = o.x == -INFINITY ? 0.f : ex2(o.x - to);
+                // group 0's part first on both sides
+                sum = g == 0 ? sum * a_of[0] + o.y * a_of[1] : o.y * a_of[0] + sum * a_of[1];
+                ref = to;
+            } else if (steps > 0) {
+                hold(sh, &sh.o_full[g], on[g]++ & 1, status);
+                // the other group's accumulators went through a phase too; this
+                // group next waits for them in a split tile, where its own
+                // phase (or the other's, for group 1) comes later in the
+                // order of the products
+                ++on[1 - g];
+            }
+            tc::fence_after();
+            const int c0 = p.split ? g * (DP / 2) : 0;      // this group's columns
+            const int c1 = p.split ? c0 + DP / 2 : DP;
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const int64_t j = pr / A.group;
+            uint16_t *out = static_cast<uint16_t *>(A.out) + (row0 + j) * A.o_st[0] +
+                            ((int64_t)p.h * A.group + (pr - j * A.group)) * A.o_st[1];
+            const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
+            if (any) {
+                for (int cc = c0; cc < c1; cc += 32) {
+                    float v[32];
+                    uint32_t o[32];
+                    if (p.split) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+                            if (n_of[s] > 0) {
+                                tc::ld32(o, t_o[s] + cc);
+                                tc::wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    v[e] += a_of[s] * __uint_as_float(o[e]);
+                            }
+                    } else if (steps > 0) {
+                        tc::ld32(o, t_o[g] + cc);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                    }
+                    if (p.parts > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            part_out[((int64_t)slot * (kMaxHeadDim / 4) + (cc + e) / 4) * 256 +
+                                     (p.split ? 0 : g * kRows) + gt] =
+                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    } else if (mine) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            if (cc + e < D) {
+                                uint4 y;
+                                y.x = pack2<T>(v[e] * inv, v[e + 1] * inv);
+                                y.y = pack2<T>(v[e + 2] * inv, v[e + 3] * inv);
+                                y.z = pack2<T>(v[e + 4] * inv, v[e + 5] * inv);
+                                y.w = pack2<T>(v[e + 6] * inv, v[e + 7] * inv);
+                                if (sum == 0.f) y = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(out + cc + e) = y;
+                            }
+                    }
+                }
+                tc::fence_before();
+            }
+            if (p.parts > 1) {
+                part_stats[(slot * 2 + g) * kRows + gt] = make_float2(ref, sum);
+                __threadfence();
+                tc::named_barrier(2 + g, 128);
+                if (gt == 0) {
+                    uint32_t *c = counters + 2 * p.first + g;
+                    const bool last = atomicAdd(c, 1u) == (uint32_t)p.parts - 1;
+                    if (last) *c = 0;
+                    sh.last[g] = last;
+                }
+                tc::named_barrier(2 + g, 128);
+                if (sh.last[g]) {
+                    __threadfence();
+                    // warps share the 32-row strips; a strip's warps share its columns
+                    const int strips = (rows + 31) / 32;
+                    const int per = strips == 1 ? 4 : strips == 2 ? 2 : 1;
+                    const int strip = gw / per, share = gw % per;
+                    const int wide = (c1 - c0) / per;
+                    const int r = strip * 32 + lane;
+                    const int64_t cr = r_base + r, cj = cr / A.group;
+                    uint16_t *co = static_cast<uint16_t *>(A.out) + (row0 + cj) * A.o_st[0] +
+                                   ((int64_t)p.h * A.group + (cr - cj * A.group)) * A.o_st[1];
+                    auto slot_of = [&](int i) -> int {
+                        return (p.first + i) * 2 + (i == 0 ? 1 : 0);
+                    };
+                    if (strip < strips) {
+                        float top = -INFINITY, all = 0.f;
+                        for (int i = 0; i < p.parts; ++i)
+                            top = fmaxf(top, __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]).x);
+                        for (int i = 0; i < p.parts; ++i) {
+                            const float2 x = __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]);
+                            all += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - top);
+                        }
+                        const float norm = all > 0.f ? 1.f / all : 0.f;
+                        for (int cc = c0 + share * wide; cc < c0 + (share + 1) * wide; cc += 8) {
+                            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                            for (int i = 0; i < p.parts; ++i) {
+                                const float m = __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]).x;
+                                const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                                const float4 *at =
+                                    part_out + ((int64_t)slot_of(i) * (kMaxHeadDim / 4) + cc / 4) * 256 +
+                                    (p.split ? 0 : g * kRows) + r;
+                                const float4 a = __ldcg(at), b = __ldcg(at + 256);
+                                v[0] += f * a.x;
+                                v[1] += f * a.y;
+                                v[2] += f * a.z;
+                                v[3] += f * a.w;
+                                v[4] += f * b.x;
+                                v[5] += f * b.y;
+                                v[6] += f * b.z;
+                                v[7] += f * b.w;
+                            }
+                            if (r < rows && cc < D) {
+                                uint4 y;
+                                y.x = pack2<T>(v[0] * norm, v[1] * norm);
+                                y.y = pack2<T>(v[2] * norm, v[3] * norm);
+                                y.z = pack2<T>(v[4] * norm, v[5] * norm);
+                                y.w = pack2<T>(v[6] * norm, v[7] * norm);
+                                if (all == 0.f) y = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(co + cc) = y;
+                            }
+                        }
+                    }
+                }
+            }
+            // the joined states have been read before the next piece reuses the
+            // query tiles and the accumulators
+            if (p.split) tc::named_barrier(1, 256);
         }
     }
-    T *out = static_cast<T *>(A.out) + t * A.o_st[0] + h * A.o_st[1];
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < A.head_dim) out[lane + 32 * i] = from_f32<T>(l > 0.f ? o[i] / l : 0.f);
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc::tmem_free(tmem, kTmemCols);
+    }
 }
 
 }  // namespace sv
