@@ -255,7 +255,8 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     sv::AttendParams A{};
     int rc = check_cache(cache);
     if (rc != SV_OK) return rc;
-    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || !std::isfinite(scale) || window < 0)
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || !std::isfinite(scale) || window < 0 ||
+        (int64_t)cache->tokens * (q_heads / cache->kv_heads) > INT32_MAX - 1024)
         return SV_EINVAL;
     if (cache->B == 0 || cache->tokens == 0) return SV_OK;
     if (!q || !out || !q_stride || !out_stride || !vec_ok(q, q_stride, 2) ||
@@ -272,6 +273,8 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     A.q_heads = q_heads;
     A.kv_heads = cache->kv_heads;
     A.group = q_heads / cache->kv_heads;
+    A.by_group.set((uint32_t)A.group);
+    A.by_page.set((uint32_t)cache->page_size);
     A.head_dim = cache->head_dim;
     A.window = window;
     A.piece = 8;

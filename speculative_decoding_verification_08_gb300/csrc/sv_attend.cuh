@@ -31,11 +31,13 @@
 // workspace, and the last CTA of a tile to arrive joins them in order: results
 // do not depend on timing.
 //
-// Warps 0-7 softmax (208 registers a thread), 8 copies (one TMA box per page piece and 64 values of a
+// Warps 0-7 softmax, 8 copies (one TMA box per page piece and 64 values of a
 // head, 128-byte swizzle), 9 issues the products.  Every wait is bounded; when
-// one gives up the CTA runs through its remaining steps without waiting,
-// copying or multiplying, and reports SV_STATUS_TIMEOUT.
+// one gives up the CTA runs through its remaining steps without waiting or
+// copying, on whatever its buffers hold, and reports SV_STATUS_TIMEOUT.
 #pragma once
+
+#include <type_traits>
 
 #include "sv_append.cuh"
 #include "sv_cache.cuh"
@@ -44,14 +46,11 @@
 namespace sv {
 
 constexpr int kAttendThreads = 384;
-// Registers per thread after the roles part: 256 softmax threads and 128 others
-// share the 384 x 168 that the block is launched with.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kAttendThreads * 168, "register split");
 constexpr int kRows = 128;           // packed rows per softmax group
 constexpr int kKeys = 128;           // slots per key block
 constexpr int kAttendMaxCtas = 160;  // partial states the workspace holds room for
 constexpr uint32_t kTmemCols = 512;
+constexpr int kNoPage = 0x7fffffff;  // outside every cache: its boxes read zeros
 constexpr float kRescaleAbove = 8.f;  // log2
 
 // Workspace: header (status), tile counters [ctas][2], partial statistics
@@ -63,8 +62,25 @@ constexpr size_t kAttendOut = kAttendStats + (size_t)kAttendMaxCtas * 2 * 2 * kR
 constexpr size_t kAttendWorkspace =
     kAttendOut + (size_t)kAttendMaxCtas * 2 * (kMaxHeadDim / 4) * 2 * kRows * sizeof(float4);
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: the high word of n m, shifted;
+// m = ceil(2^(31 + s) / d) with 2^s >= d, whose excess over the exact factor
+// is too small to reach the next integer for these n.
+struct FastDiv {
+    uint32_t d, m, s;
+    __host__ void set(uint32_t by) {
+        d = by;
+        s = 0;
+        while ((1ull << s) < by) ++s;
+        m = (uint32_t)(((1ull << (31 + s)) + by - 1) / by);
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return d == 1 ? n : (int)(__umulhi((uint32_t)n, m) >> (s - 1));
+    }
+};
+
 struct AttendParams {
     Batch batch;
+    FastDiv by_group, by_page;
     const void *q;
     void *out;
     int64_t q_st[2], o_st[2];
@@ -86,42 +102,41 @@ struct AttendSmem {
 // ---------------------------------------------------------------------------
 // the split of the work
 
+// A tile's fixed cost (queries in, states joined, rows out) in key blocks.
+constexpr int kTileCost = 2;
+
 struct SeqCost {
-    int32_t n, len, row0, tiles;
-    int32_t G, window;
+    int32_t n, len, row0, tiles, packed;  // packed: rows n * G
     __device__ __forceinline__ void load(const AttendParams &A, int32_t b) {
         const Sequence s = load_sequence(A.batch, b);
         n = s.n;
         len = s.len;
         row0 = s.row0;
-        G = A.group;
-        window = A.window;
-        tiles = (int32_t)(((int64_t)n * G + 2 * kRows - 1) / (2 * kRows));
+        packed = n * A.group;  // the host checks that it fits
+        tiles = (packed + 2 * kRows - 1) / (2 * kRows);
     }
-    __device__ __forceinline__ int rows(int t) const {
-        return (int)min((int64_t)(2 * kRows), (int64_t)n * G - (int64_t)t * 2 * kRows);
-    }
+    __device__ __forceinline__ int rows(int t) const { return min(2 * kRows, packed - t * 2 * kRows); }
     // key blocks [lo, hi) that tile t's rows see, and one past its last slot
-    __device__ __forceinline__ void blocks(int t, int &lo, int &hi, int &end) const {
-        const int64_t r0 = (int64_t)t * 2 * kRows;
-        const int jlo = (int)(r0 / G), jhi = (int)((r0 + rows(t) - 1) / G);
-        end = max(0, len - n + jhi + 1);
+    __device__ __forceinline__ void blocks(const AttendParams &A, int t, int &lo, int &hi,
+                                           int &end) const {
+        const int r0 = t * 2 * kRows;
+        end = max(0, len - n + A.by_group.div(r0 + rows(t) - 1) + 1);
         hi = (end + kKeys - 1) / kKeys;
-        lo = window > 0 ? max(0, len - n + jlo - window + 1) / kKeys : 0;
-        if (lo > hi) lo = hi;
+        lo = A.window > 0 ? max(0, len - n + A.by_group.div(r0) - A.window + 1) / kKeys : 0;
+        lo = min(lo, hi);
     }
-    __device__ __forceinline__ int cost(int t) const {
+    __device__ __forceinline__ int cost(const AttendParams &A, int t) const {
         int lo, hi, end;
-        blocks(t, lo, hi, end);
-        return max(1, hi - lo);
+        blocks(A, t, lo, hi, end);
+        return kTileCost + max(1, hi - lo);
     }
 };
 
 struct Piece {
     int32_t b, h, tile, rows;  // rows of the whole tile
-    int32_t lo, hi;            // its key blocks, this CTA's part
+    int32_t lo, n;             // this CTA's key blocks
     int32_t end;               // one past the tile's last slot
-    int32_t first;             // CTA that holds the tile's start
+    int32_t first;             // CTA that holds the tile's first block
     int32_t parts;             // CTAs that share the tile
     bool split;                // split tile
     int32_t n0, n1;            // blocks of group 0 and 1
@@ -130,7 +145,7 @@ struct Piece {
     }
 };
 
-// Walks one CTA's run of the work, the same way in every warp.
+// Walks one CTA's run of the work, the same way in every warp (whole warps).
 struct Walker {
     SeqCost s;
     int32_t b, t, h, off;
@@ -139,7 +154,7 @@ struct Walker {
 
     __device__ __forceinline__ void start(const AttendParams &A, int32_t b0, int64_t skip,
                                           int64_t unit0, int64_t count, int64_t total_,
-                                          int32_t ctas_) {
+                                          int32_t ctas_, int lane) {
         b = b0;
         left = count;
         unit = unit0;
@@ -148,12 +163,23 @@ struct Walker {
         t = h = off = 0;
         if (left <= 0) return;
         s.load(A, b);
-        for (; t < s.tiles; ++t) {
-            const int64_t c = (int64_t)s.cost(t) * A.kv_heads;
-            if (skip < c) break;
-            skip -= c;
+        for (;; t += 32) {  // the tile that unit `skip` of the sequence lies in
+            const int64_t own = t + lane < s.tiles ? (int64_t)s.cost(A, t + lane) * A.kv_heads : 0;
+            int64_t inc = own;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += o;
+            }
+            const unsigned at = __ballot_sync(0xffffffffu, inc > skip);
+            if (at || t + 32 >= s.tiles) {
+                const int w = at ? __ffs(at) - 1 : 31;
+                skip -= __shfl_sync(0xffffffffu, inc - own, w);
+                t += w;
+                break;
+            }
+            skip -= __shfl_sync(0xffffffffu, inc, 31);
         }
-        const int c = s.cost(t);
+        const int c = s.cost(A, t);
         h = (int32_t)(skip / c);
         off = (int32_t)(skip - (int64_t)h * c);
     }
@@ -163,40 +189,43 @@ struct Walker {
     }
 
     __device__ __forceinline__ bool next(const AttendParams &A, Piece &p) {
-        if (left <= 0) return false;
-        while (t >= s.tiles) {
-            if (++b >= A.batch.B) return false;
-            s.load(A, b);
-            t = h = off = 0;
-        }
-        int lo, hi, end;
-        s.blocks(t, lo, hi, end);
-        const int cost = max(1, hi - lo);
-        const int take = (int)min(left, (int64_t)(cost - off));
-        p.b = b;
-        p.h = h;
-        p.tile = t;
-        p.rows = s.rows(t);
-        p.end = end;
-        p.lo = lo + off;
-        p.hi = min(hi, lo + off + take);
-        p.split = p.rows <= kRows;
-        const int nb = p.hi - p.lo;
-        p.n0 = p.split ? (nb + 1) / 2 : nb;
-        p.n1 = p.split ? nb / 2 : nb;
-        p.first = cta_of(unit - off);
-        p.parts = cta_of(unit - off + cost - 1) - p.first + 1;
-        left -= take;
-        unit += take;
-        off += take;
-        if (off >= cost) {
-            off = 0;
-            if (++h >= A.kv_heads) {
-                h = 0;
-                ++t;
+        while (left > 0) {
+            while (t >= s.tiles) {
+                if (++b >= A.batch.B) return false;
+                s.load(A, b);
+                t = h = off = 0;
             }
+            int lo, hi, end;
+            s.blocks(A, t, lo, hi, end);
+            const int cost = kTileCost + max(1, hi - lo);
+            const int from = off, to = (int)min((int64_t)cost, off + left);
+            p.b = b;
+            p.h = h;
+            p.tile = t;
+            const int64_t unit_of_tile = unit - off;
+            left -= to - from;
+            unit += to - from;
+            off = to;
+            if (to == cost) {
+                off = 0;
+                if (++h >= A.kv_heads) {
+                    h = 0;
+                    ++t;
+                }
+            }
+            if (to <= kTileCost) continue;  // the run ends before the tile's first block
+            p.rows = s.rows(p.tile);
+            p.end = end;
+            p.lo = lo + max(0, from - kTileCost);
+            p.n = hi > lo ? to - max(from, kTileCost) : 0;
+            p.split = p.rows <= kRows;
+            p.n0 = p.split ? (p.n + 1) / 2 : p.n;
+            p.n1 = p.split ? p.n / 2 : p.n;
+            p.first = from <= kTileCost ? (int32_t)blockIdx.x : cta_of(unit_of_tile + kTileCost);
+            p.parts = (to == cost ? (int32_t)blockIdx.x : cta_of(unit_of_tile + cost - 1)) - p.first + 1;
+            return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -236,21 +265,27 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // A wait that gives up for the whole CTA.
 __device__ __forceinline__ bool hold(AttendShared &sh, unsigned long long *bar, uint32_t parity,
                                      uint32_t *status) {
-    if (*(volatile int32_t *)&sh.dead) return false;
-    if (mbar_wait(bar, parity)) return true;
-    *(volatile int32_t *)&sh.dead = 1;
-    atomicOr(status, SV_STATUS_TIMEOUT);
-    return false;
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try(bar, parity)) {
+        if (*(volatile int32_t *)&sh.dead) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *(volatile int32_t *)&sh.dead = 1;
+            atomicOr(status, SV_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
 }
 
 // Cost of sequence b's tiles over all heads, for each lane's own b (< 0: none).
 __device__ __forceinline__ int64_t sequence_cost(const AttendParams &A, int32_t b, int lane) {
     SeqCost s;
-    s.n = s.tiles = 0;
+    s.n = s.len = s.tiles = s.packed = 0;
     if (b >= 0) s.load(A, b);
     int64_t c = 0;
     if (s.tiles <= 2)
-        for (int t = 0; t < s.tiles; ++t) c += s.cost(t);
+        for (int t = 0; t < s.tiles; ++t) c += s.cost(A, t);
     // long prompts: the whole warp adds up one lane's tiles
     unsigned long_ones = __ballot_sync(0xffffffffu, s.tiles > 2);
     while (long_ones) {
@@ -260,10 +295,9 @@ __device__ __forceinline__ int64_t sequence_cost(const AttendParams &A, int32_t 
         o.n = __shfl_sync(0xffffffffu, s.n, who);
         o.len = __shfl_sync(0xffffffffu, s.len, who);
         o.tiles = __shfl_sync(0xffffffffu, s.tiles, who);
-        o.G = A.group;
-        o.window = A.window;
+        o.packed = __shfl_sync(0xffffffffu, s.packed, who);
         int64_t x = 0;
-        for (int t = lane; t < o.tiles; t += 32) x += o.cost(t);
+        for (int t = lane; t < o.tiles; t += 32) x += o.cost(A, t);
         for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
         if (lane == who) c = x;
     }
@@ -309,10 +343,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     wait_for_primary_grid();
 
     // the batch's blocks, and where this CTA's run of them begins
-    int64_t c = 0;
+    int64_t c = 0, last_cost = 0;
     for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
         const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
-        c += sequence_cost(A, b, lane);
+        last_cost = sequence_cost(A, b, lane);
+        c += last_cost;
         if (blockIdx.x == 0 && b >= 0 && load_sequence(A.batch, b).bad)
             atomicOr(status, SV_STATUS_BAD_LENGTH);
     }
@@ -330,7 +365,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         int64_t base = 0;
         for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
             const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
-            const int64_t own = sequence_cost(A, b, lane);
+            const int64_t own = A.batch.B <= kAttendThreads ? last_cost : sequence_cost(A, b, lane);
             int64_t inc = own;
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
@@ -355,68 +390,72 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const uint32_t tmem = sh.tmem;
 
     Walker walk;
-    if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas);
+    if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas, lane);
     else walk.left = 0;
     Piece p;
-
-    if (warp >= 8)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
 
     if (warp == 8) {
         // ---- copies -------------------------------------------------------
         const int pieces = kKeys / A.piece;
         const int mine = lane % pieces, half = lane / pieces;
         const bool active = half < kHalves;
-        int it = 0;
+        char *dst = ring + half * kHalfBytes + mine * A.piece * 128;
+        int it = 0, st = 0;
+        uint32_t turn = 1;  // parity of the stage's last release
         while (walk.next(A, p)) {
-            const int64_t table = p.b * A.batch.pages_stride;
-            const int first = A.window > 0 ? max(0, walk.s.len - walk.s.n +
-                                                        (int)((int64_t)p.tile * 2 * kRows / A.group) -
-                                                        A.window + 1)
+            if (p.n == 0) continue;
+            const int32_t *table = A.batch.pages + p.b * A.batch.pages_stride;
+            const int first = A.window > 0 ? walk.s.len - walk.s.n +
+                                                 A.by_group.div(p.tile * 2 * kRows) - A.window + 1
                                            : 0;
-            auto load = [&](const CUtensorMap &map, int kb) {
-                const int st = it % L::kStages;
-                const int s0 = kb * kKeys + mine * A.piece;
-                int id = A.batch.num_pages, at = 0;  // outside the cache: zeros
-                if (active && s0 < p.end && s0 + A.piece > first) {
-                    const int pg = s0 / A.batch.page_size;
-                    at = s0 - pg * A.batch.page_size;
-                    id = __ldg(A.batch.pages + table + pg);
-                    if (id < 0 || id >= A.batch.num_pages) {
-                        atomicOr(status, SV_STATUS_BAD_PAGE);
-                        id = A.batch.num_pages;
-                    }
-                }
-                const bool ok = hold(sh, &sh.empty[st], ((it / L::kStages) & 1) ^ 1, status);
-                if (__all_sync(0xffffffffu, ok)) {
+            // this lane's slots of block i: page id, or one outside the cache
+            // (its box reads zeros) where no row looks
+            auto page_of = [&](int i) -> int {
+                const int s0 = (p.lo + i) * kKeys + mine * A.piece;
+                if (!active || i >= p.n || s0 >= p.end || s0 + A.piece <= first)
+                    return kNoPage;
+                return __ldg(table + A.by_page.div(s0));
+            };
+            auto load = [&](const CUtensorMap &map, int i, int id) {
+                if (__all_sync(0xffffffffu, hold(sh, &sh.empty[st], turn, status))) {
                     if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], L::kTile);
                     __syncwarp();
-                    if (active)
-                        tc::load_box(ring + st * L::kTile + half * kHalfBytes + mine * A.piece * 128,
-                                     &map, half * 64, p.h, at, id, &sh.full[st]);
+                    if (active) {
+                        const int s0 = (p.lo + i) * kKeys + mine * A.piece;
+                        tc::load_box(dst + st * L::kTile, &map, half * 64, p.h,
+                                     s0 - A.by_page.div(s0) * A.batch.page_size, id, &sh.full[st]);
+                    }
                     ++it;
-                }
-            };
-            if (p.n0 == 0) continue;
-            if (p.split) {
-                load(kmap, p.block(0, 0));
-                if (p.n1 > 0) load(kmap, p.block(1, 0));
-                for (int i = 0; i < p.n0; ++i) {
-                    load(vmap, p.block(0, i));
-                    if (i + 1 < p.n0) load(kmap, p.block(0, i + 1));
-                    if (i < p.n1) {
-                        load(vmap, p.block(1, i));
-                        if (i + 1 < p.n1) load(kmap, p.block(1, i + 1));
+                    if (++st == L::kStages) {
+                        st = 0;
+                        turn ^= 1;
                     }
                 }
-            } else {
-                load(kmap, p.block(0, 0));
-                for (int i = 0; i < p.n0; ++i) {
-                    load(vmap, p.block(0, i));
-                    if (i + 1 < p.n0) load(kmap, p.block(0, i + 1));
+                __syncwarp();
+            };
+            auto checked = [&](int id) -> int {
+                if (id != kNoPage && (id < 0 || id >= A.batch.num_pages)) {
+                    atomicOr(status, SV_STATUS_BAD_PAGE);
+                    id = kNoPage;
                 }
+                return id;
+            };
+            // keys run ahead of values by one block (pair) or two (split);
+            // page ids are fetched one block further ahead
+            const int ahead = p.split ? 2 : 1;
+            int id0 = page_of(0), id1 = page_of(1), id2 = page_of(2);
+            id0 = checked(id0);
+            load(kmap, 0, id0);
+            id1 = checked(id1);
+            if (ahead == 2 && p.n > 1) load(kmap, 1, id1);
+            for (int i = 0; i < p.n; ++i) {
+                const int id3 = page_of(i + 3);
+                load(vmap, i, id0);
+                id2 = checked(id2);
+                if (i + ahead < p.n) load(kmap, i + ahead, ahead == 2 ? id2 : id1);
+                id0 = id1;
+                id1 = id2;
+                id2 = id3;
             }
         }
         // the last fills must have been taken before the CTA may end; after a
@@ -430,48 +469,55 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
     } else if (warp == 9) {
         // ---- products -----------------------------------------------------
-        int it = 0;
-        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
-        const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(sq);
+        int st = 0;
+        uint32_t turn = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
+        const uint32_t ring_at = smem_u32(ring);
+        const uint64_t q_desc = tc::smem_desc(smem_u32(sq), 16, 1024);
+        const uint64_t k_desc = tc::smem_desc(ring_at, 16, 1024);
+        const uint64_t v_desc = tc::smem_desc(ring_at, kHalfBytes, 1024);
+        // (a descriptor's start address is in units of 16 bytes)
         auto acquire = [&]() -> int {  // the next stage, filled
-            const int st = it % L::kStages;
-            hold(sh, &sh.full[st], (it / L::kStages) & 1, status);
-            ++it;
-            return st;
+            const int x = st;
+            hold(sh, &sh.full[x], turn, status);
+            if (++st == L::kStages) {
+                st = 0;
+                turn ^= 1;
+            }
+            return x;
         };
-        auto alive = [&]() -> bool {
-            return __all_sync(0xffffffffu, *(volatile int32_t *)&sh.dead == 0);
+        auto release = [&](int x) {
+            if (lane == 0) tc::commit(&sh.empty[x]);
         };
-        auto release = [&](int st) {
-            if (alive() && lane == 0) tc::commit(&sh.empty[st]);
-        };
-        auto scores = [&](int g, int st) {  // S_g = Q_g K^T
-            if (alive() && lane == 0) {
+        auto scores = [&](auto gc, int x) {  // S_g = Q_g K^T
+            constexpr int g = decltype(gc)::value;
+            if (lane == 0) {
                 tc::fence_after();
+                const uint64_t kd = k_desc + (uint32_t)(x * (L::kTile / 16));
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t at = (k / 4) * kHalfBytes + (k % 4) * 32;
-                    tc::mma_ss(tmem + g * kKeys,
-                               tc::smem_desc(q_at + g * L::kTile + at, 16, 1024),
-                               tc::smem_desc(ring_at + st * L::kTile + at, 16, 1024), kIdescS,
+                    const uint32_t at = ((k / 4) * kHalfBytes + (k % 4) * 32) / 16;
+                    tc::mma_ss(tmem + g * kKeys, q_desc + (g * (L::kTile / 16) + at), kd + at, kIdescS,
                                k > 0);
                 }
                 tc::commit(&sh.s_full[g]);
             }
             __syncwarp();
         };
-        auto values = [&](int g, int st, bool add) {  // O_g (+)= P_g V
-            hold(sh, &sh.p_full[g], pn[g]++ & 1, status);
-            if (alive() && lane == 0) {
+        auto values = [&](auto gc, int x, bool add) {  // O_g (+)= P_g V
+            constexpr int g = decltype(gc)::value;
+            hold(sh, &sh.p_full[g], (g ? pn1++ : pn0++) & 1, status);
+            if (lane == 0) {
                 tc::fence_after();
+                const uint64_t vd = v_desc + (uint32_t)(x * (L::kTile / 16));
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                     tc::mma_ts(tmem + 2 * kKeys + g * 128, tmem + g * kKeys + k * 8,
-                               tc::smem_desc(ring_at + st * L::kTile + k * 2048, kHalfBytes, 1024),
-                               kIdescO, add || k > 0);
+                               vd + k * (2048 / 16), kIdescO, add || k > 0);
             }
             __syncwarp();
         };
+        const std::integral_constant<int, 0> g0{};
+        const std::integral_constant<int, 1> g1{};
         // slots past the tile's last one in a page that holds it: their weights
         // are zero, and zero times whatever lies there must be zero
         auto clear_tail = [&](int st, int kb) {
@@ -489,58 +535,59 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             __syncwarp();
         };
         while (walk.next(A, p)) {
-            if (p.n0 == 0) continue;
-            hold(sh, &sh.q_full[0], qn[0]++ & 1, status);
+            if (p.n == 0) continue;
+            hold(sh, &sh.q_full[0], qn0++ & 1, status);
             if (p.split) {
-                int st = acquire();
-                scores(0, st);
-                release(st);
+                int x = acquire();
+                scores(g0, x);
+                release(x);
                 if (p.n1 > 0) {
-                    hold(sh, &sh.q_full[1], qn[1]++ & 1, status);
-                    st = acquire();
-                    scores(1, st);
-                    release(st);
+                    hold(sh, &sh.q_full[1], qn1++ & 1, status);
+                    x = acquire();
+                    scores(g1, x);
+                    release(x);
                 }
-                for (int i = 0; i < p.n0; ++i)
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int ng = g ? p.n1 : p.n0;
-                        if (i >= ng) continue;
-                        st = acquire();
-                        clear_tail(st, p.block(g, i));
-                        values(g, st, i > 0);
-                        release(st);
-                        if (i + 1 < ng) {
-                            st = acquire();
-                            scores(g, st);
-                            release(st);
-                        } else if (alive() && lane == 0) {
-                            tc::commit(&sh.o_full[g]);
-                        }
+                auto step = [&](auto gc, int i) {  // block i of the tile's run
+                    constexpr int g = decltype(gc)::value;
+                    x = acquire();
+                    clear_tail(x, p.lo + i);
+                    values(gc, x, i > 1);
+                    release(x);
+                    if (i + 2 < p.n) {
+                        x = acquire();
+                        scores(gc, x);
+                        release(x);
+                    } else if (lane == 0) {
+                        tc::commit(&sh.o_full[g]);
                     }
+                };
+                for (int i = 0; i < p.n; i += 2) {
+                    step(g0, i);
+                    if (i + 1 < p.n) step(g1, i + 1);
+                }
             } else {
-                hold(sh, &sh.q_full[1], qn[1]++ & 1, status);
+                hold(sh, &sh.q_full[1], qn1++ & 1, status);
                 int ks = acquire();
-                scores(0, ks);
-                scores(1, ks);
+                scores(g0, ks);
+                scores(g1, ks);
                 release(ks);
-                for (int i = 0; i < p.n0; ++i) {
+                for (int i = 0; i < p.n; ++i) {
                     const int vs = acquire();
-                    clear_tail(vs, p.block(0, i));
-                    const bool more = i + 1 < p.n0;
-                    values(0, vs, i > 0);
+                    clear_tail(vs, p.lo + i);
+                    const bool more = i + 1 < p.n;
+                    values(g0, vs, i > 0);
                     if (more) {
                         ks = acquire();
-                        scores(0, ks);
-                    } else if (alive() && lane == 0) {
+                        scores(g0, ks);
+                    } else if (lane == 0) {
                         tc::commit(&sh.o_full[0]);
                     }
-                    values(1, vs, i > 0);
+                    values(g1, vs, i > 0);
                     release(vs);
                     if (more) {
-                        scores(1, ks);
+                        scores(g1, ks);
                         release(ks);
-                    } else if (alive() && lane == 0) {
+                    } else if (lane == 0) {
                         tc::commit(&sh.o_full[1]);
                     }
                 }
@@ -555,10 +602,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const int g = warp / 4, gt = tid - g * 128, gw = warp % 4;
         const uint32_t lanes = (uint32_t)(gw * 32) << 16;
         const uint32_t t_s = tmem + lanes + g * kKeys;
-        const uint32_t t_o[2] = {tmem + lanes + 2 * kKeys, tmem + lanes + 2 * kKeys + 128};
-        uint32_t sn = 0, on[2] = {0, 0};
+        const uint32_t t_own = tmem + lanes + 2 * kKeys + g * 128;  // O of this group
+        const uint32_t t_other = tmem + lanes + 2 * kKeys + (1 - g) * 128;
+        uint32_t sn = 0, own_n = 0, other_n = 0;
         char *q_s = sq + g * L::kTile;
-        float2 *stats[2] = {reinterpret_cast<float2 *>(sq), reinterpret_cast<float2 *>(sq + L::kTile)};
+        float2 *own_stats = reinterpret_cast<float2 *>(q_s);
+        const float2 *other_stats = reinterpret_cast<const float2 *>(sq + (1 - g) * L::kTile);
         float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
         float4 *part_out = reinterpret_cast<float4 *>(A.workspace + kAttendOut);
         uint32_t *counters = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters);
@@ -567,18 +616,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         while (walk.next(A, p)) {
             const int n = walk.s.n, len = walk.s.len, row0 = walk.s.row0;
             const int steps = g ? p.n1 : p.n0;
-            const int64_t r_base = (int64_t)p.tile * 2 * kRows + (p.split ? 0 : g * kRows);
+            const int r_base = p.tile * 2 * kRows + (p.split ? 0 : g * kRows);
             const int rows = p.split ? p.rows : min(kRows, p.rows - g * kRows);
             if (steps > 0) {
                 for (int i = gt; i < rows * (DP / 8); i += 128) {
                     const int r = i / (DP / 8), ch = i - r * (DP / 8);
-                    const int64_t pr = r_base + r;
-                    const int64_t j = pr / A.group;
-                    const int64_t hq = (int64_t)p.h * A.group + (pr - j * A.group);
+                    const int pr = r_base + r, j = A.by_group.div(pr);
+                    const int hq = p.h * A.group + (pr - j * A.group);
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (ch * 8 < D && A.q_mode != 2)
                         x = __ldg(reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(A.q) + (row0 + j) * A.q_st[0] +
+                            static_cast<const uint16_t *>(A.q) + (int64_t)(row0 + j) * A.q_st[0] +
                             hq * A.q_st[1] + ch * 8));
                     if (A.q_mode == 1) {
                         x.x ^= 0x80008000u;
@@ -595,35 +643,45 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
             const bool mine = gw * 32 + lane < rows;       // this thread's row exists
             const bool any = gw * 32 < rows;               // one of the warp's does
-            const int64_t pr = r_base + gw * 32 + lane;
-            const int limit = mine ? len - n + (int)(pr / A.group) : len;  // last slot it sees
+            const int pr = r_base + gw * 32 + lane, j = A.by_group.div(pr);
+            const int limit = mine ? len - n + j : len;    // last slot it sees
             const int lowest = A.window > 0 ? limit - A.window + 1 : 0;
             float ref = -INFINITY, sum = 0.f;
             for (int i = 0; i < steps; ++i) {
-                const bool ok = hold(sh, &sh.s_full[g], sn++ & 1, status);
-                if (any && __all_sync(0xffffffffu, ok)) {
+                hold(sh, &sh.s_full[g], sn++ & 1, status);
+                __syncwarp();
+                if (any) {
                     tc::fence_after();
                     const int k0 = p.block(g, i) * kKeys;
-                    uint32_t x[4][32];
+                    const bool edge =
+                        __any_sync(0xffffffffu, mine && (k0 + kKeys - 1 > limit || k0 < lowest));
+                    const int hi = limit - k0, lo = lowest - k0;
+                    // the row of S is read twice, 64 columns at a time: keeping
+                    // all 128 in registers spills
+                    auto columns = [&](uint32_t (&x)[2][32], int at) {
+                        tc::ld32(x[0], t_s + at);
+                        tc::ld32(x[1], t_s + at + 32);
+                        tc::wait_ld();
+                        if (edge) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tc::ld32(x[q], t_s + 32 * q);
-                    tc::wait_ld();
-                    if (__any_sync(0xffffffffu, mine && (k0 + kKeys - 1 > limit || k0 < lowest))) {
-                        const int hi = limit - k0, lo = lowest - k0;
+                            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * q + e > hi || 32 * q + e < lo) x[q][e] = 0xff800000u;
-                    }
+                                for (int e = 0; e < 32; ++e)
+                                    if (at + 32 * q + e > hi || at + 32 * q + e < lo)
+                                        x[q][e] = 0xff800000u;
+                        }
+                    };
                     float m = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int at = 0; at < kKeys; at += 64) {
+                        uint32_t x[2][32];
+                        columns(x, at);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            m = fmaxf(m, __uint_as_float(x[q][e]));
-                            m1 = fmaxf(m1, __uint_as_float(x[q][e + 1]));
+                        for (int e = 0; e < 32; ++e) {
+                            m = fmaxf(m, __uint_as_float(x[0][e]));
+                            m1 = fmaxf(m1, __uint_as_float(x[1][e]));
                         }
+                    }
                     m = fmaxf(m, m1) * A.scale_log2;
                     const bool grow = mine && (m > ref + kRescaleAbove || (ref == -INFINITY && m > ref));
                     if (__any_sync(0xffffffffu, grow)) {
@@ -634,12 +692,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 #pragma unroll
                             for (int q = 0; q < DP / 32; ++q) {
                                 uint32_t o[32];
-                                tc::ld32(o, t_o[g] + 32 * q);
+                                tc::ld32(o, t_own + 32 * q);
                                 tc::wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tc::st32(t_o[g] + 32 * q, o);
+                                tc::st32(t_own + 32 * q, o);
                             }
                         }
                         if (grow) sum *= a;
@@ -648,19 +706,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     const float minus = ref == -INFINITY ? 0.f : -ref;
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        uint32_t w[32];
+                    for (int at = 0; at < kKeys; at += 64) {
+                        uint32_t x[2][32], w[32];
+                        columns(x, at);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const float a = ex2(fmaf(__uint_as_float(x[q + e / 16][2 * (e % 16)]),
+                            const float a = ex2(fmaf(__uint_as_float(x[e / 16][2 * (e % 16)]),
                                                      A.scale_log2, minus));
-                            const float b = ex2(fmaf(__uint_as_float(x[q + e / 16][2 * (e % 16) + 1]),
+                            const float b = ex2(fmaf(__uint_as_float(x[e / 16][2 * (e % 16) + 1]),
                                                      A.scale_log2, minus));
                             s0 += a;
                             s1 += b;
                             w[e] = pack2<T>(a, b);
                         }
-                        tc::st32(t_s + 16 * q, w);
+                        // over columns that have been read
+                        tc::st32(t_s + at / 2, w);
                     }
                     sum += s0 + s1;
                     tc::wait_st();
@@ -669,61 +729,53 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full[g]);
             }
-            const int n_of[2] = {p.n0, p.n1};
-            float a_of[2] = {1.f, 1.f};
+            const int other_steps = g ? p.n0 : p.n1;
+            float own_f = 1.f, other_f = 0.f;  // factors of the two groups' O
             if (p.split) {
                 // join the groups' states; group g then has half the columns
-                if (steps > 0) hold(sh, &sh.o_full[g], on[g]++ & 1, status);
-                if (n_of[1 - g] > 0) hold(sh, &sh.o_full[1 - g], on[1 - g]++ & 1, status);
-                stats[g][gt] = make_float2(ref, sum);
+                if (steps > 0) hold(sh, &sh.o_full[g], own_n++ & 1, status);
+                if (other_steps > 0) hold(sh, &sh.o_full[1 - g], other_n++ & 1, status);
+                own_stats[gt] = make_float2(ref, sum);
                 tc::named_barrier(1, 256);
-                const float2 o = stats[1 - g][gt];
+                const float2 o = other_stats[gt];
                 const float to = fmaxf(ref, o.x);
-                a_of[g] = ref == -INFINITY ? 0.f : ex2(ref - to);
-                a_of[1 - g] = o.x == -INFINITY ? 0.f : ex2(o.x - to);
-                // group 0's part first on both sides
-                sum = g == 0 ? sum * a_of[0] + o.y * a_of[1] : o.y * a_of[0] + sum * a_of[1];
+                own_f = ref == -INFINITY ? 0.f : ex2(ref - to);
+                other_f = o.x == -INFINITY ? 0.f : ex2(o.x - to);
+                sum = sum * own_f + o.y * other_f;
                 ref = to;
             } else if (steps > 0) {
-                hold(sh, &sh.o_full[g], on[g]++ & 1, status);
+                hold(sh, &sh.o_full[g], own_n++ & 1, status);
                 // the other group's accumulators went through a phase too; this
                 // group next waits for them in a split tile, where its own
                 // phase (or the other's, for group 1) comes later in the
                 // order of the products
-                ++on[1 - g];
+                ++other_n;
             }
             tc::fence_after();
             const int c0 = p.split ? g * (DP / 2) : 0;      // this group's columns
             const int c1 = p.split ? c0 + DP / 2 : DP;
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const int64_t j = pr / A.group;
-            uint16_t *out = static_cast<uint16_t *>(A.out) + (row0 + j) * A.o_st[0] +
-                            ((int64_t)p.h * A.group + (pr - j * A.group)) * A.o_st[1];
+            uint16_t *out = static_cast<uint16_t *>(A.out) + (int64_t)(row0 + j) * A.o_st[0] +
+                            (p.h * A.group + (pr - j * A.group)) * A.o_st[1];
             const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
             if (any) {
                 for (int cc = c0; cc < c1; cc += 32) {
                     float v[32];
                     uint32_t o[32];
-                    if (p.split) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-                            if (n_of[s] > 0) {
-                                tc::ld32(o, t_o[s] + cc);
-                                tc::wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    v[e] += a_of[s] * __uint_as_float(o[e]);
-                            }
-                    } else if (steps > 0) {
-                        tc::ld32(o, t_o[g] + cc);
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                    if (steps > 0) {
+                        tc::ld32(o, t_own + cc);
                         tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]);
-                    } else {
+                        for (int e = 0; e < 32; ++e) v[e] = own_f * __uint_as_float(o[e]);
+                    }
+                    if (p.split && other_steps > 0) {
+                        tc::ld32(o, t_other + cc);
+                        tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = fmaf(other_f, __uint_as_float(o[e]), v[e]);
                     }
                     if (p.parts > 1) {
 #pragma unroll
@@ -766,9 +818,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     const int strip = gw / per, share = gw % per;
                     const int wide = (c1 - c0) / per;
                     const int r = strip * 32 + lane;
-                    const int64_t cr = r_base + r, cj = cr / A.group;
-                    uint16_t *co = static_cast<uint16_t *>(A.out) + (row0 + cj) * A.o_st[0] +
-                                   ((int64_t)p.h * A.group + (cr - cj * A.group)) * A.o_st[1];
+                    const int cr = r_base + r, cj = A.by_group.div(cr);
+                    uint16_t *co = static_cast<uint16_t *>(A.out) + (int64_t)(row0 + cj) * A.o_st[0] +
+                                   (p.h * A.group + (cr - cj * A.group)) * A.o_st[1];
                     auto slot_of = [&](int i) -> int {
                         return (p.first + i) * 2 + (i == 0 ? 1 : 0);
                     };
