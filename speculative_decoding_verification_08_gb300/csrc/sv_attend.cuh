@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     AttendShared &sh = *reinterpret_cast<AttendShared *>(smem);
     char *sq = smem + L::kMisc;
     char *ring = sq + 2 * L::kTile;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = tc::uniform(tid / 32), lane = tid % 32;
     uint32_t *status = A.batch.status;
 
     if (warp == 9) tc::tmem_alloc(&sh.tmem, kTmemCols);
@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
     } else if (warp == 9) {
         // ---- products -----------------------------------------------------
+        const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
         int st = 0;
         uint32_t turn = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
         const uint32_t ring_at = smem_u32(ring);
@@ -486,17 +487,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             return x;
         };
         auto release = [&](int x) {
-            if (lane == 0) tc::commit(&sh.empty[x]);
+            if (tc::elect()) tc::commit(&sh.empty[x]);
         };
         auto scores = [&](auto gc, int x) {  // S_g = Q_g K^T
             constexpr int g = decltype(gc)::value;
-            if (lane == 0) {
-                tc::fence_after();
+            tc::fence_after();
+            if (tc::elect()) {
                 const uint64_t kd = k_desc + (uint32_t)(x * (L::kTile / 16));
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const uint32_t at = ((k / 4) * kHalfBytes + (k % 4) * 32) / 16;
-                    tc::mma_ss(tmem + g * kKeys, q_desc + (g * (L::kTile / 16) + at), kd + at, kIdescS,
+                    tc::mma_ss(tm + g * kKeys, q_desc + (g * (L::kTile / 16) + at), kd + at, kIdescS,
                                k > 0);
                 }
                 tc::commit(&sh.s_full[g]);
@@ -506,12 +507,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         auto values = [&](auto gc, int x, bool add) {  // O_g (+)= P_g V
             constexpr int g = decltype(gc)::value;
             hold(sh, &sh.p_full[g], (g ? pn1++ : pn0++) & 1, status);
-            if (lane == 0) {
-                tc::fence_after();
+            tc::fence_after();
+            if (tc::elect()) {
                 const uint64_t vd = v_desc + (uint32_t)(x * (L::kTile / 16));
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_ts(tmem + 2 * kKeys + g * 128, tmem + g * kKeys + k * 8,
+                    tc::mma_ts(tm + 2 * kKeys + g * 128, tm + g * kKeys + k * 8,
                                vd + k * (2048 / 16), kIdescO, add || k > 0);
             }
             __syncwarp();
@@ -535,13 +536,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             __syncwarp();
         };
         while (walk.next(A, p)) {
-            if (p.n == 0) continue;
+            const int blocks = tc::uniform(p.n), lo = tc::uniform(p.lo), n1 = tc::uniform(p.n1);
+            const bool split = tc::uniform(p.split);
+            if (blocks == 0) continue;
             hold(sh, &sh.q_full[0], qn0++ & 1, status);
-            if (p.split) {
+            if (split) {
                 int x = acquire();
                 scores(g0, x);
                 release(x);
-                if (p.n1 > 0) {
+                if (n1 > 0) {
                     hold(sh, &sh.q_full[1], qn1++ & 1, status);
                     x = acquire();
                     scores(g1, x);
@@ -550,20 +553,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 auto step = [&](auto gc, int i) {  // block i of the tile's run
                     constexpr int g = decltype(gc)::value;
                     x = acquire();
-                    clear_tail(x, p.lo + i);
+                    clear_tail(x, lo + i);
                     values(gc, x, i > 1);
                     release(x);
-                    if (i + 2 < p.n) {
+                    if (i + 2 < blocks) {
                         x = acquire();
                         scores(gc, x);
                         release(x);
-                    } else if (lane == 0) {
+                    } else if (tc::elect()) {
                         tc::commit(&sh.o_full[g]);
                     }
                 };
-                for (int i = 0; i < p.n; i += 2) {
+                for (int i = 0; i < blocks; i += 2) {
                     step(g0, i);
-                    if (i + 1 < p.n) step(g1, i + 1);
+                    if (i + 1 < blocks) step(g1, i + 1);
                 }
             } else {
                 hold(sh, &sh.q_full[1], qn1++ & 1, status);
@@ -571,15 +574,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 scores(g0, ks);
                 scores(g1, ks);
                 release(ks);
-                for (int i = 0; i < p.n; ++i) {
+                for (int i = 0; i < blocks; ++i) {
                     const int vs = acquire();
-                    clear_tail(vs, p.lo + i);
-                    const bool more = i + 1 < p.n;
+                    clear_tail(vs, lo + i);
+                    const bool more = i + 1 < blocks;
                     values(g0, vs, i > 0);
                     if (more) {
                         ks = acquire();
                         scores(g0, ks);
-                    } else if (lane == 0) {
+                    } else if (tc::elect()) {
                         tc::commit(&sh.o_full[0]);
                     }
                     values(g1, vs, i > 0);
@@ -587,14 +590,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     if (more) {
                         scores(g1, ks);
                         release(ks);
-                    } else if (lane == 0) {
+                    } else if (tc::elect()) {
                         tc::commit(&sh.o_full[1]);
                     }
                 }
             }
             __syncwarp();
         }
-        if (lane == 0) tc::commit(&sh.drain);
+        if (tc::elect()) tc::commit(&sh.drain);
         __syncwarp();
         mbar_wait(&sh.drain, 0);
     } else if (warp < 8) {
@@ -619,23 +622,32 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const int r_base = p.tile * 2 * kRows + (p.split ? 0 : g * kRows);
             const int rows = p.split ? p.rows : min(kRows, p.rows - g * kRows);
             if (steps > 0) {
-                for (int i = gt; i < rows * (DP / 8); i += 128) {
-                    const int r = i / (DP / 8), ch = i - r * (DP / 8);
-                    const int pr = r_base + r, j = A.by_group.div(pr);
-                    const int hq = p.h * A.group + (pr - j * A.group);
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (ch * 8 < D && A.q_mode != 2)
-                        x = __ldg(reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(A.q) + (int64_t)(row0 + j) * A.q_st[0] +
-                            hq * A.q_st[1] + ch * 8));
-                    if (A.q_mode == 1) {
-                        x.x ^= 0x80008000u;
-                        x.y ^= 0x80008000u;
-                        x.z ^= 0x80008000u;
-                        x.w ^= 0x80008000u;
+                // eight loads in flight per thread
+                constexpr int kChunks = DP / 8, kStep = 128 / kChunks;
+                const int ch = gt % kChunks;
+                for (int r0 = gt / kChunks; r0 < rows; r0 += 8 * kStep) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * kStep;
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (r < rows && ch * 8 < D && A.q_mode != 2) {
+                            const int pr = r_base + r, j = A.by_group.div(pr);
+                            const int hq = p.h * A.group + (pr - j * A.group);
+                            x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                static_cast<const uint16_t *>(A.q) + (int64_t)(row0 + j) * A.q_st[0] +
+                                hq * A.q_st[1] + ch * 8));
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(q_s + (ch / 8) * kHalfBytes + r * 128 +
-                                               (((ch % 8) ^ (r & 7)) * 16)) = x;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * kStep;
+                        const uint32_t flip = A.q_mode == 1 ? 0x80008000u : 0u;
+                        if (r < rows)
+                            *reinterpret_cast<uint4 *>(q_s + (ch / 8) * kHalfBytes + r * 128 +
+                                                       (((ch % 8) ^ (r & 7)) * 16)) =
+                                make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
+                    }
                 }
                 tc::fence_async_smem();
                 __syncwarp();

@@ -67,6 +67,18 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t (&r)[32]) {
         : "memory");
 }
 
+// True on one lane of a converged warp, the same one each time.  The compiler
+// knows that at most one thread follows, so what the branch uses stays in
+// uniform registers, where the product instructions take their operands from.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
+// A value that all lanes hold, marked as such.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ---- products --------------------------------------------------------------
 
 // Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5), A and B type
