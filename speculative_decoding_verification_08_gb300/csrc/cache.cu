@@ -136,6 +136,28 @@ int box_map(CUtensorMap *map, const sv_paged_cache *c, void *base, const int64_t
     return r == CUDA_SUCCESS ? SV_OK : SV_EINVAL;
 }
 
+// A map of the queries for boxes of 64 values x the group's heads x the tokens
+// that make 128 packed rows: [tokens][kv heads][group][values].
+int query_map(CUtensorMap *map, const sv_paged_cache *c, const void *q, const int64_t *stride,
+              int group) {
+    const EncodeTiled encode = encoder();
+    if (!encode) return SV_ECUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)group, (cuuint64_t)c->kv_heads,
+                                (cuuint64_t)c->tokens};
+    cuuint64_t bytes[3] = {(cuuint64_t)stride[1] * 2, (cuuint64_t)stride[1] * 2 * group,
+                           (cuuint64_t)stride[0] * 2};
+    for (int i = 0; i < 3; ++i)
+        if (dims[i + 1] == 1) bytes[i] = (cuuint64_t)c->head_dim * 2;
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)(sv::kRows / group)},
+                     step[4] = {1, 1, 1, 1};
+    const CUresult r = encode(
+        map, c->dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+        4, const_cast<void *>(q), dims, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SV_OK : SV_EINVAL;
+}
+
 // SM count of the current device, queried once.
 int sm_count() {
     int dev = 0;
@@ -151,7 +173,7 @@ int sm_count() {
 
 template <class T, int DP>
 int launch_attend(const sv::AttendParams &A, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                  cudaStream_t st) {
+                  const CUtensorMap &qmap, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ECUDA;
     constexpr int bytes = sv::AttendSmem<DP>::kBytes;
@@ -175,7 +197,7 @@ int launch_attend(const sv::AttendParams &A, const CUtensorMap &kmap, const CUte
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, sv::attend_kernel<T, DP>, A, kmap, vmap) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, sv::attend_kernel<T, DP>, A, kmap, vmap, qmap) != cudaSuccess)
         return SV_ECUDA;
     g_last_grid = grid;
     g_last_kernels = 1;
@@ -276,7 +298,7 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     A.by_group.set((uint32_t)A.group);
     A.by_page.set((uint32_t)cache->page_size);
     A.head_dim = cache->head_dim;
-    A.window = window;
+    A.window = window < (int64_t)cache->max_pages * cache->page_size ? window : 0;
     A.piece = 8;
     while (A.piece < sv::kKeys && cache->page_size % (2 * A.piece) == 0) A.piece *= 2;
     A.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504f;
@@ -285,13 +307,19 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     CUtensorMap kmap, vmap;
     if ((rc = box_map(&kmap, cache, cache->k, cache->k_stride, A.piece)) != SV_OK) return rc;
     if ((rc = box_map(&vmap, cache, cache->v, cache->v_stride, A.piece)) != SV_OK) return rc;
+    // queries by TMA boxes of 128 packed rows when whole tokens make them up
+    A.q_boxes = A.q_mode == 0 && sv::kRows % A.group == 0;
+    CUtensorMap qmap = kmap;  // unused otherwise
+    if (A.q_boxes && (rc = query_map(&qmap, cache, q, q_stride, A.group)) != SV_OK) return rc;
+    A.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && out_stride[0] % 16 == 0 &&
+                 out_stride[1] % 16 == 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = cache->dtype == SV_BF16;
     if (cache->head_dim > 64)
-        return bf16 ? launch_attend<__nv_bfloat16, 128>(A, kmap, vmap, st)
-                    : launch_attend<__half, 128>(A, kmap, vmap, st);
-    return bf16 ? launch_attend<__nv_bfloat16, 64>(A, kmap, vmap, st)
-                : launch_attend<__half, 64>(A, kmap, vmap, st);
+        return bf16 ? launch_attend<__nv_bfloat16, 128>(A, kmap, vmap, qmap, st)
+                    : launch_attend<__half, 128>(A, kmap, vmap, qmap, st);
+    return bf16 ? launch_attend<__nv_bfloat16, 64>(A, kmap, vmap, qmap, st)
+                : launch_attend<__half, 64>(A, kmap, vmap, qmap, st);
 }
 
 }  // extern "C"

@@ -31,10 +31,11 @@
 // workspace, and the last CTA of a tile to arrive joins them in order: results
 // do not depend on timing.
 //
-// Warps 0-7 softmax, 8 copies (one TMA box per page piece and 64 values of a
-// head, 128-byte swizzle), 9 issues the products.  Every wait is bounded; when
-// one gives up the CTA runs through its remaining steps without waiting or
-// copying, on whatever its buffers hold, and reports SV_STATUS_TIMEOUT.
+// Warps 0-7 softmax, 8 copies of keys and values (one TMA box per page piece and 64 values of a
+// head, 128-byte swizzle), 9 issues the products,
+// 10 copies of queries, 11 walks the CTA's run and publishes its pieces.  Every wait is bounded; when
+// one gives up the CTA's warps leave at the next piece they miss, without further
+// waits or copies, and the call reports SV_STATUS_TIMEOUT.
 #pragma once
 
 #include <type_traits>
@@ -46,6 +47,10 @@
 namespace sv {
 
 constexpr int kAttendThreads = 384;
+// Registers per thread after the roles part: 256 softmax threads and 128 others
+// share the 384 x 168 that the block is launched with.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kAttendThreads * 168, "register split");
 constexpr int kRows = 128;           // packed rows per softmax group
 constexpr int kKeys = 128;           // slots per key block
 constexpr int kAttendMaxCtas = 160;  // partial states the workspace holds room for
@@ -88,6 +93,8 @@ struct AttendParams {
     int32_t piece;      // slots per copied box: the largest power of two in page_size, <= 128
     float scale_log2;   // |scale| * log2(e); the sign goes into q
     int32_t q_mode;     // 0: q, 1: -q, 2: zeros (scale 0)
+    int32_t wide_out;   // rows of out start on 32 bytes
+    int32_t q_boxes;    // queries come by TMA boxes (else the softmax threads load them)
     char *workspace;
 };
 
@@ -95,8 +102,9 @@ template <int DP>
 struct AttendSmem {
     static constexpr int kTile = kRows * DP * 2;  // a Q tile, a K or V block
     static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr int kMisc = 1024;
-    static constexpr int kBytes = kMisc + (2 + kStages) * kTile + 1024;
+    static constexpr int kStats = 1024;               // states of the two groups
+    static constexpr int kMisc = kStats + 2 * kRows * 8;
+    static constexpr int kBytes = kMisc + (2 + kStages) * kTile;
 };
 
 // ---------------------------------------------------------------------------
@@ -132,20 +140,22 @@ struct SeqCost {
     }
 };
 
+// One CTA's part of a tile, as the scheduler warp publishes it.
 struct Piece {
-    int32_t b, h, tile, rows;  // rows of the whole tile
-    int32_t lo, n;             // this CTA's key blocks
-    int32_t end;               // one past the tile's last slot
-    int32_t first;             // CTA that holds the tile's first block
-    int32_t parts;             // CTAs that share the tile
-    bool split;                // split tile
-    int32_t n0, n1;            // blocks of group 0 and 1
-    __device__ __forceinline__ int block(int g, int i) const {
-        return split ? lo + 2 * i + g : lo + i;
-    }
+    int32_t n;                  // its key blocks; -1: no more pieces
+    int32_t lo;                 // the first of them
+    int32_t n1;                 // blocks of group 1 (group 0 has the others)
+    int32_t split;              // split tile
+    int32_t b, h;
+    int32_t row, rows;          // first packed row of the tile, rows of the tile
+    int32_t end;                // one past the tile's last slot
+    int32_t token;              // first token row of the sequence
+    int32_t past;               // slots before its new tokens
+    int32_t first, parts;       // CTA that holds the tile's first block, CTAs that share the tile
+    int32_t pad[3];
 };
 
-// Walks one CTA's run of the work, the same way in every warp (whole warps).
+// Walks one CTA's run of the work (a whole warp).
 struct Walker {
     SeqCost s;
     int32_t b, t, h, off;
@@ -201,7 +211,11 @@ struct Walker {
             const int from = off, to = (int)min((int64_t)cost, off + left);
             p.b = b;
             p.h = h;
-            p.tile = t;
+            p.row = t * 2 * kRows;
+            p.rows = s.rows(t);
+            p.end = end;
+            p.token = s.row0;
+            p.past = s.len - s.n;
             const int64_t unit_of_tile = unit - off;
             left -= to - from;
             unit += to - from;
@@ -214,12 +228,9 @@ struct Walker {
                 }
             }
             if (to <= kTileCost) continue;  // the run ends before the tile's first block
-            p.rows = s.rows(p.tile);
-            p.end = end;
             p.lo = lo + max(0, from - kTileCost);
             p.n = hi > lo ? to - max(from, kTileCost) : 0;
             p.split = p.rows <= kRows;
-            p.n0 = p.split ? (p.n + 1) / 2 : p.n;
             p.n1 = p.split ? p.n / 2 : p.n;
             p.first = from <= kTileCost ? (int32_t)blockIdx.x : cta_of(unit_of_tile + kTileCost);
             p.parts = (to == cost ? (int32_t)blockIdx.x : cta_of(unit_of_tile + cost - 1)) - p.first + 1;
@@ -231,12 +242,19 @@ struct Walker {
 
 // ---------------------------------------------------------------------------
 
+constexpr int kPieces = 4;  // pieces the scheduler may be ahead
+// arrivals that free a piece: softmax warps, keys and values, queries, products
+constexpr int kPieceReaders = 11;
+
 struct AttendShared {
     unsigned long long full[8], empty[8];
-    unsigned long long s_full[2], p_full[2], o_full[2], q_full[2], drain;
+    unsigned long long s_full[2], p_full[2][2], o_full[2], q_full[2], q_free[2], drain;
+    unsigned long long piece_full[kPieces], piece_empty[kPieces];
+    unsigned long long group_sync[2], both_sync;
+    Piece pieces[kPieces];
     uint32_t tmem;
     int32_t dead, b0, last[2];
-    int64_t skip, total;
+    int64_t skip;
     int64_t sums[kAttendThreads / 32];
 };
 static_assert(sizeof(AttendShared) <= 1024, "misc region");
@@ -262,6 +280,28 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
     return r;
 }
 
+// 32 values of a row (those below `left`), in 32-byte stores where the rows
+// allow: a thread has a row of its own, so a store touches as many lines as it
+// has lanes, and half the stores take half the time.
+__device__ __forceinline__ void store_row(uint16_t *to, const uint32_t (&y)[16], int left,
+                                          bool wide) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+        if (wide && 2 * e + 16 <= left) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * e),
+                         "r"(y[e]), "r"(y[e + 1]), "r"(y[e + 2]), "r"(y[e + 3]), "r"(y[e + 4]),
+                         "r"(y[e + 5]), "r"(y[e + 6]), "r"(y[e + 7])
+                         : "memory");
+        } else {
+            if (2 * e < left)
+                *reinterpret_cast<uint4 *>(to + 2 * e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            if (2 * e + 8 < left)
+                *reinterpret_cast<uint4 *>(to + 2 * e + 8) =
+                    make_uint4(y[e + 4], y[e + 5], y[e + 6], y[e + 7]);
+        }
+    }
+}
+
 // A wait that gives up for the whole CTA.
 __device__ __forceinline__ bool hold(AttendShared &sh, unsigned long long *bar, uint32_t parity,
                                      uint32_t *status) {
@@ -276,6 +316,35 @@ __device__ __forceinline__ bool hold(AttendShared &sh, unsigned long long *bar, 
         }
     }
     return true;
+}
+
+// The pieces as a reader warp sees them, in order.
+struct PieceReader {
+    int k = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ const Piece *next(AttendShared &sh, uint32_t *status) {
+        const bool ok = __all_sync(0xffffffffu, hold(sh, &sh.piece_full[k], turn, status));
+        return ok && sh.pieces[k].n >= 0 ? &sh.pieces[k] : nullptr;
+    }
+    __device__ __forceinline__ void done(AttendShared &sh, int lane) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.piece_empty[k]);
+        if (++k == kPieces) {
+            k = 0;
+            turn ^= 1;
+        }
+    }
+};
+
+// A barrier among warps, by an mbarrier so that the wait is bounded: no warp
+// hangs when another has left after a timeout.
+__device__ __forceinline__ void meet(AttendShared &sh, unsigned long long *bar, uint32_t &turn,
+                                     int lane, uint32_t *status) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    hold(sh, bar, turn, status);
+    __syncwarp();
+    turn ^= 1;
 }
 
 // Cost of sequence b's tiles over all heads, for each lane's own b (< 0: none).
@@ -307,21 +376,24 @@ __device__ __forceinline__ int64_t sequence_cost(const AttendParams &A, int32_t 
 template <class T, int DP>
 __global__ void __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const __grid_constant__ AttendParams A, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap) {
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
     typedef AttendSmem<DP> L;
     constexpr bool kBf16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
     constexpr int kHalves = DP / 64;
     constexpr int kHalfBytes = kKeys * 128;
     constexpr uint32_t kIdescS = tc::instr_desc(kBf16, false, kRows, kKeys);
     constexpr uint32_t kIdescO = tc::instr_desc(kBf16, true, kRows, DP);
-    extern __shared__ char raw[];
-    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) char smem[];
     AttendShared &sh = *reinterpret_cast<AttendShared *>(smem);
     char *sq = smem + L::kMisc;
     char *ring = sq + 2 * L::kTile;
     const int tid = threadIdx.x, warp = tc::uniform(tid / 32), lane = tid % 32;
     uint32_t *status = A.batch.status;
 
+    if (smem_u32(smem) & 1023) {  // the swizzle counts on it; no room is left to round up
+        if (tid == 0) atomicOr(status, SV_STATUS_TIMEOUT);
+        return;
+    }
     if (warp == 9) tc::tmem_alloc(&sh.tmem, kTmemCols);
     if (tid == 0) {
         for (int i = 0; i < L::kStages; ++i) {
@@ -330,11 +402,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&sh.s_full[g], 1);
-            mbar_init(&sh.p_full[g], 4);
+            mbar_init(&sh.p_full[g][0], 4);
+            mbar_init(&sh.p_full[g][1], 4);
             mbar_init(&sh.o_full[g], 1);
-            mbar_init(&sh.q_full[g], 4);
+            mbar_init(&sh.q_full[g], A.q_boxes ? 1 : 4);
+            mbar_init(&sh.q_free[g], 1);
         }
         mbar_init(&sh.drain, 1);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sh.piece_full[i], 1);
+            mbar_init(&sh.piece_empty[i], kPieceReaders);
+        }
+        mbar_init(&sh.group_sync[0], 4);
+        mbar_init(&sh.group_sync[1], 4);
+        mbar_init(&sh.both_sync, 8);
         sh.dead = 0;
         sh.b0 = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -389,242 +470,299 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     }
     const uint32_t tmem = sh.tmem;
 
-    Walker walk;
-    if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas, lane);
-    else walk.left = 0;
-    Piece p;
-
-    if (warp == 8) {
-        // ---- copies -------------------------------------------------------
-        const int pieces = kKeys / A.piece;
-        const int mine = lane % pieces, half = lane / pieces;
-        const bool active = half < kHalves;
-        char *dst = ring + half * kHalfBytes + mine * A.piece * 128;
-        int it = 0, st = 0;
-        uint32_t turn = 1;  // parity of the stage's last release
-        while (walk.next(A, p)) {
-            if (p.n == 0) continue;
-            const int32_t *table = A.batch.pages + p.b * A.batch.pages_stride;
-            const int first = A.window > 0 ? walk.s.len - walk.s.n +
-                                                 A.by_group.div(p.tile * 2 * kRows) - A.window + 1
-                                           : 0;
-            // this lane's slots of block i: page id, or one outside the cache
-            // (its box reads zeros) where no row looks
-            auto page_of = [&](int i) -> int {
-                const int s0 = (p.lo + i) * kKeys + mine * A.piece;
-                if (!active || i >= p.n || s0 >= p.end || s0 + A.piece <= first)
-                    return kNoPage;
-                return __ldg(table + A.by_page.div(s0));
-            };
-            auto load = [&](const CUtensorMap &map, int i, int id) {
-                if (__all_sync(0xffffffffu, hold(sh, &sh.empty[st], turn, status))) {
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], L::kTile);
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 11) {
+            // ---- the schedule ---------------------------------------------
+            Walker walk;
+            walk.left = 0;
+            if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas, lane);
+            int k = 0;
+            uint32_t turn = 1;
+            for (bool more = true; more;) {
+                Piece p;
+                more = walk.next(A, p);
+                if (!more) p.n = -1;
+                // (after a timeout the readers stop at the first piece they miss)
+                if (!__all_sync(0xffffffffu, hold(sh, &sh.piece_empty[k], turn, status))) break;
+                if (lane == 0) {
+                    sh.pieces[k] = p;
+                    mbar_arrive(&sh.piece_full[k]);
+                }
+                __syncwarp();
+                if (++k == kPieces) {
+                    k = 0;
+                    turn ^= 1;
+                }
+            }
+        } else if (warp == 8) {
+            // ---- copies of keys and values --------------------------------
+            const int pieces = kKeys / A.piece;
+            const int mine = lane % pieces, half = lane / pieces;
+            const bool active = half < kHalves;
+            char *dst = ring + half * kHalfBytes + mine * A.piece * 128;
+            int it = 0, st = 0;
+            uint32_t turn = 1;  // parity of the stage's last release
+            PieceReader reader;
+            while (const Piece *pp = reader.next(sh, status)) {
+                const Piece p = *pp;
+                reader.done(sh, lane);
+                if (p.n == 0) continue;
+                const int32_t *table = A.batch.pages + p.b * A.batch.pages_stride;
+                const int first = A.window > 0 ? p.past + A.by_group.div(p.row) - A.window + 1 : 0;
+                // this lane's slots of block i: page id, or one outside the cache
+                // (its box reads zeros) where no row looks
+                auto page_of = [&](int i) -> int {
+                    const int s0 = (p.lo + i) * kKeys + mine * A.piece;
+                    if (!active || i >= p.n || s0 >= p.end || s0 + A.piece <= first) return kNoPage;
+                    return __ldg(table + A.by_page.div(s0));
+                };
+                auto load = [&](const CUtensorMap &map, int i, int id) {
+                    if (__all_sync(0xffffffffu, hold(sh, &sh.empty[st], turn, status))) {
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], L::kTile);
+                        __syncwarp();
+                        if (active) {
+                            const int s0 = (p.lo + i) * kKeys + mine * A.piece;
+                            tc::load_box(dst + st * L::kTile, &map, half * 64, p.h,
+                                         s0 - A.by_page.div(s0) * A.batch.page_size, id,
+                                         &sh.full[st]);
+                        }
+                        ++it;
+                        if (++st == L::kStages) {
+                            st = 0;
+                            turn ^= 1;
+                        }
+                    }
                     __syncwarp();
-                    if (active) {
-                        const int s0 = (p.lo + i) * kKeys + mine * A.piece;
-                        tc::load_box(dst + st * L::kTile, &map, half * 64, p.h,
-                                     s0 - A.by_page.div(s0) * A.batch.page_size, id, &sh.full[st]);
+                };
+                auto checked = [&](int id) -> int {
+                    if (id != kNoPage && (id < 0 || id >= A.batch.num_pages)) {
+                        atomicOr(status, SV_STATUS_BAD_PAGE);
+                        id = kNoPage;
                     }
-                    ++it;
-                    if (++st == L::kStages) {
-                        st = 0;
-                        turn ^= 1;
+                    return id;
+                };
+                // keys run ahead of values by one block (pair) or two (split);
+                // page ids are fetched one block further ahead
+                const int ahead = p.split ? 2 : 1;
+                int id0 = page_of(0), id1 = page_of(1), id2 = page_of(2);
+                id0 = checked(id0);
+                load(kmap, 0, id0);
+                id1 = checked(id1);
+                if (ahead == 2 && p.n > 1) load(kmap, 1, id1);
+                for (int i = 0; i < p.n; ++i) {
+                    const int id3 = page_of(i + 3);
+                    load(vmap, i, id0);
+                    id2 = checked(id2);
+                    if (i + ahead < p.n) load(kmap, i + ahead, ahead == 2 ? id2 : id1);
+                    id0 = id1;
+                    id1 = id2;
+                    id2 = id3;
+                }
+            }
+            // the last fills must have been taken before the CTA may end; after a
+            // wait gave up, they must at least have landed
+            if (*(volatile int32_t *)&sh.dead) {
+                for (int k = max(0, it - L::kStages); k < it; ++k)
+                    mbar_wait(&sh.full[k % L::kStages], (k / L::kStages) & 1);
+            } else {
+                for (int k = max(0, it - L::kStages); k < it; ++k)
+                    hold(sh, &sh.empty[k % L::kStages], (k / L::kStages) & 1, status);
+            }
+        } else if (warp == 9) {
+            // ---- products -----------------------------------------------------
+            const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
+            int st = 0;
+            uint32_t turn = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
+            const uint32_t ring_at = smem_u32(ring);
+            const uint64_t q_desc = tc::smem_desc(smem_u32(sq), 16, 1024);
+            const uint64_t k_desc = tc::smem_desc(ring_at, 16, 1024);
+            const uint64_t v_desc = tc::smem_desc(ring_at, kHalfBytes, 1024);
+            // (a descriptor's start address is in units of 16 bytes)
+            auto acquire = [&]() -> int {  // the next stage, filled
+                const int x = st;
+                hold(sh, &sh.full[x], turn, status);
+                if (++st == L::kStages) {
+                    st = 0;
+                    turn ^= 1;
+                }
+                return x;
+            };
+            auto release = [&](int x) {
+                if (tc::elect()) tc::commit(&sh.empty[x]);
+            };
+            auto scores = [&](auto gc, int x, bool last) {  // S_g = Q_g K^T
+                constexpr int g = decltype(gc)::value;
+                tc::fence_after();
+                if (tc::elect()) {
+                    const uint64_t kd = k_desc + (uint32_t)(x * (L::kTile / 16));
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint32_t at = ((k / 4) * kHalfBytes + (k % 4) * 32) / 16;
+                        tc::mma_ss(tm + g * kKeys, q_desc + (g * (L::kTile / 16) + at), kd + at, kIdescS,
+                                   k > 0);
                     }
+                    tc::commit(&sh.s_full[g]);
+                    if (last) tc::commit(&sh.q_free[g]);
                 }
                 __syncwarp();
             };
-            auto checked = [&](int id) -> int {
-                if (id != kNoPage && (id < 0 || id >= A.batch.num_pages)) {
-                    atomicOr(status, SV_STATUS_BAD_PAGE);
-                    id = kNoPage;
-                }
-                return id;
-            };
-            // keys run ahead of values by one block (pair) or two (split);
-            // page ids are fetched one block further ahead
-            const int ahead = p.split ? 2 : 1;
-            int id0 = page_of(0), id1 = page_of(1), id2 = page_of(2);
-            id0 = checked(id0);
-            load(kmap, 0, id0);
-            id1 = checked(id1);
-            if (ahead == 2 && p.n > 1) load(kmap, 1, id1);
-            for (int i = 0; i < p.n; ++i) {
-                const int id3 = page_of(i + 3);
-                load(vmap, i, id0);
-                id2 = checked(id2);
-                if (i + ahead < p.n) load(kmap, i + ahead, ahead == 2 ? id2 : id1);
-                id0 = id1;
-                id1 = id2;
-                id2 = id3;
-            }
-        }
-        // the last fills must have been taken before the CTA may end; after a
-        // wait gave up, they must at least have landed
-        if (*(volatile int32_t *)&sh.dead) {
-            for (int k = max(0, it - L::kStages); k < it; ++k)
-                mbar_wait(&sh.full[k % L::kStages], (k / L::kStages) & 1);
-        } else {
-            for (int k = max(0, it - L::kStages); k < it; ++k)
-                hold(sh, &sh.empty[k % L::kStages], (k / L::kStages) & 1, status);
-        }
-    } else if (warp == 9) {
-        // ---- products -----------------------------------------------------
-        const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
-        int st = 0;
-        uint32_t turn = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
-        const uint32_t ring_at = smem_u32(ring);
-        const uint64_t q_desc = tc::smem_desc(smem_u32(sq), 16, 1024);
-        const uint64_t k_desc = tc::smem_desc(ring_at, 16, 1024);
-        const uint64_t v_desc = tc::smem_desc(ring_at, kHalfBytes, 1024);
-        // (a descriptor's start address is in units of 16 bytes)
-        auto acquire = [&]() -> int {  // the next stage, filled
-            const int x = st;
-            hold(sh, &sh.full[x], turn, status);
-            if (++st == L::kStages) {
-                st = 0;
-                turn ^= 1;
-            }
-            return x;
-        };
-        auto release = [&](int x) {
-            if (tc::elect()) tc::commit(&sh.empty[x]);
-        };
-        auto scores = [&](auto gc, int x) {  // S_g = Q_g K^T
-            constexpr int g = decltype(gc)::value;
-            tc::fence_after();
-            if (tc::elect()) {
-                const uint64_t kd = k_desc + (uint32_t)(x * (L::kTile / 16));
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t at = ((k / 4) * kHalfBytes + (k % 4) * 32) / 16;
-                    tc::mma_ss(tm + g * kKeys, q_desc + (g * (L::kTile / 16) + at), kd + at, kIdescS,
-                               k > 0);
-                }
-                tc::commit(&sh.s_full[g]);
-            }
-            __syncwarp();
-        };
-        auto values = [&](auto gc, int x, bool add) {  // O_g (+)= P_g V
-            constexpr int g = decltype(gc)::value;
-            hold(sh, &sh.p_full[g], (g ? pn1++ : pn0++) & 1, status);
-            tc::fence_after();
-            if (tc::elect()) {
+            auto values = [&](auto gc, int x, bool add) {  // O_g (+)= P_g V
+                constexpr int g = decltype(gc)::value;
+                const uint32_t phase = (g ? pn1++ : pn0++) & 1;
                 const uint64_t vd = v_desc + (uint32_t)(x * (L::kTile / 16));
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_ts(tm + 2 * kKeys + g * 128, tm + g * kKeys + k * 8,
-                               vd + k * (2048 / 16), kIdescO, add || k > 0);
-            }
-            __syncwarp();
-        };
-        const std::integral_constant<int, 0> g0{};
-        const std::integral_constant<int, 1> g1{};
-        // slots past the tile's last one in a page that holds it: their weights
-        // are zero, and zero times whatever lies there must be zero
-        auto clear_tail = [&](int st, int kb) {
-            const int r0 = p.end - kb * kKeys;
-            if (r0 >= kKeys || r0 <= 0) return;
-            const int r1 = min(kKeys, (r0 + A.piece - 1) / A.piece * A.piece);
-            if (r0 == r1) return;
-            char *v = ring + st * L::kTile;
-            for (int i = lane; i < (r1 - r0) * 8 * kHalves; i += 32) {
-                const int half = i / ((r1 - r0) * 8), x = i - half * (r1 - r0) * 8;
-                *reinterpret_cast<uint4 *>(v + half * kHalfBytes + r0 * 128 + x * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-        };
-        while (walk.next(A, p)) {
-            const int blocks = tc::uniform(p.n), lo = tc::uniform(p.lo), n1 = tc::uniform(p.n1);
-            const bool split = tc::uniform(p.split);
-            if (blocks == 0) continue;
-            hold(sh, &sh.q_full[0], qn0++ & 1, status);
-            if (split) {
-                int x = acquire();
-                scores(g0, x);
-                release(x);
-                if (n1 > 0) {
-                    hold(sh, &sh.q_full[1], qn1++ & 1, status);
-                    x = acquire();
-                    scores(g1, x);
-                    release(x);
+                for (int half = 0; half < 2; ++half) {  // the weights come in two halves
+                    hold(sh, &sh.p_full[g][half], phase, status);
+                    tc::fence_after();
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int k = half * (kKeys / 32); k < (half + 1) * (kKeys / 32); ++k)
+                            tc::mma_ts(tm + 2 * kKeys + g * 128, tm + g * kKeys + k * 8,
+                                       vd + k * (2048 / 16), kIdescO, add || k > 0);
+                    }
+                    __syncwarp();
                 }
-                auto step = [&](auto gc, int i) {  // block i of the tile's run
-                    constexpr int g = decltype(gc)::value;
-                    x = acquire();
-                    clear_tail(x, lo + i);
-                    values(gc, x, i > 1);
+            };
+            const std::integral_constant<int, 0> g0{};
+            const std::integral_constant<int, 1> g1{};
+            // slots past the tile's last one in a page that holds it: their weights
+            // are zero, and zero times whatever lies there must be zero
+            auto clear_tail = [&](int st, int kb, int end) {
+                const int r0 = end - kb * kKeys;
+                if (r0 >= kKeys || r0 <= 0) return;
+                const int r1 = min(kKeys, (r0 + A.piece - 1) / A.piece * A.piece);
+                if (r0 == r1) return;
+                char *v = ring + st * L::kTile;
+                for (int i = lane; i < (r1 - r0) * 8 * kHalves; i += 32) {
+                    const int half = i / ((r1 - r0) * 8), x = i - half * (r1 - r0) * 8;
+                    *reinterpret_cast<uint4 *>(v + half * kHalfBytes + r0 * 128 + x * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+            };
+            PieceReader reader;
+            while (const Piece *p = reader.next(sh, status)) {
+                const int blocks = tc::uniform(p->n), lo = tc::uniform(p->lo), n1 = tc::uniform(p->n1);
+                const int end = tc::uniform(p->end);
+                const bool split = tc::uniform(p->split);
+                reader.done(sh, lane);
+                if (blocks == 0) continue;
+                hold(sh, &sh.q_full[0], qn0++ & 1, status);
+                if (split) {
+                    int x = acquire();
+                    scores(g0, x, blocks <= 2);
                     release(x);
-                    if (i + 2 < blocks) {
+                    if (n1 > 0) {
+                        hold(sh, &sh.q_full[1], qn1++ & 1, status);
                         x = acquire();
-                        scores(gc, x);
+                        scores(g1, x, blocks <= 3);
                         release(x);
-                    } else if (tc::elect()) {
-                        tc::commit(&sh.o_full[g]);
                     }
-                };
-                for (int i = 0; i < blocks; i += 2) {
-                    step(g0, i);
-                    if (i + 1 < blocks) step(g1, i + 1);
+                    auto step = [&](auto gc, int i) {  // block i of the tile's run
+                        constexpr int g = decltype(gc)::value;
+                        x = acquire();
+                        clear_tail(x, lo + i, end);
+                        values(gc, x, i > 1);
+                        release(x);
+                        if (i + 2 < blocks) {
+                            x = acquire();
+                            scores(gc, x, i + 4 >= blocks);
+                            release(x);
+                        } else if (tc::elect()) {
+                            tc::commit(&sh.o_full[g]);
+                        }
+                    };
+                    for (int i = 0; i < blocks; i += 2) {
+                        step(g0, i);
+                        if (i + 1 < blocks) step(g1, i + 1);
+                    }
+                } else {
+                    hold(sh, &sh.q_full[1], qn1++ & 1, status);
+                    int ks = acquire();
+                    scores(g0, ks, blocks == 1);
+                    scores(g1, ks, blocks == 1);
+                    release(ks);
+                    for (int i = 0; i < blocks; ++i) {
+                        const int vs = acquire();
+                        clear_tail(vs, lo + i, end);
+                        const bool more = i + 1 < blocks;
+                        values(g0, vs, i > 0);
+                        if (more) {
+                            ks = acquire();
+                            scores(g0, ks, i + 2 == blocks);
+                        } else if (tc::elect()) {
+                            tc::commit(&sh.o_full[0]);
+                        }
+                        values(g1, vs, i > 0);
+                        release(vs);
+                        if (more) {
+                            scores(g1, ks, i + 2 == blocks);
+                            release(ks);
+                        } else if (tc::elect()) {
+                            tc::commit(&sh.o_full[1]);
+                        }
+                    }
                 }
-            } else {
-                hold(sh, &sh.q_full[1], qn1++ & 1, status);
-                int ks = acquire();
-                scores(g0, ks);
-                scores(g1, ks);
-                release(ks);
-                for (int i = 0; i < blocks; ++i) {
-                    const int vs = acquire();
-                    clear_tail(vs, lo + i);
-                    const bool more = i + 1 < blocks;
-                    values(g0, vs, i > 0);
-                    if (more) {
-                        ks = acquire();
-                        scores(g0, ks);
-                    } else if (tc::elect()) {
-                        tc::commit(&sh.o_full[0]);
-                    }
-                    values(g1, vs, i > 0);
-                    release(vs);
-                    if (more) {
-                        scores(g1, ks);
-                        release(ks);
-                    } else if (tc::elect()) {
-                        tc::commit(&sh.o_full[1]);
-                    }
+                __syncwarp();
+            }
+            if (tc::elect()) tc::commit(&sh.drain);
+            __syncwarp();
+            mbar_wait(&sh.drain, 0);
+        } else if (A.q_boxes) {
+            // ---- copies of queries: a tile's boxes as soon as the last scores
+            // of the tile before it are done
+            uint32_t qn0 = 0, qn1 = 0;
+            PieceReader reader;
+            while (const Piece *pp = reader.next(sh, status)) {
+                const Piece p = *pp;
+                reader.done(sh, lane);
+                if (p.n == 0) continue;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g == 1 && p.n1 == 0) continue;
+                    const uint32_t turn = ((g ? qn1 : qn0) & 1) ^ 1;
+                    if (!__all_sync(0xffffffffu, hold(sh, &sh.q_free[g], turn, status))) continue;
+                    const int r0 = p.row + (p.split ? 0 : g * kRows);
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], L::kTile);
+                    __syncwarp();
+                    if (lane < kHalves)
+                        tc::load_box(sq + g * L::kTile + lane * kHalfBytes, &qmap, lane * 64, 0, p.h,
+                                     p.token + A.by_group.div(r0), &sh.q_full[g]);
+                    if (g) ++qn1;
+                    else ++qn0;
                 }
             }
-            __syncwarp();
+            // every box has landed before the CTA may end
+            if (qn0 > 0) mbar_wait(&sh.q_full[0], (qn0 - 1) & 1);
+            if (qn1 > 0) mbar_wait(&sh.q_full[1], (qn1 - 1) & 1);
+        } else {
+            PieceReader reader;
+            while (reader.next(sh, status)) reader.done(sh, lane);
         }
-        if (tc::elect()) tc::commit(&sh.drain);
-        __syncwarp();
-        mbar_wait(&sh.drain, 0);
-    } else if (warp < 8) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax ------------------------------------------------------
-        const int g = warp / 4, gt = tid - g * 128, gw = warp % 4;
-        const uint32_t lanes = (uint32_t)(gw * 32) << 16;
-        const uint32_t t_s = tmem + lanes + g * kKeys;
-        const uint32_t t_own = tmem + lanes + 2 * kKeys + g * 128;  // O of this group
-        const uint32_t t_other = tmem + lanes + 2 * kKeys + (1 - g) * 128;
-        uint32_t sn = 0, own_n = 0, other_n = 0;
-        char *q_s = sq + g * L::kTile;
-        float2 *own_stats = reinterpret_cast<float2 *>(q_s);
-        const float2 *other_stats = reinterpret_cast<const float2 *>(sq + (1 - g) * L::kTile);
-        float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
-        float4 *part_out = reinterpret_cast<float4 *>(A.workspace + kAttendOut);
-        uint32_t *counters = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters);
+        const int g = warp / 4, gw = warp % 4, gt = gw * 32 + lane;
+        const uint32_t t_s = tmem + ((uint32_t)(gw * 32) << 16) + g * kKeys;
+        const uint32_t t_o = tmem + ((uint32_t)(gw * 32) << 16) + 2 * kKeys;  // group 0's O
+        float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
         const int D = A.head_dim;
-
-        while (walk.next(A, p)) {
-            const int n = walk.s.n, len = walk.s.len, row0 = walk.s.row0;
-            const int steps = g ? p.n1 : p.n0;
-            const int r_base = p.tile * 2 * kRows + (p.split ? 0 : g * kRows);
-            const int rows = p.split ? p.rows : min(kRows, p.rows - g * kRows);
-            if (steps > 0) {
+        uint32_t sn = 0, own_n = 0, other_n = 0, group_turn = 0, both_turn = 0;
+        PieceReader reader;
+        while (const Piece *pp = reader.next(sh, status)) {
+            const Piece &p = *pp;
+            const bool split = p.split != 0;
+            const int steps = g == 0 && split ? p.n - p.n1 : p.n1;
+            const int r_base = p.row + (split ? 0 : g * kRows);
+            const int rows = split ? p.rows : min(kRows, p.rows - g * kRows);
+            if (steps > 0 && !A.q_boxes) {
                 // eight loads in flight per thread
+                char *q_s = sq + g * L::kTile;
                 constexpr int kChunks = DP / 8, kStep = 128 / kChunks;
                 const int ch = gt % kChunks;
+                const uint32_t flip = A.q_mode == 1 ? 0x80008000u : 0u;
                 for (int r0 = gt / kChunks; r0 < rows; r0 += 8 * kStep) {
                     uint4 x[8];
 #pragma unroll
@@ -635,14 +773,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             const int pr = r_base + r, j = A.by_group.div(pr);
                             const int hq = p.h * A.group + (pr - j * A.group);
                             x[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                static_cast<const uint16_t *>(A.q) + (int64_t)(row0 + j) * A.q_st[0] +
-                                hq * A.q_st[1] + ch * 8));
+                                static_cast<const uint16_t *>(A.q) +
+                                (int64_t)(p.token + j) * A.q_st[0] + hq * A.q_st[1] + ch * 8));
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = r0 + i * kStep;
-                        const uint32_t flip = A.q_mode == 1 ? 0x80008000u : 0u;
                         if (r < rows)
                             *reinterpret_cast<uint4 *>(q_s + (ch / 8) * kHalfBytes + r * 128 +
                                                        (((ch % 8) ^ (r & 7)) * 16)) =
@@ -653,103 +790,104 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_full[g]);
             }
-            const bool mine = gw * 32 + lane < rows;       // this thread's row exists
-            const bool any = gw * 32 < rows;               // one of the warp's does
-            const int pr = r_base + gw * 32 + lane, j = A.by_group.div(pr);
-            const int limit = mine ? len - n + j : len;    // last slot it sees
-            const int lowest = A.window > 0 ? limit - A.window + 1 : 0;
+            const bool mine = gt < rows;        // this thread's row exists
+            const bool any = gw * 32 < rows;    // one of the warp's does
             float ref = -INFINITY, sum = 0.f;
-            for (int i = 0; i < steps; ++i) {
-                hold(sh, &sh.s_full[g], sn++ & 1, status);
-                __syncwarp();
-                if (any) {
-                    tc::fence_after();
-                    const int k0 = p.block(g, i) * kKeys;
-                    const bool edge =
-                        __any_sync(0xffffffffu, mine && (k0 + kKeys - 1 > limit || k0 < lowest));
-                    const int hi = limit - k0, lo = lowest - k0;
-                    // the row of S is read twice, 64 columns at a time: keeping
-                    // all 128 in registers spills
-                    auto columns = [&](uint32_t (&x)[2][32], int at) {
-                        tc::ld32(x[0], t_s + at);
-                        tc::ld32(x[1], t_s + at + 32);
-                        tc::wait_ld();
-                        if (edge) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (at + 32 * q + e > hi || at + 32 * q + e < lo)
-                                        x[q][e] = 0xff800000u;
+            {
+                // last slot the row sees, relative to the block at hand
+                int limit = mine ? p.past + A.by_group.div(r_base + gt) : 0x7fffff00;
+                const int k0 = (p.lo + (split ? g : 0)) * kKeys;
+                limit -= k0;
+                const int stride = split ? 2 * kKeys : kKeys;
+                const int span = A.window > 0 ? A.window : 0x7fffffff;  // slots a row may see
+                for (int i = 0; i < steps; ++i, limit -= stride) {
+                    hold(sh, &sh.s_full[g], sn++ & 1, status);
+                    __syncwarp();
+                    if (!any) {
+                        if (lane == 0) {
+                            mbar_arrive(&sh.p_full[g][0]);
+                            mbar_arrive(&sh.p_full[g][1]);
                         }
-                    };
+                        continue;
+                    }
+                    tc::fence_after();
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc::ld32(x[q], t_s + 32 * q);
+                    tc::wait_ld();
+                    if (__any_sync(0xffffffffu, mine && (limit < kKeys - 1 || limit >= span))) {
+                        const int lo = max(limit, -1) - span + 1;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * q + e > limit || 32 * q + e < lo) x[q][e] = 0xff800000u;
+                    }
                     float m = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int at = 0; at < kKeys; at += 64) {
-                        uint32_t x[2][32];
-                        columns(x, at);
+                    for (int q = 0; q < 4; q += 2)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            m = fmaxf(m, __uint_as_float(x[0][e]));
-                            m1 = fmaxf(m1, __uint_as_float(x[1][e]));
+                            m = fmaxf(m, __uint_as_float(x[q][e]));
+                            m1 = fmaxf(m1, __uint_as_float(x[q + 1][e]));
                         }
-                    }
                     m = fmaxf(m, m1) * A.scale_log2;
-                    const bool grow = mine && (m > ref + kRescaleAbove || (ref == -INFINITY && m > ref));
+                    const bool grow =
+                        mine && (m > ref + kRescaleAbove || (ref == -INFINITY && m > ref));
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to = grow ? m : ref;
-                        const float a = ref == -INFINITY ? 0.f : ex2(ref - to);
+                        const float f = grow ? (ref == -INFINITY ? 0.f : ex2(ref - to)) : 1.f;
                         if (i > 0 && __any_sync(0xffffffffu, grow && ref != -INFINITY)) {
-                            const float f = grow ? a : 1.f;
-#pragma unroll
-                            for (int q = 0; q < DP / 32; ++q) {
-                                uint32_t o[32];
-                                tc::ld32(o, t_own + 32 * q);
+#pragma unroll 1
+                            for (int q = 0; q < DP / 16; ++q) {
+                                uint32_t o[16];
+                                tc::ld16(o, t_o + g * 128 + 16 * q);
                                 tc::wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tc::st32(t_own + 32 * q, o);
+                                tc::st16(t_o + g * 128 + 16 * q, o);
                             }
                         }
-                        if (grow) sum *= a;
+                        sum *= f;
                         ref = to;
                     }
                     const float minus = ref == -INFINITY ? 0.f : -ref;
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int at = 0; at < kKeys; at += 64) {
-                        uint32_t x[2][32], w[32];
-                        columns(x, at);
+                    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float a = ex2(fmaf(__uint_as_float(x[e / 16][2 * (e % 16)]),
-                                                     A.scale_log2, minus));
-                            const float b = ex2(fmaf(__uint_as_float(x[e / 16][2 * (e % 16) + 1]),
-                                                     A.scale_log2, minus));
-                            s0 += a;
-                            s1 += b;
-                            w[e] = pack2<T>(a, b);
+                        for (int q = 2 * half; q < 2 * half + 2; ++q) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float a =
+                                    ex2(fmaf(__uint_as_float(x[q][2 * e]), A.scale_log2, minus));
+                                const float b =
+                                    ex2(fmaf(__uint_as_float(x[q][2 * e + 1]), A.scale_log2, minus));
+                                s0 += a;
+                                s1 += b;
+                                w[e] = pack2<T>(a, b);
+                            }
+                            tc::st16(t_s + 16 * q, w);
                         }
-                        // over columns that have been read
-                        tc::st32(t_s + at / 2, w);
+                        tc::wait_st();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p_full[g][half]);
                     }
                     sum += s0 + s1;
-                    tc::wait_st();
-                    tc::fence_before();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[g]);
             }
-            const int other_steps = g ? p.n0 : p.n1;
+            const int other_steps = g == 0 ? (split ? p.n1 : 0) : (split ? p.n - p.n1 : 0);
             float own_f = 1.f, other_f = 0.f;  // factors of the two groups' O
-            if (p.split) {
+            if (split) {
                 // join the groups' states; group g then has half the columns
                 if (steps > 0) hold(sh, &sh.o_full[g], own_n++ & 1, status);
                 if (other_steps > 0) hold(sh, &sh.o_full[1 - g], other_n++ & 1, status);
-                own_stats[gt] = make_float2(ref, sum);
-                tc::named_barrier(1, 256);
-                const float2 o = other_stats[gt];
+                stats[g * kRows + gt] = make_float2(ref, sum);
+                meet(sh, &sh.both_sync, both_turn, lane, status);
+                const float2 o = stats[(1 - g) * kRows + gt];
                 const float to = fmaxf(ref, o.x);
                 own_f = ref == -INFINITY ? 0.f : ex2(ref - to);
                 other_f = o.x == -INFINITY ? 0.f : ex2(o.x - to);
@@ -763,27 +901,36 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 // order of the products
                 ++other_n;
             }
+            __syncwarp();
             tc::fence_after();
-            const int c0 = p.split ? g * (DP / 2) : 0;      // this group's columns
-            const int c1 = p.split ? c0 + DP / 2 : DP;
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            uint16_t *out = static_cast<uint16_t *>(A.out) + (int64_t)(row0 + j) * A.o_st[0] +
-                            (p.h * A.group + (pr - j * A.group)) * A.o_st[1];
+            const int c0 = split ? g * (DP / 2) : 0;      // this group's columns
+            const int c1 = split ? c0 + DP / 2 : DP;
+            const int part_row = split ? 0 : g * kRows;
             const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
+            auto row_of = [&](int r) -> uint16_t * {      // row r of the group in out
+                const int pr = r_base + r, j = A.by_group.div(pr);
+                return static_cast<uint16_t *>(A.out) + (int64_t)(p.token + j) * A.o_st[0] +
+                       (p.h * A.group + (pr - j * A.group)) * A.o_st[1];
+            };
             if (any) {
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                uint16_t *out = row_of(gt);
+                float4 *part = reinterpret_cast<float4 *>(A.workspace + kAttendOut) +
+                               (int64_t)slot * (kMaxHeadDim / 4) * 256 + part_row + gt;
+#pragma unroll 1
                 for (int cc = c0; cc < c1; cc += 32) {
                     float v[32];
                     uint32_t o[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                     if (steps > 0) {
-                        tc::ld32(o, t_own + cc);
+                        tc::ld32(o, t_o + g * 128 + cc);
                         tc::wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = own_f * __uint_as_float(o[e]);
                     }
-                    if (p.split && other_steps > 0) {
-                        tc::ld32(o, t_other + cc);
+                    if (split && other_steps > 0) {
+                        tc::ld32(o, t_o + (1 - g) * 128 + cc);
                         tc::wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
@@ -792,36 +939,31 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     if (p.parts > 1) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            part_out[((int64_t)slot * (kMaxHeadDim / 4) + (cc + e) / 4) * 256 +
-                                     (p.split ? 0 : g * kRows) + gt] =
-                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                            part[(cc + e) / 4 * 256] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     } else if (mine) {
+                        uint32_t y[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            if (cc + e < D) {
-                                uint4 y;
-                                y.x = pack2<T>(v[e] * inv, v[e + 1] * inv);
-                                y.y = pack2<T>(v[e + 2] * inv, v[e + 3] * inv);
-                                y.z = pack2<T>(v[e + 4] * inv, v[e + 5] * inv);
-                                y.w = pack2<T>(v[e + 6] * inv, v[e + 7] * inv);
-                                if (sum == 0.f) y = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4 *>(out + cc + e) = y;
-                            }
+                        for (int e = 0; e < 16; ++e)
+                            y[e] = sum == 0.f ? 0u : pack2<T>(v[2 * e] * inv, v[2 * e + 1] * inv);
+                        store_row(out + cc, y, D - cc, A.wide_out);
                     }
                 }
                 tc::fence_before();
             }
             if (p.parts > 1) {
+                float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
+                const float4 *part_out = reinterpret_cast<const float4 *>(A.workspace + kAttendOut);
                 part_stats[(slot * 2 + g) * kRows + gt] = make_float2(ref, sum);
                 __threadfence();
-                tc::named_barrier(2 + g, 128);
+                meet(sh, &sh.group_sync[g], group_turn, lane, status);
                 if (gt == 0) {
-                    uint32_t *c = counters + 2 * p.first + g;
+                    uint32_t *c = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters) +
+                                  2 * p.first + g;
                     const bool last = atomicAdd(c, 1u) == (uint32_t)p.parts - 1;
                     if (last) *c = 0;
                     sh.last[g] = last;
                 }
-                tc::named_barrier(2 + g, 128);
+                meet(sh, &sh.group_sync[g], group_turn, lane, status);
                 if (sh.last[g]) {
                     __threadfence();
                     // warps share the 32-row strips; a strip's warps share its columns
@@ -830,55 +972,67 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     const int strip = gw / per, share = gw % per;
                     const int wide = (c1 - c0) / per;
                     const int r = strip * 32 + lane;
-                    const int cr = r_base + r, cj = A.by_group.div(cr);
-                    uint16_t *co = static_cast<uint16_t *>(A.out) + (int64_t)(row0 + cj) * A.o_st[0] +
-                                   (p.h * A.group + (cr - cj * A.group)) * A.o_st[1];
-                    auto slot_of = [&](int i) -> int {
-                        return (p.first + i) * 2 + (i == 0 ? 1 : 0);
-                    };
+                    auto slot_of = [&](int i) -> int { return (p.first + i) * 2 + (i == 0 ? 1 : 0); };
                     if (strip < strips) {
+                        uint16_t *co = row_of(r);
                         float top = -INFINITY, all = 0.f;
+#pragma unroll 4
                         for (int i = 0; i < p.parts; ++i)
                             top = fmaxf(top, __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]).x);
+#pragma unroll 4
                         for (int i = 0; i < p.parts; ++i) {
                             const float2 x = __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]);
                             all += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - top);
                         }
                         const float norm = all > 0.f ? 1.f / all : 0.f;
-                        for (int cc = c0 + share * wide; cc < c0 + (share + 1) * wide; cc += 8) {
-                            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        // 16 columns at a time, four parts' loads in flight
+#pragma unroll 1
+                        for (int cc = c0 + share * wide; cc < c0 + (share + 1) * wide; cc += 16) {
+                            const int quads = min(4, (c0 + (share + 1) * wide - cc) / 4);
+                            float4 v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                             for (int i = 0; i < p.parts; ++i) {
                                 const float m = __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]).x;
+                                const float4 *at = part_out +
+                                                   ((int64_t)slot_of(i) * (kMaxHeadDim / 4) + cc / 4) * 256 +
+                                                   part_row + r;
+                                float4 a[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (e < quads) a[e] = __ldcg(at + e * 256);
                                 const float f = m == -INFINITY ? 0.f : ex2(m - top);
-                                const float4 *at =
-                                    part_out + ((int64_t)slot_of(i) * (kMaxHeadDim / 4) + cc / 4) * 256 +
-                                    (p.split ? 0 : g * kRows) + r;
-                                const float4 a = __ldcg(at), b = __ldcg(at + 256);
-                                v[0] += f * a.x;
-                                v[1] += f * a.y;
-                                v[2] += f * a.z;
-                                v[3] += f * a.w;
-                                v[4] += f * b.x;
-                                v[5] += f * b.y;
-                                v[6] += f * b.z;
-                                v[7] += f * b.w;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (e < quads) {
+                                        v[e].x += f * a[e].x;
+                                        v[e].y += f * a[e].y;
+                                        v[e].z += f * a[e].z;
+                                        v[e].w += f * a[e].w;
+                                    }
                             }
-                            if (r < rows && cc < D) {
-                                uint4 y;
-                                y.x = pack2<T>(v[0] * norm, v[1] * norm);
-                                y.y = pack2<T>(v[2] * norm, v[3] * norm);
-                                y.z = pack2<T>(v[4] * norm, v[5] * norm);
-                                y.w = pack2<T>(v[6] * norm, v[7] * norm);
-                                if (all == 0.f) y = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4 *>(co + cc) = y;
+                            if (r < rows) {
+#pragma unroll
+                                for (int e = 0; e < 4; e += 2)
+                                    if (e < quads && cc + 4 * e < D) {
+                                        uint4 y;
+                                        y.x = pack2<T>(v[e].x * norm, v[e].y * norm);
+                                        y.y = pack2<T>(v[e].z * norm, v[e].w * norm);
+                                        y.z = pack2<T>(v[e + 1].x * norm, v[e + 1].y * norm);
+                                        y.w = pack2<T>(v[e + 1].z * norm, v[e + 1].w * norm);
+                                        if (all == 0.f) y = make_uint4(0, 0, 0, 0);
+                                        *reinterpret_cast<uint4 *>(co + cc + 4 * e) = y;
+                                    }
                             }
                         }
                     }
                 }
             }
-            // the joined states have been read before the next piece reuses the
-            // query tiles and the accumulators
-            if (p.split) tc::named_barrier(1, 256);
+            // the joined states and accumulators have been read before the next
+            // piece writes its own
+            if (split) meet(sh, &sh.both_sync, both_turn, lane, status);
+            reader.done(sh, lane);
         }
     }
     tc::fence_before();
