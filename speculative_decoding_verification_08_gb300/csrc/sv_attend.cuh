@@ -265,6 +265,35 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Two floats in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t bits2(uint32_t a, uint32_t b) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "r"(a), "r"(b));
+    return y;
+}
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    return bits2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void unpair2(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
@@ -823,19 +852,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             for (int e = 0; e < 32; ++e)
                                 if (32 * q + e > limit || 32 * q + e < lo) x[q][e] = 0xff800000u;
                     }
-                    float m = -INFINITY, m1 = -INFINITY;
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2)
+                    for (int e = 0; e < 32; e += 2)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            m = fmaxf(m, __uint_as_float(x[q][e]));
-                            m1 = fmaxf(m1, __uint_as_float(x[q + 1][e]));
-                        }
-                    m = fmaxf(m, m1) * A.scale_log2;
+                        for (int q = 0; q < 4; ++q)
+                            m[q] = max3(m[q], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
+                    const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * A.scale_log2;
                     const bool grow =
-                        mine && (m > ref + kRescaleAbove || (ref == -INFINITY && m > ref));
+                        mine && (top > ref + kRescaleAbove || (ref == -INFINITY && top > ref));
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float to = grow ? m : ref;
+                        const float to = grow ? top : ref;
                         const float f = grow ? (ref == -INFINITY ? 0.f : ex2(ref - to)) : 1.f;
                         if (i > 0 && __any_sync(0xffffffffu, grow && ref != -INFINITY)) {
 #pragma unroll 1
@@ -853,7 +880,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         ref = to;
                     }
                     const float minus = ref == -INFINITY ? 0.f : -ref;
-                    float s0 = 0.f, s1 = 0.f;
+                    const uint64_t scale2 = pair2(A.scale_log2, A.scale_log2), minus2 = pair2(minus, minus);
+                    uint64_t sums = 0;  // of even and odd columns
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -861,12 +889,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             uint32_t w[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const float a =
-                                    ex2(fmaf(__uint_as_float(x[q][2 * e]), A.scale_log2, minus));
-                                const float b =
-                                    ex2(fmaf(__uint_as_float(x[q][2 * e + 1]), A.scale_log2, minus));
-                                s0 += a;
-                                s1 += b;
+                                float a, b;
+                                unpair2(fma2(bits2(x[q][2 * e], x[q][2 * e + 1]), scale2, minus2), a, b);
+                                a = ex2(a);
+                                b = ex2(b);
+                                sums = add2(sums, pair2(a, b));
                                 w[e] = pack2<T>(a, b);
                             }
                             tc::st16(t_s + 16 * q, w);
@@ -876,7 +903,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.p_full[g][half]);
                     }
-                    sum += s0 + s1;
+                    float even, odd;
+                    unpair2(sums, even, odd);
+                    sum += even + odd;
                 }
             }
             const int other_steps = g == 0 ? (split ? p.n1 : 0) : (split ? p.n - p.n1 : 0);
