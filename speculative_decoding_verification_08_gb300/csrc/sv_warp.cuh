@@ -1,10 +1,18 @@
 // sv_warp.cuh -- the warp of logits into probability rows (temperature, top-k,
 // top-p, min-p) and draws from them.
 //
+// A cluster of CTAs takes a row and keeps it in its shared memory (a slice per
+// CTA), so the row is read from memory once whatever the filters need.
+//
 // Every filter keeps a prefix of the row's order (logit descending, index
 // ascending), so the kept set is one threshold on the 64-bit composite
-// (ordered logit bits, ~index).  A row's thresholds are found by bisection:
-// counts for top-k, masses for top-p; min-p gives its logit directly.
+// (ordered logit bits, ~index); min-p gives its logit directly.  Top-k and
+// top-p find theirs in two sweeps: a histogram over the distance from the
+// maximum (counts, or masses in fixed point, whose integer sums do not depend
+// on the order of the atomics) narrows the border to a bin or two, then the
+// elements of those bins are gathered, ranked, and the border is settled on
+// exact values.  A border bin too full to gather (rows of equal logits) is
+// settled by bisection of the composite instead.
 //
 // Masses decide which tokens stay and which one is drawn, and must give the
 // answers of a 64-bit evaluation.  fp64 runs at 1/64 of the fp32 rate here, so
@@ -13,12 +21,21 @@
 // the low part, good to about 5e-12 relative.
 #pragma once
 
+#include <cooperative_groups.h>
+
+#include "sv_barrier.cuh"
 #include "sv_cache.cuh"
 
 namespace sv {
 
-constexpr int kWarpThreads = 1024;
+constexpr int kWarpThreads = 512;
 constexpr int kWarpWarps = kWarpThreads / 32;
+constexpr int kWarpMaxCluster = 8;
+constexpr int kBins = 1024;
+constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
+constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
+constexpr int kLocalList = 256;        // border elements one CTA may gather
+constexpr int kList = 1024;            // and the row
 
 struct WarpParams {
     const void *z;
@@ -30,7 +47,8 @@ struct WarpParams {
     float *probs;
     int64_t ps;
     uint32_t *status;
-    int32_t R;
+    int32_t R, slice;   // elements per CTA, a multiple of 16
+    int32_t cached;     // 16-byte words of a slice that fit in shared memory
 };
 
 // Floats in order: a < b iff ordered(a) < ordered(b) (-0 and 0 alike).
@@ -47,18 +65,29 @@ __device__ __forceinline__ uint64_t composite(float z, int64_t v) {
     return ((uint64_t)ordered(z) << 32) | (uint32_t)~(uint32_t)v;
 }
 
-// 2^(j / 32), j = -16..16, as hi + lo, in shared memory.
-struct ExpTable {
-    float2 t[33];
-};
+// 2^(j / 32), j = -16..15, as hi + lo (correctly rounded); every CTA copies it
+// to shared memory, where its lanes read different entries at once.
+__constant__ float2 kPow2[32] = {
+    {0.707106769f, 1.21016175e-08f}, {0.722590387f, 1.66209997e-08f},
+    {0.738413095f, -2.25044943e-08f}, {0.754582226f, -1.24796866e-08f},
+    {0.771105409f, 4.03545242e-09f}, {0.787990451f, -2.83051271e-08f},
+    {0.805245161f, 4.91810859e-09f}, {0.822877765f, -2.56248605e-08f},
+    {0.840896428f, -1.23776633e-08f}, {0.859309673f, -2.4248088e-08f},
+    {0.878126085f, -4.61788519e-09f}, {0.897354543f, -5.70752245e-09f},
+    {0.917004049f, -5.61963898e-09f}, {0.93708384f, -2.33150281e-08f},
+    {0.957603276f, 4.92266405e-09f}, {0.978572071f, -8.51090221e-09f},
+    {1.f, 0.f}, {1.0218972f, -4.81155986e-08f},
+    {1.04427373f, 4.83347016e-08f}, {1.06714046f, -5.93375198e-08f},
+    {1.09050775f, -1.30775399e-08f}, {1.1143868f, -5.43554002e-08f},
+    {1.13878858f, 5.38622231e-08f}, {1.1637249f, -4.05144149e-08f},
+    {1.18920708f, 3.79763527e-08f}, {1.21524739f, -3.26739489e-08f},
+    {1.24185777f, 4.4968381e-08f}, {1.26905096f, 1.41933332e-09f},
+    {1.29683959f, -4.01899953e-08f}, {1.32523668f, -3.49637332e-08f},
+    {1.35425556f, -1.01233493e-08f}, {1.38390994f, -5.87557736e-08f}};
 
-__device__ __forceinline__ void fill_table(ExpTable &tab) {
-    for (int i = threadIdx.x; i < 33; i += blockDim.x) {
-        const double x = exp2((i - 16) / 32.0);
-        const float h = (float)x;
-        tab.t[i] = make_float2(h, (float)(x - (double)h));
-    }
-}
+struct ExpTable {
+    float2 t[32];
+};
 
 struct RowScale {
     float m, ch, cl;  // row maximum; log2(e) / temperature as hi + lo
@@ -106,6 +135,46 @@ __device__ __forceinline__ float2 weight(float z, const RowScale &S, const ExpTa
     return make_float2(wh * scale, wl * scale);
 }
 
+// Sums of weights as pairs of floats (fp64 runs at 1/64 of the fp32 rate here):
+// relative errors near 2^-46.
+struct dd2 {
+    float h, l;
+};
+
+__device__ __forceinline__ dd2 norm2(float h, float l) {
+    const float s = h + l;
+    return {s, l - (s - h)};
+}
+__device__ __forceinline__ dd2 add_dd(dd2 a, dd2 b) {
+    const float s = a.h + b.h, x = s - a.h;
+    return norm2(s, ((a.h - (s - x)) + (b.h - x)) + (a.l + b.l));
+}
+__device__ __forceinline__ dd2 mul_dd(dd2 a, dd2 b) {
+    const float p = a.h * b.h;
+    return norm2(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h));
+}
+__device__ __forceinline__ bool less_dd(dd2 a, dd2 b) {
+    return a.h < b.h || (a.h == b.h && a.l < b.l);
+}
+__device__ __forceinline__ dd2 shfl_dd(dd2 a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
+}
+// The sum over the warp, the same in every lane (the steps are symmetric).
+__device__ __forceinline__ dd2 warp_sum_dd(dd2 a) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        a = add_dd(a, {__shfl_xor_sync(0xffffffffu, a.h, d), __shfl_xor_sync(0xffffffffu, a.l, d)});
+    return a;
+}
+__device__ __forceinline__ dd2 warp_scan_dd(dd2 a, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const dd2 o = {__shfl_up_sync(0xffffffffu, a.h, d), __shfl_up_sync(0xffffffffu, a.l, d)};
+        if (lane >= d) a = add_dd(o, a);
+    }
+    return a;
+}
+
 // A running sum of weights.
 struct Mass {
     float h = 0.f, l = 0.f;
@@ -114,178 +183,815 @@ struct Mass {
         l += ((h - (s - b)) + (w.x - b)) + w.y;
         h = s;
     }
-    __device__ __forceinline__ double value() const { return (double)h + (double)l; }
+    __device__ __forceinline__ dd2 value() const { return norm2(h, l); }
+};
+
+namespace cg = cooperative_groups;
+
+// exp((z - max) / T) in fp32, good to about 2^-22: the exponent with its low
+// part, its fraction through ex2.approx.
+__device__ __forceinline__ float fast_weight(float z, const RowScale &S) {
+    const float d = z - S.m;
+    const float e = d * S.ch;
+    if (!(e >= -125.f)) return 0.f;
+    const float bb = d - z;
+    const float dl = (z - (d - bb)) - (S.m + bb);
+    float el = fmaf(d, S.ch, -e);
+    el = fmaf(d, S.cl, el);
+    el = fmaf(dl, S.ch, el);
+    const float n = rintf(e);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((e - n) + el));
+    return __int_as_float(__float_as_int(y) + ((int)n << 23));
+}
+
+// What the CTAs of a cluster read of one another.
+struct alignas(16) WarpShared {
+    unsigned long long bar;
+    ExpTable tab;
+    float top, low;                 // slice maximum and smallest finite logit
+    int32_t bad;
+    float ch, cl;                   // log2(e) / temperature
+    dd2 min_off;                    // temperature * ln(min_p)
+    uint32_t count, gathered;       // border elements
+    int32_t k_bin, lo_bin, hi_bin, k_before;
+    float k_mass, k_slack;
+    uint64_t threshold;
+    dd2 slice_mass[3];              // kept, above, within
+    dd2 rank_mass[kWarpMaxCluster]; // what stays of every rank's slice
+    dd2 run_mass[kWarpWarps];       // kept mass of each warp's run
+    dd2 part_mass[kWarpWarps], in_mass[kWarpWarps];
+    uint64_t warp_key[kWarpWarps];
+    float warp_f[2][kWarpWarps];
+    uint32_t warp_u[kWarpWarps];
+    uint64_t list[kLocalList];
+    union {
+        struct {
+            uint32_t count[kBins], mass[kBins];
+        } hist;
+        uint64_t all[kList];        // the row's border elements
+    };
 };
 
 template <class T>
-__device__ __forceinline__ T block_sum(T x, T *sm) {
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = x;
-    __syncthreads();
-    T s = 0;
-    for (int w = 0; w < kWarpWarps; ++w) s += sm[w];  // one order on every thread
-    return s;
+struct WordOf {
+    static constexpr int kElems = 16 / (int)sizeof(T);
+};
+
+template <class T>
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[16 / sizeof(T)]) {
+    if constexpr (sizeof(T) == 4) {
+        x[0] = __uint_as_float(w.x);
+        x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z);
+        x[3] = __uint_as_float(w.w);
+    } else {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            T a, b;
+            *reinterpret_cast<uint16_t *>(&a) = (uint16_t)(u[i] & 0xffffu);
+            *reinterpret_cast<uint16_t *>(&b) = (uint16_t)(u[i] >> 16);
+            x[2 * i] = to_f32<T>(a);
+            x[2 * i + 1] = to_f32<T>(b);
+        }
+    }
 }
 
 template <class T>
-__global__ void __launch_bounds__(kWarpThreads) warp_kernel(const __grid_constant__ WarpParams A) {
-    __shared__ ExpTable tab;
-    __shared__ double sm[kWarpWarps];
-    __shared__ uint64_t smk[kWarpWarps];
-    __shared__ int64_t found;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int64_t r = blockIdx.x;
-    const T *z = static_cast<const T *>(A.z) + r * A.zs;
-    const int64_t V = A.V;
-    auto at = [&](int64_t v) -> float { return to_f32<T>(z[v]); };
-    fill_table(tab);
-    if (tid == 0) found = -1;
+__device__ __forceinline__ T minus_inf();
+template <>
+__device__ __forceinline__ float minus_inf() {
+    return -INFINITY;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 minus_inf() {
+    return __ushort_as_bfloat16(0xff80u);
+}
+template <>
+__device__ __forceinline__ __half minus_inf() {
+    return __ushort_as_half(0xfc00u);
+}
 
-    // the row's first element in the order; NaN and +inf counted as bad
-    uint64_t top = 0;
-    int bad = 0;
-    for (int64_t v = tid; v < V; v += kWarpThreads) {
-        const float x = at(v);
-        bad |= !(x < INFINITY);
-        const uint64_t c = composite(x, v);
-        top = c > top ? c : top;
+template <class T>
+__global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_constant__ WarpParams A) {
+    constexpr int E = WordOf<T>::kElems;
+    extern __shared__ __align__(16) char raw[];
+    WarpShared &sh = *reinterpret_cast<WarpShared *>(raw);
+    uint4 *words = reinterpret_cast<uint4 *>(raw + sizeof(WarpShared));
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int64_t r = blockIdx.x / C;
+    const int64_t base = min(A.V, (int64_t)rank * A.slice);  // this CTA's elements
+    const int n = (int)(min(A.V, base + A.slice) - base);
+    const T *z = static_cast<const T *>(A.z) + r * A.zs + base;
+    // word w holds elements w * E - shift ..; what lies outside is -inf
+    const int shift = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
+    const int W = n > 0 ? (n + shift + E - 1) / E : 0;
+    const int held = min(W, A.cached);
+
+    // ---- the slice into shared memory ------------------------------------
+    if (tid == 0) {
+        mbar_init(&sh.bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.bad = 0;
+        sh.count = 0;
     }
-    for (int d = 16; d > 0; d >>= 1) {
-        const uint64_t o = __shfl_xor_sync(0xffffffffu, top, d);
-        top = o > top ? o : top;
+    if (tid >= 32 && tid < 64) sh.tab.t[lane] = kPow2[lane];
+    __syncthreads();
+    wait_for_primary_grid();
+    const int w0 = shift ? 1 : 0;                          // first whole word
+    const int w1 = min(held, (n + shift) / E);             // one past the last
+    const int whole = max(0, w1 - w0);
+    if (tid == 0) {
+        mbar_arrive_expect_tx(&sh.bar, (uint32_t)whole * 16u);
+        const char *src = reinterpret_cast<const char *>(z - shift) + w0 * 16;
+        for (int at = 0; at < whole; at += 1024) {
+            const int part = min(1024, whole - at);
+            bulk_copy_g2s(words + w0 + at, src + (int64_t)at * 16, (uint32_t)part * 16u, &sh.bar);
+        }
     }
-    if (lane == 0) smk[warp] = top;
-    bad = __syncthreads_or(bad);
-    for (int w = 0; w < kWarpWarps; ++w) top = smk[w] > top ? smk[w] : top;
-    const float m = unordered((uint32_t)(top >> 32));
+    if (tid < 2 * E) {  // the ragged words at both ends
+        const int w = tid < E ? 0 : W - 1;
+        if (w >= 0 && w < held && (w < w0 || w >= w1)) {
+            const int e = w * E - shift + tid % E;
+            reinterpret_cast<T *>(words)[w * E + tid % E] = e >= 0 && e < n ? z[e] : minus_inf<T>();
+        }
+    }
+    // the row's settings; what of them needs fp64 is one thread's work while
+    // the copy runs
     const float temp = A.temperature ? A.temperature[r] : 1.f;
-    bad |= !(temp > 0.f && temp < INFINITY);
+    const int64_t k = A.top_k ? A.top_k[r] : 0;
+    const float p = A.top_p ? A.top_p[r] : 1.f;
+    const float mp = A.min_p ? A.min_p[r] : 0.f;
+    if (tid == 64) {
+        const RowScale s = row_scale(0.f, temp);
+        sh.ch = s.ch;
+        sh.cl = s.cl;
+    }
+    if (tid == 96 && mp > 0.f) {
+        const double off = (double)temp * log((double)mp);
+        sh.min_off = {(float)off, (float)(off - (double)(float)off)};
+    }
+    const bool came = mbar_wait(&sh.bar, 0);
+    if (!__syncthreads_and(came) && tid == 0) {
+        atomicOr(A.status, SV_STATUS_TIMEOUT);
+        sh.bad = 1;
+    }
+
+    // every warp takes a run of words, its lanes in turn
+    const int run = (W + kWarpWarps * 32 - 1) / (kWarpWarps * 32) * 32;
+    const int s0 = min(W, run * warp), s1 = min(W, s0 + run);
+    auto load = [&](int w, float (&x)[E]) {
+        if (w < held) {
+            unpack<T>(words[w], x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int e = w * E - shift + i;
+                x[i] = e >= 0 && e < n ? to_f32<T>(z[e]) : -INFINITY;
+            }
+        }
+    };
+    auto index_of = [&](int w, int i) -> int64_t { return base + w * E - shift + i; };
+    auto largest = [&](const float (&x)[E]) -> float {
+        float y = x[0];
+#pragma unroll
+        for (int i = 1; i < E; ++i) y = fmaxf(y, x[i]);
+        return y;
+    };
+
+    // ---- maximum, smallest finite logit, values that spoil the row ---------
+    {
+        float top = -INFINITY, low = INFINITY;
+        bool bad = false;
+        for (int w = s0 + lane; w < s1; w += 32) {
+            float x[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                bad |= !(x[i] < INFINITY);
+                top = fmaxf(top, x[i]);
+                low = fminf(low, x[i] == -INFINITY ? INFINITY : x[i]);
+            }
+        }
+        for (int d = 16; d > 0; d >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
+        }
+        if (lane == 0) {
+            sh.warp_f[0][warp] = top;
+            sh.warp_f[1][warp] = low;
+        }
+        for (int i = tid; i < kBins; i += kWarpThreads) sh.hist.count[i] = sh.hist.mass[i] = 0;
+        bad = __syncthreads_or(bad);
+        if (warp == 0) {
+            top = lane < kWarpWarps ? sh.warp_f[0][lane] : -INFINITY;
+            low = lane < kWarpWarps ? sh.warp_f[1][lane] : INFINITY;
+            for (int d = 16; d > 0; d >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
+            }
+            if (lane == 0) {
+                sh.top = top;
+                sh.low = low;
+                if (bad) sh.bad = 1;
+            }
+        }
+    }
+    cluster.sync();
+    float m = -INFINITY, low = INFINITY;
+    int bad = 0;
+    if (lane < C) {
+        const WarpShared *o = cluster.map_shared_rank(&sh, lane);
+        m = o->top;
+        low = o->low;
+        bad = o->bad;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
+    }
+    bad = __any_sync(0xffffffffu, bad) || !(temp > 0.f && temp < INFINITY);
+    float *out = A.probs ? A.probs + r * A.ps + base : nullptr;
     if (bad || m == -INFINITY) {
-        if (tid == 0) {
+        if (rank == 0 && tid == 0) {
             atomicOr(A.status, bad ? SV_STATUS_BAD_VALUE : SV_STATUS_ZERO_MASS);
             if (A.token) A.token[r] = -1;
         }
-        if (A.probs)
-            for (int64_t v = tid; v < V; v += kWarpThreads) A.probs[r * A.ps + v] = 0.f;
+        if (out)
+            for (int e = tid; e < n; e += kWarpThreads) out[e] = 0.f;
+        cluster.sync();
         return;
     }
-    const RowScale S = row_scale(m, temp);
-
-    auto count_from = [&](uint64_t thr) -> int64_t {  // elements at or above thr
-        int64_t c = 0;
-        for (int64_t v = tid; v < V; v += kWarpThreads) c += composite(at(v), v) >= thr;
-        return block_sum<int64_t>(c, reinterpret_cast<int64_t *>(smk));
-    };
-    auto mass_from = [&](uint64_t thr) -> double {  // their mass
-        Mass a;
-        for (int64_t v = tid; v < V; v += kWarpThreads) {
-            const float x = at(v);
-            if (composite(x, v) >= thr) a.add(weight(x, S, tab));
-        }
-        return block_sum<double>(a.value(), sm);
-    };
-
-    uint64_t thr = 0;  // kept: composite >= thr
-    const int64_t k = A.top_k ? A.top_k[r] : 0;
-    if (k > 0 && k < V) {
-        uint64_t lo = 0, hi = top;  // count(lo) >= k; the largest such threshold
-        while (lo < hi) {
-            const uint64_t mid = lo + (hi - lo) / 2 + 1;
-            if (count_from(mid) >= k) lo = mid;
-            else hi = mid - 1;
-        }
-        thr = lo;
-    }
-    const float p = A.top_p ? A.top_p[r] : 1.f;
-    if (p < 1.f) {
-        const double goal = (double)p * mass_from(thr);
-        // the smallest threshold whose successors (strictly before it) weigh less than the goal
-        uint64_t lo = thr, hi = top;
-        while (lo < hi) {
-            const uint64_t mid = lo + (hi - lo) / 2;
-            if (mass_from(mid + 1) < goal) hi = mid;
-            else lo = mid + 1;
-        }
-        thr = lo;
-    }
-    const float mp = A.min_p ? A.min_p[r] : 0.f;
+    const RowScale S = {m, sh.ch, sh.cl};
+    const bool by_k = k > 0 && k < A.V, by_p = p < 1.f;
+    float zmin = -INFINITY;  // min-p's lowest logit
     if (mp > 0.f) {
-        uint64_t t = top;
+        zmin = m;
         if (mp <= 1.f) {
-            const double edge = (double)m + (double)temp * log((double)mp);
-            float f = (float)edge;
-            if ((double)f < edge) f = nextafterf(f, INFINITY);
-            t = (uint64_t)ordered(f) << 32;
+            // the smallest float at or above max + temperature * ln(min_p)
+            const dd2 edge = add_dd({m, 0.f}, sh.min_off);
+            zmin = fminf(edge.l > 0.f ? nextafterf(edge.h, INFINITY) : edge.h, m);
         }
-        t = t < top ? t : top;
+    }
+
+    // ---- slow paths: the row's first element, sums over composites ----------
+    auto first_of_row = [&]() -> uint64_t {
+        uint64_t first = 0;
+        for (int w = s0 + lane; w < s1; w += 32) {
+            float x[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (x[i] == m) {
+                    const uint64_t key = composite(x[i], index_of(w, i));
+                    first = key > first ? key : first;
+                }
+        }
+        for (int d = 16; d > 0; d >>= 1) {
+            const uint64_t o = __shfl_xor_sync(0xffffffffu, first, d);
+            first = o > first ? o : first;
+        }
+        cluster.sync();
+        if (lane == 0) sh.warp_key[warp] = first;
+        cluster.sync();
+        for (int c = 0; c < C; ++c)
+            for (int w = 0; w < kWarpWarps; ++w) {
+                const uint64_t o = cluster.map_shared_rank(&sh, c)->warp_key[w];
+                first = o > first ? o : first;
+            }
+        return first;
+    };
+    auto sum_from = [&](uint64_t from, bool masses) -> dd2 {  // of the elements at or above
+        Mass a;
+        for (int w = s0 + lane; w < s1; w += 32) {
+            float x[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (x[i] > -INFINITY && composite(x[i], index_of(w, i)) >= from)
+                    a.add(masses ? weight(x[i], S, sh.tab) : make_float2(1.f, 0.f));
+        }
+        const dd2 own = warp_sum_dd(a.value());
+        cluster.sync();  // the last sum has been read everywhere
+        if (lane == 0) sh.part_mass[warp] = own;
+        cluster.sync();
+        dd2 s = {0.f, 0.f};
+        for (int c = 0; c < C; ++c)
+            for (int w = 0; w < kWarpWarps; ++w)
+                s = add_dd(s, cluster.map_shared_rank(&sh, c)->part_mass[w]);
+        return s;
+    };
+
+    // ---- top-k and top-p: the border bins -------------------------------------
+    // t(x) = 2^23 + the element's bin: a monotone function of x, so that bins
+    // are runs of the row's order
+    const float span = fminf(m - low, kRangeOctaves / S.ch);
+    const float per = span > 1e-30f ? (float)(kBins - 1) / span : 0.f;   // bins per unit of z
+    auto t_of = [&](float x) -> float {
+        return fminf(fmaf(m - x, per, kMagic), kMagic + (float)(kBins - 1));
+    };
+    const float never = kMagic + (float)kBins;
+    // kept by top-k and top-p for sure: t < t_keep; to be settled: t_keep <= t
+    // <= t_last, and t == t_k, of which top-k keeps the k_left largest
+    float t_keep = never, t_last = 0.f, t_k = never;
+    int64_t k_left = 0;
+    uint64_t thr = 0;       // kept: composite >= thr
+    if (by_k || by_p) {
+        // masses relative to the bin's middle: the tangent of that short arc of
+        // the exponential, off by less than 1e-4
+        const float drop = per > 0.f ? S.ch / per : 0.f;                 // octaves per bin
+        const float unit = exp2f((float)min(22, 30 - (31 - __clz(A.slice + 16))));
+        const float slope = unit * 0.693147182f * drop;
+        for (int w = s0 + lane; w < s1; w += 32) {
+            float x[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (x[i] > -INFINITY) {
+                    const float t = t_of(x[i]);
+                    const int b = __float_as_int(t) & (kBins - 1);
+                    if (by_k) atomicAdd(&sh.hist.count[b], 1u);
+                    if (by_p) {
+                        const float f = fminf(fmaf(m - x[i], per, kMagic - t), 0.5f);
+                        atomicAdd(&sh.hist.mass[b],
+                                  __float_as_uint(fmaf(-slope, f, unit) + kMagic) & 0x7fffffu);
+                    }
+                }
+        }
+        cluster.sync();
+        // every rank adds the row's histogram up: thread t has bins 2t and 2t + 1
+        uint32_t cnt[2] = {0, 0};
+        float mass[2] = {0.f, 0.f};
+        {
+            uint2 hc[kWarpMaxCluster], hm[kWarpMaxCluster];
+#pragma unroll
+            for (int c = 0; c < kWarpMaxCluster; ++c) {
+                hc[c] = hm[c] = make_uint2(0, 0);
+                if (c < C) {
+                    const WarpShared *o = cluster.map_shared_rank(&sh, c);
+                    if (by_k) hc[c] = reinterpret_cast<const uint2 *>(o->hist.count)[tid];
+                    if (by_p) hm[c] = reinterpret_cast<const uint2 *>(o->hist.mass)[tid];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kWarpMaxCluster; ++c) {
+                cnt[0] += hc[c].x;
+                cnt[1] += hc[c].y;
+                mass[0] += (float)hm[c].x;
+                mass[1] += (float)hm[c].y;
+            }
+        }
+        mass[0] *= exp2f(-drop * (float)(2 * tid)) / unit;
+        mass[1] *= exp2f(-drop * (float)(2 * tid + 1)) / unit;
+        uint32_t ci = cnt[0] + cnt[1];
+        float mi = mass[0] + mass[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t oc = __shfl_up_sync(0xffffffffu, ci, d);
+            const float om = __shfl_up_sync(0xffffffffu, mi, d);
+            if (lane >= d) {
+                ci += oc;
+                mi += om;
+            }
+        }
+        if (lane == 31) {
+            sh.warp_u[warp] = ci;
+            sh.warp_f[0][warp] = mi;
+        }
+        if (tid == 0) {
+            sh.k_bin = sh.lo_bin = sh.hi_bin = kBins;
+            sh.k_before = 0;
+            sh.k_mass = 0.f;
+        }
+        __syncthreads();
+        uint32_t c_at = ci - cnt[0] - cnt[1], c_all = 0;
+        float m_at = mi - mass[0] - mass[1], m_all = 0.f;
+        for (int w = 0; w < kWarpWarps; ++w) {
+            if (w < warp) {
+                c_at += sh.warp_u[w];
+                m_at += sh.warp_f[0][w];
+            }
+            c_all += sh.warp_u[w];
+            m_all += sh.warp_f[0][w];
+        }
+        // (a row with no more than k finite logits has no border of top-k)
+        const bool k_cuts = by_k && (int64_t)c_all > k;
+        float slack = 0.f;  // of the mass that top-k leaves, its border bin's share
+        if (k_cuts) {
+            uint32_t before = c_at;
+            float mass_before = m_at;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if ((int64_t)before < k && k <= (int64_t)before + cnt[i]) {
+                    const float part = (float)(k - before) / (float)cnt[i];
+                    sh.k_bin = 2 * tid + i;
+                    sh.k_before = (int32_t)before;
+                    sh.k_mass = mass_before + mass[i] * part;
+                    sh.k_slack = mass[i] * part * 0.03f;
+                }
+                before += cnt[i];
+                mass_before += mass[i];
+            }
+            __syncthreads();
+            t_k = kMagic + (float)sh.k_bin;
+            k_left = k - sh.k_before;
+            t_keep = t_k;
+            m_all = sh.k_mass;
+            slack = sh.k_slack;
+        }
+        if (by_p) {
+            // bins lo..hi hold the first element before which at least the goal
+            // lies, whatever the approximate masses are off by
+            const float err = 4e-4f + 0.5f / unit, goal = p * m_all, rest = m_all - goal;
+            const float loose = slack + 4e-6f * m_all;
+            float through = m_at;
+            int lo = kBins, hi = kBins;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                through += mass[i];
+                const float after = m_all - through;
+                const int b = 2 * tid + i;
+                if (through * (1.f + err) >= goal * (1.f - err) - loose &&
+                    after * (1.f - err) <= rest * (1.f + err) + loose)
+                    lo = min(lo, b);
+                if (through * (1.f - err) >= goal * (1.f + err) + loose ||
+                    after * (1.f + err) <= rest * (1.f - err) - loose)
+                    hi = min(hi, b);
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_min_sync(0xffffffffu, hi);
+            if (lane == 0) {
+                atomicMin(&sh.lo_bin, lo);
+                atomicMin(&sh.hi_bin, hi);
+            }
+            __syncthreads();
+            const int edge = k_cuts ? sh.k_bin : kBins - 1;  // nothing below it is left
+            t_keep = kMagic + (float)min(sh.lo_bin, edge);
+            t_last = kMagic + (float)min(sh.hi_bin, edge);
+        }
+    }
+
+    // ---- masses of what stays, and the border's elements ----------------------
+    // above: before the border (for top-p's goal); within: the rest of what
+    // top-k leaves, its own border bin aside; kept: what stays for sure
+    Mass above, within, kept;
+    const float t_goal = by_p ? (t_k < never ? t_k : never) : 0.f;   // masses wanted below it
+    for (int w = s0 + lane; w < s1; w += 32) {
+        float x[E];
+        load(w, x);
+        const float x_top = largest(x), t_top = t_of(x_top);
+        if (!by_k && !by_p && x_top < zmin) continue;
+        if (t_top > fmaxf(fmaxf(t_goal, t_last), t_k < never ? t_k : 0.f) && t_top >= t_keep) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (x[i] > -INFINITY) {
+                const float t = t_of(x[i]);
+                const bool stays = t < t_keep;
+                if ((stays && x[i] >= zmin) || t < t_goal) {
+                    const float2 y = weight(x[i], S, sh.tab);
+                    if (by_p) {
+                        if (stays) above.add(y);
+                        else within.add(y);
+                    }
+                    if (stays && x[i] >= zmin) kept.add(y);
+                }
+                if ((t >= t_keep && t <= t_last) || t == t_k) {
+                    const uint32_t at = atomicAdd(&sh.count, 1u);
+                    if (at < kLocalList) sh.list[at] = composite(x[i], index_of(w, i));
+                }
+            }
+    }
+    {
+        const dd2 a = warp_sum_dd(kept.value());
+        const dd2 b = by_p ? warp_sum_dd(above.value()) : dd2{0.f, 0.f};
+        const dd2 c = by_p ? warp_sum_dd(within.value()) : dd2{0.f, 0.f};
+        if (lane == 0) {
+            sh.run_mass[warp] = a;
+            sh.part_mass[warp] = b;
+            sh.in_mass[warp] = c;
+        }
+    }
+    __syncthreads();
+    if (warp < 3) {
+        const dd2 *from = warp == 0 ? sh.run_mass : warp == 1 ? sh.part_mass : sh.in_mass;
+        const dd2 s = warp_sum_dd(lane < kWarpWarps ? from[lane] : dd2{0.f, 0.f});
+        if (lane == 0) {
+            sh.slice_mass[warp] = s;
+            if (warp == 0) sh.gathered = sh.count;
+        }
+    }
+    cluster.sync();
+    // every rank: the row's masses (in rank order) and border
+    dd2 rank_kept = {0.f, 0.f};  // lane c: of rank c
+    dd2 row_above = {0.f, 0.f}, row_within = {0.f, 0.f};
+    int got = 0;
+    bool full = false;
+    {
+        dd2 a = {0.f, 0.f}, b = a, c = a;
+        int have = 0;
+        if (lane < C) {
+            const WarpShared *o = cluster.map_shared_rank(&sh, lane);
+            a = o->slice_mass[0];
+            b = o->slice_mass[1];
+            c = o->slice_mass[2];
+            have = (int)o->gathered;
+        }
+        full = __any_sync(0xffffffffu, have > kLocalList);
+        int at = have;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, at, d);
+            if (lane >= d) at += o;
+        }
+        got = __shfl_sync(0xffffffffu, at, 31);
+        full |= got > kList;
+        rank_kept = a;
+        row_above = warp_sum_dd(b);
+        row_within = warp_sum_dd(c);
+        // (the histogram that `all` lies over has been read everywhere)
+        if (!full)
+            for (int s = warp; s < C; s += kWarpWarps) {
+                const int cnt = __shfl_sync(0xffffffffu, have, s);
+                const int to = __shfl_sync(0xffffffffu, at, s) - cnt;
+                const uint64_t *from = cluster.map_shared_rank(&sh, s)->list;
+                for (int i = lane; i < cnt; i += 32) sh.all[to + i] = from[i];
+            }
+    }
+    if (got > 0 || full) {
+        if (full) {
+            // too many to gather: bisect the composite over the whole row
+            if (t_k < never) {
+                uint64_t l = 0, h = first_of_row();
+                while (l < h) {
+                    const uint64_t mid = l + (h - l) / 2;
+                    // counts as pairs of floats: whole up to 2^47
+                    const dd2 s = sum_from(mid + 1, false);
+                    if ((double)s.h + (double)s.l >= (double)k) l = mid + 1;
+                    else h = mid;
+                }
+                thr = l;
+            }
+            if (by_p) {
+                const dd2 goal = mul_dd(sum_from(thr, true), {p > 0.f ? p : 0.f, 0.f});
+                uint64_t l = thr, h = first_of_row();
+                while (l < h) {
+                    const uint64_t mid = l + (h - l) / 2;
+                    if (less_dd(sum_from(mid + 1, true), goal)) h = mid;
+                    else l = mid + 1;
+                }
+                thr = l;
+            }
+        } else {
+            __syncthreads();
+            // rank them: an element goes to the number of larger ones
+            uint64_t key[kList / kWarpThreads];
+            int at_of[kList / kWarpThreads];
+#pragma unroll
+            for (int j = 0; j < kList / kWarpThreads; ++j) {
+                const int i = tid + j * kWarpThreads;
+                at_of[j] = 0;
+                if (i < got) {
+                    key[j] = sh.all[i];
+#pragma unroll 4
+                    for (int x = 0; x < got; ++x) at_of[j] += sh.all[x] > key[j];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kList / kWarpThreads; ++j)
+                if (tid + j * kWarpThreads < got) sh.all[at_of[j]] = key[j];
+            __syncthreads();
+            if (warp == 0) {
+                // the elements that top-k leaves: those above its border bin
+                // (first in the order) and k_left of it
+                int stay = got;
+                if (t_k < never) {
+                    int above_k = 0;
+                    for (int i = lane; i < got; i += 32)
+                        above_k += t_of(unordered((uint32_t)(sh.all[i] >> 32))) < t_k;
+                    for (int d = 16; d > 0; d >>= 1) above_k += __shfl_xor_sync(0xffffffffu, above_k, d);
+                    stay = above_k + (int)k_left;
+                    if (by_p) {
+                        Mass a;
+                        for (int i = above_k + lane; i < stay; i += 32)
+                            a.add(weight(unordered((uint32_t)(sh.all[i] >> 32)), S, sh.tab));
+                        row_within = add_dd(row_within, warp_sum_dd(a.value()));
+                    }
+                    if (t_last < t_k && by_p) stay = above_k;
+                }
+                int last = stay - 1;
+                if (by_p) {
+                    // the last element before which less than the goal lies
+                    const dd2 goal = mul_dd(add_dd(row_above, row_within), {p > 0.f ? p : 0.f, 0.f});
+                    dd2 at = row_above;
+                    last = -1;
+                    for (int i = 0; i < stay; i += 32) {
+                        dd2 y = {0.f, 0.f};
+                        if (i + lane < stay) {
+                            const float2 q = weight(unordered((uint32_t)(sh.all[i + lane] >> 32)), S, sh.tab);
+                            y = {q.x, q.y};
+                        }
+                        const dd2 inc = warp_scan_dd(y, lane);
+                        dd2 ex = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
+                        if (lane == 0) ex = {0.f, 0.f};
+                        const bool stays = i + lane < stay && less_dd(add_dd(at, ex), goal);
+                        const unsigned any = __ballot_sync(0xffffffffu, stays);
+                        if (any) last = i + 31 - __clz(any);
+                        at = add_dd(at, shfl_dd(inc, 31));
+                    }
+                }
+                if (lane == 0) {
+                    // none of the border's: everything above it, at least the row's first
+                    const bool first_too = last < 0 && t_keep <= kMagic;
+                    sh.threshold = last >= 0 ? sh.all[last] : first_too ? sh.all[0] : sh.all[0] + 1;
+                }
+            }
+            __syncthreads();
+            thr = sh.threshold;
+        }
+    }
+    // min-p's threshold: whole values, or the row's first element alone
+    if (mp > 0.f) {
+        const uint64_t t = mp > 1.f ? first_of_row() : (uint64_t)ordered(zmin) << 32;
         thr = t > thr ? t : thr;
     }
-
-    const double total = mass_from(thr);
-    if (A.token && A.u) {
-        const double goal = A.u[r] * total;
-        // each warp takes a run of the row: its mass, the run that crosses the
-        // goal, then that run again in steps of 32
-        const int64_t run = (V + kWarpWarps - 1) / kWarpWarps;
-        const int64_t v0 = min(V, run * warp), v1 = min(V, v0 + run);
+    if (full || mp > 1.f) {
+        // the sums above do not hold: once more, with the threshold at hand
         Mass a;
-        for (int64_t v = v0 + lane; v < v1; v += 32) {
-            const float x = at(v);
-            if (composite(x, v) >= thr) a.add(weight(x, S, tab));
+        for (int w = s0 + lane; w < s1; w += 32) {
+            float x[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (x[i] > -INFINITY && composite(x[i], index_of(w, i)) >= thr) a.add(weight(x[i], S, sh.tab));
         }
-        double w = a.value();
-        for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-        __syncthreads();
-        if (lane == 0) sm[warp] = w;
-        __syncthreads();
-        double before = 0;
-        int mine = -1;
-        for (int i = 0; i < kWarpWarps; ++i) {
-            if (sm[i] > 0) mine = i;
-            if (before + sm[i] > goal) break;
-            if (sm[i] > 0 && i + 1 < kWarpWarps) {
-                bool more = false;
-                for (int x = i + 1; x < kWarpWarps; ++x) more |= sm[x] > 0;
-                if (!more) break;
-            }
-            before += sm[i];
-        }
-        if (warp == mine) {
-            int64_t last = -1, hit = -1;
-            for (int64_t v = v0; v < v1 && hit < 0; v += 32) {
-                float2 x = make_float2(0.f, 0.f);
-                if (v + lane < v1) {
-                    const float y = at(v + lane);
-                    if (composite(y, v + lane) >= thr) x = weight(y, S, tab);
-                }
-                double inc = (double)x.x + (double)x.y;
-                const bool has = inc > 0;
-                for (int d = 1; d < 32; d <<= 1) {
-                    const double o = __shfl_up_sync(0xffffffffu, inc, d);
-                    if (lane >= d) inc += o;
-                }
-                const unsigned any = __ballot_sync(0xffffffffu, has);
-                const unsigned over = __ballot_sync(0xffffffffu, has && before + inc > goal);
-                if (any) last = v + 31 - __clz(any);
-                if (over) hit = v + __ffs(over) - 1;
-                before += __shfl_sync(0xffffffffu, inc, 31);
-            }
-            if (lane == 0) found = hit >= 0 ? hit : last;
-        }
-        __syncthreads();
-        if (tid == 0) A.token[r] = (int32_t)found;
+        const dd2 own = warp_sum_dd(a.value());
+        cluster.sync();
+        if (lane == 0) sh.run_mass[warp] = own;
+        cluster.sync();
+        rank_kept = {0.f, 0.f};
+        if (lane < C)
+            for (int w = 0; w < kWarpWarps; ++w)
+                rank_kept = add_dd(rank_kept, cluster.map_shared_rank(&sh, lane)->run_mass[w]);
+        got = 0;
     }
-    if (A.probs) {
-        const double inv = 1.0 / total;
-        const float ih = (float)inv;
-        for (int64_t v = tid; v < V; v += kWarpThreads) {
-            const float x = at(v);
-            float o = 0.f;
-            if (composite(x, v) >= thr) o = weight(x, S, tab).x * ih;
-            A.probs[r * A.ps + v] = o;
+    // the border elements that stay, into the runs and ranks they belong to;
+    // every rank adds them up alike, so that all agree on where the goal lies
+    if (got > 0) {
+        Mass mine, of[kWarpMaxCluster];
+        for (int i = lane; i < got; i += 32) {
+            const uint64_t key = sh.all[i];
+            if (key < thr) break;       // (in the row's order)
+            const float2 y = weight(unordered((uint32_t)(key >> 32)), S, sh.tab);
+            const int64_t v = (int64_t)(uint32_t)~(uint32_t)key;
+            const int c = (int)(v / A.slice), w = (int)((v - base + shift) / E);
+            if (c == rank && w >= s0 && w < s1) mine.add(y);
+            if (warp == 0)
+#pragma unroll
+                for (int x = 0; x < kWarpMaxCluster; ++x)
+                    if (x == c) of[x].add(y);
+        }
+        __syncwarp();
+        const dd2 d = warp_sum_dd(mine.value());
+        if (lane == 0) sh.run_mass[warp] = add_dd(sh.run_mass[warp], d);
+        if (warp == 0)
+#pragma unroll
+            for (int x = 0; x < kWarpMaxCluster; ++x) {
+                const dd2 s = warp_sum_dd(of[x].value());
+                if (lane == x) rank_kept = add_dd(rank_kept, s);
+            }
+    }
+    if (warp == 0 && lane < kWarpMaxCluster) sh.rank_mass[lane] = rank_kept;
+    __syncthreads();
+    const dd2 rank_own = lane < C ? sh.rank_mass[lane] : dd2{0.f, 0.f};
+    const dd2 rank_upto = warp_scan_dd(rank_own, lane);
+    const dd2 total = shfl_dd(rank_upto, 31);
+
+    // ---- the draw ---------------------------------------------------------------
+    // The first rank, run, part and element whose running mass passes the goal,
+    // or, where rounding lets none, the last with mass.
+    if (A.token) {
+        const double u = A.u[r];
+        const float uh = (float)u;
+        const dd2 goal = mul_dd(total, norm2(uh, (float)(u - (double)uh)));
+        const unsigned full_ranks = __ballot_sync(0xffffffffu, rank_own.h > 0.f);
+        const unsigned past_ranks = __ballot_sync(0xffffffffu, rank_own.h > 0.f && less_dd(goal, rank_upto));
+        const int holder = past_ranks ? __ffs(past_ranks) - 1 : 31 - __clz(full_ranks);
+        if (holder == rank) {
+            dd2 at = {0.f, 0.f};
+            if (rank > 0) at = shfl_dd(rank_upto, rank - 1);
+            const dd2 mass = lane < kWarpWarps ? sh.run_mass[lane] : dd2{0.f, 0.f};
+            const dd2 upto = add_dd(at, warp_scan_dd(mass, lane));
+            const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
+            const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, upto));
+            const int pick = over ? __ffs(over) - 1 : 31 - __clz(some);
+            if (pick > 0) at = shfl_dd(upto, pick - 1);
+            // the run once more: every warp a part of it, then its part's words
+            const int r0 = min(W, run * pick), r1 = min(W, r0 + run);
+            const int part = (run / 32 + kWarpWarps - 1) / kWarpWarps * 32;
+            const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
+            auto stays = [&](float x, int w, int i) -> bool {
+                return x >= zmin && composite(x, index_of(w, i)) >= thr && x > -INFINITY;
+            };
+            Mass a;
+            for (int w = p0 + lane; w < p1; w += 32) {
+                float x[E];
+                load(w, x);
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (stays(x[i], w, i)) a.add(weight(x[i], S, sh.tab));
+            }
+            const dd2 own = warp_sum_dd(a.value());
+            if (lane == 0) sh.part_mass[warp] = own;
+            __syncthreads();
+            if (warp == 0) {
+                const dd2 mass = lane < kWarpWarps ? sh.part_mass[lane] : dd2{0.f, 0.f};
+                const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
+                const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
+                const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
+                const int q = over ? __ffs(over) - 1 : 31 - __clz(some);
+                if (q > 0) at = shfl_dd(reach, q - 1);
+                const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part);
+                int64_t hit = -1, end = -1;
+                for (int w = q0; w < q1 && hit < 0; w += 32) {
+                    float x[E];
+                    float2 y[E];
+                    Mass sum;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) x[i] = -INFINITY;
+                    if (w + lane < q1) load(w + lane, x);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        y[i] = stays(x[i], w + lane, i) ? weight(x[i], S, sh.tab) : make_float2(0.f, 0.f);
+                        sum.add(y[i]);
+                    }
+                    const dd2 inc = warp_scan_dd(sum.value(), lane);
+                    const bool any = sum.h > 0.f;
+                    const unsigned filled = __ballot_sync(0xffffffffu, any);
+                    const unsigned past = __ballot_sync(0xffffffffu, any && less_dd(goal, add_dd(at, inc)));
+                    dd2 walk = at;
+                    {
+                        dd2 ex = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
+                        if (lane > 0) walk = add_dd(at, ex);
+                    }
+                    int here = -1, final_ = -1;
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        if (y[i].x > 0.f) {
+                            walk = add_dd(walk, {y[i].x, y[i].y});
+                            final_ = i;
+                            if (here < 0 && less_dd(goal, walk)) here = i;
+                        }
+                    if (here < 0) here = final_;
+                    if (filled) {
+                        const int l = 31 - __clz(filled);
+                        end = index_of(w + l, 0) + __shfl_sync(0xffffffffu, final_, l);
+                    }
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        hit = index_of(w + l, 0) + __shfl_sync(0xffffffffu, here, l);
+                    }
+                    at = add_dd(at, shfl_dd(inc, 31));
+                }
+                if (lane == 0) A.token[r] = (int32_t)(hit >= 0 ? hit : end);
+            }
         }
     }
+
+    // ---- the row ------------------------------------------------------------------
+    if (out) {
+        const float inv = 1.f / total.h;
+        const float kz = fmaxf(zmin, unordered((uint32_t)(thr >> 32)));
+        const bool all_stay = thr == 0;
+        const bool vec = ((reinterpret_cast<uintptr_t>(out) - (uintptr_t)shift * 4u) & 15u) == 0;
+        for (int w = s0 + lane; w < s1; w += 32) {
+            float x[E], y[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) y[i] = 0.f;
+            if (all_stay || largest(x) >= kz) {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (all_stay || (x[i] >= kz && composite(x[i], index_of(w, i)) >= thr))
+                        y[i] = fast_weight(x[i], S) * inv;
+            }
+            const int e0 = w * E - shift;
+            if (vec && e0 >= 0 && e0 + E <= n) {
+#pragma unroll
+                for (int i = 0; i < E; i += 4)
+                    *reinterpret_cast<float4 *>(out + e0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (e0 + i >= 0 && e0 + i < n) out[e0 + i] = y[i];
+            }
+        }
+    }
+    cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
 }  // namespace sv

@@ -2,11 +2,18 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "specverify.h"
 #include "sv_host.cuh"
 #include "sv_warp.cuh"
 
 namespace {
+
+constexpr int kSms = 152;
+// 16-byte words of a slice that shared memory holds beside WarpShared
+constexpr int kMaxWords = (227 * 1024 - (int)sizeof(sv::WarpShared)) / 16;
 
 using svhost::kAlign;
 using svhost::kOnDevice;
@@ -15,6 +22,50 @@ using svhost::place;
 bool on_device(const void *p) {
     const void *x = p;
     return place(x) == kOnDevice;  // true for null: optional arrays
+}
+
+template <class T>
+int launch(sv::WarpParams &A, cudaStream_t st) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ECUDA;
+    // Cluster: as many CTAs as keep a slice within 64 KB (three of them then
+    // share an SM and hide one another's barriers), and more while the whole
+    // batch has fewer CTAs than SMs, down to 2048 elements each.
+    const int64_t row = A.V * (int64_t)sizeof(T);
+    int c = 1;
+    while (c < sv::kWarpMaxCluster &&
+           ((row + c - 1) / c > 65536 || ((int64_t)A.R * c * 2 <= kSms && A.V / (2 * c) >= 2048)))
+        c *= 2;
+    A.slice = (int32_t)(((A.V + c - 1) / c + 15) / 16 * 16);
+    const int per_word = 16 / (int)sizeof(T);
+    A.cached = std::min(A.slice / per_word + 1, kMaxWords);
+    const size_t bytes = sizeof(sv::WarpShared) + (size_t)A.cached * 16;
+    static std::atomic<int> raised[64];
+    if (!raised[dev].load()) {
+        if (cudaFuncSetAttribute(sv::warp_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(sizeof(sv::WarpShared) + (size_t)kMaxWords * 16)) != cudaSuccess)
+            return SV_ECUDA;
+        raised[dev].store(1);
+    }
+    if ((int64_t)A.R * c > INT32_MAX) return SV_EINVAL;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(A.R * c));
+    cfg.blockDim = dim3(sv::kWarpThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, sv::warp_kernel<T>, A) != cudaSuccess) return SV_ECUDA;
+    svhost::g_last_grid = (int64_t)A.R * c;
+    svhost::g_last_kernels = 1;
+    return SV_OK;
 }
 
 }  // namespace
@@ -53,12 +104,8 @@ extern "C" int sv_warp_sample(const void *z, int64_t z_row_stride, int32_t z_dty
     A.R = R;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     switch (z_dtype) {
-        case SV_F32: sv::warp_kernel<float><<<R, sv::kWarpThreads, 0, st>>>(A); break;
-        case SV_BF16: sv::warp_kernel<__nv_bfloat16><<<R, sv::kWarpThreads, 0, st>>>(A); break;
-        default: sv::warp_kernel<__half><<<R, sv::kWarpThreads, 0, st>>>(A); break;
+        case SV_F32: return launch<float>(A, st);
+        case SV_BF16: return launch<__nv_bfloat16>(A, st);
+        default: return launch<__half>(A, st);
     }
-    if (cudaGetLastError() != cudaSuccess) return SV_ECUDA;
-    svhost::g_last_grid = R;
-    svhost::g_last_kernels = 1;
-    return SV_OK;
 }
