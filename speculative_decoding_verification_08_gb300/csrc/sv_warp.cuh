@@ -23,19 +23,22 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "sv_barrier.cuh"
 #include "sv_cache.cuh"
 
 namespace sv {
 
-constexpr int kWarpThreads = 512;
+constexpr int kWarpThreads = 256;
 constexpr int kWarpWarps = kWarpThreads / 32;
 constexpr int kWarpMaxCluster = 8;
-constexpr int kBins = 1024;
+constexpr int kBins = 1024;            // of a histogram of counts and masses; of one alone twice as many
 constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
 constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
 constexpr int kLocalList = 256;        // border elements one CTA may gather
 constexpr int kList = 1024;            // and the row
+constexpr int kShared = 512;           // of them, ranked by the whole cluster
 
 struct WarpParams {
     const void *z;
@@ -214,6 +217,8 @@ struct alignas(16) WarpShared {
     float ch, cl;                   // log2(e) / temperature
     dd2 min_off;                    // temperature * ln(min_p)
     uint32_t count, gathered;       // border elements
+    int32_t list_end[kWarpMaxCluster], full, pick;
+    float total;
     int32_t k_bin, lo_bin, hi_bin, k_before;
     float k_mass, k_slack;
     uint64_t threshold;
@@ -226,12 +231,24 @@ struct alignas(16) WarpShared {
     uint32_t warp_u[kWarpWarps];
     uint64_t list[kLocalList];
     union {
+        alignas(16) uint32_t hist[2 * kBins];  // counts or masses; or counts, then masses
+        uint64_t all[kList];        // the row's border elements, ranked
         struct {
-            uint32_t count[kBins], mass[kBins];
-        } hist;
-        uint64_t all[kList];        // the row's border elements
+            uint64_t raw[kShared], ranked[kShared];
+        } share;
     };
 };
+
+static_assert(sizeof(WarpShared) % 16 == 0 && offsetof(WarpShared, hist) % 16 == 0,
+              "16-byte accesses to the histogram and to the words behind this");
+
+// The cluster's barrier in two parts.
+__device__ __forceinline__ void cluster_arrive_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_all() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <class T>
 struct WordOf {
@@ -273,7 +290,9 @@ __device__ __forceinline__ __half minus_inf() {
     return __ushort_as_half(0xfc00u);
 }
 
-template <class T>
+// kHeld: every slice fits in shared memory, in words padded with -inf to whole
+// rounds of the block, so that the sweeps need no bounds.
+template <class T, bool kHeld>
 __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_constant__ WarpParams A) {
     constexpr int E = WordOf<T>::kElems;
     extern __shared__ __align__(16) char raw[];
@@ -289,7 +308,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // word w holds elements w * E - shift ..; what lies outside is -inf
     const int shift = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
     const int W = n > 0 ? (n + shift + E - 1) / E : 0;
-    const int held = min(W, A.cached);
+    const int held = kHeld ? W : min(W, A.cached);
 
     // ---- the slice into shared memory ------------------------------------
     if (tid == 0) {
@@ -319,6 +338,12 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             reinterpret_cast<T *>(words)[w * E + tid % E] = e >= 0 && e < n ? z[e] : minus_inf<T>();
         }
     }
+    // every warp takes a run of words, its lanes in turn
+    const int run = (W + kWarpThreads - 1) / kWarpThreads * 32;
+    if (kHeld)
+        for (int w = W + tid; w < run * kWarpWarps; w += kWarpThreads)
+#pragma unroll
+            for (int i = 0; i < E; ++i) reinterpret_cast<T *>(words)[w * E + i] = minus_inf<T>();
     // the row's settings; what of them needs fp64 is one thread's work while
     // the copy runs
     const float temp = A.temperature ? A.temperature[r] : 1.f;
@@ -340,11 +365,9 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         sh.bad = 1;
     }
 
-    // every warp takes a run of words, its lanes in turn
-    const int run = (W + kWarpWarps * 32 - 1) / (kWarpWarps * 32) * 32;
-    const int s0 = min(W, run * warp), s1 = min(W, s0 + run);
+    const int s0 = kHeld ? run * warp : min(W, run * warp), s1 = kHeld ? s0 + run : min(W, s0 + run);
     auto load = [&](int w, float (&x)[E]) {
-        if (w < held) {
+        if (kHeld || w < held) {
             unpack<T>(words[w], x);
         } else {
 #pragma unroll
@@ -366,6 +389,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     {
         float top = -INFINITY, low = INFINITY;
         bool bad = false;
+#pragma unroll 4
         for (int w = s0 + lane; w < s1; w += 32) {
             float x[E];
             load(w, x);
@@ -384,7 +408,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             sh.warp_f[0][warp] = top;
             sh.warp_f[1][warp] = low;
         }
-        for (int i = tid; i < kBins; i += kWarpThreads) sh.hist.count[i] = sh.hist.mass[i] = 0;
+        for (int i = tid; i < 2 * kBins; i += kWarpThreads) sh.hist[i] = 0;
         bad = __syncthreads_or(bad);
         if (warp == 0) {
             top = lane < kWarpWarps ? sh.warp_f[0][lane] : -INFINITY;
@@ -489,66 +513,109 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // ---- top-k and top-p: the border bins -------------------------------------
     // t(x) = 2^23 + the element's bin: a monotone function of x, so that bins
     // are runs of the row's order
+    const bool both = by_k && by_p;
+    const int bins = both ? kBins : 2 * kBins;
     const float span = fminf(m - low, kRangeOctaves / S.ch);
-    const float per = span > 1e-30f ? (float)(kBins - 1) / span : 0.f;   // bins per unit of z
+    const float per = span > 1e-30f ? (float)(bins - 1) / span : 0.f;    // bins per unit of z
     auto t_of = [&](float x) -> float {
-        return fminf(fmaf(m - x, per, kMagic), kMagic + (float)(kBins - 1));
+        return fminf(fmaf(m - x, per, kMagic), kMagic + (float)(bins - 1));
     };
-    const float never = kMagic + (float)kBins;
+    const float never = kMagic + (float)bins;
     // kept by top-k and top-p for sure: t < t_keep; to be settled: t_keep <= t
     // <= t_last, and t == t_k, of which top-k keeps the k_left largest
     float t_keep = never, t_last = 0.f, t_k = never;
     int64_t k_left = 0;
     uint64_t thr = 0;       // kept: composite >= thr
     if (by_k || by_p) {
-        // masses relative to the bin's middle: the tangent of that short arc of
-        // the exponential, off by less than 1e-4
+        // masses relative to the bin's middle, in fixed point: that short arc of
+        // the exponential (at most +-0.02 octaves) to its square term
         const float drop = per > 0.f ? S.ch / per : 0.f;                 // octaves per bin
         const float unit = exp2f((float)min(22, 30 - (31 - __clz(A.slice + 16))));
-        const float slope = unit * 0.693147182f * drop;
-        for (int w = s0 + lane; w < s1; w += 32) {
-            float x[E];
-            load(w, x);
+        const float c1 = -unit * 0.693147182f * drop, c2 = unit * 0.240226507f * drop * drop;
+        uint32_t *masses = sh.hist + (both ? kBins : 0);
+        auto count_up = [&](auto want_k, auto want_p) {
+#pragma unroll 2
+            for (int w = s0 + lane; w < s1; w += 32) {
+                float x[E];
+                load(w, x);
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (x[i] > -INFINITY) {
-                    const float t = t_of(x[i]);
-                    const int b = __float_as_int(t) & (kBins - 1);
-                    if (by_k) atomicAdd(&sh.hist.count[b], 1u);
-                    if (by_p) {
-                        const float f = fminf(fmaf(m - x[i], per, kMagic - t), 0.5f);
-                        atomicAdd(&sh.hist.mass[b],
-                                  __float_as_uint(fmaf(-slope, f, unit) + kMagic) & 0x7fffffu);
+                for (int i = 0; i < E; ++i) {
+                    const float d = m - x[i], t = fminf(fmaf(d, per, kMagic), never - 1.f);
+                    const int b = __float_as_int(t) & (2 * kBins - 1);
+                    const bool real = x[i] > -INFINITY;
+                    if (decltype(want_k)::value) atomicAdd(&sh.hist[b], real ? 1u : 0u);
+                    if (decltype(want_p)::value) {
+                        const float f = fminf(fmaf(d, per, kMagic - t), 0.5f);
+                        const float y = fmaf(f, fmaf(f, c2, c1), unit + kMagic);
+                        atomicAdd(&masses[b], real ? __float_as_uint(y) & 0x7fffffu : 0u);
                     }
                 }
-        }
+            }
+        };
+        const std::true_type yes{};
+        const std::false_type no{};
+        if (both) count_up(yes, yes);
+        else if (by_k) count_up(yes, no);
+        else count_up(no, yes);
         cluster.sync();
-        // every rank adds the row's histogram up: thread t has bins 2t and 2t + 1
-        uint32_t cnt[2] = {0, 0};
-        float mass[2] = {0.f, 0.f};
-        {
-            uint2 hc[kWarpMaxCluster], hm[kWarpMaxCluster];
+        // every rank adds the row's histogram up: thread t has kMine bins from
+        // kMine t on (with both kinds, half of the threads have none)
+        constexpr int kMine = 2 * kBins / kWarpThreads;
+        uint32_t cnt[kMine];
+        float mass[kMine];
 #pragma unroll
-            for (int c = 0; c < kWarpMaxCluster; ++c) {
-                hc[c] = hm[c] = make_uint2(0, 0);
-                if (c < C) {
-                    const WarpShared *o = cluster.map_shared_rank(&sh, c);
-                    if (by_k) hc[c] = reinterpret_cast<const uint2 *>(o->hist.count)[tid];
-                    if (by_p) hm[c] = reinterpret_cast<const uint2 *>(o->hist.mass)[tid];
+        for (int i = 0; i < kMine; ++i) {
+            cnt[i] = 0;
+            mass[i] = 0.f;
+        }
+        if (kMine * tid < bins) {
+            auto gather = [&](int at, auto add) {  // eight ranks' loads in flight
+                uint4 y[kWarpMaxCluster];
+#pragma unroll
+                for (int c = 0; c < kWarpMaxCluster; ++c) {
+                    y[c] = make_uint4(0, 0, 0, 0);
+                    if (c < C)
+                        y[c] = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(sh.hist, c) + at);
                 }
-            }
 #pragma unroll
-            for (int c = 0; c < kWarpMaxCluster; ++c) {
-                cnt[0] += hc[c].x;
-                cnt[1] += hc[c].y;
-                mass[0] += (float)hm[c].x;
-                mass[1] += (float)hm[c].y;
+                for (int c = 0; c < kWarpMaxCluster; ++c) add(y[c]);
+            };
+#pragma unroll
+            for (int q = 0; q < kMine; q += 4) {
+                if (by_k)
+                    gather(kMine * tid + q, [&](uint4 y) {
+                        cnt[q] += y.x;
+                        cnt[q + 1] += y.y;
+                        cnt[q + 2] += y.z;
+                        cnt[q + 3] += y.w;
+                    });
+                if (by_p)
+                    gather((both ? kBins : 0) + kMine * tid + q, [&](uint4 y) {
+                        mass[q] += (float)y.x;
+                        mass[q + 1] += (float)y.y;
+                        mass[q + 2] += (float)y.z;
+                        mass[q + 3] += (float)y.w;
+                    });
             }
         }
-        mass[0] *= exp2f(-drop * (float)(2 * tid)) / unit;
-        mass[1] *= exp2f(-drop * (float)(2 * tid + 1)) / unit;
-        uint32_t ci = cnt[0] + cnt[1];
-        float mi = mass[0] + mass[1];
+        if (by_p) {
+            const float first = exp2f(-drop * (float)(kMine * tid)) / unit, next = exp2f(-drop);
+            float f = first;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                mass[i] *= f;
+                f *= next;
+            }
+        }
+        uint32_t ci = 0;
+        float mi = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            ci += cnt[i];
+            mi += mass[i];
+        }
+        const uint32_t c_mine = ci;
+        const float m_mine = mi;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t oc = __shfl_up_sync(0xffffffffu, ci, d);
@@ -563,13 +630,13 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             sh.warp_f[0][warp] = mi;
         }
         if (tid == 0) {
-            sh.k_bin = sh.lo_bin = sh.hi_bin = kBins;
+            sh.k_bin = sh.lo_bin = sh.hi_bin = bins;
             sh.k_before = 0;
             sh.k_mass = 0.f;
         }
         __syncthreads();
-        uint32_t c_at = ci - cnt[0] - cnt[1], c_all = 0;
-        float m_at = mi - mass[0] - mass[1], m_all = 0.f;
+        uint32_t c_at = ci - c_mine, c_all = 0;
+        float m_at = mi - m_mine, m_all = 0.f;
         for (int w = 0; w < kWarpWarps; ++w) {
             if (w < warp) {
                 c_at += sh.warp_u[w];
@@ -585,10 +652,10 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             uint32_t before = c_at;
             float mass_before = m_at;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < kMine; ++i) {
                 if ((int64_t)before < k && k <= (int64_t)before + cnt[i]) {
                     const float part = (float)(k - before) / (float)cnt[i];
-                    sh.k_bin = 2 * tid + i;
+                    sh.k_bin = kMine * tid + i;
                     sh.k_before = (int32_t)before;
                     sh.k_mass = mass_before + mass[i] * part;
                     sh.k_slack = mass[i] * part * 0.03f;
@@ -606,15 +673,15 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         if (by_p) {
             // bins lo..hi hold the first element before which at least the goal
             // lies, whatever the approximate masses are off by
-            const float err = 4e-4f + 0.5f / unit, goal = p * m_all, rest = m_all - goal;
+            const float err = 2e-5f + 0.5f / unit, goal = p * m_all, rest = m_all - goal;
             const float loose = slack + 4e-6f * m_all;
             float through = m_at;
-            int lo = kBins, hi = kBins;
+            int lo = bins, hi = bins;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < kMine; ++i) {
                 through += mass[i];
                 const float after = m_all - through;
-                const int b = 2 * tid + i;
+                const int b = kMine * tid + i;
                 if (through * (1.f + err) >= goal * (1.f - err) - loose &&
                     after * (1.f - err) <= rest * (1.f + err) + loose)
                     lo = min(lo, b);
@@ -629,7 +696,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 atomicMin(&sh.hi_bin, hi);
             }
             __syncthreads();
-            const int edge = k_cuts ? sh.k_bin : kBins - 1;  // nothing below it is left
+            const int edge = k_cuts ? sh.k_bin : bins - 1;  // nothing below it is left
             t_keep = kMagic + (float)min(sh.lo_bin, edge);
             t_last = kMagic + (float)min(sh.hi_bin, edge);
         }
@@ -640,6 +707,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // top-k leaves, its own border bin aside; kept: what stays for sure
     Mass above, within, kept;
     const float t_goal = by_p ? (t_k < never ? t_k : never) : 0.f;   // masses wanted below it
+#pragma unroll 2
     for (int w = s0 + lane; w < s1; w += 32) {
         float x[E];
         load(w, x);
@@ -686,11 +754,8 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     }
     cluster.sync();
     // every rank: the row's masses (in rank order) and border
-    dd2 rank_kept = {0.f, 0.f};  // lane c: of rank c
-    dd2 row_above = {0.f, 0.f}, row_within = {0.f, 0.f};
-    int got = 0;
-    bool full = false;
-    {
+    dd2 row_above = {0.f, 0.f}, row_within = {0.f, 0.f};   // (warp 0)
+    if (warp == 0) {
         dd2 a = {0.f, 0.f}, b = a, c = a;
         int have = 0;
         if (lane < C) {
@@ -700,27 +765,34 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             c = o->slice_mass[2];
             have = (int)o->gathered;
         }
-        full = __any_sync(0xffffffffu, have > kLocalList);
+        const bool over = __any_sync(0xffffffffu, have > kLocalList);
         int at = have;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+        for (int d = 1; d < kWarpMaxCluster; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, at, d);
             if (lane >= d) at += o;
         }
-        got = __shfl_sync(0xffffffffu, at, 31);
-        full |= got > kList;
-        rank_kept = a;
-        row_above = warp_sum_dd(b);
-        row_within = warp_sum_dd(c);
-        // (the histogram that `all` lies over has been read everywhere)
-        if (!full)
-            for (int s = warp; s < C; s += kWarpWarps) {
-                const int cnt = __shfl_sync(0xffffffffu, have, s);
-                const int to = __shfl_sync(0xffffffffu, at, s) - cnt;
-                const uint64_t *from = cluster.map_shared_rank(&sh, s)->list;
-                for (int i = lane; i < cnt; i += 32) sh.all[to + i] = from[i];
-            }
+        if (by_p) {
+            row_above = warp_sum_dd(b);
+            row_within = warp_sum_dd(c);
+        }
+        if (lane < kWarpMaxCluster) {
+            sh.rank_mass[lane] = a;
+            sh.list_end[lane] = at;
+        }
+        if (lane == C - 1) sh.full = over || at > kList;
     }
+    __syncthreads();
+    int got = sh.list_end[C - 1];
+    const bool full = sh.full != 0;
+    // (the histogram that the lists lie over has been read everywhere)
+    if (!full)
+        for (int s = warp; s < C; s += kWarpWarps) {
+            const int to = s > 0 ? sh.list_end[s - 1] : 0, cnt = sh.list_end[s] - to;
+            const uint64_t *from = cluster.map_shared_rank(sh.list, s);
+            for (int i = lane; i < cnt; i += 32) sh.all[to + i] = from[i];
+        }
+    const uint64_t *border = sh.all;   // in the row's order
     if (got > 0 || full) {
         if (full) {
             // too many to gather: bisect the composite over the whole row
@@ -748,23 +820,51 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         } else {
             __syncthreads();
             // rank them: an element goes to the number of larger ones
-            uint64_t key[kList / kWarpThreads];
-            int at_of[kList / kWarpThreads];
-#pragma unroll
-            for (int j = 0; j < kList / kWarpThreads; ++j) {
-                const int i = tid + j * kWarpThreads;
-                at_of[j] = 0;
-                if (i < got) {
-                    key[j] = sh.all[i];
-#pragma unroll 4
-                    for (int x = 0; x < got; ++x) at_of[j] += sh.all[x] > key[j];
+            if (got <= 32) {
+                if (warp == 0) {
+                    const uint64_t key = lane < got ? sh.share.raw[lane] : 0;
+                    int at = 0;
+                    for (int x = 0; x < got; ++x) at += __shfl_sync(0xffffffffu, key, x) > key;
+                    if (lane < got) sh.share.ranked[at] = key;
                 }
-            }
-            __syncthreads();
+                __syncthreads();
+            } else if (got <= kShared) {
+                // every rank places a share of them, eight threads to an element,
+                // in every rank's list
+                const int part = lane % 8, total_groups = kWarpThreads / 8 * C;
+                for (int i0 = 0; i0 < got; i0 += total_groups) {
+                    const int i = i0 + (tid / 8) * C + rank;
+                    const uint64_t key = i < got ? sh.share.raw[i] : 0;
+                    int at = 0;
+                    if (i < got)
+                        for (int x = part; x < got; x += 8) at += sh.share.raw[x] > key;
+                    at += __shfl_xor_sync(0xffffffffu, at, 1);
+                    at += __shfl_xor_sync(0xffffffffu, at, 2);
+                    at += __shfl_xor_sync(0xffffffffu, at, 4);
+                    if (i < got && part < C)
+                        cluster.map_shared_rank(&sh, part)->share.ranked[at] = key;
+                }
+                cluster.sync();
+            } else {
+                uint64_t key[kList / kWarpThreads];
+                int at_of[kList / kWarpThreads];
 #pragma unroll
-            for (int j = 0; j < kList / kWarpThreads; ++j)
-                if (tid + j * kWarpThreads < got) sh.all[at_of[j]] = key[j];
-            __syncthreads();
+                for (int j = 0; j < kList / kWarpThreads; ++j) {
+                    const int i = tid + j * kWarpThreads;
+                    at_of[j] = 0;
+                    if (i < got) {
+                        key[j] = sh.all[i];
+#pragma unroll 4
+                        for (int x = 0; x < got; ++x) at_of[j] += sh.all[x] > key[j];
+                    }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kList / kWarpThreads; ++j)
+                    if (tid + j * kWarpThreads < got) sh.all[at_of[j]] = key[j];
+                __syncthreads();
+            }
+            border = got <= kShared ? sh.share.ranked : sh.all;
             if (warp == 0) {
                 // the elements that top-k leaves: those above its border bin
                 // (first in the order) and k_left of it
@@ -772,13 +872,13 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 if (t_k < never) {
                     int above_k = 0;
                     for (int i = lane; i < got; i += 32)
-                        above_k += t_of(unordered((uint32_t)(sh.all[i] >> 32))) < t_k;
+                        above_k += t_of(unordered((uint32_t)(border[i] >> 32))) < t_k;
                     for (int d = 16; d > 0; d >>= 1) above_k += __shfl_xor_sync(0xffffffffu, above_k, d);
                     stay = above_k + (int)k_left;
                     if (by_p) {
                         Mass a;
                         for (int i = above_k + lane; i < stay; i += 32)
-                            a.add(weight(unordered((uint32_t)(sh.all[i] >> 32)), S, sh.tab));
+                            a.add(weight(unordered((uint32_t)(border[i] >> 32)), S, sh.tab));
                         row_within = add_dd(row_within, warp_sum_dd(a.value()));
                     }
                     if (t_last < t_k && by_p) stay = above_k;
@@ -792,7 +892,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                     for (int i = 0; i < stay; i += 32) {
                         dd2 y = {0.f, 0.f};
                         if (i + lane < stay) {
-                            const float2 q = weight(unordered((uint32_t)(sh.all[i + lane] >> 32)), S, sh.tab);
+                            const float2 q = weight(unordered((uint32_t)(border[i + lane] >> 32)), S, sh.tab);
                             y = {q.x, q.y};
                         }
                         const dd2 inc = warp_scan_dd(y, lane);
@@ -807,7 +907,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 if (lane == 0) {
                     // none of the border's: everything above it, at least the row's first
                     const bool first_too = last < 0 && t_keep <= kMagic;
-                    sh.threshold = last >= 0 ? sh.all[last] : first_too ? sh.all[0] : sh.all[0] + 1;
+                    sh.threshold = last >= 0 ? border[last] : first_too ? border[0] : border[0] + 1;
                 }
             }
             __syncthreads();
@@ -833,141 +933,88 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         cluster.sync();
         if (lane == 0) sh.run_mass[warp] = own;
         cluster.sync();
-        rank_kept = {0.f, 0.f};
-        if (lane < C)
+        if (warp == 0 && lane < C) {
+            dd2 s = {0.f, 0.f};
             for (int w = 0; w < kWarpWarps; ++w)
-                rank_kept = add_dd(rank_kept, cluster.map_shared_rank(&sh, lane)->run_mass[w]);
+                s = add_dd(s, cluster.map_shared_rank(&sh, lane)->run_mass[w]);
+            sh.rank_mass[lane] = s;
+        }
         got = 0;
     }
+    cluster_arrive_all();  // the last access to another CTA's shared memory is made
     // the border elements that stay, into the runs and ranks they belong to;
     // every rank adds them up alike, so that all agree on where the goal lies
     if (got > 0) {
-        Mass mine, of[kWarpMaxCluster];
+        // their weights (over the unranked list, where it is done with)
+        float2 *weights = reinterpret_cast<float2 *>(sh.share.raw);
+        if (got <= kShared) {
+            for (int i = tid; i < got; i += kWarpThreads)
+                weights[i] = border[i] >= thr ? weight(unordered((uint32_t)(border[i] >> 32)), S, sh.tab)
+                                              : make_float2(0.f, 0.f);
+            __syncthreads();
+        }
+        // warp w adds up rank w's, and those of its own run
+        Mass mine, of_rank;
+        const uint32_t rank_base = (uint32_t)warp * (uint32_t)A.slice;
         for (int i = lane; i < got; i += 32) {
-            const uint64_t key = sh.all[i];
+            const uint64_t key = border[i];
             if (key < thr) break;       // (in the row's order)
-            const float2 y = weight(unordered((uint32_t)(key >> 32)), S, sh.tab);
-            const int64_t v = (int64_t)(uint32_t)~(uint32_t)key;
-            const int c = (int)(v / A.slice), w = (int)((v - base + shift) / E);
-            if (c == rank && w >= s0 && w < s1) mine.add(y);
-            if (warp == 0)
-#pragma unroll
-                for (int x = 0; x < kWarpMaxCluster; ++x)
-                    if (x == c) of[x].add(y);
+            const float2 y = got <= kShared ? weights[i]
+                                            : weight(unordered((uint32_t)(key >> 32)), S, sh.tab);
+            const uint32_t v = ~(uint32_t)key;
+            if (warp < C && v - rank_base < (uint32_t)A.slice) of_rank.add(y);
+            const uint32_t e = v - (uint32_t)base;
+            const int w = (int)((e + (uint32_t)shift) / (uint32_t)E);
+            if (e < (uint32_t)n && w >= s0 && w < s1) mine.add(y);
         }
         __syncwarp();
-        const dd2 d = warp_sum_dd(mine.value());
-        if (lane == 0) sh.run_mass[warp] = add_dd(sh.run_mass[warp], d);
-        if (warp == 0)
-#pragma unroll
-            for (int x = 0; x < kWarpMaxCluster; ++x) {
-                const dd2 s = warp_sum_dd(of[x].value());
-                if (lane == x) rank_kept = add_dd(rank_kept, s);
-            }
+        const dd2 a = warp_sum_dd(mine.value()), b = warp_sum_dd(of_rank.value());
+        if (lane == 0) {
+            sh.run_mass[warp] = add_dd(sh.run_mass[warp], a);
+            if (warp < C) sh.rank_mass[warp] = add_dd(sh.rank_mass[warp], b);
+        }
     }
-    if (warp == 0 && lane < kWarpMaxCluster) sh.rank_mass[lane] = rank_kept;
     __syncthreads();
-    const dd2 rank_own = lane < C ? sh.rank_mass[lane] : dd2{0.f, 0.f};
-    const dd2 rank_upto = warp_scan_dd(rank_own, lane);
-    const dd2 total = shfl_dd(rank_upto, 31);
 
-    // ---- the draw ---------------------------------------------------------------
+    // ---- the total and the draw -------------------------------------------------
     // The first rank, run, part and element whose running mass passes the goal,
     // or, where rounding lets none, the last with mass.
-    if (A.token) {
-        const double u = A.u[r];
-        const float uh = (float)u;
-        const dd2 goal = mul_dd(total, norm2(uh, (float)(u - (double)uh)));
-        const unsigned full_ranks = __ballot_sync(0xffffffffu, rank_own.h > 0.f);
-        const unsigned past_ranks = __ballot_sync(0xffffffffu, rank_own.h > 0.f && less_dd(goal, rank_upto));
-        const int holder = past_ranks ? __ffs(past_ranks) - 1 : 31 - __clz(full_ranks);
-        if (holder == rank) {
-            dd2 at = {0.f, 0.f};
-            if (rank > 0) at = shfl_dd(rank_upto, rank - 1);
-            const dd2 mass = lane < kWarpWarps ? sh.run_mass[lane] : dd2{0.f, 0.f};
-            const dd2 upto = add_dd(at, warp_scan_dd(mass, lane));
-            const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
-            const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, upto));
-            const int pick = over ? __ffs(over) - 1 : 31 - __clz(some);
-            if (pick > 0) at = shfl_dd(upto, pick - 1);
-            // the run once more: every warp a part of it, then its part's words
-            const int r0 = min(W, run * pick), r1 = min(W, r0 + run);
-            const int part = (run / 32 + kWarpWarps - 1) / kWarpWarps * 32;
-            const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
-            auto stays = [&](float x, int w, int i) -> bool {
-                return x >= zmin && composite(x, index_of(w, i)) >= thr && x > -INFINITY;
-            };
-            Mass a;
-            for (int w = p0 + lane; w < p1; w += 32) {
-                float x[E];
-                load(w, x);
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (stays(x[i], w, i)) a.add(weight(x[i], S, sh.tab));
-            }
-            const dd2 own = warp_sum_dd(a.value());
-            if (lane == 0) sh.part_mass[warp] = own;
-            __syncthreads();
-            if (warp == 0) {
-                const dd2 mass = lane < kWarpWarps ? sh.part_mass[lane] : dd2{0.f, 0.f};
+    dd2 goal = {0.f, 0.f}, at = {0.f, 0.f};   // (warp 0)
+    if (warp == 0) {
+        const dd2 own = lane < C ? sh.rank_mass[lane] : dd2{0.f, 0.f};
+        const dd2 upto = warp_scan_dd(own, lane);
+        const dd2 total = shfl_dd(upto, 31);
+        if (lane == 0) {
+            sh.total = total.h;
+            sh.pick = -1;
+        }
+        if (A.token) {
+            const double u = A.u[r];
+            const float uh = (float)u;
+            goal = mul_dd(total, norm2(uh, (float)(u - (double)uh)));
+            const unsigned some = __ballot_sync(0xffffffffu, own.h > 0.f);
+            const unsigned over = __ballot_sync(0xffffffffu, own.h > 0.f && less_dd(goal, upto));
+            const int holder = over ? __ffs(over) - 1 : 31 - __clz(some);
+            if (holder == rank) {
+                if (rank > 0) at = shfl_dd(upto, rank - 1);
+                const dd2 mass = lane < kWarpWarps ? sh.run_mass[lane] : dd2{0.f, 0.f};
                 const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
-                const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
-                const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
-                const int q = over ? __ffs(over) - 1 : 31 - __clz(some);
-                if (q > 0) at = shfl_dd(reach, q - 1);
-                const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part);
-                int64_t hit = -1, end = -1;
-                for (int w = q0; w < q1 && hit < 0; w += 32) {
-                    float x[E];
-                    float2 y[E];
-                    Mass sum;
-#pragma unroll
-                    for (int i = 0; i < E; ++i) x[i] = -INFINITY;
-                    if (w + lane < q1) load(w + lane, x);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        y[i] = stays(x[i], w + lane, i) ? weight(x[i], S, sh.tab) : make_float2(0.f, 0.f);
-                        sum.add(y[i]);
-                    }
-                    const dd2 inc = warp_scan_dd(sum.value(), lane);
-                    const bool any = sum.h > 0.f;
-                    const unsigned filled = __ballot_sync(0xffffffffu, any);
-                    const unsigned past = __ballot_sync(0xffffffffu, any && less_dd(goal, add_dd(at, inc)));
-                    dd2 walk = at;
-                    {
-                        dd2 ex = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
-                        if (lane > 0) walk = add_dd(at, ex);
-                    }
-                    int here = -1, final_ = -1;
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        if (y[i].x > 0.f) {
-                            walk = add_dd(walk, {y[i].x, y[i].y});
-                            final_ = i;
-                            if (here < 0 && less_dd(goal, walk)) here = i;
-                        }
-                    if (here < 0) here = final_;
-                    if (filled) {
-                        const int l = 31 - __clz(filled);
-                        end = index_of(w + l, 0) + __shfl_sync(0xffffffffu, final_, l);
-                    }
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        hit = index_of(w + l, 0) + __shfl_sync(0xffffffffu, here, l);
-                    }
-                    at = add_dd(at, shfl_dd(inc, 31));
-                }
-                if (lane == 0) A.token[r] = (int32_t)(hit >= 0 ? hit : end);
+                const unsigned runs = __ballot_sync(0xffffffffu, mass.h > 0.f);
+                const unsigned past = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
+                const int pick = past ? __ffs(past) - 1 : 31 - __clz(runs);
+                if (pick > 0) at = shfl_dd(reach, pick - 1);
+                if (lane == 0) sh.pick = pick;
             }
         }
     }
-
+    __syncthreads();
     // ---- the row ------------------------------------------------------------------
     if (out) {
-        const float inv = 1.f / total.h;
+        const float inv = 1.f / sh.total;
         const float kz = fmaxf(zmin, unordered((uint32_t)(thr >> 32)));
         const bool all_stay = thr == 0;
         const bool vec = ((reinterpret_cast<uintptr_t>(out) - (uintptr_t)shift * 4u) & 15u) == 0;
+#pragma unroll 2
         for (int w = s0 + lane; w < s1; w += 32) {
             float x[E], y[E];
             load(w, x);
@@ -991,7 +1038,79 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             }
         }
     }
-    cluster.sync();  // no CTA leaves while another may read its shared memory
+    // ---- the drawn element, on the rank that holds it ---------------------------
+    if (sh.pick >= 0) {
+        // the run once more: every warp a part of it, then its part's words
+        const int r0 = min(W, run * sh.pick), r1 = min(W, r0 + run);
+        const int part = (run / 32 + kWarpWarps - 1) / kWarpWarps * 32;
+        const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
+        auto stays = [&](float x, int w, int i) -> bool {
+            return x > -INFINITY && composite(x, index_of(w, i)) >= thr;
+        };
+        Mass a;
+        for (int w = p0 + lane; w < p1; w += 32) {
+            float x[E];
+            load(w, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (stays(x[i], w, i)) a.add(weight(x[i], S, sh.tab));
+        }
+        const dd2 own = warp_sum_dd(a.value());
+        if (lane == 0) sh.part_mass[warp] = own;
+        __syncthreads();
+        if (warp == 0) {
+            const dd2 mass = lane < kWarpWarps ? sh.part_mass[lane] : dd2{0.f, 0.f};
+            const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
+            const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
+            const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
+            const int q = over ? __ffs(over) - 1 : 31 - __clz(some);
+            if (q > 0) at = shfl_dd(reach, q - 1);
+            const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part);
+            int64_t hit = -1, end = -1;
+            for (int w = q0; w < q1 && hit < 0; w += 32) {
+                float x[E];
+                float2 y[E];
+                Mass sum;
+#pragma unroll
+                for (int i = 0; i < E; ++i) x[i] = -INFINITY;
+                if (w + lane < q1) load(w + lane, x);
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    y[i] = stays(x[i], w + lane, i) ? weight(x[i], S, sh.tab) : make_float2(0.f, 0.f);
+                    sum.add(y[i]);
+                }
+                const dd2 inc = warp_scan_dd(sum.value(), lane);
+                const bool any = sum.h > 0.f;
+                const unsigned filled = __ballot_sync(0xffffffffu, any);
+                const unsigned past = __ballot_sync(0xffffffffu, any && less_dd(goal, add_dd(at, inc)));
+                dd2 walk = at;
+                {
+                    const dd2 ex = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
+                    if (lane > 0) walk = add_dd(at, ex);
+                }
+                int here = -1, final_ = -1;
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (y[i].x > 0.f) {
+                        walk = add_dd(walk, {y[i].x, y[i].y});
+                        final_ = i;
+                        if (here < 0 && less_dd(goal, walk)) here = i;
+                    }
+                if (here < 0) here = final_;
+                if (filled) {
+                    const int l = 31 - __clz(filled);
+                    end = index_of(w + l, 0) + __shfl_sync(0xffffffffu, final_, l);
+                }
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    hit = index_of(w + l, 0) + __shfl_sync(0xffffffffu, here, l);
+                }
+                at = add_dd(at, shfl_dd(inc, 31));
+            }
+            if (lane == 0) A.token[r] = (int32_t)(hit >= 0 ? hit : end);
+        }
+    }
+    cluster_wait_all();  // no CTA leaves while another may read its shared memory
 }
 
 }  // namespace sv

@@ -38,12 +38,20 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
         c *= 2;
     A.slice = (int32_t)(((A.V + c - 1) / c + 15) / 16 * 16);
     const int per_word = 16 / (int)sizeof(T);
-    A.cached = std::min(A.slice / per_word + 1, kMaxWords);
+    // words of a slice (one more where rows do not start on one), in whole rounds
+    // of the block
+    const int words = (int)(((int64_t)A.slice / per_word + 1 + sv::kWarpThreads - 1) /
+                            sv::kWarpThreads * sv::kWarpThreads);
+    const bool held = words <= kMaxWords;
+    A.cached = std::min(words, kMaxWords);
     const size_t bytes = sizeof(sv::WarpShared) + (size_t)A.cached * 16;
     static std::atomic<int> raised[64];
     if (!raised[dev].load()) {
-        if (cudaFuncSetAttribute(sv::warp_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(sizeof(sv::WarpShared) + (size_t)kMaxWords * 16)) != cudaSuccess)
+        const int most = (int)(sizeof(sv::WarpShared) + (size_t)kMaxWords * 16);
+        if (cudaFuncSetAttribute(sv::warp_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 most) != cudaSuccess ||
+            cudaFuncSetAttribute(sv::warp_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 most) != cudaSuccess)
             return SV_ECUDA;
         raised[dev].store(1);
     }
@@ -62,7 +70,9 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, sv::warp_kernel<T>, A) != cudaSuccess) return SV_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, held ? sv::warp_kernel<T, true> : sv::warp_kernel<T, false>, A) !=
+        cudaSuccess)
+        return SV_ECUDA;
     svhost::g_last_grid = (int64_t)A.R * c;
     svhost::g_last_kernels = 1;
     return SV_OK;
