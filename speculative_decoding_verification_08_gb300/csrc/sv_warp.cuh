@@ -36,7 +36,7 @@ constexpr int kWarpMaxCluster = 8;
 constexpr int kBins = 1024;            // of a histogram of counts and masses; of one alone twice as many
 constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
 constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
-constexpr int kLocalList = 256;        // border elements one CTA may gather
+constexpr int kLocalList = 192;        // border elements one CTA may gather
 constexpr int kList = 1024;            // and the row
 constexpr int kShared = 512;           // of them, ranked by the whole cluster
 
@@ -138,6 +138,10 @@ __device__ __forceinline__ float2 weight(float z, const RowScale &S, const ExpTa
     return make_float2(wh * scale, wl * scale);
 }
 
+__device__ __noinline__ float2 weight_of(float z, RowScale S, const ExpTable *tab) {
+    return weight(z, S, *tab);
+}
+
 // Sums of weights as pairs of floats (fp64 runs at 1/64 of the fp32 rate here):
 // relative errors near 2^-46.
 struct dd2 {
@@ -173,7 +177,8 @@ __device__ __forceinline__ dd2 warp_scan_dd(dd2 a, int lane) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const dd2 o = {__shfl_up_sync(0xffffffffu, a.h, d), __shfl_up_sync(0xffffffffu, a.l, d)};
-        if (lane >= d) a = add_dd(o, a);
+        const dd2 s = add_dd(o, a);
+        a = lane >= d ? s : a;
     }
     return a;
 }
@@ -208,6 +213,15 @@ __device__ __forceinline__ float fast_weight(float z, const RowScale &S) {
     return __int_as_float(__float_as_int(y) + ((int)n << 23));
 }
 
+// A CTA's slice of the row, for the slow paths.
+struct RowSlice {
+    const void *z;
+    const uint4 *words;
+    int64_t base;
+    int32_t n, shift, held;
+    RowScale S;
+};
+
 // What the CTAs of a cluster read of one another.
 struct alignas(16) WarpShared {
     unsigned long long bar;
@@ -219,10 +233,11 @@ struct alignas(16) WarpShared {
     uint32_t count, gathered;       // border elements
     int32_t list_end[kWarpMaxCluster], full, pick;
     float total;
+    double coarse[2][32];           // counts and masses of 32 groups of bins
     int32_t k_bin, lo_bin, hi_bin, k_before;
-    float k_mass, k_slack;
     uint64_t threshold;
-    dd2 slice_mass[3];              // kept, above, within
+    RowSlice slice;
+    dd2 slice_mass[3];              // kept, above, all below t_goal
     dd2 rank_mass[kWarpMaxCluster]; // what stays of every rank's slice
     dd2 run_mass[kWarpWarps];       // kept mass of each warp's run
     dd2 part_mass[kWarpWarps], in_mass[kWarpWarps];
@@ -239,15 +254,21 @@ struct alignas(16) WarpShared {
     };
 };
 
+static_assert(sizeof(WarpShared) <= 11264, "three CTAs of 64 KB slices to an SM");
 static_assert(sizeof(WarpShared) % 16 == 0 && offsetof(WarpShared, hist) % 16 == 0,
               "16-byte accesses to the histogram and to the words behind this");
 
-// The cluster's barrier in two parts.
+// A value that all lanes hold, marked as such: in branches that the compiler
+// takes for divergent, every shuffle costs hundreds of cycles.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ float uniform(float x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// The cluster's barrier in two parts, for a CTA's end: nothing is handed over.
 __device__ __forceinline__ void cluster_arrive_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait_all() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <class T>
@@ -290,6 +311,165 @@ __device__ __forceinline__ __half minus_inf() {
     return __ushort_as_half(0xfc00u);
 }
 
+__device__ __forceinline__ double scan_f64(double x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, x, d);
+        x += lane >= d ? o : 0.;
+    }
+    return x;
+}
+
+// One group of the row's bins, `per` (1 or 2) to a lane, added over the ranks
+// and summed up to and including each: masses when `inv_unit` is not zero, else
+// counts.  A warp's work; what it reads of the other CTAs is a few words each
+// (whole histograms took most of a row's time).
+__device__ __forceinline__ double2 scan_bins(WarpShared &sh, int C, int slot, int per, float octaves,
+                                          float drop, float inv_unit, int lane) {
+    cg::cluster_group cluster = cg::this_cluster();
+    uint32_t x[kWarpMaxCluster], y[kWarpMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kWarpMaxCluster; ++c) {
+        x[c] = y[c] = 0;
+        if (c < C) {
+            const uint32_t *h = cluster.map_shared_rank(sh.hist, c) + slot + lane * per;
+            x[c] = h[0];
+            if (per == 2) y[c] = h[1];
+        }
+    }
+    double a = 0, b = 0;
+#pragma unroll
+    for (int c = 0; c < kWarpMaxCluster; ++c) {
+        a += (double)x[c];
+        b += (double)y[c];
+    }
+    if (inv_unit != 0.f) {
+        a *= (double)(exp2f(-octaves - drop * (float)(lane * per)) * inv_unit);
+        b *= (double)(exp2f(-octaves - drop * (float)(lane * per + 1)) * inv_unit);
+    }
+    const double upto = scan_f64(a + b, lane);
+    return make_double2(upto - b, upto);
+}
+
+// ---- slow paths, rarely taken: out of line, an element at a time --------------
+
+template <class T>
+__device__ __forceinline__ float slice_elem(const RowSlice &c, int e) {
+    const int at = e + c.shift;
+    const T *src = at / (16 / (int)sizeof(T)) < c.held ? reinterpret_cast<const T *>(c.words) + at
+                                                       : static_cast<const T *>(c.z) + e;
+    return to_f32<T>(*src);
+}
+
+// The row's first element (largest logit, lowest index); by the whole cluster.
+template <class T>
+__device__ __noinline__ uint64_t first_of_row(WarpShared &sh) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const RowSlice &c = sh.slice;
+    uint64_t first = 0;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < c.n; e += kWarpThreads) {
+        const float x = slice_elem<T>(c, e);
+        if (x == c.S.m) {
+            const uint64_t key = composite(x, c.base + e);
+            first = key > first ? key : first;
+        }
+    }
+#pragma unroll 1
+    for (int d = 16; d > 0; d >>= 1) {
+        const uint64_t o = __shfl_xor_sync(0xffffffffu, first, d);
+        first = o > first ? o : first;
+    }
+    cluster.sync();
+    if (threadIdx.x % 32 == 0) sh.warp_key[threadIdx.x / 32] = first;
+    cluster.sync();
+#pragma unroll 1
+    for (int r = 0; r < (int)cluster.num_blocks(); ++r)
+#pragma unroll 1
+        for (int w = 0; w < kWarpWarps; ++w) {
+            const uint64_t o = cluster.map_shared_rank(&sh, r)->warp_key[w];
+            first = o > first ? o : first;
+        }
+    return first;
+}
+
+// Mass (or number) of the row's elements at or above a composite; by the whole
+// cluster.  run_mass keeps the parts of this CTA's warps (masses, by runs).
+template <class T>
+__device__ __noinline__ dd2 sum_from(WarpShared &sh, uint64_t from, bool masses) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const RowSlice &c = sh.slice;
+    Mass a;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < c.n; e += kWarpThreads) {
+        const float x = slice_elem<T>(c, e);
+        if (x > -INFINITY && composite(x, c.base + e) >= from)
+            a.add(masses ? weight_of(x, c.S, &sh.tab) : make_float2(1.f, 0.f));
+    }
+    __syncwarp();
+    const dd2 own = warp_sum_dd(a.value());
+    cluster.sync();  // the last sum has been read everywhere
+    if (threadIdx.x % 32 == 0) sh.part_mass[threadIdx.x / 32] = own;
+    cluster.sync();
+    dd2 s = {0.f, 0.f};
+#pragma unroll 1
+    for (int r = 0; r < (int)cluster.num_blocks(); ++r)
+#pragma unroll 1
+        for (int w = 0; w < kWarpWarps; ++w)
+            s = add_dd(s, cluster.map_shared_rank(&sh, r)->part_mass[w]);
+    return s;
+}
+
+// The threshold that top-k (k > 0) and then top-p (p < 1) leave, by bisection of
+// the composite over the whole row: for borders with too many elements to
+// gather.
+template <class T>
+__device__ __noinline__ uint64_t bisect_row(WarpShared &sh, int64_t k, float p) {
+    uint64_t thr = 0;
+    const uint64_t top = first_of_row<T>(sh);
+#pragma unroll 1
+    for (int by = 0; by < 2; ++by) {   // top-k, top-p
+        if (by == 0 ? k <= 0 : !(p < 1.f)) continue;
+        dd2 goal = {0.f, 0.f};
+        if (by == 1) goal = mul_dd(sum_from<T>(sh, thr, true), {p > 0.f ? p : 0.f, 0.f});
+        uint64_t l = thr, h = top;
+#pragma unroll 1
+        while (l < h) {
+            const uint64_t mid = l + (h - l) / 2;
+            // (counts as pairs of floats are whole up to 2^47)
+            const dd2 s = sum_from<T>(sh, mid + 1, by == 1);
+            if (by == 0 ? (double)s.h + (double)s.l >= (double)k : !less_dd(s, goal)) l = mid + 1;
+            else h = mid;
+        }
+        thr = l;
+    }
+    return thr;
+}
+
+// Ranks the row's border in place, every CTA for itself: for lists too long for
+// the shared ranking.
+__device__ __noinline__ void rank_alone(WarpShared &sh, int got) {
+    uint64_t key[kList / kWarpThreads];
+    int at_of[kList / kWarpThreads];
+#pragma unroll
+    for (int j = 0; j < kList / kWarpThreads; ++j) {
+        const int i = (int)threadIdx.x + j * kWarpThreads;
+        key[j] = i < got ? sh.all[i] : 0;
+        at_of[j] = 0;
+    }
+#pragma unroll 1
+    for (int x = 0; x < got; ++x) {
+        const uint64_t o = sh.all[x];
+#pragma unroll
+        for (int j = 0; j < kList / kWarpThreads; ++j) at_of[j] += o > key[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kList / kWarpThreads; ++j)
+        if ((int)threadIdx.x + j * kWarpThreads < got) sh.all[at_of[j]] = key[j];
+    __syncthreads();
+}
+
 // kHeld: every slice fits in shared memory, in words padded with -inf to whole
 // rounds of the block, so that the sweeps need no bounds.
 template <class T, bool kHeld>
@@ -300,7 +480,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     uint4 *words = reinterpret_cast<uint4 *>(raw + sizeof(WarpShared));
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
     const int64_t r = blockIdx.x / C;
     const int64_t base = min(A.V, (int64_t)rank * A.slice);  // this CTA's elements
     const int n = (int)(min(A.V, base + A.slice) - base);
@@ -326,6 +506,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     if (tid == 0) {
         mbar_arrive_expect_tx(&sh.bar, (uint32_t)whole * 16u);
         const char *src = reinterpret_cast<const char *>(z - shift) + w0 * 16;
+#pragma unroll 1
         for (int at = 0; at < whole; at += 1024) {
             const int part = min(1024, whole - at);
             bulk_copy_g2s(words + w0 + at, src + (int64_t)at * 16, (uint32_t)part * 16u, &sh.bar);
@@ -341,15 +522,16 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // every warp takes a run of words, its lanes in turn
     const int run = (W + kWarpThreads - 1) / kWarpThreads * 32;
     if (kHeld)
+#pragma unroll 1
         for (int w = W + tid; w < run * kWarpWarps; w += kWarpThreads)
 #pragma unroll
             for (int i = 0; i < E; ++i) reinterpret_cast<T *>(words)[w * E + i] = minus_inf<T>();
     // the row's settings; what of them needs fp64 is one thread's work while
     // the copy runs
-    const float temp = A.temperature ? A.temperature[r] : 1.f;
-    const int64_t k = A.top_k ? A.top_k[r] : 0;
-    const float p = A.top_p ? A.top_p[r] : 1.f;
-    const float mp = A.min_p ? A.min_p[r] : 0.f;
+    const float temp = uniform(A.temperature ? A.temperature[r] : 1.f);
+    const int64_t k = uniform(A.top_k ? A.top_k[r] : 0);
+    const float p = uniform(A.top_p ? A.top_p[r] : 1.f);
+    const float mp = uniform(A.min_p ? A.min_p[r] : 0.f);
     if (tid == 64) {
         const RowScale s = row_scale(0.f, temp);
         sh.ch = s.ch;
@@ -389,7 +571,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     {
         float top = -INFINITY, low = INFINITY;
         bool bad = false;
-#pragma unroll 4
+#pragma unroll 2
         for (int w = s0 + lane; w < s1; w += 32) {
             float x[E];
             load(w, x);
@@ -400,6 +582,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 low = fminf(low, x[i] == -INFINITY ? INFINITY : x[i]);
             }
         }
+#pragma unroll 1
         for (int d = 16; d > 0; d >>= 1) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
@@ -408,11 +591,13 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             sh.warp_f[0][warp] = top;
             sh.warp_f[1][warp] = low;
         }
+#pragma unroll 1
         for (int i = tid; i < 2 * kBins; i += kWarpThreads) sh.hist[i] = 0;
         bad = __syncthreads_or(bad);
         if (warp == 0) {
             top = lane < kWarpWarps ? sh.warp_f[0][lane] : -INFINITY;
             low = lane < kWarpWarps ? sh.warp_f[1][lane] : INFINITY;
+#pragma unroll 1
             for (int d = 16; d > 0; d >>= 1) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
@@ -438,7 +623,9 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
     }
-    bad = __any_sync(0xffffffffu, bad) || !(temp > 0.f && temp < INFINITY);
+    m = uniform(m);
+    low = uniform(low);
+    bad = uniform(__any_sync(0xffffffffu, bad)) || !(temp > 0.f && temp < INFINITY);
     float *out = A.probs ? A.probs + r * A.ps + base : nullptr;
     if (bad || m == -INFINITY) {
         if (rank == 0 && tid == 0) {
@@ -446,6 +633,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             if (A.token) A.token[r] = -1;
         }
         if (out)
+#pragma unroll 1
             for (int e = tid; e < n; e += kWarpThreads) out[e] = 0.f;
         cluster.sync();
         return;
@@ -462,54 +650,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
     }
 
-    // ---- slow paths: the row's first element, sums over composites ----------
-    auto first_of_row = [&]() -> uint64_t {
-        uint64_t first = 0;
-        for (int w = s0 + lane; w < s1; w += 32) {
-            float x[E];
-            load(w, x);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (x[i] == m) {
-                    const uint64_t key = composite(x[i], index_of(w, i));
-                    first = key > first ? key : first;
-                }
-        }
-        for (int d = 16; d > 0; d >>= 1) {
-            const uint64_t o = __shfl_xor_sync(0xffffffffu, first, d);
-            first = o > first ? o : first;
-        }
-        cluster.sync();
-        if (lane == 0) sh.warp_key[warp] = first;
-        cluster.sync();
-        for (int c = 0; c < C; ++c)
-            for (int w = 0; w < kWarpWarps; ++w) {
-                const uint64_t o = cluster.map_shared_rank(&sh, c)->warp_key[w];
-                first = o > first ? o : first;
-            }
-        return first;
-    };
-    auto sum_from = [&](uint64_t from, bool masses) -> dd2 {  // of the elements at or above
-        Mass a;
-        for (int w = s0 + lane; w < s1; w += 32) {
-            float x[E];
-            load(w, x);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (x[i] > -INFINITY && composite(x[i], index_of(w, i)) >= from)
-                    a.add(masses ? weight(x[i], S, sh.tab) : make_float2(1.f, 0.f));
-        }
-        const dd2 own = warp_sum_dd(a.value());
-        cluster.sync();  // the last sum has been read everywhere
-        if (lane == 0) sh.part_mass[warp] = own;
-        cluster.sync();
-        dd2 s = {0.f, 0.f};
-        for (int c = 0; c < C; ++c)
-            for (int w = 0; w < kWarpWarps; ++w)
-                s = add_dd(s, cluster.map_shared_rank(&sh, c)->part_mass[w]);
-        return s;
-    };
-
+    if (tid == 0) sh.slice = {z, words, base, n, shift, held, S};
     // ---- top-k and top-p: the border bins -------------------------------------
     // t(x) = 2^23 + the element's bin: a monotone function of x, so that bins
     // are runs of the row's order
@@ -534,7 +675,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         const float c1 = -unit * 0.693147182f * drop, c2 = unit * 0.240226507f * drop * drop;
         uint32_t *masses = sh.hist + (both ? kBins : 0);
         auto count_up = [&](auto want_k, auto want_p) {
-#pragma unroll 2
+#pragma unroll 1
             for (int w = s0 + lane; w < s1; w += 32) {
                 float x[E];
                 load(w, x);
@@ -557,194 +698,211 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         if (both) count_up(yes, yes);
         else if (by_k) count_up(yes, no);
         else count_up(no, yes);
-        cluster.sync();
-        // every rank adds the row's histogram up: thread t has kMine bins from
-        // kMine t on (with both kinds, half of the threads have none)
-        constexpr int kMine = 2 * kBins / kWarpThreads;
-        uint32_t cnt[kMine];
-        float mass[kMine];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            cnt[i] = 0;
-            mass[i] = 0.f;
+        __syncthreads();
+        // sums of 32 groups of bins, a warp to a group
+        const int group = bins / 32, per = group / 32;
+        const float inv_unit = 1.f / unit;
+#pragma unroll 1
+        for (int g = warp; g < 32; g += kWarpWarps) {
+            uint32_t c = 0;
+            float y = 0.f;
+#pragma unroll 1
+            for (int i = lane; i < group; i += 32) {
+                const int b = g * group + i;
+                if (by_k) c += sh.hist[b];
+                if (by_p) y += (float)masses[b] * (exp2f(-drop * (float)b) * inv_unit);
+            }
+            if (by_k) c = __reduce_add_sync(0xffffffffu, c);
+            if (by_p)
+#pragma unroll 1
+                for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+            if (lane == 0) {
+                sh.coarse[0][g] = (double)c;
+                sh.coarse[1][g] = (double)y;
+            }
         }
-        if (kMine * tid < bins) {
-            auto gather = [&](int at, auto add) {  // eight ranks' loads in flight
-                uint4 y[kWarpMaxCluster];
+        cluster.sync();
+        // every rank's first warp: the row's groups, then the bins of the ones
+        // that hold the borders
+        if (warp == 0) {
+            double count = 0, mass = 0;
+            {
+                double x[kWarpMaxCluster], y[kWarpMaxCluster];
 #pragma unroll
                 for (int c = 0; c < kWarpMaxCluster; ++c) {
-                    y[c] = make_uint4(0, 0, 0, 0);
-                    if (c < C)
-                        y[c] = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(sh.hist, c) + at);
+                    x[c] = y[c] = 0;
+                    if (c < C) {
+                        const WarpShared *o = cluster.map_shared_rank(&sh, c);
+                        x[c] = o->coarse[0][lane];
+                        y[c] = o->coarse[1][lane];
+                    }
                 }
 #pragma unroll
-                for (int c = 0; c < kWarpMaxCluster; ++c) add(y[c]);
-            };
-#pragma unroll
-            for (int q = 0; q < kMine; q += 4) {
-                if (by_k)
-                    gather(kMine * tid + q, [&](uint4 y) {
-                        cnt[q] += y.x;
-                        cnt[q + 1] += y.y;
-                        cnt[q + 2] += y.z;
-                        cnt[q + 3] += y.w;
-                    });
-                if (by_p)
-                    gather((both ? kBins : 0) + kMine * tid + q, [&](uint4 y) {
-                        mass[q] += (float)y.x;
-                        mass[q + 1] += (float)y.y;
-                        mass[q + 2] += (float)y.z;
-                        mass[q + 3] += (float)y.w;
-                    });
+                for (int c = 0; c < kWarpMaxCluster; ++c) {
+                    count += x[c];
+                    mass += y[c];
+                }
             }
-        }
-        if (by_p) {
-            const float first = exp2f(-drop * (float)(kMine * tid)) / unit, next = exp2f(-drop);
-            float f = first;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                mass[i] *= f;
-                f *= next;
+            int k_bin = bins, k_before = 0, lo = bins, hi = bins;
+            const double m_upto = by_p ? scan_f64(mass, lane) : 0.;
+            double m_all = __shfl_sync(0xffffffffu, m_upto, 31), slack = 0;
+            if (by_k) {
+                const double upto = scan_f64(count, lane);
+                const unsigned at = __ballot_sync(0xffffffffu, upto >= (double)k);
+                // (a row with no more than k finite logits has no border of top-k)
+                if (__shfl_sync(0xffffffffu, upto, 31) > (double)k) {
+                    const int g = __ffs(at) - 1;
+                    const double before = __shfl_sync(0xffffffffu, upto - count, g);
+                    double2 in = scan_bins(sh, C, g * group, per, 0.f, 0.f, 0.f, lane);
+                    in.x += before;
+                    in.y += before;
+                    const unsigned bin = __ballot_sync(0xffffffffu, in.y >= (double)k);
+                    const int l = __ffs(bin) - 1;
+                    const int second = __shfl_sync(0xffffffffu, (int)(per == 2 && !(in.x >= (double)k)), l);
+                    k_bin = g * group + l * per + second;
+                    // what lies before that bin, and in it
+                    const double down = __shfl_up_sync(0xffffffffu, in.y, 1);
+                    const double start = second ? in.x : lane > 0 ? down : before;
+                    const double end = per == 2 && !second ? in.x : in.y;
+                    k_before = (int)__shfl_sync(0xffffffffu, start, l);
+                    const double inside = __shfl_sync(0xffffffffu, end - start, l);
+                    if (by_p) {
+                        double2 y = scan_bins(sh, C, kBins + g * group, per, drop * (float)(g * group), drop,
+                                              inv_unit, lane);
+                        const double m_before = __shfl_sync(0xffffffffu, m_upto - mass, g);
+                        const double m_down = __shfl_up_sync(0xffffffffu, y.y, 1);
+                        const double ms = __shfl_sync(0xffffffffu, second ? y.x : lane > 0 ? m_down : 0., l);
+                        const double me = __shfl_sync(0xffffffffu, per == 2 && !second ? y.x : y.y, l);
+                        const double part = (me - ms) * ((double)(k - k_before) / inside);
+                        m_all = m_before + ms + part;
+                        slack = 0.03 * part;   // the bin's elements differ by less
+                    }
+                }
             }
-        }
-        uint32_t ci = 0;
-        float mi = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            ci += cnt[i];
-            mi += mass[i];
-        }
-        const uint32_t c_mine = ci;
-        const float m_mine = mi;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t oc = __shfl_up_sync(0xffffffffu, ci, d);
-            const float om = __shfl_up_sync(0xffffffffu, mi, d);
-            if (lane >= d) {
-                ci += oc;
-                mi += om;
+            if (by_p) {
+                // bins lo..hi hold the first element before which at least the goal
+                // lies, whatever the approximate masses are off by
+                const double err = 2e-5 + 0.5 * (double)inv_unit, goal = (double)p * m_all,
+                             rest = m_all - goal, loose = slack + 1e-6 * m_all;
+                auto low = [&](double through) -> bool {
+                    return through * (1 + err) >= goal * (1 - err) - loose &&
+                           (m_all - through) * (1 - err) <= rest * (1 + err) + loose;
+                };
+                auto high = [&](double through) -> bool {
+                    return through * (1 - err) >= goal * (1 + err) + loose ||
+                           (m_all - through) * (1 + err) <= rest * (1 - err) - loose;
+                };
+                const unsigned gl = __ballot_sync(0xffffffffu, low(m_upto));
+                const unsigned gh = __ballot_sync(0xffffffffu, high(m_upto));
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side) {
+                    const unsigned at = side == 0 ? gl : gh;
+                    if (at == 0) continue;
+                    const int g = __ffs(at) - 1;
+                    double2 y = scan_bins(sh, C, (both ? kBins : 0) + g * group, per,
+                                          drop * (float)(g * group), drop, inv_unit, lane);
+                    const double before = __shfl_sync(0xffffffffu, m_upto - mass, g);
+                    const bool in0 = side == 0 ? low(before + y.x) : high(before + y.x);
+                    const bool in1 = side == 0 ? low(before + y.y) : high(before + y.y);
+                    const unsigned bin = __ballot_sync(0xffffffffu, in1);
+                    const int l = bin ? __ffs(bin) - 1 : 31;   // (its end passed, to rounding)
+                    const int second = __shfl_sync(0xffffffffu, (int)(per == 2 && !in0), l);
+                    (side == 0 ? lo : hi) = g * group + l * per + second;
+                }
             }
-        }
-        if (lane == 31) {
-            sh.warp_u[warp] = ci;
-            sh.warp_f[0][warp] = mi;
-        }
-        if (tid == 0) {
-            sh.k_bin = sh.lo_bin = sh.hi_bin = bins;
-            sh.k_before = 0;
-            sh.k_mass = 0.f;
+            if (lane == 0) {
+                sh.k_bin = k_bin;
+                sh.k_before = k_before;
+                sh.lo_bin = lo;
+                sh.hi_bin = hi;
+            }
         }
         __syncthreads();
-        uint32_t c_at = ci - c_mine, c_all = 0;
-        float m_at = mi - m_mine, m_all = 0.f;
-        for (int w = 0; w < kWarpWarps; ++w) {
-            if (w < warp) {
-                c_at += sh.warp_u[w];
-                m_at += sh.warp_f[0][w];
-            }
-            c_all += sh.warp_u[w];
-            m_all += sh.warp_f[0][w];
-        }
-        // (a row with no more than k finite logits has no border of top-k)
-        const bool k_cuts = by_k && (int64_t)c_all > k;
-        float slack = 0.f;  // of the mass that top-k leaves, its border bin's share
-        if (k_cuts) {
-            uint32_t before = c_at;
-            float mass_before = m_at;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                if ((int64_t)before < k && k <= (int64_t)before + cnt[i]) {
-                    const float part = (float)(k - before) / (float)cnt[i];
-                    sh.k_bin = kMine * tid + i;
-                    sh.k_before = (int32_t)before;
-                    sh.k_mass = mass_before + mass[i] * part;
-                    sh.k_slack = mass[i] * part * 0.03f;
-                }
-                before += cnt[i];
-                mass_before += mass[i];
-            }
-            __syncthreads();
-            t_k = kMagic + (float)sh.k_bin;
+        const int k_bin = uniform(sh.k_bin);
+        if (k_bin < bins) {
+            t_k = kMagic + (float)k_bin;
             k_left = k - sh.k_before;
             t_keep = t_k;
-            m_all = sh.k_mass;
-            slack = sh.k_slack;
         }
         if (by_p) {
-            // bins lo..hi hold the first element before which at least the goal
-            // lies, whatever the approximate masses are off by
-            const float err = 2e-5f + 0.5f / unit, goal = p * m_all, rest = m_all - goal;
-            const float loose = slack + 4e-6f * m_all;
-            float through = m_at;
-            int lo = bins, hi = bins;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                through += mass[i];
-                const float after = m_all - through;
-                const int b = kMine * tid + i;
-                if (through * (1.f + err) >= goal * (1.f - err) - loose &&
-                    after * (1.f - err) <= rest * (1.f + err) + loose)
-                    lo = min(lo, b);
-                if (through * (1.f - err) >= goal * (1.f + err) + loose ||
-                    after * (1.f + err) <= rest * (1.f - err) - loose)
-                    hi = min(hi, b);
-            }
-            lo = __reduce_min_sync(0xffffffffu, lo);
-            hi = __reduce_min_sync(0xffffffffu, hi);
-            if (lane == 0) {
-                atomicMin(&sh.lo_bin, lo);
-                atomicMin(&sh.hi_bin, hi);
-            }
-            __syncthreads();
-            const int edge = k_cuts ? sh.k_bin : bins - 1;  // nothing below it is left
-            t_keep = kMagic + (float)min(sh.lo_bin, edge);
-            t_last = kMagic + (float)min(sh.hi_bin, edge);
+            const int edge = min(k_bin, bins - 1);    // nothing below it is left
+            t_keep = kMagic + (float)min(uniform(sh.lo_bin), edge);
+            t_last = kMagic + (float)min(uniform(sh.hi_bin), edge);
         }
     }
 
     // ---- masses of what stays, and the border's elements ----------------------
-    // above: before the border (for top-p's goal); within: the rest of what
-    // top-k leaves, its own border bin aside; kept: what stays for sure
-    Mass above, within, kept;
-    const float t_goal = by_p ? (t_k < never ? t_k : never) : 0.f;   // masses wanted below it
-#pragma unroll 2
+    // above: before the border (for top-p's goal); in: all that top-k leaves, its
+    // own border bin aside; kept: what stays for sure
+    Mass above, in, kept;
+    const float t_goal = by_p ? t_k : 0.f;           // `in` wanted below it
+    const bool dense = by_p ? t_k >= never : t_keep >= never && zmin == -INFINITY;
+    const float t_far = fmaxf(fmaxf(t_goal, t_last), t_k < never ? t_k : 0.f);
+#pragma unroll 1
     for (int w = s0 + lane; w < s1; w += 32) {
         float x[E];
         load(w, x);
-        const float x_top = largest(x), t_top = t_of(x_top);
-        if (!by_k && !by_p && x_top < zmin) continue;
-        if (t_top > fmaxf(fmaxf(t_goal, t_last), t_k < never ? t_k : 0.f) && t_top >= t_keep) continue;
+        if (dense) {
+            // every element's weight, four chains at a time
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (x[i] > -INFINITY) {
-                const float t = t_of(x[i]);
-                const bool stays = t < t_keep;
-                if ((stays && x[i] >= zmin) || t < t_goal) {
-                    const float2 y = weight(x[i], S, sh.tab);
-                    if (by_p) {
-                        if (stays) above.add(y);
-                        else within.add(y);
+            for (int h = 0; h < E; h += 4) {
+                float2 y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = weight(x[h + i], S, sh.tab);
+                if (by_p) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        in.add(y[i]);
+                        const float t = t_of(x[h + i]);
+                        if (t < t_keep) {
+                            above.add(y[i]);
+                            if (mp > 0.f && x[h + i] >= zmin) kept.add(y[i]);
+                        } else if (t <= t_last && x[h + i] > -INFINITY) {
+                            const uint32_t at = atomicAdd(&sh.count, 1u);
+                            if (at < kLocalList) sh.list[at] = composite(x[h + i], index_of(w, h + i));
+                        }
                     }
-                    if (stays && x[i] >= zmin) kept.add(y);
-                }
-                if ((t >= t_keep && t <= t_last) || t == t_k) {
-                    const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < kLocalList) sh.list[at] = composite(x[i], index_of(w, i));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kept.add(y[i]);
                 }
             }
+            continue;
+        }
+        const float x_top = largest(x), t_top = t_of(x_top);
+        if (x_top == -INFINITY || (t_top > t_far && (t_top >= t_keep || x_top < zmin))) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float t = t_of(x[i]);
+            if (!(x[i] > -INFINITY) || (t > t_far && (t >= t_keep || x[i] < zmin))) continue;
+            const bool stays = t < t_keep;
+            if ((stays && x[i] >= zmin) || t < t_goal) {
+                const float2 y = weight_of(x[i], S, &sh.tab);
+                if (t < t_goal) in.add(y);
+                if (stays && by_p) above.add(y);
+                if (stays && x[i] >= zmin) kept.add(y);
+            }
+            if ((t >= t_keep && t <= t_last) || t == t_k) {
+                const uint32_t at = atomicAdd(&sh.count, 1u);
+                if (at < kLocalList) sh.list[at] = composite(x[i], index_of(w, i));
+            }
+        }
     }
+    __syncwarp();
     {
+        if (dense && by_p && !(mp > 0.f)) kept = above;
         const dd2 a = warp_sum_dd(kept.value());
-        const dd2 b = by_p ? warp_sum_dd(above.value()) : dd2{0.f, 0.f};
-        const dd2 c = by_p ? warp_sum_dd(within.value()) : dd2{0.f, 0.f};
-        if (lane == 0) {
-            sh.run_mass[warp] = a;
-            sh.part_mass[warp] = b;
-            sh.in_mass[warp] = c;
+        if (lane == 0) sh.run_mass[warp] = a;
+        if (by_p) {
+            const dd2 b = warp_sum_dd(above.value()), c = warp_sum_dd(in.value());
+            if (lane == 0) {
+                sh.part_mass[warp] = b;
+                sh.in_mass[warp] = c;
+            }
         }
     }
     __syncthreads();
-    if (warp < 3) {
+    if (warp < (by_p ? 3 : 1)) {
         const dd2 *from = warp == 0 ? sh.run_mass : warp == 1 ? sh.part_mass : sh.in_mass;
         const dd2 s = warp_sum_dd(lane < kWarpWarps ? from[lane] : dd2{0.f, 0.f});
         if (lane == 0) {
@@ -754,7 +912,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     }
     cluster.sync();
     // every rank: the row's masses (in rank order) and border
-    dd2 row_above = {0.f, 0.f}, row_within = {0.f, 0.f};   // (warp 0)
+    dd2 row_above = {0.f, 0.f}, row_in = {0.f, 0.f};   // (warp 0)
     if (warp == 0) {
         dd2 a = {0.f, 0.f}, b = a, c = a;
         int have = 0;
@@ -774,7 +932,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
         if (by_p) {
             row_above = warp_sum_dd(b);
-            row_within = warp_sum_dd(c);
+            row_in = warp_sum_dd(c);
         }
         if (lane < kWarpMaxCluster) {
             sh.rank_mass[lane] = a;
@@ -783,40 +941,21 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         if (lane == C - 1) sh.full = over || at > kList;
     }
     __syncthreads();
-    int got = sh.list_end[C - 1];
-    const bool full = sh.full != 0;
+    int got = uniform(sh.list_end[C - 1]);
+    const bool full = uniform(sh.full) != 0;
     // (the histogram that the lists lie over has been read everywhere)
     if (!full)
+#pragma unroll 1
         for (int s = warp; s < C; s += kWarpWarps) {
             const int to = s > 0 ? sh.list_end[s - 1] : 0, cnt = sh.list_end[s] - to;
             const uint64_t *from = cluster.map_shared_rank(sh.list, s);
+#pragma unroll 1
             for (int i = lane; i < cnt; i += 32) sh.all[to + i] = from[i];
         }
     const uint64_t *border = sh.all;   // in the row's order
     if (got > 0 || full) {
         if (full) {
-            // too many to gather: bisect the composite over the whole row
-            if (t_k < never) {
-                uint64_t l = 0, h = first_of_row();
-                while (l < h) {
-                    const uint64_t mid = l + (h - l) / 2;
-                    // counts as pairs of floats: whole up to 2^47
-                    const dd2 s = sum_from(mid + 1, false);
-                    if ((double)s.h + (double)s.l >= (double)k) l = mid + 1;
-                    else h = mid;
-                }
-                thr = l;
-            }
-            if (by_p) {
-                const dd2 goal = mul_dd(sum_from(thr, true), {p > 0.f ? p : 0.f, 0.f});
-                uint64_t l = thr, h = first_of_row();
-                while (l < h) {
-                    const uint64_t mid = l + (h - l) / 2;
-                    if (less_dd(sum_from(mid + 1, true), goal)) h = mid;
-                    else l = mid + 1;
-                }
-                thr = l;
-            }
+            thr = bisect_row<T>(sh, t_k < never ? k : 0, by_p ? p : 1.f);
         } else {
             __syncthreads();
             // rank them: an element goes to the number of larger ones
@@ -824,6 +963,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 if (warp == 0) {
                     const uint64_t key = lane < got ? sh.share.raw[lane] : 0;
                     int at = 0;
+#pragma unroll 1
                     for (int x = 0; x < got; ++x) at += __shfl_sync(0xffffffffu, key, x) > key;
                     if (lane < got) sh.share.ranked[at] = key;
                 }
@@ -832,11 +972,13 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 // every rank places a share of them, eight threads to an element,
                 // in every rank's list
                 const int part = lane % 8, total_groups = kWarpThreads / 8 * C;
+#pragma unroll 1
                 for (int i0 = 0; i0 < got; i0 += total_groups) {
                     const int i = i0 + (tid / 8) * C + rank;
                     const uint64_t key = i < got ? sh.share.raw[i] : 0;
                     int at = 0;
                     if (i < got)
+#pragma unroll 1
                         for (int x = part; x < got; x += 8) at += sh.share.raw[x] > key;
                     at += __shfl_xor_sync(0xffffffffu, at, 1);
                     at += __shfl_xor_sync(0xffffffffu, at, 2);
@@ -846,23 +988,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 }
                 cluster.sync();
             } else {
-                uint64_t key[kList / kWarpThreads];
-                int at_of[kList / kWarpThreads];
-#pragma unroll
-                for (int j = 0; j < kList / kWarpThreads; ++j) {
-                    const int i = tid + j * kWarpThreads;
-                    at_of[j] = 0;
-                    if (i < got) {
-                        key[j] = sh.all[i];
-#pragma unroll 4
-                        for (int x = 0; x < got; ++x) at_of[j] += sh.all[x] > key[j];
-                    }
-                }
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < kList / kWarpThreads; ++j)
-                    if (tid + j * kWarpThreads < got) sh.all[at_of[j]] = key[j];
-                __syncthreads();
+                rank_alone(sh, got);
             }
             border = got <= kShared ? sh.share.ranked : sh.all;
             if (warp == 0) {
@@ -871,28 +997,32 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 int stay = got;
                 if (t_k < never) {
                     int above_k = 0;
+#pragma unroll 1
                     for (int i = lane; i < got; i += 32)
                         above_k += t_of(unordered((uint32_t)(border[i] >> 32))) < t_k;
+#pragma unroll 1
                     for (int d = 16; d > 0; d >>= 1) above_k += __shfl_xor_sync(0xffffffffu, above_k, d);
                     stay = above_k + (int)k_left;
                     if (by_p) {
                         Mass a;
+#pragma unroll 1
                         for (int i = above_k + lane; i < stay; i += 32)
-                            a.add(weight(unordered((uint32_t)(border[i] >> 32)), S, sh.tab));
-                        row_within = add_dd(row_within, warp_sum_dd(a.value()));
+                            a.add(weight_of(unordered((uint32_t)(border[i] >> 32)), S, &sh.tab));
+                        row_in = add_dd(row_in, warp_sum_dd(a.value()));
                     }
                     if (t_last < t_k && by_p) stay = above_k;
                 }
                 int last = stay - 1;
                 if (by_p) {
                     // the last element before which less than the goal lies
-                    const dd2 goal = mul_dd(add_dd(row_above, row_within), {p > 0.f ? p : 0.f, 0.f});
+                    const dd2 goal = mul_dd(row_in, {p > 0.f ? p : 0.f, 0.f});
                     dd2 at = row_above;
                     last = -1;
+#pragma unroll 1
                     for (int i = 0; i < stay; i += 32) {
                         dd2 y = {0.f, 0.f};
                         if (i + lane < stay) {
-                            const float2 q = weight(unordered((uint32_t)(border[i + lane] >> 32)), S, sh.tab);
+                            const float2 q = weight_of(unordered((uint32_t)(border[i + lane] >> 32)), S, &sh.tab);
                             y = {q.x, q.y};
                         }
                         const dd2 inc = warp_scan_dd(y, lane);
@@ -916,25 +1046,26 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     }
     // min-p's threshold: whole values, or the row's first element alone
     if (mp > 0.f) {
-        const uint64_t t = mp > 1.f ? first_of_row() : (uint64_t)ordered(zmin) << 32;
+        const uint64_t t = mp > 1.f ? first_of_row<T>(sh) : (uint64_t)ordered(zmin) << 32;
         thr = t > thr ? t : thr;
     }
     if (full || mp > 1.f) {
         // the sums above do not hold: once more, with the threshold at hand
         Mass a;
-        for (int w = s0 + lane; w < s1; w += 32) {
-            float x[E];
-            load(w, x);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (x[i] > -INFINITY && composite(x[i], index_of(w, i)) >= thr) a.add(weight(x[i], S, sh.tab));
+#pragma unroll 1
+        for (int e = s0 * E - shift + lane; e < s1 * E - shift; e += 32) {
+            if (e < 0 || e >= n) continue;
+            const float x = slice_elem<T>(sh.slice, e);
+            if (x > -INFINITY && composite(x, base + e) >= thr) a.add(weight_of(x, S, &sh.tab));
         }
+        __syncwarp();
         const dd2 own = warp_sum_dd(a.value());
         cluster.sync();
         if (lane == 0) sh.run_mass[warp] = own;
         cluster.sync();
         if (warp == 0 && lane < C) {
             dd2 s = {0.f, 0.f};
+#pragma unroll 1
             for (int w = 0; w < kWarpWarps; ++w)
                 s = add_dd(s, cluster.map_shared_rank(&sh, lane)->run_mass[w]);
             sh.rank_mass[lane] = s;
@@ -948,19 +1079,21 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         // their weights (over the unranked list, where it is done with)
         float2 *weights = reinterpret_cast<float2 *>(sh.share.raw);
         if (got <= kShared) {
+#pragma unroll 1
             for (int i = tid; i < got; i += kWarpThreads)
-                weights[i] = border[i] >= thr ? weight(unordered((uint32_t)(border[i] >> 32)), S, sh.tab)
+                weights[i] = border[i] >= thr ? weight_of(unordered((uint32_t)(border[i] >> 32)), S, &sh.tab)
                                               : make_float2(0.f, 0.f);
             __syncthreads();
         }
         // warp w adds up rank w's, and those of its own run
         Mass mine, of_rank;
         const uint32_t rank_base = (uint32_t)warp * (uint32_t)A.slice;
+#pragma unroll 1
         for (int i = lane; i < got; i += 32) {
             const uint64_t key = border[i];
             if (key < thr) break;       // (in the row's order)
             const float2 y = got <= kShared ? weights[i]
-                                            : weight(unordered((uint32_t)(key >> 32)), S, sh.tab);
+                                            : weight_of(unordered((uint32_t)(key >> 32)), S, &sh.tab);
             const uint32_t v = ~(uint32_t)key;
             if (warp < C && v - rank_base < (uint32_t)A.slice) of_rank.add(y);
             const uint32_t e = v - (uint32_t)base;
@@ -1014,7 +1147,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         const float kz = fmaxf(zmin, unordered((uint32_t)(thr >> 32)));
         const bool all_stay = thr == 0;
         const bool vec = ((reinterpret_cast<uintptr_t>(out) - (uintptr_t)shift * 4u) & 15u) == 0;
-#pragma unroll 2
+#pragma unroll 1
         for (int w = s0 + lane; w < s1; w += 32) {
             float x[E], y[E];
             load(w, x);
@@ -1039,22 +1172,22 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
     }
     // ---- the drawn element, on the rank that holds it ---------------------------
-    if (sh.pick >= 0) {
-        // the run once more: every warp a part of it, then its part's words
-        const int r0 = min(W, run * sh.pick), r1 = min(W, r0 + run);
-        const int part = (run / 32 + kWarpWarps - 1) / kWarpWarps * 32;
+    const int pick = uniform(sh.pick);
+    if (pick >= 0) {
+        // the run once more: every warp a part of it, then its part's elements
+        const int r0 = max(0, run * pick * E - shift), r1 = min(n, run * (pick + 1) * E - shift);
+        const int part = (r1 - r0 + kWarpThreads - 1) / kWarpThreads * 32;
         const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
-        auto stays = [&](float x, int w, int i) -> bool {
-            return x > -INFINITY && composite(x, index_of(w, i)) >= thr;
+        auto mass_at = [&](int e, int end) -> float2 {   // of element e, if it stays
+            if (e < end) {
+                const float x = slice_elem<T>(sh.slice, e);
+                if (x > -INFINITY && composite(x, base + e) >= thr) return weight_of(x, S, &sh.tab);
+            }
+            return make_float2(0.f, 0.f);
         };
         Mass a;
-        for (int w = p0 + lane; w < p1; w += 32) {
-            float x[E];
-            load(w, x);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (stays(x[i], w, i)) a.add(weight(x[i], S, sh.tab));
-        }
+#pragma unroll 1
+        for (int e = p0; e < p1; e += 32) a.add(mass_at(e + lane, p1));
         const dd2 own = warp_sum_dd(a.value());
         if (lane == 0) sh.part_mass[warp] = own;
         __syncthreads();
@@ -1066,50 +1199,22 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             const int q = over ? __ffs(over) - 1 : 31 - __clz(some);
             if (q > 0) at = shfl_dd(reach, q - 1);
             const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part);
-            int64_t hit = -1, end = -1;
-            for (int w = q0; w < q1 && hit < 0; w += 32) {
-                float x[E];
-                float2 y[E];
-                Mass sum;
-#pragma unroll
-                for (int i = 0; i < E; ++i) x[i] = -INFINITY;
-                if (w + lane < q1) load(w + lane, x);
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    y[i] = stays(x[i], w + lane, i) ? weight(x[i], S, sh.tab) : make_float2(0.f, 0.f);
-                    sum.add(y[i]);
-                }
-                const dd2 inc = warp_scan_dd(sum.value(), lane);
-                const bool any = sum.h > 0.f;
-                const unsigned filled = __ballot_sync(0xffffffffu, any);
-                const unsigned past = __ballot_sync(0xffffffffu, any && less_dd(goal, add_dd(at, inc)));
-                dd2 walk = at;
-                {
-                    const dd2 ex = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
-                    if (lane > 0) walk = add_dd(at, ex);
-                }
-                int here = -1, final_ = -1;
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (y[i].x > 0.f) {
-                        walk = add_dd(walk, {y[i].x, y[i].y});
-                        final_ = i;
-                        if (here < 0 && less_dd(goal, walk)) here = i;
-                    }
-                if (here < 0) here = final_;
-                if (filled) {
-                    const int l = 31 - __clz(filled);
-                    end = index_of(w + l, 0) + __shfl_sync(0xffffffffu, final_, l);
-                }
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    hit = index_of(w + l, 0) + __shfl_sync(0xffffffffu, here, l);
-                }
-                at = add_dd(at, shfl_dd(inc, 31));
+            int hit = -1, end = -1;
+#pragma unroll 1
+            for (int e = q0; e < q1 && hit < 0; e += 32) {
+                const float2 y = mass_at(e + lane, q1);
+                __syncwarp();
+                const dd2 upto = add_dd(at, warp_scan_dd({y.x, y.y}, lane));
+                const unsigned has = __ballot_sync(0xffffffffu, y.x > 0.f);
+                const unsigned past = __ballot_sync(0xffffffffu, y.x > 0.f && less_dd(goal, upto));
+                if (has) end = e + 31 - __clz(has);
+                if (past) hit = e + __ffs(past) - 1;
+                at = shfl_dd(upto, 31);
             }
-            if (lane == 0) A.token[r] = (int32_t)(hit >= 0 ? hit : end);
+            if (lane == 0) A.token[r] = (int32_t)(base + (hit >= 0 ? hit : end));
         }
     }
+
     cluster_wait_all();  // no CTA leaves while another may read its shared memory
 }
 
