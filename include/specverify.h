@@ -71,7 +71,7 @@
  *                            build does not look, and such inputs give
  *                            unspecified results.  sv_warp_sample always
  *                            looks: a NaN or +infinite logit, or a
- *                            temperature that is not positive and finite;
+ *                            temperature outside [1e-36, 1e36];
  *       SV_STATUS_BAD_PAGE   a page id outside the cache (the append skips
  *                            the token; the attention takes zeros in place
  *                            of that page's keys and values);
@@ -363,7 +363,7 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
  *   probs     (not NULL): [R] rows of V f32, probs_row_stride (>= V) apart:
  *             w_v over the kept mass, 0 for what was left out.
  * The kept set and the token are those of a 64-bit evaluation: masses are
- * summed to about 1e-11.  -inf logits have no mass.  A row without mass (all
+ * good to about 1e-10 (weights below e^-85 count as 0).  -inf logits have no mass.  A row without mass (all
  * -inf: SV_STATUS_ZERO_MASS), with a NaN or +inf logit, or with a bad
  * temperature (SV_STATUS_BAD_VALUE) gives token -1 and a row of zeros.  Rows
  * warped alike serve as the p and q of sv_verify_sample. */

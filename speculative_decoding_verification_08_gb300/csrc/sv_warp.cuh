@@ -18,7 +18,7 @@
 // answers of a 64-bit evaluation.  fp64 runs at 1/64 of the fp32 rate here, so
 // a weight exp((z - max) / T) is formed as a pair of floats (weight()): the
 // exponent and the table-and-polynomial value keep their rounding errors in
-// the low part, good to about 5e-12 relative.
+// the low part.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -35,6 +35,7 @@ constexpr int kWarpWarps = kWarpThreads / 32;
 constexpr int kWarpMaxCluster = 8;
 constexpr int kBins = 1024;            // of a histogram of counts and masses; of one alone twice as many
 constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
+constexpr float kColdest = 1e-36f, kHottest = 1e36f;  // temperatures
 constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
 constexpr int kLocalList = 192;        // border elements one CTA may gather
 constexpr int kList = 1024;            // and the row
@@ -93,49 +94,35 @@ struct ExpTable {
 };
 
 struct RowScale {
-    float m, ch, cl;  // row maximum; log2(e) / temperature as hi + lo
+    float m;          // row maximum
+    float ih, il;     // 1 / temperature as hi + lo
+    float ch, cl;     // log2(e) / temperature
+    float floor;      // -85 T: what lies further down weighs nothing
 };
 
-__device__ __forceinline__ RowScale row_scale(float m, float temperature) {
-    const double c = 1.4426950408889634 / (double)temperature;
-    RowScale s;
-    s.m = m;
-    s.ch = (float)c;
-    s.cl = (float)(c - (double)s.ch);
-    return s;
-}
-
-// exp((z - max) / T) as x + y (hi, lo); 0 below 2^-100.
-//   z - max = d + dl exactly; (d + dl) * c = e + el; e = n + j/32 + r with
-//   |r| <= 1/64; 2^e = 2^n T_j (1 + s), s = 2^r - 1 by its series to r^5.
+// exp(x), x = (z - max) / T, as hi + lo, to about 2^-35 relative; 0 below exp(-85).
+//   z - max = d + dl and x = xh + xl to twice the fp32 digits; x = k ln2/32 + r
+//   with |r| < 0.011; 2^(k/32) from the table, exp(r) - 1 = r + r^2/2 + r^3/6
+//   + r^4/24.
 __device__ __forceinline__ float2 weight(float z, const RowScale &S, const ExpTable &tab) {
-    const float d = z - S.m;
-    const float e = d * S.ch;
-    if (!(e >= -100.f)) return make_float2(0.f, 0.f);
-    const float bb = d - z;
-    const float dl = (z - (d - bb)) - (S.m + bb);
-    float el = fmaf(d, S.ch, -e);
-    el = fmaf(d, S.cl, el);
-    el = fmaf(dl, S.ch, el);
-    const float k = rintf(e * 32.f);
-    const float r = fmaf(k, -0.03125f, e);  // exact
-    const int ki = (int)k;
-    const int n = (ki + 16) >> 5, j = ki - n * 32;  // j in [-16, 15]
-    const float2 T = tab.t[j + 16];
-    const float ph = r * 0.693147182f;
-    float pl = fmaf(r, 0.693147182f, -ph);
-    pl = fmaf(r, -1.90465421e-9f, pl);
-    pl = fmaf(el, 0.693147182f, pl);
-    float q = fmaf(r, 1.33335581e-3f, 9.61812911e-3f);
-    q = fmaf(r, q, 5.55041087e-2f);
-    q = fmaf(r, q, 2.40226507e-1f);
-    const float t = fmaf(r * r, q, pl);
-    const float sh = ph + t, sl = t - (sh - ph);
-    const float u = T.x * sh;
-    const float ul = fmaf(T.x, sl, fmaf(T.x, sh, -u)) + fmaf(T.y, sh, T.y);
-    const float wh = T.x + u, wl = (u - (wh - T.x)) + ul;
-    const float scale = __int_as_float((n + 127) << 23);
-    return make_float2(wh * scale, wl * scale);
+    const float far = z - S.m, b = far - z;
+    const bool in = far >= S.floor;
+    const float d = in ? far : S.floor;
+    const float dl = in ? (z - (far - b)) - (S.m + b) : 0.f;
+    const float xh = d * S.ih;
+    const float xl = fmaf(dl, S.ih, fmaf(d, S.il, fmaf(d, S.ih, -xh)));
+    const float km = fmaf(xh, 46.1662413f, 12582912.f);  // 1.5 * 2^23: the low bits hold k
+    const float k = km - 12582912.f;
+    const float r = fmaf(k, -0.0216608495f, xh);   // exact: few bits are left
+    const float rl = fmaf(k, 5.95204441e-11f, xl), q = r + rl;
+    const float t = fmaf(q * q, fmaf(q, fmaf(q, 4.16666667e-2f, 0.166666667f), 0.5f), rl);
+    const int ki = __float_as_int(km) + 16;
+    const float2 T = tab.t[ki & 31];
+    const float scale = in ? __uint_as_float(((uint32_t)ki >> 5 << 23) + 0x3f800000u) : 0.f;
+    const float v = T.x * r, vl = fmaf(T.x, r, -v), u = fmaf(T.x, t, fmaf(T.y, r, T.y));
+    const float h = T.x + v;
+    const float l = (v - (h - T.x)) + (vl + u);
+    return make_float2(h * scale, l * scale);
 }
 
 __device__ __noinline__ float2 weight_of(float z, RowScale S, const ExpTable *tab) {
@@ -183,18 +170,30 @@ __device__ __forceinline__ dd2 warp_scan_dd(dd2 a, int lane) {
     return a;
 }
 
-// A running sum of weights.
+// A running sum of weights (each at most 1): it starts at 4, so that every sum
+// is larger than what is added and its rounding error is a two-term difference.
 struct Mass {
-    float h = 0.f, l = 0.f;
+    float h = 4.f, l = 0.f;
     __device__ __forceinline__ void add(float2 w) {
-        const float s = h + w.x, b = s - h;
-        l += ((h - (s - b)) + (w.x - b)) + w.y;
+        const float s = h + w.x;
+        l += (w.x - (s - h)) + w.y;
         h = s;
     }
-    __device__ __forceinline__ dd2 value() const { return norm2(h, l); }
+    __device__ __forceinline__ dd2 value() const { return norm2(h - 4.f, l); }
 };
 
 namespace cg = cooperative_groups;
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // exp((z - max) / T) in fp32, good to about 2^-22: the exponent with its low
 // part, its fraction through ex2.approx.
@@ -228,12 +227,13 @@ struct alignas(16) WarpShared {
     ExpTable tab;
     float top, low;                 // slice maximum and smallest finite logit
     int32_t bad;
-    float ch, cl;                   // log2(e) / temperature
+    float ih, il, ch, cl;           // 1 / temperature, log2(e) / temperature
     dd2 min_off;                    // temperature * ln(min_p)
     uint32_t count, gathered;       // border elements
     int32_t list_end[kWarpMaxCluster], full, pick;
     float total;
-    double coarse[2][32];           // counts and masses of 32 groups of bins
+    uint32_t coarse_count[32];      // of 32 groups of bins
+    float coarse_mass[32];
     int32_t k_bin, lo_bin, hi_bin, k_before;
     uint64_t threshold;
     RowSlice slice;
@@ -311,44 +311,52 @@ __device__ __forceinline__ __half minus_inf() {
     return __ushort_as_half(0xfc00u);
 }
 
-__device__ __forceinline__ double scan_f64(double x, int lane) {
+// A histogram's increment, left out for -inf (padding among it), without a branch.
+__device__ __forceinline__ void add_if_finite(uint32_t *bin, uint32_t by, float x) {
+    asm volatile("{ .reg .pred p; setp.gt.f32 p, %2, 0fFF800000; @p red.shared.add.u32 [%0], %1; }" ::"r"(
+                     smem_u32(bin)),
+                 "r"(by), "f"(x)
+                 : "memory");
+}
+
+__device__ __forceinline__ float scan_f32(float x, int lane) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, x, d);
-        x += lane >= d ? o : 0.;
+        const float o = __shfl_up_sync(0xffffffffu, x, d);
+        x += lane >= d ? o : 0.f;
+    }
+    return x;
+}
+__device__ __forceinline__ uint32_t scan_u32(uint32_t x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, x, d);
+        x += lane >= d ? o : 0u;
     }
     return x;
 }
 
-// One group of the row's bins, `per` (1 or 2) to a lane, added over the ranks
-// and summed up to and including each: masses when `inv_unit` is not zero, else
-// counts.  A warp's work; what it reads of the other CTAs is a few words each
-// (whole histograms took most of a row's time).
-__device__ __forceinline__ double2 scan_bins(WarpShared &sh, int C, int slot, int per, float octaves,
-                                          float drop, float inv_unit, int lane) {
+// One or two neighbouring bins of the row, added over the ranks.  (A few words
+// of each CTA: reading whole histograms took most of a row's time.)
+__device__ __forceinline__ uint2 row_bins(WarpShared &sh, int C, int slot, int per_lane) {
     cg::cluster_group cluster = cg::this_cluster();
+    uint2 s = make_uint2(0, 0);
     uint32_t x[kWarpMaxCluster], y[kWarpMaxCluster];
 #pragma unroll
     for (int c = 0; c < kWarpMaxCluster; ++c) {
         x[c] = y[c] = 0;
         if (c < C) {
-            const uint32_t *h = cluster.map_shared_rank(sh.hist, c) + slot + lane * per;
+            const uint32_t *h = cluster.map_shared_rank(sh.hist, c) + slot;
             x[c] = h[0];
-            if (per == 2) y[c] = h[1];
+            if (per_lane == 2) y[c] = h[1];
         }
     }
-    double a = 0, b = 0;
 #pragma unroll
     for (int c = 0; c < kWarpMaxCluster; ++c) {
-        a += (double)x[c];
-        b += (double)y[c];
+        s.x += x[c];
+        s.y += y[c];
     }
-    if (inv_unit != 0.f) {
-        a *= (double)(exp2f(-octaves - drop * (float)(lane * per)) * inv_unit);
-        b *= (double)(exp2f(-octaves - drop * (float)(lane * per + 1)) * inv_unit);
-    }
-    const double upto = scan_f64(a + b, lane);
-    return make_double2(upto - b, upto);
+    return s;
 }
 
 // ---- slow paths, rarely taken: out of line, an element at a time --------------
@@ -451,17 +459,24 @@ __device__ __noinline__ uint64_t bisect_row(WarpShared &sh, int64_t k, float p) 
 __device__ __noinline__ void rank_alone(WarpShared &sh, int got) {
     uint64_t key[kList / kWarpThreads];
     int at_of[kList / kWarpThreads];
+    const int mine = (got + kWarpThreads - 1) / kWarpThreads;   // elements per thread
 #pragma unroll
     for (int j = 0; j < kList / kWarpThreads; ++j) {
         const int i = (int)threadIdx.x + j * kWarpThreads;
         key[j] = i < got ? sh.all[i] : 0;
         at_of[j] = 0;
     }
+    if (mine == 1) {
+        if ((int)threadIdx.x / 32 * 32 < got)
+#pragma unroll 8
+            for (int x = 0; x < got; ++x) at_of[0] += sh.all[x] > key[0];
+    } else {
 #pragma unroll 1
-    for (int x = 0; x < got; ++x) {
-        const uint64_t o = sh.all[x];
+        for (int x = 0; x < got; ++x) {
+            const uint64_t o = sh.all[x];
 #pragma unroll
-        for (int j = 0; j < kList / kWarpThreads; ++j) at_of[j] += o > key[j];
+            for (int j = 0; j < kList / kWarpThreads; ++j) at_of[j] += o > key[j];
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -533,9 +548,11 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     const float p = uniform(A.top_p ? A.top_p[r] : 1.f);
     const float mp = uniform(A.min_p ? A.min_p[r] : 0.f);
     if (tid == 64) {
-        const RowScale s = row_scale(0.f, temp);
-        sh.ch = s.ch;
-        sh.cl = s.cl;
+        const double i = 1.0 / (double)temp, c = i * 1.4426950408889634;
+        sh.ih = (float)i;
+        sh.il = (float)(i - (double)sh.ih);
+        sh.ch = (float)c;
+        sh.cl = (float)(c - (double)sh.ch);
     }
     if (tid == 96 && mp > 0.f) {
         const double off = (double)temp * log((double)mp);
@@ -567,24 +584,21 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         return y;
     };
 
-    // ---- maximum, smallest finite logit, values that spoil the row ---------
+    // ---- the maximum (NaN where there is one) ------------------------------
     {
         float top = -INFINITY, low = INFINITY;
-        bool bad = false;
-#pragma unroll 2
+        // (the smallest of a sample: it only sets the histogram's scale)
+#pragma unroll 4
         for (int w = s0 + lane; w < s1; w += 32) {
             float x[E];
             load(w, x);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                bad |= !(x[i] < INFINITY);
-                top = fmaxf(top, x[i]);
-                low = fminf(low, x[i] == -INFINITY ? INFINITY : x[i]);
-            }
+            for (int i = 0; i < E; ++i) top = max_nan(top, x[i]);
+            low = fminf(low, x[0] == -INFINITY ? INFINITY : x[0]);
         }
 #pragma unroll 1
         for (int d = 16; d > 0; d >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
             low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
         }
         if (lane == 0) {
@@ -593,19 +607,18 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
 #pragma unroll 1
         for (int i = tid; i < 2 * kBins; i += kWarpThreads) sh.hist[i] = 0;
-        bad = __syncthreads_or(bad);
+        __syncthreads();
         if (warp == 0) {
             top = lane < kWarpWarps ? sh.warp_f[0][lane] : -INFINITY;
             low = lane < kWarpWarps ? sh.warp_f[1][lane] : INFINITY;
 #pragma unroll 1
             for (int d = 16; d > 0; d >>= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
                 low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
             }
             if (lane == 0) {
                 sh.top = top;
                 sh.low = low;
-                if (bad) sh.bad = 1;
             }
         }
     }
@@ -620,12 +633,12 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
         low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
     }
     m = uniform(m);
     low = uniform(low);
-    bad = uniform(__any_sync(0xffffffffu, bad)) || !(temp > 0.f && temp < INFINITY);
+    bad = uniform(__any_sync(0xffffffffu, bad)) || !(m < INFINITY) || !(temp >= kColdest && temp <= kHottest);
     float *out = A.probs ? A.probs + r * A.ps + base : nullptr;
     if (bad || m == -INFINITY) {
         if (rank == 0 && tid == 0) {
@@ -638,7 +651,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         cluster.sync();
         return;
     }
-    const RowScale S = {m, sh.ch, sh.cl};
+    const RowScale S = {m, sh.ih, sh.il, sh.ch, sh.cl, -85.f * temp};
     const bool by_k = k > 0 && k < A.V, by_p = p < 1.f;
     float zmin = -INFINITY;  // min-p's lowest logit
     if (mp > 0.f) {
@@ -656,8 +669,9 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // are runs of the row's order
     const bool both = by_k && by_p;
     const int bins = both ? kBins : 2 * kBins;
-    const float span = fminf(m - low, kRangeOctaves / S.ch);
-    const float per = span > 1e-30f ? (float)(bins - 1) / span : 0.f;    // bins per unit of z
+    // the last bin is for what lies further down
+    const float reach = kRangeOctaves / S.ch, span = low < m ? fmaxf(fminf(m - low, reach), 1e-30f) : reach;
+    const float per = (float)(bins - 2) / span;                          // bins per unit of z
     auto t_of = [&](float x) -> float {
         return fminf(fmaf(m - x, per, kMagic), kMagic + (float)(bins - 1));
     };
@@ -667,11 +681,12 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     float t_keep = never, t_last = 0.f, t_k = never;
     int64_t k_left = 0;
     uint64_t thr = 0;       // kept: composite >= thr
+    bool far = false;
     if (by_k || by_p) {
         // masses relative to the bin's middle, in fixed point: that short arc of
         // the exponential (at most +-0.02 octaves) to its square term
-        const float drop = per > 0.f ? S.ch / per : 0.f;                 // octaves per bin
-        const float unit = exp2f((float)min(22, 30 - (31 - __clz(A.slice + 16))));
+        const float drop = S.ch / per;                                   // octaves per bin
+        const float unit = exp2f((float)min(22, 27 - (31 - __clz(A.slice + 16))));
         const float c1 = -unit * 0.693147182f * drop, c2 = unit * 0.240226507f * drop * drop;
         uint32_t *masses = sh.hist + (both ? kBins : 0);
         auto count_up = [&](auto want_k, auto want_p) {
@@ -683,12 +698,11 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 for (int i = 0; i < E; ++i) {
                     const float d = m - x[i], t = fminf(fmaf(d, per, kMagic), never - 1.f);
                     const int b = __float_as_int(t) & (2 * kBins - 1);
-                    const bool real = x[i] > -INFINITY;
-                    if (decltype(want_k)::value) atomicAdd(&sh.hist[b], real ? 1u : 0u);
+                    if (decltype(want_k)::value) add_if_finite(&sh.hist[b], 1u, x[i]);
                     if (decltype(want_p)::value) {
                         const float f = fminf(fmaf(d, per, kMagic - t), 0.5f);
                         const float y = fmaf(f, fmaf(f, c2, c1), unit + kMagic);
-                        atomicAdd(&masses[b], real ? __float_as_uint(y) & 0x7fffffu : 0u);
+                        add_if_finite(&masses[b], __float_as_uint(y) & 0x7fffffu, x[i]);
                     }
                 }
             }
@@ -700,41 +714,44 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         else count_up(no, yes);
         __syncthreads();
         // sums of 32 groups of bins, a warp to a group
-        const int group = bins / 32, per = group / 32;
+        const int group = bins / 32, per_lane = group / 32;
         const float inv_unit = 1.f / unit;
-#pragma unroll 1
         for (int g = warp; g < 32; g += kWarpWarps) {
             uint32_t c = 0;
             float y = 0.f;
-#pragma unroll 1
-            for (int i = lane; i < group; i += 32) {
-                const int b = g * group + i;
-                if (by_k) c += sh.hist[b];
-                if (by_p) y += (float)masses[b] * (exp2f(-drop * (float)b) * inv_unit);
-            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (h < per_lane) {
+                    const int b = g * group + h * 32 + lane;
+                    if (by_k) c += sh.hist[b];
+                    if (by_p) y += (float)masses[b] * (pow2(-drop * (float)b) * inv_unit);
+                }
             if (by_k) c = __reduce_add_sync(0xffffffffu, c);
             if (by_p)
-#pragma unroll 1
+#pragma unroll
                 for (int d = 16; d > 0; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
             if (lane == 0) {
-                sh.coarse[0][g] = (double)c;
-                sh.coarse[1][g] = (double)y;
+                sh.coarse_count[g] = c;
+                sh.coarse_mass[g] = y;
             }
         }
         cluster.sync();
         // every rank's first warp: the row's groups, then the bins of the ones
         // that hold the borders
         if (warp == 0) {
-            double count = 0, mass = 0;
+            uint32_t count = 0;
+            float mass = 0.f;
             {
-                double x[kWarpMaxCluster], y[kWarpMaxCluster];
+                uint32_t x[kWarpMaxCluster];
+                float y[kWarpMaxCluster];
 #pragma unroll
                 for (int c = 0; c < kWarpMaxCluster; ++c) {
-                    x[c] = y[c] = 0;
+                    x[c] = 0;
+                    y[c] = 0.f;
                     if (c < C) {
                         const WarpShared *o = cluster.map_shared_rank(&sh, c);
-                        x[c] = o->coarse[0][lane];
-                        y[c] = o->coarse[1][lane];
+                        x[c] = o->coarse_count[lane];
+                        y[c] = o->coarse_mass[lane];
                     }
                 }
 #pragma unroll
@@ -744,70 +761,66 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                 }
             }
             int k_bin = bins, k_before = 0, lo = bins, hi = bins;
-            const double m_upto = by_p ? scan_f64(mass, lane) : 0.;
-            double m_all = __shfl_sync(0xffffffffu, m_upto, 31), slack = 0;
-            if (by_k) {
-                const double upto = scan_f64(count, lane);
-                const unsigned at = __ballot_sync(0xffffffffu, upto >= (double)k);
-                // (a row with no more than k finite logits has no border of top-k)
-                if (__shfl_sync(0xffffffffu, upto, 31) > (double)k) {
-                    const int g = __ffs(at) - 1;
-                    const double before = __shfl_sync(0xffffffffu, upto - count, g);
-                    double2 in = scan_bins(sh, C, g * group, per, 0.f, 0.f, 0.f, lane);
-                    in.x += before;
-                    in.y += before;
-                    const unsigned bin = __ballot_sync(0xffffffffu, in.y >= (double)k);
-                    const int l = __ffs(bin) - 1;
-                    const int second = __shfl_sync(0xffffffffu, (int)(per == 2 && !(in.x >= (double)k)), l);
-                    k_bin = g * group + l * per + second;
-                    // what lies before that bin, and in it
-                    const double down = __shfl_up_sync(0xffffffffu, in.y, 1);
-                    const double start = second ? in.x : lane > 0 ? down : before;
-                    const double end = per == 2 && !second ? in.x : in.y;
-                    k_before = (int)__shfl_sync(0xffffffffu, start, l);
-                    const double inside = __shfl_sync(0xffffffffu, end - start, l);
-                    if (by_p) {
-                        double2 y = scan_bins(sh, C, kBins + g * group, per, drop * (float)(g * group), drop,
-                                              inv_unit, lane);
-                        const double m_before = __shfl_sync(0xffffffffu, m_upto - mass, g);
-                        const double m_down = __shfl_up_sync(0xffffffffu, y.y, 1);
-                        const double ms = __shfl_sync(0xffffffffu, second ? y.x : lane > 0 ? m_down : 0., l);
-                        const double me = __shfl_sync(0xffffffffu, per == 2 && !second ? y.x : y.y, l);
-                        const double part = (me - ms) * ((double)(k - k_before) / inside);
-                        m_all = m_before + ms + part;
-                        slack = 0.03 * part;   // the bin's elements differ by less
-                    }
+            const float m_upto = scan_f32(mass, lane);
+            const uint32_t c_upto = scan_u32(count, lane);
+            float m_all = __shfl_sync(0xffffffffu, m_upto, 31), slack = 0.f;
+            // (a row with no more than k logits has no border of top-k)
+            if (by_k && (int64_t)__shfl_sync(0xffffffffu, c_upto, 31) > k) {
+                const int g = __ffs(__ballot_sync(0xffffffffu, (int64_t)c_upto >= k)) - 1;
+                const uint32_t before = __shfl_sync(0xffffffffu, c_upto - count, g);
+                const uint2 own = row_bins(sh, C, g * group + lane * per_lane, per_lane);
+                const uint32_t upto = before + scan_u32(own.x + own.y, lane);
+                const int l = __ffs(__ballot_sync(0xffffffffu, (int64_t)upto >= k)) - 1;
+                const bool first = per_lane == 1 || (int64_t)(upto - own.y) >= k;
+                const int second = __shfl_sync(0xffffffffu, (int)!first, l);
+                k_bin = g * group + l * per_lane + second;
+                k_before = (int)__shfl_sync(0xffffffffu, upto - own.y - (first ? own.x : 0u), l);
+                const uint32_t inside = __shfl_sync(0xffffffffu, first ? own.x : own.y, l);
+                if (by_p) {   // (then a bin to a lane)
+                    const uint2 w = row_bins(sh, C, kBins + g * group + lane, 1);
+                    const float y = (float)w.x * (pow2(-drop * (float)(g * group + lane)) * inv_unit);
+                    const float start = __shfl_sync(0xffffffffu, m_upto - mass, g) +
+                                        __shfl_sync(0xffffffffu, scan_f32(y, lane) - y, l);
+                    const float part = __shfl_sync(0xffffffffu, y, l) * ((float)(k - k_before) / (float)inside);
+                    m_all = start + part;
+                    slack = 0.03f * part;   // the bin's elements differ by less
                 }
             }
             if (by_p) {
                 // bins lo..hi hold the first element before which at least the goal
                 // lies, whatever the approximate masses are off by
-                const double err = 2e-5 + 0.5 * (double)inv_unit, goal = (double)p * m_all,
-                             rest = m_all - goal, loose = slack + 1e-6 * m_all;
-                auto low = [&](double through) -> bool {
-                    return through * (1 + err) >= goal * (1 - err) - loose &&
-                           (m_all - through) * (1 - err) <= rest * (1 + err) + loose;
+                // (the last bin's mass is too large, by less than what it is)
+                const float last = (float)row_bins(sh, C, (both ? kBins : 0) + bins - 1, 1).x *
+                                   (pow2(-drop * (float)(bins - 1)) * inv_unit);
+                const float err = 2e-5f + 0.5f * inv_unit, goal = p * m_all, rest = m_all - goal,
+                            loose = slack + 4e-6f * m_all + last;
+                auto low_ok = [&](float through) -> bool {
+                    return through * (1.f + err) >= goal * (1.f - err) - loose &&
+                           (m_all - through) * (1.f - err) <= rest * (1.f + err) + loose;
                 };
-                auto high = [&](double through) -> bool {
-                    return through * (1 - err) >= goal * (1 + err) + loose ||
-                           (m_all - through) * (1 + err) <= rest * (1 - err) - loose;
+                auto high_ok = [&](float through) -> bool {
+                    return through * (1.f - err) >= goal * (1.f + err) + loose ||
+                           (m_all - through) * (1.f + err) <= rest * (1.f - err) - loose;
                 };
-                const unsigned gl = __ballot_sync(0xffffffffu, low(m_upto));
-                const unsigned gh = __ballot_sync(0xffffffffu, high(m_upto));
+                const unsigned gl = __ballot_sync(0xffffffffu, low_ok(m_upto));
+                const unsigned gh = __ballot_sync(0xffffffffu, high_ok(m_upto));
 #pragma unroll 1
                 for (int side = 0; side < 2; ++side) {
                     const unsigned at = side == 0 ? gl : gh;
                     if (at == 0) continue;
                     const int g = __ffs(at) - 1;
-                    double2 y = scan_bins(sh, C, (both ? kBins : 0) + g * group, per,
-                                          drop * (float)(g * group), drop, inv_unit, lane);
-                    const double before = __shfl_sync(0xffffffffu, m_upto - mass, g);
-                    const bool in0 = side == 0 ? low(before + y.x) : high(before + y.x);
-                    const bool in1 = side == 0 ? low(before + y.y) : high(before + y.y);
+                    const uint2 w = row_bins(sh, C, (both ? kBins : 0) + g * group + lane * per_lane, per_lane);
+                    const float b0 = (float)(g * group + lane * per_lane);
+                    const float y0 = (float)w.x * (pow2(-drop * b0) * inv_unit);
+                    const float y1 = (float)w.y * (pow2(-drop * (b0 + 1.f)) * inv_unit);
+                    const float upto = __shfl_sync(0xffffffffu, m_upto - mass, g) + scan_f32(y0 + y1, lane);
+                    const bool in1 = side == 0 ? low_ok(upto) : high_ok(upto);
+                    const bool in0 = side == 0 ? low_ok(upto - y1) : high_ok(upto - y1);
+                    // (where rounding lets none pass: the group's last bin)
                     const unsigned bin = __ballot_sync(0xffffffffu, in1);
-                    const int l = bin ? __ffs(bin) - 1 : 31;   // (its end passed, to rounding)
-                    const int second = __shfl_sync(0xffffffffu, (int)(per == 2 && !in0), l);
-                    (side == 0 ? lo : hi) = g * group + l * per + second;
+                    const int l = bin ? __ffs(bin) - 1 : 31;
+                    const int second = __shfl_sync(0xffffffffu, (int)(per_lane == 2 && !in0), l);
+                    (side == 0 ? lo : hi) = g * group + l * per_lane + second;
                 }
             }
             if (lane == 0) {
@@ -819,6 +832,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
         __syncthreads();
         const int k_bin = uniform(sh.k_bin);
+        far = k_bin == bins - 1;    // what lies there is in no order: by bisection
         if (k_bin < bins) {
             t_k = kMagic + (float)k_bin;
             k_left = k - sh.k_before;
@@ -942,7 +956,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     }
     __syncthreads();
     int got = uniform(sh.list_end[C - 1]);
-    const bool full = uniform(sh.full) != 0;
+    const bool full = uniform(sh.full) != 0 || far;
     // (the histogram that the lists lie over has been read everywhere)
     if (!full)
 #pragma unroll 1
@@ -968,7 +982,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
                     if (lane < got) sh.share.ranked[at] = key;
                 }
                 __syncthreads();
-            } else if (got <= kShared) {
+            } else if (got > 128 && got <= kShared) {
                 // every rank places a share of them, eight threads to an element,
                 // in every rank's list
                 const int part = lane % 8, total_groups = kWarpThreads / 8 * C;
@@ -990,7 +1004,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             } else {
                 rank_alone(sh, got);
             }
-            border = got <= kShared ? sh.share.ranked : sh.all;
+            border = got <= 32 || (got > 128 && got <= kShared) ? sh.share.ranked : sh.all;
             if (warp == 0) {
                 // the elements that top-k leaves: those above its border bin
                 // (first in the order) and k_left of it
@@ -1076,9 +1090,10 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // the border elements that stay, into the runs and ranks they belong to;
     // every rank adds them up alike, so that all agree on where the goal lies
     if (got > 0) {
-        // their weights (over the unranked list, where it is done with)
-        float2 *weights = reinterpret_cast<float2 *>(sh.share.raw);
-        if (got <= kShared) {
+        // their weights, in the half of the lists that is free
+        const bool stored = got <= kShared;
+        float2 *weights = reinterpret_cast<float2 *>(border == sh.all ? sh.share.ranked : sh.share.raw);
+        if (stored) {
 #pragma unroll 1
             for (int i = tid; i < got; i += kWarpThreads)
                 weights[i] = border[i] >= thr ? weight_of(unordered((uint32_t)(border[i] >> 32)), S, &sh.tab)
@@ -1092,7 +1107,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         for (int i = lane; i < got; i += 32) {
             const uint64_t key = border[i];
             if (key < thr) break;       // (in the row's order)
-            const float2 y = got <= kShared ? weights[i]
+            const float2 y = stored ? weights[i]
                                             : weight_of(unordered((uint32_t)(key >> 32)), S, &sh.tab);
             const uint32_t v = ~(uint32_t)key;
             if (warp < C && v - rank_base < (uint32_t)A.slice) of_rank.add(y);
@@ -1122,9 +1137,10 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             sh.pick = -1;
         }
         if (A.token) {
-            const double u = A.u[r];
-            const float uh = (float)u;
-            goal = mul_dd(total, norm2(uh, (float)(u - (double)uh)));
+            // the goal rounded as in 64 bits
+            const double g = A.u[r] * ((double)total.h + (double)total.l);
+            const float gh = (float)g;
+            goal = {gh, (float)(g - (double)gh)};
             const unsigned some = __ballot_sync(0xffffffffu, own.h > 0.f);
             const unsigned over = __ballot_sync(0xffffffffu, own.h > 0.f && less_dd(goal, upto));
             const int holder = over ? __ffs(over) - 1 : 31 - __clz(some);
