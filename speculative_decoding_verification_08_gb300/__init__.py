@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import _build
@@ -78,22 +79,6 @@ def load():
         return _lib
 
 
-class _PagedCache(ctypes.Structure):
-    """sv_paged_cache of include/specverify.h."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
-                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("tokens", ctypes.c_int32),
-                ("max_pages", ctypes.c_int32), ("pages", ctypes.c_void_p),
-                ("pages_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
-                ("kv_len", ctypes.c_void_p)]
-
-
-_Stride2 = ctypes.c_int64 * 2
-_Stride3 = ctypes.c_int64 * 3
-
-
 def _declare(lib):
     """Sets the argument and result types of every C-ABI call on a loaded
     copy of the library (the regular build, or a debug build)."""
@@ -133,7 +118,7 @@ def _declare(lib):
     lib.sv_trace_reset.restype = ctypes.c_int
     lib.sv_trace_read.argtypes = [P, sz, ctypes.POINTER(sz), P]
     lib.sv_trace_read.restype = ctypes.c_int
-    C, S = ctypes.POINTER(_PagedCache), ctypes.POINTER(ctypes.c_int64)
+    C = S = ctypes.c_char_p      # sv_paged_cache and strides, packed
     lib.sv_cache_workspace_size.argtypes = []
     lib.sv_cache_workspace_size.restype = sz
     lib.sv_append_kv.argtypes = [C, P, S, P, S, P, S, P, S, i32, P, i32, i32, P, P, sz, P]
@@ -551,83 +536,115 @@ def cache_workspace(device=None, stream=None) -> CacheWorkspace:
     """The workspace that calls without one share on this device and stream
     (calls on different streams never share an implicit one)."""
     torch = _torch()
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
     return _cache_ws(None, dev, _raw_stream(dev, stream), stream)
 
 
 def _raw_stream(device, stream) -> int:
     if stream is not None:
         return stream.cuda_stream
-    return _torch().cuda.current_stream(device).cuda_stream
+    # (the plain handle: a Stream object costs more than the rest of the checks)
+    return _torch_c()._cuda_getCurrentRawStream(device)
+
+
+_TORCH_C = None
+
+
+def _torch_c():
+    global _TORCH_C
+    if _TORCH_C is None:
+        _TORCH_C = _torch()._C
+    return _TORCH_C
 
 
 def _cache_ws(ws, device, raw, stream):
     if ws is not None:
         return ws
-    key = (device.index, raw)
+    key = (device, raw)
     w = _ws_cache.get(key)
     if w is None:
-        w = _ws_cache[key] = CacheWorkspace(device, stream)
+        w = _ws_cache[key] = CacheWorkspace(_torch().device("cuda", device), stream)
     return w
 
 
+_CACHE_TYPES = None
+
+
 def _cache_dtype(dtype, name) -> int:
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return 1
-    if dtype == torch.float16:
-        return 2
-    raise SpecVerifyError(f"{name} must be torch.bfloat16 or torch.float16, got {dtype}")
+    global _CACHE_TYPES
+    if _CACHE_TYPES is None:
+        torch = _torch()
+        _CACHE_TYPES = {torch.bfloat16: 1, torch.float16: 2}
+    code = _CACHE_TYPES.get(dtype)
+    if code is None:
+        raise SpecVerifyError(f"{name} must be torch.bfloat16 or torch.float16, got {dtype}")
+    return code
 
 
-def _heads3(x, like, heads, D, N, name):
-    """A token array [N][heads][D] of the cache's type and device."""
-    if x.dtype != like.dtype or x.device != like.device:
-        raise SpecVerifyError(f"{name} must be {like.dtype} on {like.device}, got {x.dtype} on "
+# sv_paged_cache and a token array's strides as bytes: one packing call each,
+# where a ctypes structure would be filled field by field
+_PACK_CACHE = struct.Struct("@QQ3q3q8iQqQQ").pack
+_PACK_2 = struct.Struct("@2q").pack
+
+
+def _heads3(x, dtype, device, heads, D, N, name):
+    """A token array [N][heads][D] of the cache's type and device: its packed
+    strides."""
+    if x.dtype is not dtype or x.get_device() != device:
+        raise SpecVerifyError(f"{name} must be {dtype} on cuda:{device}, got {x.dtype} on "
                               f"{x.device}")
     shape = x.shape
-    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads) or \
-            (N is not None and shape[0] != N):
-        raise SpecVerifyError(f"{name}: expected [{'N' if N is None else N}]"
-                              f"[{'heads' if heads is None else heads}][{D}], got {tuple(shape)}")
-    st = x.stride()
-    if st[2] != 1 and D > 1:
+    if len(shape) != 3 or shape[2] != D or shape[1] != heads or shape[0] != N:
+        raise SpecVerifyError(f"{name}: expected [{N}][{heads}][{D}], got {tuple(shape)}")
+    s = x.stride()
+    if s[2] != 1 and D > 1:
         raise SpecVerifyError(f"{name}: the head dimension must be contiguous")
-    return _Stride2(st[0], st[1])
+    return _PACK_2(s[0], s[1])
 
 
-def _ints(x, shape, name, device):
-    torch = _torch()
-    if x.dtype != torch.int32 or x.device != device:
-        raise SpecVerifyError(f"{name} must be torch.int32 on {device}, got {x.dtype} on {x.device}")
-    if shape is not None and (tuple(x.shape) != shape or not x.is_contiguous()):
-        raise SpecVerifyError(f"{name}: expected {list(shape)} contiguous, got {tuple(x.shape)}")
+def _ints(x, n, name, device):
+    """A contiguous int32 vector of n elements on the device."""
+    if x.dtype is not _INT32 or x.get_device() != device:
+        raise SpecVerifyError(f"{name} must be torch.int32 on cuda:{device}, got {x.dtype} on "
+                              f"{x.device}")
+    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
+        raise SpecVerifyError(f"{name}: expected {n} contiguous elements, got {tuple(x.shape)}")
+
+
+_INT32 = None
 
 
 def _paged(k_cache, v_cache, pages, q_start, kv_len, N):
-    """The batch's sv_paged_cache, checked."""
-    if not k_cache.is_cuda or v_cache.device != k_cache.device:
+    """The batch's sv_paged_cache, checked and packed; its type, device, heads
+    and head size."""
+    global _INT32
+    if _INT32 is None:
+        _INT32 = _torch().int32
+    dev, dtype, shape = k_cache.get_device(), k_cache.dtype, k_cache.shape
+    if dev < 0 or v_cache.get_device() != dev:
         raise SpecVerifyError("k_cache and v_cache must be CUDA tensors on one device")
-    dt = _cache_dtype(k_cache.dtype, "k_cache")
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or k_cache.dim() != 4:
+    code = _cache_dtype(dtype, "k_cache")
+    if v_cache.dtype is not dtype or v_cache.shape != shape or len(shape) != 4:
         raise SpecVerifyError("k_cache and v_cache must be [pages][page_size][kv_heads][head_dim] "
                               "of one type")
-    P, ps, H, D = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if k3 != 1 or v3 != 1:
         raise SpecVerifyError("the caches' head dimension must be contiguous")
-    dev = k_cache.device
-    _ints(kv_len, None, "kv_len", dev)
+    P, ps, H, D = shape
     B = kv_len.numel()
-    _ints(kv_len, (B,), "kv_len", dev)
-    _ints(q_start, (B + 1,), "q_start", dev)
-    _ints(pages, None, "pages", dev)
-    if pages.dim() != 2 or pages.shape[0] != B or (pages.shape[1] > 1 and pages.stride(1) != 1):
-        raise SpecVerifyError(f"pages: expected [{B}][max_pages] rows, got {tuple(pages.shape)}")
-    wide = pages.shape[1]
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _Stride3(*ks[:3]), _Stride3(*vs[:3]),
-                       P, ps, H, D, dt, B, N, wide, pages.data_ptr(),
-                       pages.stride(0) if B > 1 else wide, q_start.data_ptr(), kv_len.data_ptr())
+    _ints(kv_len, B, "kv_len", dev)
+    _ints(q_start, B + 1, "q_start", dev)
+    if pages.dtype is not _INT32 or pages.get_device() != dev:
+        raise SpecVerifyError(f"pages must be torch.int32 on cuda:{dev}, got {pages.dtype} on "
+                              f"{pages.device}")
+    table = pages.shape
+    if len(table) != 2 or table[0] != B or (table[1] > 1 and pages.stride(1) != 1):
+        raise SpecVerifyError(f"pages: expected [{B}][max_pages] rows, got {tuple(table)}")
+    wide = table[1]
+    return _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, P, ps, H, D,
+                       code, B, N, wide, pages.data_ptr(), pages.stride(0) if B > 1 else wide,
+                       q_start.data_ptr(), kv_len.data_ptr()), dtype, dev, H, D
 
 
 def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, q=None,
@@ -642,37 +659,34 @@ def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, 
     [rot_dim / 2] f64 gives radians per position of each pair (None: no
     rotation); pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) when
     interleaved.  positions [N] int32 overrides the slots as positions."""
-    torch = _torch()
     N = k.shape[0]
-    c = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
-    dev, D = k_cache.device, c.head_dim
-    kst = _heads3(k, k_cache, c.kv_heads, D, N, "k")
-    vst = _heads3(v, k_cache, c.kv_heads, D, N, "v")
-    rot = 0
+    c, dtype, dev, H, D = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
+    kst = _heads3(k, dtype, dev, H, D, N, "k")
+    vst = _heads3(v, dtype, dev, H, D, N, "v")
+    rot = fp = pp = heads = qp = op = 0
+    qst = ost = None
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1 or \
-                not inv_freq.is_contiguous():
-            raise SpecVerifyError(f"inv_freq must be a contiguous float64 vector on {dev}")
-        rot = 2 * inv_freq.shape[0]
+        if inv_freq.dtype is not _torch().float64 or inv_freq.get_device() != dev or \
+                inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise SpecVerifyError(f"inv_freq must be a contiguous float64 vector on cuda:{dev}")
+        rot, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
     if positions is not None:
-        _ints(positions, (N,), "positions", dev)
-    heads, qp, qst, op, ost = 0, 0, None, 0, None
+        _ints(positions, N, "positions", dev)
+        pp = positions.data_ptr()
     if q is not None:
-        qst = _heads3(q, k_cache, None, D, N, "q")
-        heads = q.shape[1]
+        heads = q.shape[1] if q.dim() == 3 else 0
+        qst = _heads3(q, dtype, dev, heads, D, N, "q")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        ost = _heads3(q_out, k_cache, heads, D, N, "q_out")
+            q_out = _torch().empty_like(q)
+        ost = _heads3(q_out, dtype, dev, heads, D, N, "q_out")
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise SpecVerifyError("q_out without q")
     raw = _raw_stream(dev, stream)
     w = _cache_ws(ws, dev, raw, stream)
-    rc = load().sv_append_kv(c, k.data_ptr(), kst, v.data_ptr(), vst, qp, qst, op, ost, heads,
-                             0 if inv_freq is None else inv_freq.data_ptr(), rot,
-                             1 if interleaved else 0,
-                             0 if positions is None else positions.data_ptr(), w.ptr, w.nbytes,
-                             raw)
+    rc = (_lib or load()).sv_append_kv(c, k.data_ptr(), kst, v.data_ptr(), vst, qp, qst, op, ost,
+                                       heads, fp, rot, 1 if interleaved else 0, pp, w.ptr,
+                                       w.nbytes, raw)
     if rc:
         _check(rc, "sv_append_kv")
     return q_out
@@ -685,20 +699,18 @@ def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, 
     window > 0, scale 1 / sqrt(D) by default; q_heads a multiple of kv_heads.
     Arrays as for append_kv.  Rows that see nothing are zeros.  Returns out
     [N][q_heads][D]."""
-    torch = _torch()
     N = q.shape[0]
-    c = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
-    D = c.head_dim
-    qst = _heads3(q, k_cache, None, D, N, "q")
-    heads = q.shape[1]
+    c, dtype, dev, _, D = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
+    heads = q.shape[1] if q.dim() == 3 else 0
+    qst = _heads3(q, dtype, dev, heads, D, N, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ost = _heads3(out, k_cache, heads, D, N, "out")
-    raw = _raw_stream(q.device, stream)
-    w = _cache_ws(ws, q.device, raw, stream)
-    rc = load().sv_paged_attention(c, q.data_ptr(), qst, out.data_ptr(), ost, heads,
-                                   D ** -0.5 if scale is None else scale, window, w.ptr, w.nbytes,
-                                   raw)
+        out = _torch().empty_like(q)
+    ost = _heads3(out, dtype, dev, heads, D, N, "out")
+    raw = _raw_stream(dev, stream)
+    w = _cache_ws(ws, dev, raw, stream)
+    rc = (_lib or load()).sv_paged_attention(c, q.data_ptr(), qst, out.data_ptr(), ost, heads,
+                                             D ** -0.5 if scale is None else scale, window, w.ptr,
+                                             w.nbytes, raw)
     if rc:
         _check(rc, "sv_paged_attention")
     return out
@@ -707,8 +719,9 @@ def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, 
 def _per_row(x, R, name, dtype, device):
     if x is None:
         return 0
-    if x.dtype != dtype or x.device != device or x.numel() != R or not x.is_contiguous():
-        raise SpecVerifyError(f"{name}: expected {R} contiguous {dtype} on {device}")
+    if x.dtype is not dtype or x.get_device() != device or x.numel() != R or \
+            not x.is_contiguous():
+        raise SpecVerifyError(f"{name}: expected {R} contiguous {dtype} on cuda:{device}")
     return x.data_ptr()
 
 
@@ -724,40 +737,42 @@ def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=No
     torch = _torch()
     if not z.is_cuda:
         raise SpecVerifyError("z must be a CUDA tensor")
-    dt = 0 if z.dtype == torch.float32 else _cache_dtype(z.dtype, "z (or torch.float32)")
-    lead, dev = z.shape[:-1], z.device
-    V = z.shape[-1]
-    z2 = z if z.dim() == 2 else z.reshape(1, V) if z.dim() == 1 else z.view(-1, V)
-    if z2.stride(1) != 1 and V > 1:
+    f32 = torch.float32
+    dt = 0 if z.dtype is f32 else _cache_dtype(z.dtype, "z (or torch.float32)")
+    shape, dev = z.shape, z.get_device()
+    V, lead = shape[-1], shape[:-1]
+    z2 = z if len(shape) == 2 else z.reshape(1, V) if len(shape) == 1 else z.view(-1, V)
+    row, one = z2.stride()
+    if one != 1 and V > 1:
         raise SpecVerifyError("z: the vocabulary dimension must be contiguous")
     R = z2.shape[0]
     up = _per_row(u, R, "u", torch.float64, dev)
-    tp = _per_row(temperature, R, "temperature", torch.float32, dev)
+    tp = _per_row(temperature, R, "temperature", f32, dev)
     kp = _per_row(top_k, R, "top_k", torch.int32, dev)
-    pp = _per_row(top_p, R, "top_p", torch.float32, dev)
-    mp = _per_row(min_p, R, "min_p", torch.float32, dev)
+    pp = _per_row(top_p, R, "top_p", f32, dev)
+    mp = _per_row(min_p, R, "min_p", f32, dev)
+    tok = out = 0
     if u is not None:
         if token_out is None:
-            token_out = torch.empty(lead, dtype=torch.int32, device=dev)
+            token_out = torch.empty(lead, dtype=torch.int32, device=z.device)
         else:
             _per_row(token_out, R, "token_out", torch.int32, dev)
+        tok = token_out.data_ptr()
     elif token_out is not None:
         raise SpecVerifyError("token_out without u")
-    pst = V
     if probs or probs_out is not None:
         if probs_out is None:
-            probs_out = torch.empty(z.shape, dtype=torch.float32, device=dev)
-        elif probs_out.dtype != torch.float32 or probs_out.device != dev or \
-                probs_out.shape != z.shape or not probs_out.is_contiguous():
-            raise SpecVerifyError(f"probs_out: expected {tuple(z.shape)} contiguous f32 on {dev}")
-    if token_out is None and probs_out is None:
+            probs_out = torch.empty(shape, dtype=f32, device=z.device)
+        elif probs_out.dtype is not f32 or probs_out.get_device() != dev or \
+                probs_out.shape != shape or not probs_out.is_contiguous():
+            raise SpecVerifyError(f"probs_out: expected {tuple(shape)} contiguous f32 on cuda:{dev}")
+        out = probs_out.data_ptr()
+    if not tok and not out and R > 0:
         raise SpecVerifyError("nothing to compute: give u, or ask for probs")
     raw = _raw_stream(dev, stream)
     w = _cache_ws(ws, dev, raw, stream)
-    rc = load().sv_warp_sample(z2.data_ptr(), z2.stride(0) if R > 1 else V, dt, R, V, tp, kp, pp,
-                               mp, up, 0 if token_out is None else token_out.data_ptr(),
-                               0 if probs_out is None else probs_out.data_ptr(), pst, w.ptr,
-                               w.nbytes, raw)
+    rc = (_lib or load()).sv_warp_sample(z2.data_ptr(), row if R > 1 else V, dt, R, V, tp, kp, pp,
+                                         mp, up, tok, out, V, w.ptr, w.nbytes, raw)
     if rc:
         _check(rc, "sv_warp_sample")
     return token_out, probs_out

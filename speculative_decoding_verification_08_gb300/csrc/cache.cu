@@ -14,6 +14,8 @@
 
 namespace {
 
+constexpr int kSms = 152;
+
 using svhost::g_last_grid;
 using svhost::g_last_kernels;
 using svhost::kAlign;
@@ -71,25 +73,39 @@ int bind_cache(const sv_paged_cache *c, void *ws, size_t ws_bytes, sv::Batch &b)
 }
 
 template <class T, int kVec>
-void launch_append(const sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
-                   cudaStream_t st) {
-    if (interleaved)
-        sv::append_kernel<T, kVec, true><<<grid, sv::kAppendThreads, 0, st>>>(A, per_block);
-    else
-        sv::append_kernel<T, kVec, false><<<grid, sv::kAppendThreads, 0, st>>>(A, per_block);
+int launch_append(sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
+                  cudaStream_t st) {
+    const int turned = A.rot_dim / 2 / kVec + (A.head_dim - A.rot_dim) / kVec;
+    const int per_value = A.head_dim / kVec;
+    // as many threads as share a token's items evenly
+    const int items = (A.q_heads + A.kv_heads) * turned + A.kv_heads * per_value;
+    const int rounds = (items + sv::kAppendThreads - 1) / sv::kAppendThreads;
+    const int threads = std::max(32, ((items + rounds - 1) / rounds + 31) / 32 * 32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg,
+                              interleaved ? sv::append_kernel<T, kVec, true>
+                                          : sv::append_kernel<T, kVec, false>,
+                              A, per_block) == cudaSuccess
+               ? SV_OK
+               : SV_ECUDA;
 }
 
 template <class T>
-void launch_append(const sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
-                   cudaStream_t st) {
+int launch_append(sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
+                  cudaStream_t st) {
     // both halves of a rotated pair start on a pack: 16, 8 or 4 bytes
     const int half = A.rot_dim / 2;
-    if (half % 8 == 0)
-        launch_append<T, 8>(A, interleaved, grid, per_block, st);
-    else if (half % 4 == 0)
-        launch_append<T, 4>(A, interleaved, grid, per_block, st);
-    else
-        launch_append<T, 2>(A, interleaved, grid, per_block, st);
+    if (half % 8 == 0) return launch_append<T, 8>(A, interleaved, grid, per_block, st);
+    if (half % 4 == 0) return launch_append<T, 4>(A, interleaved, grid, per_block, st);
+    return launch_append<T, 2>(A, interleaved, grid, per_block, st);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -220,7 +236,8 @@ int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_st
     int rc = check_cache(cache);
     if (rc != SV_OK) return rc;
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 4 != 0 || (rot_dim > 0 && !inv_freq) ||
-        q_heads < 0 || (q == nullptr) != (q_heads == 0))
+        q_heads < 0 || q_heads > (1 << 16) || cache->kv_heads > (1 << 16) ||
+        (q == nullptr) != (q_heads == 0))
         return SV_EINVAL;
     if (cache->B == 0 || cache->tokens == 0) return SV_OK;
     if (!k || !v || !k_stride || !v_stride || !vec_ok(k, k_stride, 2) || !vec_ok(v, v_stride, 2))
@@ -252,19 +269,21 @@ int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_st
         A.vc_st[i] = cache->v_stride[i];
     }
     A.inv_freq = inv_freq;
+    A.by_page.set((uint32_t)cache->page_size);
     A.positions = positions;
     A.q_heads = q_heads;
     A.kv_heads = cache->kv_heads;
     A.head_dim = cache->head_dim;
     A.rot_dim = rot_dim;
-    const int per_block = cache->tokens >= 16384 ? sv::kAppendTokens : 1;
+    // tokens per block: one wave of eight blocks to an SM where that suffices
+    const int per_block = (int)std::min<int64_t>(
+        sv::kAppendTokens, std::max<int64_t>(1, ((int64_t)cache->tokens + kSms * 8 - 1) / (kSms * 8)));
     const unsigned grid = (unsigned)((cache->tokens + per_block - 1) / per_block);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cache->dtype == SV_BF16)
-        launch_append<__nv_bfloat16>(A, interleaved != 0, grid, per_block, st);
-    else
-        launch_append<__half>(A, interleaved != 0, grid, per_block, st);
-    if (cudaGetLastError() != cudaSuccess) return SV_ECUDA;
+    rc = cache->dtype == SV_BF16
+             ? launch_append<__nv_bfloat16>(A, interleaved != 0, grid, per_block, st)
+             : launch_append<__half>(A, interleaved != 0, grid, per_block, st);
+    if (rc != SV_OK) return rc;
     g_last_grid = grid;
     g_last_kernels = 1;
     return SV_OK;

@@ -8,22 +8,25 @@
 // position of 2^20 would leave an angle error of 0.06).
 //
 // Bound by memory: every value is read once and written once and the
-// arithmetic is a few operations each.  A block takes kAppendTokens tokens (or
-// one, when there are few): a warp per token finds its sequence (32-way
-// search of q_start), slot, page and its rot_dim / 2 cosines and sines, then
-// all threads stream the tokens' heads with 16-byte accesses.
+// arithmetic is a few operations each.  A block takes up to kAppendTokens
+// tokens: a warp per token finds its sequence (32-way search of q_start), slot,
+// page and its rot_dim / 2 cosines and sines, while every thread's first loads
+// are on their way; then the threads, a pair of packs of a rotated head (or one
+// pack of what is copied) to each, go through the tokens.
 #pragma once
 
+#include "sv_barrier.cuh"
 #include "sv_cache.cuh"
 
 namespace sv {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 8;
+constexpr int kAppendTokens = 4;
 constexpr int kMaxHeadDim = 128;
 
 struct AppendParams {
     Batch batch;
+    FastDiv by_page;
     const void *k, *v, *q;
     void *q_out, *k_cache, *v_cache;
     int64_t k_st[2], v_st[2], q_st[2], o_st[2];  // token and head strides, elements
@@ -51,88 +54,114 @@ __device__ __forceinline__ int32_t find_sequence(const int32_t *q_start, int32_t
 
 template <int N>
 struct alignas(2 * N) Pack {
-    uint16_t x[N];
+    uint32_t x[N / 2];  // two values each
 };
 
-template <class T>
-__device__ __forceinline__ float f32_of(uint16_t x) {
-    T y;
-    *reinterpret_cast<uint16_t *>(&y) = x;
-    return to_f32<T>(y);
+__device__ __forceinline__ float2 pair_of(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_of(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ uint32_t bits_of(float lo, float hi, __nv_bfloat16) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
+__device__ __forceinline__ uint32_t bits_of(float lo, float hi, __half) {
+    const __half2 y = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&y);
 }
 
-template <class T>
-__device__ __forceinline__ uint16_t bits_of(float x) {
-    const T y = from_f32<T>(x);
-    return *reinterpret_cast<const uint16_t *>(&y);
-}
-
-// One head's work item i: a pair of packs of the rotated part, or one pack of
-// the rest.  kVec values per pack.
+// Turns a pair of packs.  cs: cosines and sines of pairs 2 e and 2 e + 1 of the
+// item, `step` apart (so that neighbouring items' lie side by side).
 template <class T, int kVec, bool kInterleaved>
-__device__ __forceinline__ void rotate_item(const uint16_t *src, uint16_t *dst, int i, int half,
-                                            const float2 *cs) {
-    typedef Pack<kVec> P;
-    const int pairs = half / kVec;
-    if (i < pairs) {
-        P a, c;
-        int ia, ic;
-        if (kInterleaved) {
-            ia = 2 * i * kVec;
-            ic = ia + kVec;
-        } else {
-            ia = i * kVec;
-            ic = ia + half;
-        }
-        a = *reinterpret_cast<const P *>(src + ia);
-        c = *reinterpret_cast<const P *>(src + ic);
-        const float2 *t = cs + i * kVec;
-        if (kInterleaved) {
+__device__ __forceinline__ void turn(Pack<kVec> &a, Pack<kVec> &c, const float4 *cs, int step) {
+    if (kInterleaved) {
 #pragma unroll
-            for (int e = 0; e < kVec; e += 2) {
-                const float2 u = t[e / 2], w = t[(kVec + e) / 2];
-                const float a0 = f32_of<T>(a.x[e]), a1 = f32_of<T>(a.x[e + 1]);
-                a.x[e] = bits_of<T>(a0 * u.x - a1 * u.y);
-                a.x[e + 1] = bits_of<T>(a0 * u.y + a1 * u.x);
-                const float c0 = f32_of<T>(c.x[e]), c1 = f32_of<T>(c.x[e + 1]);
-                c.x[e] = bits_of<T>(c0 * w.x - c1 * w.y);
-                c.x[e + 1] = bits_of<T>(c0 * w.y + c1 * w.x);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const float2 u = t[e];
-                const float x = f32_of<T>(a.x[e]), y = f32_of<T>(c.x[e]);
-                a.x[e] = bits_of<T>(x * u.x - y * u.y);
-                c.x[e] = bits_of<T>(x * u.y + y * u.x);
-            }
+        for (int e = 0; e < kVec / 2; ++e) {   // pair e of a, pair kVec / 2 + e of c
+            const float2 x = pair_of(a.x[e], T()), y = pair_of(c.x[e], T());
+            const float4 p = cs[e / 2 * step], q = cs[(kVec / 2 + e) / 2 * step];
+            const float2 u = e % 2 ? make_float2(p.z, p.w) : make_float2(p.x, p.y);
+            const float2 w = (kVec / 2 + e) % 2 ? make_float2(q.z, q.w) : make_float2(q.x, q.y);
+            a.x[e] = bits_of(x.x * u.x - x.y * u.y, x.x * u.y + x.y * u.x, T());
+            c.x[e] = bits_of(y.x * w.x - y.y * w.y, y.x * w.y + y.y * w.x, T());
         }
-        *reinterpret_cast<P *>(dst + ia) = a;
-        *reinterpret_cast<P *>(dst + ic) = c;
     } else {
-        const int at = 2 * half + (i - pairs) * kVec;
-        *reinterpret_cast<P *>(dst + at) = *reinterpret_cast<const P *>(src + at);
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e) {   // pairs 2 e and 2 e + 1
+            const float2 x = pair_of(a.x[e], T()), y = pair_of(c.x[e], T());
+            const float4 u = cs[e * step];
+            a.x[e] = bits_of(x.x * u.x - y.x * u.y, x.y * u.z - y.y * u.w, T());
+            c.x[e] = bits_of(x.x * u.y + y.x * u.x, x.y * u.w + y.y * u.z, T());
+        }
     }
 }
 
+// Where a block's token goes: offsets into q_out, the key and the value cache;
+// -1: nowhere.
 struct TokenPlace {
-    int32_t token;      // -1: no sequence takes this row
-    int32_t page, at;   // page -1: not written to the cache
+    int64_t to[3];
 };
 
 template <class T, int kVec, bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 6)
     append_kernel(const __grid_constant__ AppendParams A, int per_block) {
     __shared__ TokenPlace place[kAppendTokens];
-    __shared__ float2 cs[kAppendTokens][kMaxHeadDim / 2];
+    __shared__ float4 cs[kAppendTokens][kMaxHeadDim / 4];
+    typedef Pack<kVec> P;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int32_t t0 = (int32_t)blockIdx.x * per_block;
     const int here = min(per_block, A.batch.tokens - t0);
     const int half = A.rot_dim / 2;
+    const int pairs = half / kVec;
+    const int turned = pairs + (A.head_dim - A.rot_dim) / kVec;  // items of a rotated head
+    const int per_value = A.head_dim / kVec;
+    const int rot_items = (A.q_heads + A.kv_heads) * turned;
+    const int items = rot_items + A.kv_heads * per_value;
 
-    for (int w = warp; w < here; w += kAppendThreads / 32) {
+    // item i of a token: a pair of packs of a head's rotated part, or one pack of
+    // what is copied (its rest, or a value)
+    int kind, second, x;   // kind 0 query, 1 key, 2 value
+    int64_t step;
+    const uint16_t *src;
+    uint16_t *dst;
+    P a, c, a1, c1;
+    auto fetch = [&](int i) {
+        int head, at;
+        second = 0;
+        if (i < rot_items) {
+            head = i / turned;
+            x = i - head * turned;
+            kind = head < A.q_heads ? 0 : 1;
+            if (kind) head -= A.q_heads;
+            if (x < pairs) {
+                at = kInterleaved ? 2 * x * kVec : x * kVec;
+                second = kInterleaved ? kVec : half;
+            } else {
+                at = A.rot_dim + (x - pairs) * kVec;
+            }
+        } else {
+            x = i - rot_items;
+            kind = 2;
+            head = x / per_value;
+            at = (x - head * per_value) * kVec;
+        }
+        const int64_t *st = kind == 0 ? A.q_st : kind == 1 ? A.k_st : A.v_st;
+        step = st[0];
+        src = static_cast<const uint16_t *>(kind == 0 ? A.q : kind == 1 ? A.k : A.v) + t0 * step +
+              head * st[1] + at;
+        dst = static_cast<uint16_t *>(kind == 0 ? A.q_out : kind == 1 ? A.k_cache : A.v_cache) +
+              head * (kind == 0 ? A.o_st[1] : kind == 1 ? A.kc_st[2] : A.vc_st[2]) + at;
+        a = *reinterpret_cast<const P *>(src);
+        if (second) c = *reinterpret_cast<const P *>(src + second);
+    };
+
+    wait_for_primary_grid();
+    // the first loads are on their way while the tokens' places are found
+    if ((int)threadIdx.x < items) fetch(threadIdx.x);
+    for (int w = warp; w < here; w += (int)blockDim.x / 32) {
         const int32_t t = t0 + w;
-        TokenPlace p = {-1, -1, 0};
+        TokenPlace p = {{-1, -1, -1}};
         int64_t pos = 0;
         const int32_t b = find_sequence(A.batch.q_start, A.batch.B, t, lane);
         if (b >= 0) {
@@ -141,68 +170,57 @@ __global__ void __launch_bounds__(kAppendThreads)
             if (s.bad) {
                 if (lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_LENGTH);
             } else if (j >= 0 && j < s.n) {
-                p.token = t;
+                p.to[0] = t * A.o_st[0];
                 const int64_t slot = (int64_t)s.len - s.n + j;
                 pos = A.positions ? (int64_t)__ldg(A.positions + t) : slot;
                 if (slot < 0) {
                     if (lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_LENGTH);
                 } else {
-                    const int32_t pg = (int32_t)slot / A.batch.page_size;
+                    const int32_t pg = A.by_page.div((int)slot);
                     const int32_t id = __ldg(A.batch.pages + b * A.batch.pages_stride + pg);
                     if (id < 0 || id >= A.batch.num_pages) {
                         if (lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_PAGE);
                     } else {
-                        p.page = id;
-                        p.at = (int32_t)slot - pg * A.batch.page_size;
+                        const int64_t in = (int32_t)slot - pg * A.batch.page_size;
+                        p.to[1] = id * A.kc_st[0] + in * A.kc_st[1];
+                        p.to[2] = id * A.vc_st[0] + in * A.vc_st[1];
                     }
                 }
             }
         }
         if (lane == 0) place[w] = p;
-        if (p.token >= 0)
-            for (int i = lane; i < half; i += 32) {
-                const double turns = (double)pos * __ldg(A.inv_freq + i) * 0.15915494309189535;
-                float s, c;
-                sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-                cs[w][i] = make_float2(c, s);
+        if (p.to[0] >= 0)
+            for (int e = lane; e < half; e += 32) {
+                const double turns = (double)pos * __ldg(A.inv_freq + e) * 0.15915494309189535;
+                float s, co;
+                sincospif((float)(2.0 * (turns - rint(turns))), &s, &co);
+                // pair e: item e / kVec's, its e % kVec
+                float2 *to = reinterpret_cast<float2 *>(&cs[w][e % kVec / 2 * pairs + e / kVec]);
+                to[e % 2] = make_float2(co, s);
             }
     }
     __syncthreads();
 
-    const uint16_t *q = static_cast<const uint16_t *>(A.q);
-    const uint16_t *k = static_cast<const uint16_t *>(A.k);
-    const uint16_t *v = static_cast<const uint16_t *>(A.v);
-    const int turned = half / kVec + (A.head_dim - A.rot_dim) / kVec;  // items per rotated head
-    const int per_head_v = A.head_dim / 8;
-    const int rot_items = (A.q_heads + A.kv_heads) * turned;
-    const int items = rot_items + A.kv_heads * per_head_v;
-    for (int w = 0; w < here; ++w) {
-        const TokenPlace p = place[w];
-        if (p.token < 0) continue;
-        const int64_t t = p.token;
-        for (int i = threadIdx.x; i < items; i += kAppendThreads) {
-            if (i < rot_items) {
-                const int h = i / turned, x = i - h * turned;
-                if (h < A.q_heads) {
-                    rotate_item<T, kVec, kInterleaved>(
-                        q + t * A.q_st[0] + h * A.q_st[1],
-                        static_cast<uint16_t *>(A.q_out) + t * A.o_st[0] + h * A.o_st[1], x, half,
-                        cs[w]);
-                } else if (p.page >= 0) {
-                    const int g = h - A.q_heads;
-                    rotate_item<T, kVec, kInterleaved>(
-                        k + t * A.k_st[0] + g * A.k_st[1],
-                        static_cast<uint16_t *>(A.k_cache) + p.page * A.kc_st[0] +
-                            p.at * A.kc_st[1] + g * A.kc_st[2],
-                        x, half, cs[w]);
-                }
-            } else if (p.page >= 0) {
-                const int r = i - rot_items, g = r / per_head_v, x = (r - g * per_head_v) * 8;
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(A.v_cache) +
-                                           p.page * A.vc_st[0] + p.at * A.vc_st[1] +
-                                           g * A.vc_st[2] + x) =
-                    *reinterpret_cast<const uint4 *>(v + t * A.v_st[0] + g * A.v_st[1] + x);
+    for (int i = threadIdx.x; i < items; i += blockDim.x) {
+        if (i != (int)threadIdx.x) fetch(i);
+#pragma unroll 1
+        for (int w = 0; w < here; ++w) {
+            const bool more = w + 1 < here;
+            src += step;
+            if (more) {
+                a1 = *reinterpret_cast<const P *>(src);
+                if (second) c1 = *reinterpret_cast<const P *>(src + second);
             }
+            const int64_t to = place[w].to[kind];
+            if (to >= 0) {
+                if (second) {
+                    turn<T, kVec, kInterleaved>(a, c, &cs[w][x], pairs);
+                    *reinterpret_cast<P *>(dst + to + second) = c;
+                }
+                *reinterpret_cast<P *>(dst + to) = a;
+            }
+            a = a1;
+            c = c1;
         }
     }
 }

@@ -67,22 +67,6 @@ constexpr size_t kAttendOut = kAttendStats + (size_t)kAttendMaxCtas * 2 * 2 * kR
 constexpr size_t kAttendWorkspace =
     kAttendOut + (size_t)kAttendMaxCtas * 2 * (kMaxHeadDim / 4) * 2 * kRows * sizeof(float4);
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1: the high word of n m, shifted;
-// m = ceil(2^(31 + s) / d) with 2^s >= d, whose excess over the exact factor
-// is too small to reach the next integer for these n.
-struct FastDiv {
-    uint32_t d, m, s;
-    __host__ void set(uint32_t by) {
-        d = by;
-        s = 0;
-        while ((1ull << s) < by) ++s;
-        m = (uint32_t)(((1ull << (31 + s)) + by - 1) / by);
-    }
-    __device__ __forceinline__ int div(int n) const {
-        return d == 1 ? n : (int)(__umulhi((uint32_t)n, m) >> (s - 1));
-    }
-};
-
 struct AttendParams {
     Batch batch;
     FastDiv by_group, by_page;

@@ -11,6 +11,22 @@
 
 namespace sv {
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: the high word of n m, shifted;
+// m = ceil(2^(31 + s) / d) with 2^s >= d, whose excess over the exact factor
+// is too small to reach the next integer for these n.
+struct FastDiv {
+    uint32_t d, m, s;
+    __host__ void set(uint32_t by) {
+        d = by;
+        s = 0;
+        while ((1ull << s) < by) ++s;
+        m = (uint32_t)(((1ull << (31 + s)) + by - 1) / by);
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return d == 1 ? n : (int)(__umulhi((uint32_t)n, m) >> (s - 1));
+    }
+};
+
 struct Batch {
     const int32_t *pages;
     int64_t pages_stride;

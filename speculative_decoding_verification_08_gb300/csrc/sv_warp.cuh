@@ -30,14 +30,13 @@
 
 namespace sv {
 
-constexpr int kWarpThreads = 256;
-constexpr int kWarpWarps = kWarpThreads / 32;
+constexpr int kMaxWarps = 32;
 constexpr int kWarpMaxCluster = 8;
 constexpr int kBins = 1024;            // of a histogram of counts and masses; of one alone twice as many
 constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
 constexpr float kColdest = 1e-36f, kHottest = 1e36f;  // temperatures
 constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
-constexpr int kLocalList = 192;        // border elements one CTA may gather
+constexpr int kLocalList = 160;        // border elements one CTA may gather
 constexpr int kList = 1024;            // and the row
 constexpr int kShared = 512;           // of them, ranked by the whole cluster
 
@@ -239,11 +238,13 @@ struct alignas(16) WarpShared {
     RowSlice slice;
     dd2 slice_mass[3];              // kept, above, all below t_goal
     dd2 rank_mass[kWarpMaxCluster]; // what stays of every rank's slice
-    dd2 run_mass[kWarpWarps];       // kept mass of each warp's run
-    dd2 part_mass[kWarpWarps], in_mass[kWarpWarps];
-    uint64_t warp_key[kWarpWarps];
-    float warp_f[2][kWarpWarps];
-    uint32_t warp_u[kWarpWarps];
+    dd2 run_mass[kMaxWarps];       // kept mass of each warp's run
+    dd2 part_mass[kMaxWarps];
+    union {
+        dd2 in_mass[kMaxWarps];
+        uint64_t warp_key[kMaxWarps];
+        float warp_f[2][kMaxWarps];
+    };
     uint64_t list[kLocalList];
     union {
         alignas(16) uint32_t hist[2 * kBins];  // counts or masses; or counts, then masses
@@ -376,7 +377,7 @@ __device__ __noinline__ uint64_t first_of_row(WarpShared &sh) {
     const RowSlice &c = sh.slice;
     uint64_t first = 0;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < c.n; e += kWarpThreads) {
+    for (int e = threadIdx.x; e < c.n; e += blockDim.x) {
         const float x = slice_elem<T>(c, e);
         if (x == c.S.m) {
             const uint64_t key = composite(x, c.base + e);
@@ -394,7 +395,7 @@ __device__ __noinline__ uint64_t first_of_row(WarpShared &sh) {
 #pragma unroll 1
     for (int r = 0; r < (int)cluster.num_blocks(); ++r)
 #pragma unroll 1
-        for (int w = 0; w < kWarpWarps; ++w) {
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
             const uint64_t o = cluster.map_shared_rank(&sh, r)->warp_key[w];
             first = o > first ? o : first;
         }
@@ -409,7 +410,7 @@ __device__ __noinline__ dd2 sum_from(WarpShared &sh, uint64_t from, bool masses)
     const RowSlice &c = sh.slice;
     Mass a;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < c.n; e += kWarpThreads) {
+    for (int e = threadIdx.x; e < c.n; e += blockDim.x) {
         const float x = slice_elem<T>(c, e);
         if (x > -INFINITY && composite(x, c.base + e) >= from)
             a.add(masses ? weight_of(x, c.S, &sh.tab) : make_float2(1.f, 0.f));
@@ -423,7 +424,7 @@ __device__ __noinline__ dd2 sum_from(WarpShared &sh, uint64_t from, bool masses)
 #pragma unroll 1
     for (int r = 0; r < (int)cluster.num_blocks(); ++r)
 #pragma unroll 1
-        for (int w = 0; w < kWarpWarps; ++w)
+        for (int w = 0; w < (int)blockDim.x / 32; ++w)
             s = add_dd(s, cluster.map_shared_rank(&sh, r)->part_mass[w]);
     return s;
 }
@@ -457,16 +458,17 @@ __device__ __noinline__ uint64_t bisect_row(WarpShared &sh, int64_t k, float p) 
 // Ranks the row's border in place, every CTA for itself: for lists too long for
 // the shared ranking.
 __device__ __noinline__ void rank_alone(WarpShared &sh, int got) {
-    uint64_t key[kList / kWarpThreads];
-    int at_of[kList / kWarpThreads];
-    const int mine = (got + kWarpThreads - 1) / kWarpThreads;   // elements per thread
+    constexpr int kMost = 4;   // elements per thread
+    const int n = (int)blockDim.x;
+    uint64_t key[kMost];
+    int at_of[kMost];
 #pragma unroll
-    for (int j = 0; j < kList / kWarpThreads; ++j) {
-        const int i = (int)threadIdx.x + j * kWarpThreads;
+    for (int j = 0; j < kMost; ++j) {
+        const int i = (int)threadIdx.x + j * n;
         key[j] = i < got ? sh.all[i] : 0;
         at_of[j] = 0;
     }
-    if (mine == 1) {
+    if (got <= n) {
         if ((int)threadIdx.x / 32 * 32 < got)
 #pragma unroll 8
             for (int x = 0; x < got; ++x) at_of[0] += sh.all[x] > key[0];
@@ -475,21 +477,22 @@ __device__ __noinline__ void rank_alone(WarpShared &sh, int got) {
         for (int x = 0; x < got; ++x) {
             const uint64_t o = sh.all[x];
 #pragma unroll
-            for (int j = 0; j < kList / kWarpThreads; ++j) at_of[j] += o > key[j];
+            for (int j = 0; j < kMost; ++j) at_of[j] += o > key[j];
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kList / kWarpThreads; ++j)
-        if ((int)threadIdx.x + j * kWarpThreads < got) sh.all[at_of[j]] = key[j];
+    for (int j = 0; j < kMost; ++j)
+        if ((int)threadIdx.x + j * n < got) sh.all[at_of[j]] = key[j];
     __syncthreads();
 }
 
 // kHeld: every slice fits in shared memory, in words padded with -inf to whole
 // rounds of the block, so that the sweeps need no bounds.
-template <class T, bool kHeld>
-__global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_constant__ WarpParams A) {
-    constexpr int E = WordOf<T>::kElems;
+// kThreads: 256, three CTAs to an SM, or 1024 for slices that fill one.
+template <class T, bool kHeld, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kernel(const __grid_constant__ WarpParams A) {
+    constexpr int E = WordOf<T>::kElems, kWarps = kThreads / 32;
     extern __shared__ __align__(16) char raw[];
     WarpShared &sh = *reinterpret_cast<WarpShared *>(raw);
     uint4 *words = reinterpret_cast<uint4 *>(raw + sizeof(WarpShared));
@@ -535,10 +538,10 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
     }
     // every warp takes a run of words, its lanes in turn
-    const int run = (W + kWarpThreads - 1) / kWarpThreads * 32;
+    const int run = (W + kThreads - 1) / kThreads * 32;
     if (kHeld)
 #pragma unroll 1
-        for (int w = W + tid; w < run * kWarpWarps; w += kWarpThreads)
+        for (int w = W + tid; w < run * kWarps; w += kThreads)
 #pragma unroll
             for (int i = 0; i < E; ++i) reinterpret_cast<T *>(words)[w * E + i] = minus_inf<T>();
     // the row's settings; what of them needs fp64 is one thread's work while
@@ -606,11 +609,11 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             sh.warp_f[1][warp] = low;
         }
 #pragma unroll 1
-        for (int i = tid; i < 2 * kBins; i += kWarpThreads) sh.hist[i] = 0;
+        for (int i = tid; i < 2 * kBins; i += kThreads) sh.hist[i] = 0;
         __syncthreads();
         if (warp == 0) {
-            top = lane < kWarpWarps ? sh.warp_f[0][lane] : -INFINITY;
-            low = lane < kWarpWarps ? sh.warp_f[1][lane] : INFINITY;
+            top = lane < kWarps ? sh.warp_f[0][lane] : -INFINITY;
+            low = lane < kWarps ? sh.warp_f[1][lane] : INFINITY;
 #pragma unroll 1
             for (int d = 16; d > 0; d >>= 1) {
                 top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         }
         if (out)
 #pragma unroll 1
-            for (int e = tid; e < n; e += kWarpThreads) out[e] = 0.f;
+            for (int e = tid; e < n; e += kThreads) out[e] = 0.f;
         cluster.sync();
         return;
     }
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         // sums of 32 groups of bins, a warp to a group
         const int group = bins / 32, per_lane = group / 32;
         const float inv_unit = 1.f / unit;
-        for (int g = warp; g < 32; g += kWarpWarps) {
+        for (int g = warp; g < 32; g += kWarps) {
             uint32_t c = 0;
             float y = 0.f;
 #pragma unroll
@@ -918,7 +921,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     __syncthreads();
     if (warp < (by_p ? 3 : 1)) {
         const dd2 *from = warp == 0 ? sh.run_mass : warp == 1 ? sh.part_mass : sh.in_mass;
-        const dd2 s = warp_sum_dd(lane < kWarpWarps ? from[lane] : dd2{0.f, 0.f});
+        const dd2 s = warp_sum_dd(lane < kWarps ? from[lane] : dd2{0.f, 0.f});
         if (lane == 0) {
             sh.slice_mass[warp] = s;
             if (warp == 0) sh.gathered = sh.count;
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     // (the histogram that the lists lie over has been read everywhere)
     if (!full)
 #pragma unroll 1
-        for (int s = warp; s < C; s += kWarpWarps) {
+        for (int s = warp; s < C; s += kWarps) {
             const int to = s > 0 ? sh.list_end[s - 1] : 0, cnt = sh.list_end[s] - to;
             const uint64_t *from = cluster.map_shared_rank(sh.list, s);
 #pragma unroll 1
@@ -985,7 +988,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             } else if (got > 128 && got <= kShared) {
                 // every rank places a share of them, eight threads to an element,
                 // in every rank's list
-                const int part = lane % 8, total_groups = kWarpThreads / 8 * C;
+                const int part = lane % 8, total_groups = kThreads / 8 * C;
 #pragma unroll 1
                 for (int i0 = 0; i0 < got; i0 += total_groups) {
                     const int i = i0 + (tid / 8) * C + rank;
@@ -1080,7 +1083,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         if (warp == 0 && lane < C) {
             dd2 s = {0.f, 0.f};
 #pragma unroll 1
-            for (int w = 0; w < kWarpWarps; ++w)
+            for (int w = 0; w < kWarps; ++w)
                 s = add_dd(s, cluster.map_shared_rank(&sh, lane)->run_mass[w]);
             sh.rank_mass[lane] = s;
         }
@@ -1095,7 +1098,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         float2 *weights = reinterpret_cast<float2 *>(border == sh.all ? sh.share.ranked : sh.share.raw);
         if (stored) {
 #pragma unroll 1
-            for (int i = tid; i < got; i += kWarpThreads)
+            for (int i = tid; i < got; i += kThreads)
                 weights[i] = border[i] >= thr ? weight_of(unordered((uint32_t)(border[i] >> 32)), S, &sh.tab)
                                               : make_float2(0.f, 0.f);
             __syncthreads();
@@ -1146,7 +1149,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
             const int holder = over ? __ffs(over) - 1 : 31 - __clz(some);
             if (holder == rank) {
                 if (rank > 0) at = shfl_dd(upto, rank - 1);
-                const dd2 mass = lane < kWarpWarps ? sh.run_mass[lane] : dd2{0.f, 0.f};
+                const dd2 mass = lane < kWarps ? sh.run_mass[lane] : dd2{0.f, 0.f};
                 const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
                 const unsigned runs = __ballot_sync(0xffffffffu, mass.h > 0.f);
                 const unsigned past = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
@@ -1192,7 +1195,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
     if (pick >= 0) {
         // the run once more: every warp a part of it, then its part's elements
         const int r0 = max(0, run * pick * E - shift), r1 = min(n, run * (pick + 1) * E - shift);
-        const int part = (r1 - r0 + kWarpThreads - 1) / kWarpThreads * 32;
+        const int part = (r1 - r0 + kThreads - 1) / kThreads * 32;
         const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
         auto mass_at = [&](int e, int end) -> float2 {   // of element e, if it stays
             if (e < end) {
@@ -1208,7 +1211,7 @@ __global__ void __launch_bounds__(kWarpThreads, 3) warp_kernel(const __grid_cons
         if (lane == 0) sh.part_mass[warp] = own;
         __syncthreads();
         if (warp == 0) {
-            const dd2 mass = lane < kWarpWarps ? sh.part_mass[lane] : dd2{0.f, 0.f};
+            const dd2 mass = lane < kWarps ? sh.part_mass[lane] : dd2{0.f, 0.f};
             const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
             const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
             const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include "specverify.h"
 #include "sv_host.cuh"
@@ -13,6 +14,8 @@ namespace {
 
 constexpr int kSms = 152;
 // 16-byte words of a slice that shared memory holds beside WarpShared
+constexpr int kThreads = 256;
+constexpr int kSharedWords = 4096 + 1;  // of slices that three CTAs on an SM may have
 constexpr int kMaxWords = (227 * 1024 - (int)sizeof(sv::WarpShared)) / 16;
 
 using svhost::kAlign;
@@ -38,27 +41,30 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
         c *= 2;
     A.slice = (int32_t)(((A.V + c - 1) / c + 15) / 16 * 16);
     const int per_word = 16 / (int)sizeof(T);
+    const bool wide = (int64_t)A.slice / per_word + 1 > kSharedWords;
+    const int threads = wide ? 1024 : kThreads;
     // words of a slice (one more where rows do not start on one), in whole rounds
     // of the block
-    const int words = (int)(((int64_t)A.slice / per_word + 1 + sv::kWarpThreads - 1) /
-                            sv::kWarpThreads * sv::kWarpThreads);
+    const int64_t words = ((int64_t)A.slice / per_word + 1 + threads - 1) / threads * threads;
     const bool held = words <= kMaxWords;
-    A.cached = std::min(words, kMaxWords);
+    A.cached = (int32_t)std::min<int64_t>(words, kMaxWords);
     const size_t bytes = sizeof(sv::WarpShared) + (size_t)A.cached * 16;
+    auto *kernel = !held ? sv::warp_kernel<T, false, 1024>
+                   : wide ? sv::warp_kernel<T, true, 1024>
+                          : sv::warp_kernel<T, true, kThreads>;
     static std::atomic<int> raised[64];
     if (!raised[dev].load()) {
         const int most = (int)(sizeof(sv::WarpShared) + (size_t)kMaxWords * 16);
-        if (cudaFuncSetAttribute(sv::warp_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 most) != cudaSuccess ||
-            cudaFuncSetAttribute(sv::warp_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 most) != cudaSuccess)
-            return SV_ECUDA;
+        for (auto *k : {sv::warp_kernel<T, false, 1024>, sv::warp_kernel<T, true, 1024>,
+                        sv::warp_kernel<T, true, kThreads>})
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+                return SV_ECUDA;
         raised[dev].store(1);
     }
     if ((int64_t)A.R * c > INT32_MAX) return SV_EINVAL;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(A.R * c));
-    cfg.blockDim = dim3(sv::kWarpThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -70,8 +76,7 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, held ? sv::warp_kernel<T, true> : sv::warp_kernel<T, false>, A) !=
-        cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kernel, A) != cudaSuccess)
         return SV_ECUDA;
     svhost::g_last_grid = (int64_t)A.R * c;
     svhost::g_last_kernels = 1;

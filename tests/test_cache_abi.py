@@ -1,6 +1,7 @@
 """Host-side refusals of the paged-cache and warp calls (no GPU needed: every
 call fails its checks, or is a no-op, before any CUDA work)."""
 import ctypes
+import struct
 
 import pytest
 
@@ -18,11 +19,13 @@ def cache(**kw):
              num_pages=4, page_size=16, kv_heads=2, head_dim=64, dtype=1, B=2, tokens=3, max_pages=2,
              pages=4096, pages_stride=2, q_start=4096, kv_len=4096)
     a.update(kw)
-    a["k_stride"], a["v_stride"] = sv._Stride3(*a["k_stride"]), sv._Stride3(*a["v_stride"])
-    return sv._PagedCache(*(a[n] for n, _ in sv._PagedCache._fields_))
+    flat = []
+    for x in a.values():
+        flat.extend(x if isinstance(x, tuple) else (x,))
+    return struct.pack("@QQ3q3q8iQqQQ", *flat)         # sv_paged_cache
 
 
-S2 = sv._Stride2(128, 64)
+S2 = struct.pack("@2q", 128, 64)
 WS, BIG = 1 << 20, 1 << 30
 
 
