@@ -94,6 +94,13 @@ struct AttendSmem {
 // ---------------------------------------------------------------------------
 // the split of the work
 
+// a / b for a, b >= 0: most quotients here are of small numbers, and a 64-bit
+// division costs hundreds of cycles.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // A tile's fixed cost (queries in, states joined, rows out) in key blocks.
 constexpr int kTileCost = 2;
 
@@ -174,12 +181,12 @@ struct Walker {
             skip -= __shfl_sync(0xffffffffu, inc, 31);
         }
         const int c = s.cost(A, t);
-        h = (int32_t)(skip / c);
+        h = (int32_t)quotient(skip, c);
         off = (int32_t)(skip - (int64_t)h * c);
     }
 
     __device__ __forceinline__ int32_t cta_of(int64_t u) const {
-        return (int32_t)(((u + 1) * ctas - 1) / total);
+        return (int32_t)quotient((u + 1) * ctas - 1, total);
     }
 
     __device__ __forceinline__ bool next(const AttendParams &A, Piece &p) {
@@ -453,7 +460,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     int64_t total = 0;
     for (int w = 0; w < kAttendThreads / 32; ++w) total += sh.sums[w];
     const int32_t ctas = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, total));
-    const int64_t u0 = (int64_t)blockIdx.x * total / ctas, u1 = ((int64_t)blockIdx.x + 1) * total / ctas;
+    const int64_t u0 = quotient((int64_t)blockIdx.x * total, ctas),
+                  u1 = quotient(((int64_t)blockIdx.x + 1) * total, ctas);
     const bool idle = total == 0 || (int32_t)blockIdx.x >= ctas || u0 >= u1;
     if (!idle) {
         int64_t base = 0;
@@ -967,9 +975,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
                 const float4 *part_out = reinterpret_cast<const float4 *>(A.workspace + kAttendOut);
                 part_stats[(slot * 2 + g) * kRows + gt] = make_float2(ref, sum);
-                __threadfence();
                 meet(sh, &sh.group_sync[g], group_turn, lane, status);
                 if (gt == 0) {
+                    __threadfence();   // the group's writes, after the meeting
                     uint32_t *c = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters) +
                                   2 * p.first + g;
                     const bool last = atomicAdd(c, 1u) == (uint32_t)p.parts - 1;
@@ -988,42 +996,60 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     auto slot_of = [&](int i) -> int { return (p.first + i) * 2 + (i == 0 ? 1 : 0); };
                     if (strip < strips) {
                         uint16_t *co = row_of(r);
+                        // kBatch parts' loads in flight; a part past the last
+                        // one is the last once more, with no weight
+                        constexpr int kBatch = 8;
                         float top = -INFINITY, all = 0.f;
-#pragma unroll 4
-                        for (int i = 0; i < p.parts; ++i)
-                            top = fmaxf(top, __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]).x);
-#pragma unroll 4
-                        for (int i = 0; i < p.parts; ++i) {
-                            const float2 x = __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]);
-                            all += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - top);
+#pragma unroll 1
+                        for (int i0 = 0; i0 < p.parts; i0 += kBatch) {
+                            float2 x[kBatch];
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i)
+                                x[i] = __ldcg(&part_stats[(slot_of(min(i0 + i, p.parts - 1)) * 2 + g) * kRows + r]);
+                            float m = top;
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) m = fmaxf(m, x[i].x);
+                            all *= top == -INFINITY ? 0.f : ex2(top - m);
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i)
+                                if (i0 + i < p.parts && x[i].x != -INFINITY) all += x[i].y * ex2(x[i].x - m);
+                            top = m;
                         }
                         const float norm = all > 0.f ? 1.f / all : 0.f;
-                        // 16 columns at a time, four parts' loads in flight
 #pragma unroll 1
                         for (int cc = c0 + share * wide; cc < c0 + (share + 1) * wide; cc += 16) {
                             const int quads = min(4, (c0 + (share + 1) * wide - cc) / 4);
                             float4 v[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                            for (int i = 0; i < p.parts; ++i) {
-                                const float m = __ldcg(&part_stats[(slot_of(i) * 2 + g) * kRows + r]).x;
-                                const float4 *at = part_out +
-                                                   ((int64_t)slot_of(i) * (kMaxHeadDim / 4) + cc / 4) * 256 +
-                                                   part_row + r;
-                                float4 a[4];
+#pragma unroll 1
+                            for (int i0 = 0; i0 < p.parts; i0 += kBatch / 2) {
+                                float m[kBatch / 2];
+                                float4 a[kBatch / 2][4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (e < quads) a[e] = __ldcg(at + e * 256);
-                                const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                                for (int i = 0; i < kBatch / 2; ++i) {
+                                    const int s = slot_of(min(i0 + i, p.parts - 1));
+                                    m[i] = __ldcg(&part_stats[(s * 2 + g) * kRows + r]).x;
+                                    const float4 *at = part_out +
+                                                       ((int64_t)s * (kMaxHeadDim / 4) + cc / 4) * 256 +
+                                                       part_row + r;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (e < quads) {
-                                        v[e].x += f * a[e].x;
-                                        v[e].y += f * a[e].y;
-                                        v[e].z += f * a[e].z;
-                                        v[e].w += f * a[e].w;
-                                    }
+                                    for (int e = 0; e < 4; ++e)
+                                        if (e < quads) a[i][e] = __ldcg(at + e * 256);
+                                }
+#pragma unroll
+                                for (int i = 0; i < kBatch / 2; ++i) {
+                                    const float f =
+                                        i0 + i >= p.parts || m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (e < quads) {
+                                            v[e].x = fmaf(f, a[i][e].x, v[e].x);
+                                            v[e].y = fmaf(f, a[i][e].y, v[e].y);
+                                            v[e].z = fmaf(f, a[i][e].z, v[e].z);
+                                            v[e].w = fmaf(f, a[i][e].w, v[e].w);
+                                        }
+                                }
                             }
                             if (r < rows) {
 #pragma unroll
