@@ -22,6 +22,7 @@
 #pragma once
 
 #include <cooperative_groups.h>
+#include <string.h>
 
 #include <type_traits>
 
@@ -36,6 +37,7 @@ constexpr int kBins = 1024;            // of a histogram of counts and masses; o
 constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
 constexpr float kColdest = 1e-36f, kHottest = 1e36f;  // temperatures
 constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
+constexpr int kPlainThreads = 256;
 constexpr int kLocalList = 160;        // border elements one CTA may gather
 constexpr int kList = 1024;            // and the row
 constexpr int kShared = 512;           // of them, ranked by the whole cluster
@@ -485,6 +487,93 @@ __device__ __noinline__ void rank_alone(WarpShared &sh, int got) {
     for (int j = 0; j < kMost; ++j)
         if ((int)threadIdx.x + j * n < got) sh.all[at_of[j]] = key[j];
     __syncthreads();
+}
+
+// The element of r0 .. r1 - 1 whose running mass, from `at` on, passes the goal;
+// or, where rounding lets none, the last with mass.  By the whole CTA; goal and
+// at are warp 0's.
+template <class T, int kThreads>
+__device__ __forceinline__ void draw_element(const RowSlice &c, const ExpTable &tab, dd2 *part_mass, uint64_t thr,
+                                             int r0, int r1, dd2 goal, dd2 at, int32_t *token) {
+    constexpr int kWarps = kThreads / 32;
+    const int warp = uniform((int)threadIdx.x / 32), lane = threadIdx.x % 32;
+    // every warp a part, its lanes in turn
+    const int part = (r1 - r0 + kThreads - 1) / kThreads * 32;
+    auto mass_of = [&](float x, int e) -> float2 {   // of element e, if it stays
+        return x > -INFINITY && composite(x, c.base + e) >= thr ? weight_of(x, c.S, &tab) : make_float2(0.f, 0.f);
+    };
+    {
+        const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
+        Mass a;
+#pragma unroll 1
+        for (int e = p0 + lane; e - lane < p1; e += 256) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = e + 32 * i < p1 ? slice_elem<T>(c, e + 32 * i) : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p0 + part > e - lane + 32 * i) a.add(mass_of(x[i], e + 32 * i));
+        }
+        __syncwarp();
+        const dd2 own = warp_sum_dd(a.value());
+        if (lane == 0) part_mass[warp] = own;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    // the first of 32 masses that passes the goal, and the mass before it
+    auto choose = [&](dd2 mass) -> int {
+        const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
+        const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
+        const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
+        const int q = over ? __ffs(over) - 1 : 31 - __clz(some);
+        if (q > 0) at = shfl_dd(reach, q - 1);
+        return q;
+    };
+    const int q = choose(lane < kWarps ? part_mass[lane] : dd2{0.f, 0.f});
+    // of that part the lane's stretch, then the stretch's elements
+    const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part), per = part / 32;
+    int l0 = min(q1, q0 + per * lane), l1 = min(q1, l0 + per);
+    Mass a;
+#pragma unroll 1
+    for (int i = 0; i < per; i += 4) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = l0 + i + j < l1 ? slice_elem<T>(c, l0 + i + j) : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a.add(mass_of(x[j], l0 + i + j));
+    }
+    __syncwarp();
+    const int l = choose(a.value());
+    l0 = __shfl_sync(0xffffffffu, l0, l);
+    l1 = __shfl_sync(0xffffffffu, l1, l);
+    int hit = -1, end = -1;
+#pragma unroll 1
+    for (int e = l0; e < l1 && hit < 0; e += 32) {
+        const float2 y = e + lane < l1 ? mass_of(slice_elem<T>(c, e + lane), e + lane) : make_float2(0.f, 0.f);
+        __syncwarp();
+        const dd2 upto = add_dd(at, warp_scan_dd({y.x, y.y}, lane));
+        const unsigned has = __ballot_sync(0xffffffffu, y.x > 0.f);
+        const unsigned past = __ballot_sync(0xffffffffu, y.x > 0.f && less_dd(goal, upto));
+        if (has) end = e + 31 - __clz(has);
+        if (past) hit = e + __ffs(past) - 1;
+        at = shfl_dd(upto, 31);
+    }
+    if (lane == 0) *token = (int32_t)(c.base + (hit >= 0 ? hit : end));
+}
+
+// Elements e0 .. of a row of probabilities, E of them, 16 bytes at a time where
+// that is aligned.
+template <int E>
+__device__ __forceinline__ void store_probs(float *out, int e0, int n, bool vec, const float (&y)[E]) {
+    if (vec && e0 >= 0 && e0 + E <= n) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4)
+            *reinterpret_cast<float4 *>(out + e0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (e0 + i >= 0 && e0 + i < n) out[e0 + i] = y[i];
+    }
 }
 
 // kHeld: every slice fits in shared memory, in words padded with -inf to whole
@@ -1179,62 +1268,249 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
                         y[i] = fast_weight(x[i], S) * inv;
             }
             const int e0 = w * E - shift;
-            if (vec && e0 >= 0 && e0 + E <= n) {
-#pragma unroll
-                for (int i = 0; i < E; i += 4)
-                    *reinterpret_cast<float4 *>(out + e0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (e0 + i >= 0 && e0 + i < n) out[e0 + i] = y[i];
-            }
+            store_probs<E>(out, e0, n, vec, y);
         }
     }
     // ---- the drawn element, on the rank that holds it ---------------------------
     const int pick = uniform(sh.pick);
     if (pick >= 0) {
-        // the run once more: every warp a part of it, then its part's elements
         const int r0 = max(0, run * pick * E - shift), r1 = min(n, run * (pick + 1) * E - shift);
-        const int part = (r1 - r0 + kThreads - 1) / kThreads * 32;
-        const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
-        auto mass_at = [&](int e, int end) -> float2 {   // of element e, if it stays
-            if (e < end) {
-                const float x = slice_elem<T>(sh.slice, e);
-                if (x > -INFINITY && composite(x, base + e) >= thr) return weight_of(x, S, &sh.tab);
-            }
-            return make_float2(0.f, 0.f);
-        };
-        Mass a;
-#pragma unroll 1
-        for (int e = p0; e < p1; e += 32) a.add(mass_at(e + lane, p1));
-        const dd2 own = warp_sum_dd(a.value());
-        if (lane == 0) sh.part_mass[warp] = own;
-        __syncthreads();
-        if (warp == 0) {
-            const dd2 mass = lane < kWarps ? sh.part_mass[lane] : dd2{0.f, 0.f};
-            const dd2 reach = add_dd(at, warp_scan_dd(mass, lane));
-            const unsigned some = __ballot_sync(0xffffffffu, mass.h > 0.f);
-            const unsigned over = __ballot_sync(0xffffffffu, mass.h > 0.f && less_dd(goal, reach));
-            const int q = over ? __ffs(over) - 1 : 31 - __clz(some);
-            if (q > 0) at = shfl_dd(reach, q - 1);
-            const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part);
-            int hit = -1, end = -1;
-#pragma unroll 1
-            for (int e = q0; e < q1 && hit < 0; e += 32) {
-                const float2 y = mass_at(e + lane, q1);
-                __syncwarp();
-                const dd2 upto = add_dd(at, warp_scan_dd({y.x, y.y}, lane));
-                const unsigned has = __ballot_sync(0xffffffffu, y.x > 0.f);
-                const unsigned past = __ballot_sync(0xffffffffu, y.x > 0.f && less_dd(goal, upto));
-                if (has) end = e + 31 - __clz(has);
-                if (past) hit = e + __ffs(past) - 1;
-                at = shfl_dd(upto, 31);
-            }
-            if (lane == 0) A.token[r] = (int32_t)(base + (hit >= 0 ? hit : end));
-        }
+        draw_element<T, kThreads>(sh.slice, sh.tab, sh.part_mass, thr, r0, r1, goal, at, A.token + r);
     }
 
     cluster_wait_all();  // no CTA leaves while another may read its shared memory
+}
+
+// ---- no filter at all ---------------------------------------------------------
+
+struct PlainShared {
+    ExpTable tab;
+    float ih, il, ch, cl;
+    float run_top[kPlainThreads / 32];   // each warp's run: its maximum, and its mass relative to that
+    dd2 run_mass[kPlainThreads / 32];
+    float top;                           // and the slice's
+    dd2 slice_mass;
+    dd2 part_mass[kPlainThreads / 32];
+    RowSlice slice;
+    float total;
+    int32_t pick;
+};
+
+// A row that no filter applies to needs its maximum and its mass only, and both
+// come in one pass over memory: every warp's sum is relative to the maximum so
+// far of its run, and is rescaled when that grows (a handful of times).  Nothing
+// is kept in shared memory; what is read again, the drawn run and, for
+// probabilities, the row, mostly comes from L2.
+template <class T>
+__global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_constant__ WarpParams A) {
+    constexpr int E = WordOf<T>::kElems, kWarps = kPlainThreads / 32, U = 16 / E;
+    __shared__ PlainShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
+    const int64_t r = blockIdx.x / C;
+    const int64_t base = min(A.V, (int64_t)rank * A.slice);
+    const int n = (int)(min(A.V, base + A.slice) - base);
+    const T *z = static_cast<const T *>(A.z) + r * A.zs + base;
+    const int shift = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
+    const uint4 *words = reinterpret_cast<const uint4 *>(z - shift);
+    const int W = n > 0 ? (n + shift + E - 1) / E : 0;
+    const int w0 = shift ? 1 : 0, w1 = (n + shift) / E;   // whole words
+    if (tid < 32) sh.tab.t[lane] = kPow2[lane];
+    wait_for_primary_grid();
+    const float temp = uniform(A.temperature ? A.temperature[r] : 1.f);
+    if (tid == 64) {
+        const double i = 1.0 / (double)temp, c = i * 1.4426950408889634;
+        sh.ih = (float)i;
+        sh.il = (float)(i - (double)sh.ih);
+        sh.ch = (float)c;
+        sh.cl = (float)(c - (double)sh.ch);
+    }
+    __syncthreads();
+    RowScale S = {-INFINITY, sh.ih, sh.il, sh.ch, sh.cl, -85.f * temp};
+
+    // U words of a lane, 32 apart; what lies outside the slice is -inf
+    auto load = [&](int w, float (&x)[16]) {
+        uint4 v[U];
+        if (w - lane >= w0 && w - lane + 32 * U <= w1) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[j] = __ldg(words + w + 32 * j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int at = w + 32 * j;
+                if (at >= w0 && at < w1) {
+                    v[j] = __ldg(words + at);
+                } else {
+                    T q[E];
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const int e = at * E - shift + i;
+                        q[i] = e >= 0 && e < n ? z[e] : minus_inf<T>();
+                    }
+                    memcpy(&v[j], q, 16);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            float y[E];
+            unpack<T>(v[j], y);
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[j * E + i] = y[i];
+        }
+    };
+
+    // every warp takes a run of words
+    const int run = (W + kPlainThreads - 1) / kPlainThreads * 32;
+    const int s0 = min(W, run * warp), s1 = min(W, s0 + run);
+    // (a run ends inside a lane's words: what follows is the next run's)
+    auto outside = [&](int w, float (&x)[16]) {
+        if (w - lane + 32 * U > s1)
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (w + 32 * j >= s1)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) x[j * E + i] = -INFINITY;
+    };
+    Mass a;
+#pragma unroll 1
+    for (int w = s0 + lane; w - lane < s1; w += 32 * U) {
+        float x[16];
+        load(w, x);
+        outside(w, x);
+        float most = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) most = max_nan(most, x[i]);
+        if (__any_sync(0xffffffffu, !(most <= S.m))) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, d));
+            const float old = S.m;
+            S.m = max_nan(old, uniform(most));
+            const float2 by = weight_of(old, S, &sh.tab);   // (of -inf: 0)
+            const dd2 v = mul_dd(a.value(), {by.x, by.y}), start = add_dd({4.f, 0.f}, v);
+            a.h = start.h;
+            a.l = start.l;
+        }
+        if (!(fabsf(S.m) < INFINITY)) continue;
+#pragma unroll
+        for (int h = 0; h < 16; h += 4) {
+            float2 y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = weight(x[h + i], S, sh.tab);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.add(y[i]);
+        }
+    }
+    __syncwarp();
+    {
+        const dd2 own = warp_sum_dd(a.value());
+        if (lane == 0) {
+            sh.run_top[warp] = S.m;
+            sh.run_mass[warp] = own;
+        }
+    }
+    __syncthreads();
+    // a warp's 32 masses relative to their tops, as relative to m
+    auto rebase = [&](float top, dd2 mass, float m) -> dd2 {
+        RowScale to = S;
+        to.m = m;
+        const float2 by = weight_of(fabsf(m) < INFINITY ? top : -INFINITY, to, &sh.tab);
+        // (a mass counts if its largest element has weight)
+        return by.x > 0.f ? mul_dd(mass, {by.x, by.y}) : dd2{0.f, 0.f};
+    };
+    auto largest_of = [&](float x) -> float {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, d));
+        return uniform(x);
+    };
+    if (warp == 0) {
+        const float own = lane < kWarps ? sh.run_top[lane] : -INFINITY;
+        const float top = largest_of(own);
+        const dd2 mass = warp_sum_dd(rebase(own, lane < kWarps ? sh.run_mass[lane] : dd2{0.f, 0.f}, top));
+        if (lane == 0) {
+            sh.top = top;
+            sh.slice_mass = mass;
+            sh.pick = -1;
+        }
+    }
+    cluster.sync();
+    float top = -INFINITY;
+    dd2 mass = {0.f, 0.f};
+    if (lane < C) {
+        const PlainShared *o = cluster.map_shared_rank(&sh, lane);
+        top = o->top;
+        mass = o->slice_mass;
+    }
+    const float m = largest_of(top);
+    const dd2 own = rebase(top, mass, m);
+    cluster_arrive_all();  // the last access to another CTA's shared memory is made
+    float *out = A.probs ? A.probs + r * A.ps + base : nullptr;
+    const bool bad = !(m < INFINITY) || !(temp >= kColdest && temp <= kHottest);
+    if (bad || m == -INFINITY) {
+        if (rank == 0 && tid == 0) {
+            atomicOr(A.status, bad ? SV_STATUS_BAD_VALUE : SV_STATUS_ZERO_MASS);
+            if (A.token) A.token[r] = -1;
+        }
+        if (out)
+#pragma unroll 1
+            for (int e = tid; e < n; e += kPlainThreads) out[e] = 0.f;
+        cluster_wait_all();
+        return;
+    }
+    S.m = m;
+    // the first rank, then run, whose running mass passes the goal
+    dd2 goal = {0.f, 0.f}, at = {0.f, 0.f};   // (warp 0)
+    if (warp == 0) {
+        const dd2 upto = warp_scan_dd(own, lane);
+        const dd2 total = shfl_dd(upto, 31);
+        if (lane == 0) {
+            sh.total = total.h;
+            sh.slice = {z, words, base, n, shift, 0, S};
+        }
+        if (A.token) {
+            const double g = A.u[r] * ((double)total.h + (double)total.l);   // rounded as in 64 bits
+            const float gh = (float)g;
+            goal = {gh, (float)(g - (double)gh)};
+            const unsigned some = __ballot_sync(0xffffffffu, own.h > 0.f);
+            const unsigned over = __ballot_sync(0xffffffffu, own.h > 0.f && less_dd(goal, upto));
+            const int holder = over ? __ffs(over) - 1 : 31 - __clz(some);
+            if (holder == rank) {
+                if (rank > 0) at = shfl_dd(upto, rank - 1);
+                const dd2 part = rebase(lane < kWarps ? sh.run_top[lane] : -INFINITY,
+                                        lane < kWarps ? sh.run_mass[lane] : dd2{0.f, 0.f}, m);
+                const dd2 reach = add_dd(at, warp_scan_dd(part, lane));
+                const unsigned runs = __ballot_sync(0xffffffffu, part.h > 0.f);
+                const unsigned past = __ballot_sync(0xffffffffu, part.h > 0.f && less_dd(goal, reach));
+                const int pick = past ? __ffs(past) - 1 : 31 - __clz(runs);
+                if (pick > 0) at = shfl_dd(reach, pick - 1);
+                if (lane == 0) sh.pick = pick;
+            }
+        }
+    }
+    __syncthreads();
+    if (out) {
+        const float inv = 1.f / sh.total;
+        const bool vec = ((reinterpret_cast<uintptr_t>(out) - (uintptr_t)shift * 4u) & 15u) == 0;
+#pragma unroll 1
+        for (int w = s0 + lane; w - lane < s1; w += 32 * U) {
+            float x[16];
+            load(w, x);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                float y[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) y[i] = fast_weight(x[j * E + i], S) * inv;
+                if (w + 32 * j < s1) store_probs<E>(out, (w + 32 * j) * E - shift, n, vec, y);
+            }
+        }
+    }
+    const int pick = uniform(sh.pick);
+    if (pick >= 0) {
+        const int r0 = max(0, run * pick * E - shift), r1 = min(n, run * (pick + 1) * E - shift);
+        draw_element<T, kPlainThreads>(sh.slice, sh.tab, sh.part_mass, 0, r0, r1, goal, at, A.token + r);
+    }
+    cluster_wait_all();
 }
 
 }  // namespace sv

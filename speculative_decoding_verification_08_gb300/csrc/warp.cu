@@ -27,10 +27,34 @@ bool on_device(const void *p) {
     return place(x) == kOnDevice;  // true for null: optional arrays
 }
 
+int launch_clusters(void (*kernel)(sv::WarpParams), const sv::WarpParams &A, int c, int threads, size_t bytes,
+                    cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(A.R * c));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, A) != cudaSuccess)
+        return SV_ECUDA;
+    svhost::g_last_grid = (int64_t)A.R * c;
+    svhost::g_last_kernels = 1;
+    return SV_OK;
+}
+
 template <class T>
 int launch(sv::WarpParams &A, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ECUDA;
+    const bool plain = !A.top_k && !A.top_p && !A.min_p;
     // Cluster: as many CTAs as keep a slice within 64 KB (three of them then
     // share an SM and hide one another's barriers), and more while the whole
     // batch has fewer CTAs than SMs, down to 2048 elements each.
@@ -40,6 +64,8 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
            ((row + c - 1) / c > 65536 || ((int64_t)A.R * c * 2 <= kSms && A.V / (2 * c) >= 2048)))
         c *= 2;
     A.slice = (int32_t)(((A.V + c - 1) / c + 15) / 16 * 16);
+    if ((int64_t)A.R * c > INT32_MAX) return SV_EINVAL;
+    if (plain) return launch_clusters(sv::plain_kernel<T>, A, c, sv::kPlainThreads, 0, st);
     const int per_word = 16 / (int)sizeof(T);
     const bool wide = (int64_t)A.slice / per_word + 1 > kSharedWords;
     const int threads = wide ? 1024 : kThreads;
@@ -61,26 +87,7 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
                 return SV_ECUDA;
         raised[dev].store(1);
     }
-    if ((int64_t)A.R * c > INT32_MAX) return SV_EINVAL;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(A.R * c));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, A) != cudaSuccess)
-        return SV_ECUDA;
-    svhost::g_last_grid = (int64_t)A.R * c;
-    svhost::g_last_kernels = 1;
-    return SV_OK;
+    return launch_clusters(kernel, A, c, threads, bytes, st);
 }
 
 }  // namespace

@@ -130,6 +130,60 @@ def test_masked_logits_and_a_single_survivor():
     check(z, u, np.full(6, 2.0), None, None, np.full(6, 0.05))
 
 
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_rows_in_rising_order(dt):
+    """Without filters the maximum is found on the way: rows that rise, that
+    jump late, and whose first parts are masked."""
+    V = 70001
+    up = torch.linspace(-60.0, 25.0, V)
+    late = torch.full((V,), -3.0)
+    late[-5] = 40.0
+    masked = torch.linspace(-1.0, 1.0, V)
+    masked[: V * 3 // 4] = float("-inf")
+    saw = (torch.arange(V) % 977).float() / 100 + torch.arange(V).float() / 3000
+    z = torch.stack([up, late, masked, saw, up.flip(0)]).to(TYPES[dt]).cuda()
+    zc = z.float().cpu().numpy()
+    for T in (np.ones(5), np.array([0.3, 1.0, 5.0, 2.0, 0.7])):
+        temp = torch.as_tensor(T, dtype=torch.float32).cuda()
+        for u in (0.0, 0.3, 0.77, 1 - 2.0 ** -53):
+            tok, probs = sv.warp_sample(z, torch.full((5,), u, dtype=torch.float64, device="cuda"),
+                                        temperature=temp, probs=True)
+            for r in range(5):
+                # (what lies more than 85 T below the maximum weighs nothing)
+                low = zc[r] - zc[r].max() < np.float32(-85) * np.float32(T[r])
+                want, _, t = warp_row(np.where(low, -np.inf, zc[r]), float(temp[r]), u=u)
+                # masses are good to 1e-10: that far from a border either side may be drawn
+                # (the falling row's last e^-23 lie within it of the row's end)
+                got, c = int(tok[r]), np.cumsum(want)
+                assert want[got] > 0 and c[got] - want[got] <= u + 1e-10 and c[got] >= u - 1e-10, (r, u)
+                assert got == t or abs(c[min(got, t)] - u) <= 1e-10, (r, u)
+                assert np.all(np.abs(probs[r].cpu().numpy() - want) <= PROB_TOL * want + 1e-29), (r, u)
+
+
+@pytest.mark.parametrize("R,V,dt", [(3, 262144, "f32"), (2, 262145, "bf16"), (40, 9001, "f16"), (300, 700, "f32")])
+def test_plain_rows_without_answers(R, V, dt):
+    z = logits(R, V, dt, seed=R)
+    z[0, V // 2:] = float("-inf")
+    z[1] = float("-inf")
+    u = torch.rand(R, dtype=torch.float64, generator=torch.Generator().manual_seed(R)).cuda()
+    ws = sv.CacheWorkspace()
+    tok, probs = sv.warp_sample(z, u, probs=True, ws=ws)
+    assert ws.status() == sv.STATUS_ZERO_MASS
+    assert int(tok[1]) == -1 and not bool(probs[1].any())
+    for r in (0, R - 1):
+        if r != 1:
+            want, _, t = warp_row(z[r].float().cpu().numpy(), u=float(u[r]))
+            assert int(tok[r]) == t
+            assert np.all(np.abs(probs[r].cpu().numpy() - want) <= PROB_TOL * want + 1e-29)
+    for bad in (float("nan"), float("inf")):
+        y = z.clone()
+        y[0, V - 1] = bad
+        ws = sv.CacheWorkspace()
+        tok, probs = sv.warp_sample(y, u, probs=True, ws=ws)
+        assert ws.status() == sv.STATUS_ZERO_MASS | sv.STATUS_BAD_VALUE
+        assert int(tok[0]) == -1 and not bool(probs[0].any())
+
+
 def test_rows_without_an_answer():
     V = 3000
     z = logits(6, V, "bf16", seed=3)
