@@ -91,7 +91,7 @@ __constant__ float2 kPow2[32] = {
     {1.35425556f, -1.01233493e-08f}, {1.38390994f, -5.87557736e-08f}};
 
 struct ExpTable {
-    float2 t[32];
+    float x[32], y[32];   // (columns: 32 lanes' lookups then meet no bank conflicts)
 };
 
 struct RowScale {
@@ -118,7 +118,7 @@ __device__ __forceinline__ float2 weight(float z, const RowScale &S, const ExpTa
     const float rl = fmaf(k, 5.95204441e-11f, xl), q = r + rl;
     const float t = fmaf(q * q, fmaf(q, fmaf(q, 4.16666667e-2f, 0.166666667f), 0.5f), rl);
     const int ki = __float_as_int(km) + 16;
-    const float2 T = tab.t[ki & 31];
+    const float2 T = make_float2(tab.x[ki & 31], tab.y[ki & 31]);
     const float scale = in ? __uint_as_float(((uint32_t)ki >> 5 << 23) + 0x3f800000u) : 0.f;
     const float v = T.x * r, vl = fmaf(T.x, r, -v), u = fmaf(T.x, t, fmaf(T.y, r, T.y));
     const float h = T.x + v;
@@ -182,6 +182,113 @@ struct Mass {
     }
     __device__ __forceinline__ dd2 value() const { return norm2(h - 4.f, l); }
 };
+
+// ---- exact weights two at a time, for maxima not far from zero -----------------
+//
+// Where no |z| is above some 64 T, exp(z / T) itself fits fp32's range: the
+// difference from the maximum, and its rounding error, need not be formed, and
+// a power of two 2^E takes the maximum's place.  Packed fp32 pairs halve the
+// instructions.
+
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ f32x2 pair(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 halves(f32x2 x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, pair(-1.f), a); }
+
+constexpr float kLn2 = 0.693147182f;
+constexpr float kNear = 64.f;      // |max| / T up to here
+constexpr int kNearDepth = 120;    // octaves below 2^E that are held
+
+struct NearScale {
+    float ih, il;   // 1 / temperature
+    float lo;       // the smallest z
+    uint32_t bias;  // of the exponent: one's less E
+};
+
+__device__ __forceinline__ NearScale near_scale(const RowScale &S, float temp, int E) {
+    return {S.ih, S.il, (float)(E - kNearDepth) * (kLn2 * temp), 0x3f800000u - ((uint32_t)E << 23)};
+}
+// The octave above a maximum: exp(max / T) <= 2^E.
+__device__ __forceinline__ int near_octave(float m, const RowScale &S) { return (int)ceilf(m * S.ch) + 1; }
+
+struct Pair2 {
+    f32x2 h, l;
+};
+
+// exp(z / T) / 2^E of two elements, each as hi + lo; steps as in weight().
+__device__ __forceinline__ Pair2 near_weights(float z0, float z1, const NearScale &N, const ExpTable &tab) {
+    const f32x2 z = pair(z0, z1);
+    const f32x2 nx = mul2(z, pair(-N.ih));                                       // -xh
+    const f32x2 xl = fma2(z, pair(N.il), fma2(z, pair(N.ih), nx));
+    const f32x2 km = fma2(nx, pair(-46.1662413f), pair(12582912.f + 16.f));      // the low bits hold k + 16
+    const f32x2 k = add2(km, pair(-12582912.f - 16.f));
+    const f32x2 nr = fma2(k, pair(0.0216608495f), nx);                           // -r
+    const f32x2 rl = fma2(k, pair(5.95204441e-11f), xl);
+    const f32x2 r = mul2(nr, pair(-1.f)), q = add2(r, rl);
+    const f32x2 t = fma2(mul2(q, q), fma2(q, fma2(q, pair(4.16666667e-2f), pair(0.166666667f)), pair(0.5f)), rl);
+    const float2 ks = halves(km);
+    const uint32_t k0 = __float_as_uint(ks.x), k1 = __float_as_uint(ks.y);
+    const f32x2 Tx = pair(tab.x[k0 & 31], tab.x[k1 & 31]), Ty = pair(tab.y[k0 & 31], tab.y[k1 & 31]);
+    const f32x2 scale = pair(__uint_as_float(((k0 & ~31u) << 18) + N.bias), __uint_as_float(((k1 & ~31u) << 18) + N.bias));
+    const f32x2 v = mul2(Tx, r), nvl = fma2(Tx, nr, v);
+    const f32x2 u = fma2(Tx, t, fma2(Ty, r, Ty));
+    const f32x2 h = add2(Tx, v);
+    const f32x2 l = add2(sub2(v, sub2(h, Tx)), sub2(u, nvl));
+    return {mul2(h, scale), mul2(l, scale)};
+}
+
+// Two running sums, as Mass.
+struct Mass2 {
+    f32x2 h = pair(4.f), l = pair(0.f);
+    __device__ __forceinline__ void add(Pair2 w) {
+        const f32x2 s = add2(h, w.h);
+        l = add2(l, add2(sub2(w.h, sub2(s, h)), w.l));
+        h = s;
+    }
+    __device__ __forceinline__ dd2 value() const {
+        const float2 a = halves(h), b = halves(l);
+        return add_dd(norm2(a.x - 4.f, b.x), norm2(a.y - 4.f, b.y));
+    }
+    __device__ __forceinline__ void scale(float by) {
+        const float2 a = halves(h), b = halves(l);
+        const dd2 x = add_dd({4.f, 0.f}, {(a.x - 4.f) * by, b.x * by});
+        const dd2 y = add_dd({4.f, 0.f}, {(a.y - 4.f) * by, b.y * by});
+        h = pair(x.h, y.h);
+        l = pair(x.l, y.l);
+    }
+};
+
+// What turns such a mass into one relative to the maximum m: 2^E exp(-m / T).
+__device__ __forceinline__ dd2 near_to_max(const RowScale &S, const ExpTable *tab, int E) {
+    const float2 y = weight_of(0.f, S, tab);
+    const float by = __uint_as_float((uint32_t)(127 + E) << 23);
+    return {y.x * by, y.y * by};
+}
 
 namespace cg = cooperative_groups;
 
@@ -491,8 +598,9 @@ __device__ __noinline__ void rank_alone(WarpShared &sh, int got) {
 
 // The element of r0 .. r1 - 1 whose running mass, from `at` on, passes the goal;
 // or, where rounding lets none, the last with mass.  By the whole CTA; goal and
-// at are warp 0's.
-template <class T, int kThreads>
+// at are warp 0's.  U loads at a time: one from shared memory, where short code
+// counts (a single row's time is mostly its first passes through the code).
+template <class T, int kThreads, int U>
 __device__ __forceinline__ void draw_element(const RowSlice &c, const ExpTable &tab, dd2 *part_mass, uint64_t thr,
                                              int r0, int r1, dd2 goal, dd2 at, int32_t *token) {
     constexpr int kWarps = kThreads / 32;
@@ -506,13 +614,12 @@ __device__ __forceinline__ void draw_element(const RowSlice &c, const ExpTable &
         const int p0 = min(r1, r0 + part * warp), p1 = min(r1, p0 + part);
         Mass a;
 #pragma unroll 1
-        for (int e = p0 + lane; e - lane < p1; e += 256) {
-            float x[8];
+        for (int e = p0 + lane; e - lane < p1; e += 32 * U) {
+            float x[U];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = e + 32 * i < p1 ? slice_elem<T>(c, e + 32 * i) : -INFINITY;
+            for (int i = 0; i < U; ++i) x[i] = e + 32 * i < p1 ? slice_elem<T>(c, e + 32 * i) : -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (p0 + part > e - lane + 32 * i) a.add(mass_of(x[i], e + 32 * i));
+            for (int i = 0; i < U; ++i) a.add(mass_of(x[i], e + 32 * i));
         }
         __syncwarp();
         const dd2 own = warp_sum_dd(a.value());
@@ -530,22 +637,26 @@ __device__ __forceinline__ void draw_element(const RowSlice &c, const ExpTable &
         return q;
     };
     const int q = choose(lane < kWarps ? part_mass[lane] : dd2{0.f, 0.f});
-    // of that part the lane's stretch, then the stretch's elements
     const int q0 = min(r1, r0 + part * q), q1 = min(r1, q0 + part), per = part / 32;
-    int l0 = min(q1, q0 + per * lane), l1 = min(q1, l0 + per);
-    Mass a;
+    int l0 = q0, l1 = q1;
+    if (per > 2) {
+        // of a long part first the lane's stretch
+        l0 = min(q1, q0 + per * lane);
+        l1 = min(q1, l0 + per);
+        Mass a;
 #pragma unroll 1
-    for (int i = 0; i < per; i += 4) {
-        float x[4];
+        for (int i = 0; i < per; i += (U + 1) / 2) {
+            float x[(U + 1) / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = l0 + i + j < l1 ? slice_elem<T>(c, l0 + i + j) : -INFINITY;
+            for (int j = 0; j < (U + 1) / 2; ++j) x[j] = l0 + i + j < l1 ? slice_elem<T>(c, l0 + i + j) : -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a.add(mass_of(x[j], l0 + i + j));
+            for (int j = 0; j < (U + 1) / 2; ++j) a.add(mass_of(x[j], l0 + i + j));
+        }
+        __syncwarp();
+        const int l = choose(a.value());
+        l0 = __shfl_sync(0xffffffffu, l0, l);
+        l1 = __shfl_sync(0xffffffffu, l1, l);
     }
-    __syncwarp();
-    const int l = choose(a.value());
-    l0 = __shfl_sync(0xffffffffu, l0, l);
-    l1 = __shfl_sync(0xffffffffu, l1, l);
     int hit = -1, end = -1;
 #pragma unroll 1
     for (int e = l0; e < l1 && hit < 0; e += 32) {
@@ -604,7 +715,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
         sh.bad = 0;
         sh.count = 0;
     }
-    if (tid >= 32 && tid < 64) sh.tab.t[lane] = kPow2[lane];
+    if (tid >= 32 && tid < 64) {
+        sh.tab.x[lane] = kPow2[lane].x;
+        sh.tab.y[lane] = kPow2[lane].y;
+    }
     __syncthreads();
     wait_for_primary_grid();
     const int w0 = shift ? 1 : 0;                          // first whole word
@@ -944,10 +1058,44 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
     const float t_goal = by_p ? t_k : 0.f;           // `in` wanted below it
     const bool dense = by_p ? t_k >= never : t_keep >= never && zmin == -INFINITY;
     const float t_far = fmaxf(fmaxf(t_goal, t_last), t_k < never ? t_k : 0.f);
+    // (all but the first of a dense row in pairs, where its maximum allows that)
+    const bool near = kHeld && dense && fabsf(m) <= kNear * temp;
+    const int octave = near ? near_octave(m, S) : 0;
+    const NearScale N = near_scale(S, temp, octave);
+    Mass2 near_all;
+    Mass near_above, near_kept;
 #pragma unroll 1
     for (int w = s0 + lane; w < s1; w += 32) {
         float x[E];
         load(w, x);
+        if (kHeld && near) {
+            float least = x[0];
+#pragma unroll
+            for (int i = 1; i < E; ++i) least = fminf(least, x[i]);
+            if (__all_sync(0xffffffffu, least >= N.lo)) {
+#pragma unroll
+                for (int i = 0; i < E; i += 2) {
+                    const Pair2 y = near_weights(x[i], x[i + 1], N, sh.tab);
+                    near_all.add(y);
+                    if (!by_p) continue;
+                    const float2 h = halves(y.h), l = halves(y.l);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float t = t_of(x[i + j]);
+                        if (t > t_last) continue;
+                        const float2 one = j == 0 ? make_float2(h.x, l.x) : make_float2(h.y, l.y);
+                        if (t < t_keep) {
+                            near_above.add(one);
+                            if (mp > 0.f && x[i + j] >= zmin) near_kept.add(one);
+                        } else {
+                            const uint32_t at = atomicAdd(&sh.count, 1u);
+                            if (at < kLocalList) sh.list[at] = composite(x[i + j], index_of(w, i + j));
+                        }
+                    }
+                }
+                continue;
+            }
+        }
         if (dense) {
             // every element's weight, four chains at a time
 #pragma unroll
@@ -996,11 +1144,18 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
     }
     __syncwarp();
     {
-        if (dense && by_p && !(mp > 0.f)) kept = above;
-        const dd2 a = warp_sum_dd(kept.value());
+        dd2 own_kept = kept.value(), own_above = above.value(), own_in = in.value();
+        if (near) {
+            const dd2 by = near_to_max(S, &sh.tab, octave), all = mul_dd(near_all.value(), by);
+            own_above = add_dd(own_above, mul_dd(near_above.value(), by));
+            own_kept = add_dd(own_kept, by_p ? mul_dd(near_kept.value(), by) : all);
+            own_in = add_dd(own_in, all);
+        }
+        if (dense && by_p && !(mp > 0.f)) own_kept = own_above;
+        const dd2 a = warp_sum_dd(own_kept);
         if (lane == 0) sh.run_mass[warp] = a;
         if (by_p) {
-            const dd2 b = warp_sum_dd(above.value()), c = warp_sum_dd(in.value());
+            const dd2 b = warp_sum_dd(own_above), c = warp_sum_dd(own_in);
             if (lane == 0) {
                 sh.part_mass[warp] = b;
                 sh.in_mass[warp] = c;
@@ -1275,7 +1430,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
     const int pick = uniform(sh.pick);
     if (pick >= 0) {
         const int r0 = max(0, run * pick * E - shift), r1 = min(n, run * (pick + 1) * E - shift);
-        draw_element<T, kThreads>(sh.slice, sh.tab, sh.part_mass, thr, r0, r1, goal, at, A.token + r);
+        draw_element<T, kThreads, 1>(sh.slice, sh.tab, sh.part_mass, thr, r0, r1, goal, at, A.token + r);
     }
 
     cluster_wait_all();  // no CTA leaves while another may read its shared memory
@@ -1316,7 +1471,10 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
     const uint4 *words = reinterpret_cast<const uint4 *>(z - shift);
     const int W = n > 0 ? (n + shift + E - 1) / E : 0;
     const int w0 = shift ? 1 : 0, w1 = (n + shift) / E;   // whole words
-    if (tid < 32) sh.tab.t[lane] = kPow2[lane];
+    if (tid < 32) {
+        sh.tab.x[lane] = kPow2[lane].x;
+        sh.tab.y[lane] = kPow2[lane].y;
+    }
     wait_for_primary_grid();
     const float temp = uniform(A.temperature ? A.temperature[r] : 1.f);
     if (tid == 64) {
@@ -1330,8 +1488,7 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
     RowScale S = {-INFINITY, sh.ih, sh.il, sh.ch, sh.cl, -85.f * temp};
 
     // U words of a lane, 32 apart; what lies outside the slice is -inf
-    auto load = [&](int w, float (&x)[16]) {
-        uint4 v[U];
+    auto fetch = [&](int w, uint4 (&v)[U]) {
         if (w - lane >= w0 && w - lane + 32 * U <= w1) {
 #pragma unroll
             for (int j = 0; j < U; ++j) v[j] = __ldg(words + w + 32 * j);
@@ -1352,6 +1509,8 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
                 }
             }
         }
+    };
+    auto spread = [&](const uint4 (&v)[U], float (&x)[16]) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             float y[E];
@@ -1365,20 +1524,84 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
     const int run = (W + kPlainThreads - 1) / kPlainThreads * 32;
     const int s0 = min(W, run * warp), s1 = min(W, s0 + run);
     // (a run ends inside a lane's words: what follows is the next run's)
-    auto outside = [&](int w, float (&x)[16]) {
+    auto outside = [&](int w, float (&x)[16], float instead) {
         if (w - lane + 32 * U > s1)
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (w + 32 * j >= s1)
 #pragma unroll
-                    for (int i = 0; i < E; ++i) x[j * E + i] = -INFINITY;
+                    for (int i = 0; i < E; ++i) x[j * E + i] = instead;
     };
+    auto largest_of = [&](float x) -> float {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, d));
+        return uniform(x);
+    };
+    // near zero, in pairs, as far as that goes
     Mass a;
+    int w = s0 + lane;
+    uint4 v[U];
+    fetch(w, v);
+    {
+        Mass2 near;
+        NearScale N = near_scale(S, temp, 0);
+        int octave = 0;
+        float hi = -INFINITY, top = -INFINITY;
+        N.lo = INFINITY;
 #pragma unroll 1
-    for (int w = s0 + lane; w - lane < s1; w += 32 * U) {
+        for (; w - lane < s1; w += 32 * U) {
+            float x[16];
+            spread(v, x);
+            if (w - lane + 32 * U < s1) fetch(w + 32 * U, v);
+            outside(w, x, N.lo < INFINITY ? N.lo : -INFINITY);   // (2^-120: nothing)
+            float most = x[0], least = x[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                most = fmaxf(most, x[i]);
+                least = fminf(least, x[i]);
+            }
+            if (!__all_sync(0xffffffffu, most <= hi && least >= N.lo)) {
+                float high = most, low = least;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) {
+                    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+                    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
+                }
+                high = uniform(high);
+                low = uniform(low);
+                int up = octave;
+                if (high > hi) {
+                    if (!(fabsf(high) <= kNear * temp)) break;
+                    up = near_octave(high, S);
+                }
+                if (!(low >= (float)(up - kNearDepth) * (kLn2 * temp))) break;
+                if (hi > -INFINITY) near.scale(exp2f((float)max(octave - up, -126)));
+                octave = up;
+                hi = (float)octave * (kLn2 * temp);
+                N = near_scale(S, temp, octave);
+            }
+            top = fmaxf(top, most);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) near.add(near_weights(x[i], x[i + 1], N, sh.tab));
+        }
+        top = largest_of(top);
+        if (top > -INFINITY) {
+            S.m = top;
+            const dd2 v = mul_dd(near.value(), near_to_max(S, &sh.tab, octave));
+            const dd2 start = add_dd({4.f, 0.f}, v);
+            a.h = start.h;
+            a.l = start.l;
+            // (a NaN shows in the sum alone)
+            if (__any_sync(0xffffffffu, !(a.h < INFINITY))) S.m = __int_as_float(0x7fffffff);
+        }
+    }
+    // the rest relative to the maximum so far
+#pragma unroll 1
+    for (; w - lane < s1; w += 32 * U) {
         float x[16];
-        load(w, x);
-        outside(w, x);
+        fetch(w, v);
+        spread(v, x);
+        outside(w, x, -INFINITY);
         float most = x[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) most = max_nan(most, x[i]);
@@ -1418,11 +1641,6 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
         const float2 by = weight_of(fabsf(m) < INFINITY ? top : -INFINITY, to, &sh.tab);
         // (a mass counts if its largest element has weight)
         return by.x > 0.f ? mul_dd(mass, {by.x, by.y}) : dd2{0.f, 0.f};
-    };
-    auto largest_of = [&](float x) -> float {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, d));
-        return uniform(x);
     };
     if (warp == 0) {
         const float own = lane < kWarps ? sh.run_top[lane] : -INFINITY;
@@ -1495,7 +1713,8 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
 #pragma unroll 1
         for (int w = s0 + lane; w - lane < s1; w += 32 * U) {
             float x[16];
-            load(w, x);
+            fetch(w, v);
+            spread(v, x);
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 float y[E];
@@ -1508,7 +1727,7 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
     const int pick = uniform(sh.pick);
     if (pick >= 0) {
         const int r0 = max(0, run * pick * E - shift), r1 = min(n, run * (pick + 1) * E - shift);
-        draw_element<T, kPlainThreads>(sh.slice, sh.tab, sh.part_mass, 0, r0, r1, goal, at, A.token + r);
+        draw_element<T, kPlainThreads, 8>(sh.slice, sh.tab, sh.part_mass, 0, r0, r1, goal, at, A.token + r);
     }
     cluster_wait_all();
 }
