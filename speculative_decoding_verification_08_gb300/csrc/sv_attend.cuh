@@ -31,11 +31,25 @@
 // workspace, and the last CTA of a tile to arrive joins them in order: results
 // do not depend on timing.
 //
-// Warps 0-7 softmax, 8 copies of keys and values (one TMA box per page piece and 64 values of a
-// head, 128-byte swizzle), 9 issues the products,
-// 10 copies of queries, 11 walks the CTA's run and publishes its pieces.  Every wait is bounded; when
-// one gives up the CTA's warps leave at the next piece they miss, without further
-// waits or copies, and the call reports SV_STATUS_TIMEOUT.
+// Warps 0-7 softmax, 8 copies of keys and values (one TMA box per page piece and
+// 64 values of a head, 128-byte swizzle), 9 issues the products, 10 copies of
+// queries, 11 walks the CTA's run and publishes its pieces.  Every wait is
+// bounded; when one gives up the CTA's warps leave at the next piece they miss,
+// without further waits or copies, and the call reports SV_STATUS_TIMEOUT.
+//
+// Measured (32 query heads over 8 of 128, bf16, unless said otherwise):
+//   rounds of 6 tokens over up to 4096 slots, 256 sequences: 367 us, 6.5 TB/s:
+//     bound by memory;
+//   6 tokens over 131071 slots, 2 sequences, 16 over 4 heads of 64 in fp16:
+//     65 us, 4.1 TB/s: only 24 of 128 rows are used, so that one warp of each
+//     group turns scores into weights, and its latency per key block shows;
+//   two prompts of 8192 tokens: 0.73 ms in short bursts, 0.79 under sustained
+//     load (1.5 and 1.4 PFLOP/s of the causal half): the softmax of a pair of
+//     key blocks takes a group 2800 cycles where the products take 2048;
+//   five chunks of up to 1025 tokens over up to 7000: 159 us (1.16 PFLOP/s):
+//     the same, and each tile's start, end and joining;
+//   one token over 1000 slots: 12.5 us, mostly latency (launch, table lookups,
+//     one block after another, join).
 #pragma once
 
 #include <type_traits>
@@ -56,7 +70,7 @@ constexpr int kKeys = 128;           // slots per key block
 constexpr int kAttendMaxCtas = 160;  // partial states the workspace holds room for
 constexpr uint32_t kTmemCols = 512;
 constexpr int kNoPage = 0x7fffffff;  // outside every cache: its boxes read zeros
-constexpr float kRescaleAbove = 8.f;  // log2
+constexpr float kRescaleAbove = 8.f;  // log2 (0: 0.90 instead of 0.79 ms for two prompts of 8192)
 
 // Workspace: header (status), tile counters [ctas][2], partial statistics
 // [ctas * 2 slots][2 groups][128 rows] (reference, sum), partial O
@@ -101,7 +115,9 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return a / b;
 }
 
-// A tile's fixed cost (queries in, states joined, rows out) in key blocks.
+// A tile's fixed cost (queries in, states joined, rows out) in key blocks: 2
+// and 4 measure alike, 0 takes 1.05 instead of 0.79 ms for two prompts of 8192
+// tokens (CTAs with many short tiles finish late).
 constexpr int kTileCost = 2;
 
 struct SeqCost {

@@ -162,6 +162,28 @@ def test_attention_matches_the_definition(case):
         within(got, want, tol)
 
 
+def test_attention_over_many_sequences():
+    """More sequences than one pass of the scheduler's search covers, empty ones
+    among them."""
+    seqs = [((b * 7) % 4, (b * 7) % 4 + (b * 13) % 37) for b in range(1000)]
+    cb = CacheBatch(seqs, 1, 64, 16, BF, seed=14)
+    q = cb.tokens(2)
+    ws = sv.CacheWorkspace()
+    want, tol = attention(cb, q, default_scale(64), 0)
+    got = sv.paged_attention(q, *cb.args(), ws=ws)
+    assert ws.status() == 0
+    within(got, want, tol)
+
+
+@pytest.mark.parametrize("group,d,page", [(3, 64, 8), (7, 96, 24), (5, 128, 16), (16, 64, 64), (130, 32, 8)])
+def test_attention_group_sizes_and_scales(group, d, page):
+    cb = CacheBatch([(5, 140), (1, 33), (45, 45)], 1, d, page, BF, seed=group)
+    q = cb.tokens(group)
+    for scale in (0.2, -0.1, 0.0):
+        want, tol = attention(cb, q, scale, 0)
+        within(sv.paged_attention(q, *cb.args(), scale=scale), want, tol)
+
+
 def test_attention_same_bits_again_and_on_another_stream():
     cb = CacheBatch([(6, 900), (1, 77), (50, 300)], 2, 128, 64, BF, seed=5)
     q = cb.tokens(8)

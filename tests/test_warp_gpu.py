@@ -251,6 +251,61 @@ def test_a_nucleus_that_needs_every_digit():
     check(z.expand(len(ps), V).contiguous(), np.full(len(ps), 0.5), None, None, ps)
 
 
+@pytest.mark.parametrize("step", [0.01, 0.02, 0.05, 0.1, 0.25, 1.0])
+def test_borders_of_many_equal_logits(step):
+    """Logits on a grid: a border holds from a few dozen to thousands of equal
+    values, ranked by one warp, by a CTA, by the cluster, or bisected."""
+    V, R = 50000, 6
+    g = torch.Generator().manual_seed(int(step * 1000))
+    z = (torch.round(torch.randn(R, V, generator=g) * 3 / step) * step).cuda()
+    rng = np.random.RandomState(9)
+    u, k, p = rng.rand(R), rng.randint(1, V, R), rng.uniform(0.3, 0.999, R)
+    check(z, u, None, k)
+    check(z, u, None, None, p)
+    check(z, u, np.full(R, 0.8), k, p, np.full(R, 1e-4))
+
+
+def test_rows_larger_than_shared_memory():
+    V = 2_000_003
+    z = logits(2, V, "f32", 2.0, seed=9)
+    u = np.array([0.25, 0.9])
+    check(z, u)
+    check(z, u, None, np.array([50, V - 3]), np.array([0.9, 0.999]))
+    check(z, u, None, None, np.array([0.5, 0.95]), np.array([1e-4, 0.0]))
+
+
+def test_a_border_far_below_the_maximum():
+    """Top-k keeps elements that lie beyond the histogram's reach."""
+    V = 6000
+    z = logits(3, V, "f32", 1.0, seed=10)
+    z[:, :3000] -= 200.0
+    u, k = np.array([0.1, 0.5, 0.9]), np.array([3001, 4000, V - 1])
+    zc = z.cpu().numpy()
+    tok, probs = sv.warp_sample(z, torch.as_tensor(u).cuda(), top_k=torch.as_tensor(k, dtype=torch.int32).cuda(), probs=True)
+    for r in range(3):
+        want, _, t = warp_row(zc[r], 1.0, int(k[r]), u=float(u[r]))
+        assert int(tok[r]) == t
+        assert np.all(np.abs(probs[r].cpu().numpy() - want) <= PROB_TOL * want + 1e-29)
+    check(z, u, np.full(3, 30.0), k, np.array([0.999, 1.0, 0.5]))
+
+
+@pytest.mark.parametrize("filters", [False, True])
+def test_temperatures_at_their_limits(filters):
+    V = 4000
+    z = logits(6, V, "f32", seed=11)
+    T = torch.tensor([1e-36, 1e36, 0.9e-36, 1.1e36, float("nan"), -1.0], device="cuda")
+    u = torch.full((6,), 0.6, dtype=torch.float64, device="cuda")
+    p = torch.full((6,), 0.9, device="cuda") if filters else None
+    ws = sv.CacheWorkspace()
+    tok, probs = sv.warp_sample(z, u, temperature=T, top_p=p, probs=True, ws=ws)
+    assert ws.status() == sv.STATUS_BAD_VALUE
+    assert tok[2:].tolist() == [-1] * 4 and not bool(probs[2:].any())
+    assert int(tok[0]) == int(z[0].argmax()) and float(probs[0].max()) == 1.0
+    want, kept, t = warp_row(z[1].cpu().numpy(), float(T[1]), 0, float(p[1]) if filters else 1.0, 0.0, 0.6)
+    assert int(tok[1]) == t and np.array_equal(probs[1].cpu().numpy() > 0, kept)
+    assert np.all(np.abs(probs[1].cpu().numpy() - want) <= PROB_TOL * want)
+
+
 def test_bindings_refuse_what_does_not_fit():
     z = logits(2, 100, "f32")
     u = torch.rand(2, dtype=torch.float64, device="cuda")
