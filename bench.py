@@ -34,6 +34,7 @@ NOMINAL_HBM_GBS = 8000.0      # the ~8 TB/s nominal HBM3e figure, a second denom
 PRE_STEPS = 3                 # untimed steps issued just before the timed ones
 DEFAULT_MODE = {1: "sample", 2: "greedy", 3: "sample", 4: "round", 5: "sample"}
 KERNEL_SOURCES = [
+    "speculative_decoding_verification_08_gb300/csrc/sv_barrier.cuh",
     "speculative_decoding_verification_08_gb300/csrc/sv_device.cuh",
     "speculative_decoding_verification_08_gb300/csrc/sv_tma.cuh",
     "speculative_decoding_verification_08_gb300/csrc/sv_item.cuh",
