@@ -4,7 +4,8 @@ Python binding of ``libspecverify.so`` (C ABI in ``include/specverify.h``).
 This module only marshals arguments: torch CUDA tensors are checked for
 dtype, device and layout and their pointers, strides and the current CUDA
 stream are passed to the library, whose kernels do every step of the
-verification.  There is no CPU path: if the library is missing or a tensor is
+verification (for append_kv, paged_attention and warp_sample a small C++
+extension does so, ``csrc/tensors.cpp``).  There is no CPU path: if the library is missing or a tensor is
 not on a CUDA device, the call raises.
 
 The operation is the one on the "spec-verify" page (Hugging Face kernels page
@@ -16,8 +17,9 @@ sequences, plus the speculative-sampling rule of section "Method".
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 from . import _build
@@ -61,7 +63,8 @@ class SpecVerifyError(RuntimeError):
 
 
 def build(force: bool = False) -> str:
-    """Compiles libspecverify.so in-tree (nvcc, sm_103a)."""
+    """Compiles libspecverify.so in-tree (nvcc, sm_103a) and the extension
+    beside it."""
     return _build.build(force=force)
 
 
@@ -567,84 +570,38 @@ def _cache_ws(ws, device, raw, stream):
     return w
 
 
-_CACHE_TYPES = None
+_tensors = None
 
 
-def _cache_dtype(dtype, name) -> int:
-    global _CACHE_TYPES
-    if _CACHE_TYPES is None:
-        torch = _torch()
-        _CACHE_TYPES = {torch.bfloat16: 1, torch.float16: 2}
-    code = _CACHE_TYPES.get(dtype)
-    if code is None:
-        raise SpecVerifyError(f"{name} must be torch.bfloat16 or torch.float16, got {dtype}")
-    return code
+def _native():
+    """The extension that checks the tensors of these calls and hands them to
+    the library."""
+    global _tensors
+    lib = load()
+    with _lock:
+        if _tensors is None:
+            _torch()
+            if not os.path.exists(_build.EXTENSION):
+                raise SpecVerifyError(f"{_build.EXTENSION} is missing: build it with "
+                                      "speculative_decoding_verification_08_gb300.build()")
+            loader = importlib.machinery.ExtensionFileLoader(__name__ + "._tensors", _build.EXTENSION)
+            spec = importlib.util.spec_from_file_location(loader.name, _build.EXTENSION, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                          for f in (lib.sv_append_kv, lib.sv_paged_attention, lib.sv_warp_sample)),
+                        SpecVerifyError, _check)
+            _tensors = module
+        return _tensors
 
 
-# sv_paged_cache and a token array's strides as bytes: one packing call each,
-# where a ctypes structure would be filled field by field
-_PACK_CACHE = struct.Struct("@QQ3q3q8iQqQQ").pack
-_PACK_2 = struct.Struct("@2q").pack
-
-
-def _heads3(x, dtype, device, heads, D, N, name):
-    """A token array [N][heads][D] of the cache's type and device: its packed
-    strides."""
-    if x.dtype is not dtype or x.get_device() != device:
-        raise SpecVerifyError(f"{name} must be {dtype} on cuda:{device}, got {x.dtype} on "
-                              f"{x.device}")
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != D or shape[1] != heads or shape[0] != N:
-        raise SpecVerifyError(f"{name}: expected [{N}][{heads}][{D}], got {tuple(shape)}")
-    s = x.stride()
-    if s[2] != 1 and D > 1:
-        raise SpecVerifyError(f"{name}: the head dimension must be contiguous")
-    return _PACK_2(s[0], s[1])
-
-
-def _ints(x, n, name, device):
-    """A contiguous int32 vector of n elements on the device."""
-    if x.dtype is not _INT32 or x.get_device() != device:
-        raise SpecVerifyError(f"{name} must be torch.int32 on cuda:{device}, got {x.dtype} on "
-                              f"{x.device}")
-    if x.dim() != 1 or x.shape[0] != n or (n > 1 and x.stride(0) != 1):
-        raise SpecVerifyError(f"{name}: expected {n} contiguous elements, got {tuple(x.shape)}")
-
-
-_INT32 = None
-
-
-def _paged(k_cache, v_cache, pages, q_start, kv_len, N):
-    """The batch's sv_paged_cache, checked and packed; its type, device, heads
-    and head size."""
-    global _INT32
-    if _INT32 is None:
-        _INT32 = _torch().int32
-    dev, dtype, shape = k_cache.get_device(), k_cache.dtype, k_cache.shape
-    if dev < 0 or v_cache.get_device() != dev:
-        raise SpecVerifyError("k_cache and v_cache must be CUDA tensors on one device")
-    code = _cache_dtype(dtype, "k_cache")
-    if v_cache.dtype is not dtype or v_cache.shape != shape or len(shape) != 4:
-        raise SpecVerifyError("k_cache and v_cache must be [pages][page_size][kv_heads][head_dim] "
-                              "of one type")
-    k0, k1, k2, k3 = k_cache.stride()
-    v0, v1, v2, v3 = v_cache.stride()
-    if k3 != 1 or v3 != 1:
-        raise SpecVerifyError("the caches' head dimension must be contiguous")
-    P, ps, H, D = shape
-    B = kv_len.numel()
-    _ints(kv_len, B, "kv_len", dev)
-    _ints(q_start, B + 1, "q_start", dev)
-    if pages.dtype is not _INT32 or pages.get_device() != dev:
-        raise SpecVerifyError(f"pages must be torch.int32 on cuda:{dev}, got {pages.dtype} on "
-                              f"{pages.device}")
-    table = pages.shape
-    if len(table) != 2 or table[0] != B or (table[1] > 1 and pages.stride(1) != 1):
-        raise SpecVerifyError(f"pages: expected [{B}][max_pages] rows, got {tuple(table)}")
-    wide = table[1]
-    return _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, P, ps, H, D,
-                       code, B, N, wide, pages.data_ptr(), pages.stride(0) if B > 1 else wide,
-                       q_start.data_ptr(), kv_len.data_ptr()), dtype, dev, H, D
+def _scratch(x, name, ws, stream):
+    """(raw stream, workspace) of a call on x's device."""
+    device = x.get_device()
+    if device < 0:
+        raise SpecVerifyError(f"{name} must be a CUDA tensor")
+    raw = _raw_stream(device, stream)
+    return raw, _cache_ws(ws, device, raw, stream)
 
 
 def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, q=None,
@@ -659,37 +616,9 @@ def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, 
     [rot_dim / 2] f64 gives radians per position of each pair (None: no
     rotation); pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) when
     interleaved.  positions [N] int32 overrides the slots as positions."""
-    N = k.shape[0]
-    c, dtype, dev, H, D = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
-    kst = _heads3(k, dtype, dev, H, D, N, "k")
-    vst = _heads3(v, dtype, dev, H, D, N, "v")
-    rot = fp = pp = heads = qp = op = 0
-    qst = ost = None
-    if inv_freq is not None:
-        if inv_freq.dtype is not _torch().float64 or inv_freq.get_device() != dev or \
-                inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-            raise SpecVerifyError(f"inv_freq must be a contiguous float64 vector on cuda:{dev}")
-        rot, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-    if positions is not None:
-        _ints(positions, N, "positions", dev)
-        pp = positions.data_ptr()
-    if q is not None:
-        heads = q.shape[1] if q.dim() == 3 else 0
-        qst = _heads3(q, dtype, dev, heads, D, N, "q")
-        if q_out is None:
-            q_out = _torch().empty_like(q)
-        ost = _heads3(q_out, dtype, dev, heads, D, N, "q_out")
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise SpecVerifyError("q_out without q")
-    raw = _raw_stream(dev, stream)
-    w = _cache_ws(ws, dev, raw, stream)
-    rc = (_lib or load()).sv_append_kv(c, k.data_ptr(), kst, v.data_ptr(), vst, qp, qst, op, ost,
-                                       heads, fp, rot, 1 if interleaved else 0, pp, w.ptr,
-                                       w.nbytes, raw)
-    if rc:
-        _check(rc, "sv_append_kv")
-    return q_out
+    raw, w = _scratch(k_cache, "k_cache", ws, stream)
+    return (_tensors or _native()).append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, inv_freq, q,
+                                             q_out, positions, interleaved, w.ptr, w.nbytes, raw)
 
 
 def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, window=0,
@@ -699,30 +628,9 @@ def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, 
     window > 0, scale 1 / sqrt(D) by default; q_heads a multiple of kv_heads.
     Arrays as for append_kv.  Rows that see nothing are zeros.  Returns out
     [N][q_heads][D]."""
-    N = q.shape[0]
-    c, dtype, dev, _, D = _paged(k_cache, v_cache, pages, q_start, kv_len, N)
-    heads = q.shape[1] if q.dim() == 3 else 0
-    qst = _heads3(q, dtype, dev, heads, D, N, "q")
-    if out is None:
-        out = _torch().empty_like(q)
-    ost = _heads3(out, dtype, dev, heads, D, N, "out")
-    raw = _raw_stream(dev, stream)
-    w = _cache_ws(ws, dev, raw, stream)
-    rc = (_lib or load()).sv_paged_attention(c, q.data_ptr(), qst, out.data_ptr(), ost, heads,
-                                             D ** -0.5 if scale is None else scale, window, w.ptr,
-                                             w.nbytes, raw)
-    if rc:
-        _check(rc, "sv_paged_attention")
-    return out
-
-
-def _per_row(x, R, name, dtype, device):
-    if x is None:
-        return 0
-    if x.dtype is not dtype or x.get_device() != device or x.numel() != R or \
-            not x.is_contiguous():
-        raise SpecVerifyError(f"{name}: expected {R} contiguous {dtype} on cuda:{device}")
-    return x.data_ptr()
+    raw, w = _scratch(k_cache, "k_cache", ws, stream)
+    return (_tensors or _native()).paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, scale,
+                                                   window, out, w.ptr, w.nbytes, raw)
 
 
 def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=None, probs=False,
@@ -734,48 +642,9 @@ def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=No
     or None without u, probs [..., V] f32 or None unless probs or probs_out):
     rows as verify_sample takes them.  A row without mass or with a NaN or +inf
     logit gives token -1 and zeros."""
-    torch = _torch()
-    if not z.is_cuda:
-        raise SpecVerifyError("z must be a CUDA tensor")
-    f32 = torch.float32
-    dt = 0 if z.dtype is f32 else _cache_dtype(z.dtype, "z (or torch.float32)")
-    shape, dev = z.shape, z.get_device()
-    V, lead = shape[-1], shape[:-1]
-    z2 = z if len(shape) == 2 else z.reshape(1, V) if len(shape) == 1 else z.view(-1, V)
-    row, one = z2.stride()
-    if one != 1 and V > 1:
-        raise SpecVerifyError("z: the vocabulary dimension must be contiguous")
-    R = z2.shape[0]
-    up = _per_row(u, R, "u", torch.float64, dev)
-    tp = _per_row(temperature, R, "temperature", f32, dev)
-    kp = _per_row(top_k, R, "top_k", torch.int32, dev)
-    pp = _per_row(top_p, R, "top_p", f32, dev)
-    mp = _per_row(min_p, R, "min_p", f32, dev)
-    tok = out = 0
-    if u is not None:
-        if token_out is None:
-            token_out = torch.empty(lead, dtype=torch.int32, device=z.device)
-        else:
-            _per_row(token_out, R, "token_out", torch.int32, dev)
-        tok = token_out.data_ptr()
-    elif token_out is not None:
-        raise SpecVerifyError("token_out without u")
-    if probs or probs_out is not None:
-        if probs_out is None:
-            probs_out = torch.empty(shape, dtype=f32, device=z.device)
-        elif probs_out.dtype is not f32 or probs_out.get_device() != dev or \
-                probs_out.shape != shape or not probs_out.is_contiguous():
-            raise SpecVerifyError(f"probs_out: expected {tuple(shape)} contiguous f32 on cuda:{dev}")
-        out = probs_out.data_ptr()
-    if not tok and not out and R > 0:
-        raise SpecVerifyError("nothing to compute: give u, or ask for probs")
-    raw = _raw_stream(dev, stream)
-    w = _cache_ws(ws, dev, raw, stream)
-    rc = (_lib or load()).sv_warp_sample(z2.data_ptr(), row if R > 1 else V, dt, R, V, tp, kp, pp,
-                                         mp, up, tok, out, V, w.ptr, w.nbytes, raw)
-    if rc:
-        _check(rc, "sv_warp_sample")
-    return token_out, probs_out
+    raw, w = _scratch(z, "z", ws, stream)
+    return (_tensors or _native()).warp_sample(z, u, temperature, top_k, top_p, min_p, probs, probs_out,
+                                               token_out, w.ptr, w.nbytes, raw)
 
 
 # ---------------------------------------------------------------------------
