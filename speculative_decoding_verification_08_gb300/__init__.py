@@ -16,6 +16,7 @@ sequences, plus the speculative-sampling rule of section "Method".
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -522,7 +523,10 @@ class CacheWorkspace:
         torch = _torch()
         dev = torch.device("cuda") if device is None else torch.device(device)
         self.nbytes = int(load().sv_cache_workspace_size())
-        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+        # (from the pool of the stream it serves: what another stream still has
+        # to do with a freed block must not land in it)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
         self.ptr = self.buf.data_ptr()
         _check(load().sv_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
                "sv_workspace_init")
@@ -595,13 +599,18 @@ def _native():
         return _tensors
 
 
-def _scratch(x, name, ws, stream):
-    """(raw stream, workspace) of a call on x's device."""
+def _call(name, x, what, args, ws, stream):
+    """One call on x's device.  On a stream other than the current one the
+    outputs come from that stream's pool, as if it were current."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return _call(name, x, what, args, ws, None)
     device = x.get_device()
     if device < 0:
-        raise SpecVerifyError(f"{name} must be a CUDA tensor")
-    raw = _raw_stream(device, stream)
-    return raw, _cache_ws(ws, device, raw, stream)
+        raise SpecVerifyError(f"{what} must be a CUDA tensor")
+    raw = _raw_stream(device, None)
+    w = _cache_ws(ws, device, raw, None)
+    return getattr(_tensors or _native(), name)(*args, w.ptr, w.nbytes, raw)
 
 
 def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, q=None,
@@ -616,9 +625,9 @@ def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, 
     [rot_dim / 2] f64 gives radians per position of each pair (None: no
     rotation); pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) when
     interleaved.  positions [N] int32 overrides the slots as positions."""
-    raw, w = _scratch(k_cache, "k_cache", ws, stream)
-    return (_tensors or _native()).append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, inv_freq, q,
-                                             q_out, positions, interleaved, w.ptr, w.nbytes, raw)
+    return _call("append_kv", k_cache, "k_cache",
+                 (k, v, k_cache, v_cache, pages, q_start, kv_len, inv_freq, q, q_out, positions, interleaved),
+                 ws, stream)
 
 
 def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, window=0,
@@ -628,9 +637,8 @@ def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, 
     window > 0, scale 1 / sqrt(D) by default; q_heads a multiple of kv_heads.
     Arrays as for append_kv.  Rows that see nothing are zeros.  Returns out
     [N][q_heads][D]."""
-    raw, w = _scratch(k_cache, "k_cache", ws, stream)
-    return (_tensors or _native()).paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, scale,
-                                                   window, out, w.ptr, w.nbytes, raw)
+    return _call("paged_attention", k_cache, "k_cache",
+                 (q, k_cache, v_cache, pages, q_start, kv_len, scale, window, out), ws, stream)
 
 
 def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=None, probs=False,
@@ -642,9 +650,8 @@ def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=No
     or None without u, probs [..., V] f32 or None unless probs or probs_out):
     rows as verify_sample takes them.  A row without mass or with a NaN or +inf
     logit gives token -1 and zeros."""
-    raw, w = _scratch(z, "z", ws, stream)
-    return (_tensors or _native()).warp_sample(z, u, temperature, top_k, top_p, min_p, probs, probs_out,
-                                               token_out, w.ptr, w.nbytes, raw)
+    return _call("warp_sample", z, "z",
+                 (z, u, temperature, top_k, top_p, min_p, probs, probs_out, token_out), ws, stream)
 
 
 # ---------------------------------------------------------------------------

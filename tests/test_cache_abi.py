@@ -85,3 +85,18 @@ def test_status_words(lib):
     assert "page" in sv.status_string(sv.STATUS_BAD_PAGE)
     assert "length" in sv.status_string(sv.STATUS_BAD_LENGTH)
     assert lib.sv_cache_workspace_size() % 256 == 0
+
+
+def test_bindings_refuse_without_a_gpu(lib):
+    """What is no CUDA tensor is refused before any CUDA work."""
+    import torch
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    c = torch.zeros(2, 8, 1, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    for bad in (lambda: sv.append_kv(x, x, c, c, i, i, i), lambda: sv.paged_attention(x, c, c, i, i, i),
+                lambda: sv.warp_sample(torch.zeros(2, 8)),
+                lambda: sv._native().append_kv(x, x, c, c, i, i, i, *[None] * 4, False, 0, 0, 0),
+                lambda: sv._native().paged_attention(x, c, c, i, i, i, None, 0, None, 0, 0, 0),
+                lambda: sv._native().warp_sample(*[None] * 12), lambda: sv._native().append_kv(x)):
+        with pytest.raises(sv.SpecVerifyError):
+            bad()

@@ -195,6 +195,32 @@ def test_attention_same_bits_again_and_on_another_stream():
     assert torch.equal(a, b)
 
 
+def test_outputs_on_another_stream_come_from_its_own_memory():
+    """A block that the current stream has freed but not finished with is not
+    handed out as the output of a call on another stream."""
+    cb = CacheBatch([(40, 300), (1, 77)], 2, 128, 64, BF, seed=5)
+    q, k, v = cb.tokens(8), cb.tokens(2), cb.tokens(2)
+    z, u = torch.randn(41, 1024, device="cuda"), torch.rand(41, dtype=torch.float64, device="cuda")
+    big = torch.zeros(1 << 27, device="cuda")
+    calls = [lambda **kw: sv.append_kv(k, v, *cb.args(), inv_freq=freqs(128), q=q, **kw),
+             lambda **kw: sv.paged_attention(q, *cb.args(), **kw),
+             lambda **kw: sv.warp_sample(z, u, probs=True, **kw)[1]]
+    want = [f() for f in calls]
+    s = torch.cuda.Stream()
+    for f in calls:
+        f(stream=s)                         # workspace of this stream
+    torch.cuda.synchronize()
+    for f, w in zip(calls, want):
+        late = torch.empty_like(w)
+        for _ in range(20):
+            big.add_(1)                     # some milliseconds
+        late.fill_(9)
+        del late
+        got = f(stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, w)
+
+
 def test_attention_large_scores_and_scale():
     """Scores in the thousands: one key takes all the weight, nothing overflows."""
     cb = CacheBatch([(6, 400), (130, 260)], 1, 64, 16, HF, seed=6, spread=12.0)
