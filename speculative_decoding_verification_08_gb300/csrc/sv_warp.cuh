@@ -1082,8 +1082,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
     const bool near = kHeld && dense && fabsf(m) <= kNear * temp;
     const int octave = near ? near_octave(m, S) : 0;
     const NearScale N = near_scale(S, temp, octave);
-    // (below this no element can have t <= t_last: t_of's rounding is half a bin)
-    const float z_last = m - (t_last - kMagic + 1.f) / per;
+    // (below this no element can have t <= t_last: t_of's rounding is half a bin,
+    // and only the last bin has no lower end)
+    const float z_last = t_last >= never - 1.f ? -INFINITY : m - (t_last - kMagic + 1.f) / per;
     Mass2 near_all;
     Mass near_above, near_kept;
 #pragma unroll 1

@@ -265,6 +265,20 @@ def test_borders_of_many_equal_logits(step):
     check(z, u, np.full(R, 0.8), k, p, np.full(R, 1e-4))
 
 
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("V", [40, 310, 1913, 30011])
+def test_a_nucleus_that_reaches_the_smallest_logits(dt, V):
+    """Flat rows and top-p near one: the border lies among the smallest logits,
+    below what the histogram's scale was taken from."""
+    R = 8
+    z = logits(R, V, dt, 3.0, seed=V + 1)
+    T = np.array([1.0, 7.5, 17.0, 23.0, 42.0, 45.0, 70.0, 1000.0])
+    u = np.linspace(0.01, 0.99, R)
+    for p in (0.98, 0.999, 0.99999):
+        check(z, u, T, None, np.full(R, p))
+        check(z, u, T, None, np.full(R, p), np.full(R, 1e-7))
+
+
 def test_rows_larger_than_shared_memory():
     V = 2_000_003
     z = logits(2, V, "f32", 2.0, seed=9)
