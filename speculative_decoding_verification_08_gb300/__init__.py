@@ -526,6 +526,7 @@ class CacheWorkspace:
         # (from the pool of the stream it serves: what another stream still has
         # to do with a freed block must not land in it)
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            _no_capture("is zeroed once, when it is made: make it before the capture")
             self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
         self.ptr = self.buf.data_ptr()
         _check(load().sv_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
@@ -539,9 +540,15 @@ class CacheWorkspace:
         return int(out.value)
 
 
+def _no_capture(what):
+    if _torch_c()._cuda_isCurrentStreamCapturing():
+        raise SpecVerifyError(f"a CacheWorkspace {what}")
+
+
 def cache_workspace(device=None, stream=None) -> CacheWorkspace:
     """The workspace that calls without one share on this device and stream
-    (calls on different streams never share an implicit one)."""
+    (calls on different streams never share an implicit one, and a call that is
+    captured into a graph has none)."""
     torch = _torch()
     dev = torch.cuda.current_device() if device is None else torch.device(device).index
     return _cache_ws(None, dev, _raw_stream(dev, stream), stream)
@@ -567,6 +574,9 @@ def _torch_c():
 def _cache_ws(ws, device, raw, stream):
     if ws is not None:
         return ws
+    # (a graph keeps the workspace's address and may be replayed on any stream,
+    # beside other graphs)
+    _no_capture("of its own is needed by a captured call: pass ws=, made before the capture")
     key = (device, raw)
     w = _ws_cache.get(key)
     if w is None:

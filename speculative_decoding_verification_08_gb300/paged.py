@@ -92,15 +92,16 @@ class PagedCache:
             raise SpecVerifyError("begin() comes first")
         return self._batch
 
-    def append(self, layer: int, q, k, v):
-        """Writes the pass's keys and values of a layer; returns q rotated."""
+    def append(self, layer: int, q, k, v, ws=None):
+        """Writes the pass's keys and values of a layer; returns q rotated.
+        (ws as for ``append_kv``: a pass captured into a graph needs one.)"""
         return append_kv(k, v, self.k[layer], self.v[layer], *self._pass(), inv_freq=self.inv_freq,
-                         q=q, interleaved=self.interleaved)
+                         q=q, interleaved=self.interleaved, ws=ws)
 
-    def attend(self, layer: int, q, scale: Optional[float] = None, window: int = 0):
+    def attend(self, layer: int, q, scale: Optional[float] = None, window: int = 0, ws=None):
         """The pass's queries over a layer of the cache."""
         return paged_attention(q, self.k[layer], self.v[layer], *self._pass(), scale=scale,
-                               window=window)
+                               window=window, ws=ws)
 
     def rollback(self, seq, n: int) -> None:
         """Drops a sequence's last n tokens."""

@@ -1,0 +1,77 @@
+"""append_kv and paged_attention where the usual batches do not go."""
+import pytest
+import torch
+
+import speculative_decoding_verification_08_gb300 as sv
+from speculative_decoding_verification_08_gb300 import paged as sv_paged
+from cache_refs import CacheBatch, attention, default_scale
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.build()
+    return sv.load()
+
+
+def within(got, want, tol):
+    off = (got.cpu().double() - want).abs()
+    bad = ~(off <= tol)
+    assert not bool(bad.any()), f"{int(bad.sum())} values off, worst {float(off.max())}"
+
+
+def test_a_captured_call_needs_a_workspace_of_its_own():
+    """A graph keeps the workspace's address and may be replayed anywhere, and a
+    workspace made during a capture would be zeroed by that graph alone: calls
+    without one are refused while the stream is captured."""
+    cb = CacheBatch([(3, 700), (2, 33)], 2, 64, 16, BF, seed=20)
+    q, k, v = cb.tokens(4), cb.tokens(2), cb.tokens(2)
+    z, u = torch.randn(3, 500, device="cuda"), torch.rand(3, dtype=torch.float64, device="cuda")
+    calls = [lambda **kw: sv.append_kv(k, v, *cb.args(), q=q, **kw),
+             lambda **kw: sv.paged_attention(q, *cb.args(), **kw),
+             lambda **kw: sv.warp_sample(z, u, **kw)]
+    used = torch.cuda.Stream()                        # a stream that has an implicit workspace already
+    for f in calls:
+        f(stream=used)
+    torch.cuda.synchronize()
+    for where in ({}, {"stream": used}):
+        for f in calls:
+            with pytest.raises(sv.SpecVerifyError, match="ws="):
+                with torch.cuda.graph(torch.cuda.CUDAGraph(), **where):
+                    f()
+    for f in (sv.CacheWorkspace, sv.cache_workspace, lambda: sv.CacheWorkspace(stream=used)):
+        with pytest.raises(sv.SpecVerifyError, match="capture"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=used):
+                f()
+    torch.cuda.synchronize()
+    want = sv.paged_attention(q, *cb.args())
+    # two graphs, each with its workspace, in either order
+    graphs = []
+    for _ in range(2):
+        ws, out, g = sv.CacheWorkspace(), torch.empty_like(q), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sv.paged_attention(q, *cb.args(), out=out, ws=ws)
+        graphs.append((g, out, ws))
+    for g, out, ws in reversed(graphs):
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert ws.status() == 0 and torch.equal(out, want)
+
+
+def test_a_captured_pass_over_a_paged_cache():
+    c = sv_paged.PagedCache(1, 8, 16, 2, 64)
+    g = torch.Generator().manual_seed(25)
+    q, k, v = (torch.randn(5, h, 64, generator=g).to(BF).cuda() for h in (4, 2, 2))
+    c.begin({0: 5})
+    want = c.attend(0, c.append(0, q, k, v))
+    c.k.zero_()
+    graph, ws = torch.cuda.CUDAGraph(), sv.CacheWorkspace()
+    with torch.cuda.graph(graph):
+        got = c.attend(0, c.append(0, q, k, v, ws=ws), ws=ws)
+    graph.replay()
+    assert ws.status() == 0 and torch.equal(got, want)
