@@ -264,8 +264,9 @@ int sv_alpha(const float *p, int64_t p_row_stride, const float *q, int64_t q_row
  * The target pass of a round: a paged cache of keys and values, attention of
  * the new tokens over it, and the warp of logits into probability rows.  The
  * pages have no counterpart to these calls; they make the rows that the
- * verification calls above take.  All arrays are device memory (else
- * SV_EINVAL).  The calls share a workspace of their own kind:
+ * verification calls above take.  All arrays are memory of the current
+ * device or managed memory (else SV_EINVAL; the workspace: SV_EWORKSPACE).
+ * The calls share a workspace of their own kind:
  * sv_cache_workspace_size() bytes, 256-byte aligned, zeroed once with
  * sv_workspace_init, one call at a time in stream order, status read with
  * sv_get_status.  A workspace of the verification calls does not serve here,

@@ -521,23 +521,37 @@ class CacheWorkspace:
 
     def __init__(self, device=None, stream=None):
         torch = _torch()
-        dev = torch.device("cuda") if device is None else torch.device(device)
         self.nbytes = int(load().sv_cache_workspace_size())
+        dev = _cuda_index(device, stream)
         # (from the pool of the stream it serves: what another stream still has
         # to do with a freed block must not land in it)
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with torch.cuda.device(dev), _on(stream):
             _no_capture("is zeroed once, when it is made: make it before the capture")
-            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
-        self.ptr = self.buf.data_ptr()
-        _check(load().sv_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
-               "sv_workspace_init")
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+            self.ptr = self.buf.data_ptr()
+            _check(load().sv_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
+                   "sv_workspace_init")
 
     def status(self, stream=None) -> int:
         """Waits for the stream and returns (and clears) the device status bits."""
         out = ctypes.c_uint32(0)
-        _check(load().sv_get_status(self.ptr, _stream_handle(stream), ctypes.byref(out)),
-               "sv_get_status")
+        with _torch().cuda.device(self.buf.device):
+            _check(load().sv_get_status(self.ptr, _stream_handle(stream), ctypes.byref(out)),
+                   "sv_get_status")
         return int(out.value)
+
+
+def _on(stream):
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _cuda_index(device, stream) -> int:
+    """The device meant: the one named, else the stream's, else the current one."""
+    torch = _torch()
+    index = None if device is None else torch.device(device).index
+    if index is None and stream is not None:
+        index = stream.device.index
+    return torch.cuda.current_device() if index is None else index
 
 
 def _no_capture(what):
@@ -549,8 +563,7 @@ def cache_workspace(device=None, stream=None) -> CacheWorkspace:
     """The workspace that calls without one share on this device and stream
     (calls on different streams never share an implicit one, and a call that is
     captured into a graph has none)."""
-    torch = _torch()
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    dev = _cuda_index(device, stream)
     return _cache_ws(None, dev, _raw_stream(dev, stream), stream)
 
 
@@ -610,8 +623,9 @@ def _native():
 
 
 def _call(name, x, what, args, ws, stream):
-    """One call on x's device.  On a stream other than the current one the
-    outputs come from that stream's pool, as if it were current."""
+    """One call on x's device and, unless one is given, its current stream.  On a
+    stream other than the current one the outputs come from that stream's pool,
+    as if it were current."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return _call(name, x, what, args, ws, None)

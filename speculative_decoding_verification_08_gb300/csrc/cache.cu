@@ -18,14 +18,8 @@ constexpr int kSms = 152;
 
 using svhost::g_last_grid;
 using svhost::g_last_kernels;
+using svhost::CurrentDevice;
 using svhost::kAlign;
-using svhost::kOnDevice;
-using svhost::place;
-
-bool on_device(const void *p) {
-    const void *x = p;
-    return p && place(x) == kOnDevice;
-}
 
 bool vec_ok(const void *p, const int64_t *st, int n) {
     if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return false;
@@ -51,13 +45,13 @@ int check_cache(const sv_paged_cache *c) {
 
 // Checks where the workspace and the cache's arrays live, and fills in the
 // batch the device sees.
-int bind_cache(const sv_paged_cache *c, void *ws, size_t ws_bytes, sv::Batch &b) {
+int bind_cache(const CurrentDevice &here, const sv_paged_cache *c, void *ws, size_t ws_bytes, sv::Batch &b) {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0 ||
         ws_bytes < sv_cache_workspace_size())
         return SV_EWORKSPACE;
-    if (!on_device(ws)) return SV_EWORKSPACE;
-    if (!on_device(c->k) || !on_device(c->v) || !on_device(c->pages) || !on_device(c->q_start) ||
-        !on_device(c->kv_len))
+    if (!here.holds(ws)) return SV_EWORKSPACE;
+    if (!here.holds(c->k) || !here.holds(c->v) || !here.holds(c->pages) || !here.holds(c->q_start) ||
+        !here.holds(c->kv_len))
         return SV_EINVAL;
     b.pages = c->pages;
     b.pages_stride = c->pages_stride;
@@ -246,10 +240,10 @@ int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_st
     if (q && (!q_out || !q_stride || !q_out_stride || !vec_ok(q, q_stride, 2) ||
               !vec_ok(q_out, q_out_stride, 2)))
         return SV_EINVAL;
-    if ((rc = bind_cache(cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
-    if (!on_device(k) || !on_device(v) || (q && (!on_device(q) || !on_device(q_out))))
-        return SV_EINVAL;
-    if ((inv_freq && !on_device(inv_freq)) || (positions && !on_device(positions)))
+    const CurrentDevice here;
+    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!here.holds(k) || !here.holds(v) || (q && (!here.holds(q) || !here.holds(q_out))) ||
+        !here.holds_or_null(inv_freq) || !here.holds_or_null(positions))
         return SV_EINVAL;
     A.k = k;
     A.v = v;
@@ -307,8 +301,9 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
     if (!q || !out || !q_stride || !out_stride || !vec_ok(q, q_stride, 2) ||
         !vec_ok(out, out_stride, 2))
         return SV_EINVAL;
-    if ((rc = bind_cache(cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
-    if (!on_device(q) || !on_device(out)) return SV_EINVAL;
+    const CurrentDevice here;
+    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!here.holds(q) || !here.holds(out)) return SV_EINVAL;
     A.q = q;
     A.out = out;
     for (int i = 0; i < 2; ++i) {

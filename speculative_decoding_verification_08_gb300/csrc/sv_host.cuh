@@ -59,4 +59,26 @@ Residence place(T *&ptr) {
     return kOnHost;
 }
 
+// The device that this thread's launches go to.  A kernel there is handed memory
+// of that device (or managed memory, which is every device's) and no other's.
+struct CurrentDevice {
+    int id = -1;
+    CurrentDevice() {
+        if (cudaGetDevice(&id) != cudaSuccess) {
+            cudaGetLastError();
+            id = -1;
+        }
+    }
+    bool holds(const void *p) const {
+        if (!p || id < 0) return false;
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == id);
+    }
+    bool holds_or_null(const void *p) const { return !p || holds(p); }
+};
+
 }  // namespace svhost

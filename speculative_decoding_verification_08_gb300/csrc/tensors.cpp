@@ -6,12 +6,14 @@
 // reading some sixty tensor attributes from Python takes three times as long
 // (one token appended: 18.7 us of host time from Python, of which the C call is
 // 3.9).  Nothing is computed here, and there is no path without the library:
-// its entry points are handed over by bind().
+// its entry points are handed over by bind().  Each call runs with its tensors'
+// device as the current one.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/DeviceGuard.h>
 
 #include <cmath>
 #include <limits>
@@ -160,6 +162,7 @@ PyObject *append_kv(PyObject *const *a) {
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
     const int64_t N = rows_of(k, "k");
     const Paged P(a[2], a[3], a[4], a[5], a[6], N);
+    const c10::DeviceGuard here(tensor(a[2], "k_cache").device());
     const Heads hk(k, P, P.c.kv_heads, "k"), hv(v, P, P.c.kv_heads, "v");
     const double *freq = nullptr;
     int64_t rot = 0;
@@ -198,6 +201,7 @@ PyObject *paged_attention(PyObject *const *a) {
     const at::Tensor &q = tensor(a[0], "q");
     const int64_t N = rows_of(q, "q"), heads = q.size(1);
     const Paged P(a[1], a[2], a[3], a[4], a[5], N);
+    const c10::DeviceGuard here(tensor(a[1], "k_cache").device());
     const Heads hq(q, P, heads, "q");
     at::Tensor made;
     if (a[8] == Py_None) made = at::empty_like(q);
@@ -220,6 +224,7 @@ PyObject *warp_sample(PyObject *const *a) {
     const at::Tensor &given = tensor(a[0], "z");
     const int64_t dev = given.get_device();
     if (dev < 0) refuse("z must be a CUDA tensor");
+    const c10::DeviceGuard here(given.device());
     const at::ScalarType type = given.scalar_type();
     if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
         refuse("z must be torch.float32, torch.bfloat16 or torch.float16, got ", type);

@@ -21,13 +21,6 @@ constexpr int kSharedWords = 4096 + 1;
 constexpr int kMaxWords = (227 * 1024 - (int)sizeof(sv::WarpShared)) / 16;
 
 using svhost::kAlign;
-using svhost::kOnDevice;
-using svhost::place;
-
-bool on_device(const void *p) {
-    const void *x = p;
-    return place(x) == kOnDevice;  // true for null: optional arrays
-}
 
 int launch_clusters(void (*kernel)(sv::WarpParams), const sv::WarpParams &A, int c, int threads, size_t bytes,
                     cudaStream_t st) {
@@ -109,12 +102,13 @@ extern "C" int sv_warp_sample(const void *z, int64_t z_row_stride, int32_t z_dty
     if (!z || z_row_stride < V || (!token && !probs) || (token && !u) ||
         (probs && probs_row_stride < V))
         return SV_EINVAL;
+    const svhost::CurrentDevice here;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
-        workspace_bytes < sv_cache_workspace_size() || !on_device(workspace))
+        workspace_bytes < sv_cache_workspace_size() || !here.holds(workspace))
         return SV_EWORKSPACE;
-    if (!on_device(z) || !on_device(temperature) || !on_device(top_k) || !on_device(top_p) ||
-        !on_device(min_p) || !on_device(u) || !on_device(token) || !on_device(probs))
-        return SV_EINVAL;
+    for (const void *p : {z, (const void *)temperature, (const void *)top_k, (const void *)top_p, (const void *)min_p,
+                          (const void *)u, (const void *)token, (const void *)probs})
+        if (!here.holds_or_null(p)) return SV_EINVAL;
     sv::WarpParams A{};
     A.z = z;
     A.zs = z_row_stride;
