@@ -75,3 +75,13 @@ def test_a_captured_pass_over_a_paged_cache():
         got = c.attend(0, c.append(0, q, k, v, ws=ws), ws=ws)
     graph.replay()
     assert ws.status() == 0 and torch.equal(got, want)
+
+
+def test_the_implicit_workspace_by_any_name_of_the_device():
+    want = sv.cache_workspace()
+    assert sv.cache_workspace("cuda") is want
+    assert sv.cache_workspace("cuda:0") is want
+    assert sv.cache_workspace(torch.device("cuda")) is want
+    s = torch.cuda.Stream()
+    assert sv.cache_workspace("cuda", stream=s) is sv.cache_workspace(stream=s)
+    assert sv.cache_workspace(stream=s) is not want
