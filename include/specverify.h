@@ -56,7 +56,8 @@
  *                            next_token = -1 for that sequence;
  *       SV_STATUS_ZERO_MASS  the distribution to draw from has zero mass;
  *       SV_STATUS_OVERFLOW   a commit would pass max_len (nothing written);
- *                            from sv_verify_sample_logits: its workspace
+ *                            from sv_verify_sample_logits and
+ *                            sv_paged_attention: the workspace
  *                            held a count it cannot have left there (a
  *                            workspace reused without re-initialising it
  *                            after SV_STATUS_TIMEOUT, or overwritten);

@@ -529,15 +529,24 @@ class CacheWorkspace:
             _no_capture("is zeroed once, when it is made: make it before the capture")
             self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
             self.ptr = self.buf.data_ptr()
+            self.reset(stream)
+
+    def reset(self, stream=None):
+        """Zeroes the workspace, in stream order."""
+        with _torch().cuda.device(self.buf.device):
             _check(load().sv_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
                    "sv_workspace_init")
 
     def status(self, stream=None) -> int:
-        """Waits for the stream and returns (and clears) the device status bits."""
+        """Waits for the stream and returns (and clears) the device status bits.
+        After STATUS_TIMEOUT or STATUS_OVERFLOW the workspace is zeroed as well:
+        counts that a call did not finish are left in it."""
         out = ctypes.c_uint32(0)
         with _torch().cuda.device(self.buf.device):
             _check(load().sv_get_status(self.ptr, _stream_handle(stream), ctypes.byref(out)),
                    "sv_get_status")
+        if out.value & (STATUS_TIMEOUT | STATUS_OVERFLOW):
+            self.reset(stream)
         return int(out.value)
 
 

@@ -996,8 +996,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     __threadfence();   // the group's writes, after the meeting
                     uint32_t *c = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters) +
                                   2 * p.first + g;
-                    const bool last = atomicAdd(c, 1u) == (uint32_t)p.parts - 1;
+                    const uint32_t before = atomicAdd(c, 1u);
+                    const bool last = before == (uint32_t)p.parts - 1;
                     if (last) *c = 0;
+                    // no call leaves such a count: the workspace was not initialised
+                    if (before >= (uint32_t)p.parts) atomicOr(status, SV_STATUS_OVERFLOW);
                     sh.last[g] = last;
                 }
                 meet(sh, &sh.group_sync[g], group_turn, lane, status);

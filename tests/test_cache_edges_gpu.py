@@ -85,3 +85,22 @@ def test_the_implicit_workspace_by_any_name_of_the_device():
     s = torch.cuda.Stream()
     assert sv.cache_workspace("cuda", stream=s) is sv.cache_workspace(stream=s)
     assert sv.cache_workspace(stream=s) is not want
+
+
+def test_counts_left_in_a_workspace_are_reported_and_cleared():
+    """The tiles' counters (two per CTA from byte 256 on) hold what no call
+    leaves there: the call says so, and the next one is right."""
+    cb = CacheBatch([(6, 3000), (2, 700)], 2, 64, 16, BF, seed=24)
+    q = cb.tokens(4)
+    want, tol = attention(cb, q, default_scale(64), 0)
+    ws = sv.CacheWorkspace()
+    counters = ws.buf[256:256 + 4 * 2 * 160].view(torch.int32)
+    for clear in (ws.status, lambda: (ws.reset(), ws.status())[1]):
+        counters.fill_(1 << 20)
+        sv.paged_attention(q, *cb.args(), ws=ws)
+        assert clear() == (sv.STATUS_OVERFLOW if clear == ws.status else 0)
+        assert not bool(counters.any())
+        got = sv.paged_attention(q, *cb.args(), ws=ws)
+        assert ws.status() == 0
+        within(got, want, tol)
+        assert not bool(counters.any())
