@@ -58,6 +58,12 @@
 #include "sv_cache.cuh"
 #include "sv_tc.cuh"
 
+// 1: a build for the test of the bounded waits.  Every other CTA's scheduler stops
+// after its first piece, without a word: the other warps wait for what never comes.
+#ifndef SV_STALL
+#define SV_STALL 0
+#endif
+
 namespace sv {
 
 constexpr int kAttendThreads = 384;
@@ -520,6 +526,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 Piece p;
                 more = walk.next(A, p);
                 if (!more) p.n = -1;
+                if (SV_STALL && k == 1 && blockIdx.x % 2 == 1) break;
                 // (after a timeout the readers stop at the first piece they miss)
                 if (!__all_sync(0xffffffffu, hold(sh, &sh.piece_empty[k], turn, status))) break;
                 if (lane == 0) {
@@ -598,14 +605,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 }
             }
             // the last fills must have been taken before the CTA may end; after a
-            // wait gave up, they must at least have landed
-            if (*(volatile int32_t *)&sh.dead) {
+            // wait gave up, here or elsewhere, they must at least have landed
+            for (int k = max(0, it - L::kStages); k < it; ++k)
+                hold(sh, &sh.empty[k % L::kStages], (k / L::kStages) & 1, status);
+            if (*(volatile int32_t *)&sh.dead)
                 for (int k = max(0, it - L::kStages); k < it; ++k)
                     mbar_wait(&sh.full[k % L::kStages], (k / L::kStages) & 1);
-            } else {
-                for (int k = max(0, it - L::kStages); k < it; ++k)
-                    hold(sh, &sh.empty[k % L::kStages], (k / L::kStages) & 1, status);
-            }
         } else if (warp == 9) {
             // ---- products -----------------------------------------------------
             const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
@@ -616,9 +621,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const uint64_t k_desc = tc::smem_desc(ring_at, 16, 1024);
             const uint64_t v_desc = tc::smem_desc(ring_at, kHalfBytes, 1024);
             // (a descriptor's start address is in units of 16 bytes)
+            // Once a fill did not come, nothing is handed back any more: a stage or a
+            // query tile that is still being filled must not be filled again.
+            // (Each lane's own; the elected one's counts.)
+            bool filled = true;
             auto acquire = [&]() -> int {  // the next stage, filled
                 const int x = st;
-                hold(sh, &sh.full[x], turn, status);
+                if (!hold(sh, &sh.full[x], turn, status)) filled = false;
                 if (++st == L::kStages) {
                     st = 0;
                     turn ^= 1;
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 return x;
             };
             auto release = [&](int x) {
-                if (tc::elect()) tc::commit(&sh.empty[x]);
+                if (tc::elect() && filled) tc::commit(&sh.empty[x]);
             };
             auto scores = [&](auto gc, int x, bool last) {  // S_g = Q_g K^T
                 constexpr int g = decltype(gc)::value;
@@ -640,7 +649,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                                    k > 0);
                     }
                     tc::commit(&sh.s_full[g]);
-                    if (last) tc::commit(&sh.q_free[g]);
+                    if (last && filled) tc::commit(&sh.q_free[g]);
                 }
                 __syncwarp();
             };
@@ -686,13 +695,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 const bool split = tc::uniform(p->split);
                 reader.done(sh, lane);
                 if (blocks == 0) continue;
-                hold(sh, &sh.q_full[0], qn0++ & 1, status);
+                if (!hold(sh, &sh.q_full[0], qn0++ & 1, status)) filled = false;
                 if (split) {
                     int x = acquire();
                     scores(g0, x, blocks <= 2);
                     release(x);
                     if (n1 > 0) {
-                        hold(sh, &sh.q_full[1], qn1++ & 1, status);
+                        if (!hold(sh, &sh.q_full[1], qn1++ & 1, status)) filled = false;
                         x = acquire();
                         scores(g1, x, blocks <= 3);
                         release(x);
@@ -716,7 +725,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         if (i + 1 < blocks) step(g1, i + 1);
                     }
                 } else {
-                    hold(sh, &sh.q_full[1], qn1++ & 1, status);
+                    if (!hold(sh, &sh.q_full[1], qn1++ & 1, status)) filled = false;
                     int ks = acquire();
                     scores(g0, ks, blocks == 1);
                     scores(g1, ks, blocks == 1);

@@ -1,9 +1,12 @@
 """append_kv and paged_attention where the usual batches do not go."""
+import contextlib
+import ctypes
+
 import pytest
 import torch
 
 import speculative_decoding_verification_08_gb300 as sv
-from speculative_decoding_verification_08_gb300 import paged as sv_paged
+from speculative_decoding_verification_08_gb300 import _build, paged as sv_paged
 from cache_refs import CacheBatch, attention, default_scale
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +107,39 @@ def test_counts_left_in_a_workspace_are_reported_and_cleared():
         assert ws.status() == 0
         within(got, want, tol)
         assert not bool(counters.any())
+
+
+@pytest.fixture(scope="module")
+def stalled(tmp_path_factory):
+    """The entry points of a build whose attention leaves waits unanswered
+    (SV_STALL=1); the extension calls them inside `with`."""
+    out = str(tmp_path_factory.mktemp("specverify_stall") / "libspecverify_stall.so")
+    other = sv._declare(ctypes.CDLL(_build.build_variant(out, ["-DSV_STALL=1"])))
+
+    @contextlib.contextmanager
+    def bound():
+        def bind(lib):
+            sv._native().bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                                for f in (lib.sv_append_kv, lib.sv_paged_attention, lib.sv_warp_sample)),
+                              sv.SpecVerifyError, sv._check)
+        bind(other)
+        try:
+            yield
+        finally:
+            bind(sv.load())
+    return bound
+
+
+@pytest.mark.parametrize("group", [2, 3])             # queries by tensor copies, and by the threads
+def test_a_wait_that_runs_out_is_reported_and_the_workspace_serves_again(stalled, group):
+    cb = CacheBatch([(6, 880 + b) for b in range(60)] + [(150, 400)] * 8, 2, 64, 16, BF, seed=26)
+    q = cb.tokens(2 * group)
+    ws = sv.CacheWorkspace()
+    want = sv.paged_attention(q, *cb.args(), ws=ws)
+    assert ws.status() == 0
+    for _ in range(2):
+        with stalled():
+            sv.paged_attention(q, *cb.args(), ws=ws)
+        assert ws.status() == sv.STATUS_TIMEOUT
+        got = sv.paged_attention(q, *cb.args(), ws=ws)
+        assert ws.status() == 0 and torch.equal(got, want)
