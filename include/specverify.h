@@ -337,7 +337,8 @@ int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_st
  *   out[t][h] = sum_s softmax_s(scale * q[t][h] . k[s][g]) v[s][g],
  * g = h / (q_heads / kv_heads), over the slots s <= kv_len[b] - n + j of
  * token j of n (causal), and s > kv_len[b] - n + j - window when window > 0.
- * A row that sees no slot is written as zeros.  q and out are
+ * A row that sees no slot is written as zeros; one whose query holds a NaN and
+ * that sees a slot, as NaN (a scale of 0 reads no queries).  q and out are
  * [tokens][q_heads][head_dim] of the cache's type, strides as for
  * sv_append_kv; q_heads is a multiple of kv_heads.  scale must be finite.
  * Products are accumulated and the softmax's statistics kept in fp32; the

@@ -1025,7 +1025,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     if (strip < strips) {
                         uint16_t *co = row_of(r);
                         // kBatch parts' loads in flight; a part past the last
-                        // one is the last once more, with no weight
+                        // one is the last once more, with no weight.  (A part
+                        // whose row saw nothing has the sum 0; a query of NaN
+                        // leaves a sum of NaN and no reference.)
                         constexpr int kBatch = 8;
                         float top = -INFINITY, all = 0.f;
 #pragma unroll 1
@@ -1040,7 +1042,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             all *= top == -INFINITY ? 0.f : ex2(top - m);
 #pragma unroll
                             for (int i = 0; i < kBatch; ++i)
-                                if (i0 + i < p.parts && x[i].x != -INFINITY) all += x[i].y * ex2(x[i].x - m);
+                                if (i0 + i < p.parts && x[i].y != 0.f) all += x[i].y * ex2(x[i].x - m);
                             top = m;
                         }
                         const float norm = all > 0.f ? 1.f / all : 0.f;

@@ -143,3 +143,22 @@ def test_a_wait_that_runs_out_is_reported_and_the_workspace_serves_again(stalled
         assert ws.status() == sv.STATUS_TIMEOUT
         got = sv.paged_attention(q, *cb.args(), ws=ws)
         assert ws.status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("seqs", [[(2, 3000), (40, 300)],          # few tiles, cut between CTAs
+                                  [(2, 40 + b % 7) for b in range(400)] + [(130, 200)]])
+@pytest.mark.parametrize("group", [2, 3])
+def test_a_nan_query_gives_nan_whatever_the_cut(seqs, group):
+    cb = CacheBatch(seqs, 2, 64, 16, BF, seed=21)
+    q = cb.tokens(2 * group)
+    want, tol = attention(cb, q, default_scale(64), 0)
+    rows = [(0, 1), (3, 0), (cb.N - 1, 2)]            # (token, head)
+    for t, h in rows:
+        q[t, h, 5] = float("nan")
+    ws = sv.CacheWorkspace()
+    got = sv.paged_attention(q, *cb.args(), ws=ws)
+    assert ws.status() == 0
+    for t, h in rows:
+        assert bool(torch.isnan(got[t, h]).all()), (t, h)
+        got[t, h], want[t, h] = 0.0, 0.0
+    within(got, want, tol)
