@@ -342,7 +342,8 @@ int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_st
  * [tokens][q_heads][head_dim] of the cache's type, strides as for
  * sv_append_kv; q_heads is a multiple of kv_heads.  scale must be finite.
  * Products are accumulated and the softmax's statistics kept in fp32; the
- * weights are rounded to the cache's type for the product with v.  What an
+ * weights are rounded to the cache's type for the product with v (SV_F16:
+ * those below 2^-21 of the row's largest to steps of 2^-31 of it).  What an
  * unused slot of a page holds does not matter (NaN included); slots inside a
  * sequence's length must be finite.  With a window, pages that lie wholly
  * before every row's window are not read. */

@@ -19,8 +19,8 @@
 //
 // Running maximum.  Weights are taken relative to a reference that follows the
 // maximum only when it has grown by more than 2^8: up to that the weights stay
-// below 256, which no type here overflows, and the 128 x head_dim rescaling of
-// O is skipped for nearly all blocks.  P rounded to 16 bits is the one
+// below 256 (fp16: below 2^15, see kHalfLift), which no type here overflows, and the
+// 128 x head_dim rescaling of O is skipped for nearly all blocks.  P rounded to 16 bits is the one
 // rounding between fp32 scores and the result; the sum is of the unrounded
 // weights.
 //
@@ -76,6 +76,10 @@ constexpr int kKeys = 128;           // slots per key block
 constexpr int kAttendMaxCtas = 160;  // partial states the workspace holds room for
 constexpr uint32_t kTmemCols = 512;
 constexpr int kNoPage = 0x7fffffff;  // outside every cache: its boxes read zeros
+// fp16 weights are taken 2^7 times as large (2^15 at most): numbers below 2^-14 are
+// held in steps of 2^-24, and without this what a key far below the reference weighs
+// vanished (20,000 of 2^-25 beside one of 1: all of their 0.0005).
+constexpr float kHalfLift = 7.f;
 constexpr float kRescaleAbove = 8.f;  // log2 (0: 0.90 instead of 0.79 ms for two prompts of 8192)
 
 // Workspace: header (status), tile counters [ctas][2], partial statistics
@@ -421,6 +425,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
     typedef AttendSmem<DP> L;
     constexpr bool kBf16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
+    constexpr float kLift = kBf16 ? 0.f : kHalfLift;
     constexpr int kHalves = DP / 64;
     constexpr int kHalfBytes = kKeys * 128;
     constexpr uint32_t kIdescS = tc::instr_desc(kBf16, false, kRows, kKeys);
@@ -896,7 +901,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         sum *= f;
                         ref = to;
                     }
-                    const float minus = ref == -INFINITY ? 0.f : -ref;
+                    const float minus = ref == -INFINITY ? 0.f : kLift - ref;
                     const uint64_t scale2 = pair2(A.scale_log2, A.scale_log2), minus2 = pair2(minus, minus);
                     uint64_t sums = 0;  // of even and odd columns
 #pragma unroll

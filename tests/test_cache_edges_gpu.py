@@ -162,3 +162,33 @@ def test_a_nan_query_gives_nan_whatever_the_cut(seqs, group):
         assert bool(torch.isnan(got[t, h]).all()), (t, h)
         got[t, h], want[t, h] = 0.0, 0.0
     within(got, want, tol)
+
+
+@pytest.mark.parametrize("bits", [25.25, 23.5, 18.0])
+@pytest.mark.parametrize("new", [1, 130])             # rows that split the keys, rows that share them
+def test_many_small_weights_beside_a_large_one(bits, new):
+    """One key outweighs each of 20,000 others by `bits` octaves: together they
+    still count, fp16's range of 24 octaves below one notwithstanding.  Weights
+    are held in steps of 2^-31 of one that the row's largest reaches: each is off
+    by half a step at most, beside its relative rounding.  400 sequences share
+    the pages, so that a CTA sees a tile's keys from the first to the last."""
+    L, d, page, B = 20000, 64, 80, 400
+    cb = CacheBatch([(new, L)], 1, d, page, HF, fill=False, seed=22)
+    cb.k.zero_()
+    cb.v.fill_(1.0)
+    at = int(cb.table[0, 0])
+    cb.k[at, 0, 0, 0] = bits * 0.6931471805599453
+    cb.v[at, 0] = 0.0
+    q = torch.zeros(B * new, 1, d, dtype=HF, device="cuda")
+    q[..., 0] = 1.0
+    gap = float(cb.k[at, 0, 0, 0])
+    n = (L - new + torch.arange(new, dtype=torch.float64)).repeat(B).view(-1, 1, 1)   # equal slots a row sees
+    small = n * torch.exp(torch.tensor(-gap, dtype=torch.float64))
+    want = (small / (1 + small)).expand(B * new, 1, d)
+    tol = want * (2 * 2.0 ** -11 + 2 * (d + 4) * 2.0 ** -24 * gap + 2.0 ** -21 + (L / 8 + 64) * 2.0 ** -23)
+    start = torch.arange(B + 1, dtype=torch.int32, device="cuda") * new
+    ws = sv.CacheWorkspace()
+    got = sv.paged_attention(q, cb.k, cb.v, cb.pages.expand(B, -1).contiguous(), start, cb.kv_len.expand(B).contiguous(),
+                             scale=1.0, ws=ws)
+    assert ws.status() == 0
+    within(got, want, tol + L * 2.0 ** -32)
