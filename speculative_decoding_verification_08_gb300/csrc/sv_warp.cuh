@@ -294,6 +294,15 @@ struct Mass2 {
     }
 };
 
+// The mass itself, or the whole number that it misses by less than such a mass's
+// error.  Where only the maxima of a row count, masses relative to the maximum are
+// whole, and goals may fall exactly on a border; their factor 2^E exp(-m / T) does
+// not cancel exactly.  (2^-34 of the mass: other masses lose nothing that counts.)
+__device__ __forceinline__ dd2 whole_mass(dd2 a) {
+    const float n = rintf(a.h), rest = (a.h - n) + a.l, k = rintf(rest);
+    return fabsf(rest - k) <= 5.8207661e-11f * a.h ? norm2(n, k) : a;
+}
+
 // What turns such a mass into one relative to the maximum m: 2^E exp(-m / T).
 __device__ __forceinline__ dd2 near_to_max(const RowScale &S, const ExpTable *tab, int E) {
     const float2 y = weight_of(0.f, S, tab);
@@ -1170,9 +1179,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
     {
         dd2 own_kept = kept.value(), own_above = above.value(), own_in = in.value();
         if (near) {
-            const dd2 by = near_to_max(S, &sh.tab, octave), all = mul_dd(near_all.value(), by);
-            own_above = add_dd(own_above, mul_dd(near_above.value(), by));
-            own_kept = add_dd(own_kept, by_p ? mul_dd(near_kept.value(), by) : all);
+            const dd2 by = near_to_max(S, &sh.tab, octave), all = whole_mass(mul_dd(near_all.value(), by));
+            own_above = add_dd(own_above, whole_mass(mul_dd(near_above.value(), by)));
+            own_kept = add_dd(own_kept, by_p ? whole_mass(mul_dd(near_kept.value(), by)) : all);
             own_in = add_dd(own_in, all);
         }
         if (dense && by_p && !(mp > 0.f)) own_kept = own_above;
@@ -1623,7 +1632,7 @@ __global__ void __launch_bounds__(kPlainThreads, 4) plain_kernel(const __grid_co
         top = largest_of(top);
         if (top > -INFINITY) {
             S.m = top;
-            const dd2 v = mul_dd(near.value(), near_to_max(S, &sh.tab, octave));
+            const dd2 v = whole_mass(mul_dd(near.value(), near_to_max(S, &sh.tab, octave)));
             const dd2 start = add_dd({4.f, 0.f}, v);
             a.h = start.h;
             a.l = start.l;

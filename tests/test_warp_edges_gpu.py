@@ -1,0 +1,61 @@
+"""warp_sample at exact ties and at the smallest temperatures, against its
+64-bit definition."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_08_gb300 as sv
+from cache_refs import warp_row
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+# one exp2 good to 2^-22, the reciprocal of the mass and two products rounded
+PROB_TOL = 2.0 ** -22 + 4 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.build()
+    return sv.load()
+
+
+def check(z, u, T=1.0, p=1.0, m=0.0, filtered=True):
+    """Every row of z under one setting of the filters against the definition."""
+    R = z.shape[0]
+    full = lambda x: torch.full((R,), x, dtype=torch.float32, device="cuda")  # noqa: E731
+    ws = sv.CacheWorkspace()
+    kw = dict(top_p=full(p), min_p=full(m)) if filtered else {}
+    tok, probs = sv.warp_sample(z, torch.as_tensor(u, dtype=torch.float64).cuda(), temperature=full(T),
+                                probs=True, ws=ws, **kw)
+    assert ws.status() == 0
+    zc, f32 = z.float().cpu().numpy(), lambda x: float(np.float32(x))  # noqa: E731
+    for r in range(R):
+        want, kept, t = warp_row(zc[r], f32(T), 0, f32(p), f32(m), float(u[r]))
+        got = probs[r].cpu().numpy()
+        assert np.array_equal(got > 0, kept & (want > 1e-29)), (r, int((got > 0).sum()), int(kept.sum()))
+        assert int(tok[r]) == t, (r, int(tok[r]), t)
+        assert np.all(np.abs(got - want) <= PROB_TOL * want + 1e-29), r
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("value", [-3.5, 0.0, 2.75, 5.1, -41.3])
+@pytest.mark.parametrize("V", [2, 100, 128, 160, 4096, 40000])
+def test_goals_that_fall_on_a_border_between_equal_logits(dt, value, V):
+    """Rows of one value (alone, beside masked logits, beside ones too small to
+    count): every mass is a whole number, and goals u V and p V fall exactly on a
+    border."""
+    rows = torch.full((6, V), value)
+    rows[1, 1::2] = float("-inf")                     # V / 2 are left
+    rows[2, ::2] = float("-inf")
+    rows[3, 1::2] = value - 200.0
+    u = np.array([0.5, 0.5, 0.25, 0.5, 0.0, 0.75])
+    for T in (1.0, 0.7, 1.9):
+        if abs(rows[0, 0].to(TYPES[dt]).float()) > 60 * T:
+            continue
+        z = rows.to(TYPES[dt]).cuda()
+        check(z, u, T, filtered=False)
+        for p in (0.5, 0.25, 0.75, 1.0):
+            check(z, u, T, p)
+        check(z, u, T, 0.5, 0.3)
