@@ -43,6 +43,8 @@ constexpr int kWarpMaxCluster = 8;
 constexpr int kBins = 1024;            // of a histogram of counts and masses; of one alone twice as many
 constexpr float kRangeOctaves = 40.f;  // the histogram's reach below the maximum
 constexpr float kColdest = 1e-36f, kHottest = 1e36f;  // temperatures
+constexpr float kTiny = 1e-35f;        // no histogram spans less
+static_assert(kColdest * kRangeOctaves * 0.69f > kTiny, "the coldest row's reach");
 constexpr float kMagic = 8388608.f;    // 2^23: adding it rounds to a whole number in the low bits
 constexpr int kPlainThreads = 256;
 constexpr int kLocalList = 160;        // border elements one CTA may gather
@@ -900,7 +902,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
     const bool both = by_k && by_h;
     const int bins = both ? kBins : 2 * kBins;
     // the last bin is for what lies further down
-    const float reach = kRangeOctaves / S.ch, span = low < m ? fmaxf(fminf(m - low, reach), 1e-30f) : reach;
+    // (kTiny: bins per unit stay finite; the coldest temperature's reach is above it,
+    // so that a bin never spans more than kRangeOctaves / (bins - 2))
+    const float reach = kRangeOctaves / S.ch, span = low < m ? fmaxf(fminf(m - low, reach), kTiny) : reach;
     const float per = (float)(bins - 2) / span;                          // bins per unit of z
     auto t_of = [&](float x) -> float {
         return fminf(fmaf(m - x, per, kMagic), kMagic + (float)(bins - 1));

@@ -59,3 +59,14 @@ def test_goals_that_fall_on_a_border_between_equal_logits(dt, value, V):
         for p in (0.5, 0.25, 0.75, 1.0):
             check(z, u, T, p)
         check(z, u, T, 0.5, 0.3)
+
+
+@pytest.mark.parametrize("T", [1e-32, 1e-33, 1e-34, 1e-35, 1.1e-36])
+def test_a_nucleus_at_the_smallest_temperatures(T):
+    """Logits as close together as the temperature is small."""
+    R, V = 24, 3000
+    T = float(np.float32(T))
+    z = (torch.randn(R, V, generator=torch.Generator().manual_seed(31), dtype=torch.float64) * (3 * T)).float().cuda()
+    u = np.linspace(0.02, 0.98, R)
+    for p in (0.3, 0.7, 0.95):
+        check(z, u, T, p)
