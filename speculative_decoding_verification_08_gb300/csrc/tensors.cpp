@@ -89,6 +89,10 @@ void *vector_or_null(PyObject *o, at::ScalarType type, int64_t n, int64_t dev, c
     return o == Py_None ? nullptr : vector(o, type, n, dev, name);
 }
 
+// The stride of axis i; that of an axis of length one, which means nothing, as one
+// that every call takes.
+int64_t stride_of(const at::Tensor &x, int i) { return x.size(i) == 1 ? 0 : x.stride(i); }
+
 struct Paged {
     sv_paged_cache c;
     at::ScalarType type;
@@ -115,8 +119,8 @@ struct Paged {
         c.k = k.data_ptr();
         c.v = v.data_ptr();
         for (int i = 0; i < 3; ++i) {
-            c.k_stride[i] = k.stride(i);
-            c.v_stride[i] = v.stride(i);
+            c.k_stride[i] = stride_of(k, i);
+            c.v_stride[i] = stride_of(v, i);
         }
         c.num_pages = int32(k.size(0), "pages");
         c.page_size = int32(k.size(1), "page_size");
@@ -146,8 +150,8 @@ struct Heads {
             refuse(name, ": expected [", P.c.tokens, "][", heads, "][", P.c.head_dim, "], got ", x.sizes());
         if (x.stride(2) != 1 && x.size(2) > 1) refuse(name, ": the head dimension must be contiguous");
         p = x.data_ptr();
-        st[0] = x.stride(0);
-        st[1] = x.stride(1);
+        st[0] = stride_of(x, 0);
+        st[1] = stride_of(x, 1);
     }
 };
 

@@ -192,3 +192,24 @@ def test_many_small_weights_beside_a_large_one(bits, new):
                              scale=1.0, ws=ws)
     assert ws.status() == 0
     within(got, want, tol + L * 2.0 ** -32)
+
+
+def test_the_stride_of_an_axis_of_length_one_means_nothing():
+    """One token, one head, one page of one sequence: whatever stride such an
+    axis carries, it is never multiplied by anything but zero."""
+    cb = CacheBatch([(1, 9)], 1, 64, 16, BF, seed=23)
+    q, k, v = cb.tokens(1), cb.tokens(1), cb.tokens(1)
+    f = torch.pow(10000.0, -2.0 * torch.arange(32, dtype=torch.float64, device="cuda") / 64)
+    page = int(cb.table[0, 0])
+    kc, vc = cb.k[page:page + 1].clone(), cb.v[page:page + 1].clone()
+    zero = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    odd = lambda x: x.as_strided(x.shape, [7 if n == 1 else s for n, s in zip(x.shape, x.stride())])  # noqa: E731
+    want = []
+    for g in (lambda x: x, odd):
+        ck, cv = kc.clone(), vc.clone()
+        r = sv.append_kv(g(k), g(v), g(ck), g(cv), zero, cb.q_start, cb.kv_len, inv_freq=f, q=g(q),
+                         q_out=g(torch.empty_like(q)))
+        o = sv.paged_attention(g(q), g(ck), g(cv), zero, cb.q_start, cb.kv_len, out=g(torch.empty_like(q)))
+        want.append((ck, cv, r, o))
+    for a, b in zip(*want):
+        assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
