@@ -395,12 +395,13 @@ static_assert(sizeof(WarpShared) % 16 == 0 && offsetof(WarpShared, hist) % 16 ==
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ float uniform(float x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// The cluster's barrier in two parts, for a CTA's end: nothing is handed over.
+// The cluster's barrier in two parts, for a CTA's end.  The arrival releases: what
+// the CTA has read of another's shared memory has been read by then.
 __device__ __forceinline__ void cluster_arrive_all() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait_all() {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <class T>
