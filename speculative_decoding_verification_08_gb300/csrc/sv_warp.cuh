@@ -788,6 +788,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 3) warp_kerne
         sh.min_off = {(float)off, (float)(off - (double)(float)off)};
     }
     const bool came = mbar_wait(&sh.bar, 0);
+    // (one that gave up waits once more: the copies should land before the CTA ends)
+    if (!came) mbar_wait(&sh.bar, 0);
     if (!__syncthreads_and(came) && tid == 0) {
         atomicOr(A.status, SV_STATUS_TIMEOUT);
         sh.bad = 1;
