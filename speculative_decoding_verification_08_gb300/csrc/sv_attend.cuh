@@ -349,13 +349,14 @@ __device__ __forceinline__ void store_row(uint16_t *to, const uint32_t (&y)[16],
 }
 
 // A wait that gives up for the whole CTA.
+template <uint64_t kLimitNs = kWaitLimitNs>
 __device__ __forceinline__ bool hold(AttendShared &sh, unsigned long long *bar, uint32_t parity,
                                      uint32_t *status) {
     if (mbar_try(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     while (!mbar_try(bar, parity)) {
         if (*(volatile int32_t *)&sh.dead) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
+        if (global_ns() - t0 > kLimitNs) {
             *(volatile int32_t *)&sh.dead = 1;
             atomicOr(status, SV_STATUS_TIMEOUT);
             return false;
@@ -364,12 +365,19 @@ __device__ __forceinline__ bool hold(AttendShared &sh, unsigned long long *bar, 
     return true;
 }
 
+// The scheduler and the queries' warp wait for whole pieces, whose millions of slots
+// may well take seconds (2^31 of them half a minute); the others wait for a key
+// block at most, and when one of them gives up these see it.  (A limit that any
+// progress renews: 2 us of 65 for 6 tokens over 131071 slots.)
+constexpr uint64_t kPieceLimitNs = 100000000000ull;
+
 // The pieces as a reader warp sees them, in order.
 struct PieceReader {
     int k = 0;
     uint32_t turn = 0;
+    template <uint64_t kLimitNs = kWaitLimitNs>
     __device__ __forceinline__ const Piece *next(AttendShared &sh, uint32_t *status) {
-        const bool ok = __all_sync(0xffffffffu, hold(sh, &sh.piece_full[k], turn, status));
+        const bool ok = __all_sync(0xffffffffu, hold<kLimitNs>(sh, &sh.piece_full[k], turn, status));
         return ok && sh.pieces[k].n >= 0 ? &sh.pieces[k] : nullptr;
     }
     __device__ __forceinline__ void done(AttendShared &sh, int lane) {
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 if (!more) p.n = -1;
                 if (SV_STALL && k == 1 && blockIdx.x % 2 == 1) break;
                 // (after a timeout the readers stop at the first piece they miss)
-                if (!__all_sync(0xffffffffu, hold(sh, &sh.piece_empty[k], turn, status))) break;
+                if (!__all_sync(0xffffffffu, hold<kPieceLimitNs>(sh, &sh.piece_empty[k], turn, status))) break;
                 if (lane == 0) {
                     sh.pieces[k] = p;
                     mbar_arrive(&sh.piece_full[k]);
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             // of the tile before it are done
             uint32_t qn0 = 0, qn1 = 0;
             PieceReader reader;
-            while (const Piece *pp = reader.next(sh, status)) {
+            while (const Piece *pp = reader.next<kPieceLimitNs>(sh, status)) {
                 const Piece p = *pp;
                 reader.done(sh, lane);
                 if (p.n == 0) continue;
@@ -774,7 +782,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 for (int g = 0; g < 2; ++g) {
                     if (g == 1 && p.n1 == 0) continue;
                     const uint32_t turn = ((g ? qn1 : qn0) & 1) ^ 1;
-                    if (!__all_sync(0xffffffffu, hold(sh, &sh.q_free[g], turn, status))) continue;
+                    if (!__all_sync(0xffffffffu, hold<kPieceLimitNs>(sh, &sh.q_free[g], turn, status))) continue;
                     const int r0 = p.row + (p.split ? 0 : g * kRows);
                     if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[g], L::kTile);
                     __syncwarp();
@@ -790,7 +798,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (qn1 > 0) mbar_wait(&sh.q_full[1], (qn1 - 1) & 1);
         } else {
             PieceReader reader;
-            while (reader.next(sh, status)) reader.done(sh, lane);
+            while (reader.next<kPieceLimitNs>(sh, status)) reader.done(sh, lane);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));

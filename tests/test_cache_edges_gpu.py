@@ -213,3 +213,29 @@ def test_the_stride_of_an_axis_of_length_one_means_nothing():
         want.append((ck, cv, r, o))
     for a, b in zip(*want):
         assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+
+def test_pieces_that_take_longer_than_a_wait_may():
+    """48 million slots (one page of zero values, listed over and over, and one of
+    others at the end) before four rows of 128 heads: a tile keeps a CTA busy for
+    more than the 250 ms after which a wait without progress gives up, and its next
+    tile's queries wait for that long.  Scores are 0, so that every sum is exact."""
+    page, L, d, G, B = 1 << 18, 48 << 20, 64, 128, 95
+    k = torch.randn(2, page, 1, d, generator=torch.Generator().manual_seed(27)).to(BF).cuda()
+    v = torch.zeros(2, page, 1, d, dtype=BF, device="cuda")
+    row = torch.linspace(-3, 3, d).to(BF)
+    v[1] = row.cuda()
+    pages = torch.zeros(B, L // page, dtype=torch.int32, device="cuda")
+    pages[:, -1] = 1
+    start = torch.arange(B + 1, dtype=torch.int32, device="cuda") * 4      # two tiles each
+    q = torch.zeros(4 * B, G, d, dtype=BF, device="cuda")
+    ws = sv.CacheWorkspace()
+    t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    t[0].record()
+    got = sv.paged_attention(q, k, v, pages, start, torch.full((B,), L, dtype=torch.int32, device="cuda"), ws=ws)
+    t[1].record()
+    assert ws.status() == 0
+    assert t[0].elapsed_time(t[1]) > 250
+    last = torch.arange(-3, 1, dtype=torch.float64).repeat(B).view(-1, 1, 1)
+    want = (row.double() * (page + last) / (L + last)).expand(4 * B, G, d)
+    within(got, want, want.abs() * (2.0 ** -8 + 2.0 ** -20))
