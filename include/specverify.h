@@ -367,8 +367,11 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
  *   probs     (not NULL): [R] rows of V f32, probs_row_stride (>= V) apart:
  *             w_v over the kept mass, 0 for what was left out.
  * The kept set and the token are those of a 64-bit evaluation: masses are
- * good to about 1e-10 (weights below e^-85 count as 0).  -inf logits have no
- * mass.  A row without mass (all -inf: SV_STATUS_ZERO_MASS), with a NaN or
+ * good to about 1e-10 (weights below e^-85 count as 0).  A goal (top_p times
+ * the mass, u times it, or min_p) that lies closer than that to a border may
+ * fall on either side of it; where all the mass lies in equal maxima, masses
+ * are whole numbers and even goals on a border are settled exactly.  -inf
+ * logits have no mass.  A row without mass (all -inf: SV_STATUS_ZERO_MASS), with a NaN or
  * +inf logit, or with a temperature that is NaN or outside [1e-36, 1e36]
  * (SV_STATUS_BAD_VALUE) gives token -1 and a row of zeros.  Rows warped alike
  * serve as the p and q of sv_verify_sample. */

@@ -15,7 +15,10 @@
 // pack of what is copied) to each, go through the tokens.
 //
 // 25400 tokens of 16 + 16 + 16 heads of 64 (fp16, half of a head rotated, pages
-// of 16): 67 us, 4.7 TB/s.  1536 tokens of 32 + 8 + 8 heads of 128: 11.8 us, 3.2
+// of 16): 67 us, 4.7 TB/s, half of the issue slots taken: 6354 blocks of four tokens
+// pay the lookup, the angles and a barrier each before their first store, 16-byte
+// packs of 40 registers spill a little (24 bytes; 44 with adjacent pairs), and those
+// of adjacent pairs leave in half sectors.  1536 tokens of 32 + 8 + 8 heads of 128: 11.8 us, 3.2
 // TB/s, 3 us of it launch and lookup; one token 4.5 us.
 #pragma once
 

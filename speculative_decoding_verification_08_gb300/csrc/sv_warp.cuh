@@ -13,7 +13,9 @@
 // on the order of the atomics) narrows the border to a bin or two, then the
 // elements of those bins are gathered, ranked, and the border is settled on
 // exact values.  A border bin too full to gather (rows of equal logits) is
-// settled by bisection of the composite instead.
+// settled by bisection of the composite instead, in up to 64 sweeps of the row: 256
+// rows of 128256 fp32 rounded to whole numbers take 11.7 ms with top-p (274 us
+// unrounded), 8.1 with a top-k of 20000 (315 us), one row of 32000 0.88 (24 us).
 //
 // Masses decide which tokens stay and which one is drawn, and must give the
 // answers of a 64-bit evaluation.  fp64 runs at 1/64 of the fp32 rate here, so

@@ -14,8 +14,9 @@ namespace {
 
 constexpr int kSms = 152;
 constexpr int kThreads = 256;
-// Slices of more than this many words fill an SM: 1024 threads then, not 256
-// (64 rows of 262144 fp32 with top-p: 162 against 199 us).
+// Slices of more than this many words (64 KB and one) leave room for two CTAs of an
+// SM at most, and soon for one: 1024 threads then, not 256 (64 rows of 262144 fp32
+// with top-p: 162 against 199 us).
 constexpr int kSharedWords = 4096 + 1;
 // 16-byte words of a slice that shared memory holds beside WarpShared
 constexpr int kMaxWords = (227 * 1024 - (int)sizeof(sv::WarpShared)) / 16;
@@ -52,7 +53,10 @@ int launch(sv::WarpParams &A, cudaStream_t st) {
     const bool plain = !A.top_k && !A.top_p && !A.min_p;
     // Cluster: as many CTAs as keep a slice within 64 KB (three of them then
     // share an SM and hide one another's barriers: 256 rows of 128256 fp32 with
-    // top-k 107 us, 141 with slices of 128 KB and one CTA to an SM), and more
+    // top-k 107 us, 141 with slices of 128 KB and one CTA to an SM; a slice of 64 KB
+    // itself, with the word that alignment may take, is rounded up to one more round
+    // of the block and leaves two: 131072 logits take 1.2 to 1.3 times as long as
+    // 128256), and more
     // while the whole batch has fewer CTAs than SMs, down to 2048 elements each.
     // Rows without filters keep to the same rule (768 rows of 128256 bf16: 226,
     // 180, 167 and 181 us with 1, 2, 4 and 8 CTAs).
