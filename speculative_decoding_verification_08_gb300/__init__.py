@@ -557,7 +557,12 @@ def _on(stream):
 def _cuda_index(device, stream) -> int:
     """The device meant: the one named, else the stream's, else the current one."""
     torch = _torch()
-    index = None if device is None else torch.device(device).index
+    index = None
+    if device is not None:
+        named = torch.device(device)
+        if named.type != "cuda":
+            raise SpecVerifyError(f"a CacheWorkspace lives on a CUDA device, not on {named}")
+        index = named.index
     if index is None and stream is not None:
         index = stream.device.index
     return torch.cuda.current_device() if index is None else index

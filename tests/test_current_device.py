@@ -6,6 +6,7 @@ import subprocess
 
 import pytest
 
+import speculative_decoding_verification_08_gb300 as sv
 from speculative_decoding_verification_08_gb300 import _build
 
 PROGRAM = r"""
@@ -62,3 +63,10 @@ def test_only_memory_of_the_current_device_is_taken(tmp_path):
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
     # null, device 0, device 1, managed, page-locked, pageable, unknown; null where that is allowed
     assert out == ["00000001", "01010001", "00110001", "3"]
+
+
+def test_a_workspace_is_not_made_off_the_gpu():
+    sv.build()
+    for make in (sv.CacheWorkspace, sv.cache_workspace):
+        with pytest.raises(sv.SpecVerifyError, match="CUDA device"):
+            make("cpu")
