@@ -686,8 +686,8 @@ def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=No
     a token per row with u [...] f64 in [0, 1).  The filters are tensors with
     one value per row (f32; top_k int32) or None (off).  Returns (token int32
     or None without u, probs [..., V] f32 or None unless probs or probs_out):
-    rows as verify_sample takes them.  A row without mass or with a NaN or +inf
-    logit gives token -1 and zeros."""
+    rows as verify_sample takes them; probs_out must not overlap z.  A row
+    without mass or with a NaN or +inf logit gives token -1 and zeros."""
     return _call("warp_sample", z, "z",
                  (z, u, temperature, top_k, top_p, min_p, probs, probs_out, token_out), ws, stream)
 

@@ -271,6 +271,10 @@ PyObject *warp_sample(PyObject *const *a) {
                 !x.is_contiguous())
                 refuse("probs_out: expected ", given.sizes(), " contiguous float32 on cuda:", dev);
             pp = static_cast<float *>(x.data_ptr());
+            // (a row's draw reads its logits after its probabilities are written)
+            const char *z0 = static_cast<const char *>(z.data_ptr()), *p0 = reinterpret_cast<const char *>(pp);
+            if (R > 0 && p0 < z0 + ((R - 1) * row + V) * (int64_t)z.element_size() && z0 < p0 + 4 * R * V)
+                refuse("probs_out must not overlap z");
         }
     }
     if (!draw && !want && R > 0) refuse("nothing to compute: give u, or ask for probs");

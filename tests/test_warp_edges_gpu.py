@@ -70,3 +70,16 @@ def test_a_nucleus_at_the_smallest_temperatures(T):
     u = np.linspace(0.02, 0.98, R)
     for p in (0.3, 0.7, 0.95):
         check(z, u, T, p)
+
+
+def test_rows_are_not_written_over_their_logits():
+    wide = torch.randn(5, 40, device="cuda")
+    u = torch.rand(4, dtype=torch.float64, device="cuda")
+    for z, out in ((wide[:4], wide[:4]), (wide[:4], wide[1:]), (wide[1:], wide[:4]), (wide[::3], wide[2:4])):
+        with pytest.raises(sv.SpecVerifyError, match="overlap"):
+            sv.warp_sample(z, u[:z.shape[0]], probs_out=out)
+    out = torch.empty(9, 40, device="cuda")
+    out[5:] = wide[:4]                                # side by side, in one block of memory
+    token, rows = sv.warp_sample(out[5:], u, probs_out=out[1:5])
+    same = sv.warp_sample(wide[:4], u, probs=True)
+    assert torch.equal(token, same[0]) and torch.equal(rows, same[1])
