@@ -235,7 +235,14 @@ PyObject *warp_sample(PyObject *const *a) {
     if (given.dim() < 1) refuse("z: expected [..., V]");
     const int64_t V = given.size(-1);
     at::Tensor flat;
-    if (given.dim() > 2) flat = given.view({-1, V});
+    if (given.dim() > 2) {
+        try {
+            flat = given.view({-1, V});
+        } catch (const c10::Error &) {
+            refuse("z: rows of all leading axes must be evenly strided, got ", given.sizes(), " with strides ",
+                   given.strides());
+        }
+    }
     const at::Tensor &z = given.dim() > 2 ? flat : given;
     const int64_t R = z.dim() == 2 ? z.size(0) : 1, row = R > 1 ? z.stride(0) : V;
     if (z.stride(-1) != 1 && V > 1) refuse("z: the vocabulary dimension must be contiguous");

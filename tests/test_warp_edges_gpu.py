@@ -83,3 +83,12 @@ def test_rows_are_not_written_over_their_logits():
     token, rows = sv.warp_sample(out[5:], u, probs_out=out[1:5])
     same = sv.warp_sample(wide[:4], u, probs=True)
     assert torch.equal(token, same[0]) and torch.equal(rows, same[1])
+
+
+def test_leading_axes_that_make_no_rows_are_refused():
+    z, u = torch.randn(3, 4, 50, device="cuda"), torch.rand(12, dtype=torch.float64, device="cuda")
+    for bad in (z.transpose(0, 1), z[:, :3].expand(3, 3, 50), torch.empty(2, 3, 0, device="cuda")):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.warp_sample(bad, u[:bad.shape[0] * bad.shape[1]])
+    token, _ = sv.warp_sample(z[:, :1], u[:3])        # an axis of length one is no axis
+    assert token.shape == (3, 1) and torch.equal(token[:, 0], sv.warp_sample(z[:, 0], u[:3])[0])
