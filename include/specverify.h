@@ -277,6 +277,7 @@ int sv_alpha(const float *p, int64_t p_row_stride, const float *q, int64_t q_row
 #define SV_F32 0
 #define SV_BF16 1
 #define SV_F16 2
+#define SV_E4M3 3 /* caches only, with sv_cache_scales */
 
 /* A paged cache and the batch that works on it.
  *   k, v       [num_pages][page_size][kv_heads][head_dim] of `dtype` (SV_BF16
@@ -351,6 +352,55 @@ int sv_paged_attention(const sv_paged_cache *cache, const void *q, const int64_t
                        void *out, const int64_t *out_stride, int32_t q_heads, float scale,
                        int32_t window, void *workspace, size_t workspace_bytes,
                        sv_stream_t stream);
+
+/* Caches of 8-bit values.  A cache of dtype SV_E4M3 holds, for every slot and kv
+ * head, head_dim codes (e4m3: 4 exponent bits, 3 of mantissa, largest 448) and, in
+ * arrays of their own, one scale byte (e8m0: 2^(byte - 127), 255 NaN): a value is
+ * its code times the scale.  The codes' strides are multiples of 16 and head_dim
+ * one of 16, 16 to 128; the scale of (page p, slot s, head h) is at p * stride[0] +
+ * s * stride[1] + h * stride[2] bytes, in any order of the axes. */
+typedef struct sv_cache_scales {
+    uint8_t *k, *v;
+    int64_t k_stride[3], v_stride[3];
+} sv_cache_scales;
+
+/* sv_append_kv with norms of queries and keys for each head in the same pass, and
+ * for caches of 8-bit values (scales not NULL; cache->dtype SV_E4M3).  `dtype` is
+ * the tokens' type (SV_BF16 or SV_F16); with scales NULL it is the cache's.
+ *   q_norm, k_norm [head_dim] of norm_dtype (SV_F32 or the tokens' type), or NULL:
+ *         a head's vector x becomes x * rsqrt(mean(x^2) + eps) * norm before it
+ *         turns; eps >= 0 and finite.  (Squares are summed in fp32.)
+ * Norm and rotation are fp32 and the result is rounded once: to the tokens' type,
+ * or, for keys and values of an 8-bit cache, to e4m3 after the division by the
+ * vector's scale, the smallest power of two from 2^-100 to 2^100 that is at least
+ * 1/448 of its largest magnitude (larger vectors saturate).  A vector that then
+ * holds a NaN or an infinity has the scale NaN and codes of zero.  All else is as
+ * for sv_append_kv. */
+int sv_append_kv_normed(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
+                        const void *k, const int64_t *k_stride, const void *v, const int64_t *v_stride,
+                        const void *q, const int64_t *q_stride, void *q_out, const int64_t *q_out_stride,
+                        int32_t q_heads, const void *q_norm, const void *k_norm, int32_t norm_dtype, float eps,
+                        const double *inv_freq, int32_t rot_dim, int32_t interleaved, const int32_t *positions,
+                        void *workspace, size_t workspace_bytes, sv_stream_t stream);
+
+/* The way back: row q_start[b] + j of n, j < n = q_start[b + 1] - q_start[b], of
+ * k_out and v_out [tokens][kv_heads][head_dim] (`dtype`, strides as for the token
+ * arrays) is the key and value in slot kv_len[b] - n + j.  From an 8-bit cache (scales
+ * not NULL) code times scale, rounded once (exact in bf16; past fp16's range infinite); from a
+ * cache of `dtype` (scales NULL) the value itself.  Rows whose slot is negative
+ * (SV_STATUS_BAD_LENGTH) or whose page id is outside the cache
+ * (SV_STATUS_BAD_PAGE) are zeros; rows of no sequence are not written. */
+int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype, void *k_out,
+               const int64_t *k_out_stride, void *v_out, const int64_t *v_out_stride, void *workspace,
+               size_t workspace_bytes, sv_stream_t stream);
+
+/* sv_paged_attention over a cache of 8-bit values; q and out are of `dtype` (SV_BF16
+ * or SV_F16). */
+size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads);
+int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
+                        const void *q, const int64_t *q_stride, void *out, const int64_t *out_stride,
+                        int32_t q_heads, float scale, int32_t window, void *scratch, size_t scratch_bytes,
+                        void *workspace, size_t workspace_bytes, sv_stream_t stream);
 
 /* Warps rows of logits and draws from them.  z holds R rows of V logits of
  * type z_dtype (SV_F32, SV_BF16 or SV_F16), z_row_stride (>= V) apart.  Row r:

@@ -4,7 +4,7 @@ Python binding of ``libspecverify.so`` (C ABI in ``include/specverify.h``).
 This module only marshals arguments: torch CUDA tensors are checked for
 dtype, device and layout and their pointers, strides and the current CUDA
 stream are passed to the library, whose kernels do every step of the
-verification (for append_kv, paged_attention and warp_sample a small C++
+verification (for append_kv, read_kv, paged_attention and warp_sample a small C++
 extension does so, ``csrc/tensors.cpp``).  There is no CPU path: if the library is missing or a tensor is
 not on a CUDA device, the call raises.
 
@@ -52,7 +52,8 @@ EXPORTED = (
     "sv_last_kernel_count", "sv_alpha", "sv_verify_sample_logits",
     "sv_status_string", "sv_version", "sv_verify_sample_noalloc", "sv_trace_reset",
     "sv_trace_read", "sv_cache_workspace_size", "sv_append_kv", "sv_paged_attention",
-    "sv_warp_sample",
+    "sv_warp_sample", "sv_append_kv_normed", "sv_read_kv", "sv_paged_attention_scaled",
+    "sv_paged_attention_scratch_size",
 )
 
 _lock = threading.Lock()
@@ -129,6 +130,16 @@ def _declare(lib):
     lib.sv_append_kv.restype = ctypes.c_int
     lib.sv_paged_attention.argtypes = [C, P, S, P, S, i32, ctypes.c_float, i32, P, sz, P]
     lib.sv_paged_attention.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.sv_append_kv_normed.argtypes = [C, C, i32, P, S, P, S, P, S, P, S, i32, P, P, i32, f32, P, i32, i32, P, P,
+                                        sz, P]
+    lib.sv_append_kv_normed.restype = ctypes.c_int
+    lib.sv_read_kv.argtypes = [C, C, i32, P, S, P, S, P, sz, P]
+    lib.sv_read_kv.restype = ctypes.c_int
+    lib.sv_paged_attention_scratch_size.argtypes = [C, i32]
+    lib.sv_paged_attention_scratch_size.restype = sz
+    lib.sv_paged_attention_scaled.argtypes = [C, C, i32, P, S, P, S, i32, f32, i32, P, sz, P, sz, P]
+    lib.sv_paged_attention_scaled.restype = ctypes.c_int
     lib.sv_warp_sample.argtypes = [P, i64, i32, i32, i64, P, P, P, P, P, P, P, i64, P, sz, P]
     lib.sv_warp_sample.restype = ctypes.c_int
     return lib
@@ -629,9 +640,12 @@ def _native():
             spec = importlib.util.spec_from_file_location(loader.name, _build.EXTENSION, loader=loader)
             module = importlib.util.module_from_spec(spec)
             loader.exec_module(module)
-            module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                          for f in (lib.sv_append_kv, lib.sv_paged_attention, lib.sv_warp_sample)),
+            def at(*calls):
+                return (ctypes.cast(f, ctypes.c_void_p).value for f in calls)
+            module.bind(*at(lib.sv_append_kv, lib.sv_paged_attention, lib.sv_warp_sample),
                         SpecVerifyError, _check)
+            module.bind8(*at(lib.sv_append_kv_normed, lib.sv_read_kv, lib.sv_paged_attention_scaled,
+                             lib.sv_paged_attention_scratch_size))
             _tensors = module
         return _tensors
 
@@ -652,7 +666,8 @@ def _call(name, x, what, args, ws, stream):
 
 
 def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, q=None,
-              q_out=None, positions=None, interleaved=False, ws=None, stream=None):
+              q_out=None, positions=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
+              k_scale=None, v_scale=None, ws=None, stream=None):
     """Writes the new tokens' keys and values [N][kv_heads][D] into their slots
     of the paged cache [pages][page_size][kv_heads][D] (any order of the axes),
     the keys rotated by their positions, and returns q [N][q_heads][D] rotated
@@ -662,21 +677,55 @@ def append_kv(k, v, k_cache, v_cache, pages, q_start, kv_len, *, inv_freq=None, 
     new tokens), kv_len [B] int32 (lengths with the new tokens).  inv_freq
     [rot_dim / 2] f64 gives radians per position of each pair (None: no
     rotation); pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) when
-    interleaved.  positions [N] int32 overrides the slots as positions."""
-    return _call("append_kv", k_cache, "k_cache",
-                 (k, v, k_cache, v_cache, pages, q_start, kv_len, inv_freq, q, q_out, positions, interleaved),
-                 ws, stream)
+    interleaved.  positions [N] int32 overrides the slots as positions.
+
+    q_norm, k_norm [D] (f32 or the tokens' type) norm each head before it
+    turns: x / sqrt(mean(x^2) + eps) * norm.  With k_scale and v_scale
+    [pages][page_size][kv_heads] (float8_e8m0fnu, any order of the axes) the
+    caches are float8_e4m3fn: each vector is divided by the power of two that
+    brings its largest magnitude to 448 or less, and rounded once."""
+    if q_norm is None and k_norm is None and k_scale is None and v_scale is None:
+        return _call("append_kv", k_cache, "k_cache",
+                     (k, v, k_cache, v_cache, pages, q_start, kv_len, inv_freq, q, q_out, positions, interleaved),
+                     ws, stream)
+    return _call("append_kv_normed", k_cache, "k_cache",
+                 (k, v, k_cache, v_cache, pages, q_start, kv_len, inv_freq, q, q_out, positions, interleaved,
+                  q_norm, k_norm, eps, k_scale, v_scale), ws, stream)
+
+
+def read_kv(k_cache, v_cache, pages, q_start, kv_len, *, rows=None, dtype=None, k_scale=None, v_scale=None,
+            k_out=None, v_out=None, ws=None, stream=None):
+    """The way back from a paged cache: (k, v) [rows][kv_heads][D], row
+    q_start[b] + j of n being what slot kv_len[b] - n + j holds, as append_kv
+    put it there (n = kv_len[b] for whole sequences).  `rows` says how many
+    there are in all (q_start's last entry, which only the device knows) unless
+    k_out or v_out does.  A float8_e4m3fn cache (k_scale and v_scale as for
+    append_kv) comes back as `dtype`, bfloat16 or float16 (default bfloat16),
+    others as what they are."""
+    code = 0
+    if dtype is not None or k_scale is not None:
+        torch = _torch()
+        code = {None: 1, torch.bfloat16: 1, torch.float16: 2}.get(dtype)
+        if code is None:
+            raise SpecVerifyError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    return _call("read_kv", k_cache, "k_cache",
+                 (k_cache, v_cache, pages, q_start, kv_len, -1 if rows is None else rows, code, k_scale, v_scale,
+                  k_out, v_out), ws, stream)
 
 
 def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, window=0,
-                    out=None, ws=None, stream=None):
+                    out=None, k_scale=None, v_scale=None, ws=None, stream=None):
     """Attention of the new tokens q [N][q_heads][D] over the paged cache that
     holds them already (append_kv): causal, over the last `window` slots when
     window > 0, scale 1 / sqrt(D) by default; q_heads a multiple of kv_heads.
-    Arrays as for append_kv.  Rows that see nothing are zeros.  Returns out
+    Arrays as for append_kv; a float8_e4m3fn cache comes with its k_scale and
+    v_scale.  Rows that see nothing are zeros.  Returns out
     [N][q_heads][D]."""
-    return _call("paged_attention", k_cache, "k_cache",
-                 (q, k_cache, v_cache, pages, q_start, kv_len, scale, window, out), ws, stream)
+    if k_scale is None and v_scale is None:
+        return _call("paged_attention", k_cache, "k_cache",
+                     (q, k_cache, v_cache, pages, q_start, kv_len, scale, window, out), ws, stream)
+    return _call("paged_attention_scaled", k_cache, "k_cache",
+                 (q, k_cache, v_cache, pages, q_start, kv_len, scale, window, out, k_scale, v_scale), ws, stream)
 
 
 def warp_sample(z, u=None, *, temperature=None, top_k=None, top_p=None, min_p=None, probs=False,

@@ -13,12 +13,13 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "specverify.cu"), os.path.join(CSRC, "cache.cu"),
-           os.path.join(CSRC, "warp.cu")]
+           os.path.join(CSRC, "cache8.cu"), os.path.join(CSRC, "warp.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "sv_device.cuh"), os.path.join(CSRC, "sv_tma.cuh"),
                      os.path.join(CSRC, "sv_item.cuh"), os.path.join(CSRC, "sv_alpha.cuh"),
                      os.path.join(CSRC, "sv_logits.cuh"), os.path.join(CSRC, "sv_debug.cuh"),
                      os.path.join(CSRC, "sv_trace.cuh"), os.path.join(CSRC, "sv_host.cuh"),
                      os.path.join(CSRC, "sv_cache.cuh"), os.path.join(CSRC, "sv_append.cuh"),
+                     os.path.join(CSRC, "sv_append8.cuh"), os.path.join(CSRC, "sv_cache_host.cuh"),
                      os.path.join(CSRC, "sv_attend.cuh"), os.path.join(CSRC, "sv_warp.cuh"),
                      os.path.join(CSRC, "sv_tc.cuh"), os.path.join(CSRC, "sv_barrier.cuh"),
                      os.path.join(INCLUDE, "specverify.h")]

@@ -10,61 +10,13 @@
 #include "specverify.h"
 #include "sv_append.cuh"
 #include "sv_attend.cuh"
-#include "sv_host.cuh"
+#include "sv_cache_host.cuh"
 
 namespace {
 
 constexpr int kSms = 152;
 
-using svhost::g_last_grid;
-using svhost::g_last_kernels;
-using svhost::CurrentDevice;
-using svhost::kAlign;
-
-bool vec_ok(const void *p, const int64_t *st, int n) {
-    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return false;
-    for (int i = 0; i < n; ++i)
-        if (st[i] < 0 || st[i] % 8 != 0) return false;
-    return true;
-}
-
-// What can be told from the cache descriptor's values alone.
-int check_cache(const sv_paged_cache *c) {
-    if (!c) return SV_EINVAL;
-    if (c->B < 0 || c->tokens < 0 || c->kv_heads < 1 || c->head_dim < 8 ||
-        c->head_dim > sv::kMaxHeadDim || c->head_dim % 8 != 0 || c->page_size < 8 ||
-        c->page_size % 8 != 0 || c->num_pages < 1 || c->max_pages < 1 ||
-        (c->dtype != SV_BF16 && c->dtype != SV_F16))
-        return SV_EINVAL;
-    if ((int64_t)c->max_pages * c->page_size > (int64_t)INT32_MAX - 1024) return SV_EINVAL;
-    if (c->B == 0 || c->tokens == 0) return SV_OK;
-    if (!c->k || !c->v || !c->pages || !c->q_start || !c->kv_len || c->pages_stride < c->max_pages)
-        return SV_EINVAL;
-    return vec_ok(c->k, c->k_stride, 3) && vec_ok(c->v, c->v_stride, 3) ? SV_OK : SV_EINVAL;
-}
-
-// Checks where the workspace and the cache's arrays live, and fills in the
-// batch the device sees.
-int bind_cache(const CurrentDevice &here, const sv_paged_cache *c, void *ws, size_t ws_bytes, sv::Batch &b) {
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0 ||
-        ws_bytes < sv_cache_workspace_size())
-        return SV_EWORKSPACE;
-    if (!here.holds(ws)) return SV_EWORKSPACE;
-    if (!here.holds(c->k) || !here.holds(c->v) || !here.holds(c->pages) || !here.holds(c->q_start) ||
-        !here.holds(c->kv_len))
-        return SV_EINVAL;
-    b.pages = c->pages;
-    b.pages_stride = c->pages_stride;
-    b.q_start = c->q_start;
-    b.kv_len = c->kv_len;
-    b.B = c->B;
-    b.tokens = c->tokens;
-    b.num_pages = c->num_pages;
-    b.page_size = c->page_size;
-    b.max_pages = c->max_pages;
-    b.status = static_cast<uint32_t *>(ws);
-    return SV_OK;
-}
+using namespace svhost;
 
 template <class T, int kVec>
 int launch_append(sv::AppendParams &A, bool interleaved, unsigned grid, int per_block,
@@ -101,28 +53,6 @@ int launch_append(sv::AppendParams &A, bool interleaved, unsigned grid, int per_
     if (half % 8 == 0) return launch_append<T, 8>(A, interleaved, grid, per_block, st);
     if (half % 4 == 0) return launch_append<T, 4>(A, interleaved, grid, per_block, st);
     return launch_append<T, 2>(A, interleaved, grid, per_block, st);
-}
-
-typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (looked up once; the library does not link
-// libcuda).
-EncodeTiled encoder() {
-    static const EncodeTiled f = [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                             &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            fn = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(fn);
-    }();
-    return f;
 }
 
 // A map of one cache for boxes of 64 values x one head x `piece` slots of a
@@ -169,19 +99,6 @@ int query_map(CUtensorMap *map, const sv_paged_cache *c, const void *q, const in
     return r == CUDA_SUCCESS ? SV_OK : SV_EINVAL;
 }
 
-// SM count of the current device, queried once.
-int sm_count() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    static std::atomic<int> cached[64];
-    int n = cached[dev].load();
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cached[dev].store(n);
-    }
-    return n;
-}
-
 template <class T, int DP>
 int launch_attend(const sv::AttendParams &A, const CUtensorMap &kmap, const CUtensorMap &vmap,
                   const CUtensorMap &qmap, cudaStream_t st) {
@@ -219,7 +136,7 @@ int launch_attend(const sv::AttendParams &A, const CUtensorMap &kmap, const CUte
 
 extern "C" {
 
-size_t sv_cache_workspace_size(void) { return svhost::round_up(sv::kAttendWorkspace); }
+size_t sv_cache_workspace_size(void) { return round_up(sv::kAttendWorkspace); }
 
 int sv_append_kv(const sv_paged_cache *cache, const void *k, const int64_t *k_stride,
                  const void *v, const int64_t *v_stride, const void *q, const int64_t *q_stride,

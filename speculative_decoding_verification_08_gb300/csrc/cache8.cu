@@ -1,0 +1,291 @@
+// cache8.cu -- host side of the calls on caches of 8-bit values and of the append
+// with norms (sv_append_kv_normed, sv_read_kv, sv_paged_attention_scaled): argument
+// checks and launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "specverify.h"
+#include "sv_append8.cuh"
+#include "sv_cache_host.cuh"
+
+namespace {
+
+constexpr int kSms = 152;
+
+using namespace svhost;
+
+bool token_type(int32_t dtype) { return dtype == SV_BF16 || dtype == SV_F16; }
+
+// A cache of 16-bit values of the tokens' type, or of 8-bit values with scales.
+int check_either(const sv_paged_cache *c, const sv_cache_scales *s, int32_t dtype) {
+    const int rc = check_cache(c, s != nullptr);
+    if (rc != SV_OK) return rc;
+    if (!token_type(dtype) || (!s && c->dtype != dtype)) return SV_EINVAL;
+    if (!s || c->B == 0 || c->tokens == 0) return SV_OK;
+    if (!s->k || !s->v) return SV_EINVAL;
+    for (int i = 0; i < 3; ++i)
+        if (s->k_stride[i] < 0 || s->v_stride[i] < 0) return SV_EINVAL;
+    return SV_OK;
+}
+
+// Whether no two of a cache's vectors share a scale's byte by a stride of zero.
+bool own_bytes(const sv_paged_cache *c, const sv_cache_scales *s) {
+    const int32_t sizes[3] = {c->num_pages, c->page_size, c->kv_heads};
+    for (int i = 0; i < 3; ++i)
+        if (sizes[i] > 1 && (s->k_stride[i] == 0 || s->v_stride[i] == 0)) return false;
+    return true;
+}
+
+bool holds_scales(const CurrentDevice &here, const sv_cache_scales *s) {
+    return !s || (here.holds(s->k) && here.holds(s->v));
+}
+
+sv::Scales device_scales(const sv_cache_scales *s) {
+    sv::Scales d{};
+    if (!s) return d;
+    d.k = s->k;
+    d.v = s->v;
+    for (int i = 0; i < 3; ++i) {
+        d.k_st[i] = s->k_stride[i];
+        d.v_st[i] = s->v_stride[i];
+    }
+    return d;
+}
+
+template <class... P, class... A>
+int launch(void (*kernel)(P...), unsigned grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return SV_ECUDA;
+    g_last_grid = grid;
+    g_last_kernels = 1;
+    return SV_OK;
+}
+
+template <class T, bool kEight>
+int launch_append(const sv::AppendNormParams &A, bool interleaved, cudaStream_t st) {
+    const int rot = A.a.rot_dim;
+    int lanes = 1;
+    while (lanes * 8 < A.a.head_dim) lanes *= 2;
+    const int tokens = A.a.batch.tokens;
+    const int per_block = (int)std::min<int64_t>(
+        sv::kAppendTokens, std::max<int64_t>(1, ((int64_t)tokens + kSms * 4 - 1) / (kSms * 4)));
+    const unsigned grid = (unsigned)((tokens + per_block - 1) / per_block);
+    // as many warps as share a token's vectors evenly
+    const int vectors = A.a.q_heads + 2 * A.a.kv_heads, per_warp = 32 / lanes;
+    const int warps = (vectors + per_warp - 1) / per_warp;
+    const int rounds = (warps + sv::kAppendThreads / 32 - 1) / (sv::kAppendThreads / 32);
+    const int threads = (warps + rounds - 1) / rounds * 32;
+    auto kernel = interleaved || rot == 0 ? sv::append_norm_kernel<T, kEight, sv::kAdjacentTurn>
+                  : rot % 16 == 0         ? sv::append_norm_kernel<T, kEight, sv::kPackTurn>
+                                          : sv::append_norm_kernel<T, kEight, sv::kPairTurn>;
+    return launch(kernel, grid, threads, st, A, per_block, lanes);
+}
+
+template <class T, bool kPages>
+int launch_read(const sv::ReadParams &A, bool eight, int64_t rows, int per_block, cudaStream_t st) {
+    const int64_t grid = (rows + per_block - 1) / per_block;
+    if (grid > INT32_MAX) return SV_ETOOLARGE;
+    auto kernel = eight ? sv::read_kernel<T, true, kPages> : sv::read_kernel<T, false, kPages>;
+    return launch(kernel, (unsigned)grid, sv::kReadThreads, st, A, per_block);
+}
+
+// The parameters of read_kernel that do not depend on where the rows go.
+sv::ReadParams read_params(const sv_paged_cache *c, const sv_cache_scales *s) {
+    sv::ReadParams A{};
+    A.k_cache = c->k;
+    A.v_cache = c->v;
+    for (int i = 0; i < 3; ++i) {
+        A.kc_st[i] = c->k_stride[i];
+        A.vc_st[i] = c->v_stride[i];
+    }
+    A.scales = device_scales(s);
+    A.kv_heads = c->kv_heads;
+    A.head_dim = c->head_dim;
+    A.chunks = (c->head_dim + 15) / 16;
+    A.by_page.set((uint32_t)c->page_size);
+    A.by_chunks.set((uint32_t)A.chunks);
+    A.by_heads.set((uint32_t)c->kv_heads);
+    return A;
+}
+
+// The batch's sequences in 16 bits: keys, values and a page table.
+struct Scratch {
+    size_t half, table, bytes;
+    explicit Scratch(const sv_paged_cache *c) {
+        const size_t slots = (size_t)c->B * c->max_pages * c->page_size;
+        half = round_up(slots * c->kv_heads * c->head_dim * 2);
+        table = 2 * half;
+        bytes = table + round_up((size_t)c->B * c->max_pages * sizeof(int32_t));
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+int sv_append_kv_normed(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
+                        const void *k, const int64_t *k_stride, const void *v, const int64_t *v_stride,
+                        const void *q, const int64_t *q_stride, void *q_out, const int64_t *q_out_stride,
+                        int32_t q_heads, const void *q_norm, const void *k_norm, int32_t norm_dtype, float eps,
+                        const double *inv_freq, int32_t rot_dim, int32_t interleaved, const int32_t *positions,
+                        void *workspace, size_t workspace_bytes, sv_stream_t stream) {
+    sv::AppendNormParams P{};
+    int rc = check_either(cache, scales, dtype);
+    if (rc != SV_OK) return rc;
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 4 != 0 || (rot_dim > 0 && !inv_freq) ||
+        q_heads < 0 || q_heads > (1 << 16) || cache->kv_heads > (1 << 16) ||
+        (q == nullptr) != (q_heads == 0) || (q_norm && !q))
+        return SV_EINVAL;
+    if ((q_norm || k_norm) &&
+        ((norm_dtype != SV_F32 && norm_dtype != dtype) || !(eps >= 0.f) || !std::isfinite(eps)))
+        return SV_EINVAL;
+    if (cache->B == 0 || cache->tokens == 0) return SV_OK;
+    if (!k || !v || !k_stride || !v_stride || !vec_ok(k, k_stride, 2) || !vec_ok(v, v_stride, 2))
+        return SV_EINVAL;
+    if (q && (!q_out || !q_stride || !q_out_stride || !vec_ok(q, q_stride, 2) ||
+              !vec_ok(q_out, q_out_stride, 2)))
+        return SV_EINVAL;
+    if (scales && !own_bytes(cache, scales)) return SV_EINVAL;
+    const CurrentDevice here;
+    sv::AppendParams &A = P.a;
+    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!here.holds(k) || !here.holds(v) || (q && (!here.holds(q) || !here.holds(q_out))) ||
+        !here.holds_or_null(inv_freq) || !here.holds_or_null(positions) || !here.holds_or_null(q_norm) ||
+        !here.holds_or_null(k_norm) || !holds_scales(here, scales))
+        return SV_EINVAL;
+    A.k = k;
+    A.v = v;
+    A.q = q;
+    A.q_out = q_out;
+    A.k_cache = cache->k;
+    A.v_cache = cache->v;
+    for (int i = 0; i < 2; ++i) {
+        A.k_st[i] = k_stride[i];
+        A.v_st[i] = v_stride[i];
+        if (q) {
+            A.q_st[i] = q_stride[i];
+            A.o_st[i] = q_out_stride[i];
+        }
+    }
+    for (int i = 0; i < 3; ++i) {
+        A.kc_st[i] = cache->k_stride[i];
+        A.vc_st[i] = cache->v_stride[i];
+    }
+    A.inv_freq = inv_freq;
+    A.by_page.set((uint32_t)cache->page_size);
+    A.positions = positions;
+    A.q_heads = q_heads;
+    A.kv_heads = cache->kv_heads;
+    A.head_dim = cache->head_dim;
+    A.rot_dim = rot_dim;
+    P.scales = device_scales(scales);
+    P.q_norm = q_norm;
+    P.k_norm = k_norm;
+    P.norm_f32 = norm_dtype == SV_F32;
+    P.eps = eps;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool turn = interleaved != 0;
+    if (dtype == SV_BF16)
+        return scales ? launch_append<__nv_bfloat16, true>(P, turn, st) : launch_append<__nv_bfloat16, false>(P, turn, st);
+    return scales ? launch_append<__half, true>(P, turn, st) : launch_append<__half, false>(P, turn, st);
+}
+
+int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype, void *k_out,
+               const int64_t *k_out_stride, void *v_out, const int64_t *v_out_stride, void *workspace,
+               size_t workspace_bytes, sv_stream_t stream) {
+    int rc = check_either(cache, scales, dtype);
+    if (rc != SV_OK) return rc;
+    if (cache->kv_heads > (1 << 16)) return SV_EINVAL;
+    if (cache->B == 0 || cache->tokens == 0) return SV_OK;
+    if (!k_out || !v_out || !k_out_stride || !v_out_stride || !vec_ok(k_out, k_out_stride, 2) ||
+        !vec_ok(v_out, v_out_stride, 2))
+        return SV_EINVAL;
+    const CurrentDevice here;
+    sv::ReadParams A = read_params(cache, scales);
+    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!here.holds(k_out) || !here.holds(v_out) || !holds_scales(here, scales)) return SV_EINVAL;
+    A.k = k_out;
+    A.v = v_out;
+    for (int i = 0; i < 2; ++i) {
+        A.k_st[i] = k_out_stride[i];
+        A.v_st[i] = v_out_stride[i];
+    }
+    const int per_block = (int)std::min<int64_t>(
+        sv::kReadRows, std::max<int64_t>(1, ((int64_t)cache->tokens + kSms * 4 - 1) / (kSms * 4)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == SV_BF16 ? launch_read<__nv_bfloat16, false>(A, scales != nullptr, cache->tokens, per_block, st)
+                            : launch_read<__half, false>(A, scales != nullptr, cache->tokens, per_block, st);
+}
+
+size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads) {
+    if (check_cache(cache, true) != SV_OK || q_heads < 1 || cache->B == 0 || cache->tokens == 0) return 0;
+    return Scratch(cache).bytes;
+}
+
+int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
+                        const void *q, const int64_t *q_stride, void *out, const int64_t *out_stride,
+                        int32_t q_heads, float scale, int32_t window, void *scratch, size_t scratch_bytes,
+                        void *workspace, size_t workspace_bytes, sv_stream_t stream) {
+    int rc = check_cache(cache, true);
+    if (rc != SV_OK) return rc;
+    if (!scales) return SV_EINVAL;
+    if ((rc = check_either(cache, scales, dtype)) != SV_OK) return rc;
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || !std::isfinite(scale) || window < 0 ||
+        (int64_t)cache->tokens * (q_heads / cache->kv_heads) > INT32_MAX - 1024)
+        return SV_EINVAL;
+    if (cache->B == 0 || cache->tokens == 0) return SV_OK;
+    if (!q || !out || !q_stride || !out_stride || !vec_ok(q, q_stride, 2) || !vec_ok(out, out_stride, 2))
+        return SV_EINVAL;
+    const CurrentDevice here;
+    sv::ReadParams A = read_params(cache, scales);
+    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    if (!here.holds(q) || !here.holds(out) || !holds_scales(here, scales)) return SV_EINVAL;
+    const Scratch room(cache);
+    if (!scratch || scratch_bytes < room.bytes || (reinterpret_cast<uintptr_t>(scratch) % kAlign) != 0 ||
+        !here.holds(scratch))
+        return SV_EWORKSPACE;
+    char *base = static_cast<char *>(scratch);
+    A.k = base;
+    A.v = base + room.half;
+    A.table = reinterpret_cast<int32_t *>(base + room.table);
+    A.window = window < (int64_t)cache->max_pages * cache->page_size ? window : 0;
+    for (int64_t *s : {A.k_st, A.v_st}) {
+        s[0] = (int64_t)cache->kv_heads * cache->head_dim;
+        s[1] = cache->head_dim;
+    }
+    const int64_t rows = (int64_t)cache->B * cache->max_pages * cache->page_size;
+    const int per_block = cache->page_size % 16 == 0 ? 16 : 8;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    rc = dtype == SV_BF16 ? launch_read<__nv_bfloat16, true>(A, true, rows, per_block, st)
+                          : launch_read<__half, true>(A, true, rows, per_block, st);
+    if (rc != SV_OK) return rc;
+    sv_paged_cache plain = *cache;
+    plain.k = A.k;
+    plain.v = A.v;
+    plain.dtype = dtype;
+    for (int64_t *s : {plain.k_stride, plain.v_stride}) {
+        s[0] = (int64_t)cache->page_size * cache->kv_heads * cache->head_dim;
+        s[1] = (int64_t)cache->kv_heads * cache->head_dim;
+        s[2] = cache->head_dim;
+    }
+    plain.num_pages = cache->B * cache->max_pages;
+    plain.pages = A.table;
+    plain.pages_stride = cache->max_pages;
+    rc = sv_paged_attention(&plain, q, q_stride, out, out_stride, q_heads, scale, window, workspace,
+                            workspace_bytes, stream);
+    if (rc == SV_OK) g_last_kernels = 2;
+    return rc;
+}
+
+}  // extern "C"

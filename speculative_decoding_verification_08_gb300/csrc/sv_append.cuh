@@ -29,7 +29,6 @@ namespace sv {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 4;
-constexpr int kMaxHeadDim = 128;
 
 struct AppendParams {
     Batch batch;

@@ -11,6 +11,8 @@
 
 namespace sv {
 
+constexpr int kMaxHeadDim = 128;
+
 // Division of 0 <= n < 2^31 by a fixed d >= 1: the high word of n m, shifted;
 // m = ceil(2^(31 + s) / d) with 2^s >= d, whose excess over the exact factor
 // is too small to reach the next integer for these n.
