@@ -5,10 +5,12 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "specverify.h"
 #include "sv_append8.cuh"
+#include "sv_attend8.cuh"
 #include "sv_cache_host.cuh"
 
 namespace {
@@ -56,10 +58,11 @@ sv::Scales device_scales(const sv_cache_scales *s) {
 }
 
 template <class... P, class... A>
-int launch(void (*kernel)(P...), unsigned grid, int threads, cudaStream_t st, A... args) {
+int launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -89,7 +92,7 @@ int launch_append(const sv::AppendNormParams &A, bool interleaved, cudaStream_t 
     auto kernel = interleaved || rot == 0 ? sv::append_norm_kernel<T, kEight, sv::kAdjacentTurn>
                   : rot % 16 == 0         ? sv::append_norm_kernel<T, kEight, sv::kPackTurn>
                                           : sv::append_norm_kernel<T, kEight, sv::kPairTurn>;
-    return launch(kernel, grid, threads, st, A, per_block, lanes);
+    return launch(kernel, grid, threads, 0, st, A, per_block, lanes);
 }
 
 template <class T, bool kPages>
@@ -97,7 +100,7 @@ int launch_read(const sv::ReadParams &A, bool eight, int64_t rows, int per_block
     const int64_t grid = (rows + per_block - 1) / per_block;
     if (grid > INT32_MAX) return SV_ETOOLARGE;
     auto kernel = eight ? sv::read_kernel<T, true, kPages> : sv::read_kernel<T, false, kPages>;
-    return launch(kernel, (unsigned)grid, sv::kReadThreads, st, A, per_block);
+    return launch(kernel, (unsigned)grid, sv::kReadThreads, 0, st, A, per_block);
 }
 
 // The parameters of read_kernel that do not depend on where the rows go.
@@ -129,6 +132,43 @@ struct Scratch {
         bytes = table + round_up((size_t)c->B * c->max_pages * sizeof(int32_t));
     }
 };
+
+// A map of one cache of codes for boxes of 128 values x one head x `piece` slots of
+// a page: [pages][slots][heads][values], whatever their order in memory.  Values
+// past head_dim and pages outside the cache read as zeros.
+int code_map(CUtensorMap *map, const sv_paged_cache *c, void *base, const int64_t *stride, int piece) {
+    const EncodeTiled encode = encoder();
+    if (!encode) return SV_ECUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->kv_heads, (cuuint64_t)c->page_size,
+                                (cuuint64_t)c->num_pages};
+    cuuint64_t bytes[3] = {(cuuint64_t)stride[2], (cuuint64_t)stride[1], (cuuint64_t)stride[0]};
+    // the stride of an axis of length 1 means nothing: any valid one will do
+    for (int i = 0; i < 3; ++i)
+        if (dims[i + 1] == 1) bytes[i] = (cuuint64_t)c->head_dim;
+    const cuuint32_t box[4] = {128, 1, (cuuint32_t)piece, 1}, step[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, bytes, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SV_OK : SV_EINVAL;
+}
+
+template <class T>
+int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ECUDA;
+    constexpr int bytes = sv::Attend8Smem<T>::kBytes;
+    static std::atomic<int> raised[64];
+    if (!raised[dev].load()) {
+        if (cudaFuncSetAttribute(sv::attend8_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess)
+            return SV_ECUDA;
+        raised[dev].store(1);
+    }
+    const int sms = sm_count();
+    if (sms <= 0) return SV_ECUDA;
+    const unsigned grid = (unsigned)std::min(sms, sv::kAttendMaxCtas);
+    return launch(sv::attend8_kernel<T>, grid, sv::kAttendThreads, bytes, st, A, kmap, vmap);
+}
 
 }  // namespace
 
@@ -230,6 +270,9 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
 
 size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads) {
     if (check_cache(cache, true) != SV_OK || q_heads < 1 || cache->B == 0 || cache->tokens == 0) return 0;
+    // (rows of a sequence and kv head, on average)
+    const int64_t rows = (int64_t)cache->tokens * (q_heads / cache->kv_heads) / cache->B;
+    if (rows <= 64) return 0;
     return Scratch(cache).bytes;
 }
 
@@ -248,25 +291,57 @@ int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales
     if (!q || !out || !q_stride || !out_stride || !vec_ok(q, q_stride, 2) || !vec_ok(out, out_stride, 2))
         return SV_EINVAL;
     const CurrentDevice here;
-    sv::ReadParams A = read_params(cache, scales);
-    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, A.batch)) != SV_OK) return rc;
+    sv::Batch batch{};
+    if ((rc = bind_cache(here, cache, workspace, workspace_bytes, batch)) != SV_OK) return rc;
     if (!here.holds(q) || !here.holds(out) || !holds_scales(here, scales)) return SV_EINVAL;
+    if (window >= (int64_t)cache->max_pages * cache->page_size) window = 0;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!scratch) {
+        sv::Attend8Params P{};
+        sv::AttendParams &A = P.a;
+        A.batch = batch;
+        A.q = q;
+        A.out = out;
+        for (int i = 0; i < 2; ++i) {
+            A.q_st[i] = q_stride[i];
+            A.o_st[i] = out_stride[i];
+        }
+        A.q_heads = q_heads;
+        A.kv_heads = cache->kv_heads;
+        A.group = q_heads / cache->kv_heads;
+        A.by_group.set((uint32_t)A.group);
+        A.by_page.set((uint32_t)cache->page_size);
+        A.head_dim = cache->head_dim;
+        A.window = window;
+        A.piece = 8;
+        while (A.piece < sv::kKeys && cache->page_size % (2 * A.piece) == 0) A.piece *= 2;
+        A.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504f;
+        A.q_mode = scale == 0.f ? 2 : scale < 0.f ? 1 : 0;
+        A.workspace = static_cast<char *>(workspace);
+        P.scales = device_scales(scales);
+        CUtensorMap kmap, vmap;
+        if ((rc = code_map(&kmap, cache, cache->k, cache->k_stride, A.piece)) != SV_OK) return rc;
+        if ((rc = code_map(&vmap, cache, cache->v, cache->v_stride, A.piece)) != SV_OK) return rc;
+        return dtype == SV_BF16 ? launch_attend8<__nv_bfloat16>(P, kmap, vmap, st)
+                                : launch_attend8<__half>(P, kmap, vmap, st);
+    }
+    // many rows: the sequences back to 16 bits, and the attention over those
     const Scratch room(cache);
-    if (!scratch || scratch_bytes < room.bytes || (reinterpret_cast<uintptr_t>(scratch) % kAlign) != 0 ||
-        !here.holds(scratch))
+    if (scratch_bytes < room.bytes || (reinterpret_cast<uintptr_t>(scratch) % kAlign) != 0 || !here.holds(scratch))
         return SV_EWORKSPACE;
+    sv::ReadParams A = read_params(cache, scales);
+    A.batch = batch;
     char *base = static_cast<char *>(scratch);
     A.k = base;
     A.v = base + room.half;
     A.table = reinterpret_cast<int32_t *>(base + room.table);
-    A.window = window < (int64_t)cache->max_pages * cache->page_size ? window : 0;
+    A.window = window;
     for (int64_t *s : {A.k_st, A.v_st}) {
         s[0] = (int64_t)cache->kv_heads * cache->head_dim;
         s[1] = cache->head_dim;
     }
     const int64_t rows = (int64_t)cache->B * cache->max_pages * cache->page_size;
     const int per_block = cache->page_size % 16 == 0 ? 16 : 8;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     rc = dtype == SV_BF16 ? launch_read<__nv_bfloat16, true>(A, true, rows, per_block, st)
                           : launch_read<__half, true>(A, true, rows, per_block, st);
     if (rc != SV_OK) return rc;

@@ -130,6 +130,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // tokens (CTAs with many short tiles finish late).
 constexpr int kTileCost = 2;
 
+// (kTileRows: packed rows of a tile; kFixed: its fixed cost.)
+template <int kTileRows, int kFixed>
 struct SeqCost {
     int32_t n, len, row0, tiles, packed;  // packed: rows n * G
     __device__ __forceinline__ void load(const AttendParams &A, int32_t b) {
@@ -138,13 +140,13 @@ struct SeqCost {
         len = s.len;
         row0 = s.row0;
         packed = n * A.group;  // the host checks that it fits
-        tiles = (packed + 2 * kRows - 1) / (2 * kRows);
+        tiles = (packed + kTileRows - 1) / kTileRows;
     }
-    __device__ __forceinline__ int rows(int t) const { return min(2 * kRows, packed - t * 2 * kRows); }
+    __device__ __forceinline__ int rows(int t) const { return min(kTileRows, packed - t * kTileRows); }
     // key blocks [lo, hi) that tile t's rows see, and one past its last slot
     __device__ __forceinline__ void blocks(const AttendParams &A, int t, int &lo, int &hi,
                                            int &end) const {
-        const int r0 = t * 2 * kRows;
+        const int r0 = t * kTileRows;
         end = max(0, len - n + A.by_group.div(r0 + rows(t) - 1) + 1);
         hi = (end + kKeys - 1) / kKeys;
         lo = A.window > 0 ? max(0, len - n + A.by_group.div(r0) - A.window + 1) / kKeys : 0;
@@ -153,7 +155,7 @@ struct SeqCost {
     __device__ __forceinline__ int cost(const AttendParams &A, int t) const {
         int lo, hi, end;
         blocks(A, t, lo, hi, end);
-        return kTileCost + max(1, hi - lo);
+        return kFixed + max(1, hi - lo);
     }
 };
 
@@ -173,8 +175,9 @@ struct Piece {
 };
 
 // Walks one CTA's run of the work (a whole warp).
+template <int kTileRows, int kFixed>
 struct Walker {
-    SeqCost s;
+    SeqCost<kTileRows, kFixed> s;
     int32_t b, t, h, off;
     int64_t left, unit, total;
     int32_t ctas;
@@ -224,11 +227,11 @@ struct Walker {
             }
             int lo, hi, end;
             s.blocks(A, t, lo, hi, end);
-            const int cost = kTileCost + max(1, hi - lo);
+            const int cost = kFixed + max(1, hi - lo);
             const int from = off, to = (int)min((int64_t)cost, off + left);
             p.b = b;
             p.h = h;
-            p.row = t * 2 * kRows;
+            p.row = t * kTileRows;
             p.rows = s.rows(t);
             p.end = end;
             p.token = s.row0;
@@ -244,12 +247,12 @@ struct Walker {
                     ++t;
                 }
             }
-            if (to <= kTileCost) continue;  // the run ends before the tile's first block
-            p.lo = lo + max(0, from - kTileCost);
-            p.n = hi > lo ? to - max(from, kTileCost) : 0;
+            if (to <= kFixed) continue;  // the run ends before the tile's first block
+            p.lo = lo + max(0, from - kFixed);
+            p.n = hi > lo ? to - max(from, kFixed) : 0;
             p.split = p.rows <= kRows;
             p.n1 = p.split ? p.n / 2 : p.n;
-            p.first = from <= kTileCost ? (int32_t)blockIdx.x : cta_of(unit_of_tile + kTileCost);
+            p.first = from <= kFixed ? (int32_t)blockIdx.x : cta_of(unit_of_tile + kFixed);
             p.parts = (to == cost ? (int32_t)blockIdx.x : cta_of(unit_of_tile + cost - 1)) - p.first + 1;
             return true;
         }
@@ -402,8 +405,9 @@ __device__ __forceinline__ void meet(AttendShared &sh, unsigned long long *bar, 
 }
 
 // Cost of sequence b's tiles over all heads, for each lane's own b (< 0: none).
+template <int kTileRows, int kFixed>
 __device__ __forceinline__ int64_t sequence_cost(const AttendParams &A, int32_t b, int lane) {
-    SeqCost s;
+    SeqCost<kTileRows, kFixed> s;
     s.n = s.len = s.tiles = s.packed = 0;
     if (b >= 0) s.load(A, b);
     int64_t c = 0;
@@ -414,7 +418,7 @@ __device__ __forceinline__ int64_t sequence_cost(const AttendParams &A, int32_t 
     while (long_ones) {
         const int who = __ffs(long_ones) - 1;
         long_ones &= long_ones - 1;
-        SeqCost o;
+        SeqCost<kTileRows, kFixed> o;
         o.n = __shfl_sync(0xffffffffu, s.n, who);
         o.len = __shfl_sync(0xffffffffu, s.len, who);
         o.tiles = __shfl_sync(0xffffffffu, s.tiles, who);
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     int64_t c = 0, last_cost = 0;
     for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
         const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
-        last_cost = sequence_cost(A, b, lane);
+        last_cost = sequence_cost<2 * kRows, kTileCost>(A, b, lane);
         c += last_cost;
         if (blockIdx.x == 0 && b >= 0 && load_sequence(A.batch, b).bad)
             atomicOr(status, SV_STATUS_BAD_LENGTH);
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         int64_t base = 0;
         for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
             const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
-            const int64_t own = A.batch.B <= kAttendThreads ? last_cost : sequence_cost(A, b, lane);
+            const int64_t own = A.batch.B <= kAttendThreads ? last_cost : sequence_cost<2 * kRows, kTileCost>(A, b, lane);
             int64_t inc = own;
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 11) {
             // ---- the schedule ---------------------------------------------
-            Walker walk;
+            Walker<2 * kRows, kTileCost> walk;
             walk.left = 0;
             if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas, lane);
             int k = 0;

@@ -122,6 +122,21 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A e4m3 (bits 7-9: 0), B
+// e5m2 (10-12: 1), both with contiguous K.
+__host__ __device__ constexpr uint32_t instr_desc_f8(int m, int n) {
+    return (1u << 4) | (1u << 10) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(m / 16) << 24);
+}
+
+// d (+)= a b^T of 8-bit floats, one thread; a and b in shared memory.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
 // Arrives on the barrier once every product issued so far by this thread is done.
 __device__ __forceinline__ void commit(unsigned long long *bar) {
     asm volatile(
