@@ -167,7 +167,7 @@ int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CU
     const int sms = sm_count();
     if (sms <= 0) return SV_ECUDA;
     const unsigned grid = (unsigned)std::min(sms, sv::kAttendMaxCtas);
-    return launch(sv::attend8_kernel<T>, grid, sv::kAttendThreads, bytes, st, A, kmap, vmap);
+    return launch(sv::attend8_kernel<T>, grid, sv::kThreads8, bytes, st, A, kmap, vmap);
 }
 
 }  // namespace

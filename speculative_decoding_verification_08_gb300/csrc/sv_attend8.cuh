@@ -16,19 +16,23 @@
 // the tile's largest and good to 2^-33 of it below.  The parts are columns of their own
 // (their products are added in fp32 by the softmax threads), so a block of keys is
 // read from shared memory once.
-// Values need their rows' axis contiguous in pairs: four warps turn codes into bf16
-// (exact: the code's bits moved, times 2^120); their scales go into the weights.
-// Weights are rounded to bf16 for the second product, or for fp16 queries taken as
-// the sum of two bf16 (2^-17), in columns beside each other.
+// Values need their slots' axis contiguous for the second product, which 16-bit types
+// have: four warps turn codes into fp16 (exact).  Their scales go into the weights,
+// relative to a power of two that follows the largest scale: weight times scale, in
+// fp16 and taken 2^7 times as large, is the one rounding between fp32 scores and the
+// result (11 bits; what is below 2^-21 of the row's and the scales' largest is rounded
+// to steps of 2^-31 of them).
 //
 // Softmax: weights are relative to a reference per row, which follows the row's
 // maximum only when a score is more than 2^8 above it; whether any is, is one vote
-// of the 128 threads per block, and finding the new maxima the rare way.
+// of the 128 threads per block, and finding the new maxima the rare way.  Two groups of
+// four warps take the even and the odd blocks of a tile, each with scores, weights,
+// outputs and references of its own, and join them at the tile's end.
 //
 // Work split, partial states and their join: as in sv_attend.cuh.
 //
-// Warps 0-3 softmax, 4-7 values to bf16, 8 copies (TMA boxes of page pieces), 9
-// issues S, 10 issues O, 11 walks the CTA's run, publishes its pieces and prepares
+// Warps 0-7 softmax, 8-11 values to fp16, 12 copies (TMA boxes of page pieces), 13
+// issues S, 14 issues O, 15 walks the CTA's run, publishes its pieces and prepares
 // the queries.  Every wait is bounded, as there.
 #pragma once
 
@@ -39,11 +43,13 @@ namespace sv {
 
 constexpr int kRows8 = 32;      // packed rows of a tile
 constexpr int kTileCost8 = 3;   // a tile's fixed cost in key blocks
-constexpr int kSoftmaxRegs8 = 232, kOtherRegs8 = 136;
-static_assert(128 * kSoftmaxRegs8 + 256 * kOtherRegs8 <= kAttendThreads * 168, "register split");
+constexpr int kThreads8 = 512;
+constexpr int kSoftmaxRegs8 = 168, kOtherRegs8 = 88;
+static_assert(256 * kSoftmaxRegs8 + 256 * kOtherRegs8 <= kThreads8 * 128, "register split");
 constexpr int kRaw = kKeys * 128;     // a block of codes
 constexpr int kRing8 = 3;             // blocks of keys, and of values, in flight
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
+constexpr int kNoScale = -200;        // below every e8m0 exponent
 
 struct Attend8Params {
     AttendParams a;
@@ -53,16 +59,15 @@ struct Attend8Params {
 template <class T>
 struct Attend8Smem {
     static constexpr int kParts = __is_same(T, __nv_bfloat16) ? 3 : 4;
-    static constexpr int kWeights = __is_same(T, __nv_bfloat16) ? 1 : 2;
     static constexpr int kQuery = kParts * kRows8 * 128;
     static constexpr int kMisc = 3072;
     static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRing8 * kRaw, kVc = kV + kRing8 * kRaw,
                          kP = kVc + 2 * 2 * kRaw, kBytes = kP + 2 * kRaw;
-    static constexpr int kScoreCols = kParts * kRows8, kOutCols = kWeights * kRows8;
-    static constexpr int kOut = 2 * kScoreCols;  // first column of O
-    static constexpr uint32_t kCols = kOut + kOutCols <= 256 ? 256 : 512;
+    static constexpr int kScoreCols = kParts * kRows8;
+    static constexpr int kOut = 2 * kScoreCols;  // first column of the groups' O
+    static constexpr uint32_t kCols = kOut + 2 * kRows8 <= 256 ? 256 : 512;
     static_assert(kBytes <= 227 * 1024 && kQ % 1024 == 0 && kQuery % 1024 == 0, "shared memory");
-    static_assert(kOut + kOutCols <= 512, "tensor memory");
+    static_assert(kOut + 2 * kRows8 <= 512, "tensor memory");
 };
 
 struct Attend8Shared {
@@ -74,14 +79,15 @@ struct Attend8Shared {
     int32_t dead, b0, last;
     float q_factor[2];          // power of two of a tile's queries, times the score scale
     int64_t skip;
-    int64_t sums[kAttendThreads / 32];
+    int64_t sums[kThreads8 / 32];
 };
 static_assert(sizeof(Attend8Shared) <= 1024, "misc region");
 
-struct Attend8Rows {            // behind it
-    float across[4][kRows8];    // a warp's maxima or sums
-    float minus[4][kRows8];     // each warp's copy of what all of them know alike
-    float factor[4][kRows8];
+struct __align__(16) Attend8Rows {  // behind it, for each of the two groups
+    float minus[2][kRows8];     // minus the rows' references
+    float factor[2][kRows8];    // what a new reference makes of sums and outputs
+    float across[2][4][kRows8]; // its warps' maxima or sums
+    int32_t exponent[2][4];     // its warps' largest scales
 };
 static_assert(sizeof(Attend8Rows) <= 2048, "misc region");
 
@@ -119,19 +125,30 @@ struct PieceReader8 {
         }
     }
 };
-constexpr int kPieceReaders8 = 11;
+constexpr int kPieceReaders8 = 15;
 
-// The softmax's 128 threads: all of them come to each, whatever timed out.
-__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
+// Barriers of the softmax's threads: a group's 128 (number 1 or 2), or all 256 (3).
+// All of them come to each, whatever timed out.
+template <int kCount>
+__device__ __forceinline__ void softmax_barrier(int number) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(number), "n"(kCount) : "memory");
+}
+template <int kCount>
+__device__ __forceinline__ bool softmax_any(int number, bool x) {
     uint32_t r;
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.u32 q, %1, 0;\n"
-        "barrier.cta.red.or.pred p, 1, 128, q; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p, q; setp.ne.u32 q, %2, 0;\n"
+        "barrier.cta.red.or.pred p, %1, %3, q; selp.u32 %0, 1, 0, p; }"
         : "=r"(r)
-        : "r"((uint32_t)x)
+        : "r"(number), "r"((uint32_t)x), "n"(kCount)
         : "memory");
     return r != 0;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
 }
 
 // Joins each of 32 columns over a warp's lanes; lane i gets column i.
@@ -149,18 +166,11 @@ __device__ __forceinline__ float across_lanes(float (&v)[32], int lane, F join) 
     return v[0];
 }
 
-// Four e4m3 codes as bf16: the bits of exponent and mantissa moved into bf16's
-// places stand for the value times 2^-120 (subnormals too).  No code is read as NaN
-// (0x7f is 480): what lies in unused slots stays finite.
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
-    uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-    a = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
-    b = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a), up);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&b), up);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
+// Four e4m3 codes as fp16.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 // Four floats to e5m2 codes, and what the codes leave of them.
@@ -181,19 +191,18 @@ __device__ __forceinline__ uint32_t split_off(float (&x)[4]) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(kAttendThreads, 1)
+__global__ void __launch_bounds__(kThreads8, 1)
     attend8_kernel(const __grid_constant__ Attend8Params P8, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
     typedef Attend8Smem<T> L;
     typedef SeqCost<kRows8, kTileCost8> Cost;
     constexpr int kParts = L::kParts;
-    constexpr bool kTwo = L::kWeights == 2;
     constexpr uint32_t kIdescS = tc::instr_desc_f8(kKeys, L::kScoreCols);
     // (bit 15: A's slots are its rows in memory, as B's)
-    constexpr uint32_t kIdescO = tc::instr_desc(true, true, 128, L::kOutCols) | (1u << 15);
+    constexpr uint32_t kIdescO = tc::instr_desc(false, true, 128, kRows8) | (1u << 15);
     extern __shared__ __align__(1024) char smem[];
     Attend8Shared &sh = *reinterpret_cast<Attend8Shared *>(smem);
-    Attend8Rows &rows_of = *reinterpret_cast<Attend8Rows *>(smem + 1024);
+    Attend8Rows &shared = *reinterpret_cast<Attend8Rows *>(smem + 1024);
     const AttendParams &A = P8.a;
     const int tid = threadIdx.x, warp = tc::uniform(tid / 32), lane = tid % 32;
     uint32_t *status = A.batch.status;
@@ -204,7 +213,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         if (tid == 0) atomicOr(status, SV_STATUS_TIMEOUT);
         return;
     }
-    if (warp == 9) tc::tmem_alloc(&sh.tmem, L::kCols);
+    if (warp == 13) tc::tmem_alloc(&sh.tmem, L::kCols);
     if (tid == 0) {
         for (int i = 0; i < kRing8; ++i) {
             mbar_init(&sh.k_full[i], 1);
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.q_full[i], 1);
-            mbar_init(&sh.q_empty[i], 5);
+            mbar_init(&sh.q_empty[i], 9);
             mbar_init(&sh.drain[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     }
     // heads of up to 64 values: the other half of the values' rows is zero throughout
     if (!wide)
-        for (int i = tid; i < 2 * kRaw / 16; i += kAttendThreads)
+        for (int i = tid; i < 2 * kRaw / 16; i += kThreads8)
             *reinterpret_cast<uint4 *>(smem + L::kVc + (i / (kRaw / 16) * 2 + 1) * kRaw + i % (kRaw / 16) * 16) =
                 make_uint4(0, 0, 0, 0);
     tc::fence_async_smem();
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
     // the batch's blocks, and where this CTA's run of them begins
     int64_t c = 0, last_cost = 0;
-    for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
+    for (int32_t b0 = 0; b0 < A.batch.B; b0 += kThreads8) {
         const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
         last_cost = sequence_cost<kRows8, kTileCost8>(A, b, lane);
         c += last_cost;
@@ -253,17 +262,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     __syncthreads();
     tc::fence_after();
     int64_t total = 0;
-    for (int w = 0; w < kAttendThreads / 32; ++w) total += sh.sums[w];
+    for (int w = 0; w < kThreads8 / 32; ++w) total += sh.sums[w];
     const int32_t ctas = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, total));
     const int64_t u0 = quotient((int64_t)blockIdx.x * total, ctas),
                   u1 = quotient(((int64_t)blockIdx.x + 1) * total, ctas);
     const bool idle = total == 0 || (int32_t)blockIdx.x >= ctas || u0 >= u1;
     if (!idle) {
         int64_t base = 0;
-        for (int32_t b0 = 0; b0 < A.batch.B; b0 += kAttendThreads) {
+        for (int32_t b0 = 0; b0 < A.batch.B; b0 += kThreads8) {
             const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
             const int64_t own =
-                A.batch.B <= kAttendThreads ? last_cost : sequence_cost<kRows8, kTileCost8>(A, b, lane);
+                A.batch.B <= kThreads8 ? last_cost : sequence_cost<kRows8, kTileCost8>(A, b, lane);
             int64_t inc = own;
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (lane == 31) sh.sums[warp] = inc;
             __syncthreads();
             int64_t at = base;
-            for (int w = 0; w < kAttendThreads / 32; ++w) {
+            for (int w = 0; w < kThreads8 / 32; ++w) {
                 if (w < warp) at += sh.sums[w];
                 base += sh.sums[w];
             }
@@ -287,9 +296,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     }
     const uint32_t tmem = sh.tmem;
 
-    if (warp >= 4) {
+    if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs8));
-        if (warp == 11) {
+        if (warp == 15) {
             // ---- the schedule, and the queries of its pieces -------------------
             Walker<kRows8, kTileCost8> walk;
             walk.left = 0;
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_full[qb]);
             }
-        } else if (warp == 8) {
+        } else if (warp == 12) {
             // ---- copies of codes ------------------------------------------------
             const int boxes = kKeys / A.piece;
             const bool active = lane < boxes;
@@ -422,13 +431,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             // the last copies have landed before the CTA may end
             for (int n = max(0, kn - kRing8); n < kn; ++n) mbar_wait(&sh.k_full[n % kRing8], n / kRing8 & 1);
             for (int n = max(0, vn - kRing8); n < vn; ++n) mbar_wait(&sh.v_full[n % kRing8], n / kRing8 & 1);
-        } else if (warp == 9) {
+        } else if (warp == 13) {
             // ---- scores ---------------------------------------------------------
             const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
             const uint64_t k_desc = tc::smem_desc(smem_u32(smem + L::kK), 16, 1024);
             const uint64_t q_desc = tc::smem_desc(smem_u32(smem + L::kQ), 16, 1024);
             const int steps = (D + 31) / 32;
-            uint32_t n = 0, qn = 0;
+            uint32_t n = 0, qn = 0, used[2] = {0, 0};  // blocks, tiles, blocks of each group
             PieceReader8 reader;
             bool ok = true;  // a wait gave up: nothing more is issued or handed back
             while (ok && reader.next(sh, status)) {
@@ -439,9 +448,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 ok = ok && __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.q_full[qb], (qn >> 1) & 1, status));
                 ++qn;
                 for (int i = 0; i < blocks && ok; ++i, ++n) {
-                    const uint32_t st = n % kRing8, sb = n & 1;
+                    const uint32_t st = n % kRing8, sb = i & 1;
+                    const uint32_t turn = sb ? used[1]++ : used[0]++;
                     ok = __all_sync(0xffffffffu, hold8(sh, &sh.k_full[st], n / kRing8 & 1, status));
-                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.s_empty[sb], ((n >> 1) & 1) ^ 1, status));
+                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.s_empty[sb], (turn & 1) ^ 1, status));
                     if (!ok) break;
                     tc::fence_after();
                     if (tc::elect()) {
@@ -458,19 +468,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (tc::elect()) tc::commit(&sh.drain[0]);
             __syncwarp();
             mbar_wait(&sh.drain[0], 0);
-        } else if (warp == 10) {
+        } else if (warp == 14) {
             // ---- outputs --------------------------------------------------------
             const uint32_t tm = (uint32_t)tc::uniform((int)tmem) + L::kOut;
             const uint64_t v_desc = tc::smem_desc(smem_u32(smem + L::kVc), kRaw, 1024);
             const uint64_t p_desc = tc::smem_desc(smem_u32(smem + L::kP), kRaw, 1024);
-            uint32_t n = 0;
+            uint32_t used[2] = {0, 0};
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh, status)) {
                 const int blocks = tc::uniform(sh.pieces[reader.k].n);
                 reader.done(sh, lane);
-                for (int i = 0; i < blocks && ok; ++i, ++n) {
-                    const uint32_t b = n & 1, turn = (n >> 1) & 1;
+                for (int i = 0; i < blocks && ok; ++i) {
+                    const uint32_t b = i & 1, turn = (b ? used[1]++ : used[0]++) & 1;
                     ok = __all_sync(0xffffffffu, hold8(sh, &sh.vc_full[b], turn, status));
                     ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.p_full[b], turn, status));
                     if (!ok) break;
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * (kRaw / 16);
 #pragma unroll
                         for (int s = 0; s < kKeys / 16; ++s)
-                            tc::mma_ss(tm, vd + s * (2048 / 16), pd + s * (2048 / 16), kIdescO, i > 0 || s > 0);
+                            tc::mma_ss(tm + b * kRows8, vd + s * (2048 / 16), pd + s * (2048 / 16), kIdescO, i > 1 || s > 0);
                         tc::commit(&sh.pv_done[b]);
                     }
                     __syncwarp();
@@ -489,37 +499,41 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             __syncwarp();
             mbar_wait(&sh.drain[1], 0);
         } else {
-            // ---- values to bf16 ---------------------------------------------------
-            const int t = tid - 128;
+            // ---- values to fp16 ---------------------------------------------------
+            const int t = tid - 256;
             // a thread's chunk of 16 values and its slot of a group (eight lanes' chunks
             // lie in different banks)
             const int ch = wide ? t % 8 : t % 4, u = t / 4;
             const int slot0 = wide ? t / 8 : (u >> 3) * 8 + ((u & 1) << 2) + ((u >> 1) & 3);
             const int rounds = wide ? 8 : 4, per = wide ? 16 : 32;
             const bool odd_first = wide ? ch >= 4 : u & 1;
-            uint32_t n = 0;
+            uint32_t n = 0, used[2] = {0, 0};
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh, status)) {
                 const int blocks = sh.pieces[reader.k].n;
+                // slots from the tile's end on: whatever lies there, zeros
+                const int end = sh.pieces[reader.k].end - sh.pieces[reader.k].lo * kKeys;
                 reader.done(sh, lane);
                 for (int i = 0; i < blocks && ok; ++i, ++n) {
-                    const uint32_t st = n % kRing8, b = n & 1;
+                    const uint32_t st = n % kRing8, b = i & 1, turn = b ? used[1]++ : used[0]++;
+                    const int here = end - i * kKeys;
                     ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[st], n / kRing8 & 1, status));
-                    if (ok && n >= 2)
-                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], ((n >> 1) - 1) & 1, status));
+                    if (ok && turn > 0)
+                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1, status));
                     if (!ok) break;
                     const char *from = smem + L::kV + st * kRaw;
                     char *to = smem + L::kVc + b * 2 * kRaw + (ch / 4) * kRaw;
 #pragma unroll 4
                     for (int k = 0; k < rounds; ++k) {
                         const int slot = k * per + slot0, x = slot & 7;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(from + slot * 128 + ((ch ^ x) * 16));
+                        uint4 w = *reinterpret_cast<const uint4 *>(from + slot * 128 + ((ch ^ x) * 16));
+                        if (slot >= here) w = make_uint4(0, 0, 0, 0);
                         uint4 lo, hi;
-                        codes_to_bf16(w.x, lo.x, lo.y);
-                        codes_to_bf16(w.y, lo.z, lo.w);
-                        codes_to_bf16(w.z, hi.x, hi.y);
-                        codes_to_bf16(w.w, hi.z, hi.w);
+                        codes_to_half(w.x, lo.x, lo.y);
+                        codes_to_half(w.y, lo.z, lo.w);
+                        codes_to_half(w.z, hi.x, hi.y);
+                        codes_to_half(w.w, hi.z, hi.w);
                         const int j = (ch % 4) * 2;
                         char *row = to + slot * 128;
                         *reinterpret_cast<uint4 *>(row + (((j + (odd_first ? 1 : 0)) ^ x) * 16)) = odd_first ? hi : lo;
@@ -537,219 +551,308 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs8));
         // ---- softmax: a slot to a thread ------------------------------------------
-        const int gt = tid;
-        const uint32_t lanes_at = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t t_o = lanes_at + L::kOut;
-        uint32_t n = 0, qn = 0;
+        const int g = warp / 4, gw = warp % 4, gt = gw * 32 + lane;
+        const uint32_t lanes_at = tmem + ((uint32_t)(gw * 32) << 16);
+        const uint32_t t_s = lanes_at + g * L::kScoreCols, t_o = lanes_at + L::kOut;
+        uint32_t used = 0, others = 0, qn = 0;  // blocks of this group and of the other, tiles
         PieceReader8 reader;
         for (;;) {
-            // (all four warps go on, or none: they meet at barriers)
-            const bool got = !softmax_any(!reader.next(sh, status));
-            if (!got) break;
+            // (all eight warps go on, or none: they meet at barriers; and the last
+            // tile's outputs have been read)
+            if (softmax_any<256>(3, !reader.next(sh, status))) break;
             const Piece &p = sh.pieces[reader.k];
-            float minus[kRows8];  // minus the rows' references
-            float sums[kRows8];   // this thread's slots'
+            const int blocks = p.n, past = p.past, row0 = p.row, rows = p.rows;
+            const int mine = (blocks + 1 - g) / 2, theirs = blocks - mine;
+            const int octets = (rows + 7) / 8;  // columns in use, by eight
+            uint64_t sums[kRows8 / 2];  // this thread's slots', of rows 2 r and 2 r + 1
 #pragma unroll
-            for (int r = 0; r < kRows8; ++r) {
-                minus[r] = kUnset;
-                sums[r] = 0.f;
-            }
-            rows_of.minus[warp][lane] = kUnset;
-            __syncwarp();
-            if (p.n > 0) {
+            for (int r = 0; r < kRows8 / 2; ++r) sums[r] = 0;
+            int exponent = kNoScale;  // weights are times 2^-exponent
+            if (gw == 0) shared.minus[g][lane] = kUnset;
+            if (blocks > 0) {
                 const uint32_t qb = qn & 1;
                 hold8<kPieceLimitNs>(sh, &sh.q_full[qb], (qn >> 1) & 1, status);
                 ++qn;
                 const float q_factor = sh.q_factor[qb];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_empty[qb]);
+                softmax_barrier<128>(1 + g);
 
-                // scales: a block ahead, page ids two
+                // scales: one of the group's blocks ahead, page ids two
                 const int32_t *table = A.batch.pages + p.b * A.batch.pages_stride;
-                const int slot0 = p.lo * kKeys + gt;
-                const int j0 = A.by_group.div(p.row), j1 = A.by_group.div(p.row + p.rows - 1);
-                const int first_seen = A.window > 0 ? p.past + j0 - A.window + 1 : 0;
+                const int lo = p.lo, end = p.end;
+                const int j0 = A.by_group.div(row0), j1 = A.by_group.div(row0 + rows - 1);
+                const int first_seen = A.window > 0 ? past + j0 - A.window + 1 : 0;
+                const uint8_t *k_scales = P8.scales.k + p.h * P8.scales.k_st[2];
+                const uint8_t *v_scales = P8.scales.v + p.h * P8.scales.v_st[2];
+                auto slot_at = [&](int i) -> int { return (lo + 2 * i + g) * kKeys + gt; };
                 auto page_of = [&](int i) -> int {
-                    const int s = slot0 + i * kKeys;
-                    if (i >= p.n || s >= p.end || s < first_seen) return -1;
+                    const int s = slot_at(i);
+                    if (i >= mine || s >= end || s < first_seen) return -1;
                     const int id = __ldg(table + A.by_page.div(s));
                     return id < A.batch.num_pages ? id : -1;
                 };
-                auto scales_of = [&](int i, int id) -> uint32_t {  // of key and value
-                    if (id < 0) return 127u | 127u << 8;
-                    const int s = slot0 + i * kKeys;
+                // (bytes as they come: nothing waits for them before the next block)
+                uint32_t key_byte, value_byte, next_key, next_value;
+                auto scales_of = [&](int i, int id) {
+                    next_key = next_value = 127 + kMinScale;
+                    if (id < 0) return;  // (no codes either)
+                    const int s = slot_at(i);
                     const int64_t in = s - A.by_page.div(s) * A.batch.page_size;
-                    const Scales &S = P8.scales;
-                    return (uint32_t)__ldg(S.k + id * S.k_st[0] + in * S.k_st[1] + p.h * S.k_st[2]) |
-                           (uint32_t)__ldg(S.v + id * S.v_st[0] + in * S.v_st[1] + p.h * S.v_st[2]) << 8;
+                    next_key = __ldg(k_scales + id * P8.scales.k_st[0] + in * P8.scales.k_st[1]);
+                    next_value = __ldg(v_scales + id * P8.scales.v_st[0] + in * P8.scales.v_st[1]);
                 };
-                uint32_t scale = scales_of(0, page_of(0));
+                scales_of(0, page_of(0));
                 int next_page = page_of(1);
-                for (int i = 0; i < p.n; ++i, ++n) {
-                    const uint32_t b = n & 1;
-                    const uint32_t next_scale = scales_of(i + 1, next_page);
+                for (int i = 0; i < mine; ++i, ++used) {
+                    key_byte = next_key;
+                    value_byte = next_value;
+                    scales_of(i + 1, next_page);
                     next_page = page_of(i + 2);
-                    const float key_scale = q_factor * scale_of(scale & 255u);
-                    hold8(sh, &sh.s_full[b], (n >> 1) & 1, status);
+                    hold8(sh, &sh.s_full[g], used & 1, status);
                     __syncwarp();
                     tc::fence_after();
-                    float s[kRows8];
-                    {
-                        uint32_t x[kParts][32];
+                    uint64_t y[kRows8 / 2];  // of rows 2 r and 2 r + 1
+                    const float key_scale = q_factor * scale_of(key_byte);
+                    const int k0 = (lo + 2 * i + g) * kKeys;
+                    const bool masked =
+                        k0 + kKeys - 1 > past + j0 || (A.window > 0 && k0 <= past + j1 - A.window);
+                    auto scores = [&]() {
+                        const uint64_t key_scale2 = pair2(key_scale, key_scale);
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-                            tc::ld32(x[part], lanes_at + b * L::kScoreCols + part * kRows8);
-                        tc::wait_ld();
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.s_empty[b]);
-                        // the small parts first
+                        for (int o = 0; o < 4; ++o) {
+                            if (o >= octets) break;
+                            uint32_t x[kParts][8];
 #pragma unroll
-                        for (int r = 0; r < kRows8; ++r) {
-                            float y = __uint_as_float(x[kParts - 1][r]);
+                            for (int part = 0; part < kParts; ++part) tc::ld8(x[part], t_s + part * kRows8 + o * 8);
+                            tc::wait_ld();
 #pragma unroll
-                            for (int part = kParts - 2; part >= 0; --part) y += __uint_as_float(x[part][r]);
-                            s[r] = y * key_scale;
+                            for (int c = 0; c < 8; c += 2) {
+                                // the small parts first
+                                uint64_t sum = bits2(x[kParts - 1][c], x[kParts - 1][c + 1]);
+#pragma unroll
+                                for (int part = kParts - 2; part >= 0; --part)
+                                    sum = add2(sum, bits2(x[part][c], x[part][c + 1]));
+                                y[o * 4 + c / 2] = mul2(sum, key_scale2);
+                            }
                         }
-                    }
-                    const int k0 = (p.lo + i) * kKeys, slot = k0 + gt;
-                    if (k0 + kKeys - 1 > p.past + j0 || (A.window > 0 && k0 <= p.past + j1 - A.window)) {
-                        const int span = A.window > 0 ? A.window : 0x7fffffff;
+                        if (masked) {
+                            // row r sees the slot when its token does: row0 + r >= t G, and
+                            // < (t + window) G
+                            const int64_t t = (int64_t)k0 + gt - past;
+                            const int64_t from = t * A.group - row0;
+                            const int64_t to = A.window > 0 ? from + (int64_t)A.window * A.group : kRows8;
+                            const int r0 = (int)max((int64_t)0, min(from, (int64_t)kRows8));
+                            const int r1 = (int)max((int64_t)0, min(to, (int64_t)kRows8));
 #pragma unroll
-                        for (int r = 0; r < kRows8; ++r) {
-                            const int behind = p.past + A.by_group.div(p.row + r) - slot;
-                            if (behind < 0 || behind >= span) s[r] = -INFINITY;
+                            for (int r = 0; r < kRows8 / 2; ++r) {
+                                float a, b;
+                                unpair2(y[r], a, b);
+                                if (2 * r < r0 || 2 * r >= r1) a = -INFINITY;
+                                if (2 * r + 1 < r0 || 2 * r + 1 >= r1) b = -INFINITY;
+                                y[r] = pair2(a, b);
+                            }
                         }
-                    }
-                    float top = -INFINITY;
+                    };
+                    // scores relative to the references, and the largest of them
+                    auto relative = [&]() -> float {
+                        float top = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < kRows8; r += 2) top = max3(top, s[r] + minus[r], s[r + 1] + minus[r + 1]);
-                    if (softmax_any(top > kRescaleAbove)) {
+                        for (int o = 0; o < 4; ++o) {
+                            if (o >= octets) break;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float4 m = *reinterpret_cast<const float4 *>(&shared.minus[g][o * 8 + c * 4]);
+                                const int r = o * 4 + c * 2;
+                                y[r] = add2(y[r], pair2(m.x, m.y));
+                                y[r + 1] = add2(y[r + 1], pair2(m.z, m.w));
+                                float a, b;
+                                unpair2(y[r], a, b);
+                                top = max3(top, a, b);
+                                unpair2(y[r + 1], a, b);
+                                top = max3(top, a, b);
+                            }
+                        }
+                        return top;
+                    };
+                    // (a byte of 255 is no scale: the vector is NaN)
+                    const int e8 = value_byte == kScaleNan ? kNoScale : (int)value_byte - 127;
+                    scores();
+                    const float top = relative();
+                    if (softmax_any<128>(1 + g, top > kRescaleAbove || e8 > exponent)) {
                         // the rows' maxima over the block, and new references where they grew
-                        float v[kRows8];
+                        scores();
+                        {
+                            float v[kRows8];
 #pragma unroll
-                        for (int r = 0; r < kRows8; ++r) v[r] = s[r];
-                        rows_of.across[warp][lane] =
-                            across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
-                        softmax_barrier();
-                        float high = rows_of.across[0][lane];
+                            for (int r = 0; r < kRows8 / 2; ++r) {
+                                v[2 * r] = v[2 * r + 1] = -INFINITY;
+                                if (r / 4 < octets) unpair2(y[r], v[2 * r], v[2 * r + 1]);
+                            }
+                            shared.across[g][gw][lane] =
+                                across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                        }
+                        const int largest = __reduce_max_sync(0xffffffffu, e8);
+                        if (lane == 0) shared.exponent[g][gw] = largest;
+                        softmax_barrier<128>(1 + g);
+                        float high = shared.across[g][0][lane];
+                        int most = shared.exponent[g][0];
 #pragma unroll
-                        for (int w = 1; w < 4; ++w) high = fmaxf(high, rows_of.across[w][lane]);
-                        const float old = rows_of.minus[warp][lane];
+                        for (int w = 1; w < 4; ++w) {
+                            high = fmaxf(high, shared.across[g][w][lane]);
+                            most = max(most, shared.exponent[g][w]);
+                        }
+                        // (one more, so that the next larger scale is no new reference)
+                        const int now_e = most > exponent ? most + 1 : exponent;
+                        const float old = shared.minus[g][lane];
                         const bool grow = high + old > kRescaleAbove;
                         const float now = grow ? -high : old;
                         const float f = !grow ? 1.f : old == kUnset ? 0.f : ex2(now - old);
-                        rows_of.minus[warp][lane] = now;
-                        rows_of.factor[warp][lane] = f;
-                        const bool scaled = __any_sync(0xffffffffu, grow && old != kUnset);
-                        __syncwarp();
+                        const float fe = exponent == kNoScale ? 0.f : ex2((float)(exponent - now_e));
+                        const bool scaled = __any_sync(0xffffffffu, grow && old != kUnset) || now_e != exponent;
+                        exponent = now_e;
+                        softmax_barrier<128>(1 + g);
+                        if (gw == 0) {
+                            shared.minus[g][lane] = now;
+                            shared.factor[g][lane] = f;
+                        }
+                        softmax_barrier<128>(1 + g);
 #pragma unroll
-                        for (int r = 0; r < kRows8; ++r) {
-                            minus[r] = rows_of.minus[warp][r];
-                            sums[r] *= rows_of.factor[warp][r];
+                        for (int o = 0; o < kRows8 / 4; ++o) {
+                            const float4 m = *reinterpret_cast<const float4 *>(&shared.factor[g][o * 4]);
+                            sums[2 * o] = mul2(sums[2 * o], pair2(m.x, m.y));
+                            sums[2 * o + 1] = mul2(sums[2 * o + 1], pair2(m.z, m.w));
                         }
                         if (scaled && i > 0) {
-                            hold8(sh, &sh.pv_done[b ^ 1], ((n - 1) >> 1) & 1, status);
+                            hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
                             __syncwarp();
                             tc::fence_after();
-#pragma unroll
-                            for (int half = 0; half < L::kOutCols / 16; ++half) {
+#pragma unroll 1
+                            for (int half = 0; half < 2; ++half) {
                                 uint32_t o[16];
-                                tc::ld16(o, t_o + half * 16);
+                                tc::ld16(o, t_o + g * kRows8 + half * 16);
                                 tc::wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) *
-                                                           rows_of.factor[warp][(half * 16 + e) % kRows8]);
-                                tc::st16(t_o + half * 16, o);
+                                                           (shared.factor[g][half * 16 + e] * fe));
+                                tc::st16(t_o + g * kRows8 + half * 16, o);
                             }
                             tc::wait_st();
-                            tc::fence_before();
                         }
+                        relative();
                     }
-                    const uint32_t value_byte = scale >> 8;
-                    const float value_scale = value_byte == kScaleNan ? 0.f : scale_of(value_byte);
-                    if (n >= 2) hold8(sh, &sh.pv_done[b], ((n >> 1) - 1) & 1, status);
+                    tc::fence_before();
                     __syncwarp();
-                    char *row = smem + L::kP + b * kRaw + gt * 128;
+                    if (lane == 0) mbar_arrive(&sh.s_empty[g]);
+                    // a weight times its scale, in fp16's range (2^15 at most)
+                    const int shift = e8 - exponent + (int)kHalfLift;
+                    const float value_scale = shift < -126 ? 0.f : power_of_two(shift);
+                    const uint64_t value_scale2 = pair2(value_scale, value_scale);
+                    const bool any_nan = __any_sync(0xffffffffu, value_byte == kScaleNan);
+                    if (used > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
+                    __syncwarp();
+                    char *row = smem + L::kP + g * kRaw + gt * 128;
 #pragma unroll
-                    for (int r0 = 0; r0 < kRows8; r0 += 8) {
-                        float w[8];
+                    for (int o = 0; o < 4; ++o) {
+                        if (o >= octets) break;
+                        uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x = ex2(s[r0 + e] + minus[r0 + e]);
-                            sums[r0 + e] += x;
-                            w[e] = x * value_scale;
-                            // a value vector that is NaN: for the rows that see it
-                            if (value_byte == kScaleNan && s[r0 + e] != -INFINITY) w[e] = __uint_as_float(0x7fffffffu);
-                        }
-                        uint4 y;
-                        y.x = pack2<__nv_bfloat16>(w[0], w[1]);
-                        y.y = pack2<__nv_bfloat16>(w[2], w[3]);
-                        y.z = pack2<__nv_bfloat16>(w[4], w[5]);
-                        y.w = pack2<__nv_bfloat16>(w[6], w[7]);
-                        *reinterpret_cast<uint4 *>(row + (((r0 / 8) ^ (gt & 7)) * 16)) = y;
-                        if (kTwo) {  // what the rounding left
-                            const uint32_t u[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f = pair_of(u[e], __nv_bfloat16());
-                                w[2 * e] -= f.x;
-                                w[2 * e + 1] -= f.y;
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = o * 4 + e;
+                            float a, b;
+                            unpair2(y[r], a, b);
+                            const uint64_t x = pair2(ex2(a), ex2(b));
+                            sums[r] = add2(sums[r], x);
+                            unpair2(mul2(x, value_scale2), a, b);
+                            if (any_nan && value_byte == kScaleNan) {  // for the rows that see it
+                                float u, v;
+                                unpair2(y[r], u, v);
+                                a = u == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu);
+                                b = v == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu);
                             }
-                            y.x = pack2<__nv_bfloat16>(w[0], w[1]);
-                            y.y = pack2<__nv_bfloat16>(w[2], w[3]);
-                            y.z = pack2<__nv_bfloat16>(w[4], w[5]);
-                            y.w = pack2<__nv_bfloat16>(w[6], w[7]);
-                            *reinterpret_cast<uint4 *>(row + (((4 + r0 / 8) ^ (gt & 7)) * 16)) = y;
+                            w[e] = pack2<__half>(a, b);
                         }
+                        *reinterpret_cast<uint4 *>(row + ((o ^ (gt & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     tc::fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_full[b]);
-                    scale = next_scale;
+                    if (lane == 0) mbar_arrive(&sh.p_full[g]);
                 }
-                hold8(sh, &sh.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, status);
+                others += theirs;
+                if (mine > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
+                if (theirs > 0) hold8(sh, &sh.pv_done[1 - g], (others - 1) & 1, status);
                 __syncwarp();
                 tc::fence_after();
             }
 
-            // ---- the rows' sums; thread d then has value d of all rows ----------------
-            rows_of.across[warp][lane] = across_lanes(sums, lane, [](float a, float b) { return a + b; });
-            softmax_barrier();
-            const float sum = (rows_of.across[0][lane] + rows_of.across[1][lane]) +
-                              (rows_of.across[2][lane] + rows_of.across[3][lane]);
-            const float low = rows_of.minus[warp][lane];
-            const float ref = low == kUnset ? -INFINITY : -low;
-            float o[kRows8];
+            // ---- the groups' states, joined: lane r has row r's --------------------------
+            {
+                float v[kRows8];
 #pragma unroll
-            for (int r = 0; r < kRows8; ++r) o[r] = 0.f;
-            if (p.n > 0) {
-                uint32_t x[L::kWeights][32];
-#pragma unroll
-                for (int part = 0; part < L::kWeights; ++part) tc::ld32(x[part], t_o + part * kRows8);
-                tc::wait_ld();
-                tc::fence_before();
-#pragma unroll
-                for (int r = 0; r < kRows8; ++r)
-                    o[r] = kTwo ? __uint_as_float(x[0][r]) + __uint_as_float(x[L::kWeights - 1][r])
-                                : __uint_as_float(x[0][r]);
+                for (int r = 0; r < kRows8 / 2; ++r) unpair2(sums[r], v[2 * r], v[2 * r + 1]);
+                shared.across[g][gw][lane] = across_lanes(v, lane, [](float a, float b) { return a + b; });
+                if (lane == 0) shared.exponent[g][gw] = exponent;
             }
-            auto store = [&](int r, float y) {
-                const int pr = p.row + r, j = A.by_group.div(pr);
-                static_cast<T *>(A.out)[(int64_t)(p.token + j) * A.o_st[0] +
-                                        (p.h * A.group + (pr - j * A.group)) * A.o_st[1] + gt] = from_f32<T>(y);
+            softmax_barrier<256>(3);
+            float ref = -INFINITY, sum = 0.f, f[2];
+            {
+                float own_ref[2], own_sum[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float m = shared.minus[x][lane];
+                    own_ref[x] = m == kUnset ? -INFINITY : -m;
+                    own_sum[x] = (shared.across[x][0][lane] + shared.across[x][1][lane]) +
+                                 (shared.across[x][2][lane] + shared.across[x][3][lane]);
+                    ref = fmaxf(ref, own_ref[x]);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    f[x] = own_ref[x] == -INFINITY ? 0.f : ex2(own_ref[x] - ref);
+                    sum += own_sum[x] * f[x];
+                    const int e = shared.exponent[x][0];
+                    f[x] *= e == kNoScale ? 0.f : ex2((float)(e - (int)kHalfLift));
+                }
+            }
+            // thread d of group g has value d of rows 16 g .. 16 g + 15
+            const int r0 = g * 16, here = min(16, rows - r0);
+            float o[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[r] = 0.f;
+            if (here > 0) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (blocks <= x) break;
+                    uint32_t u[16];
+                    tc::ld16(u, t_o + x * kRows8 + r0);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        o[r] = fmaf(__shfl_sync(0xffffffffu, f[x], r0 + r), __uint_as_float(u[r]), o[r]);
+                }
+                tc::fence_before();
+            }
+            // rows of out, one after another
+            const int j_first = A.by_group.div(row0 + r0);
+            int head = row0 + r0 - j_first * A.group;
+            T *out = static_cast<T *>(A.out) + (int64_t)(p.token + j_first) * A.o_st[0] +
+                     ((int64_t)p.h * A.group + head) * A.o_st[1] + gt;
+            const int64_t wrap = A.o_st[0] - A.group * A.o_st[1];
+            auto store = [&](float y) {
+                *out = from_f32<T>(y);
+                out += A.o_st[1];
+                if (++head == A.group) {
+                    head = 0;
+                    out += wrap;
+                }
             };
             if (p.parts == 1) {
                 // (a row that saw nothing has the sum 0, and zeros)
-                rows_of.factor[warp][lane] = sum == 0.f ? 0.f : 1.f / sum;
-                __syncwarp();
-                if (gt < D) {
+                const float norm = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-                    for (int r = 0; r < kRows8; ++r) {
-                        const float f = rows_of.factor[warp][r];
-                        if (r < p.rows) store(r, f == 0.f ? 0.f : o[r] * f);
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const float n = __shfl_sync(0xffffffffu, norm, r0 + r);
+                    if (r < here && gt < D) store(n == 0.f ? 0.f : o[r] * n);
                 }
             } else {
                 const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
@@ -757,12 +860,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 float *part_out = reinterpret_cast<float *>(A.workspace + kAttendOut);
                 constexpr int64_t kSlot = (int64_t)(kMaxHeadDim / 4) * 2 * kRows * 4;  // floats of a slot
 #pragma unroll
-                for (int r = 0; r < kRows8; ++r)
-                    if (r < p.rows) part_out[slot * kSlot + r * 128 + gt] = o[r];
+                for (int r = 0; r < 16; ++r)
+                    if (r < here) part_out[slot * kSlot + (r0 + r) * 128 + gt] = o[r];
                 if (warp == 0) part_stats[(int64_t)slot * 2 * kRows + lane] = make_float2(ref, sum);
-                softmax_barrier();
-                if (gt == 0) {
-                    __threadfence();  // all 128 threads' writes, after the barrier
+                softmax_barrier<256>(3);
+                if (tid == 0) {
+                    __threadfence();  // all 256 threads' writes, after the barrier
                     uint32_t *count = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters) + 2 * p.first;
                     const uint32_t before = atomicAdd(count, 1u);
                     const bool last = before == (uint32_t)p.parts - 1;
@@ -771,8 +874,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     if (before >= (uint32_t)p.parts) atomicOr(status, SV_STATUS_OVERFLOW);
                     sh.last = last;
                 }
-                softmax_barrier();
-                if (sh.last) {
+                softmax_barrier<256>(3);
+                if (sh.last && here > 0) {
                     __threadfence();
                     auto slot_of = [&](int i) -> int { return (p.first + i) * 2 + (i == 0 ? 1 : 0); };
                     // lane r: row r's reference and sum over the parts (as many loads in
@@ -794,54 +897,45 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             if (i0 + i < p.parts && x[i].y != 0.f) all += x[i].y * ex2(x[i].x - m);
                         top = m;
                     }
-                    rows_of.factor[warp][lane] = all == 0.f ? 0.f : 1.f / all;
-                    rows_of.minus[warp][lane] = top;
-                    __syncwarp();
+                    const float norm = all == 0.f ? 0.f : 1.f / all;
+                    float acc[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
 #pragma unroll 1
-                    for (int r0 = 0; r0 < p.rows; r0 += 4) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                        for (int i0 = 0; i0 < p.parts; i0 += 4) {
-                            float y[4][4], m[4][4];
+                    for (int i0 = 0; i0 < p.parts; i0 += 2) {
+                        float x[2][16], m[2];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int64_t at = slot_of(min(i0 + i, p.parts - 1));
+                        for (int i = 0; i < 2; ++i) {
+                            const int64_t at = slot_of(min(i0 + i, p.parts - 1));
+                            m[i] = __ldcg(&part_stats[at * 2 * kRows + lane]).x;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int r = min(r0 + e, p.rows - 1);
-                                    m[i][e] = __ldcg(&part_stats[at * 2 * kRows + r]).x;
-                                    y[i][e] = __ldcg(&part_out[at * kSlot + r * 128 + gt]);
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float t = rows_of.minus[warp][min(r0 + e, p.rows - 1)];
-                                    // (a NaN query leaves no reference, and NaN in O)
-                                    const float f = i0 + i >= p.parts ? 0.f
-                                                    : m[i][e] == -INFINITY ? 0.f
-                                                                           : ex2(m[i][e] - t);
-                                    acc[e] = fmaf(f, y[i][e], acc[e]);
-                                }
+                            for (int r = 0; r < 16; ++r)
+                                if (r < here) x[i][r] = __ldcg(&part_out[at * kSlot + (r0 + r) * 128 + gt]);
                         }
-                        if (gt < D)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (r0 + e < p.rows) {
-                                    const float f = rows_of.factor[warp][r0 + e];
-                                    store(r0 + e, f == 0.f ? 0.f : acc[e] * f);
-                                }
+                        for (int i = 0; i < 2; ++i) {
+                            // (a NaN query leaves no reference, and NaN in O)
+                            const float w = i0 + i >= p.parts || m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) {
+                                const float fr = __shfl_sync(0xffffffffu, w, r0 + r);
+                                if (r < here) acc[r] = fmaf(fr, x[i][r], acc[r]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float n = __shfl_sync(0xffffffffu, norm, r0 + r);
+                        if (r < here && gt < D) store(n == 0.f ? 0.f : acc[r] * n);
                     }
                 }
             }
-            __syncwarp();
             reader.done(sh, lane);
         }
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 13) {
         __syncwarp();
         tc::tmem_free(tmem, L::kCols);
     }
