@@ -152,14 +152,14 @@ int code_map(CUtensorMap *map, const sv_paged_cache *c, void *base, const int64_
     return r == CUDA_SUCCESS ? SV_OK : SV_EINVAL;
 }
 
-template <class T>
+template <class T, int kRows>
 int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CUtensorMap &vmap, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ECUDA;
-    constexpr int bytes = sv::Attend8Smem<T>::kBytes;
+    constexpr int bytes = sv::Attend8Smem<T, kRows>::kBytes;
     static std::atomic<int> raised[64];
     if (!raised[dev].load()) {
-        if (cudaFuncSetAttribute(sv::attend8_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        if (cudaFuncSetAttribute(sv::attend8_kernel<T, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
             cudaSuccess)
             return SV_ECUDA;
         raised[dev].store(1);
@@ -167,7 +167,24 @@ int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CU
     const int sms = sm_count();
     if (sms <= 0) return SV_ECUDA;
     const unsigned grid = (unsigned)std::min(sms, sv::kAttendMaxCtas);
-    return launch(sv::attend8_kernel<T>, grid, sv::kThreads8, bytes, st, A, kmap, vmap);
+    return launch(sv::attend8_kernel<T, kRows>, grid, sv::kThreads8, bytes, st, A, kmap, vmap);
+}
+
+// Packed rows of a sequence and kv head, on average and rounded up.
+int64_t average_rows(const sv_paged_cache *c, int32_t q_heads) {
+    return ((int64_t)c->tokens * (q_heads / c->kv_heads) + c->B - 1) / c->B;
+}
+
+template <class T>
+int launch_attend8(const sv::Attend8Params &A, int64_t rows, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                   cudaStream_t st) {
+    // as few tiles as hold them, and as few columns to a tile
+    const int64_t tiles = (rows + sv::kMaxRows8 - 1) / sv::kMaxRows8;
+    rows = (rows + tiles - 1) / tiles;
+    if (rows <= 8) return launch_attend8<T, 8>(A, kmap, vmap, st);
+    if (rows <= 16) return launch_attend8<T, 16>(A, kmap, vmap, st);
+    if (rows <= 24) return launch_attend8<T, 24>(A, kmap, vmap, st);
+    return launch_attend8<T, 32>(A, kmap, vmap, st);
 }
 
 }  // namespace
@@ -270,9 +287,7 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
 
 size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads) {
     if (check_cache(cache, true) != SV_OK || q_heads < 1 || cache->B == 0 || cache->tokens == 0) return 0;
-    // (rows of a sequence and kv head, on average)
-    const int64_t rows = (int64_t)cache->tokens * (q_heads / cache->kv_heads) / cache->B;
-    if (rows <= 64) return 0;
+    if (q_heads % cache->kv_heads != 0 || average_rows(cache, q_heads) <= 64) return 0;
     return Scratch(cache).bytes;
 }
 
@@ -322,8 +337,9 @@ int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales
         CUtensorMap kmap, vmap;
         if ((rc = code_map(&kmap, cache, cache->k, cache->k_stride, A.piece)) != SV_OK) return rc;
         if ((rc = code_map(&vmap, cache, cache->v, cache->v_stride, A.piece)) != SV_OK) return rc;
-        return dtype == SV_BF16 ? launch_attend8<__nv_bfloat16>(P, kmap, vmap, st)
-                                : launch_attend8<__half>(P, kmap, vmap, st);
+        const int64_t rows = average_rows(cache, q_heads);
+        return dtype == SV_BF16 ? launch_attend8<__nv_bfloat16>(P, rows, kmap, vmap, st)
+                                : launch_attend8<__half>(P, rows, kmap, vmap, st);
     }
     // many rows: the sequences back to 16 bits, and the attention over those
     const Scratch room(cache);

@@ -41,7 +41,7 @@
 
 namespace sv {
 
-constexpr int kRows8 = 32;      // packed rows of a tile
+constexpr int kMaxRows8 = 32;   // packed rows of a tile at most
 constexpr int kTileCost8 = 3;   // a tile's fixed cost in key blocks
 constexpr int kThreads8 = 512;
 constexpr int kSoftmaxRegs8 = 168, kOtherRegs8 = 88;
@@ -56,18 +56,20 @@ struct Attend8Params {
     Scales scales;
 };
 
-template <class T>
+template <class T, int kRows8>
 struct Attend8Smem {
     static constexpr int kParts = __is_same(T, __nv_bfloat16) ? 3 : 4;
-    static constexpr int kQuery = kParts * kRows8 * 128;
+    // columns of scores: a whole product has a multiple of 16
+    static constexpr int kScoreCols = (kParts * kRows8 + 15) / 16 * 16;
+    static constexpr int kQuery = kScoreCols * 128;
     static constexpr int kMisc = 3072;
     static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRing8 * kRaw, kVc = kV + kRing8 * kRaw,
                          kP = kVc + 2 * 2 * kRaw, kBytes = kP + 2 * kRaw;
-    static constexpr int kScoreCols = kParts * kRows8;
-    static constexpr int kOut = 2 * kScoreCols;  // first column of the groups' O
-    static constexpr uint32_t kCols = kOut + 2 * kRows8 <= 256 ? 256 : 512;
+    // O: the groups' first columns, and a whole product's columns
+    static constexpr int kOutCols = (kRows8 + 15) / 16 * 16, kOut = 2 * kScoreCols;
+    static constexpr uint32_t kCols = kOut + 2 * kOutCols <= 128 ? 128 : kOut + 2 * kOutCols <= 256 ? 256 : 512;
     static_assert(kBytes <= 227 * 1024 && kQ % 1024 == 0 && kQuery % 1024 == 0, "shared memory");
-    static_assert(kOut + 2 * kRows8 <= 512, "tensor memory");
+    static_assert(kOut + 2 * kOutCols <= 512, "tensor memory");
 };
 
 struct Attend8Shared {
@@ -84,10 +86,10 @@ struct Attend8Shared {
 static_assert(sizeof(Attend8Shared) <= 1024, "misc region");
 
 struct __align__(16) Attend8Rows {  // behind it, for each of the two groups
-    float minus[2][kRows8];     // minus the rows' references
-    float factor[2][kRows8];    // what a new reference makes of sums and outputs
-    float across[2][4][kRows8]; // its warps' maxima or sums
-    int32_t exponent[2][4];     // its warps' largest scales
+    float minus[2][kMaxRows8];     // minus the rows' references
+    float factor[2][kMaxRows8];    // what a new reference makes of sums and outputs
+    float across[2][4][kMaxRows8]; // its warps' maxima or sums
+    int32_t exponent[2][4];        // its warps' largest scales
 };
 static_assert(sizeof(Attend8Rows) <= 2048, "misc region");
 
@@ -190,16 +192,16 @@ __device__ __forceinline__ uint32_t split_off(float (&x)[4]) {
     return w;
 }
 
-template <class T>
+template <class T, int kRows8>
 __global__ void __launch_bounds__(kThreads8, 1)
     attend8_kernel(const __grid_constant__ Attend8Params P8, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
-    typedef Attend8Smem<T> L;
-    typedef SeqCost<kRows8, kTileCost8> Cost;
+    typedef Attend8Smem<T, kRows8> L;
     constexpr int kParts = L::kParts;
+    constexpr int kAtOnce = kRows8 < 32 ? kRows8 / 8 : 2;  // columns of scores by eight, as registers allow
     constexpr uint32_t kIdescS = tc::instr_desc_f8(kKeys, L::kScoreCols);
     // (bit 15: A's slots are its rows in memory, as B's)
-    constexpr uint32_t kIdescO = tc::instr_desc(false, true, 128, kRows8) | (1u << 15);
+    constexpr uint32_t kIdescO = tc::instr_desc(false, true, 128, L::kOutCols) | (1u << 15);
     extern __shared__ __align__(1024) char smem[];
     Attend8Shared &sh = *reinterpret_cast<Attend8Shared *>(smem);
     Attend8Rows &shared = *reinterpret_cast<Attend8Rows *>(smem + 1024);
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * (kRaw / 16);
 #pragma unroll
                         for (int s = 0; s < kKeys / 16; ++s)
-                            tc::mma_ss(tm + b * kRows8, vd + s * (2048 / 16), pd + s * (2048 / 16), kIdescO, i > 1 || s > 0);
+                            tc::mma_ss(tm + b * L::kOutCols, vd + s * (2048 / 16), pd + s * (2048 / 16), kIdescO, i > 1 || s > 0);
                         tc::commit(&sh.pv_done[b]);
                     }
                     __syncwarp();
@@ -563,7 +565,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const Piece &p = sh.pieces[reader.k];
             const int blocks = p.n, past = p.past, row0 = p.row, rows = p.rows;
             const int mine = (blocks + 1 - g) / 2, theirs = blocks - mine;
-            const int octets = (rows + 7) / 8;  // columns in use, by eight
             uint64_t sums[kRows8 / 2];  // this thread's slots', of rows 2 r and 2 r + 1
 #pragma unroll
             for (int r = 0; r < kRows8 / 2; ++r) sums[r] = 0;
@@ -588,15 +589,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 auto slot_at = [&](int i) -> int { return (lo + 2 * i + g) * kKeys + gt; };
                 auto page_of = [&](int i) -> int {
                     const int s = slot_at(i);
-                    if (i >= mine || s >= end || s < first_seen) return -1;
-                    const int id = __ldg(table + A.by_page.div(s));
-                    return id < A.batch.num_pages ? id : -1;
+                    return i >= mine || s >= end || s < first_seen ? -1 : __ldg(table + A.by_page.div(s));
                 };
                 // (bytes as they come: nothing waits for them before the next block)
                 uint32_t key_byte, value_byte, next_key, next_value;
                 auto scales_of = [&](int i, int id) {
                     next_key = next_value = 127 + kMinScale;
-                    if (id < 0) return;  // (no codes either)
+                    if (id < 0 || id >= A.batch.num_pages) return;  // (no codes either)
                     const int s = slot_at(i);
                     const int64_t in = s - A.by_page.div(s) * A.batch.page_size;
                     next_key = __ldg(k_scales + id * P8.scales.k_st[0] + in * P8.scales.k_st[1]);
@@ -620,23 +619,27 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     auto scores = [&]() {
                         const uint64_t key_scale2 = pair2(key_scale, key_scale);
 #pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            if (o >= octets) break;
-                            uint32_t x[kParts][8];
+                        for (int o0 = 0; o0 < kRows8 / 8; o0 += kAtOnce) {
+                            uint32_t x[kParts][kAtOnce][8];
 #pragma unroll
-                            for (int part = 0; part < kParts; ++part) tc::ld8(x[part], t_s + part * kRows8 + o * 8);
+                            for (int o = 0; o < kAtOnce; ++o)
+#pragma unroll
+                                for (int part = 0; part < kParts; ++part)
+                                    tc::ld8(x[part][o], t_s + part * kRows8 + (o0 + o) * 8);
                             tc::wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 8; c += 2) {
-                                // the small parts first
-                                uint64_t sum = bits2(x[kParts - 1][c], x[kParts - 1][c + 1]);
+                            for (int o = 0; o < kAtOnce; ++o)
 #pragma unroll
-                                for (int part = kParts - 2; part >= 0; --part)
-                                    sum = add2(sum, bits2(x[part][c], x[part][c + 1]));
-                                y[o * 4 + c / 2] = mul2(sum, key_scale2);
-                            }
+                                for (int c = 0; c < 8; c += 2) {
+                                    // the small parts first
+                                    uint64_t sum = bits2(x[kParts - 1][o][c], x[kParts - 1][o][c + 1]);
+#pragma unroll
+                                    for (int part = kParts - 2; part >= 0; --part)
+                                        sum = add2(sum, bits2(x[part][o][c], x[part][o][c + 1]));
+                                    y[(o0 + o) * 4 + c / 2] = mul2(sum, key_scale2);
+                                }
                         }
-                        if (masked) {
+                        if (__builtin_expect(masked, 0)) {
                             // row r sees the slot when its token does: row0 + r >= t G, and
                             // < (t + window) G
                             const int64_t t = (int64_t)k0 + gt - past;
@@ -658,8 +661,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     auto relative = [&]() -> float {
                         float top = -INFINITY;
 #pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            if (o >= octets) break;
+                        for (int o = 0; o < kRows8 / 8; ++o) {
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 const float4 m = *reinterpret_cast<const float4 *>(&shared.minus[g][o * 8 + c * 4]);
@@ -679,16 +681,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const int e8 = value_byte == kScaleNan ? kNoScale : (int)value_byte - 127;
                     scores();
                     const float top = relative();
-                    if (softmax_any<128>(1 + g, top > kRescaleAbove || e8 > exponent)) {
+                    if (__builtin_expect(softmax_any<128>(1 + g, top > kRescaleAbove || e8 > exponent), 0)) {
                         // the rows' maxima over the block, and new references where they grew
                         scores();
                         {
-                            float v[kRows8];
+                            float v[kMaxRows8];
 #pragma unroll
-                            for (int r = 0; r < kRows8 / 2; ++r) {
-                                v[2 * r] = v[2 * r + 1] = -INFINITY;
-                                if (r / 4 < octets) unpair2(y[r], v[2 * r], v[2 * r + 1]);
-                            }
+                            for (int r = 0; r < kMaxRows8; ++r) v[r] = -INFINITY;
+#pragma unroll
+                            for (int r = 0; r < kRows8 / 2; ++r) unpair2(y[r], v[2 * r], v[2 * r + 1]);
                             shared.across[g][gw][lane] =
                                 across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
                         }
@@ -728,15 +729,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             __syncwarp();
                             tc::fence_after();
 #pragma unroll 1
-                            for (int half = 0; half < 2; ++half) {
+                            for (int half = 0; half < L::kOutCols / 16; ++half) {
                                 uint32_t o[16];
-                                tc::ld16(o, t_o + g * kRows8 + half * 16);
+                                tc::ld16(o, t_o + g * L::kOutCols + half * 16);
                                 tc::wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) *
                                                            (shared.factor[g][half * 16 + e] * fe));
-                                tc::st16(t_o + g * kRows8 + half * 16, o);
+                                tc::st16(t_o + g * L::kOutCols + half * 16, o);
                             }
                             tc::wait_st();
                         }
@@ -754,8 +755,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     char *row = smem + L::kP + g * kRaw + gt * 128;
 #pragma unroll
-                    for (int o = 0; o < 4; ++o) {
-                        if (o >= octets) break;
+                    for (int o = 0; o < kRows8 / 8; ++o) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             const uint64_t x = pair2(ex2(a), ex2(b));
                             sums[r] = add2(sums[r], x);
                             unpair2(mul2(x, value_scale2), a, b);
-                            if (any_nan && value_byte == kScaleNan) {  // for the rows that see it
+                            if (__builtin_expect(any_nan, 0) && value_byte == kScaleNan) {  // for the rows that see it
                                 float u, v;
                                 unpair2(y[r], u, v);
                                 a = u == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu);
@@ -788,7 +788,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
             // ---- the groups' states, joined: lane r has row r's --------------------------
             {
-                float v[kRows8];
+                float v[kMaxRows8];
+#pragma unroll
+                for (int r = 0; r < kMaxRows8; ++r) v[r] = 0.f;
 #pragma unroll
                 for (int r = 0; r < kRows8 / 2; ++r) unpair2(sums[r], v[2 * r], v[2 * r + 1]);
                 shared.across[g][gw][lane] = across_lanes(v, lane, [](float a, float b) { return a + b; });
@@ -824,7 +826,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 for (int x = 0; x < 2; ++x) {
                     if (blocks <= x) break;
                     uint32_t u[16];
-                    tc::ld16(u, t_o + x * kRows8 + r0);
+                    tc::ld16(u, t_o + x * L::kOutCols + r0);
                     tc::wait_ld();
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
