@@ -32,8 +32,9 @@
 // Work split, partial states and their join: as in sv_attend.cuh.
 //
 // Warps 0-7 softmax, 8-11 values to fp16, 12 copies (TMA boxes of page pieces), 13
-// issues S, 14 issues O, 15 walks the CTA's run, publishes its pieces and prepares
-// the queries.  Every wait is bounded, as there.
+// issues S, 14 issues O, 15 fetches scales, 16-19 walk the CTA's run, publish its
+// pieces, prepare their queries and, while the next tile is under way, join a tile's
+// groups and parts and write its rows.  Every wait is bounded, as there.
 #pragma once
 
 #include "sv_append8.cuh"
@@ -43,11 +44,14 @@ namespace sv {
 
 constexpr int kMaxRows8 = 32;   // packed rows of a tile at most
 constexpr int kTileCost8 = 3;   // a tile's fixed cost in key blocks
-constexpr int kThreads8 = 512;
-constexpr int kSoftmaxRegs8 = 168, kOtherRegs8 = 88;
-static_assert(256 * kSoftmaxRegs8 + 256 * kOtherRegs8 <= kThreads8 * 128, "register split");
+constexpr int kThreads8 = 640;
+// Registers per thread after the roles part, of the 640 x 96 that the block is
+// launched with.
+constexpr int kSoftmaxRegs8 = 136, kValueRegs8 = 56, kIssueRegs8 = 56, kTileRegs8 = 96;
+static_assert(128 * (2 * kSoftmaxRegs8 + kValueRegs8 + kIssueRegs8 + kTileRegs8) <= kThreads8 * 96, "register split");
 constexpr int kRaw = kKeys * 128;     // a block of codes
-constexpr int kRing8 = 3;             // blocks of keys, and of values, in flight
+constexpr int kRing8 = 3;             // blocks of keys in flight
+constexpr int kScaleRing = 4;         // blocks of scales
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
 constexpr int kNoScale = -200;        // below every e8m0 exponent
 
@@ -62,36 +66,54 @@ struct Attend8Smem {
     // columns of scores: a whole product has a multiple of 16
     static constexpr int kScoreCols = (kParts * kRows8 + 15) / 16 * 16;
     static constexpr int kQuery = kScoreCols * 128;
-    static constexpr int kMisc = 3072;
-    static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRing8 * kRaw, kVc = kV + kRing8 * kRaw,
+    static constexpr int kMisc = 7168;
+    static constexpr int kFixed = kMisc + 2 * kQuery + kRing8 * kRaw + 2 * 2 * kRaw + 2 * kRaw;
+    static constexpr int kRingV = kFixed + 3 * kRaw <= 227 * 1024 ? 3 : 2;  // blocks of values in flight
+    static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRing8 * kRaw, kVc = kV + kRingV * kRaw,
                          kP = kVc + 2 * 2 * kRaw, kBytes = kP + 2 * kRaw;
-    // O: the groups' first columns, and a whole product's columns
+    // O of two tiles' two groups: first column, and a whole product's columns
     static constexpr int kOutCols = (kRows8 + 15) / 16 * 16, kOut = 2 * kScoreCols;
-    static constexpr uint32_t kCols = kOut + 2 * kOutCols <= 128 ? 128 : kOut + 2 * kOutCols <= 256 ? 256 : 512;
+    static constexpr uint32_t kCols = kOut + 4 * kOutCols <= 128 ? 128 : kOut + 4 * kOutCols <= 256 ? 256 : 512;
     static_assert(kBytes <= 227 * 1024 && kQ % 1024 == 0 && kQuery % 1024 == 0, "shared memory");
-    static_assert(kOut + 2 * kOutCols <= 512, "tensor memory");
+    static_assert(kOut + 4 * kOutCols <= 512, "tensor memory");
 };
+
+constexpr int kPieceReaders8 = 20;
 
 struct Attend8Shared {
     unsigned long long k_full[kRing8], k_empty[kRing8], v_full[kRing8], v_empty[kRing8];
+    unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
     unsigned long long s_full[2], s_empty[2], vc_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain[2];
+    unsigned long long state_full[2], state_empty[2], o_full[2], o_empty[2];
     unsigned long long piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];
     uint32_t tmem;
     int32_t dead, b0, last;
     float q_factor[2];          // power of two of a tile's queries, times the score scale
+    uint32_t q_top[4];          // largest magnitudes of its warps' rows, as bits
     int64_t skip;
     int64_t sums[kThreads8 / 32];
 };
-static_assert(sizeof(Attend8Shared) <= 1024, "misc region");
 
-struct __align__(16) Attend8Rows {  // behind it, for each of the two groups
-    float minus[2][kMaxRows8];     // minus the rows' references
-    float factor[2][kMaxRows8];    // what a new reference makes of sums and outputs
-    float across[2][4][kMaxRows8]; // its warps' maxima or sums
-    int32_t exponent[2][4];        // its warps' largest scales
+struct __align__(16) GroupState {   // of a softmax group
+    float minus[kMaxRows8];         // minus the rows' references
+    float factor[kMaxRows8];        // what a new reference makes of sums and outputs
+    float across[4][kMaxRows8];     // its warps' maxima
+    int32_t exponent[4];            // its warps' largest scales
 };
-static_assert(sizeof(Attend8Rows) <= 2048, "misc region");
+
+struct __align__(16) TileState {    // what the softmax leaves of a tile
+    float minus[2][kMaxRows8], sums[2][4][kMaxRows8];
+    int32_t exponent[2];
+};
+
+struct __align__(16) Attend8Misc {
+    Attend8Shared sh;
+    GroupState group[2];
+    TileState tile[2];
+    uint8_t scales[kScaleRing][2][kKeys];  // of keys and values
+};
+static_assert(sizeof(Attend8Misc) <= 7168, "misc region");
 
 // As hold() of the 16-bit kernel.
 template <uint64_t kLimitNs = kWaitLimitNs>
@@ -127,22 +149,19 @@ struct PieceReader8 {
         }
     }
 };
-constexpr int kPieceReaders8 = 15;
 
-// Barriers of the softmax's threads: a group's 128 (number 1 or 2), or all 256 (3).
-// All of them come to each, whatever timed out.
-template <int kCount>
-__device__ __forceinline__ void softmax_barrier(int number) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(number), "n"(kCount) : "memory");
+// Barriers of the 128 threads of a softmax group (number 1 or 2) or of the tile warps
+// (3).  All of them come to each, whatever timed out.
+__device__ __forceinline__ void group_barrier(int number) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(number) : "memory");
 }
-template <int kCount>
-__device__ __forceinline__ bool softmax_any(int number, bool x) {
+__device__ __forceinline__ bool group_any(int number, bool x) {
     uint32_t r;
     asm volatile(
         "{ .reg .pred p, q; setp.ne.u32 q, %2, 0;\n"
-        "barrier.cta.red.or.pred p, %1, %3, q; selp.u32 %0, 1, 0, p; }"
+        "barrier.cta.red.or.pred p, %1, 128, q; selp.u32 %0, 1, 0, p; }"
         : "=r"(r)
-        : "r"(number), "r"((uint32_t)x), "n"(kCount)
+        : "r"(number), "r"((uint32_t)x)
         : "memory");
     return r != 0;
 }
@@ -198,13 +217,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
                    const __grid_constant__ CUtensorMap vmap) {
     typedef Attend8Smem<T, kRows8> L;
     constexpr int kParts = L::kParts;
-    constexpr int kAtOnce = kRows8 < 32 ? kRows8 / 8 : 2;  // columns of scores by eight, as registers allow
+    constexpr int kAtOnce = kRows8 < 32 ? kRows8 / 8 : 1;  // columns of scores by eight, as registers allow
     constexpr uint32_t kIdescS = tc::instr_desc_f8(kKeys, L::kScoreCols);
     // (bit 15: A's slots are its rows in memory, as B's)
     constexpr uint32_t kIdescO = tc::instr_desc(false, true, 128, L::kOutCols) | (1u << 15);
     extern __shared__ __align__(1024) char smem[];
-    Attend8Shared &sh = *reinterpret_cast<Attend8Shared *>(smem);
-    Attend8Rows &shared = *reinterpret_cast<Attend8Rows *>(smem + 1024);
+    Attend8Misc &misc = *reinterpret_cast<Attend8Misc *>(smem);
+    Attend8Shared &sh = misc.sh;
     const AttendParams &A = P8.a;
     const int tid = threadIdx.x, warp = tc::uniform(tid / 32), lane = tid % 32;
     uint32_t *status = A.batch.status;
@@ -223,14 +242,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
             mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.v_empty[i], 4);
         }
+        for (int i = 0; i < kScaleRing; ++i) {
+            mbar_init(&sh.scale_full[i], 1);
+            mbar_init(&sh.scale_empty[i], 4);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.s_empty[i], 4);
             mbar_init(&sh.vc_full[i], 4);
             mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.pv_done[i], 1);
-            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_full[i], 4);
             mbar_init(&sh.q_empty[i], 9);
+            mbar_init(&sh.state_full[i], 8);
+            mbar_init(&sh.state_empty[i], 4);
+            mbar_init(&sh.o_full[i], 1);
+            mbar_init(&sh.o_empty[i], 4);
             mbar_init(&sh.drain[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
@@ -273,8 +300,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         int64_t base = 0;
         for (int32_t b0 = 0; b0 < A.batch.B; b0 += kThreads8) {
             const int32_t b = b0 + tid < A.batch.B ? b0 + tid : -1;
-            const int64_t own =
-                A.batch.B <= kThreads8 ? last_cost : sequence_cost<kRows8, kTileCost8>(A, b, lane);
+            const int64_t own = A.batch.B <= kThreads8 ? last_cost : sequence_cost<kRows8, kTileCost8>(A, b, lane);
             int64_t inc = own;
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
@@ -298,84 +324,266 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
     const uint32_t tmem = sh.tmem;
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs8));
-        if (warp == 15) {
-            // ---- the schedule, and the queries of its pieces -------------------
-            Walker<kRows8, kTileCost8> walk;
-            walk.left = 0;
-            if (!idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas, lane);
-            int k = 0;
-            uint32_t turn = 1, qn = 0;
-            for (bool more = true; more;) {
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTileRegs8));
+        // ---- tiles: their pieces and queries ahead, their rows behind the softmax ------
+        const int tw = warp - 16, tt = tid - 512;
+        const uint32_t t_o = tmem + ((uint32_t)(tw * 32) << 16) + L::kOut;
+        Walker<kRows8, kTileCost8> walk;
+        walk.left = 0;
+        if (tw == 0 && !idle) walk.start(A, sh.b0, sh.skip, u0, u1 - u0, total, ctas, lane);
+        uint32_t ready = 0, done = 0, qn = 0;  // pieces published and finished, tiles with queries
+        bool more = true;                      // pieces may follow
+        // Publishes the next piece and prepares its queries (all four warps; false after
+        // a wait gave up).
+        auto prepare = [&]() -> bool {
+            const int k = ready % kPieces;
+            bool ok = true;
+            if (tw == 0) {
                 Piece p;
-                more = walk.next(A, p);
-                if (!more) p.n = -1;
-                if (!__all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.piece_empty[k], turn, status))) break;
-                if (lane == 0) {
+                if (!walk.next(A, p)) p.n = -1;
+                ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.piece_empty[k], (ready / kPieces & 1) ^ 1,
+                                                                  status));
+                if (ok && lane == 0) {
                     sh.pieces[k] = p;
                     mbar_arrive(&sh.piece_full[k]);
                 }
                 __syncwarp();
-                if (++k == kPieces) {
-                    k = 0;
-                    turn ^= 1;
+            }
+            ok = ok && __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.piece_full[k], ready / kPieces & 1, status));
+            if (group_any(3, !ok)) return false;
+            const Piece &p = sh.pieces[k];
+            if (p.n < 0) {
+                more = false;
+                return true;
+            }
+            ++ready;
+            if (p.n == 0) return true;
+            const int qb = qn & 1;
+            ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.q_empty[qb], (qn >> 1 & 1) ^ 1, status));
+            ++qn;
+            // four values to a lane, rows tw, tw + 4, ... to a warp
+            constexpr int kMine = kRows8 / 4;
+            uint2 x[kMine];
+            uint32_t top = 0;
+            const int rows = p.rows;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int r = tw + 4 * i;
+                x[i] = make_uint2(0, 0);
+                if (r >= rows || lane * 4 >= D || A.q_mode == 2) continue;
+                const int pr = p.row + r, j = A.by_group.div(pr);
+                x[i] = __ldg(reinterpret_cast<const uint2 *>(
+                    static_cast<const uint16_t *>(A.q) + (int64_t)(p.token + j) * A.q_st[0] +
+                    (p.h * A.group + (pr - j * A.group)) * A.q_st[1] + lane * 4));
+            }
+            auto bits = [&](const float2 &f) -> uint32_t {  // of the larger finite magnitude
+                const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu, b = __float_as_uint(f.y) & 0x7fffffffu;
+                return max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u);
+            };
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                top = max(top, max(bits(pair_of(x[i].x, T())), bits(pair_of(x[i].y, T()))));
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) sh.q_top[tw] = top;
+            group_barrier(3);
+            top = max(max(sh.q_top[0], sh.q_top[1]), max(sh.q_top[2], sh.q_top[3]));
+            // the largest is brought to 57344 (e5m2's) or less
+            const int e = min(max((int)(top >> 23) - 127 - 15 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 120);
+            const float f = A.q_mode == 1 ? -power_of_two(-e) : power_of_two(-e);
+            char *to = smem + L::kQ + qb * L::kQuery;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int r = tw + 4 * i;
+                const float2 a = pair_of(x[i].x, T()), b = pair_of(x[i].y, T());
+                float y[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
+                // an infinity makes its row NaN, as a NaN does
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (!(fabsf(y[m]) <= 57344.f)) y[m] = __uint_as_float(0x7fffffffu);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+                    *reinterpret_cast<uint32_t *>(to + (part * kRows8 + r) * 128 + ((lane / 4) ^ (r & 7)) * 16 +
+                                                  lane % 4 * 4) = split_off(y);
+            }
+            if (tt == 0) sh.q_factor[qb] = A.scale_log2 * power_of_two(e);
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[qb]);
+            return !group_any(3, !ok);
+        };
+        bool ok = prepare() && (!more || prepare());
+        while (ok && done < ready) {
+            const Piece &p = sh.pieces[done % kPieces];
+            const uint32_t tb = done & 1, turn = done >> 1 & 1;
+            const int blocks = p.n, row0 = p.row, rows = p.rows;
+            ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.state_full[tb], turn, status));
+            ok = ok && __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.o_full[tb], turn, status));
+            ok = !group_any(3, !ok);
+            if (!ok) break;
+            tc::fence_after();
+            // the groups' states, joined: lane r has row r's
+            const TileState &st = misc.tile[tb];
+            float ref = -INFINITY, sum = 0.f, f[2];
+            {
+                float own_ref[2], own_sum[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float m = st.minus[x][lane];
+                    own_ref[x] = m == kUnset ? -INFINITY : -m;
+                    own_sum[x] = (st.sums[x][0][lane] + st.sums[x][1][lane]) +
+                                 (st.sums[x][2][lane] + st.sums[x][3][lane]);
+                    ref = fmaxf(ref, own_ref[x]);
                 }
-                if (p.n <= 0) continue;
-                const int qb = qn & 1;
-                if (!__all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.q_empty[qb], ((qn >> 1) & 1) ^ 1, status)))
-                    break;
-                ++qn;
-                // four values to a lane, eight rows' loads in flight
-                auto load = [&](int r) -> uint2 {
-                    if (r >= p.rows || lane * 4 >= D || A.q_mode == 2) return make_uint2(0, 0);
-                    const int pr = p.row + r, j = A.by_group.div(pr);
-                    return __ldg(reinterpret_cast<const uint2 *>(
-                        static_cast<const uint16_t *>(A.q) + (int64_t)(p.token + j) * A.q_st[0] +
-                        (p.h * A.group + (pr - j * A.group)) * A.q_st[1] + lane * 4));
-                };
-                auto bits = [&](const float2 &f) -> uint32_t {  // of the larger finite magnitude
-                    const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu, b = __float_as_uint(f.y) & 0x7fffffffu;
-                    return max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u);
-                };
-                uint32_t top = 0;
-                for (int r0 = 0; r0 < p.rows; r0 += 8) {
-                    uint2 x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = load(r0 + i);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        top = max(top, max(bits(pair_of(x[i].x, T())), bits(pair_of(x[i].y, T()))));
+                for (int x = 0; x < 2; ++x) {
+                    f[x] = own_ref[x] == -INFINITY ? 0.f : ex2(own_ref[x] - ref);
+                    sum += own_sum[x] * f[x];
+                    const int e = st.exponent[x];
+                    f[x] *= e == kNoScale ? 0.f : ex2((float)(e - (int)kHalfLift));
                 }
-                for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                // the largest is brought to 57344 (e5m2's) or less
-                const int e = min(max((int)(top >> 23) - 127 - 15 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 120);
-                const float f = A.q_mode == 1 ? -power_of_two(-e) : power_of_two(-e);
-                char *to = smem + L::kQ + qb * L::kQuery;
-                for (int r0 = 0; r0 < kRows8; r0 += 8) {
-                    uint2 x[8];
+            }
+            // (a row that saw nothing has the sum 0, and zeros)
+            const float norm = sum == 0.f ? 0.f : 1.f / sum;
+            const bool whole = p.parts == 1;
+            const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
+            float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
+            float *part_out = reinterpret_cast<float *>(A.workspace + kAttendOut);
+            constexpr int64_t kSlot = (int64_t)(kMaxHeadDim / 4) * 2 * kRows * 4;  // floats of a slot
+            // rows of out, one after another; thread d has value d
+            const int j_first = A.by_group.div(row0);
+            int head = row0 - j_first * A.group;
+            T *out = static_cast<T *>(A.out) + (int64_t)(p.token + j_first) * A.o_st[0] +
+                     ((int64_t)p.h * A.group + head) * A.o_st[1] + tt;
+            const int64_t wrap = A.o_st[0] - A.group * A.o_st[1];
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+                float o[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = load(r0 + i);
+                for (int r = 0; r < 8; ++r) o[r] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 a = pair_of(x[i].x, T()), b = pair_of(x[i].y, T());
-                        float y[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
-                        // an infinity makes its row NaN, as a NaN does
+                for (int x = 0; x < 2; ++x) {
+                    if (blocks <= x) break;
+                    uint32_t u[8];
+                    tc::ld8(u, t_o + (tb * 2 + x) * L::kOutCols + r0);
+                    tc::wait_ld();
 #pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            if (!(fabsf(y[m]) <= 57344.f)) y[m] = __uint_as_float(0x7fffffffu);
+                    for (int r = 0; r < 8; ++r)
+                        o[r] = fmaf(__shfl_sync(0xffffffffu, f[x], r0 + r), __uint_as_float(u[r]), o[r]);
+                }
+                if (whole) {
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-                            *reinterpret_cast<uint32_t *>(to + (part * kRows8 + r0 + i) * 128 +
-                                                          ((lane / 4) ^ i) * 16 + lane % 4 * 4) = split_off(y);
+                    for (int r = 0; r < 8; ++r) {
+                        const float n = __shfl_sync(0xffffffffu, norm, r0 + r);
+                        if (r0 + r >= rows) break;
+                        if (tt < D) *out = from_f32<T>(n == 0.f ? 0.f : o[r] * n);
+                        out += A.o_st[1];
+                        if (++head == A.group) {
+                            head = 0;
+                            out += wrap;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r0 + r < rows) part_out[slot * kSlot + (r0 + r) * 128 + tt] = o[r];
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.o_empty[tb]);
+                mbar_arrive(&sh.state_empty[tb]);
+            }
+            if (!whole) {
+                if (tw == 0) part_stats[(int64_t)slot * 2 * kRows + lane] = make_float2(ref, sum);
+                group_barrier(3);
+                if (tt == 0) {
+                    __threadfence();  // all 128 threads' writes, after the barrier
+                    uint32_t *count = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters) + 2 * p.first;
+                    const uint32_t before = atomicAdd(count, 1u);
+                    const bool last = before == (uint32_t)p.parts - 1;
+                    if (last) *count = 0;
+                    // no call leaves such a count: the workspace was not initialised
+                    if (before >= (uint32_t)p.parts) atomicOr(status, SV_STATUS_OVERFLOW);
+                    sh.last = last;
+                }
+                group_barrier(3);
+                if (sh.last) {
+                    __threadfence();
+                    const int parts = p.parts, first = p.first;
+                    auto slot_of = [&](int i) -> int64_t { return (first + i) * 2 + (i == 0 ? 1 : 0); };
+                    // lane r: row r's reference and sum over the parts (as many loads in
+                    // flight as a batch; one past the end is the last once more)
+                    constexpr int kBatch = 8;
+                    float top = -INFINITY, all = 0.f;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < parts; i0 += kBatch) {
+                        float2 x[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            x[i] = __ldcg(&part_stats[slot_of(min(i0 + i, parts - 1)) * 2 * kRows + lane]);
+                        float m = top;
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) m = fmaxf(m, x[i].x);
+                        all *= top == -INFINITY ? 0.f : ex2(top - m);
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (i0 + i < parts && x[i].y != 0.f) all += x[i].y * ex2(x[i].x - m);
+                        top = m;
+                    }
+                    const float over = all == 0.f ? 0.f : 1.f / all;
+                    // four values to a lane, one row to a warp, or two of up to 64 values
+                    const int per = wide ? 1 : 2, d0 = (wide ? lane : lane % 16) * 4;
+                    const int64_t base = (int64_t)p.token * A.o_st[0] + (int64_t)p.h * A.group * A.o_st[1];
+#pragma unroll 1
+                    for (int r0 = tw * per; r0 < rows; r0 += 4 * per) {
+                        const int r = min(r0 + (wide ? 0 : lane / 16), rows - 1);
+                        const float row_top = __shfl_sync(0xffffffffu, top, r);
+                        const float row_over = __shfl_sync(0xffffffffu, over, r);
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                        for (int i0 = 0; i0 < parts; i0 += kBatch) {
+                            float4 x[kBatch];
+                            float m[kBatch];
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) {
+                                const int64_t at = slot_of(min(i0 + i, parts - 1));
+                                m[i] = __ldcg(&part_stats[at * 2 * kRows + r]).x;
+                                x[i] = __ldcg(reinterpret_cast<const float4 *>(part_out + at * kSlot + r * 128 + d0));
+                            }
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) {
+                                // (a NaN query leaves no reference, and NaN in O)
+                                const float w = i0 + i >= parts || m[i] == -INFINITY ? 0.f : ex2(m[i] - row_top);
+                                if (i0 + i < parts) {
+                                    acc.x = fmaf(w, x[i].x, acc.x);
+                                    acc.y = fmaf(w, x[i].y, acc.y);
+                                    acc.z = fmaf(w, x[i].z, acc.z);
+                                    acc.w = fmaf(w, x[i].w, acc.w);
+                                }
+                            }
+                        }
+                        if (d0 < D && (wide || r0 + lane / 16 < rows)) {
+                            const int pr = row0 + r, j = A.by_group.div(pr);
+                            uint2 y;
+                            y.x = pack2<T>(acc.x * row_over, acc.y * row_over);
+                            y.y = pack2<T>(acc.z * row_over, acc.w * row_over);
+                            if (row_over == 0.f) y = make_uint2(0, 0);
+                            *reinterpret_cast<uint2 *>(static_cast<T *>(A.out) + base + j * A.o_st[0] +
+                                                       (pr - j * A.group) * A.o_st[1] + d0) = y;
+                        }
                     }
                 }
-                if (lane == 0) sh.q_factor[qb] = A.scale_log2 * power_of_two(e);
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_full[qb]);
             }
-        } else if (warp == 12) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.piece_empty[done % kPieces]);
+            ++done;
+            if (more) ok = prepare();
+        }
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs8));
+        if (warp == 12) {
             // ---- copies of codes ------------------------------------------------
             const int boxes = kKeys / A.piece;
             const bool active = lane < boxes;
@@ -383,14 +591,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh, status)) {
-                const Piece p = sh.pieces[reader.k];
+                const Piece &q = sh.pieces[reader.k];
+                const int blocks = q.n, lo = q.lo, end = q.end, h = q.h;
+                const int32_t *table = A.batch.pages + q.b * A.batch.pages_stride;
+                const int first = A.window > 0 ? q.past + A.by_group.div(q.row) - A.window + 1 : 0;
                 reader.done(sh, lane);
-                if (p.n == 0) continue;
-                const int32_t *table = A.batch.pages + p.b * A.batch.pages_stride;
-                const int first = A.window > 0 ? p.past + A.by_group.div(p.row) - A.window + 1 : 0;
+                if (blocks == 0) continue;
                 auto page_of = [&](int i) -> int {
-                    const int s0 = (p.lo + i) * kKeys + lane * A.piece;
-                    if (!active || i >= p.n || s0 >= p.end || s0 + A.piece <= first) return kNoPage;
+                    const int s0 = (lo + i) * kKeys + lane * A.piece;
+                    if (!active || i >= blocks || s0 >= end || s0 + A.piece <= first) return kNoPage;
                     return __ldg(table + A.by_page.div(s0));
                 };
                 auto checked = [&](int id) -> int {
@@ -400,31 +609,36 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     return id;
                 };
-                auto load = [&](const CUtensorMap &map, int ring, unsigned long long *full, unsigned long long *empty,
-                                int &n, int i, int id) {
-                    const int st = n % kRing8;
-                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &empty[st], (n / kRing8 & 1) ^ 1, status));
-                    if (ok) {
-                        if (lane == 0) mbar_arrive_expect_tx(&full[st], kRaw);
-                        __syncwarp();
-                        if (active) {
-                            const int s0 = (p.lo + i) * kKeys + lane * A.piece;
-                            tc::load_box(smem + ring + st * kRaw + lane * A.piece * 128, &map, 0, p.h,
-                                         s0 - A.by_page.div(s0) * A.batch.page_size, id, &full[st]);
-                        }
-                        ++n;
-                    }
+                auto load = [&](const CUtensorMap &map, int at, unsigned long long *full, unsigned long long *empty,
+                                uint32_t turn, int i, int id) {
+                    ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, turn ^ 1, status));
+                    if (!ok) return;
+                    if (lane == 0) mbar_arrive_expect_tx(full, kRaw);
                     __syncwarp();
+                    if (active) {
+                        const int s0 = (lo + i) * kKeys + lane * A.piece;
+                        tc::load_box(smem + at + lane * A.piece * 128, &map, 0, h,
+                                     s0 - A.by_page.div(s0) * A.batch.page_size, id, full);
+                    }
                 };
-                auto keys = [&](int i, int id) { load(kmap, L::kK, sh.k_full, sh.k_empty, kn, i, id); };
+                auto keys = [&](int i, int id) {
+                    const int st = kn % kRing8;
+                    load(kmap, L::kK + st * kRaw, &sh.k_full[st], &sh.k_empty[st], kn / kRing8 & 1, i, id);
+                    if (ok) ++kn;
+                };
+                auto values = [&](int i, int id) {
+                    const int st = vn % L::kRingV;
+                    load(vmap, L::kV + st * kRaw, &sh.v_full[st], &sh.v_empty[st], vn / L::kRingV & 1, i, id);
+                    if (ok) ++vn;
+                };
                 // keys run a block ahead of values, page ids a block ahead of keys
                 int id0 = checked(page_of(0)), id1 = page_of(1), id2 = page_of(2);
                 keys(0, id0);
-                for (int i = 0; i < p.n; ++i) {
+                for (int i = 0; i < blocks; ++i) {
                     const int id3 = page_of(i + 3);
                     id1 = checked(id1);
-                    if (i + 1 < p.n) keys(i + 1, id1);
-                    load(vmap, L::kV, sh.v_full, sh.v_empty, vn, i, id0);
+                    if (i + 1 < blocks) keys(i + 1, id1);
+                    values(i, id0);
                     id0 = id1;
                     id1 = id2;
                     id2 = id3;
@@ -432,7 +646,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             }
             // the last copies have landed before the CTA may end
             for (int n = max(0, kn - kRing8); n < kn; ++n) mbar_wait(&sh.k_full[n % kRing8], n / kRing8 & 1);
-            for (int n = max(0, vn - kRing8); n < vn; ++n) mbar_wait(&sh.v_full[n % kRing8], n / kRing8 & 1);
+            for (int n = max(0, vn - L::kRingV); n < vn; ++n) mbar_wait(&sh.v_full[n % L::kRingV], n / L::kRingV & 1);
         } else if (warp == 13) {
             // ---- scores ---------------------------------------------------------
             const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
@@ -475,12 +689,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const uint32_t tm = (uint32_t)tc::uniform((int)tmem) + L::kOut;
             const uint64_t v_desc = tc::smem_desc(smem_u32(smem + L::kVc), kRaw, 1024);
             const uint64_t p_desc = tc::smem_desc(smem_u32(smem + L::kP), kRaw, 1024);
-            uint32_t used[2] = {0, 0};
+            uint32_t used[2] = {0, 0}, tile = 0;
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh, status)) {
                 const int blocks = tc::uniform(sh.pieces[reader.k].n);
                 reader.done(sh, lane);
+                const uint32_t tb = tile & 1;
+                ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.o_empty[tb], (tile >> 1 & 1) ^ 1, status));
+                ++tile;
                 for (int i = 0; i < blocks && ok; ++i) {
                     const uint32_t b = i & 1, turn = (b ? used[1]++ : used[0]++) & 1;
                     ok = __all_sync(0xffffffffu, hold8(sh, &sh.vc_full[b], turn, status));
@@ -491,62 +708,120 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * (kRaw / 16);
 #pragma unroll
                         for (int s = 0; s < kKeys / 16; ++s)
-                            tc::mma_ss(tm + b * L::kOutCols, vd + s * (2048 / 16), pd + s * (2048 / 16), kIdescO, i > 1 || s > 0);
+                            tc::mma_ss(tm + (tb * 2 + b) * L::kOutCols, vd + s * (2048 / 16), pd + s * (2048 / 16),
+                                       kIdescO, i > 1 || s > 0);
                         tc::commit(&sh.pv_done[b]);
                     }
                     __syncwarp();
                 }
+                if (tc::elect() && ok) tc::commit(&sh.o_full[tb]);
+                __syncwarp();
             }
             if (tc::elect()) tc::commit(&sh.drain[1]);
             __syncwarp();
             mbar_wait(&sh.drain[1], 0);
         } else {
-            // ---- values to fp16 ---------------------------------------------------
-            const int t = tid - 256;
-            // a thread's chunk of 16 values and its slot of a group (eight lanes' chunks
-            // lie in different banks)
-            const int ch = wide ? t % 8 : t % 4, u = t / 4;
-            const int slot0 = wide ? t / 8 : (u >> 3) * 8 + ((u & 1) << 2) + ((u >> 1) & 3);
-            const int rounds = wide ? 8 : 4, per = wide ? 16 : 32;
-            const bool odd_first = wide ? ch >= 4 : u & 1;
-            uint32_t n = 0, used[2] = {0, 0};
+            // ---- scales: four slots to a lane ------------------------------------
+            const Scales &S = P8.scales;
+            // four bytes at once where they lie so
+            const bool k4 = S.k_st[1] == 1 && ((reinterpret_cast<uintptr_t>(S.k) | S.k_st[0] | S.k_st[2]) & 3) == 0;
+            const bool v4 = S.v_st[1] == 1 && ((reinterpret_cast<uintptr_t>(S.v) | S.v_st[0] | S.v_st[2]) & 3) == 0;
+            constexpr uint32_t kNone = (127 + kMinScale) * 0x01010101u;  // no page, no codes
+            uint32_t n = 0;
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh, status)) {
-                const int blocks = sh.pieces[reader.k].n;
-                // slots from the tile's end on: whatever lies there, zeros
-                const int end = sh.pieces[reader.k].end - sh.pieces[reader.k].lo * kKeys;
+                const Piece &q = sh.pieces[reader.k];
+                const int blocks = q.n, lo = q.lo, end = q.end;
+                const int32_t *table = A.batch.pages + q.b * A.batch.pages_stride;
+                const int first = A.window > 0 ? q.past + A.by_group.div(q.row) - A.window + 1 : 0;
+                const uint8_t *ks = S.k + q.h * S.k_st[2], *vs = S.v + q.h * S.v_st[2];
                 reader.done(sh, lane);
+                auto page_of = [&](int i) -> int {
+                    const int s0 = (lo + i) * kKeys + lane * 4;
+                    return i >= blocks || s0 >= end || s0 + 4 <= first ? -1 : __ldg(table + A.by_page.div(s0));
+                };
+                auto four = [&](const uint8_t *base, const int64_t *st, bool at_once, int i, int id) -> uint32_t {
+                    if (id < 0 || id >= A.batch.num_pages) return kNone;
+                    const int s0 = (lo + i) * kKeys + lane * 4;
+                    const uint8_t *at = base + id * st[0] + (s0 - A.by_page.div(s0) * A.batch.page_size) * st[1];
+                    if (at_once) return __ldg(reinterpret_cast<const uint32_t *>(at));
+                    return (uint32_t)__ldg(at) | (uint32_t)__ldg(at + st[1]) << 8 |
+                           (uint32_t)__ldg(at + 2 * st[1]) << 16 | (uint32_t)__ldg(at + 3 * st[1]) << 24;
+                };
+                // a block's bytes are loaded two blocks ahead of their use, its page ids three
+                int id2 = page_of(2);
+                uint32_t key0, value0, key1, value1;
+                {
+                    const int id0 = page_of(0), id1 = page_of(1);
+                    key0 = four(ks, S.k_st, k4, 0, id0), value0 = four(vs, S.v_st, v4, 0, id0);
+                    key1 = four(ks, S.k_st, k4, 1, id1), value1 = four(vs, S.v_st, v4, 1, id1);
+                }
                 for (int i = 0; i < blocks && ok; ++i, ++n) {
-                    const uint32_t st = n % kRing8, b = i & 1, turn = b ? used[1]++ : used[0]++;
-                    const int here = end - i * kKeys;
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[st], n / kRing8 & 1, status));
-                    if (ok && turn > 0)
-                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1, status));
+                    const uint32_t st = n % kScaleRing;
+                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[st], (n / kScaleRing & 1) ^ 1, status));
                     if (!ok) break;
-                    const char *from = smem + L::kV + st * kRaw;
-                    char *to = smem + L::kVc + b * 2 * kRaw + (ch / 4) * kRaw;
-#pragma unroll 4
-                    for (int k = 0; k < rounds; ++k) {
-                        const int slot = k * per + slot0, x = slot & 7;
-                        uint4 w = *reinterpret_cast<const uint4 *>(from + slot * 128 + ((ch ^ x) * 16));
-                        if (slot >= here) w = make_uint4(0, 0, 0, 0);
-                        uint4 lo, hi;
-                        codes_to_half(w.x, lo.x, lo.y);
-                        codes_to_half(w.y, lo.z, lo.w);
-                        codes_to_half(w.z, hi.x, hi.y);
-                        codes_to_half(w.w, hi.z, hi.w);
-                        const int j = (ch % 4) * 2;
-                        char *row = to + slot * 128;
-                        *reinterpret_cast<uint4 *>(row + (((j + (odd_first ? 1 : 0)) ^ x) * 16)) = odd_first ? hi : lo;
-                        *reinterpret_cast<uint4 *>(row + (((j + (odd_first ? 0 : 1)) ^ x) * 16)) = odd_first ? lo : hi;
-                    }
-                    tc::fence_async_smem();
+                    *reinterpret_cast<uint32_t *>(&misc.scales[st][0][lane * 4]) = key0;
+                    *reinterpret_cast<uint32_t *>(&misc.scales[st][1][lane * 4]) = value0;
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sh.vc_full[b]);
-                        mbar_arrive(&sh.v_empty[st]);
-                    }
+                    if (lane == 0) mbar_arrive(&sh.scale_full[st]);
+                    key0 = key1;
+                    value0 = value1;
+                    key1 = four(ks, S.k_st, k4, i + 2, id2);
+                    value1 = four(vs, S.v_st, v4, i + 2, id2);
+                    id2 = page_of(i + 3);
+                }
+            }
+        }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kValueRegs8));
+        // ---- values to fp16 ---------------------------------------------------
+        const int t = tid - 256;
+        // a thread's chunk of 16 values and its slot of a group (eight lanes' chunks
+        // lie in different banks)
+        const int ch = wide ? t % 8 : t % 4, u = t / 4;
+        const int slot0 = wide ? t / 8 : (u >> 3) * 8 + ((u & 1) << 2) + ((u >> 1) & 3);
+        const int rounds = wide ? 8 : 4, per = wide ? 16 : 32;
+        const bool odd_first = wide ? ch >= 4 : u & 1;
+        uint32_t n = 0, used[2] = {0, 0};
+        PieceReader8 reader;
+        bool ok = true;
+        while (ok && reader.next(sh, status)) {
+            const int blocks = sh.pieces[reader.k].n;
+            // slots from the tile's end on: whatever lies there, zeros
+            const int end = sh.pieces[reader.k].end - sh.pieces[reader.k].lo * kKeys;
+            reader.done(sh, lane);
+            for (int i = 0; i < blocks && ok; ++i, ++n) {
+                const uint32_t st = n % L::kRingV, b = i & 1, turn = b ? used[1]++ : used[0]++;
+                const int here = end - i * kKeys;
+                ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[st], n / L::kRingV & 1, status));
+                if (ok && turn > 0)
+                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1, status));
+                if (!ok) break;
+                const char *from = smem + L::kV + st * kRaw;
+                char *to = smem + L::kVc + b * 2 * kRaw + (ch / 4) * kRaw;
+                // (per is a multiple of 8: all of a thread's slots share their place in a swizzle)
+                const int x = slot0 & 7, j = (ch % 4) * 2;
+                const char *src = from + slot0 * 128 + ((ch ^ x) * 16);
+                char *dst0 = to + slot0 * 128 + (((j + (odd_first ? 1 : 0)) ^ x) * 16);
+                char *dst1 = to + slot0 * 128 + (((j + (odd_first ? 0 : 1)) ^ x) * 16);
+#pragma unroll 4
+                for (int k = 0; k < rounds; ++k) {
+                    uint4 w = *reinterpret_cast<const uint4 *>(src + k * per * 128);
+                    if (k * per + slot0 >= here) w = make_uint4(0, 0, 0, 0);
+                    uint4 lo, hi;
+                    codes_to_half(w.x, lo.x, lo.y);
+                    codes_to_half(w.y, lo.z, lo.w);
+                    codes_to_half(w.z, hi.x, hi.y);
+                    codes_to_half(w.w, hi.z, hi.w);
+                    *reinterpret_cast<uint4 *>(dst0 + k * per * 128) = odd_first ? hi : lo;
+                    *reinterpret_cast<uint4 *>(dst1 + k * per * 128) = odd_first ? lo : hi;
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.vc_full[b]);
+                    mbar_arrive(&sh.v_empty[st]);
                 }
             }
         }
@@ -555,21 +830,24 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // ---- softmax: a slot to a thread ------------------------------------------
         const int g = warp / 4, gw = warp % 4, gt = gw * 32 + lane;
         const uint32_t lanes_at = tmem + ((uint32_t)(gw * 32) << 16);
-        const uint32_t t_s = lanes_at + g * L::kScoreCols, t_o = lanes_at + L::kOut;
-        uint32_t used = 0, others = 0, qn = 0;  // blocks of this group and of the other, tiles
+        const uint32_t t_s = lanes_at + g * L::kScoreCols;
+        GroupState &own = misc.group[g];
+        uint32_t used = 0, n0 = 0, qn = 0, tile = 0;  // the group's blocks, all blocks, tiles
         PieceReader8 reader;
         for (;;) {
-            // (all eight warps go on, or none: they meet at barriers; and the last
-            // tile's outputs have been read)
-            if (softmax_any<256>(3, !reader.next(sh, status))) break;
+            // (all four warps go on, or none: they meet at barriers)
+            if (group_any(1 + g, !reader.next(sh, status))) break;
             const Piece &p = sh.pieces[reader.k];
-            const int blocks = p.n, past = p.past, row0 = p.row, rows = p.rows;
-            const int mine = (blocks + 1 - g) / 2, theirs = blocks - mine;
+            const int blocks = p.n, past = p.past, row0 = p.row, lo = p.lo, end = p.end;
+            const int mine = (blocks + 1 - g) / 2;
+            const int j0 = A.by_group.div(row0), j1 = A.by_group.div(row0 + p.rows - 1);
+            reader.done(sh, lane);
             uint64_t sums[kRows8 / 2];  // this thread's slots', of rows 2 r and 2 r + 1
 #pragma unroll
             for (int r = 0; r < kRows8 / 2; ++r) sums[r] = 0;
-            int exponent = kNoScale;  // weights are times 2^-exponent
-            if (gw == 0) shared.minus[g][lane] = kUnset;
+            int exponent = kNoScale;    // weights are times 2^-exponent
+            float minus = kUnset;       // lane r: minus row r's reference
+            const uint32_t tb = tile & 1;
             if (blocks > 0) {
                 const uint32_t qb = qn & 1;
                 hold8<kPieceLimitNs>(sh, &sh.q_full[qb], (qn >> 1) & 1, status);
@@ -577,43 +855,18 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const float q_factor = sh.q_factor[qb];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_empty[qb]);
-                softmax_barrier<128>(1 + g);
-
-                // scales: one of the group's blocks ahead, page ids two
-                const int32_t *table = A.batch.pages + p.b * A.batch.pages_stride;
-                const int lo = p.lo, end = p.end;
-                const int j0 = A.by_group.div(row0), j1 = A.by_group.div(row0 + rows - 1);
-                const int first_seen = A.window > 0 ? past + j0 - A.window + 1 : 0;
-                const uint8_t *k_scales = P8.scales.k + p.h * P8.scales.k_st[2];
-                const uint8_t *v_scales = P8.scales.v + p.h * P8.scales.v_st[2];
-                auto slot_at = [&](int i) -> int { return (lo + 2 * i + g) * kKeys + gt; };
-                auto page_of = [&](int i) -> int {
-                    const int s = slot_at(i);
-                    return i >= mine || s >= end || s < first_seen ? -1 : __ldg(table + A.by_page.div(s));
-                };
-                // (bytes as they come: nothing waits for them before the next block)
-                uint32_t key_byte, value_byte, next_key, next_value;
-                auto scales_of = [&](int i, int id) {
-                    next_key = next_value = 127 + kMinScale;
-                    if (id < 0 || id >= A.batch.num_pages) return;  // (no codes either)
-                    const int s = slot_at(i);
-                    const int64_t in = s - A.by_page.div(s) * A.batch.page_size;
-                    next_key = __ldg(k_scales + id * P8.scales.k_st[0] + in * P8.scales.k_st[1]);
-                    next_value = __ldg(v_scales + id * P8.scales.v_st[0] + in * P8.scales.v_st[1]);
-                };
-                scales_of(0, page_of(0));
-                int next_page = page_of(1);
+                const uint32_t t_o = lanes_at + L::kOut + (tb * 2 + g) * L::kOutCols;
                 for (int i = 0; i < mine; ++i, ++used) {
-                    key_byte = next_key;
-                    value_byte = next_value;
-                    scales_of(i + 1, next_page);
-                    next_page = page_of(i + 2);
+                    const int k0 = (lo + 2 * i + g) * kKeys;
+                    const uint32_t n = n0 + 2 * i + g, sc = n % kScaleRing;
+                    hold8(sh, &sh.scale_full[sc], n / kScaleRing & 1, status);
+                    const uint32_t key_byte = misc.scales[sc][0][gt], value_byte = misc.scales[sc][1][gt];
                     hold8(sh, &sh.s_full[g], used & 1, status);
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.scale_empty[sc]);
                     tc::fence_after();
                     uint64_t y[kRows8 / 2];  // of rows 2 r and 2 r + 1
                     const float key_scale = q_factor * scale_of(key_byte);
-                    const int k0 = (lo + 2 * i + g) * kKeys;
                     const bool masked =
                         k0 + kKeys - 1 > past + j0 || (A.window > 0 && k0 <= past + j1 - A.window);
                     auto scores = [&]() {
@@ -661,85 +914,85 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     auto relative = [&]() -> float {
                         float top = -INFINITY;
 #pragma unroll
-                        for (int o = 0; o < kRows8 / 8; ++o) {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const float4 m = *reinterpret_cast<const float4 *>(&shared.minus[g][o * 8 + c * 4]);
-                                const int r = o * 4 + c * 2;
-                                y[r] = add2(y[r], pair2(m.x, m.y));
-                                y[r + 1] = add2(y[r + 1], pair2(m.z, m.w));
-                                float a, b;
-                                unpair2(y[r], a, b);
-                                top = max3(top, a, b);
-                                unpair2(y[r + 1], a, b);
-                                top = max3(top, a, b);
-                            }
+                        for (int o = 0; o < kRows8 / 4; ++o) {
+                            const float4 m = *reinterpret_cast<const float4 *>(&own.minus[o * 4]);
+                            y[2 * o] = add2(y[2 * o], pair2(m.x, m.y));
+                            y[2 * o + 1] = add2(y[2 * o + 1], pair2(m.z, m.w));
+                            float a, b;
+                            unpair2(y[2 * o], a, b);
+                            top = max3(top, a, b);
+                            unpair2(y[2 * o + 1], a, b);
+                            top = max3(top, a, b);
                         }
                         return top;
                     };
-                    // (a byte of 255 is no scale: the vector is NaN)
-                    const int e8 = value_byte == kScaleNan ? kNoScale : (int)value_byte - 127;
+                    // (a byte of 255 is no scale: the vector is NaN; what lies behind the
+                    // tile's end is none either)
+                    const int e8 = value_byte == kScaleNan || k0 + gt >= end ? kNoScale : (int)value_byte - 127;
                     scores();
-                    const float top = relative();
-                    if (__builtin_expect(softmax_any<128>(1 + g, top > kRescaleAbove || e8 > exponent), 0)) {
+                    bool rare = true;
+                    if (i > 0) {
+                        const float top = relative();
+                        rare = group_any(1 + g, top > kRescaleAbove || e8 > exponent);
+                    }
+                    if (__builtin_expect(rare, 0)) {
                         // the rows' maxima over the block, and new references where they grew
-                        scores();
+                        if (i > 0) scores();
                         {
                             float v[kMaxRows8];
 #pragma unroll
                             for (int r = 0; r < kMaxRows8; ++r) v[r] = -INFINITY;
 #pragma unroll
                             for (int r = 0; r < kRows8 / 2; ++r) unpair2(y[r], v[2 * r], v[2 * r + 1]);
-                            shared.across[g][gw][lane] =
-                                across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                            own.across[gw][lane] = across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
                         }
                         const int largest = __reduce_max_sync(0xffffffffu, e8);
-                        if (lane == 0) shared.exponent[g][gw] = largest;
-                        softmax_barrier<128>(1 + g);
-                        float high = shared.across[g][0][lane];
-                        int most = shared.exponent[g][0];
+                        if (lane == 0) own.exponent[gw] = largest;
+                        group_barrier(1 + g);
+                        float high = own.across[0][lane];
+                        int most = own.exponent[0];
 #pragma unroll
                         for (int w = 1; w < 4; ++w) {
-                            high = fmaxf(high, shared.across[g][w][lane]);
-                            most = max(most, shared.exponent[g][w]);
+                            high = fmaxf(high, own.across[w][lane]);
+                            most = max(most, own.exponent[w]);
                         }
                         // (one more, so that the next larger scale is no new reference)
                         const int now_e = most > exponent ? most + 1 : exponent;
-                        const float old = shared.minus[g][lane];
-                        const bool grow = high + old > kRescaleAbove;
-                        const float now = grow ? -high : old;
-                        const float f = !grow ? 1.f : old == kUnset ? 0.f : ex2(now - old);
+                        const bool grow = high + minus > kRescaleAbove;
+                        const float now = grow ? -high : minus;
+                        const float f = !grow ? 1.f : minus == kUnset ? 0.f : ex2(now - minus);
                         const float fe = exponent == kNoScale ? 0.f : ex2((float)(exponent - now_e));
-                        const bool scaled = __any_sync(0xffffffffu, grow && old != kUnset) || now_e != exponent;
+                        const bool scaled = __any_sync(0xffffffffu, grow && minus != kUnset) || now_e != exponent;
                         exponent = now_e;
-                        softmax_barrier<128>(1 + g);
+                        minus = now;
                         if (gw == 0) {
-                            shared.minus[g][lane] = now;
-                            shared.factor[g][lane] = f;
+                            own.minus[lane] = now;
+                            own.factor[lane] = f;
                         }
-                        softmax_barrier<128>(1 + g);
+                        group_barrier(1 + g);
+                        if (i > 0) {
 #pragma unroll
-                        for (int o = 0; o < kRows8 / 4; ++o) {
-                            const float4 m = *reinterpret_cast<const float4 *>(&shared.factor[g][o * 4]);
-                            sums[2 * o] = mul2(sums[2 * o], pair2(m.x, m.y));
-                            sums[2 * o + 1] = mul2(sums[2 * o + 1], pair2(m.z, m.w));
-                        }
-                        if (scaled && i > 0) {
-                            hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
-                            __syncwarp();
-                            tc::fence_after();
-#pragma unroll 1
-                            for (int half = 0; half < L::kOutCols / 16; ++half) {
-                                uint32_t o[16];
-                                tc::ld16(o, t_o + g * L::kOutCols + half * 16);
-                                tc::wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) *
-                                                           (shared.factor[g][half * 16 + e] * fe));
-                                tc::st16(t_o + g * L::kOutCols + half * 16, o);
+                            for (int o = 0; o < kRows8 / 4; ++o) {
+                                const float4 m = *reinterpret_cast<const float4 *>(&own.factor[o * 4]);
+                                sums[2 * o] = mul2(sums[2 * o], pair2(m.x, m.y));
+                                sums[2 * o + 1] = mul2(sums[2 * o + 1], pair2(m.z, m.w));
                             }
-                            tc::wait_st();
+                            if (scaled) {
+                                hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
+                                __syncwarp();
+                                tc::fence_after();
+#pragma unroll 1
+                                for (int half = 0; half < L::kOutCols / 16; ++half) {
+                                    uint32_t o[16];
+                                    tc::ld16(o, t_o + half * 16);
+                                    tc::wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * (own.factor[half * 16 + e] * fe));
+                                    tc::st16(t_o + half * 16, o);
+                                }
+                                tc::wait_st();
+                            }
                         }
                         relative();
                     }
@@ -747,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.s_empty[g]);
                     // a weight times its scale, in fp16's range (2^15 at most)
-                    const int shift = e8 - exponent + (int)kHalfLift;
+                    const int shift = max(e8, -127) - exponent + (int)kHalfLift;
                     const float value_scale = shift < -126 ? 0.f : power_of_two(shift);
                     const uint64_t value_scale2 = pair2(value_scale, value_scale);
                     const bool any_nan = __any_sync(0xffffffffu, value_byte == kScaleNan);
@@ -779,160 +1032,27 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.p_full[g]);
                 }
-                others += theirs;
-                if (mine > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
-                if (theirs > 0) hold8(sh, &sh.pv_done[1 - g], (others - 1) & 1, status);
-                __syncwarp();
-                tc::fence_after();
+                n0 += blocks;
             }
-
-            // ---- the groups' states, joined: lane r has row r's --------------------------
+            // the tile's state, for the warps that finish it
             {
                 float v[kMaxRows8];
 #pragma unroll
                 for (int r = 0; r < kMaxRows8; ++r) v[r] = 0.f;
 #pragma unroll
                 for (int r = 0; r < kRows8 / 2; ++r) unpair2(sums[r], v[2 * r], v[2 * r + 1]);
-                shared.across[g][gw][lane] = across_lanes(v, lane, [](float a, float b) { return a + b; });
-                if (lane == 0) shared.exponent[g][gw] = exponent;
+                const float sum = across_lanes(v, lane, [](float a, float b) { return a + b; });
+                hold8<kPieceLimitNs>(sh, &sh.state_empty[tb], (tile >> 1 & 1) ^ 1, status);
+                TileState &st = misc.tile[tb];
+                st.sums[g][gw][lane] = sum;
+                if (gw == 0) {
+                    st.minus[g][lane] = minus;
+                    if (lane == 0) st.exponent[g] = exponent;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.state_full[tb]);
+                ++tile;
             }
-            softmax_barrier<256>(3);
-            float ref = -INFINITY, sum = 0.f, f[2];
-            {
-                float own_ref[2], own_sum[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float m = shared.minus[x][lane];
-                    own_ref[x] = m == kUnset ? -INFINITY : -m;
-                    own_sum[x] = (shared.across[x][0][lane] + shared.across[x][1][lane]) +
-                                 (shared.across[x][2][lane] + shared.across[x][3][lane]);
-                    ref = fmaxf(ref, own_ref[x]);
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    f[x] = own_ref[x] == -INFINITY ? 0.f : ex2(own_ref[x] - ref);
-                    sum += own_sum[x] * f[x];
-                    const int e = shared.exponent[x][0];
-                    f[x] *= e == kNoScale ? 0.f : ex2((float)(e - (int)kHalfLift));
-                }
-            }
-            // thread d of group g has value d of rows 16 g .. 16 g + 15
-            const int r0 = g * 16, here = min(16, rows - r0);
-            float o[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] = 0.f;
-            if (here > 0) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (blocks <= x) break;
-                    uint32_t u[16];
-                    tc::ld16(u, t_o + x * L::kOutCols + r0);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        o[r] = fmaf(__shfl_sync(0xffffffffu, f[x], r0 + r), __uint_as_float(u[r]), o[r]);
-                }
-                tc::fence_before();
-            }
-            // rows of out, one after another
-            const int j_first = A.by_group.div(row0 + r0);
-            int head = row0 + r0 - j_first * A.group;
-            T *out = static_cast<T *>(A.out) + (int64_t)(p.token + j_first) * A.o_st[0] +
-                     ((int64_t)p.h * A.group + head) * A.o_st[1] + gt;
-            const int64_t wrap = A.o_st[0] - A.group * A.o_st[1];
-            auto store = [&](float y) {
-                *out = from_f32<T>(y);
-                out += A.o_st[1];
-                if (++head == A.group) {
-                    head = 0;
-                    out += wrap;
-                }
-            };
-            if (p.parts == 1) {
-                // (a row that saw nothing has the sum 0, and zeros)
-                const float norm = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float n = __shfl_sync(0xffffffffu, norm, r0 + r);
-                    if (r < here && gt < D) store(n == 0.f ? 0.f : o[r] * n);
-                }
-            } else {
-                const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
-                float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
-                float *part_out = reinterpret_cast<float *>(A.workspace + kAttendOut);
-                constexpr int64_t kSlot = (int64_t)(kMaxHeadDim / 4) * 2 * kRows * 4;  // floats of a slot
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (r < here) part_out[slot * kSlot + (r0 + r) * 128 + gt] = o[r];
-                if (warp == 0) part_stats[(int64_t)slot * 2 * kRows + lane] = make_float2(ref, sum);
-                softmax_barrier<256>(3);
-                if (tid == 0) {
-                    __threadfence();  // all 256 threads' writes, after the barrier
-                    uint32_t *count = reinterpret_cast<uint32_t *>(A.workspace + kAttendCounters) + 2 * p.first;
-                    const uint32_t before = atomicAdd(count, 1u);
-                    const bool last = before == (uint32_t)p.parts - 1;
-                    if (last) *count = 0;
-                    // no call leaves such a count: the workspace was not initialised
-                    if (before >= (uint32_t)p.parts) atomicOr(status, SV_STATUS_OVERFLOW);
-                    sh.last = last;
-                }
-                softmax_barrier<256>(3);
-                if (sh.last && here > 0) {
-                    __threadfence();
-                    auto slot_of = [&](int i) -> int { return (p.first + i) * 2 + (i == 0 ? 1 : 0); };
-                    // lane r: row r's reference and sum over the parts (as many loads in
-                    // flight as a batch; one past the end is the last once more)
-                    constexpr int kBatch = 8;
-                    float top = -INFINITY, all = 0.f;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < p.parts; i0 += kBatch) {
-                        float2 x[kBatch];
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            x[i] = __ldcg(&part_stats[(int64_t)slot_of(min(i0 + i, p.parts - 1)) * 2 * kRows + lane]);
-                        float m = top;
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) m = fmaxf(m, x[i].x);
-                        all *= top == -INFINITY ? 0.f : ex2(top - m);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (i0 + i < p.parts && x[i].y != 0.f) all += x[i].y * ex2(x[i].x - m);
-                        top = m;
-                    }
-                    const float norm = all == 0.f ? 0.f : 1.f / all;
-                    float acc[16];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < p.parts; i0 += 2) {
-                        float x[2][16], m[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int64_t at = slot_of(min(i0 + i, p.parts - 1));
-                            m[i] = __ldcg(&part_stats[at * 2 * kRows + lane]).x;
-#pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                if (r < here) x[i][r] = __ldcg(&part_out[at * kSlot + (r0 + r) * 128 + gt]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            // (a NaN query leaves no reference, and NaN in O)
-                            const float w = i0 + i >= p.parts || m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) {
-                                const float fr = __shfl_sync(0xffffffffu, w, r0 + r);
-                                if (r < here) acc[r] = fmaf(fr, x[i][r], acc[r]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float n = __shfl_sync(0xffffffffu, norm, r0 + r);
-                        if (r < here && gt < D) store(n == 0.f ? 0.f : acc[r] * n);
-                    }
-                }
-            }
-            reader.done(sh, lane);
         }
     }
     tc::fence_before();
