@@ -609,36 +609,32 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     return id;
                 };
-                auto load = [&](const CUtensorMap &map, int at, unsigned long long *full, unsigned long long *empty,
-                                uint32_t turn, int i, int id) {
-                    ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, turn ^ 1, status));
-                    if (!ok) return;
-                    if (lane == 0) mbar_arrive_expect_tx(full, kRaw);
-                    __syncwarp();
-                    if (active) {
-                        const int s0 = (lo + i) * kKeys + lane * A.piece;
-                        tc::load_box(smem + at + lane * A.piece * 128, &map, 0, h,
-                                     s0 - A.by_page.div(s0) * A.batch.page_size, id, full);
-                    }
-                };
-                auto keys = [&](int i, int id) {
-                    const int st = kn % kRing8;
-                    load(kmap, L::kK + st * kRaw, &sh.k_full[st], &sh.k_empty[st], kn / kRing8 & 1, i, id);
-                    if (ok) ++kn;
-                };
-                auto values = [&](int i, int id) {
-                    const int st = vn % L::kRingV;
-                    load(vmap, L::kV + st * kRaw, &sh.v_full[st], &sh.v_empty[st], vn / L::kRingV & 1, i, id);
-                    if (ok) ++vn;
-                };
-                // keys run a block ahead of values, page ids a block ahead of keys
-                int id0 = checked(page_of(0)), id1 = page_of(1), id2 = page_of(2);
-                keys(0, id0);
-                for (int i = 0; i < blocks; ++i) {
+                // keys run a block ahead of values, page ids two blocks ahead of keys
+                int id0 = kNoPage, id1 = page_of(0), id2 = page_of(1);
+#pragma unroll 1
+                for (int i = -1; i < blocks && ok; ++i) {
                     const int id3 = page_of(i + 3);
                     id1 = checked(id1);
-                    if (i + 1 < blocks) keys(i + 1, id1);
-                    values(i, id0);
+#pragma unroll 1
+                    for (int of = 0; of < 2; ++of) {  // keys of block i + 1, values of block i
+                        const int x = of ? i : i + 1;
+                        if (x < 0 || x >= blocks) continue;
+                        const int ring = of ? L::kRingV : kRing8, n = of ? vn : kn, st = n % ring;
+                        unsigned long long *full = of ? &sh.v_full[st] : &sh.k_full[st];
+                        unsigned long long *empty = of ? &sh.v_empty[st] : &sh.k_empty[st];
+                        ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, (n / ring & 1) ^ 1, status));
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(full, kRaw);
+                        __syncwarp();
+                        if (active) {
+                            const int s0 = (lo + x) * kKeys + lane * A.piece;
+                            tc::load_box(smem + (of ? L::kV : L::kK) + st * kRaw + lane * A.piece * 128,
+                                         of ? &vmap : &kmap, 0, h, s0 - A.by_page.div(s0) * A.batch.page_size,
+                                         of ? id0 : id1, full);
+                        }
+                        if (of) ++vn;
+                        else ++kn;
+                    }
                     id0 = id1;
                     id1 = id2;
                     id2 = id3;
@@ -672,6 +668,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     tc::fence_after();
                     if (tc::elect()) {
                         const uint64_t kd = k_desc + st * (kRaw / 16), qd = q_desc + qb * (L::kQuery / 16);
+#pragma unroll 1
                         for (int s = 0; s < steps; ++s)
                             tc::mma_f8(tm + sb * L::kScoreCols, kd + s * 2, qd + s * 2, kIdescS, s > 0);
                         tc::commit(&sh.k_empty[st]);
@@ -706,7 +703,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     tc::fence_after();
                     if (tc::elect()) {
                         const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * (kRaw / 16);
-#pragma unroll
+#pragma unroll 1
                         for (int s = 0; s < kKeys / 16; ++s)
                             tc::mma_ss(tm + (tb * 2 + b) * L::kOutCols, vd + s * (2048 / 16), pd + s * (2048 / 16),
                                        kIdescO, i > 1 || s > 0);
@@ -746,30 +743,29 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const int s0 = (lo + i) * kKeys + lane * 4;
                     const uint8_t *at = base + id * st[0] + (s0 - A.by_page.div(s0) * A.batch.page_size) * st[1];
                     if (at_once) return __ldg(reinterpret_cast<const uint32_t *>(at));
-                    return (uint32_t)__ldg(at) | (uint32_t)__ldg(at + st[1]) << 8 |
-                           (uint32_t)__ldg(at + 2 * st[1]) << 16 | (uint32_t)__ldg(at + 3 * st[1]) << 24;
+                    uint32_t x = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e, at += st[1]) x |= (uint32_t)__ldg(at) << (8 * e);
+                    return x;
                 };
-                // a block's bytes are loaded two blocks ahead of their use, its page ids three
-                int id2 = page_of(2);
-                uint32_t key0, value0, key1, value1;
-                {
-                    const int id0 = page_of(0), id1 = page_of(1);
-                    key0 = four(ks, S.k_st, k4, 0, id0), value0 = four(vs, S.v_st, v4, 0, id0);
-                    key1 = four(ks, S.k_st, k4, 1, id1), value1 = four(vs, S.v_st, v4, 1, id1);
-                }
-                for (int i = 0; i < blocks && ok; ++i, ++n) {
-                    const uint32_t st = n % kScaleRing;
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[st], (n / kScaleRing & 1) ^ 1, status));
-                    if (!ok) break;
-                    *reinterpret_cast<uint32_t *>(&misc.scales[st][0][lane * 4]) = key0;
-                    *reinterpret_cast<uint32_t *>(&misc.scales[st][1][lane * 4]) = value0;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.scale_full[st]);
-                    key0 = key1;
-                    value0 = value1;
-                    key1 = four(ks, S.k_st, k4, i + 2, id2);
-                    value1 = four(vs, S.v_st, v4, i + 2, id2);
-                    id2 = page_of(i + 3);
+                // a block's bytes are loaded a block ahead of their use, its page ids two
+                uint32_t key = 0, value = 0;
+                int id = page_of(0);
+#pragma unroll 1
+                for (int i = -1; i < blocks && ok; ++i) {
+                    if (i >= 0) {
+                        const uint32_t st = n % kScaleRing;
+                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[st], (n / kScaleRing & 1) ^ 1, status));
+                        if (!ok) break;
+                        *reinterpret_cast<uint32_t *>(&misc.scales[st][0][lane * 4]) = key;
+                        *reinterpret_cast<uint32_t *>(&misc.scales[st][1][lane * 4]) = value;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.scale_full[st]);
+                        ++n;
+                    }
+                    key = four(ks, S.k_st, k4, i + 1, id);
+                    value = four(vs, S.v_st, v4, i + 1, id);
+                    id = page_of(i + 2);
                 }
             }
         }
@@ -805,7 +801,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const char *src = from + slot0 * 128 + ((ch ^ x) * 16);
                 char *dst0 = to + slot0 * 128 + (((j + (odd_first ? 1 : 0)) ^ x) * 16);
                 char *dst1 = to + slot0 * 128 + (((j + (odd_first ? 0 : 1)) ^ x) * 16);
-#pragma unroll 4
+#pragma unroll 2
                 for (int k = 0; k < rounds; ++k) {
                     uint4 w = *reinterpret_cast<const uint4 *>(src + k * per * 128);
                     if (k * per + slot0 >= here) w = make_uint4(0, 0, 0, 0);
