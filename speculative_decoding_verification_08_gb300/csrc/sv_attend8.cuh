@@ -115,19 +115,24 @@ struct __align__(16) Attend8Misc {
 };
 static_assert(sizeof(Attend8Misc) <= 7168, "misc region");
 
-// As hold() of the 16-bit kernel.
-template <uint64_t kLimitNs = kWaitLimitNs>
-__device__ __forceinline__ bool hold8(Attend8Shared &sh, unsigned long long *bar, uint32_t parity,
-                                      uint32_t *status) {
+// A wait that gives up for the whole CTA, as hold() of the 16-bit kernel; the kernel's
+// end reports it.  Every wait of every warp is a copy of this, and code that does not
+// fit the instruction cache costs a third of the time: 32 bits of the timer do.  (Short
+// waits give up after 0.25 s; long ones, which wait for whole pieces, count 2^32 ns: 24
+// of them are 103 s.)
+template <bool kLong = false>
+__device__ __forceinline__ bool hold8(Attend8Shared &sh, unsigned long long *bar, uint32_t parity) {
     if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
+    auto now = []() -> uint32_t {
+        uint32_t t;
+        if (kLong) asm volatile("mov.u32 %0, %%globaltimer_hi;" : "=r"(t));
+        else asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        return t;
+    };
+    const uint32_t t0 = now();
     while (!mbar_try(bar, parity)) {
+        if (now() - t0 > (kLong ? 24u : (uint32_t)kWaitLimitNs)) *(volatile int32_t *)&sh.dead = 1;
         if (*(volatile int32_t *)&sh.dead) return false;
-        if (global_ns() - t0 > kLimitNs) {
-            *(volatile int32_t *)&sh.dead = 1;
-            atomicOr(status, SV_STATUS_TIMEOUT);
-            return false;
-        }
     }
     return true;
 }
@@ -136,8 +141,8 @@ struct PieceReader8 {
     int k = 0;
     uint32_t turn = 0;
     // (all lanes) whether there is a piece; it is sh.pieces[k]
-    __device__ __forceinline__ bool next(Attend8Shared &sh, uint32_t *status) {
-        const bool ok = __all_sync(0xffffffffu, hold8(sh, &sh.piece_full[k], turn, status));
+    __device__ __forceinline__ bool next(Attend8Shared &sh) {
+        const bool ok = __all_sync(0xffffffffu, hold8(sh, &sh.piece_full[k], turn));
         return ok && sh.pieces[k].n >= 0;
     }
     __device__ __forceinline__ void done(Attend8Shared &sh, int lane) {
@@ -342,15 +347,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (tw == 0) {
                 Piece p;
                 if (!walk.next(A, p)) p.n = -1;
-                ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.piece_empty[k], (ready / kPieces & 1) ^ 1,
-                                                                  status));
+                ok = __all_sync(0xffffffffu, hold8<true>(sh, &sh.piece_empty[k], (ready / kPieces & 1) ^ 1));
                 if (ok && lane == 0) {
                     sh.pieces[k] = p;
                     mbar_arrive(&sh.piece_full[k]);
                 }
                 __syncwarp();
             }
-            ok = ok && __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.piece_full[k], ready / kPieces & 1, status));
+            ok = ok && __all_sync(0xffffffffu, hold8<true>(sh, &sh.piece_full[k], ready / kPieces & 1));
             if (group_any(3, !ok)) return false;
             const Piece &p = sh.pieces[k];
             if (p.n < 0) {
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             ++ready;
             if (p.n == 0) return true;
             const int qb = qn & 1;
-            ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.q_empty[qb], (qn >> 1 & 1) ^ 1, status));
+            ok = __all_sync(0xffffffffu, hold8<true>(sh, &sh.q_empty[qb], (qn >> 1 & 1) ^ 1));
             ++qn;
             // four values to a lane, rows tw, tw + 4, ... to a warp
             constexpr int kMine = kRows8 / 4;
@@ -417,8 +421,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const Piece &p = sh.pieces[done % kPieces];
             const uint32_t tb = done & 1, turn = done >> 1 & 1;
             const int blocks = p.n, row0 = p.row, rows = p.rows;
-            ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.state_full[tb], turn, status));
-            ok = ok && __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.o_full[tb], turn, status));
+            ok = __all_sync(0xffffffffu, hold8<true>(sh, &sh.state_full[tb], turn));
+            ok = ok && __all_sync(0xffffffffu, hold8<true>(sh, &sh.o_full[tb], turn));
             ok = !group_any(3, !ok);
             if (!ok) break;
             tc::fence_after();
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             int kn = 0, vn = 0;  // blocks copied so far
             PieceReader8 reader;
             bool ok = true;
-            while (ok && reader.next(sh, status)) {
+            while (ok && reader.next(sh)) {
                 const Piece &q = sh.pieces[reader.k];
                 const int blocks = q.n, lo = q.lo, end = q.end, h = q.h;
                 const int32_t *table = A.batch.pages + q.b * A.batch.pages_stride;
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         const int ring = of ? L::kRingV : kRing8, n = of ? vn : kn, st = n % ring;
                         unsigned long long *full = of ? &sh.v_full[st] : &sh.k_full[st];
                         unsigned long long *empty = of ? &sh.v_empty[st] : &sh.k_empty[st];
-                        ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, (n / ring & 1) ^ 1, status));
+                        ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, (n / ring & 1) ^ 1));
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(full, kRaw);
                         __syncwarp();
@@ -652,18 +656,18 @@ __global__ void __launch_bounds__(kThreads8, 1)
             uint32_t n = 0, qn = 0, used[2] = {0, 0};  // blocks, tiles, blocks of each group
             PieceReader8 reader;
             bool ok = true;  // a wait gave up: nothing more is issued or handed back
-            while (ok && reader.next(sh, status)) {
+            while (ok && reader.next(sh)) {
                 const int blocks = tc::uniform(sh.pieces[reader.k].n);
                 reader.done(sh, lane);
                 if (blocks == 0) continue;
                 const uint32_t qb = qn & 1;
-                ok = ok && __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.q_full[qb], (qn >> 1) & 1, status));
+                ok = ok && __all_sync(0xffffffffu, hold8<true>(sh, &sh.q_full[qb], (qn >> 1) & 1));
                 ++qn;
                 for (int i = 0; i < blocks && ok; ++i, ++n) {
                     const uint32_t st = n % kRing8, sb = i & 1;
                     const uint32_t turn = sb ? used[1]++ : used[0]++;
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.k_full[st], n / kRing8 & 1, status));
-                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.s_empty[sb], (turn & 1) ^ 1, status));
+                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.k_full[st], n / kRing8 & 1));
+                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.s_empty[sb], (turn & 1) ^ 1));
                     if (!ok) break;
                     tc::fence_after();
                     if (tc::elect()) {
@@ -689,16 +693,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
             uint32_t used[2] = {0, 0}, tile = 0;
             PieceReader8 reader;
             bool ok = true;
-            while (ok && reader.next(sh, status)) {
+            while (ok && reader.next(sh)) {
                 const int blocks = tc::uniform(sh.pieces[reader.k].n);
                 reader.done(sh, lane);
                 const uint32_t tb = tile & 1;
-                ok = __all_sync(0xffffffffu, hold8<kPieceLimitNs>(sh, &sh.o_empty[tb], (tile >> 1 & 1) ^ 1, status));
+                ok = __all_sync(0xffffffffu, hold8<true>(sh, &sh.o_empty[tb], (tile >> 1 & 1) ^ 1));
                 ++tile;
                 for (int i = 0; i < blocks && ok; ++i) {
                     const uint32_t b = i & 1, turn = (b ? used[1]++ : used[0]++) & 1;
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.vc_full[b], turn, status));
-                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.p_full[b], turn, status));
+                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.vc_full[b], turn));
+                    ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.p_full[b], turn));
                     if (!ok) break;
                     tc::fence_after();
                     if (tc::elect()) {
@@ -727,7 +731,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             uint32_t n = 0;
             PieceReader8 reader;
             bool ok = true;
-            while (ok && reader.next(sh, status)) {
+            while (ok && reader.next(sh)) {
                 const Piece &q = sh.pieces[reader.k];
                 const int blocks = q.n, lo = q.lo, end = q.end;
                 const int32_t *table = A.batch.pages + q.b * A.batch.pages_stride;
@@ -755,7 +759,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 for (int i = -1; i < blocks && ok; ++i) {
                     if (i >= 0) {
                         const uint32_t st = n % kScaleRing;
-                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[st], (n / kScaleRing & 1) ^ 1, status));
+                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[st], (n / kScaleRing & 1) ^ 1));
                         if (!ok) break;
                         *reinterpret_cast<uint32_t *>(&misc.scales[st][0][lane * 4]) = key;
                         *reinterpret_cast<uint32_t *>(&misc.scales[st][1][lane * 4]) = value;
@@ -782,7 +786,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         uint32_t n = 0, used[2] = {0, 0};
         PieceReader8 reader;
         bool ok = true;
-        while (ok && reader.next(sh, status)) {
+        while (ok && reader.next(sh)) {
             const int blocks = sh.pieces[reader.k].n;
             // slots from the tile's end on: whatever lies there, zeros
             const int end = sh.pieces[reader.k].end - sh.pieces[reader.k].lo * kKeys;
@@ -790,9 +794,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
             for (int i = 0; i < blocks && ok; ++i, ++n) {
                 const uint32_t st = n % L::kRingV, b = i & 1, turn = b ? used[1]++ : used[0]++;
                 const int here = end - i * kKeys;
-                ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[st], n / L::kRingV & 1, status));
+                ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[st], n / L::kRingV & 1));
                 if (ok && turn > 0)
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1, status));
+                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1));
                 if (!ok) break;
                 const char *from = smem + L::kV + st * kRaw;
                 char *to = smem + L::kVc + b * 2 * kRaw + (ch / 4) * kRaw;
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         PieceReader8 reader;
         for (;;) {
             // (all four warps go on, or none: they meet at barriers)
-            if (group_any(1 + g, !reader.next(sh, status))) break;
+            if (group_any(1 + g, !reader.next(sh))) break;
             const Piece &p = sh.pieces[reader.k];
             const int blocks = p.n, past = p.past, row0 = p.row, lo = p.lo, end = p.end;
             const int mine = (blocks + 1 - g) / 2;
@@ -846,7 +850,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const uint32_t tb = tile & 1;
             if (blocks > 0) {
                 const uint32_t qb = qn & 1;
-                hold8<kPieceLimitNs>(sh, &sh.q_full[qb], (qn >> 1) & 1, status);
+                hold8<true>(sh, &sh.q_full[qb], (qn >> 1) & 1);
                 ++qn;
                 const float q_factor = sh.q_factor[qb];
                 __syncwarp();
@@ -855,9 +859,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 for (int i = 0; i < mine; ++i, ++used) {
                     const int k0 = (lo + 2 * i + g) * kKeys;
                     const uint32_t n = n0 + 2 * i + g, sc = n % kScaleRing;
-                    hold8(sh, &sh.scale_full[sc], n / kScaleRing & 1, status);
+                    hold8(sh, &sh.scale_full[sc], n / kScaleRing & 1);
                     const uint32_t key_byte = misc.scales[sc][0][gt], value_byte = misc.scales[sc][1][gt];
-                    hold8(sh, &sh.s_full[g], used & 1, status);
+                    hold8(sh, &sh.s_full[g], used & 1);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.scale_empty[sc]);
                     tc::fence_after();
@@ -906,8 +910,75 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             }
                         }
                     };
-                    // scores relative to the references, and the largest of them
-                    auto relative = [&]() -> float {
+                    // (a byte of 255 is no scale: the vector is NaN; what lies behind the
+                    // tile's end is none either)
+                    const int e8 = value_byte == kScaleNan || k0 + gt >= end ? kNoScale : (int)value_byte - 127;
+                    // (once more, from tensor memory, where references grow; the first block
+                    // has none to begin with)
+                    for (bool rare = i == 0;; rare = true) {
+                        scores();
+                        if (__builtin_expect(rare, 0)) {
+                            // the rows' maxima over the block, and new references where they grew
+                            {
+                                float v[kMaxRows8];
+#pragma unroll
+                                for (int r = 0; r < kMaxRows8; ++r) v[r] = -INFINITY;
+#pragma unroll
+                                for (int r = 0; r < kRows8 / 2; ++r) unpair2(y[r], v[2 * r], v[2 * r + 1]);
+                                own.across[gw][lane] =
+                                    across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                            }
+                            const int largest = __reduce_max_sync(0xffffffffu, e8);
+                            if (lane == 0) own.exponent[gw] = largest;
+                            group_barrier(1 + g);
+                            float high = own.across[0][lane];
+                            int most = own.exponent[0];
+#pragma unroll
+                            for (int w = 1; w < 4; ++w) {
+                                high = fmaxf(high, own.across[w][lane]);
+                                most = max(most, own.exponent[w]);
+                            }
+                            // (one more, so that the next larger scale is no new reference)
+                            const int now_e = most > exponent ? most + 1 : exponent;
+                            const bool grow = high + minus > kRescaleAbove;
+                            const float now = grow ? -high : minus;
+                            const float f = !grow ? 1.f : minus == kUnset ? 0.f : ex2(now - minus);
+                            const float fe = exponent == kNoScale ? 0.f : ex2((float)(exponent - now_e));
+                            const bool scaled = __any_sync(0xffffffffu, grow && minus != kUnset) || now_e != exponent;
+                            exponent = now_e;
+                            minus = now;
+                            if (gw == 0) {
+                                own.minus[lane] = now;
+                                own.factor[lane] = f;
+                            }
+                            group_barrier(1 + g);
+                            if (i > 0) {
+#pragma unroll
+                                for (int o = 0; o < kRows8 / 4; ++o) {
+                                    const float4 m = *reinterpret_cast<const float4 *>(&own.factor[o * 4]);
+                                    sums[2 * o] = mul2(sums[2 * o], pair2(m.x, m.y));
+                                    sums[2 * o + 1] = mul2(sums[2 * o + 1], pair2(m.z, m.w));
+                                }
+                                if (scaled) {
+                                    hold8(sh, &sh.pv_done[g], (used - 1) & 1);
+                                    __syncwarp();
+                                    tc::fence_after();
+#pragma unroll 1
+                                    for (int part = 0; part < L::kOutCols / 8; ++part) {
+                                        uint32_t o[8];
+                                        tc::ld8(o, t_o + part * 8);
+                                        tc::wait_ld();
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e)
+                                            o[e] = __float_as_uint(__uint_as_float(o[e]) *
+                                                                   (own.factor[part * 8 + e] * fe));
+                                        tc::st8(t_o + part * 8, o);
+                                    }
+                                    tc::wait_st();
+                                }
+                            }
+                        }
+                        // scores relative to the references, and the largest of them
                         float top = -INFINITY;
 #pragma unroll
                         for (int o = 0; o < kRows8 / 4; ++o) {
@@ -920,77 +991,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             unpair2(y[2 * o + 1], a, b);
                             top = max3(top, a, b);
                         }
-                        return top;
-                    };
-                    // (a byte of 255 is no scale: the vector is NaN; what lies behind the
-                    // tile's end is none either)
-                    const int e8 = value_byte == kScaleNan || k0 + gt >= end ? kNoScale : (int)value_byte - 127;
-                    scores();
-                    bool rare = true;
-                    if (i > 0) {
-                        const float top = relative();
-                        rare = group_any(1 + g, top > kRescaleAbove || e8 > exponent);
-                    }
-                    if (__builtin_expect(rare, 0)) {
-                        // the rows' maxima over the block, and new references where they grew
-                        if (i > 0) scores();
-                        {
-                            float v[kMaxRows8];
-#pragma unroll
-                            for (int r = 0; r < kMaxRows8; ++r) v[r] = -INFINITY;
-#pragma unroll
-                            for (int r = 0; r < kRows8 / 2; ++r) unpair2(y[r], v[2 * r], v[2 * r + 1]);
-                            own.across[gw][lane] = across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
-                        }
-                        const int largest = __reduce_max_sync(0xffffffffu, e8);
-                        if (lane == 0) own.exponent[gw] = largest;
-                        group_barrier(1 + g);
-                        float high = own.across[0][lane];
-                        int most = own.exponent[0];
-#pragma unroll
-                        for (int w = 1; w < 4; ++w) {
-                            high = fmaxf(high, own.across[w][lane]);
-                            most = max(most, own.exponent[w]);
-                        }
-                        // (one more, so that the next larger scale is no new reference)
-                        const int now_e = most > exponent ? most + 1 : exponent;
-                        const bool grow = high + minus > kRescaleAbove;
-                        const float now = grow ? -high : minus;
-                        const float f = !grow ? 1.f : minus == kUnset ? 0.f : ex2(now - minus);
-                        const float fe = exponent == kNoScale ? 0.f : ex2((float)(exponent - now_e));
-                        const bool scaled = __any_sync(0xffffffffu, grow && minus != kUnset) || now_e != exponent;
-                        exponent = now_e;
-                        minus = now;
-                        if (gw == 0) {
-                            own.minus[lane] = now;
-                            own.factor[lane] = f;
-                        }
-                        group_barrier(1 + g);
-                        if (i > 0) {
-#pragma unroll
-                            for (int o = 0; o < kRows8 / 4; ++o) {
-                                const float4 m = *reinterpret_cast<const float4 *>(&own.factor[o * 4]);
-                                sums[2 * o] = mul2(sums[2 * o], pair2(m.x, m.y));
-                                sums[2 * o + 1] = mul2(sums[2 * o + 1], pair2(m.z, m.w));
-                            }
-                            if (scaled) {
-                                hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
-                                __syncwarp();
-                                tc::fence_after();
-#pragma unroll 1
-                                for (int half = 0; half < L::kOutCols / 16; ++half) {
-                                    uint32_t o[16];
-                                    tc::ld16(o, t_o + half * 16);
-                                    tc::wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * (own.factor[half * 16 + e] * fe));
-                                    tc::st16(t_o + half * 16, o);
-                                }
-                                tc::wait_st();
-                            }
-                        }
-                        relative();
+                        if (rare || !group_any(1 + g, top > kRescaleAbove || e8 > exponent)) break;
                     }
                     tc::fence_before();
                     __syncwarp();
@@ -1000,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const float value_scale = shift < -126 ? 0.f : power_of_two(shift);
                     const uint64_t value_scale2 = pair2(value_scale, value_scale);
                     const bool any_nan = __any_sync(0xffffffffu, value_byte == kScaleNan);
-                    if (used > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1, status);
+                    if (used > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1);
                     __syncwarp();
                     char *row = smem + L::kP + g * kRaw + gt * 128;
 #pragma unroll
@@ -1038,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                 for (int r = 0; r < kRows8 / 2; ++r) unpair2(sums[r], v[2 * r], v[2 * r + 1]);
                 const float sum = across_lanes(v, lane, [](float a, float b) { return a + b; });
-                hold8<kPieceLimitNs>(sh, &sh.state_empty[tb], (tile >> 1 & 1) ^ 1, status);
+                hold8<true>(sh, &sh.state_empty[tb], (tile >> 1 & 1) ^ 1);
                 TileState &st = misc.tile[tb];
                 st.sums[g][gw][lane] = sum;
                 if (gw == 0) {
@@ -1053,6 +1054,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
     tc::fence_before();
     __syncthreads();
+    if (tid == 0 && sh.dead) atomicOr(status, SV_STATUS_TIMEOUT);
     if (warp == 13) {
         __syncwarp();
         tc::tmem_free(tmem, L::kCols);
