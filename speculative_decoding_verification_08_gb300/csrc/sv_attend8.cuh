@@ -51,7 +51,7 @@ constexpr int kSoftmaxRegs8 = 136, kValueRegs8 = 56, kIssueRegs8 = 56, kTileRegs
 static_assert(128 * (2 * kSoftmaxRegs8 + kValueRegs8 + kIssueRegs8 + kTileRegs8) <= kThreads8 * 96, "register split");
 constexpr int kRaw = kKeys * 128;     // a block of codes
 constexpr int kRing8 = 3;             // blocks of keys in flight
-constexpr int kScaleRing = 4;         // blocks of scales
+constexpr int kScaleRing = 3;         // pairs of blocks of scales
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
 constexpr int kNoScale = -200;        // below every e8m0 exponent
 
@@ -111,7 +111,7 @@ struct __align__(16) Attend8Misc {
     Attend8Shared sh;
     GroupState group[2];
     TileState tile[2];
-    uint8_t scales[kScaleRing][2][kKeys];  // of keys and values
+    uint8_t scales[kScaleRing][2][2 * kKeys];  // of keys and values
 };
 static_assert(sizeof(Attend8Misc) <= 7168, "misc region");
 
@@ -136,6 +136,19 @@ __device__ __forceinline__ bool hold8(Attend8Shared &sh, unsigned long long *bar
     }
     return true;
 }
+
+// Where a warp is in a ring of stages.
+template <int kStages>
+struct RingPlace {
+    int st = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == kStages) {
+            st = 0;
+            turn ^= 1;
+        }
+    }
+};
 
 struct PieceReader8 {
     int k = 0;
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         for (int i = 0; i < kScaleRing; ++i) {
             mbar_init(&sh.scale_full[i], 1);
-            mbar_init(&sh.scale_empty[i], 4);
+            mbar_init(&sh.scale_empty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -591,7 +604,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
             // ---- copies of codes ------------------------------------------------
             const int boxes = kKeys / A.piece;
             const bool active = lane < boxes;
-            int kn = 0, vn = 0;  // blocks copied so far
+            RingPlace<kRing8> kp;
+            RingPlace<L::kRingV> vp;
+            int kn = 0, vn = 0;  // blocks copied so far, as far as a ring goes
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh)) {
@@ -601,9 +616,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const int first = A.window > 0 ? q.past + A.by_group.div(q.row) - A.window + 1 : 0;
                 reader.done(sh, lane);
                 if (blocks == 0) continue;
-                auto page_of = [&](int i) -> int {
-                    const int s0 = (lo + i) * kKeys + lane * A.piece;
-                    if (!active || i >= blocks || s0 >= end || s0 + A.piece <= first) return kNoPage;
+                // page ids of 32 boxes at a time, the next ones on their way
+                auto pages_of = [&](int box) -> int {
+                    const int s0 = lo * kKeys + (box + lane) * A.piece;
+                    if (s0 >= min(end, (lo + blocks) * kKeys) || s0 + A.piece <= first) return kNoPage;
                     return __ldg(table + A.by_page.div(s0));
                 };
                 auto checked = [&](int id) -> int {
@@ -613,20 +629,25 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     return id;
                 };
-                // keys run a block ahead of values, page ids two blocks ahead of keys
-                int id0 = kNoPage, id1 = page_of(0), id2 = page_of(1);
+                // keys run a block ahead of values
+                int ids = 0, next_ids = pages_of(0), key_id = kNoPage, value_id;
 #pragma unroll 1
                 for (int i = -1; i < blocks && ok; ++i) {
-                    const int id3 = page_of(i + 3);
-                    id1 = checked(id1);
+                    const int box = (i + 1) * boxes;
+                    if (box % 32 == 0) {
+                        ids = next_ids;
+                        next_ids = pages_of(box + 32);
+                    }
+                    value_id = key_id;
+                    key_id = checked(__shfl_sync(0xffffffffu, ids, box % 32 + lane % boxes));
 #pragma unroll 1
                     for (int of = 0; of < 2; ++of) {  // keys of block i + 1, values of block i
                         const int x = of ? i : i + 1;
                         if (x < 0 || x >= blocks) continue;
-                        const int ring = of ? L::kRingV : kRing8, n = of ? vn : kn, st = n % ring;
+                        const int st = of ? vp.st : kp.st;
                         unsigned long long *full = of ? &sh.v_full[st] : &sh.k_full[st];
                         unsigned long long *empty = of ? &sh.v_empty[st] : &sh.k_empty[st];
-                        ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, (n / ring & 1) ^ 1));
+                        ok = ok && __all_sync(0xffffffffu, hold8(sh, empty, (of ? vp.turn : kp.turn) ^ 1));
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(full, kRaw);
                         __syncwarp();
@@ -634,26 +655,30 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             const int s0 = (lo + x) * kKeys + lane * A.piece;
                             tc::load_box(smem + (of ? L::kV : L::kK) + st * kRaw + lane * A.piece * 128,
                                          of ? &vmap : &kmap, 0, h, s0 - A.by_page.div(s0) * A.batch.page_size,
-                                         of ? id0 : id1, full);
+                                         of ? value_id : key_id, full);
                         }
-                        if (of) ++vn;
-                        else ++kn;
+                        if (of) vp.next(), vn = min(vn + 1, L::kRingV);
+                        else kp.next(), kn = min(kn + 1, kRing8);
                     }
-                    id0 = id1;
-                    id1 = id2;
-                    id2 = id3;
                 }
             }
             // the last copies have landed before the CTA may end
-            for (int n = max(0, kn - kRing8); n < kn; ++n) mbar_wait(&sh.k_full[n % kRing8], n / kRing8 & 1);
-            for (int n = max(0, vn - L::kRingV); n < vn; ++n) mbar_wait(&sh.v_full[n % L::kRingV], n / L::kRingV & 1);
+            for (int n = 0; n < kn; ++n) {  // (stages from kp.st on are the turn before)
+                const int st = (kp.st + kRing8 - 1 - n) % kRing8;
+                mbar_wait(&sh.k_full[st], st < kp.st ? kp.turn : kp.turn ^ 1);
+            }
+            for (int n = 0; n < vn; ++n) {
+                const int st = (vp.st + L::kRingV - 1 - n) % L::kRingV;
+                mbar_wait(&sh.v_full[st], st < vp.st ? vp.turn : vp.turn ^ 1);
+            }
         } else if (warp == 13) {
             // ---- scores ---------------------------------------------------------
             const uint32_t tm = (uint32_t)tc::uniform((int)tmem);
             const uint64_t k_desc = tc::smem_desc(smem_u32(smem + L::kK), 16, 1024);
             const uint64_t q_desc = tc::smem_desc(smem_u32(smem + L::kQ), 16, 1024);
             const int steps = (D + 31) / 32;
-            uint32_t n = 0, qn = 0, used[2] = {0, 0};  // blocks, tiles, blocks of each group
+            uint32_t qn = 0, used[2] = {0, 0};  // tiles, blocks of each group
+            RingPlace<kRing8> at;
             PieceReader8 reader;
             bool ok = true;  // a wait gave up: nothing more is issued or handed back
             while (ok && reader.next(sh)) {
@@ -663,10 +688,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const uint32_t qb = qn & 1;
                 ok = ok && __all_sync(0xffffffffu, hold8<true>(sh, &sh.q_full[qb], (qn >> 1) & 1));
                 ++qn;
-                for (int i = 0; i < blocks && ok; ++i, ++n) {
-                    const uint32_t st = n % kRing8, sb = i & 1;
+                for (int i = 0; i < blocks && ok; ++i, at.next()) {
+                    const uint32_t st = at.st, sb = i & 1;
                     const uint32_t turn = sb ? used[1]++ : used[0]++;
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.k_full[st], n / kRing8 & 1));
+                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.k_full[st], at.turn));
                     ok = ok && __all_sync(0xffffffffu, hold8(sh, &sh.s_empty[sb], (turn & 1) ^ 1));
                     if (!ok) break;
                     tc::fence_after();
@@ -722,53 +747,51 @@ __global__ void __launch_bounds__(kThreads8, 1)
             __syncwarp();
             mbar_wait(&sh.drain[1], 0);
         } else {
-            // ---- scales: four slots to a lane ------------------------------------
+            // ---- scales of two blocks at a time, eight slots to a lane ---------------
             const Scales &S = P8.scales;
-            // four bytes at once where they lie so
-            const bool k4 = S.k_st[1] == 1 && ((reinterpret_cast<uintptr_t>(S.k) | S.k_st[0] | S.k_st[2]) & 3) == 0;
-            const bool v4 = S.v_st[1] == 1 && ((reinterpret_cast<uintptr_t>(S.v) | S.v_st[0] | S.v_st[2]) & 3) == 0;
-            constexpr uint32_t kNone = (127 + kMinScale) * 0x01010101u;  // no page, no codes
-            uint32_t n = 0;
+            RingPlace<kScaleRing> at;
             PieceReader8 reader;
             bool ok = true;
             while (ok && reader.next(sh)) {
                 const Piece &q = sh.pieces[reader.k];
-                const int blocks = q.n, lo = q.lo, end = q.end;
+                const int pairs = (q.n + 1) / 2, begin = q.lo * kKeys + lane * 8, end = min(q.end, (q.lo + q.n) * kKeys);
                 const int32_t *table = A.batch.pages + q.b * A.batch.pages_stride;
                 const int first = A.window > 0 ? q.past + A.by_group.div(q.row) - A.window + 1 : 0;
                 const uint8_t *ks = S.k + q.h * S.k_st[2], *vs = S.v + q.h * S.v_st[2];
                 reader.done(sh, lane);
                 auto page_of = [&](int i) -> int {
-                    const int s0 = (lo + i) * kKeys + lane * 4;
-                    return i >= blocks || s0 >= end || s0 + 4 <= first ? -1 : __ldg(table + A.by_page.div(s0));
+                    const int s0 = begin + i * 2 * kKeys;
+                    return i >= pairs || s0 >= end || s0 + 8 <= first ? -1 : __ldg(table + A.by_page.div(s0));
                 };
-                auto four = [&](const uint8_t *base, const int64_t *st, bool at_once, int i, int id) -> uint32_t {
-                    if (id < 0 || id >= A.batch.num_pages) return kNone;
-                    const int s0 = (lo + i) * kKeys + lane * 4;
-                    const uint8_t *at = base + id * st[0] + (s0 - A.by_page.div(s0) * A.batch.page_size) * st[1];
-                    if (at_once) return __ldg(reinterpret_cast<const uint32_t *>(at));
-                    uint32_t x = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e, at += st[1]) x |= (uint32_t)__ldg(at) << (8 * e);
-                    return x;
-                };
-                // a block's bytes are loaded a block ahead of their use, its page ids two
-                uint32_t key = 0, value = 0;
+                // bytes are loaded a pair ahead of their use (and put together then), page
+                // ids two
+                uint32_t key[8], value[8];
                 int id = page_of(0);
 #pragma unroll 1
-                for (int i = -1; i < blocks && ok; ++i) {
+                for (int i = -1; i < pairs; ++i) {
                     if (i >= 0) {
-                        const uint32_t st = n % kScaleRing;
-                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[st], (n / kScaleRing & 1) ^ 1));
+                        ok = __all_sync(0xffffffffu, hold8(sh, &sh.scale_empty[at.st], at.turn ^ 1));
                         if (!ok) break;
-                        *reinterpret_cast<uint32_t *>(&misc.scales[st][0][lane * 4]) = key;
-                        *reinterpret_cast<uint32_t *>(&misc.scales[st][1][lane * 4]) = value;
+                        auto four = [](const uint32_t *x) { return x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24; };
+                        *reinterpret_cast<uint2 *>(&misc.scales[at.st][0][lane * 8]) = make_uint2(four(key), four(key + 4));
+                        *reinterpret_cast<uint2 *>(&misc.scales[at.st][1][lane * 8]) =
+                            make_uint2(four(value), four(value + 4));
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.scale_full[st]);
-                        ++n;
+                        if (lane == 0) mbar_arrive(&sh.scale_full[at.st]);
+                        at.next();
                     }
-                    key = four(ks, S.k_st, k4, i + 1, id);
-                    value = four(vs, S.v_st, v4, i + 1, id);
+                    const int s0 = begin + (i + 1) * 2 * kKeys;
+                    const int64_t in = s0 - A.by_page.div(s0) * A.batch.page_size;
+                    const bool known = id >= 0 && id < A.batch.num_pages;
+                    const uint8_t *k = ks + id * S.k_st[0] + in * S.k_st[1], *v = vs + id * S.v_st[0] + in * S.v_st[1];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        key[e] = value[e] = 127 + kMinScale;  // no page, no codes
+                        if (known) {
+                            key[e] = __ldg(k + e * S.k_st[1]);
+                            value[e] = __ldg(v + e * S.v_st[1]);
+                        }
+                    }
                     id = page_of(i + 2);
                 }
             }
@@ -782,46 +805,53 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const int ch = wide ? t % 8 : t % 4, u = t / 4;
         const int slot0 = wide ? t / 8 : (u >> 3) * 8 + ((u & 1) << 2) + ((u >> 1) & 3);
         const int rounds = wide ? 8 : 4, per = wide ? 16 : 32;
+        // (lanes of the upper half, or of odd slots, write their second eight values first)
         const bool odd_first = wide ? ch >= 4 : u & 1;
-        uint32_t n = 0, used[2] = {0, 0};
+        // (per is a multiple of 8: all of a thread's slots share their place in a swizzle)
+        const int x = slot0 & 7, j = (ch % 4) * 2;
+        const int src = slot0 * 128 + ((ch ^ x) * 16), dst = (ch / 4) * kRaw + slot0 * 128;
+        const int first = dst + (((j + (odd_first ? 1 : 0)) ^ x) * 16);
+        const int second = dst + (((j + (odd_first ? 0 : 1)) ^ x) * 16);
+        uint32_t used[2] = {0, 0};
+        RingPlace<L::kRingV> at;
         PieceReader8 reader;
         bool ok = true;
         while (ok && reader.next(sh)) {
             const int blocks = sh.pieces[reader.k].n;
-            // slots from the tile's end on: whatever lies there, zeros
             const int end = sh.pieces[reader.k].end - sh.pieces[reader.k].lo * kKeys;
             reader.done(sh, lane);
-            for (int i = 0; i < blocks && ok; ++i, ++n) {
-                const uint32_t st = n % L::kRingV, b = i & 1, turn = b ? used[1]++ : used[0]++;
-                const int here = end - i * kKeys;
-                ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[st], n / L::kRingV & 1));
-                if (ok && turn > 0)
-                    ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1));
+            for (int i = 0; i < blocks && ok; ++i, at.next()) {
+                const uint32_t b = i & 1, turn = b ? used[1]++ : used[0]++;
+                ok = __all_sync(0xffffffffu, hold8(sh, &sh.v_full[at.st], at.turn));
+                if (ok && turn > 0) ok = __all_sync(0xffffffffu, hold8(sh, &sh.pv_done[b], (turn - 1) & 1));
                 if (!ok) break;
-                const char *from = smem + L::kV + st * kRaw;
-                char *to = smem + L::kVc + b * 2 * kRaw + (ch / 4) * kRaw;
-                // (per is a multiple of 8: all of a thread's slots share their place in a swizzle)
-                const int x = slot0 & 7, j = (ch % 4) * 2;
-                const char *src = from + slot0 * 128 + ((ch ^ x) * 16);
-                char *dst0 = to + slot0 * 128 + (((j + (odd_first ? 1 : 0)) ^ x) * 16);
-                char *dst1 = to + slot0 * 128 + (((j + (odd_first ? 0 : 1)) ^ x) * 16);
-#pragma unroll 2
+                char *raw = smem + L::kV + at.st * kRaw, *to = smem + L::kVc + b * 2 * kRaw;
+                const int here = end - i * kKeys;
+                if (here < kKeys) {
+                    // slots from the tile's end on: whatever lies there, zeros
+#pragma unroll 1
+                    for (int k = 0; k < rounds; ++k)
+                        if (k * per + slot0 >= here)
+                            *reinterpret_cast<uint4 *>(raw + src + k * per * 128) = make_uint4(0, 0, 0, 0);
+                }
+                // (not unrolled: 317 us for rounds of 6 tokens over up to 4096 slots, 333 by
+                // four, 391 by eight, for the instruction cache's sake)
+#pragma unroll 1
                 for (int k = 0; k < rounds; ++k) {
-                    uint4 w = *reinterpret_cast<const uint4 *>(src + k * per * 128);
-                    if (k * per + slot0 >= here) w = make_uint4(0, 0, 0, 0);
-                    uint4 lo, hi;
-                    codes_to_half(w.x, lo.x, lo.y);
-                    codes_to_half(w.y, lo.z, lo.w);
-                    codes_to_half(w.z, hi.x, hi.y);
-                    codes_to_half(w.w, hi.z, hi.w);
-                    *reinterpret_cast<uint4 *>(dst0 + k * per * 128) = odd_first ? hi : lo;
-                    *reinterpret_cast<uint4 *>(dst1 + k * per * 128) = odd_first ? lo : hi;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(raw + src + k * per * 128);
+                    uint4 y, z;
+                    codes_to_half(odd_first ? w.z : w.x, y.x, y.y);
+                    codes_to_half(odd_first ? w.w : w.y, y.z, y.w);
+                    codes_to_half(odd_first ? w.x : w.z, z.x, z.y);
+                    codes_to_half(odd_first ? w.y : w.w, z.z, z.w);
+                    *reinterpret_cast<uint4 *>(to + first + k * per * 128) = y;
+                    *reinterpret_cast<uint4 *>(to + second + k * per * 128) = z;
                 }
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&sh.vc_full[b]);
-                    mbar_arrive(&sh.v_empty[st]);
+                    mbar_arrive(&sh.v_empty[at.st]);
                 }
             }
         }
@@ -832,7 +862,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         const uint32_t lanes_at = tmem + ((uint32_t)(gw * 32) << 16);
         const uint32_t t_s = lanes_at + g * L::kScoreCols;
         GroupState &own = misc.group[g];
-        uint32_t used = 0, n0 = 0, qn = 0, tile = 0;  // the group's blocks, all blocks, tiles
+        uint32_t used = 0, qn = 0, tile = 0;  // the group's blocks, tiles with queries, tiles
+        RingPlace<kScaleRing> sc;
         PieceReader8 reader;
         for (;;) {
             // (all four warps go on, or none: they meet at barriers)
@@ -858,12 +889,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const uint32_t t_o = lanes_at + L::kOut + (tb * 2 + g) * L::kOutCols;
                 for (int i = 0; i < mine; ++i, ++used) {
                     const int k0 = (lo + 2 * i + g) * kKeys;
-                    const uint32_t n = n0 + 2 * i + g, sc = n % kScaleRing;
-                    hold8(sh, &sh.scale_full[sc], n / kScaleRing & 1);
-                    const uint32_t key_byte = misc.scales[sc][0][gt], value_byte = misc.scales[sc][1][gt];
+                    hold8(sh, &sh.scale_full[sc.st], sc.turn);
+                    const uint32_t key_byte = misc.scales[sc.st][0][g * kKeys + gt],
+                                   value_byte = misc.scales[sc.st][1][g * kKeys + gt];
                     hold8(sh, &sh.s_full[g], used & 1);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.scale_empty[sc]);
+                    if (lane == 0) mbar_arrive(&sh.scale_empty[sc.st]);
+                    sc.next();
                     tc::fence_after();
                     uint64_t y[kRows8 / 2];  // of rows 2 r and 2 r + 1
                     const float key_scale = q_factor * scale_of(key_byte);
@@ -1029,7 +1061,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.p_full[g]);
                 }
-                n0 += blocks;
+                if (g == 1 && (blocks & 1)) {  // a last pair's second block that there is none of
+                    if (lane == 0) mbar_arrive(&sh.scale_empty[sc.st]);
+                    sc.next();
+                }
             }
             // the tile's state, for the warps that finish it
             {
