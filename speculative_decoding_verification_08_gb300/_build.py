@@ -21,6 +21,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, "sv_device.cuh"), os.path.join(CSRC, "sv
                      os.path.join(CSRC, "sv_cache.cuh"), os.path.join(CSRC, "sv_append.cuh"),
                      os.path.join(CSRC, "sv_append8.cuh"), os.path.join(CSRC, "sv_attend8.cuh"),
                      os.path.join(CSRC, "sv_cache_host.cuh"),
+                     os.path.join(CSRC, "sv_pairs.cuh"),
                      os.path.join(CSRC, "sv_attend.cuh"), os.path.join(CSRC, "sv_warp.cuh"),
                      os.path.join(CSRC, "sv_tc.cuh"), os.path.join(CSRC, "sv_barrier.cuh"),
                      os.path.join(INCLUDE, "specverify.h")]

@@ -79,10 +79,10 @@ template <class T, bool kEight>
 int launch_append(const sv::AppendNormParams &A, bool interleaved, cudaStream_t st) {
     const int rot = A.a.rot_dim;
     int lanes = 1;
-    while (lanes * 8 < A.a.head_dim) lanes *= 2;
+    while (lanes * 16 < A.a.head_dim) lanes *= 2;
     const int tokens = A.a.batch.tokens;
     const int per_block = (int)std::min<int64_t>(
-        sv::kAppendTokens, std::max<int64_t>(1, ((int64_t)tokens + kSms * 4 - 1) / (kSms * 4)));
+        sv::kNormTokens, std::max<int64_t>(1, ((int64_t)tokens + kSms * 4 - 1) / (kSms * 4)));
     const unsigned grid = (unsigned)((tokens + per_block - 1) / per_block);
     // as many warps as share a token's vectors evenly
     const int vectors = A.a.q_heads + 2 * A.a.kv_heads, per_warp = 32 / lanes;

@@ -10,12 +10,16 @@
 // code times scale is exact in bf16 and fp32.  A vector with a NaN or an infinity
 // has the scale NaN (255) and codes of zero.
 //
-// Bound by memory: a group of lanes (a power of two, 8 values each) holds a
-// head's vector in registers, so that sums and maxima are a few shuffles and the
-// turn's other half is a second load of the same lines.
+// Bound by memory: a group of lanes (a power of two, 16 values each) holds a head's
+// vector in registers, a pair's two values in one lane wherever pairs start on packs of
+// 8, so that sums and maxima are a few shuffles and nothing is loaded twice.  Angles
+// are fixed-point: a frequency in turns as a 64-bit fraction, once a block (fp64 runs at
+// 1/64 of fp32 here), so that position times frequency modulo a turn is one integer
+// product, good to 2^-33 of a turn at any position.
 #pragma once
 
 #include "sv_append.cuh"
+#include "sv_pairs.cuh"
 
 namespace sv {
 
@@ -72,13 +76,14 @@ struct RowPlace {
     int64_t k, v;     // offsets into the caches; -1: nowhere
     int64_t ks, vs;   // into the scales
     int32_t known;    // the row is one of a sequence that fits
+    int32_t position;
 };
 
 // Row t of the token arrays: its slot's places, by a whole warp.  pos: its slot.
 __device__ __forceinline__ RowPlace place_of(const Batch &A, const FastDiv &by_page, const int64_t *kc_st,
                                              const int64_t *vc_st, const Scales &S, int32_t t, int64_t &pos,
                                              int lane) {
-    RowPlace p = {-1, -1, -1, -1, 0};
+    RowPlace p = {-1, -1, -1, -1, 0, 0};
     pos = 0;
     const int32_t b = find_sequence(A.q_start, A.B, t, lane);
     if (b < 0) return p;
@@ -111,34 +116,36 @@ __device__ __forceinline__ RowPlace place_of(const Batch &A, const FastDiv &by_p
 
 // ---- append ----------------------------------------------------------------------
 
+constexpr int kNormTokens = 8;  // tokens per block at most
+
+// How pairs lie.  kPackTurn: both halves start on a pack (rot_dim a multiple of 16) and
+// lane l < rot_dim / 16 has packs l of both; kAdjacentTurn: within a pack (or nothing
+// turns); kPairTurn: a pair's other value is loaded beside the lane's own.
 enum Turning { kPackTurn, kPairTurn, kAdjacentTurn };
 
+// A pack's eight values as four pairs of floats.
 template <class T>
-__device__ __forceinline__ void unpack(const Pack<8> &p, float (&y)[8]) {
+__device__ __forceinline__ void unpack(const Pack<8> &p, uint64_t (&y)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 f = pair_of(p.x[e], T());
-        y[2 * e] = f.x;
-        y[2 * e + 1] = f.y;
+        y[e] = pair2(f.x, f.y);
     }
 }
 
-// Weights of the eight values at `at`.
+// Weights i and i + 1.
 template <class T>
-__device__ __forceinline__ void weights_at(const void *w, bool f32, int at, float (&y)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        y[e] = f32 ? __ldg(static_cast<const float *>(w) + at + e) : to_f32<T>(static_cast<const T *>(w)[at + e]);
+__device__ __forceinline__ uint64_t weights_at(const void *w, bool f32, int i) {
+    return f32 ? pair2(__ldg(static_cast<const float *>(w) + i), __ldg(static_cast<const float *>(w) + i + 1))
+               : pair2(to_f32<T>(static_cast<const T *>(w)[i]), to_f32<T>(static_cast<const T *>(w)[i + 1]));
 }
 
-// kTurn: how a pair's other value comes.  kPackTurn: both halves of the pairs start
-// on a pack (rot_dim a multiple of 16): one 16-byte load; kPairTurn: four loads of
-// two; kAdjacentTurn: it lies in the same pack (also where nothing turns).
 template <class T, bool kEight, Turning kTurn>
-__global__ void __launch_bounds__(kAppendThreads, 2)
+__global__ void __launch_bounds__(kAppendThreads, kTurn == kPairTurn ? 2 : 3)
     append_norm_kernel(const __grid_constant__ AppendNormParams A, int per_block, int lanes) {
-    __shared__ RowPlace place[kAppendTokens];
-    __shared__ __align__(16) float2 cs[kAppendTokens][kMaxHeadDim / 2];
+    __shared__ RowPlace place[kNormTokens];
+    __shared__ __align__(16) float cosines[kNormTokens][kMaxHeadDim / 2], sines[kNormTokens][kMaxHeadDim / 2];
+    __shared__ uint64_t turn_of[kMaxHeadDim / 2];
     typedef Pack<8> P;
     const AppendParams &a = A.a;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -146,148 +153,226 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
     const int here = min(per_block, a.batch.tokens - t0);
     const int half = a.rot_dim / 2;
 
+    // `lanes` lanes to a vector, a warp's vectors side by side; each lane's two packs
+    const int sub = lane % lanes;
+    const bool pairs = kTurn == kPackTurn && sub * 16 < a.rot_dim;
+    const int at0 = pairs ? sub * 8 : sub * 16, at1 = pairs ? half + at0 : at0 + 8;
+    const bool in0 = at0 < a.head_dim, in1 = at1 < a.head_dim;
+    const int per_warp = 32 / lanes, stride = (int)blockDim.x / 32 * per_warp;
+    const int vectors = a.q_heads + 2 * a.kv_heads;
+
     wait_for_primary_grid();
+    for (int e = threadIdx.x; e < half; e += (int)blockDim.x) {
+        const double turns = __ldg(a.inv_freq + e) * 0.15915494309189535;
+        turn_of[e] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+    }
     for (int w = warp; w < here; w += (int)blockDim.x / 32) {
-        int64_t pos;
-        const RowPlace p = place_of(a.batch, a.by_page, a.kc_st, a.vc_st, A.scales, t0 + w, pos, lane);
+        int64_t slot;
+        RowPlace p = place_of(a.batch, a.by_page, a.kc_st, a.vc_st, A.scales, t0 + w, slot, lane);
+        p.position = a.positions ? __ldg(a.positions + t0 + w) : (int32_t)slot;
         if (lane == 0) place[w] = p;
-        if (p.known) {
-            if (a.positions) pos = (int64_t)__ldg(a.positions + t0 + w);
-            for (int e = lane; e < half; e += 32) {
-                const double turns = (double)pos * __ldg(a.inv_freq + e) * 0.15915494309189535;
-                float s, co;
-                sincospif((float)(2.0 * (turns - rint(turns))), &s, &co);
-                cs[w][e] = make_float2(co, s);
-            }
-        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < here * half; i += (int)blockDim.x) {
+        const int w = i / half, e = i - w * half;
+        const uint64_t turns = (uint64_t)(int64_t)place[w].position * turn_of[e];
+        float s, c;
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+        cosines[w][e] = c;
+        sines[w][e] = s;
     }
     __syncthreads();
 
-    // `lanes` lanes to a vector; a warp's vectors side by side
-    const int sub = lane % lanes, at = sub * 8;
-    const bool inside = at < a.head_dim;
-    const int per_warp = 32 / lanes;
-    const int vectors = a.q_heads + 2 * a.kv_heads;
-    for (int first = warp * per_warp; first < vectors; first += (int)blockDim.x / 32 * per_warp) {
+    const bool any_norm = A.q_norm || A.k_norm;
+    const float inv_dim = 1.f / (float)a.head_dim;
+    int weights_of = -1;
+    uint64_t w0[4], w1[4], z0[4], z1[4];  // norms of the lane's values, and of their others
+    for (int first = warp * per_warp; first < vectors; first += stride) {
         const int i = first + lane / lanes;
-        const bool active = i < vectors && inside;
+        const bool active = i < vectors;
         const int kind = i < a.q_heads ? 0 : i < a.q_heads + a.kv_heads ? 1 : 2;
         const int head = i - (kind == 0 ? 0 : kind == 1 ? a.q_heads : a.q_heads + a.kv_heads);
-        const int64_t *st = kind == 0 ? a.q_st : kind == 1 ? a.k_st : a.v_st;
-        const uint16_t *src = static_cast<const uint16_t *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                              t0 * st[0] + head * st[1];
-        // where a value's other one lies (kind 2 does not turn)
-        const bool turns = kind != 2 && at < a.rot_dim;
-        P own[kAppendTokens], other[kAppendTokens];
-        auto other_at = [&](int x) { return x < half ? x + half : x < a.rot_dim ? x - half : x; };
-#pragma unroll
-        for (int w = 0; w < kAppendTokens; ++w) {
-            own[w] = other[w] = P{};
-            if (!active || w >= here) continue;
-            const uint16_t *from = src + w * st[0];
-            own[w] = *reinterpret_cast<const P *>(from + at);
-            if (kTurn == kPackTurn && turns) other[w] = *reinterpret_cast<const P *>(from + other_at(at));
-            if (kTurn == kPairTurn && turns)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    other[w].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at + 2 * e));
-        }
-        __syncwarp();  // q_out may be q: a head's loads come before its stores
+        const int64_t step = kind == 0 ? a.q_st[0] : kind == 1 ? a.k_st[0] : a.v_st[0];
+        const uint16_t *src = static_cast<const uint16_t *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + t0 * step +
+                              head * (kind == 0 ? a.q_st[1] : kind == 1 ? a.k_st[1] : a.v_st[1]);
         const void *norm = kind == 0 ? A.q_norm : kind == 1 ? A.k_norm : nullptr;
-        const bool any_norm = A.q_norm || A.k_norm;
-        float wo[8], wx[8];
+        const bool turns = kind != 2 && a.rot_dim > 0;
+        auto other_at = [&](int x) { return x < half ? x + half : x < a.rot_dim ? x - half : x; };
+        if (any_norm && weights_of != kind) {
+            weights_of = kind;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wo[e] = wx[e] = 1.f;
-        if (norm && active) {
-            weights_at<T>(norm, A.norm_f32, at, wo);
-            if (kTurn == kPackTurn && turns) weights_at<T>(norm, A.norm_f32, other_at(at), wx);
-            if (kTurn == kPairTurn && turns)
+            for (int e = 0; e < 4; ++e) w0[e] = w1[e] = z0[e] = z1[e] = pair2(1.f, 1.f);
+            if (norm)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int x = other_at(at + (e & ~1)) + (e & 1);
-                    wx[e] = A.norm_f32 ? __ldg(static_cast<const float *>(norm) + x)
-                                       : to_f32<T>(static_cast<const T *>(norm)[x]);
+                for (int e = 0; e < 4; ++e) {
+                    if (in0) w0[e] = weights_at<T>(norm, A.norm_f32, at0 + 2 * e);
+                    if (in1) w1[e] = weights_at<T>(norm, A.norm_f32, at1 + 2 * e);
+                    if (kTurn == kPairTurn) {
+                        if (in0) z0[e] = weights_at<T>(norm, A.norm_f32, other_at(at0 + 2 * e));
+                        if (in1) z1[e] = weights_at<T>(norm, A.norm_f32, other_at(at1 + 2 * e));
+                    }
                 }
         }
+        // two tokens at a time
+        constexpr int kAhead = 2;
+#pragma unroll 1
+        for (int wa = 0; wa < here; wa += kAhead) {
+            P own[kAhead][2], other[kAhead][2];
 #pragma unroll
-        for (int w = 0; w < kAppendTokens; ++w) {
-            if (w >= here) break;
-            float y[8], z[8];
-            unpack<T>(own[w], y);
-            unpack<T>(other[w], z);
-            if (any_norm) {
-                float sum = 0.f;
+            for (int t = 0; t < kAhead; ++t) {
+                own[t][0] = own[t][1] = other[t][0] = other[t][1] = P{};
+                if (!active || wa + t >= here) continue;
+                const uint16_t *from = src + (wa + t) * step;
+                if (in0) own[t][0] = *reinterpret_cast<const P *>(from + at0);
+                if (in1) own[t][1] = *reinterpret_cast<const P *>(from + at1);
+                if (kTurn == kPairTurn && turns)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(y[e], y[e], sum);
-                for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float f = norm ? rsqrtf(sum / (float)a.head_dim + A.eps) : 1.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[e] *= f * wo[e];
-                    z[e] *= f * wx[e];
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        if (in0) other[t][0].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at0 + 2 * e));
+                        if (in1) other[t][1].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at1 + 2 * e));
+                    }
             }
-            if (turns) {
-                if (kTurn == kAdjacentTurn) {
+            __syncwarp();  // q_out may be q: a head's loads come before its stores
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        if (at + e < a.rot_dim) {
-                            const float2 c = cs[w][(at + e) / 2];
-                            const float u = y[e] * c.x - y[e + 1] * c.y, v = y[e] * c.y + y[e + 1] * c.x;
-                            y[e] = u;
-                            y[e + 1] = v;
-                        }
-                } else {
+            for (int t = 0; t < kAhead; ++t) {
+                const int w = wa + t;
+                if (w >= here) break;
+                uint64_t y0[4], y1[4], o0[4], o1[4];
+                unpack<T>(own[t][0], y0);
+                unpack<T>(own[t][1], y1);
+                if (kTurn == kPairTurn) {
+                    unpack<T>(other[t][0], o0);
+                    unpack<T>(other[t][1], o1);
+                }
+                if (any_norm) {
+                    uint64_t sum2 = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int x = at + e;
-                        if (x < half) {
-                            const float2 c = cs[w][x];
-                            y[e] = y[e] * c.x - z[e] * c.y;
-                        } else if (x < a.rot_dim) {
-                            const float2 c = cs[w][x - half];
-                            y[e] = z[e] * c.y + y[e] * c.x;
+                    for (int e = 0; e < 4; ++e) sum2 = fma2(y1[e], y1[e], fma2(y0[e], y0[e], sum2));
+                    float u, v;
+                    unpair2(sum2, u, v);
+                    float sum = u + v;
+                    for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    const float f = norm ? rsqrtf(fmaf(sum, inv_dim, A.eps)) : 1.f;
+                    const uint64_t f2 = pair2(f, f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y0[e] = mul2(y0[e], mul2(f2, w0[e]));
+                        y1[e] = mul2(y1[e], mul2(f2, w1[e]));
+                        if (kTurn == kPairTurn) {
+                            o0[e] = mul2(o0[e], mul2(f2, z0[e]));
+                            o1[e] = mul2(o1[e], mul2(f2, z1[e]));
                         }
                     }
                 }
-            }
-            const RowPlace &p = place[w];
-            if (kind == 0 || !kEight) {
-                if (active && p.known) {
-                    P o;
+                if (kTurn == kPackTurn && turns && pairs) {
+                    // (a, c) -> (a cos - c sin, a sin + c cos)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o.x[e] = bits_of(y[2 * e], y[2 * e + 1], T());
-                    if (kind == 0)
-                        *reinterpret_cast<P *>(static_cast<uint16_t *>(a.q_out) + (t0 + w) * a.o_st[0] +
-                                               head * a.o_st[1] + at) = o;
-                    else if (p.k >= 0)
-                        *reinterpret_cast<P *>(static_cast<uint16_t *>(kind == 1 ? a.k_cache : a.v_cache) +
-                                               (kind == 1 ? p.k + head * a.kc_st[2] : p.v + head * a.vc_st[2]) +
-                                               at) = o;
-                }
-            }
-            if (kEight) {
-                // the bits of magnitudes order as they do; NaN and infinity lie above
-                uint32_t top = 0;
+                    for (int e = 0; e < 4; e += 2) {
+                        const float4 co = *reinterpret_cast<const float4 *>(&cosines[w][at0 + 2 * e]);
+                        const float4 si = *reinterpret_cast<const float4 *>(&sines[w][at0 + 2 * e]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
-                for (int d = lanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                if (kind != 0 && active && p.k >= 0) {
-                    const bool finite = top < 0x7f800000u;
-                    const int e8 = scale_exponent(top);
-                    const float f = power_of_two(-e8);
-                    uint2 o = make_uint2(0, 0);
-                    if (finite) {
-                        o.x = codes_of(y[0] * f, y[1] * f) | codes_of(y[2] * f, y[3] * f) << 16;
-                        o.y = codes_of(y[4] * f, y[5] * f) | codes_of(y[6] * f, y[7] * f) << 16;
+                        for (int x = 0; x < 2; ++x) {
+                            const uint64_t c2 = x ? pair2(co.z, co.w) : pair2(co.x, co.y);
+                            const uint64_t s2 = x ? pair2(si.z, si.w) : pair2(si.x, si.y);
+                            const uint64_t m2 = x ? pair2(-si.z, -si.w) : pair2(-si.x, -si.y);
+                            const uint64_t p = y0[e + x], q = y1[e + x];
+                            y0[e + x] = fma2(p, c2, mul2(q, m2));
+                            y1[e + x] = fma2(p, s2, mul2(q, c2));
+                        }
                     }
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(kind == 1 ? a.k_cache : a.v_cache) +
-                                               (kind == 1 ? p.k + head * a.kc_st[2] : p.v + head * a.vc_st[2]) +
-                                               at) = o;
-                    if (sub == 0) {
-                        uint8_t *to = kind == 1 ? A.scales.k + p.ks + head * A.scales.k_st[2]
-                                                : A.scales.v + p.vs + head * A.scales.v_st[2];
-                        *to = (uint8_t)(finite ? e8 + 127 : kScaleNan);
+                }
+                if (kTurn == kAdjacentTurn && turns) {
+#pragma unroll
+                    for (int pack = 0; pack < 2; ++pack) {
+                        const int at = pack ? at1 : at0;
+                        if (at >= a.rot_dim) continue;
+                        uint64_t(&y)[4] = pack ? y1 : y0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (at + 2 * e < a.rot_dim) {
+                                const float c = cosines[w][at / 2 + e], s = sines[w][at / 2 + e];
+                                float p, q;
+                                unpair2(y[e], p, q);
+                                y[e] = pair2(p * c - q * s, p * s + q * c);
+                            }
+                    }
+                }
+                if (kTurn == kPairTurn && turns) {
+#pragma unroll
+                    for (int pack = 0; pack < 2; ++pack)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int x = (pack ? at1 : at0) + 2 * e;  // x and x + 1 lie in one half
+                            if (x >= a.rot_dim) continue;
+                            uint64_t &y = pack ? y1[e] : y0[e];
+                            const uint64_t z = pack ? o1[e] : o0[e];
+                            const int j = x < half ? x : x - half;
+                            const uint64_t c2 = pair2(cosines[w][j], cosines[w][j + 1]);
+                            const float sign = x < half ? -1.f : 1.f;
+                            y = fma2(y, c2, mul2(z, pair2(sign * sines[w][j], sign * sines[w][j + 1])));
+                        }
+                }
+                const RowPlace &p = place[w];
+                if (kind == 0 || !kEight) {
+                    if (active && p.known) {
+                        uint16_t *to = kind == 0 ? static_cast<uint16_t *>(a.q_out) + (t0 + w) * a.o_st[0] + head * a.o_st[1]
+                                       : kind == 1 ? static_cast<uint16_t *>(a.k_cache) + p.k + head * a.kc_st[2]
+                                                   : static_cast<uint16_t *>(a.v_cache) + p.v + head * a.vc_st[2];
+                        if (kind == 0 || p.k >= 0) {
+                            P o;
+#pragma unroll
+                            for (int pack = 0; pack < 2; ++pack) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float u, v;
+                                    unpair2(pack ? y1[e] : y0[e], u, v);
+                                    o.x[e] = bits_of(u, v, T());
+                                }
+                                if (pack ? in1 : in0) *reinterpret_cast<P *>(to + (pack ? at1 : at0)) = o;
+                            }
+                        }
+                    }
+                }
+                if (kEight) {
+                    float top = 0.f;
+                    uint64_t zero = 0;  // NaN where a value is not finite
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float u, v;
+                        unpair2(y0[e], u, v);
+                        top = max3(top, fabsf(u), fabsf(v));
+                        unpair2(y1[e], u, v);
+                        top = max3(top, fabsf(u), fabsf(v));
+                        zero = fma2(y1[e], 0, fma2(y0[e], 0, zero));
+                    }
+                    float u, v;
+                    unpair2(zero, u, v);
+                    const unsigned bad = __ballot_sync(0xffffffffu, !(u + v == 0.f));
+                    for (int d = lanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    if (kind != 0 && active && p.k >= 0) {
+                        const unsigned group = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1) << (lane - sub);
+                        const bool finite = (bad & group) == 0;
+                        const int e8 = scale_exponent(__float_as_uint(top));
+                        const uint64_t f2 = pair2(power_of_two(-e8), power_of_two(-e8));
+                        uint8_t *to = static_cast<uint8_t *>(kind == 1 ? a.k_cache : a.v_cache) +
+                                      (kind == 1 ? p.k + head * a.kc_st[2] : p.v + head * a.vc_st[2]);
+#pragma unroll
+                        for (int pack = 0; pack < 2; ++pack) {
+                            uint32_t c[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                unpair2(mul2(pack ? y1[e] : y0[e], f2), u, v);
+                                c[e] = finite ? codes_of(u, v) : 0u;
+                            }
+                            if (pack ? in1 : in0)
+                                *reinterpret_cast<uint2 *>(to + (pack ? at1 : at0)) =
+                                    make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+                        }
+                        if (sub == 0) {
+                            uint8_t *byte = kind == 1 ? A.scales.k + p.ks + head * A.scales.k_st[2]
+                                                      : A.scales.v + p.vs + head * A.scales.v_st[2];
+                            *byte = (uint8_t)(finite ? e8 + 127 : kScaleNan);
+                        }
                     }
                 }
             }
@@ -363,7 +448,7 @@ __global__ void __launch_bounds__(kReadThreads)
             if (!ok && lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_PAGE);
             for (int w = lane; w < here; w += 32) {
                 const int64_t in = slot0 + w - pg * A.batch.page_size;
-                RowPlace p = {-1, -1, -1, -1, slot0 + w < s.len};
+                RowPlace p = {-1, -1, -1, -1, slot0 + w < s.len, 0};
                 if (ok && p.known) {
                     p.k = id * A.kc_st[0] + in * A.kc_st[1];
                     p.v = id * A.vc_st[0] + in * A.vc_st[1];

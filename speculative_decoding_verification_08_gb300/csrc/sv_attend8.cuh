@@ -184,12 +184,6 @@ __device__ __forceinline__ bool group_any(int number, bool x) {
     return r != 0;
 }
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t y;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-    return y;
-}
-
 // Joins each of 32 columns over a warp's lanes; lane i gets column i.
 template <class F>
 __device__ __forceinline__ float across_lanes(float (&v)[32], int lane, F join) {
