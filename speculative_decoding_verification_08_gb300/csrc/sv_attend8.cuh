@@ -50,7 +50,6 @@ constexpr int kThreads8 = 640;
 constexpr int kSoftmaxRegs8 = 136, kValueRegs8 = 56, kIssueRegs8 = 56, kTileRegs8 = 96;
 static_assert(128 * (2 * kSoftmaxRegs8 + kValueRegs8 + kIssueRegs8 + kTileRegs8) <= kThreads8 * 96, "register split");
 constexpr int kRaw = kKeys * 128;     // a block of codes
-constexpr int kRing8 = 3;             // blocks of keys in flight
 constexpr int kScaleRing = 3;         // pairs of blocks of scales
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
 constexpr int kNoScale = -200;        // below every e8m0 exponent
@@ -66,11 +65,12 @@ struct Attend8Smem {
     // columns of scores: a whole product has a multiple of 16
     static constexpr int kScoreCols = (kParts * kRows8 + 15) / 16 * 16;
     static constexpr int kQuery = kScoreCols * 128;
-    static constexpr int kMisc = 7168;
-    static constexpr int kFixed = kMisc + 2 * kQuery + kRing8 * kRaw + 2 * 2 * kRaw + 2 * kRaw;
-    static constexpr int kRingV = kFixed + 3 * kRaw <= 227 * 1024 ? 3 : 2;  // blocks of values in flight
-    static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRing8 * kRaw, kVc = kV + kRingV * kRaw,
-                         kP = kVc + 2 * 2 * kRaw, kBytes = kP + 2 * kRaw;
+    // Rings: blocks of keys and of values in flight, as room allows
+    static constexpr int kMisc = 7168, kRoom = 227 * 1024;
+    static constexpr int kFixed = kMisc + 2 * kQuery + 2 * 2 * kRaw + kRaw;
+    static constexpr int kRingV = kFixed + 6 * kRaw <= kRoom ? 3 : 2, kRingK = kFixed + (4 + kRingV) * kRaw <= kRoom ? 4 : 3;
+    static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRingK * kRaw, kVc = kV + kRingV * kRaw,
+                         kP = kVc + 2 * 2 * kRaw, kBytes = kP + kRaw;
     // O of two tiles' two groups: first column, and a whole product's columns
     static constexpr int kOutCols = (kRows8 + 15) / 16 * 16, kOut = 2 * kScoreCols;
     static constexpr uint32_t kCols = kOut + 4 * kOutCols <= 128 ? 128 : kOut + 4 * kOutCols <= 256 ? 256 : 512;
@@ -81,7 +81,7 @@ struct Attend8Smem {
 constexpr int kPieceReaders8 = 20;
 
 struct Attend8Shared {
-    unsigned long long k_full[kRing8], k_empty[kRing8], v_full[kRing8], v_empty[kRing8];
+    unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
     unsigned long long scale_full[kScaleRing], scale_empty[kScaleRing];
     unsigned long long s_full[2], s_empty[2], vc_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2], drain[2];
     unsigned long long state_full[2], state_empty[2], o_full[2], o_empty[2];
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
     if (warp == 13) tc::tmem_alloc(&sh.tmem, L::kCols);
     if (tid == 0) {
-        for (int i = 0; i < kRing8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_full[i], 1);
@@ -451,12 +451,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     f[x] = own_ref[x] == -INFINITY ? 0.f : ex2(own_ref[x] - ref);
                     sum += own_sum[x] * f[x];
                     const int e = st.exponent[x];
-                    f[x] *= e == kNoScale ? 0.f : ex2((float)(e - (int)kHalfLift));
+                    if (e != kNoScale) f[x] *= ex2((float)(e - (int)kHalfLift));  // (else: zeros and NaN)
                 }
             }
             // (a row that saw nothing has the sum 0, and zeros)
-            const float norm = sum == 0.f ? 0.f : 1.f / sum;
             const bool whole = p.parts == 1;
+            if (whole) {
+                const float norm = sum == 0.f ? 0.f : 1.f / sum;
+                f[0] *= norm;
+                f[1] *= norm;
+            }
             const int slot = blockIdx.x * 2 + ((int)blockIdx.x == p.first ? 1 : 0);
             float2 *part_stats = reinterpret_cast<float2 *>(A.workspace + kAttendStats);
             float *part_out = reinterpret_cast<float *>(A.workspace + kAttendOut);
@@ -469,35 +473,25 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const int64_t wrap = A.o_st[0] - A.group * A.o_st[1];
 #pragma unroll 1
             for (int r0 = 0; r0 < rows; r0 += 8) {
-                float o[8];
+                uint32_t u[2][8] = {};  // (a group that had no block left none)
+                if (blocks > 0) tc::ld8(u[0], t_o + tb * 2 * L::kOutCols + r0);
+                if (blocks > 1) tc::ld8(u[1], t_o + (tb * 2 + 1) * L::kOutCols + r0);
+                tc::wait_ld();
 #pragma unroll
-                for (int r = 0; r < 8; ++r) o[r] = 0.f;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (blocks <= x) break;
-                    uint32_t u[8];
-                    tc::ld8(u, t_o + (tb * 2 + x) * L::kOutCols + r0);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        o[r] = fmaf(__shfl_sync(0xffffffffu, f[x], r0 + r), __uint_as_float(u[r]), o[r]);
-                }
-                if (whole) {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const float n = __shfl_sync(0xffffffffu, norm, r0 + r);
-                        if (r0 + r >= rows) break;
-                        if (tt < D) *out = from_f32<T>(n == 0.f ? 0.f : o[r] * n);
-                        out += A.o_st[1];
-                        if (++head == A.group) {
-                            head = 0;
-                            out += wrap;
-                        }
+                for (int r = 0; r < 8; ++r) {
+                    const float f0 = __shfl_sync(0xffffffffu, f[0], r0 + r), f1 = __shfl_sync(0xffffffffu, f[1], r0 + r);
+                    const float o = fmaf(f1, __uint_as_float(u[1][r]), f0 * __uint_as_float(u[0][r]));
+                    if (r0 + r >= rows) break;
+                    if (!whole) {
+                        part_out[slot * kSlot + (r0 + r) * 128 + tt] = o;
+                        continue;
                     }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (r0 + r < rows) part_out[slot * kSlot + (r0 + r) * 128 + tt] = o[r];
+                    if (tt < D) *out = from_f32<T>(o);
+                    out += A.o_st[1];
+                    if (++head == A.group) {
+                        head = 0;
+                        out += wrap;
+                    }
                 }
             }
             tc::fence_before();
@@ -598,7 +592,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             // ---- copies of codes ------------------------------------------------
             const int boxes = kKeys / A.piece;
             const bool active = lane < boxes;
-            RingPlace<kRing8> kp;
+            RingPlace<L::kRingK> kp;
             RingPlace<L::kRingV> vp;
             int kn = 0, vn = 0;  // blocks copied so far, as far as a ring goes
             PieceReader8 reader;
@@ -652,13 +646,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                          of ? value_id : key_id, full);
                         }
                         if (of) vp.next(), vn = min(vn + 1, L::kRingV);
-                        else kp.next(), kn = min(kn + 1, kRing8);
+                        else kp.next(), kn = min(kn + 1, L::kRingK);
                     }
                 }
             }
             // the last copies have landed before the CTA may end
             for (int n = 0; n < kn; ++n) {  // (stages from kp.st on are the turn before)
-                const int st = (kp.st + kRing8 - 1 - n) % kRing8;
+                const int st = (kp.st + L::kRingK - 1 - n) % L::kRingK;
                 mbar_wait(&sh.k_full[st], st < kp.st ? kp.turn : kp.turn ^ 1);
             }
             for (int n = 0; n < vn; ++n) {
@@ -672,7 +666,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const uint64_t q_desc = tc::smem_desc(smem_u32(smem + L::kQ), 16, 1024);
             const int steps = (D + 31) / 32;
             uint32_t qn = 0, used[2] = {0, 0};  // tiles, blocks of each group
-            RingPlace<kRing8> at;
+            RingPlace<L::kRingK> at;
             PieceReader8 reader;
             bool ok = true;  // a wait gave up: nothing more is issued or handed back
             while (ok && reader.next(sh)) {
@@ -725,7 +719,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     if (!ok) break;
                     tc::fence_after();
                     if (tc::elect()) {
-                        const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * (kRaw / 16);
+                        const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * 4;  // (64 bytes)
 #pragma unroll 1
                         for (int s = 0; s < kKeys / 16; ++s)
                             tc::mma_ss(tm + (tb * 2 + b) * L::kOutCols, vd + s * (2048 / 16), pd + s * (2048 / 16),
@@ -1029,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const bool any_nan = __any_sync(0xffffffffu, value_byte == kScaleNan);
                     if (used > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1);
                     __syncwarp();
-                    char *row = smem + L::kP + g * kRaw + gt * 128;
+                    char *row = smem + L::kP + gt * 128;  // the group's half of it
 #pragma unroll
                     for (int o = 0; o < kRows8 / 8; ++o) {
                         uint32_t w[4];
@@ -1049,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             }
                             w[e] = pack2<__half>(a, b);
                         }
-                        *reinterpret_cast<uint4 *>(row + ((o ^ (gt & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(row + (((4 * g + o) ^ (gt & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     tc::fence_async_smem();
                     __syncwarp();
