@@ -889,6 +889,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const float key_scale = q_factor * scale_of(key_byte);
                     const bool masked =
                         k0 + kKeys - 1 > past + j0 || (A.window > 0 && k0 <= past + j1 - A.window);
+                    // rows [r0, r1) see the slot: row r does when its token does, row0 + r >=
+                    // t G, and < (t + window) G
+                    int r0 = 0, r1 = kRows8;
+                    if (__builtin_expect(masked, 0)) {
+                        const int64_t from = ((int64_t)k0 + gt - past) * A.group - row0;
+                        const int64_t to = A.window > 0 ? from + (int64_t)A.window * A.group : kRows8;
+                        r0 = (int)max((int64_t)0, min(from, (int64_t)kRows8));
+                        r1 = (int)max((int64_t)0, min(to, (int64_t)kRows8));
+                    }
+                    auto sees = [&](int r) -> bool { return r >= r0 && r < r1; };
                     auto scores = [&]() {
                         const uint64_t key_scale2 = pair2(key_scale, key_scale);
 #pragma unroll
@@ -913,19 +923,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                 }
                         }
                         if (__builtin_expect(masked, 0)) {
-                            // row r sees the slot when its token does: row0 + r >= t G, and
-                            // < (t + window) G
-                            const int64_t t = (int64_t)k0 + gt - past;
-                            const int64_t from = t * A.group - row0;
-                            const int64_t to = A.window > 0 ? from + (int64_t)A.window * A.group : kRows8;
-                            const int r0 = (int)max((int64_t)0, min(from, (int64_t)kRows8));
-                            const int r1 = (int)max((int64_t)0, min(to, (int64_t)kRows8));
 #pragma unroll
                             for (int r = 0; r < kRows8 / 2; ++r) {
                                 float a, b;
                                 unpair2(y[r], a, b);
-                                if (2 * r < r0 || 2 * r >= r1) a = -INFINITY;
-                                if (2 * r + 1 < r0 || 2 * r + 1 >= r1) b = -INFINITY;
+                                if (!sees(2 * r)) a = -INFINITY;
+                                if (!sees(2 * r + 1)) b = -INFINITY;
                                 y[r] = pair2(a, b);
                             }
                         }
@@ -1020,7 +1023,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const int shift = max(e8, -127) - exponent + (int)kHalfLift;
                     const float value_scale = shift < -126 ? 0.f : power_of_two(shift);
                     const uint64_t value_scale2 = pair2(value_scale, value_scale);
-                    const bool any_nan = __any_sync(0xffffffffu, value_byte == kScaleNan);
                     if (used > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1);
                     __syncwarp();
                     char *row = smem + L::kP + gt * 128;  // the group's half of it
@@ -1035,15 +1037,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             const uint64_t x = pair2(ex2(a), ex2(b));
                             sums[r] = add2(sums[r], x);
                             unpair2(mul2(x, value_scale2), a, b);
-                            if (__builtin_expect(any_nan, 0) && value_byte == kScaleNan) {  // for the rows that see it
-                                float u, v;
-                                unpair2(y[r], u, v);
-                                a = u == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu);
-                                b = v == -INFINITY ? 0.f : __uint_as_float(0x7fffffffu);
-                            }
                             w[e] = pack2<__half>(a, b);
                         }
                         *reinterpret_cast<uint4 *>(row + (((4 * g + o) ^ (gt & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (__builtin_expect(value_byte == kScaleNan, 0)) {  // NaN for the rows that see it
+#pragma unroll 1
+                        for (int o = 0; o < kRows8 / 8; ++o) {
+                            uint4 *at = reinterpret_cast<uint4 *>(row + (((4 * g + o) ^ (gt & 7)) * 16));
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int r = o * 8 + 2 * e;
+                                w[e] = (sees(r) ? 0x7fffu : 0u) | (sees(r + 1) ? 0x7fff0000u : 0u);
+                            }
+                            *at = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
                     tc::fence_async_smem();
                     __syncwarp();
