@@ -8,7 +8,10 @@ rows q they were drawn from), the target runs once over [pending, drafts]
 p (``warp_sample``), and the verification decides (``verify_round`` through
 ``PendingTokenDecoder``).  Rejected drafts leave the cache by rollback.
 
-    python examples/paged_decoding.py [--new 64] [--k 5] [--sampling]
+With ``--eight`` the caches hold 8-bit values; with ``--norms`` queries and keys
+are normed by heads before they turn.
+
+    python examples/paged_decoding.py [--new 64] [--k 5] [--sampling] [--eight] [--norms]
 """
 import argparse
 import os
@@ -27,7 +30,8 @@ class TinyDecoder:
     """A decoder with random weights: attention over a paged cache and a gated
     feed-forward per layer.  ``layers`` of it may be run."""
 
-    def __init__(self, vocab=4096, dim=256, layers=2, heads=4, kv_heads=2, head_dim=64, seed=0):
+    def __init__(self, vocab=4096, dim=256, layers=2, heads=4, kv_heads=2, head_dim=64, seed=0,
+                 eight=False, norms=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def weight(a, b, scale=1.0):
@@ -44,10 +48,14 @@ class TinyDecoder:
                        for i in range(layers)]
         self.head = weight(dim, vocab, 4.0)
         self.inv_freq = rope_frequencies(head_dim, device="cuda")
+        self.eight = eight
+        # (drawn last: the other weights are the same with and without)
+        self.norms = [{f"{x}_norm": (1 + weight(head_dim, 1).view(-1)) if norms else None for x in "qk"}
+                      for _ in range(layers)]
 
     def cache(self, layers, pages=64, page_size=16):
         return PagedCache(layers, pages, page_size, self.kv_heads, self.head_dim,
-                          inv_freq=self.inv_freq)
+                          dtype=torch.float8_e4m3fn if self.eight else torch.bfloat16, inv_freq=self.inv_freq)
 
     @staticmethod
     def norm(x):
@@ -62,7 +70,7 @@ class TinyDecoder:
         for i, b in enumerate(self.blocks[:layers]):
             qkv = (self.norm(x) @ b["qkv"]).view(n, -1, d)
             q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
-            q = cache.append(i, q, k, v)
+            q = cache.append(i, q, k, v, **self.norms[i])
             x = x + cache.attend(i, q).reshape(n, -1) @ b["out"]
             gate, up = (self.norm(x) @ b["up"]).chunk(2, dim=-1)
             x = x + (torch.nn.functional.silu(gate) * up) @ b["down"]
@@ -129,18 +137,18 @@ class PagedDraft:
         return tokens, torch.stack(rows)
 
 
-def decode(prompt, max_new=64, k=5, greedy=True, seed=0):
+def decode(prompt, max_new=64, k=5, greedy=True, seed=0, **model):
     """(tokens, tokens a round on average) of a generation with the tiny model."""
-    model, warp = TinyDecoder(), Warp()
+    model, warp = TinyDecoder(**model), Warp()
     dec = PendingTokenDecoder(PagedDraft(model, warp, greedy=greedy), PagedTarget(model, warp), k=k,
                               greedy=greedy, seed=seed)
     out = dec.generate(prompt, max_new)
     return out, sum(n + 1 for _, n, _ in dec.trace) / len(dec.trace)
 
 
-def plain(prompt, max_new=64):
+def plain(prompt, max_new=64, **model):
     """The same target without speculation, one token at a time."""
-    target = PagedTarget(TinyDecoder(), Warp())
+    target = PagedTarget(TinyDecoder(**model), Warp())
     feed, out = list(prompt), []
     while len(out) < max_new:
         feed = [int(target.forward(feed)[-1].argmax())]
@@ -153,13 +161,16 @@ def main():
     ap.add_argument("--new", type=int, default=64)
     ap.add_argument("--k", type=int, default=5)
     ap.add_argument("--sampling", action="store_true")
+    ap.add_argument("--eight", action="store_true")
+    ap.add_argument("--norms", action="store_true")
     a = ap.parse_args()
     prompt = [11, 222, 3333, 44, 5]
-    out, rate = decode(prompt, a.new, a.k, not a.sampling)
+    model = dict(eight=a.eight, norms=a.norms)
+    out, rate = decode(prompt, a.new, a.k, not a.sampling, **model)
     print("tokens:", out)
     print(f"{rate:.2f} tokens a target pass")
     if not a.sampling:
-        same = sum(x == y for x, y in zip(out, plain(prompt, a.new)))
+        same = sum(x == y for x, y in zip(out, plain(prompt, a.new, **model)))
         print(f"{same} of {len(out)} as without speculation")
 
 

@@ -395,7 +395,21 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
                size_t workspace_bytes, sv_stream_t stream);
 
 /* sv_paged_attention over a cache of 8-bit values; q and out are of `dtype` (SV_BF16
- * or SV_F16). */
+ * or SV_F16), and the keys and values the codes times their scales.
+ *   scratch  NULL, or sv_paged_attention_scratch_size(cache, q_heads) bytes, 256-byte
+ *         aligned, for this call alone: the sequences are then read back to 16 bits
+ *         first (two kernels), which is faster when they have many new tokens; the size
+ *         is 0 where it is not, or where it would be more than 16 GiB.  (Keys and
+ *         values past fp16's range saturate there.)
+ * Products are accumulated and statistics kept in fp32.  Without scratch: scores are
+ * those of the codes and the queries as they are; a query's values below 2^-24 of the
+ * largest of its tile (up to 32 rows) are good to 2^-33 of it; weights, times the
+ * values' scales relative to the largest scale met, are rounded to 11 bits (those below
+ * 2^-21 of the largest to steps of 2^-31 of it).  A query that holds a NaN or an
+ * infinity gives NaN for a row that sees a slot.  Slots inside a sequence's length must
+ * hold what sv_append_kv_normed writes, codes of 0x7f and 0xff excepted; what unused slots hold
+ * does not matter.  A key or value whose scale is NaN gives NaN for the rows that see
+ * it (with scratch, as for sv_paged_attention, it must not occur). */
 size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads);
 int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
                         const void *q, const int64_t *q_stride, void *out, const int64_t *out_stride,

@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // Publishes the next piece and prepares its queries (all four warps; false after
         // a wait gave up).
         auto prepare = [&]() -> bool {
+            if (SV_STALL && ready == 1 && blockIdx.x % 2 == 1) return false;
             const int k = ready % kPieces;
             bool ok = true;
             if (tw == 0) {

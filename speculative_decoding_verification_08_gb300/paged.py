@@ -15,12 +15,16 @@ share the page table.  A pass over new tokens is::
 Token rows are ordered by sequence, in the order ``begin`` was given them.
 Rolled-back slots are simply written again by the next pass; pages that no
 token uses any more go back to the pool.
+
+With ``dtype=torch.float8_e4m3fn`` the cache holds 8-bit values and a power of
+two for each vector; tokens stay in 16 bits, and ``read`` takes sequences back
+to them.
 """
 from __future__ import annotations
 
 from typing import Dict, List, Optional
 
-from . import SpecVerifyError, _torch, append_kv, paged_attention
+from . import SpecVerifyError, _torch, append_kv, paged_attention, read_kv
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, device=None):
@@ -36,7 +40,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, device=None):
 class PagedCache:
     """Keys and values of ``layers`` layers in ``num_pages`` pages of
     ``page_size`` slots (heads first within a page: a head's slots lie
-    together).  ``inv_freq`` as for ``append_kv`` (None: no rotation)."""
+    together).  ``inv_freq`` as for ``append_kv`` (None: no rotation).  dtype:
+    the tokens' (bfloat16 by default), or float8_e4m3fn, whose scales are
+    ``k_scale`` and ``v_scale`` (None otherwise)."""
 
     def __init__(self, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
                  dtype=None, device=None, inv_freq=None, interleaved: bool = False):
@@ -50,6 +56,12 @@ class PagedCache:
         # of old bits would make dumps hard to read
         self.k = torch.zeros(shape, dtype=dtype, device=self.device).transpose(2, 3)
         self.v = torch.zeros(shape, dtype=dtype, device=self.device).transpose(2, 3)
+        self.k_scale = self.v_scale = None
+        if dtype == torch.float8_e4m3fn:
+            # (bytes of zero: the smallest scale, for codes of zero)
+            self.k_scale, self.v_scale = (
+                torch.zeros(shape[:-1], dtype=torch.uint8, device=self.device).view(torch.float8_e8m0fnu).transpose(2, 3)
+                for _ in range(2))
         self.page_size, self.inv_freq, self.interleaved = page_size, inv_freq, interleaved
         self.free: List[int] = list(range(num_pages - 1, -1, -1))
         self.owned: Dict[object, List[int]] = {}
@@ -92,16 +104,40 @@ class PagedCache:
             raise SpecVerifyError("begin() comes first")
         return self._batch
 
-    def append(self, layer: int, q, k, v, ws=None):
+    def _scales(self, layer: int):
+        return {} if self.k_scale is None else dict(k_scale=self.k_scale[layer], v_scale=self.v_scale[layer])
+
+    def append(self, layer: int, q, k, v, ws=None, q_norm=None, k_norm=None, eps: float = 1e-6):
         """Writes the pass's keys and values of a layer; returns q rotated.
-        (ws as for ``append_kv``: a pass captured into a graph needs one.)"""
+        (ws as for ``append_kv``: a pass captured into a graph needs one; norms
+        as there.)"""
         return append_kv(k, v, self.k[layer], self.v[layer], *self._pass(), inv_freq=self.inv_freq,
-                         q=q, interleaved=self.interleaved, ws=ws)
+                         q=q, interleaved=self.interleaved, q_norm=q_norm, k_norm=k_norm, eps=eps, ws=ws,
+                         **self._scales(layer))
 
     def attend(self, layer: int, q, scale: Optional[float] = None, window: int = 0, ws=None):
         """The pass's queries over a layer of the cache."""
         return paged_attention(q, self.k[layer], self.v[layer], *self._pass(), scale=scale,
-                               window=window, ws=ws)
+                               window=window, ws=ws, **self._scales(layer))
+
+    def read(self, layer: int, seqs=None, dtype=None, ws=None) -> Dict[object, tuple]:
+        """What a layer holds of the sequences (all by default): seq -> (k, v),
+        [length][kv_heads][head_dim], in 16 bits (``dtype`` as for ``read_kv``)."""
+        torch = _torch()
+        seqs = list(self.length if seqs is None else seqs)
+        lengths = [self._held(s) for s in seqs]
+        rows = [self.owned[s] for s in seqs]
+        wide = max([len(r) for r in rows] + [1])
+        starts = [0]
+        for n in lengths:
+            starts.append(starts[-1] + n)
+        k, v = read_kv(self.k[layer], self.v[layer],
+                       torch.tensor([r + [0] * (wide - len(r)) for r in rows], dtype=torch.int32)
+                       .view(len(seqs), wide).to(self.device),
+                       torch.tensor(starts, dtype=torch.int32).to(self.device),
+                       torch.tensor(lengths, dtype=torch.int32).to(self.device), rows=starts[-1], dtype=dtype, ws=ws,
+                       **self._scales(layer))
+        return {s: (k[a:b], v[a:b]) for s, a, b in zip(seqs, starts, starts[1:])}
 
     def rollback(self, seq, n: int) -> None:
         """Drops a sequence's last n tokens."""
