@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                    const __grid_constant__ CUtensorMap vmap) {
     typedef Attend8Smem<T, kRows8> L;
     constexpr int kParts = L::kParts;
-    constexpr int kAtOnce = kRows8 < 32 ? kRows8 / 8 : 1;  // columns of scores by eight, as registers allow
+    constexpr int kAtOnce = kParts * kRows8 <= 72 ? kParts : 2;  // parts of scores, as registers allow
     constexpr uint32_t kIdescS = tc::instr_desc_f8(kKeys, L::kScoreCols);
     // (bit 15: A's slots are its rows in memory, as B's)
     constexpr uint32_t kIdescO = tc::instr_desc(false, true, 128, L::kOutCols) | (1u << 15);
@@ -376,26 +376,29 @@ __global__ void __launch_bounds__(kThreads8, 1)
             ++qn;
             // four values to a lane, rows tw, tw + 4, ... to a warp
             constexpr int kMine = kRows8 / 4;
-            uint2 x[kMine];
             uint32_t top = 0;
             const int rows = p.rows;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
+            auto load = [&](int i) -> uint2 {
                 const int r = tw + 4 * i;
-                x[i] = make_uint2(0, 0);
-                if (r >= rows || lane * 4 >= D || A.q_mode == 2) continue;
+                if (r >= rows || lane * 4 >= D || A.q_mode == 2) return make_uint2(0, 0);
                 const int pr = p.row + r, j = A.by_group.div(pr);
-                x[i] = __ldg(reinterpret_cast<const uint2 *>(
+                return __ldg(reinterpret_cast<const uint2 *>(
                     static_cast<const uint16_t *>(A.q) + (int64_t)(p.token + j) * A.q_st[0] +
                     (p.h * A.group + (pr - j * A.group)) * A.q_st[1] + lane * 4));
-            }
+            };
             auto bits = [&](const float2 &f) -> uint32_t {  // of the larger finite magnitude
                 const uint32_t a = __float_as_uint(f.x) & 0x7fffffffu, b = __float_as_uint(f.y) & 0x7fffffffu;
                 return max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u);
             };
+            // (all rows' loads in flight; the second time they come from near by)
+            {
+                uint2 x[kMine];
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                top = max(top, max(bits(pair_of(x[i].x, T())), bits(pair_of(x[i].y, T()))));
+                for (int i = 0; i < kMine; ++i) x[i] = load(i);
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    top = max(top, max(bits(pair_of(x[i].x, T())), bits(pair_of(x[i].y, T()))));
+            }
             top = __reduce_max_sync(0xffffffffu, top);
             if (lane == 0) sh.q_top[tw] = top;
             group_barrier(3);
@@ -404,16 +407,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
             const int e = min(max((int)(top >> 23) - 127 - 15 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 120);
             const float f = A.q_mode == 1 ? -power_of_two(-e) : power_of_two(-e);
             char *to = smem + L::kQ + qb * L::kQuery;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < kMine; ++i) {
                 const int r = tw + 4 * i;
-                const float2 a = pair_of(x[i].x, T()), b = pair_of(x[i].y, T());
+                const uint2 x = load(i);
+                const float2 a = pair_of(x.x, T()), b = pair_of(x.y, T());
                 float y[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
                 // an infinity makes its row NaN, as a NaN does
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     if (!(fabsf(y[m]) <= 57344.f)) y[m] = __uint_as_float(0x7fffffffu);
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < kParts; ++part)
                     *reinterpret_cast<uint32_t *>(to + (part * kRows8 + r) * 128 + ((lane / 4) ^ (r & 7)) * 16 +
                                                   lane % 4 * 4) = split_off(y);
@@ -424,8 +428,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
             if (lane == 0) mbar_arrive(&sh.q_full[qb]);
             return !group_any(3, !ok);
         };
-        bool ok = prepare() && (!more || prepare());
-        while (ok && done < ready) {
+        bool ok = true;
+        for (;;) {
+            while (ok && more && ready < done + 2) ok = prepare();  // two tiles ahead
+            if (!ok || done == ready) break;
             const Piece &p = sh.pieces[done % kPieces];
             const uint32_t tb = done & 1, turn = done >> 1 & 1;
             const int blocks = p.n, row0 = p.row, rows = p.rows;
@@ -585,7 +591,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.piece_empty[done % kPieces]);
             ++done;
-            if (more) ok = prepare();
         }
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs8));
@@ -686,9 +691,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     tc::fence_after();
                     if (tc::elect()) {
                         const uint64_t kd = k_desc + st * (kRaw / 16), qd = q_desc + qb * (L::kQuery / 16);
-#pragma unroll 1
-                        for (int s = 0; s < steps; ++s)
-                            tc::mma_f8(tm + sb * L::kScoreCols, kd + s * 2, qd + s * 2, kIdescS, s > 0);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (s < steps)
+                                tc::mma_f8(tm + sb * L::kScoreCols, kd + s * 2, qd + s * 2, kIdescS, s > 0);
                         tc::commit(&sh.k_empty[st]);
                         tc::commit(&sh.s_full[sb]);
                         if (i + 1 == blocks) tc::commit(&sh.q_empty[qb]);
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     tc::fence_after();
                     if (tc::elect()) {
                         const uint64_t vd = v_desc + b * (2 * kRaw / 16), pd = p_desc + b * 4;  // (64 bytes)
-#pragma unroll 1
+#pragma unroll
                         for (int s = 0; s < kKeys / 16; ++s)
                             tc::mma_ss(tm + (tb * 2 + b) * L::kOutCols, vd + s * (2048 / 16), pd + s * (2048 / 16),
                                        kIdescO, i > 1 || s > 0);
@@ -901,28 +907,27 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     }
                     auto sees = [&](int r) -> bool { return r >= r0 && r < r1; };
                     auto scores = [&]() {
-                        const uint64_t key_scale2 = pair2(key_scale, key_scale);
+                        // the small parts first
+                        uint32_t x[kAtOnce * kRows8];
 #pragma unroll
-                        for (int o0 = 0; o0 < kRows8 / 8; o0 += kAtOnce) {
-                            uint32_t x[kParts][kAtOnce][8];
-#pragma unroll
-                            for (int o = 0; o < kAtOnce; ++o)
-#pragma unroll
-                                for (int part = 0; part < kParts; ++part)
-                                    tc::ld8(x[part][o], t_s + part * kRows8 + (o0 + o) * 8);
+                        for (int p0 = (kParts - 1) / kAtOnce * kAtOnce; p0 >= 0; p0 -= kAtOnce) {
+                            constexpr int kRest = kParts % kAtOnce ? kParts % kAtOnce : kAtOnce;
+                            const bool rest = p0 + kAtOnce > kParts;
+                            if (rest) tc::ld_columns<kRest * kRows8>(x, t_s + p0 * kRows8);
+                            else tc::ld_columns<kAtOnce * kRows8>(x, t_s + p0 * kRows8);
                             tc::wait_ld();
 #pragma unroll
-                            for (int o = 0; o < kAtOnce; ++o)
+                            for (int r = 0; r < kRows8 / 2; ++r) {
 #pragma unroll
-                                for (int c = 0; c < 8; c += 2) {
-                                    // the small parts first
-                                    uint64_t sum = bits2(x[kParts - 1][o][c], x[kParts - 1][o][c + 1]);
-#pragma unroll
-                                    for (int part = kParts - 2; part >= 0; --part)
-                                        sum = add2(sum, bits2(x[part][o][c], x[part][o][c + 1]));
-                                    y[(o0 + o) * 4 + c / 2] = mul2(sum, key_scale2);
+                                for (int part = (rest ? kRest : kAtOnce) - 1; part >= 0; --part) {
+                                    const uint64_t z = bits2(x[part * kRows8 + 2 * r], x[part * kRows8 + 2 * r + 1]);
+                                    y[r] = p0 + part == kParts - 1 ? z : add2(y[r], z);
                                 }
+                            }
                         }
+                        const uint64_t key_scale2 = pair2(key_scale, key_scale);
+#pragma unroll
+                        for (int r = 0; r < kRows8 / 2; ++r) y[r] = mul2(y[r], key_scale2);
                         if (__builtin_expect(masked, 0)) {
 #pragma unroll
                             for (int r = 0; r < kRows8 / 2; ++r) {

@@ -71,6 +71,21 @@ __device__ __forceinline__ void ld8(uint32_t (&r)[8], uint32_t addr) {
         : "r"(addr));
 }
 
+// N columns (a multiple of 8) to the first N of r, by as wide loads as there are.
+template <int N, int kAt = 0, int kSize>
+__device__ __forceinline__ void ld_columns(uint32_t (&r)[kSize], uint32_t addr) {
+    static_assert(N % 8 == 0 && kAt + N <= kSize, "columns");
+    if constexpr (N >= 32) {
+        ld32(reinterpret_cast<uint32_t(&)[32]>(r[kAt]), addr);
+        ld_columns<N - 32, kAt + 32>(r, addr + 32);
+    } else if constexpr (N >= 16) {
+        ld16(reinterpret_cast<uint32_t(&)[16]>(r[kAt]), addr);
+        ld_columns<N - 16, kAt + 16>(r, addr + 16);
+    } else if constexpr (N >= 8) {
+        ld8(reinterpret_cast<uint32_t(&)[8]>(r[kAt]), addr);
+    }
+}
+
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
