@@ -405,7 +405,7 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
  * those of the codes and the queries as they are; a query's values below 2^-24 of the
  * largest of its tile (up to 32 rows) are good to 2^-33 of it; weights, times the
  * values' scales relative to the largest scale met, are rounded to 11 bits (those below
- * 2^-21 of the largest to steps of 2^-31 of it).  A query that holds a NaN or an
+ * 2^-18 of the largest to steps of 2^-28 of it).  A query that holds a NaN or an
  * infinity gives NaN for a row that sees a slot.  Slots inside a sequence's length must
  * hold what sv_append_kv_normed writes, codes of 0x7f and 0xff excepted; what unused slots hold
  * does not matter.  A key or value whose scale is NaN gives NaN for the rows that see

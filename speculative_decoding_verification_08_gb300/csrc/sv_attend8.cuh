@@ -20,12 +20,14 @@
 // have: four warps turn codes into fp16 (exact).  Their scales go into the weights,
 // relative to a power of two that follows the largest scale: weight times scale, in
 // fp16 and taken 2^7 times as large, is the one rounding between fp32 scores and the
-// result (11 bits; what is below 2^-21 of the row's and the scales' largest is rounded
-// to steps of 2^-31 of them).
+// result (11 bits; what is below 2^-18 of the row's and the scales' largest is rounded
+// to steps of 2^-28 of them).
 //
 // Softmax: weights are relative to a reference per row, which follows the row's
-// maximum only when a score is more than 2^8 above it; whether any is, is one vote
-// of the 128 threads per block, and finding the new maxima the rare way.  Two groups of
+// maximum only when a weight would not fit fp16; whether any is so large, is one vote
+// of the 128 threads per block, and finding the new maxima the rare way (a new reference
+// is 2^3 above the maximum: with 24 rows of random scores, heavy-tailed by the keys' sizes,
+// 0.2 of the blocks go that way, the first of each tile among them, and 0.34 without).  Two groups of
 // four warps take the even and the odd blocks of a tile, each with scores, weights,
 // outputs and references of its own, and join them at the tile's end.
 //
@@ -51,6 +53,8 @@ constexpr int kSoftmaxRegs8 = 136, kValueRegs8 = 56, kIssueRegs8 = 56, kTileRegs
 static_assert(128 * (2 * kSoftmaxRegs8 + kValueRegs8 + kIssueRegs8 + kTileRegs8) <= kThreads8 * 96, "register split");
 constexpr int kRaw = kKeys * 128;     // a block of codes
 constexpr int kScaleRing = 3;         // pairs of blocks of scales
+constexpr float kGrowAbove = 8.9f;    // log2: with kHalfLift and the largest scale 2^15.9
+constexpr float kHeadroom = 3.f;      // log2, of a new reference above the maximum
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
 constexpr int kNoScale = -200;        // below every e8m0 exponent
 
@@ -967,10 +971,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                 high = fmaxf(high, own.across[w][lane]);
                                 most = max(most, own.exponent[w]);
                             }
-                            // (one more, so that the next larger scale is no new reference)
-                            const int now_e = most > exponent ? most + 1 : exponent;
-                            const bool grow = high + minus > kRescaleAbove;
-                            const float now = grow ? -high : minus;
+                            const int now_e = max(most, exponent);
+                            const bool grow = high + minus > kGrowAbove;
+                            const float now = grow ? -high - kHeadroom : minus;
                             const float f = !grow ? 1.f : minus == kUnset ? 0.f : ex2(now - minus);
                             const float fe = exponent == kNoScale ? 0.f : ex2((float)(exponent - now_e));
                             const bool scaled = __any_sync(0xffffffffu, grow && minus != kUnset) || now_e != exponent;
@@ -1020,12 +1023,12 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             unpair2(y[2 * o + 1], a, b);
                             top = max3(top, a, b);
                         }
-                        if (rare || !group_any(1 + g, top > kRescaleAbove || e8 > exponent)) break;
+                        if (rare || !group_any(1 + g, top > kGrowAbove || e8 > exponent)) break;
                     }
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.s_empty[g]);
-                    // a weight times its scale, in fp16's range (2^15 at most)
+                    // a weight times its scale, in fp16's range
                     const int shift = max(e8, -127) - exponent + (int)kHalfLift;
                     const float value_scale = shift < -126 ? 0.f : power_of_two(shift);
                     const uint64_t value_scale2 = pair2(value_scale, value_scale);
