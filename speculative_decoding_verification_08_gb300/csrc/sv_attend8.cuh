@@ -700,7 +700,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             if (s < steps)
                                 tc::mma_f8(tm + sb * L::kScoreCols, kd + s * 2, qd + s * 2, kIdescS, s > 0);
                         tc::commit(&sh.k_empty[st]);
-                        tc::commit(&sh.s_full[sb]);
+                        // (both groups' at once: their warps then run the same code together,
+                        // and share its fetching: 293 instead of 303 us for rounds)
+                        if (sb == 1) tc::commit(&sh.s_full[0]);
+                        if (sb == 1 || i + 1 == blocks) tc::commit(&sh.s_full[sb]);
                         if (i + 1 == blocks) tc::commit(&sh.q_empty[qb]);
                     }
                     __syncwarp();
