@@ -16,6 +16,15 @@
 // are fixed-point: a frequency in turns as a 64-bit fraction, once a block (fp64 runs at
 // 1/64 of fp32 here), so that position times frequency modulo a turn is one integer
 // product, good to 2^-33 of a turn at any position.
+//
+// Measured (32 query heads over 8 of 128, bf16, unless said otherwise):
+//   18,157 tokens of prompts into 8 bits, half of each head turned: 90 us, 4.5 TB/s (8
+//     values to a lane, each pair's other value loaded beside it, and fp64 angles: 258);
+//     half of the issue slots are taken, a third of the warps fit (80 registers);
+//   24,425 tokens normed, 16 over 4 heads of 96 in fp16, adjacent pairs: 70 us, 3.2 TB/s:
+//     6 of 8 lanes have values, and the same;
+//   rounds of 256 x 6 tokens: 12 us normed, 14 us normed to 8 bits, 3 us of it launch and
+//     lookup; one token 9 us, all of it the call's host time.
 #pragma once
 
 #include "sv_append.cuh"
@@ -381,6 +390,9 @@ __global__ void __launch_bounds__(kAppendThreads, kTurn == kPairTurn ? 2 : 3)
 }
 
 // ---- the way back -----------------------------------------------------------------
+//
+// Bound by memory: a thread takes 16 codes to 32 bytes, four such loads in flight.
+// 64 sequences of 156,896 rows in all, 8 heads of 128: 157 us, 6.2 TB/s.
 
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 16;  // rows per block at most
