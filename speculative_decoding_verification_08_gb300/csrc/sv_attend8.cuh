@@ -627,9 +627,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 if (blocks == 0) continue;
                 // page ids of 32 boxes at a time, the next ones on their way
                 auto pages_of = [&](int box) -> int {
+                    if (box + lane >= blocks * boxes) return kNoPage;  // (slots past 2^31 among them)
                     const int s0 = lo * kKeys + (box + lane) * A.piece;
-                    if (s0 >= min(end, (lo + blocks) * kKeys) || s0 + A.piece <= first) return kNoPage;
-                    return __ldg(table + A.by_page.div(s0));
+                    return s0 >= end || s0 + A.piece <= first ? kNoPage : __ldg(table + A.by_page.div(s0));
                 };
                 auto checked = [&](int id) -> int {
                     if (id != kNoPage && (id < 0 || id >= A.batch.num_pages)) {
@@ -773,8 +773,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const uint8_t *ks = S.k + q.h * S.k_st[2], *vs = S.v + q.h * S.v_st[2];
                 reader.done(sh, lane);
                 auto page_of = [&](int i) -> int {
+                    if (i >= pairs) return -1;
                     const int s0 = begin + i * 2 * kKeys;
-                    return i >= pairs || s0 >= end || s0 + 8 <= first ? -1 : __ldg(table + A.by_page.div(s0));
+                    return s0 >= end || s0 + 8 <= first ? -1 : __ldg(table + A.by_page.div(s0));
                 };
                 // bytes are loaded a pair ahead of their use (and put together then), page
                 // ids two
