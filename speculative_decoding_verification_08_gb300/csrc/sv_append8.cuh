@@ -125,7 +125,7 @@ __device__ __forceinline__ RowPlace place_of(const Batch &A, const FastDiv &by_p
 
 // ---- append ----------------------------------------------------------------------
 
-constexpr int kNormTokens = 8;  // tokens per block at most
+constexpr int kNormTokens = 16;  // tokens per block at most
 
 // How pairs lie.  kPackTurn: both halves start on a pack (rot_dim a multiple of 16) and
 // lane l < rot_dim / 16 has packs l of both; kAdjacentTurn: within a pack (or nothing
@@ -222,36 +222,36 @@ __global__ void __launch_bounds__(kAppendThreads, kTurn == kPairTurn ? 2 : 3)
                     }
                 }
         }
-        // two tokens at a time
-        constexpr int kAhead = 2;
+        // the next token's values are on their way while one is worked on
+        struct Values {
+            P own[2], other[2];
+        };
+        auto load = [&](int w) -> Values {
+            Values v{};
+            if (!active || w >= here) return v;
+            const uint16_t *from = src + w * step;
+            if (in0) v.own[0] = *reinterpret_cast<const P *>(from + at0);
+            if (in1) v.own[1] = *reinterpret_cast<const P *>(from + at1);
+            if (kTurn == kPairTurn && turns)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (in0) v.other[0].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at0 + 2 * e));
+                    if (in1) v.other[1].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at1 + 2 * e));
+                }
+            return v;
+        };
+        Values now = load(0);
 #pragma unroll 1
-        for (int wa = 0; wa < here; wa += kAhead) {
-            P own[kAhead][2], other[kAhead][2];
-#pragma unroll
-            for (int t = 0; t < kAhead; ++t) {
-                own[t][0] = own[t][1] = other[t][0] = other[t][1] = P{};
-                if (!active || wa + t >= here) continue;
-                const uint16_t *from = src + (wa + t) * step;
-                if (in0) own[t][0] = *reinterpret_cast<const P *>(from + at0);
-                if (in1) own[t][1] = *reinterpret_cast<const P *>(from + at1);
-                if (kTurn == kPairTurn && turns)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (in0) other[t][0].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at0 + 2 * e));
-                        if (in1) other[t][1].x[e] = *reinterpret_cast<const uint32_t *>(from + other_at(at1 + 2 * e));
-                    }
-            }
+        for (int w = 0; w < here; ++w) {
+            const Values next = load(w + 1);
             __syncwarp();  // q_out may be q: a head's loads come before its stores
-#pragma unroll
-            for (int t = 0; t < kAhead; ++t) {
-                const int w = wa + t;
-                if (w >= here) break;
+            {
                 uint64_t y0[4], y1[4], o0[4], o1[4];
-                unpack<T>(own[t][0], y0);
-                unpack<T>(own[t][1], y1);
+                unpack<T>(now.own[0], y0);
+                unpack<T>(now.own[1], y1);
                 if (kTurn == kPairTurn) {
-                    unpack<T>(other[t][0], o0);
-                    unpack<T>(other[t][1], o1);
+                    unpack<T>(now.other[0], o0);
+                    unpack<T>(now.other[1], o1);
                 }
                 if (any_norm) {
                     uint64_t sum2 = 0;
@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(kAppendThreads, kTurn == kPairTurn ? 2 : 3)
                     }
                 }
             }
+            now = next;
         }
     }
 }
