@@ -493,27 +493,24 @@ __global__ void __launch_bounds__(kThreads8, 1)
             T *out = static_cast<T *>(A.out) + (int64_t)(p.token + j_first) * A.o_st[0] +
                      ((int64_t)p.h * A.group + head) * A.o_st[1] + tt;
             const int64_t wrap = A.o_st[0] - A.group * A.o_st[1];
+            // (a row at a time: what this loop is long, the softmax's leaves the cache)
 #pragma unroll 1
-            for (int r0 = 0; r0 < rows; r0 += 8) {
-                uint32_t u[2][8] = {};  // (a group that had no block left none)
-                if (blocks > 0) tc::ld8(u[0], t_o + tb * 2 * L::kOutCols + r0);
-                if (blocks > 1) tc::ld8(u[1], t_o + (tb * 2 + 1) * L::kOutCols + r0);
+            for (int r = 0; r < rows; ++r) {
+                uint32_t u0 = 0, u1 = 0;  // (a group that had no block left none)
+                if (blocks > 0) u0 = tc::ld1(t_o + tb * 2 * L::kOutCols + r);
+                if (blocks > 1) u1 = tc::ld1(t_o + (tb * 2 + 1) * L::kOutCols + r);
                 tc::wait_ld();
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float f0 = __shfl_sync(0xffffffffu, f[0], r0 + r), f1 = __shfl_sync(0xffffffffu, f[1], r0 + r);
-                    const float o = fmaf(f1, __uint_as_float(u[1][r]), f0 * __uint_as_float(u[0][r]));
-                    if (r0 + r >= rows) break;
-                    if (!whole) {
-                        part_out[slot * kSlot + (r0 + r) * 128 + tt] = o;
-                        continue;
-                    }
+                const float f0 = __shfl_sync(0xffffffffu, f[0], r), f1 = __shfl_sync(0xffffffffu, f[1], r);
+                const float o = fmaf(f1, __uint_as_float(u1), f0 * __uint_as_float(u0));
+                if (whole) {
                     if (tt < D) *out = from_f32<T>(o);
-                    out += A.o_st[1];
-                    if (++head == A.group) {
-                        head = 0;
-                        out += wrap;
-                    }
+                } else {
+                    part_out[slot * kSlot + r * 128 + tt] = o;
+                }
+                out += A.o_st[1];
+                if (++head == A.group) {
+                    head = 0;
+                    out += wrap;
                 }
             }
             tc::fence_before();

@@ -63,6 +63,12 @@ __device__ __forceinline__ void ld16(uint32_t (&r)[16], uint32_t addr) {
         : "r"(addr));
 }
 
+__device__ __forceinline__ uint32_t ld1(uint32_t addr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
+    return r;
+}
+
 __device__ __forceinline__ void ld8(uint32_t (&r)[8], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
