@@ -172,9 +172,9 @@ int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CU
 
 // Up to so many packed rows of a sequence and kv head attention goes over the codes
 // directly, above it (and with room for it) the sequences are read back to 16 bits
-// first.  32 sequences of 4096 slots, 32 heads over 8 of 128, bf16: 91 against 252 us
-// for 8 tokens each (32 rows), 261 against 259 for 32, 371 against 277 for 48, 903
-// against 386 for 128; 4 of 32768: 220 against 257 for 32, 407 against 278 for 64.
+// first.  32 sequences of 4096 slots, 32 heads over 8 of 128, bf16: 85 against 252 us
+// for 8 tokens each (32 rows), 248 against 259 for 32, 298 against 271 for 40, 858
+// against 388 for 128; 4 of 32768: 216 against 258 for 32, 269 against 269 for 40.
 constexpr int64_t kDirectRows = 128;
 constexpr size_t kMaxScratch = (size_t)16 << 30;
 

@@ -56,7 +56,9 @@
 namespace sv {
 
 constexpr int kMaxRows8 = 32;   // packed rows of a tile at most
-constexpr int kTileCost8 = 3;   // a tile's fixed cost in key blocks
+// A tile's fixed cost in key blocks: 275 us for rounds of 6 tokens over up to 4096 slots
+// (290 with 3, 281 with 8), 103 over up to 500 (114 and 99).
+constexpr int kTileCost8 = 5;
 constexpr int kThreads8 = 640;
 // Registers per thread after the roles part, of the 640 x 96 that the block is
 // launched with.
@@ -244,7 +246,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                    const __grid_constant__ CUtensorMap vmap) {
     typedef Attend8Smem<T, kRows8> L;
     constexpr int kParts = L::kParts;
-    constexpr int kAtOnce = kParts * kRows8 <= 72 ? kParts : 2;  // parts of scores, as registers allow
+    // parts of scores loaded at once, as registers allow
+    constexpr int kAtOnce = kParts * kRows8 <= 72 ? kParts : kRows8 <= 24 ? 2 : 1;
     constexpr uint32_t kIdescS = tc::instr_desc_f8(kKeys, L::kScoreCols);
     // (bit 15: A's slots are its rows in memory, as B's)
     constexpr uint32_t kIdescO = tc::instr_desc(false, true, 128, L::kOutCols) | (1u << 15);
