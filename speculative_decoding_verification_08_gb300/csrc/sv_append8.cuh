@@ -18,13 +18,14 @@
 // product, good to 2^-33 of a turn at any position.
 //
 // Measured (32 query heads over 8 of 128, bf16, unless said otherwise):
-//   18,157 tokens of prompts into 8 bits, half of each head turned: 90 us, 4.5 TB/s (8
-//     values to a lane, each pair's other value loaded beside it, and fp64 angles: 258);
-//     half of the issue slots are taken, a third of the warps fit (80 registers);
-//   24,425 tokens normed, 16 over 4 heads of 96 in fp16, adjacent pairs: 70 us, 3.2 TB/s:
+//   18,157 tokens of prompts into 8 bits, half of each head turned: 81 us, 5.1 TB/s (90
+//     without the next token's loads ahead and with 8 tokens a block; 258 with 8 values to
+//     a lane, each pair's other value loaded beside it, and fp64 angles); 63 % of the issue
+//     slots are taken, a third of the warps fit (80 registers; 93 with 64);
+//   24,425 tokens normed, 16 over 4 heads of 96 in fp16, adjacent pairs: 60 us, 3.8 TB/s:
 //     6 of 8 lanes have values, and the same;
-//   rounds of 256 x 6 tokens: 12 us normed, 14 us normed to 8 bits, 3 us of it launch and
-//     lookup; one token 9 us, all of it the call's host time.
+//   rounds of 256 x 6 tokens: 12 to 14 us normed, 13 normed to 8 bits, 3 of it launch and
+//     lookup; one token 9 to 11, all of it the call's host time.
 #pragma once
 
 #include "sv_append.cuh"

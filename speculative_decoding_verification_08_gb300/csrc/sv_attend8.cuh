@@ -39,12 +39,12 @@
 // groups and parts and write its rows.  Every wait is bounded, as there.
 //
 // Measured (32 query heads over 8 of 128, bf16, unless said otherwise):
-//   rounds of 6 tokens over up to 4096 slots, 256 sequences: 288 us, 4.2 TB/s.  Without
+//   rounds of 6 tokens over up to 4096 slots, 256 sequences: 270 us, 4.6 TB/s.  Without
 //     its copies the kernel takes as long: the bound is a block's way through four
 //     softmax warps (4000 cycles for two blocks at a time, a tenth of it instructions of
-//     one warp), which the instruction cache feeds (85 % of its requests hit; with waits,
+//     one warp), which the instruction cache feeds (87 % of its requests hit; with waits,
 //     conversions and the queries' preparation unrolled 67 %, and 493 us);
-//   6 tokens over 131071 slots, 2 sequences, 16 over 4 heads of 64 in fp16: 74 us, 10 of
+//   6 tokens over 131071 slots, 2 sequences, 16 over 4 heads of 64 in fp16: 76 us, 10 of
 //     them for pages of 16 slots (16 boxes a block; 4 with pages of 64);
 //   one token over 1000 slots: 12 us, of which 4.5 are the call's, the rest launch,
 //     lookups, one block and the join of the parts.
