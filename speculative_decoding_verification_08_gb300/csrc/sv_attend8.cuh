@@ -27,7 +27,8 @@
 // maximum only when a weight would not fit fp16; whether any is so large, is one vote
 // of the 128 threads per block, and finding the new maxima the rare way (a new reference
 // is 2^3 above the maximum: with 24 rows of random scores, heavy-tailed by the keys' sizes,
-// 0.2 of the blocks go that way, the first of each tile among them, and 0.34 without).  Two groups of
+// 0.2 of the blocks go that way, the first of each tile among them, and 0.34 without:
+// 274 instead of 294 us for rounds).  Two groups of
 // four warps take the even and the odd blocks of a tile, each with scores, weights,
 // outputs and references of its own, and join them at the tile's end.
 //
@@ -56,8 +57,8 @@
 namespace sv {
 
 constexpr int kMaxRows8 = 32;   // packed rows of a tile at most
-// A tile's fixed cost in key blocks: 275 us for rounds of 6 tokens over up to 4096 slots
-// (290 with 3, 281 with 8), 103 over up to 500 (114 and 99).
+// A tile's fixed cost in key blocks: 274 us for rounds of 6 tokens over up to 4096 slots
+// (287 with 3, 281 with 8), 105 over up to 500 (111 and 101).
 constexpr int kTileCost8 = 5;
 constexpr int kThreads8 = 640;
 // Registers per thread after the roles part, of the 640 x 96 that the block is
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                 tc::mma_f8(tm + sb * L::kScoreCols, kd + s * 2, qd + s * 2, kIdescS, s > 0);
                         tc::commit(&sh.k_empty[st]);
                         // (both groups' at once: their warps then run the same code together,
-                        // and share its fetching: 293 instead of 303 us for rounds)
+                        // and share its fetching: 274 instead of 281 us for rounds)
                         if (sb == 1) tc::commit(&sh.s_full[0]);
                         if (sb == 1 || i + 1 == blocks) tc::commit(&sh.s_full[sb]);
                         if (i + 1 == blocks) tc::commit(&sh.q_empty[qb]);
@@ -848,8 +849,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         if (k * per + slot0 >= here)
                             *reinterpret_cast<uint4 *>(raw + src + k * per * 128) = make_uint4(0, 0, 0, 0);
                 }
-                // (not unrolled: 317 us for rounds of 6 tokens over up to 4096 slots, 333 by
-                // four, 391 by eight, for the instruction cache's sake)
+                // (not unrolled, for the instruction cache's sake: 274 us for rounds of 6 tokens
+                // over up to 4096 slots, 281 by four, 363 by eight)
 #pragma unroll 1
                 for (int k = 0; k < rounds; ++k) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(raw + src + k * per * 128);
