@@ -3,7 +3,7 @@
 //
 // Rows are packed as in sv_attend.cuh (the G query heads of a kv head side by side),
 // but the products are the transposed ones: a key block's 128 slots are the 128
-// lanes of tensor memory and the tile's up to kRows8 rows its columns,
+// lanes of tensor memory and the tile's up to 32 rows its columns,
 //   S^T = K Q^T,   O^T += V^T P^T.
 // So a thread has one slot and all rows: the exponentials of a block are spread
 // over four warps however few rows there are, a slot's scales are two numbers of
@@ -12,8 +12,8 @@
 // Keys go to the tensor cores as the e4m3 codes they are.  The queries become 8-bit
 // floats beside them: relative to one power of two for the tile, each value is the
 // sum of 3 (bf16) or 4 (fp16) e5m2 numbers, the nearest to what the ones before it
-// left (3 significant bits each, 2 and the sign of the rest), exact down to 2^-24 of
-// the tile's largest and good to 2^-33 of it below.  The parts are columns of their own
+// left (3 significant bits each, 2 and the sign of the rest): exact down to 2^-24
+// (fp16: 2^-21) of the tile's largest, and good to 2^-31 of it below.  The parts are columns of their own
 // (their products are added in fp32 by the softmax threads), so a block of keys is
 // read from shared memory once.
 // Values need their slots' axis contiguous for the second product, which 16-bit types
@@ -47,8 +47,7 @@
 //     conversions and the queries' preparation unrolled 67 %, and 493 us);
 //   6 tokens over 131071 slots, 2 sequences, 16 over 4 heads of 64 in fp16: 76 us, 10 of
 //     them for pages of 16 slots (16 boxes a block; 4 with pages of 64);
-//   one token over 1000 slots: 12 us, of which 4.5 are the call's, the rest launch,
-//     lookups, one block and the join of the parts.
+//   one token over 1000 slots: 12 us: launch, lookups, one block, join of the parts.
 #pragma once
 
 #include "sv_append8.cuh"
