@@ -402,7 +402,7 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
  *         is 0 where it is not, or where it would be more than 16 GiB.  (Keys and
  *         values past fp16's range saturate there.)
  * Products are accumulated and statistics kept in fp32.  Without scratch: scores are
- * those of the codes and the queries as they are; a query's values below 2^-21 of the
+ * those of the codes and the queries as they are; a query's values below 2^-20 of the
  * largest of its tile (up to 32 rows) are good to 2^-31 of it; weights, times the
  * values' scales relative to the largest scale met, are rounded to 11 bits (those below
  * 2^-18 of the largest to steps of 2^-28 of it).  A query that holds a NaN or an

@@ -12,8 +12,8 @@
 // Keys go to the tensor cores as the e4m3 codes they are.  The queries become 8-bit
 // floats beside them: relative to one power of two for the tile, each value is the
 // sum of 3 (bf16) or 4 (fp16) e5m2 numbers, the nearest to what the ones before it
-// left (3 significant bits each, 2 and the sign of the rest): exact down to 2^-24
-// (fp16: 2^-21) of the tile's largest, and good to 2^-31 of it below.  The parts are columns of their own
+// left (3 significant bits each, 2 and the sign of the rest): exact down to 2^-23
+// (fp16: 2^-20) of the tile's largest, and good to 2^-31 of it below.  The parts are columns of their own
 // (their products are added in fp32 by the softmax threads), so a block of keys is
 // read from shared memory once.
 // Values need their slots' axis contiguous for the second product, which 16-bit types
