@@ -151,3 +151,23 @@ def test_a_paged_cache_of_eight_bits_has_scales():
     assert PagedCache(2, 6, 8, 3, 16, device="cpu")._scales(0) == {}
     with pytest.raises(ValueError):
         c.read(0, ["nobody"])
+
+
+@pytest.mark.parametrize("dt,parts,exact", [(torch.bfloat16, 3, 23), (torch.float16, 4, 20)])
+def test_queries_are_sums_of_e5m2_numbers(dt, parts, exact):
+    """What the attention's split of queries relies on: every value is the sum of so
+    many e5m2 numbers, exactly down to 2^-exact of the largest, to 2^-31 of it below."""
+    x = torch.arange(0, 1 << 16, dtype=torch.int32).to(torch.int16).view(dt).float()
+    x = x[torch.isfinite(x)]
+    for top in (1.0, 1.75, 1.7578125, 1.99, 3.0, 57344.0):
+        top = torch.tensor(top).to(dt).float()
+        m, e = torch.frexp(top)
+        unit = 2.0 ** (int(e) - 16 + (1 if float(m) > 0.875 else 0))   # brings it to 57344 or less
+        y = (x[x.abs() <= top] / unit).double()
+        rest = y.clone()
+        for _ in range(parts):
+            rest = rest - rest.float().to(torch.float8_e5m2).double()
+        largest = float(top) / unit
+        assert 28672 < largest <= 57344
+        assert bool((rest[y.abs() >= largest * 2.0 ** -exact] == 0).all())
+        assert float(rest.abs().max()) <= largest * 2.0 ** -31
