@@ -409,7 +409,7 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
  * infinity gives NaN for a row that sees a slot.  Slots inside a sequence's length must
  * hold what sv_append_kv_normed writes, codes of 0x7f and 0xff excepted; what unused slots hold
  * does not matter.  A key or value whose scale is NaN gives NaN for the rows that see
- * it (with scratch, as for sv_paged_attention, it must not occur). */
+ * it, and for no others. */
 size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads);
 int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
                         const void *q, const int64_t *q_stride, void *out, const int64_t *out_stride,

@@ -410,10 +410,19 @@ struct ReadParams {
     int32_t kv_heads, head_dim, chunks;
     // Whole sequences into pages of their own (page i of sequence b is page b *
     // max_pages + i, slots in order) for the 16-bit attention: `table` is that page
-    // table; slots before every row's window are left out.
+    // table; slots before every row's window are left out.  A key or value that is NaN
+    // becomes a NaN key, whose score is NaN for the rows that see it and masked for others.
     int32_t *table;
     int32_t window;
 };
+
+// x within fp16's largest; NaN stays NaN.
+__device__ __forceinline__ float fp16_range(float x) {
+    asm("{ .reg .f32 y; min.NaN.f32 y, %0, %1; max.NaN.f32 %0, y, %2; }"
+        : "+f"(x)
+        : "f"(65504.f), "f"(-65504.f));
+    return x;
+}
 
 // Sixteen codes times a scale, in 16 bits.
 template <class T, bool kSaturate>
@@ -425,8 +434,8 @@ __device__ __forceinline__ void expand(uint4 c, float f, uint4 &lo, uint4 &hi) {
         float2 a = values_of(w[e] & 0xffffu), b = values_of(w[e] >> 16);
         a.x *= f, a.y *= f, b.x *= f, b.y *= f;
         if (kSaturate) {  // fp16: a vector's largest may have been rounded past 65504
-            a.x = fminf(fmaxf(a.x, -65504.f), 65504.f), a.y = fminf(fmaxf(a.y, -65504.f), 65504.f);
-            b.x = fminf(fmaxf(b.x, -65504.f), 65504.f), b.y = fminf(fmaxf(b.y, -65504.f), 65504.f);
+            a.x = fp16_range(a.x), a.y = fp16_range(a.y);
+            b.x = fp16_range(b.x), b.y = fp16_range(b.y);
         }
         o[2 * e] = bits_of(a.x, a.y, T());
         o[2 * e + 1] = bits_of(b.x, b.y, T());
@@ -488,14 +497,14 @@ __global__ void __launch_bounds__(kReadThreads)
     constexpr int kAhead = 4;
     for (int i0 = threadIdx.x; i0 < items; i0 += kAhead * kReadThreads) {
         uint4 x[kAhead], x2[kAhead];
-        uint32_t scale[kAhead];
+        uint32_t scale[kAhead], value_scale[kAhead];  // (kPages: also a key's value's)
         uint16_t *to[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
             const int i = i0 + e * kReadThreads;
             to[e] = nullptr;
             x[e] = x2[e] = make_uint4(0, 0, 0, 0);
-            scale[e] = 127;
+            scale[e] = value_scale[e] = 127;
             if (i >= items) continue;
             const int head_of_all = A.by_chunks.div(i), ch = i - head_of_all * A.chunks;
             const int row_and_kind = A.by_heads.div(head_of_all), h = head_of_all - row_and_kind * A.kv_heads;
@@ -511,6 +520,7 @@ __global__ void __launch_bounds__(kReadThreads)
                     static_cast<const uint8_t *>(kind ? A.v_cache : A.k_cache) + from));
                 scale[e] = __ldg(kind ? A.scales.v + p.vs + h * A.scales.v_st[2]
                                       : A.scales.k + p.ks + h * A.scales.k_st[2]);
+                if (kPages) value_scale[e] = __ldg(A.scales.v + p.vs + h * A.scales.v_st[2]);
             } else {
                 const uint4 *at = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(kind ? A.v_cache : A.k_cache) + from);
@@ -522,6 +532,15 @@ __global__ void __launch_bounds__(kReadThreads)
 #pragma unroll
         for (int e = 0; e < kAhead; ++e) {
             if (!to[e]) continue;
+            if (kPages && value_scale[e] == kScaleNan) {
+                // The 16-bit attention wants finite values in slots that rows do not see
+                // (weights of zero times them must be zero), but masks scores: a vector
+                // that is NaN is left to the key, and the value is zeros.
+                const int i = i0 + e * kReadThreads;
+                const bool key = (A.by_heads.div(A.by_chunks.div(i)) & 1) == 0;
+                if (!key) x[e] = make_uint4(0, 0, 0, 0);
+                scale[e] = key ? kScaleNan : 127;
+            }
             if (kEight) expand<T, kPages && __is_same(T, __half)>(x[e], scale_of(scale[e]), x[e], x2[e]);
             reinterpret_cast<uint4 *>(to[e])[0] = x[e];
             if (kEight) {
