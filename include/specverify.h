@@ -398,9 +398,13 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
  * or SV_F16), and the keys and values the codes times their scales.
  *   scratch  NULL, or sv_paged_attention_scratch_size(cache, q_heads) bytes, 256-byte
  *         aligned, for this call alone: the sequences are then read back to 16 bits
- *         first (two kernels), which is faster when they have many new tokens; the size
- *         is 0 where it is not, or where it would be more than 16 GiB.  (Keys and
- *         values past fp16's range saturate there.)
+ *         first (two kernels), which is faster when they have many new tokens.  The size
+ *         is that of the table's or of the cache's pages in 16 bits, whichever are fewer,
+ *         whatever the sequences' lengths (they are known on the device alone); it is 0
+ *         where reading back is not faster for the batch's average of new tokens, where
+ *         the table's slots would be more than 16 GiB in 16 bits, and for more than 65536
+ *         kv heads (scratch is refused for these two).  (Keys and values past fp16's
+ *         range saturate there.)
  * Products are accumulated and statistics kept in fp32.  Without scratch: scores are
  * those of the codes and the queries as they are; a query's values below 2^-20 of the
  * largest of its tile (up to 32 rows) are good to 2^-31 of it; weights, times the

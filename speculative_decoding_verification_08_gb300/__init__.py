@@ -720,7 +720,16 @@ def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, 
     window > 0, scale 1 / sqrt(D) by default; q_heads a multiple of kv_heads.
     Arrays as for append_kv; a float8_e4m3fn cache comes with its k_scale and
     v_scale.  Rows that see nothing are zeros.  Returns out
-    [N][q_heads][D]."""
+    [N][q_heads][D].
+
+    Over an 8-bit cache whose sequences have many new tokens (more than 128 rows,
+    tokens times q_heads / kv_heads, on the batch's average) the call first reads
+    them back to 16 bits, into memory of its own from the current stream's pool:
+    four bytes for each key and value pair of the table's pages or of the cache's,
+    whichever are fewer.  Where that much cannot be had, or the table's slots
+    would be more than 16 GiB so, it attends to the codes all the same (slower
+    for such batches).  float16 only: keys and values past 65504, which the
+    codes hold, saturate when they are read back."""
     if k_scale is None and v_scale is None:
         return _call("paged_attention", k_cache, "k_cache",
                      (q, k_cache, v_cache, pages, q_start, kv_len, scale, window, out), ws, stream)

@@ -122,14 +122,19 @@ sv::ReadParams read_params(const sv_paged_cache *c, const sv_cache_scales *s) {
     return A;
 }
 
-// The batch's sequences in 16 bits: keys, values and a page table.
+// Room for the batch's sequences in 16 bits: keys and values, in pages of their own with
+// a page table (page i of sequence b is page b * max_pages + i), or, where the cache has
+// fewer pages than the table has entries, in its pages under their own numbers.
 struct Scratch {
+    bool own_pages;
     size_t half, table, bytes;
-    explicit Scratch(const sv_paged_cache *c) {
-        const size_t slots = (size_t)c->B * c->max_pages * c->page_size;
-        half = round_up(slots * c->kv_heads * c->head_dim * 2);
+    explicit Scratch(const sv_paged_cache *c) {  // (can_read_back)
+        const int64_t entries = (int64_t)c->B * c->max_pages;
+        own_pages = entries <= c->num_pages;
+        const size_t rows = (size_t)std::min<int64_t>(entries, c->num_pages) * c->page_size;
+        half = round_up(rows * c->kv_heads * c->head_dim * 2);
         table = 2 * half;
-        bytes = table + round_up((size_t)c->B * c->max_pages * sizeof(int32_t));
+        bytes = table + (own_pages ? round_up((size_t)entries * sizeof(int32_t)) : 0);
     }
 };
 
@@ -176,7 +181,17 @@ int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CU
 // for 8 tokens each (32 rows), 248 against 259 for 32, 298 against 271 for 40, 858
 // against 388 for 128; 4 of 32768: 216 against 258 for 32, 269 against 269 for 40.
 constexpr int64_t kDirectRows = 128;
-constexpr size_t kMaxScratch = (size_t)16 << 30;
+// Reading back looks at every slot of the page table (a block for 16 of them, most of
+// which end at once where sequences are short): not past a table whose slots would be so
+// many bytes in 16 bits.
+constexpr size_t kMaxTable = (size_t)16 << 30;
+constexpr int32_t kMaxReadHeads = 1 << 16;  // (a block's items are numbered by 32 bits)
+
+// Whether the sequences may be read back.
+bool can_read_back(const sv_paged_cache *c) {
+    const unsigned __int128 slots = (unsigned __int128)c->B * c->max_pages * c->page_size;
+    return c->kv_heads <= kMaxReadHeads && slots * c->kv_heads * c->head_dim * 4 <= kMaxTable;
+}
 
 // Packed rows of a sequence and kv head, on average and rounded up.
 int64_t average_rows(const sv_paged_cache *c, int32_t q_heads) {
@@ -271,7 +286,7 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
                size_t workspace_bytes, sv_stream_t stream) {
     int rc = check_either(cache, scales, dtype);
     if (rc != SV_OK) return rc;
-    if (cache->kv_heads > (1 << 16)) return SV_EINVAL;
+    if (cache->kv_heads > kMaxReadHeads) return SV_EINVAL;
     if (cache->B == 0 || cache->tokens == 0) return SV_OK;
     if (!k_out || !v_out || !k_out_stride || !v_out_stride || !vec_ok(k_out, k_out_stride, 2) ||
         !vec_ok(v_out, v_out_stride, 2))
@@ -296,8 +311,7 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
 size_t sv_paged_attention_scratch_size(const sv_paged_cache *cache, int32_t q_heads) {
     if (check_cache(cache, true) != SV_OK || q_heads < 1 || cache->B == 0 || cache->tokens == 0) return 0;
     if (q_heads % cache->kv_heads != 0 || average_rows(cache, q_heads) <= kDirectRows) return 0;
-    const size_t bytes = Scratch(cache).bytes;
-    return bytes <= kMaxScratch ? bytes : 0;
+    return can_read_back(cache) ? Scratch(cache).bytes : 0;
 }
 
 int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales *scales, int32_t dtype,
@@ -314,6 +328,7 @@ int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales
     if (cache->B == 0 || cache->tokens == 0) return SV_OK;
     if (!q || !out || !q_stride || !out_stride || !vec_ok(q, q_stride, 2) || !vec_ok(out, out_stride, 2))
         return SV_EINVAL;
+    if (scratch && !can_read_back(cache)) return SV_EINVAL;
     const CurrentDevice here;
     sv::Batch batch{};
     if ((rc = bind_cache(here, cache, workspace, workspace_bytes, batch)) != SV_OK) return rc;
@@ -354,13 +369,12 @@ int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales
     const Scratch room(cache);
     if (scratch_bytes < room.bytes || (reinterpret_cast<uintptr_t>(scratch) % kAlign) != 0 || !here.holds(scratch))
         return SV_EWORKSPACE;
-    if ((int64_t)cache->B * cache->max_pages > INT32_MAX) return SV_ETOOLARGE;  // its pages are numbered
     sv::ReadParams A = read_params(cache, scales);
     A.batch = batch;
     char *base = static_cast<char *>(scratch);
     A.k = base;
     A.v = base + room.half;
-    A.table = reinterpret_cast<int32_t *>(base + room.table);
+    A.table = room.own_pages ? reinterpret_cast<int32_t *>(base + room.table) : nullptr;
     A.window = window;
     for (int64_t *s : {A.k_st, A.v_st}) {
         s[0] = (int64_t)cache->kv_heads * cache->head_dim;
@@ -380,9 +394,11 @@ int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales
         s[1] = (int64_t)cache->kv_heads * cache->head_dim;
         s[2] = cache->head_dim;
     }
-    plain.num_pages = cache->B * cache->max_pages;
-    plain.pages = A.table;
-    plain.pages_stride = cache->max_pages;
+    if (room.own_pages) {
+        plain.num_pages = cache->B * cache->max_pages;
+        plain.pages = A.table;
+        plain.pages_stride = cache->max_pages;
+    }
     rc = sv_paged_attention(&plain, q, q_stride, out, out_stride, q_heads, scale, window, workspace,
                             workspace_bytes, stream);
     if (rc == SV_OK) g_last_kernels = 2;

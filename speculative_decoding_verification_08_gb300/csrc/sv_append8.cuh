@@ -408,10 +408,11 @@ struct ReadParams {
     void *k, *v;
     int64_t k_st[2], v_st[2];   // row and head strides of the outputs, elements
     int32_t kv_heads, head_dim, chunks;
-    // Whole sequences into pages of their own (page i of sequence b is page b *
-    // max_pages + i, slots in order) for the 16-bit attention: `table` is that page
-    // table; slots before every row's window are left out.  A key or value that is NaN
-    // becomes a NaN key, whose score is NaN for the rows that see it and masked for others.
+    // Whole sequences into pages of 16 bits, slots in order, for the 16-bit attention:
+    // page i of sequence b is page b * max_pages + i, and `table` that page table; or
+    // (NULL) pages keep their numbers (one that sequences share is written by each, alike).
+    // Slots before every row's window are left out.  A key or value that is NaN becomes a
+    // NaN key, whose score is NaN for the rows that see it and masked for others.
     int32_t *table;
     int32_t window;
 };
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(kReadThreads)
     const int64_t r0 = (int64_t)blockIdx.x * per_block;
     wait_for_primary_grid();
     int here;
+    int64_t row0 = r0;  // first row of the outputs
     if (kPages) {
         // a block's rows lie in one sequence's pages (per_block divides page_size)
         const int64_t per_sequence = (int64_t)A.batch.max_pages * A.batch.page_size;
@@ -462,13 +464,17 @@ __global__ void __launch_bounds__(kReadThreads)
         if (s.bad || s.n == 0 || slot0 >= s.len) return;
         const int32_t first = A.window > 0 ? s.len - s.n - A.window + 1 : 0;
         const int32_t pg = A.by_page.div(slot0);
-        if (threadIdx.x == 0 && slot0 - pg * A.batch.page_size == 0)
+        if (A.table && threadIdx.x == 0 && slot0 - pg * A.batch.page_size == 0)
             A.table[(int64_t)b * A.batch.max_pages + pg] = b * A.batch.max_pages + pg;
         if ((pg + 1) * A.batch.page_size <= first) return;  // (the attention skips whole pages only)
+        const int32_t id = __ldg(A.batch.pages + b * A.batch.pages_stride + pg);
+        const bool ok = id >= 0 && id < A.batch.num_pages;
+        if (!ok && threadIdx.x == 0) atomicOr(A.batch.status, SV_STATUS_BAD_PAGE);
+        if (!A.table) {
+            if (!ok) return;  // (zeros to the attention, too)
+            row0 = (int64_t)id * A.batch.page_size + (slot0 - pg * A.batch.page_size);
+        }
         if (warp == 0) {
-            const int32_t id = __ldg(A.batch.pages + b * A.batch.pages_stride + pg);
-            const bool ok = id >= 0 && id < A.batch.num_pages;
-            if (!ok && lane == 0) atomicOr(A.batch.status, SV_STATUS_BAD_PAGE);
             for (int w = lane; w < here; w += 32) {
                 const int64_t in = slot0 + w - pg * A.batch.page_size;
                 RowPlace p = {-1, -1, -1, -1, slot0 + w < s.len, 0};
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(kReadThreads)
             const int w = row_and_kind >> 1, kind = row_and_kind & 1;
             const RowPlace &p = place[w];
             if (!p.known) continue;
-            to[e] = static_cast<uint16_t *>(kind ? A.v : A.k) + (r0 + w) * (kind ? A.v_st[0] : A.k_st[0]) +
+            to[e] = static_cast<uint16_t *>(kind ? A.v : A.k) + (row0 + w) * (kind ? A.v_st[0] : A.k_st[0]) +
                     h * (kind ? A.v_st[1] : A.k_st[1]) + ch * 16;
             if (p.k < 0) continue;  // no such slot or page: zeros
             const int64_t from = (kind ? p.v + h * A.vc_st[2] : p.k + h * A.kc_st[2]) + ch * 16;

@@ -14,6 +14,7 @@
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/util/Exception.h>
 
 #include <cmath>
 #include <limits>
@@ -361,8 +362,14 @@ PyObject *paged_attention_scaled(PyObject *const *a) {
     }
     const int32_t window = int32(integer(a[7]), "window"), q_heads = int32(heads, "q heads");
     // (from the current stream's pool, as the outputs)
-    const size_t bytes = g_scratch(&P.c, q_heads);
-    if (bytes) scratch = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+    size_t bytes = g_scratch(&P.c, q_heads);
+    if (bytes) {
+        try {
+            scratch = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+        } catch (const c10::OutOfMemoryError &) {
+            bytes = 0;  // (what it is for is faster, not needed)
+        }
+    }
     check(g_attend8(&P.c, P.scales_or_null(), code_of(P.type), hq.p, hq.st, ho.p, ho.st, q_heads, (float)scale, window,
                     bytes ? scratch.data_ptr() : nullptr, bytes, pointer(a[11]), (size_t)integer(a[12]),
                     stream(a[13])),

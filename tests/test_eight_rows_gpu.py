@@ -1,5 +1,6 @@
 """Attention over 8-bit caches: what one row, one slot or one batch holds does not
 reach the others, whichever way a call is computed."""
+
 import pytest
 import torch
 
@@ -63,3 +64,61 @@ def test_nan_vectors_reach_the_rows_that_see_them(dt, seqs, scale, window):
     assert ws.status() == 0
     assert torch.equal(torch.isnan(got).all(-1).cpu(), want)
     assert torch.equal(got[~want.cuda()], clean[~want.cuda()])
+
+
+# ---------------------------------------------------------------------------
+# the room that sequences are read back to
+
+def test_a_wide_and_mostly_empty_table_takes_little_memory():
+    """No more than the cache itself in 16 bits, whatever the table's width; pages
+    that sequences share, and one that is none, are read as they are."""
+    cb = EightBatch([(150, 400), (170, 300), (140, 140)], 2, 64, 16, BF, seed=63)
+    cb.table[2, :4] = cb.table[0, :4]                  # a common beginning of 64 slots
+    wide = torch.full((3, 20000), 0, dtype=torch.int32)
+    wide[:, :cb.wide] = cb.table
+    cb.pages = wide.cuda()
+    q = cb.tokens(4)
+    sv.paged_attention(q, *cb.eight(), **cb.scales())
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    ws = sv.CacheWorkspace()
+    got = sv.paged_attention(q, *cb.eight(), **cb.scales(), ws=ws)
+    assert ws.status() == 0 and sv.last_kernel_count() == 2
+    taken = torch.cuda.max_memory_allocated() - before - ws.nbytes
+    assert taken <= 2 * 2 * cb.k8.numel() + got.numel() * 2 + (1 << 16)
+    within(got, *attention(cb, q, default_scale(64), 0))
+    cb.pages[1, 2] = cb.k8.shape[0]
+    cb.k, cb.v = (torch.cat((x, torch.zeros_like(x[:1]))) for x in (cb.k, cb.v))
+    cb.table[1, 2] = cb.k.shape[0] - 1                 # zeros
+    got = sv.paged_attention(q, *cb.eight(), **cb.scales(), ws=ws)
+    assert ws.status() == sv.STATUS_BAD_PAGE
+    within(got, *attention(cb, q, default_scale(64), 0))
+
+
+def test_without_memory_to_read_back_to_the_codes_are_attended_to():
+    page, hkv, d, pool = 64, 8, 128, 2000              # 131 MB of codes, 524 to read back to
+    cb = EightBatch([(140, 300), (130, 200)], hkv, d, page, BF, seed=64)
+    for name in ("k8", "v8", "ks", "vs"):
+        x = getattr(cb, name)
+        y = torch.zeros(pool, *x.shape[1:], dtype=torch.uint8, device="cuda")
+        y[:x.shape[0]] = x.view(torch.uint8)
+        setattr(cb, name, y.view(x.dtype))
+    wide = torch.zeros(2, 1200, dtype=torch.int32)
+    wide[:, :cb.wide] = cb.table
+    cb.pages = wide.cuda()
+    q = cb.tokens(8)
+    ws = sv.CacheWorkspace()
+    want, tol = attention(cb, q, default_scale(d), 0)
+    within(sv.paged_attention(q, *cb.eight(), **cb.scales(), ws=ws), want, tol)
+    assert sv.last_kernel_count() == 2
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (100 << 20)) / total)
+    try:
+        got = sv.paged_attention(q, *cb.eight(), **cb.scales(), ws=ws)
+        assert sv.last_kernel_count() == 1 and ws.status() == 0
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    within(got, want, tol)
