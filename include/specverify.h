@@ -406,8 +406,8 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
  *         kv heads (scratch is refused for these two).  (Keys and values past fp16's
  *         range saturate there.)
  * Products are accumulated and statistics kept in fp32.  Without scratch: scores are
- * those of the codes and the queries as they are; a query's values below 2^-20 of the
- * largest of its tile (up to 32 rows) are good to 2^-31 of it; weights, times the
+ * those of the codes and the queries as they are; a query's values below 2^-20 of its
+ * largest are good to 2^-31 of that; weights, times the
  * values' scales relative to the largest scale met, are rounded to 11 bits (those below
  * 2^-18 of the largest to steps of 2^-28 of it).  A query that holds a NaN or an
  * infinity gives NaN for a row that sees a slot.  Slots inside a sequence's length must

@@ -354,10 +354,11 @@ int sv_paged_attention_scaled(const sv_paged_cache *cache, const sv_cache_scales
         A.window = window;
         A.piece = 8;
         while (A.piece < sv::kKeys && cache->page_size % (2 * A.piece) == 0) A.piece *= 2;
-        A.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504f;
         A.q_mode = scale == 0.f ? 2 : scale < 0.f ? 1 : 0;
         A.workspace = static_cast<char *>(workspace);
         P.scales = device_scales(scales);
+        P.scale_part = scale == 0.f ? 1.f
+                                    : (float)std::frexp(std::fabs((double)scale) * 1.4426950408889634, &P.scale_exponent);
         CUtensorMap kmap, vmap;
         if ((rc = code_map(&kmap, cache, cache->k, cache->k_stride, A.piece)) != SV_OK) return rc;
         if ((rc = code_map(&vmap, cache, cache->v, cache->v_stride, A.piece)) != SV_OK) return rc;

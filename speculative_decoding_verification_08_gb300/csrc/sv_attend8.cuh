@@ -10,10 +10,10 @@
 // its thread, and the tensor cores are not fed empty rows.
 //
 // Keys go to the tensor cores as the e4m3 codes they are.  The queries become 8-bit
-// floats beside them: relative to one power of two for the tile, each value is the
+// floats beside them: relative to a power of two of its row, each value is the
 // sum of 3 (bf16) or 4 (fp16) e5m2 numbers, the nearest to what the ones before it
 // left (3 significant bits each, 2 and the sign of the rest): exact down to 2^-23
-// (fp16: 2^-20) of the tile's largest, and good to 2^-31 of it below.  The parts are columns of their own
+// (fp16: 2^-20) of the row's largest, and good to 2^-31 of it below.  The parts are columns of their own
 // (their products are added in fp32 by the softmax threads), so a block of keys is
 // read from shared memory once.
 // Values need their slots' axis contiguous for the second product, which 16-bit types
@@ -69,11 +69,19 @@ constexpr int kScaleRing = 3;         // pairs of blocks of scales
 constexpr float kGrowAbove = 8.9f;    // log2: with kHalfLift and the largest scale 2^15.9
 constexpr float kHeadroom = 3.f;      // log2, of a new reference above the maximum
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
+// A score is its codes' product (up to 2^32) times the key's scale times the row's power
+// of two; the scale is taken 2^8 times smaller, and the power larger, lest the first
+// product overflow.
+constexpr int kKeyLift = 8;
 constexpr int kNoScale = -200;        // below every e8m0 exponent
 
 struct Attend8Params {
     AttendParams a;
     Scales scales;
+    // |scale| * log2(e) as a number from 1/2 to 1 and a power of two; the first goes into
+    // the keys' scales, the second into the rows' factors
+    float scale_part;
+    int32_t scale_exponent;
 };
 
 template <class T, int kRows8>
@@ -106,8 +114,6 @@ struct Attend8Shared {
     Piece pieces[kPieces];
     uint32_t tmem;
     int32_t dead, b0, last;
-    float q_factor[2];          // power of two of a tile's queries, times the score scale
-    uint32_t q_top[4];          // largest magnitudes of its warps' rows, as bits
     int64_t skip;
     int64_t sums[kThreads8 / 32];
 };
@@ -128,6 +134,7 @@ struct __align__(16) Attend8Misc {
     Attend8Shared sh;
     GroupState group[2];
     TileState tile[2];
+    float q_factor[2][kMaxRows8];  // powers of two of a tile's rows, with the call's scale's and kKeyLift
     uint8_t scales[kScaleRing][2][2 * kKeys];  // of keys and values
 };
 static_assert(sizeof(Attend8Misc) <= 7168, "misc region");
@@ -394,7 +401,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
             ++qn;
             // four values to a lane, rows tw, tw + 4, ... to a warp
             constexpr int kMine = kRows8 / 4;
-            uint32_t top = 0;
             const int rows = p.rows;
             auto load = [&](int i) -> uint2 {
                 const int r = tw + 4 * i;
@@ -409,26 +415,29 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 return max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u);
             };
             // (all rows' loads in flight; the second time they come from near by)
+            uint32_t tops = 0;  // lane i: bits of the i-th row's largest magnitude
             {
                 uint2 x[kMine];
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) x[i] = load(i);
 #pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    top = max(top, max(bits(pair_of(x[i].x, T())), bits(pair_of(x[i].y, T()))));
+                for (int i = 0; i < kMine; ++i) {
+                    const uint32_t top =
+                        __reduce_max_sync(0xffffffffu, max(bits(pair_of(x[i].x, T())), bits(pair_of(x[i].y, T()))));
+                    if (lane == i) tops = top;
+                }
             }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) sh.q_top[tw] = top;
-            group_barrier(3);
-            top = max(max(sh.q_top[0], sh.q_top[1]), max(sh.q_top[2], sh.q_top[3]));
-            // the largest is brought to 57344 (e5m2's) or less
-            const int e = min(max((int)(top >> 23) - 127 - 15 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 120);
-            const float f = A.q_mode == 1 ? -power_of_two(-e) : power_of_two(-e);
             char *to = smem + L::kQ + qb * L::kQuery;
 #pragma unroll 1
             for (int i = 0; i < kMine; ++i) {
                 const int r = tw + 4 * i;
                 const uint2 x = load(i);
+                // the row's largest is brought to 57344 (e5m2's) or less
+                const uint32_t top = __shfl_sync(0xffffffffu, tops, i);
+                const int e =
+                    min(max((int)(top >> 23) - 127 - 15 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -126), 120);
+                const float f = A.q_mode == 1 ? -power_of_two(-e) : power_of_two(-e);
+                if (lane == 0) misc.q_factor[qb][r] = power_of_two(min(max(e + kKeyLift + P8.scale_exponent, -126), 127));
                 const float2 a = pair_of(x.x, T()), b = pair_of(x.y, T());
                 float y[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
                 // an infinity makes its row NaN, as a NaN does
@@ -440,7 +449,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     *reinterpret_cast<uint32_t *>(to + (part * kRows8 + r) * 128 + ((lane / 4) ^ (r & 7)) * 16 +
                                                   lane % 4 * 4) = split_off(y);
             }
-            if (tt == 0) sh.q_factor[qb] = A.scale_log2 * power_of_two(e);
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full[qb]);
@@ -897,9 +905,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 const uint32_t qb = qn & 1;
                 hold8<true>(sh, &sh.q_full[qb], (qn >> 1) & 1);
                 ++qn;
-                const float q_factor = sh.q_factor[qb];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_empty[qb]);
+                const float *q_factor = misc.q_factor[qb];
                 const uint32_t t_o = lanes_at + L::kOut + (tb * 2 + g) * L::kOutCols;
                 for (int i = 0; i < mine; ++i, ++used) {
                     const int k0 = (lo + 2 * i + g) * kKeys;
@@ -911,8 +917,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     if (lane == 0) mbar_arrive(&sh.scale_empty[sc.st]);
                     sc.next();
                     tc::fence_after();
-                    uint64_t y[kRows8 / 2];  // of rows 2 r and 2 r + 1
-                    const float key_scale = q_factor * scale_of(key_byte);
+                    uint64_t y[kRows8 / 2];  // scores over their rows' factors, of rows 2 r and 2 r + 1
+                    const float key_scale = scale_of(key_byte) * (P8.scale_part / (1 << kKeyLift));
                     const bool masked =
                         k0 + kKeys - 1 > past + j0 || (A.window > 0 && k0 <= past + j1 - A.window);
                     // rows [r0, r1) see the slot: row r does when its token does, row0 + r >=
@@ -974,7 +980,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                                 for (int r = 0; r < kRows8 / 2; ++r) unpair2(y[r], v[2 * r], v[2 * r + 1]);
                                 own.across[gw][lane] =
-                                    across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                                    across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); }) *
+                                    (lane < kRows8 ? q_factor[lane] : 1.f);
                             }
                             const int largest = __reduce_max_sync(0xffffffffu, e8);
                             if (lane == 0) own.exponent[gw] = largest;
@@ -1030,8 +1037,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                         for (int o = 0; o < kRows8 / 4; ++o) {
                             const float4 m = *reinterpret_cast<const float4 *>(&own.minus[o * 4]);
-                            y[2 * o] = add2(y[2 * o], pair2(m.x, m.y));
-                            y[2 * o + 1] = add2(y[2 * o + 1], pair2(m.z, m.w));
+                            const float4 f = *reinterpret_cast<const float4 *>(&q_factor[o * 4]);
+                            // (the products are exact: the factors are powers of two)
+                            y[2 * o] = fma2(y[2 * o], pair2(f.x, f.y), pair2(m.x, m.y));
+                            y[2 * o + 1] = fma2(y[2 * o + 1], pair2(f.z, f.w), pair2(m.z, m.w));
                             float a, b;
                             unpair2(y[2 * o], a, b);
                             top = max3(top, a, b);
@@ -1082,6 +1091,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.p_full[g]);
                 }
+                // (the rows' factors have been read for the last time)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_empty[qb]);
                 if (g == 1 && (blocks & 1)) {  // a last pair's second block that there is none of
                     if (lane == 0) mbar_arrive(&sh.scale_empty[sc.st]);
                     sc.next();

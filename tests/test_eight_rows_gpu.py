@@ -122,3 +122,50 @@ def test_without_memory_to_read_back_to_the_codes_are_attended_to():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     within(got, want, tol)
+
+
+# ---------------------------------------------------------------------------
+# rows of a tile
+
+@pytest.mark.parametrize("seqs", [[(3, 200), (2, 1500)], [(6, 40)]])
+@pytest.mark.parametrize("dt,small,spread,big", [(BF, 1.0, 1.0, 2.0 ** 24), (BF, 1.0, 1.0, 2.0 ** 90),
+                                                 (BF, 2.0 ** -60, 1.0, 2.0 ** 30), (HF, 2.0 ** -8, 256.0, 2.0 ** 21)])
+def test_a_large_query_leaves_other_rows_alone(seqs, dt, small, spread, big):
+    """Rows of one tile whose queries differ by 2^21 and more: each is as exact as by
+    itself, and the others' bits do not change."""
+    cb = EightBatch(seqs, 1, 64, 16, dt, seed=65, spread=spread)
+    q = cb.tokens(4, small)
+    scale = default_scale(64) if small > 1e-3 else 2.0 ** 60 * default_scale(64)
+    call = lambda x: sv.paged_attention(x, *cb.eight(), scale=scale, **cb.scales())  # noqa: E731
+    clean = call(q)
+    within(clean, *attention(cb, q, scale, 0))
+    far = q.clone()
+    far[1, 2] *= big
+    far[cb.N - 1, 0] *= big
+    assert bool(torch.isfinite(far).all())
+    got = call(far)
+    within(got, *attention(cb, far, scale, 0))
+    rest = torch.ones(cb.N, 4, dtype=torch.bool, device="cuda")
+    rest[1, 2] = rest[cb.N - 1, 0] = False
+    assert torch.equal(got[rest], clean[rest])
+
+
+def test_the_largest_query_leaves_other_rows_alone():
+    cb = EightBatch([(4, 700)], 1, 128, 16, BF, seed=66)
+    q = cb.tokens(6)
+    clean = sv.paged_attention(q, *cb.eight(), **cb.scales())
+    q[2, 3] = torch.finfo(BF).max
+    got = sv.paged_attention(q, *cb.eight(), **cb.scales())
+    rest = torch.ones(4, 6, dtype=torch.bool, device="cuda")
+    rest[2, 3] = False
+    assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("power", [-110, -30, 60, 110])
+def test_far_scales_of_the_call(power):
+    """Queries and scale that are each out of the way, their product as usual."""
+    cb = EightBatch([(3, 200)], 1, 64, 16, BF, seed=71)
+    q = cb.tokens(4)
+    want = sv.paged_attention(q, *cb.eight(), scale=0.125, **cb.scales())
+    got = sv.paged_attention(q * 2.0 ** -power, *cb.eight(), scale=0.125 * 2.0 ** power, **cb.scales())
+    assert torch.equal(got, want)
