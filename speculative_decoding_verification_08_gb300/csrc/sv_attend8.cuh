@@ -17,18 +17,17 @@
 // (their products are added in fp32 by the softmax threads), so a block of keys is
 // read from shared memory once.
 // Values need their slots' axis contiguous for the second product, which 16-bit types
-// have: four warps turn codes into fp16 (exact).  Their scales go into the weights,
-// relative to a power of two that follows the largest scale: weight times scale, in
-// fp16 and taken 2^7 times as large, is the one rounding between fp32 scores and the
-// result (11 bits; what is below 2^-18 of the row's and the scales' largest is rounded
-// to steps of 2^-28 of them).
+// have: four warps turn codes into fp16 (exact).  Their scales go into the weights, as
+// logarithms beside the scores: weight times scale, relative to the row's reference, in
+// fp16 is the one rounding between fp32 scores and the result (11 bits; what is below
+// 2^-18 of the row's largest is rounded to steps of 2^-28 of it).  The sums take the
+// scales out again, in fp32.
 //
-// Softmax: weights are relative to a reference per row, which follows the row's
-// maximum only when a weight would not fit fp16; whether any is so large, is one vote
-// of the 128 threads per block, and finding the new maxima the rare way (a new reference
-// is 2^3 above the maximum: with 24 rows of random scores, heavy-tailed by the keys' sizes,
-// 0.2 of the blocks go that way, the first of each tile among them, and 0.34 without:
-// 274 instead of 294 us for rounds).  Two groups of
+// Softmax: the reference of a row follows the largest weight times scale among the slots
+// that it sees, and only when one would not fit fp16; whether any is so large, is one vote
+// of the 128 threads per block, and finding the new references the rare way (a new one
+// puts the largest at 2^4, with 2^11.9 of room above).  A row's numbers depend on no
+// other row and on no slot that it does not see.  Two groups of
 // four warps take the even and the odd blocks of a tile, each with scores, weights,
 // outputs and references of its own, and join them at the tile's end.
 //
@@ -66,14 +65,18 @@ constexpr int kSoftmaxRegs8 = 136, kValueRegs8 = 56, kIssueRegs8 = 56, kTileRegs
 static_assert(128 * (2 * kSoftmaxRegs8 + kValueRegs8 + kIssueRegs8 + kTileRegs8) <= kThreads8 * 96, "register split");
 constexpr int kRaw = kKeys * 128;     // a block of codes
 constexpr int kScaleRing = 3;         // pairs of blocks of scales
-constexpr float kGrowAbove = 8.9f;    // log2: with kHalfLift and the largest scale 2^15.9
-constexpr float kHeadroom = 3.f;      // log2, of a new reference above the maximum
+// Weights are relative to a row's reference, their values' scales included: the logarithm
+// of the largest that fp16 holds, and where a new reference puts the largest so far.
+constexpr float kGrowAbove = 15.9f, kTop = 4.f;
+constexpr float kFarOff = 10.f, kCoarse = 0x1p26f;
+constexpr int kMaxPasses = 8;
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
+constexpr float kShift = 8.f;         // of scales' logarithms: those of values about 1 become 0
+constexpr int kSumLift = 20;          // sums are so much smaller (log2), lest values of zeros' overflow
 // A score is its codes' product (up to 2^32) times the key's scale times the row's power
 // of two; the scale is taken 2^8 times smaller, and the power larger, lest the first
 // product overflow.
 constexpr int kKeyLift = 8;
-constexpr int kNoScale = -200;        // below every e8m0 exponent
 
 struct Attend8Params {
     AttendParams a;
@@ -91,7 +94,7 @@ struct Attend8Smem {
     static constexpr int kScoreCols = (kParts * kRows8 + 15) / 16 * 16;
     static constexpr int kQuery = kScoreCols * 128;
     // Rings: blocks of keys and of values in flight, as room allows
-    static constexpr int kMisc = 7168, kRoom = 227 * 1024;
+    static constexpr int kMisc = 8192, kRoom = 227 * 1024;
     static constexpr int kFixed = kMisc + 2 * kQuery + 2 * 2 * kRaw + kRaw;
     static constexpr int kRingV = kFixed + 6 * kRaw <= kRoom ? 3 : 2, kRingK = kFixed + (4 + kRingV) * kRaw <= kRoom ? 4 : 3;
     static constexpr int kQ = kMisc, kK = kQ + 2 * kQuery, kV = kK + kRingK * kRaw, kVc = kV + kRingV * kRaw,
@@ -119,15 +122,14 @@ struct Attend8Shared {
 };
 
 struct __align__(16) GroupState {   // of a softmax group
-    float minus[kMaxRows8];         // minus the rows' references
-    float factor[kMaxRows8];        // what a new reference makes of sums and outputs
+    float minus[kMaxRows8], base[kMaxRows8];  // minus the rows' references; 0 where there is none
+    float factor[kMaxRows8];        // root of what a new reference makes of sums and outputs
     float across[4][kMaxRows8];     // its warps' maxima
-    int32_t exponent[4];            // its warps' largest scales
 };
 
 struct __align__(16) TileState {    // what the softmax leaves of a tile
     float minus[2][kMaxRows8], sums[2][4][kMaxRows8];
-    int32_t exponent[2];
+    float shift[2];
 };
 
 struct __align__(16) Attend8Misc {
@@ -137,7 +139,7 @@ struct __align__(16) Attend8Misc {
     float q_factor[2][kMaxRows8];  // powers of two of a tile's rows, with the call's scale's and kKeyLift
     uint8_t scales[kScaleRing][2][2 * kKeys];  // of keys and values
 };
-static_assert(sizeof(Attend8Misc) <= 7168, "misc region");
+static_assert(sizeof(Attend8Misc) <= 8192, "misc region");
 
 // A wait that gives up for the whole CTA, as hold() of the 16-bit kernel; the kernel's
 // end reports it.  Every wait of every warp is a copy of this, and code that does not
@@ -221,6 +223,12 @@ __device__ __forceinline__ float across_lanes(float (&v)[32], int lane, F join) 
         }
     }
     return v[0];
+}
+
+// How far reference a lies above b, each given as minus it and its group's shift.  (kUnset
+// lies below every other, and as far from itself as 0.)
+__device__ __forceinline__ float above(float a_minus, float a_shift, float b_minus, float b_shift) {
+    return (b_minus - a_minus) + (b_shift - a_shift);
 }
 
 // Four e4m3 codes as fp16.
@@ -468,24 +476,17 @@ __global__ void __launch_bounds__(kThreads8, 1)
             tc::fence_after();
             // the groups' states, joined: lane r has row r's
             const TileState &st = misc.tile[tb];
-            float ref = -INFINITY, sum = 0.f, f[2];
-            {
-                float own_ref[2], own_sum[2];
+            // (references may be 2^200 apart beside sums that are as far: factors in two steps)
+            float minus = kUnset, shift = 0.f, sum = 0.f, f[2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float m = st.minus[x][lane];
-                    own_ref[x] = m == kUnset ? -INFINITY : -m;
-                    own_sum[x] = (st.sums[x][0][lane] + st.sums[x][1][lane]) +
-                                 (st.sums[x][2][lane] + st.sums[x][3][lane]);
-                    ref = fmaxf(ref, own_ref[x]);
-                }
+            for (int x = 0; x < 2; ++x)
+                if (above(st.minus[x][lane], st.shift[x], minus, shift) > 0.f)
+                    minus = st.minus[x][lane], shift = st.shift[x];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    f[x] = own_ref[x] == -INFINITY ? 0.f : ex2(own_ref[x] - ref);
-                    sum += own_sum[x] * f[x];
-                    const int e = st.exponent[x];
-                    if (e != kNoScale) f[x] *= ex2((float)(e - (int)kHalfLift));  // (else: zeros and NaN)
-                }
+            for (int x = 0; x < 2; ++x) {
+                const float h = ex2(0.5f * above(st.minus[x][lane], st.shift[x], minus, shift));
+                sum += ((st.sums[x][0][lane] + st.sums[x][1][lane]) + (st.sums[x][2][lane] + st.sums[x][3][lane])) * h * h;
+                f[x] = h * h * (1.f / (1 << kSumLift));
             }
             // (a row that saw nothing has the sum 0, and zeros)
             const bool whole = p.parts == 1;
@@ -531,7 +532,10 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 mbar_arrive(&sh.state_empty[tb]);
             }
             if (!whole) {
-                if (tw == 0) part_stats[(int64_t)slot * 2 * kRows + lane] = make_float2(ref, sum);
+                if (tw == 0) {
+                    part_stats[(int64_t)slot * 2 * kRows + lane] = make_float2(minus, sum);
+                    part_stats[(int64_t)slot * 2 * kRows + kMaxRows8 + lane] = make_float2(shift, 0.f);
+                }
                 group_barrier(3);
                 if (tt == 0) {
                     __threadfence();  // all 128 threads' writes, after the barrier
@@ -551,30 +555,40 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     // lane r: row r's reference and sum over the parts (as many loads in
                     // flight as a batch; one past the end is the last once more)
                     constexpr int kBatch = 8;
-                    float top = -INFINITY, all = 0.f;
+                    float all = 0.f;
+                    minus = kUnset, shift = 0.f;
 #pragma unroll 1
                     for (int i0 = 0; i0 < parts; i0 += kBatch) {
                         float2 x[kBatch];
+                        float n[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const float2 *at = &part_stats[slot_of(min(i0 + i, parts - 1)) * 2 * kRows + lane];
+                            x[i] = __ldcg(at);
+                            n[i] = __ldcg(at + kMaxRows8).x;
+                        }
+                        const float old_minus = minus, old_shift = shift;
 #pragma unroll
                         for (int i = 0; i < kBatch; ++i)
-                            x[i] = __ldcg(&part_stats[slot_of(min(i0 + i, parts - 1)) * 2 * kRows + lane]);
-                        float m = top;
+                            if (above(x[i].x, n[i], minus, shift) > 0.f) minus = x[i].x, shift = n[i];
+                        const float h = ex2(0.5f * above(old_minus, old_shift, minus, shift));
+                        all *= h * h;
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i) m = fmaxf(m, x[i].x);
-                        all *= top == -INFINITY ? 0.f : ex2(top - m);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (i0 + i < parts && x[i].y != 0.f) all += x[i].y * ex2(x[i].x - m);
-                        top = m;
+                        for (int i = 0; i < kBatch; ++i) {
+                            const float g = ex2(0.5f * above(x[i].x, n[i], minus, shift));
+                            if (i0 + i < parts) all += x[i].y * g * g;
+                        }
                     }
-                    const float over = all == 0.f ? 0.f : 1.f / all;
+                    const float over = 1.f / all;
                     // four values to a lane, one row to a warp, or two of up to 64 values
                     const int per = wide ? 1 : 2, d0 = (wide ? lane : lane % 16) * 4;
                     const int64_t base = (int64_t)p.token * A.o_st[0] + (int64_t)p.h * A.group * A.o_st[1];
 #pragma unroll 1
                     for (int r0 = tw * per; r0 < rows; r0 += 4 * per) {
                         const int r = min(r0 + (wide ? 0 : lane / 16), rows - 1);
-                        const float row_top = __shfl_sync(0xffffffffu, top, r);
+                        const float row_minus = __shfl_sync(0xffffffffu, minus, r);
+                        const float row_shift = __shfl_sync(0xffffffffu, shift, r);
+                        const float row_all = __shfl_sync(0xffffffffu, all, r);
                         const float row_over = __shfl_sync(0xffffffffu, over, r);
                         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -584,13 +598,13 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
                             for (int i = 0; i < kBatch; ++i) {
                                 const int64_t at = slot_of(min(i0 + i, parts - 1));
-                                m[i] = __ldcg(&part_stats[at * 2 * kRows + r]).x;
+                                m[i] = above(__ldcg(&part_stats[at * 2 * kRows + r]).x,
+                                             __ldcg(&part_stats[at * 2 * kRows + kMaxRows8 + r]).x, row_minus, row_shift);
                                 x[i] = __ldcg(reinterpret_cast<const float4 *>(part_out + at * kSlot + r * 128 + d0));
                             }
 #pragma unroll
                             for (int i = 0; i < kBatch; ++i) {
-                                // (a NaN query leaves no reference, and NaN in O)
-                                const float w = i0 + i >= parts || m[i] == -INFINITY ? 0.f : ex2(m[i] - row_top);
+                                const float w = ex2(m[i]);
                                 if (i0 + i < parts) {
                                     acc.x = fmaf(w, x[i].x, acc.x);
                                     acc.y = fmaf(w, x[i].y, acc.y);
@@ -604,7 +618,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             uint2 y;
                             y.x = pack2<T>(acc.x * row_over, acc.y * row_over);
                             y.y = pack2<T>(acc.z * row_over, acc.w * row_over);
-                            if (row_over == 0.f) y = make_uint2(0, 0);
+                            if (row_all == 0.f) y = make_uint2(0, 0);
                             *reinterpret_cast<uint2 *>(static_cast<T *>(A.out) + base + j * A.o_st[0] +
                                                        (pr - j * A.group) * A.o_st[1] + d0) = y;
                         }
@@ -888,18 +902,23 @@ __global__ void __launch_bounds__(kThreads8, 1)
         RingPlace<kScaleRing> sc;
         PieceReader8 reader;
         for (;;) {
+            // (nothing that the last tile left is read any more)
+            if (gw == 0) {
+                own.minus[lane] = kUnset;
+                own.base[lane] = 0.f;
+            }
             // (all four warps go on, or none: they meet at barriers)
             if (group_any(1 + g, !reader.next(sh))) break;
             const Piece &p = sh.pieces[reader.k];
-            const int blocks = p.n, past = p.past, row0 = p.row, lo = p.lo, end = p.end;
+            const int blocks = p.n, past = p.past, row0 = p.row, rows = p.rows, lo = p.lo;
             const int mine = (blocks + 1 - g) / 2;
-            const int j0 = A.by_group.div(row0), j1 = A.by_group.div(row0 + p.rows - 1);
+            const int j0 = A.by_group.div(row0), j1 = A.by_group.div(row0 + rows - 1);
             reader.done(sh, lane);
             uint64_t sums[kRows8 / 2];  // this thread's slots', of rows 2 r and 2 r + 1
 #pragma unroll
             for (int r = 0; r < kRows8 / 2; ++r) sums[r] = 0;
-            int exponent = kNoScale;    // weights are times 2^-exponent
             float minus = kUnset;       // lane r: minus row r's reference
+            float shift = kShift;
             const uint32_t tb = tile & 1;
             if (blocks > 0) {
                 const uint32_t qb = qn & 1;
@@ -922,13 +941,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     const bool masked =
                         k0 + kKeys - 1 > past + j0 || (A.window > 0 && k0 <= past + j1 - A.window);
                     // rows [r0, r1) see the slot: row r does when its token does, row0 + r >=
-                    // t G, and < (t + window) G
+                    // t G, and < (t + window) G (none past the tile's last, which would see
+                    // what lies behind its end)
                     int r0 = 0, r1 = kRows8;
                     if (__builtin_expect(masked, 0)) {
                         const int64_t from = ((int64_t)k0 + gt - past) * A.group - row0;
                         const int64_t to = A.window > 0 ? from + (int64_t)A.window * A.group : kRows8;
-                        r0 = (int)max((int64_t)0, min(from, (int64_t)kRows8));
-                        r1 = (int)max((int64_t)0, min(to, (int64_t)kRows8));
+                        r0 = (int)max((int64_t)0, min(from, (int64_t)rows));
+                        r1 = (int)max((int64_t)0, min(to, (int64_t)rows));
                     }
                     auto sees = [&](int r) -> bool { return r >= r0 && r < r1; };
                     auto scores = [&]() {
@@ -964,54 +984,70 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             }
                         }
                     };
-                    // (a byte of 255 is no scale: the vector is NaN; what lies behind the
-                    // tile's end is none either)
-                    const int e8 = value_byte == kScaleNan || k0 + gt >= end ? kNoScale : (int)value_byte - 127;
+                    // (a byte of 255 is no scale: the vector is NaN)
+                    const int e8 = value_byte == kScaleNan ? 0 : (int)value_byte - 127;
                     // (once more, from tensor memory, where references grow; the first block
                     // has none to begin with)
-                    for (bool rare = i == 0;; rare = true) {
+                    bool fresh = false;  // lane r: row r's reference is of the pass before
+                    for (int pass = i == 0 ? 0 : -1;; ++pass) {
+                        bool again = false;
                         scores();
-                        if (__builtin_expect(rare, 0)) {
+                        if (__builtin_expect(pass >= 0, 0)) {
                             // the rows' maxima over the block, and new references where they grew
                             {
                                 float v[kMaxRows8];
 #pragma unroll
                                 for (int r = 0; r < kMaxRows8; ++r) v[r] = -INFINITY;
+                                const uint64_t value2 = pair2((float)e8 + shift, (float)e8 + shift);
 #pragma unroll
-                                for (int r = 0; r < kRows8 / 2; ++r) unpair2(y[r], v[2 * r], v[2 * r + 1]);
+                                for (int o = 0; o < kRows8 / 4; ++o) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(&q_factor[o * 4]);
+                                    const float4 m = *reinterpret_cast<const float4 *>(&own.base[o * 4]);
+                                    unpair2(add2(fma2(y[2 * o], pair2(f.x, f.y), pair2(m.x, m.y)), value2), v[4 * o],
+                                            v[4 * o + 1]);
+                                    unpair2(add2(fma2(y[2 * o + 1], pair2(f.z, f.w), pair2(m.z, m.w)), value2),
+                                            v[4 * o + 2], v[4 * o + 3]);
+                                }
                                 own.across[gw][lane] =
-                                    across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); }) *
-                                    (lane < kRows8 ? q_factor[lane] : 1.f);
+                                    across_lanes(v, lane, [](float a, float b) { return fmaxf(a, b); });
                             }
-                            const int largest = __reduce_max_sync(0xffffffffu, e8);
-                            if (lane == 0) own.exponent[gw] = largest;
                             group_barrier(1 + g);
                             float high = own.across[0][lane];
-                            int most = own.exponent[0];
 #pragma unroll
-                            for (int w = 1; w < 4; ++w) {
-                                high = fmaxf(high, own.across[w][lane]);
-                                most = max(most, own.exponent[w]);
+                            for (int w = 1; w < 4; ++w) high = fmaxf(high, own.across[w][lane]);
+                            const bool unset = minus == kUnset;
+                            const bool grow = high > (unset ? -INFINITY : kGrowAbove) || (fresh && high < kTop - kFarOff);
+                            const float from = unset ? 0.f : minus;
+                            float to = grow ? from - (high - kTop) : minus, by = 0.f;
+                            // References from 2^26 on have steps of 4 and more, which may
+                            // swallow a value's scale: the next pass has small numbers and
+                            // finds out.  What a step is too large for, the group's shift
+                            // takes, and the other rows' references take the shift back.
+                            const float off = (to - from) + (high - kTop);
+                            const unsigned far = __ballot_sync(0xffffffffu, grow && fabsf(off) > kFarOff);
+                            if (__builtin_expect(far != 0, 0)) {
+                                by = -__shfl_sync(0xffffffffu, off, __ffs(far) - 1);
+                                shift += by;
+                                if (!(far >> lane & 1)) to -= by;
                             }
-                            const int now_e = max(most, exponent);
-                            const bool grow = high + minus > kGrowAbove;
-                            const float now = grow ? -high - kHeadroom : minus;
-                            const float f = !grow ? 1.f : minus == kUnset ? 0.f : ex2(now - minus);
-                            const float fe = exponent == kNoScale ? 0.f : ex2((float)(exponent - now_e));
-                            const bool scaled = __any_sync(0xffffffffu, grow && minus != kUnset) || now_e != exponent;
-                            exponent = now_e;
-                            minus = now;
+                            fresh = grow && fabsf(to) >= kCoarse;
+                            again = __any_sync(0xffffffffu, fresh) && pass < kMaxPasses;
+                            const float h = unset ? 0.f : ex2(0.5f * ((to - from) + by));
+                            const bool scaled = __any_sync(0xffffffffu, grow && !unset) || far != 0;
+                            minus = to;
                             if (gw == 0) {
-                                own.minus[lane] = now;
-                                own.factor[lane] = f;
+                                own.minus[lane] = minus;
+                                own.base[lane] = minus == kUnset ? 0.f : minus;
+                                own.factor[lane] = h;
                             }
                             group_barrier(1 + g);
                             if (i > 0) {
 #pragma unroll
                                 for (int o = 0; o < kRows8 / 4; ++o) {
                                     const float4 m = *reinterpret_cast<const float4 *>(&own.factor[o * 4]);
-                                    sums[2 * o] = mul2(sums[2 * o], pair2(m.x, m.y));
-                                    sums[2 * o + 1] = mul2(sums[2 * o + 1], pair2(m.z, m.w));
+                                    const uint64_t a = pair2(m.x, m.y), b = pair2(m.z, m.w);
+                                    sums[2 * o] = mul2(mul2(sums[2 * o], a), a);
+                                    sums[2 * o + 1] = mul2(mul2(sums[2 * o + 1], b), b);
                                 }
                                 if (scaled) {
                                     hold8(sh, &sh.pv_done[g], (used - 1) & 1);
@@ -1023,39 +1059,40 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                         tc::ld8(o, t_o + part * 8);
                                         tc::wait_ld();
 #pragma unroll
-                                        for (int e = 0; e < 8; ++e)
-                                            o[e] = __float_as_uint(__uint_as_float(o[e]) *
-                                                                   (own.factor[part * 8 + e] * fe));
+                                        for (int e = 0; e < 8; ++e) {
+                                            const float f = own.factor[part * 8 + e];
+                                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f * f);
+                                        }
                                         tc::st8(t_o + part * 8, o);
                                     }
                                     tc::wait_st();
                                 }
                             }
                         }
-                        // scores relative to the references, and the largest of them
+                        // logarithms of weights times scales, and the largest of them
                         float top = -INFINITY;
+                        const uint64_t value2 = pair2((float)e8 + shift, (float)e8 + shift);
 #pragma unroll
                         for (int o = 0; o < kRows8 / 4; ++o) {
                             const float4 m = *reinterpret_cast<const float4 *>(&own.minus[o * 4]);
                             const float4 f = *reinterpret_cast<const float4 *>(&q_factor[o * 4]);
                             // (the products are exact: the factors are powers of two)
-                            y[2 * o] = fma2(y[2 * o], pair2(f.x, f.y), pair2(m.x, m.y));
-                            y[2 * o + 1] = fma2(y[2 * o + 1], pair2(f.z, f.w), pair2(m.z, m.w));
+                            y[2 * o] = add2(fma2(y[2 * o], pair2(f.x, f.y), pair2(m.x, m.y)), value2);
+                            y[2 * o + 1] = add2(fma2(y[2 * o + 1], pair2(f.z, f.w), pair2(m.z, m.w)), value2);
                             float a, b;
                             unpair2(y[2 * o], a, b);
                             top = max3(top, a, b);
                             unpair2(y[2 * o + 1], a, b);
                             top = max3(top, a, b);
                         }
-                        if (rare || !group_any(1 + g, top > kGrowAbove || e8 > exponent)) break;
+                        if (pass >= 0 ? !again : !group_any(1 + g, top > kGrowAbove)) break;
                     }
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.s_empty[g]);
-                    // a weight times its scale, in fp16's range
-                    const int shift = max(e8, -127) - exponent + (int)kHalfLift;
-                    const float value_scale = shift < -126 ? 0.f : power_of_two(shift);
-                    const uint64_t value_scale2 = pair2(value_scale, value_scale);
+                    // (what takes the scale out of a weight for the sums)
+                    const float inv = power_of_two(max(-(e8 + kSumLift), -126));
+                    const uint64_t inv2 = pair2(inv, inv);
                     if (used > 0) hold8(sh, &sh.pv_done[g], (used - 1) & 1);
                     __syncwarp();
                     char *row = smem + L::kP + gt * 128;  // the group's half of it
@@ -1068,8 +1105,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                             float a, b;
                             unpair2(y[r], a, b);
                             const uint64_t x = pair2(ex2(a), ex2(b));
-                            sums[r] = add2(sums[r], x);
-                            unpair2(mul2(x, value_scale2), a, b);
+                            sums[r] = fma2(x, inv2, sums[r]);
+                            unpair2(x, a, b);
                             w[e] = pack2<__half>(a, b);
                         }
                         *reinterpret_cast<uint4 *>(row + (((4 * g + o) ^ (gt & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1112,7 +1149,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 st.sums[g][gw][lane] = sum;
                 if (gw == 0) {
                     st.minus[g][lane] = minus;
-                    if (lane == 0) st.exponent[g] = exponent;
+                    if (lane == 0) st.shift[g] = shift;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.state_full[tb]);

@@ -169,3 +169,78 @@ def test_far_scales_of_the_call(power):
     want = sv.paged_attention(q, *cb.eight(), scale=0.125, **cb.scales())
     got = sv.paged_attention(q * 2.0 ** -power, *cb.eight(), scale=0.125 * 2.0 ** power, **cb.scales())
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# slots whose values are far larger than others'
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("seqs", [[(6, 300)], [(6, 3000), (2, 70)]])
+@pytest.mark.parametrize("up", [20, 60])
+def test_values_that_a_row_does_not_see_leave_it_alone(dt, seqs, up):
+    """A new token's value 2^up times as large as the others': rows before it keep
+    their bits, and with a window those behind it."""
+    cb = EightBatch(seqs, 1, 64, 16, dt, seed=67, scale_spread=0.3)
+    q = cb.tokens(4)
+    n, t = seqs[0]
+    before = [sv.paged_attention(q, *cb.eight(), window=w, **cb.scales()) for w in (0, 2)]
+    p, at = place(cb, 0, t - n + 2)
+    cb.vs.view(torch.uint8)[p, at] += up
+    cb.refresh()
+    for w, old in zip((0, 2), before):
+        got = sv.paged_attention(q, *cb.eight(), window=w, **cb.scales())
+        assert torch.equal(got[:2], old[:2]) and torch.equal(got[6:], old[6:])
+        if w:
+            assert torch.equal(got[4:], old[4:])
+        if dt == BF or up == 20:                       # (fp16 results end at 65504)
+            want, tol = attention(cb, q, default_scale(64), w)
+            fits = want.abs() + tol < torch.finfo(dt).max
+            off = (got.cpu().double() - want).abs()
+            assert bool((off[fits] <= tol[fits]).all())
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("down", [0, -40, 30])
+def test_large_values_with_no_weight(dt, down):
+    """Values 2^30 times as large as the others', in slots that a row gives no weight
+    (keys opposite to its query), and all of them small or large."""
+    cb = EightBatch([(1, 700), (2, 3000)], 1, 64, 16, dt, seed=68, scale_spread=0.0)
+    q = cb.tokens(2)
+    q[...] = 0
+    q[..., 0] = 8.0
+    down = max(down, -14) if dt == HF else down        # (results above fp16's smallest)
+    down = min(down, 0) if dt == HF else down
+    cb.vs.view(torch.uint8)[...] += down % 256
+    for b, (_, t) in enumerate(cb.seqs):
+        for s in range(0, t, 7):
+            p, at = place(cb, b, s)
+            cb.k8[p, at, 0] = torch.zeros(64, device="cuda").to(E4M3)
+            cb.k8.view(torch.uint8)[p, at, 0, 0] = 0xfe     # -448
+            cb.ks.view(torch.uint8)[p, at, 0] = 127 - 2
+            cb.vs.view(torch.uint8)[p, at, 0] = (127 - 6 + 30 + down)
+    cb.refresh()
+    got = sv.paged_attention(q, *cb.eight(), **cb.scales())
+    within(got, *attention(cb, q, default_scale(64), 0))
+
+
+@pytest.mark.parametrize("score", [2.0 ** 20, 2.0 ** 27, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("values", [-40, -9, 0, 30])
+def test_huge_scores(score, values):
+    """Scores whose steps in fp32 would swallow the values' scales: one slot has all
+    the weight, the last of a pair of opposite ones, and gives its value."""
+    cb = EightBatch([(2, 700)], 1, 64, 16, BF, seed=72, scale_spread=0.0)
+    q = cb.tokens(4)
+    q[...] = 0
+    q[..., 0] = score
+    cb.vs.view(torch.uint8)[...] += values % 256
+    for s in range(0, 698, 99):                        # larger and larger keys, both ways
+        for i in (0, 1):
+            p, at = place(cb, 0, s + i)
+            cb.k8[p, at, 0] = torch.zeros(64, device="cuda").to(E4M3)
+            cb.k8.view(torch.uint8)[p, at, 0, 0] = 0x7e if i else 0xfe       # 448, -448
+            cb.ks.view(torch.uint8)[p, at, 0] = 127 + s // 99 - 4
+    cb.refresh()
+    got = sv.paged_attention(q, *cb.eight(), **cb.scales())
+    p, at = place(cb, 0, 694)
+    want = cb.v[p, at, 0].expand(2, 4, 64)
+    within(got, want, want.abs() * 2.0 ** -7)
