@@ -244,3 +244,40 @@ def test_huge_scores(score, values):
     p, at = place(cb, 0, 694)
     want = cb.v[p, at, 0].expand(2, 4, 64)
     within(got, want, want.abs() * 2.0 ** -7)
+
+
+# ---------------------------------------------------------------------------
+# pages that are none
+
+@pytest.mark.parametrize("seqs", [FEW, MANY])
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+def test_a_page_that_is_none_reads_as_zeros(seqs, window, bad):
+    cb = EightBatch(seqs, 2, 64, 16, BF, seed=69)
+    q = cb.tokens(4)
+    ws = sv.CacheWorkspace()
+    # page 3 (of a window none or all see: the one before the first new token)
+    at = [3, (seqs[1][1] - seqs[1][0] - 1) // 16]
+    cb.k, cb.v = (torch.cat((x, torch.zeros_like(x[:1]))) for x in (cb.k, cb.v))
+    for b in (0, 1):
+        cb.pages[b, at[b]] = bad
+        cb.table[b, at[b]] = cb.k.shape[0] - 1
+    got = sv.paged_attention(q, *cb.eight(), window=window, **cb.scales(), ws=ws)
+    assert ws.status() == sv.STATUS_BAD_PAGE
+    within(got, *attention(cb, q, default_scale(64), window))
+
+
+# ---------------------------------------------------------------------------
+# batches at the border between the two ways
+
+@pytest.mark.parametrize("seqs,kernels", [
+    ([(120, 400), (8, 900)], 1), ([(121, 400), (8, 900)], 2), ([(127, 130), (1, 1300)], 1),
+    ([(300, 300)] + [(1, 100 + 90 * i) for i in range(20)], 1), ([(500, 700), (6, 1000), (1, 40)], 2)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_long_and_short_sequences_together(seqs, kernels, window):
+    cb = EightBatch(seqs, 2, 64, 16, BF, seed=70, scale_spread=0.5)
+    q = cb.tokens(4, 1.5)
+    ws = sv.CacheWorkspace()
+    got = sv.paged_attention(q, *cb.eight(), window=window, **cb.scales(), ws=ws)
+    assert ws.status() == 0 and sv.last_kernel_count() == kernels
+    within(got, *attention(cb, q, default_scale(64), window))
