@@ -370,7 +370,8 @@ typedef struct sv_cache_scales {
  *   q_norm, k_norm [head_dim] of norm_dtype (SV_F32 or the tokens' type), or NULL:
  *         a head's vector x becomes x * rsqrt(mean(x^2) + eps) * norm before it
  *         turns; eps >= 0 and finite.  (Squares are summed in fp32.)
- * Norm and rotation are fp32 and the result is rounded once: to the tokens' type,
+ * Norm and rotation are fp32 (angles are good to 2^-26 of a turn and position times
+ * frequency times 2^-52), and the result is rounded once: to the tokens' type,
  * or, for keys and values of an 8-bit cache, to e4m3 after the division by the
  * vector's scale, the smallest power of two from 2^-100 to 2^100 that is at least
  * 1/448 of its largest magnitude (larger vectors saturate).  A vector that then

@@ -177,9 +177,17 @@ int launch_attend8(const sv::Attend8Params &A, const CUtensorMap &kmap, const CU
 
 // Up to so many packed rows of a sequence and kv head attention goes over the codes
 // directly, above it (and with room for it) the sequences are read back to 16 bits
-// first.  32 sequences of 4096 slots, 32 heads over 8 of 128, bf16: 85 against 252 us
-// for 8 tokens each (32 rows), 248 against 259 for 32, 298 against 271 for 40, 858
-// against 388 for 128; 4 of 32768: 216 against 258 for 32, 269 against 269 for 40.
+// first.  32 sequences of 4096 slots, 32 heads over 8 of 128, bf16: 89 against 252 us
+// for 8 tokens each (32 rows), 253 against 259 for 32, 304 against 272 for 40, 881
+// against 379 for 128; 4 of 32768: 225 against 259 for 32, 279 against 270 for 40.
+//
+// The rule and the tiles' width go by the batch's average (the lengths are known on the
+// device alone), which suits sequences with like numbers of new tokens.  One long one
+// among short ones fares badly: a chunk of 2048 tokens over 4096 slots takes 113 us,
+// 127 single tokens over 512 to 4096 slots 124, both in one call 552; a chunk of 4096 and
+// 255 single tokens 145, 230 and 1243 (over the codes, in narrow tiles); with 62 single
+// tokens beside the chunk of 2048 the whole batch is read back, 379 for 113 and 65.  Calls
+// of their own for the long ones and for the short ones take the sum.
 constexpr int64_t kDirectRows = 128;
 // Reading back looks at every slot of the page table (a block for 16 of them, most of
 // which end at once where sequences are short): not past a table whose slots would be so

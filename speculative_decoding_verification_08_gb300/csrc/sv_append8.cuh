@@ -15,7 +15,8 @@
 // 8, so that sums and maxima are a few shuffles and nothing is loaded twice.  Angles
 // are fixed-point: a frequency in turns as a 64-bit fraction, once a block (fp64 runs at
 // 1/64 of fp32 here), so that position times frequency modulo a turn is one integer
-// product, good to 2^-33 of a turn at any position.
+// product.  They are good to 2^-26 of a turn (the conversion to fp32) and position times
+// frequency (in turns) times 2^-52 (the frequency's own rounding in fp64).
 //
 // Measured (32 query heads over 8 of 128, bf16, unless said otherwise):
 //   18,157 tokens of prompts into 8 bits, half of each head turned: 81 us, 5.1 TB/s (90

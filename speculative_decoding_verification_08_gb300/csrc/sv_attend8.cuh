@@ -39,13 +39,14 @@
 // groups and parts and write its rows.  Every wait is bounded, as there.
 //
 // Measured (32 query heads over 8 of 128, bf16, unless said otherwise):
-//   rounds of 6 tokens over up to 4096 slots, 256 sequences: 270 us, 4.6 TB/s.  Without
-//     its copies the kernel takes as long: the bound is a block's way through four
-//     softmax warps (4000 cycles for two blocks at a time, a tenth of it instructions of
-//     one warp), which the instruction cache feeds (87 % of its requests hit; with waits,
-//     conversions and the queries' preparation unrolled 67 %, and 493 us);
-//   6 tokens over 131071 slots, 2 sequences, 16 over 4 heads of 64 in fp16: 76 us, 10 of
-//     them for pages of 16 slots (16 boxes a block; 4 with pages of 64);
+//   rounds of 6 tokens over up to 4096 slots, 256 sequences: 279 us, 4.4 TB/s (16-bit
+//     caches: 375).  The bound is a block's way through four softmax warps (latency: some
+//     4000 cycles for two blocks at a time, a tenth of it instructions of one warp), which
+//     the instruction cache feeds;
+//   6 tokens over 131071 slots, 2 sequences, 16 over 4 heads of 64 in fp16: 76 us, with
+//     pages of 64 slots instead of 16 (4 boxes a block instead of 16) 62.  A block of heads
+//     of 64 takes as long as one of 128 at half the bytes: 16-bit caches take 66 and 59,
+//     and are the faster ones for few rows of such heads over long contexts;
 //   one token over 1000 slots: 12 us: launch, lookups, one block, join of the parts.
 #pragma once
 
@@ -55,8 +56,8 @@
 namespace sv {
 
 constexpr int kMaxRows8 = 32;   // packed rows of a tile at most
-// A tile's fixed cost in key blocks: 274 us for rounds of 6 tokens over up to 4096 slots
-// (287 with 3, 281 with 8), 105 over up to 500 (111 and 101).
+// A tile's fixed cost in key blocks: 289 us for a round of 6 tokens over up to 4096 slots
+// alone (302 with 3, 291 with 8), 138 over up to 500 (147 and 134).
 constexpr int kTileCost8 = 5;
 constexpr int kThreads8 = 640;
 // Registers per thread after the roles part, of the 640 x 96 that the block is
@@ -67,7 +68,11 @@ constexpr int kRaw = kKeys * 128;     // a block of codes
 constexpr int kScaleRing = 3;         // pairs of blocks of scales
 // Weights are relative to a row's reference, their values' scales included: the logarithm
 // of the largest that fp16 holds, and where a new reference puts the largest so far.
+// (A round of 6 tokens over up to 4096 slots alone: 289 us, 310 with no more than 2^8.9 of
+// room above a new reference's largest, 283 with 2^14.9, at 3 bits less below.)
 constexpr float kGrowAbove = 15.9f, kTop = 4.f;
+// Where references have steps of 8 and more, a new one may put the largest so far beside
+// kTop; this far off it is corrected.
 constexpr float kFarOff = 10.f, kCoarse = 0x1p26f;
 constexpr int kMaxPasses = 8;
 constexpr float kUnset = 3e38f;       // minus the reference of a row that has seen nothing
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                                 tc::mma_f8(tm + sb * L::kScoreCols, kd + s * 2, qd + s * 2, kIdescS, s > 0);
                         tc::commit(&sh.k_empty[st]);
                         // (both groups' at once: their warps then run the same code together,
-                        // and share its fetching: 274 instead of 281 us for rounds)
+                        // and share its fetching: 289 instead of 295 us for a round alone)
                         if (sb == 1) tc::commit(&sh.s_full[0]);
                         if (sb == 1 || i + 1 == blocks) tc::commit(&sh.s_full[sb]);
                         if (i + 1 == blocks) tc::commit(&sh.q_empty[qb]);
@@ -870,8 +875,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                         if (k * per + slot0 >= here)
                             *reinterpret_cast<uint4 *>(raw + src + k * per * 128) = make_uint4(0, 0, 0, 0);
                 }
-                // (not unrolled, for the instruction cache's sake: 274 us for rounds of 6 tokens
-                // over up to 4096 slots, 281 by four, 363 by eight)
+                // (not unrolled, for the instruction cache's sake: 289 us for a round of 6 tokens
+                // over up to 4096 slots alone, 296 by four, 377 by eight)
 #pragma unroll 1
                 for (int k = 0; k < rounds; ++k) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(raw + src + k * per * 128);
