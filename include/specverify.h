@@ -405,13 +405,15 @@ int sv_read_kv(const sv_paged_cache *cache, const sv_cache_scales *scales, int32
  *         where reading back is not faster for the batch's average of new tokens, where
  *         the table's slots would be more than 16 GiB in 16 bits, and for more than 65536
  *         kv heads (scratch is refused for these two).  (Keys and values past fp16's
- *         range saturate there.)
+ *         range saturate there, and scores past 2^26 may give NaN, as they may in
+ *         sv_paged_attention.)
  * Products are accumulated and statistics kept in fp32.  Without scratch: scores are
  * those of the codes and the queries as they are; a query's values below 2^-20 of its
  * largest are good to 2^-31 of that; weights times the values' scales are rounded to 11
- * bits (those below 2^-18 of the row's largest to steps of 2^-28 of it; what is below
- * 2^-130 of it is neither added up nor counted).  A row's result depends on no other row
- * and on no slot that it does not see.  A query that holds a NaN or an
+ * bits (those below 2^-18 of the row's largest to steps of 2^-28 of it; a slot whose
+ * weight times scale is below 2^-126 of it does not count).  A row's result depends on no
+ * other row (but for roundings where another's scores are past 2^26) and on no slot that
+ * it does not see.  A query that holds a NaN or an
  * infinity gives NaN for a row that sees a slot.  Slots inside a sequence's length must
  * hold what sv_append_kv_normed writes, codes of 0x7f and 0xff excepted; what unused slots hold
  * does not matter.  A key or value whose scale is NaN gives NaN for the rows that see

@@ -728,8 +728,11 @@ def paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, *, scale=None, 
     four bytes for each key and value pair of the table's pages or of the cache's,
     whichever are fewer.  Where that much cannot be had, or the table's slots
     would be more than 16 GiB so, it attends to the codes all the same (slower
-    for such batches).  float16 only: keys and values past 65504, which the
-    codes hold, saturate when they are read back."""
+    for such batches).  What differs by the way taken, besides roundings: keys
+    and values of float16 tokens past 65504, which the codes hold, saturate when
+    they are read back, and scores past 2^26 may then give NaN.  Vectors that are
+    NaN reach the rows that see them and no others, either way.  A long chunk
+    beside many short rounds does better in a call of its own."""
     if k_scale is None and v_scale is None:
         return _call("paged_attention", k_cache, "k_cache",
                      (q, k_cache, v_cache, pages, q_start, kv_len, scale, window, out), ws, stream)
